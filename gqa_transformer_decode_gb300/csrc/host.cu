@@ -157,6 +157,14 @@ bool pdl_enabled() {
 }
 void count_launches(long long n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 unsigned long long launches_so_far() { return (unsigned long long)g_launches.load(); }
+ember_status set_error(ember_status st, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(st, "%s", buf);
+}
 }  // namespace ember
 
 struct ember_model {

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "ember.h"
+
 namespace ember {
 
 // Host-side count of kernel launches (every launch_* call adds its kernels).
@@ -12,6 +14,8 @@ void count_launches(long long n);
 // traces a decode step (ember_decode_step_traced); otherwise does nothing.
 void trace_launch(const void* fn, cudaStream_t s);
 unsigned long long launches_so_far();
+// Sets the calling thread's ember_last_error message and returns st.
+ember_status set_error(ember_status st, const char* fmt, ...);
 
 // Launch with the programmatic-stream-serialization attribute (PDL) unless
 // disabled (EMBER_NO_PDL=1): the kernel may start while its predecessor in
@@ -412,6 +416,76 @@ struct SampleArgs {
     int32_t* out;
 };
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
+
+// ------------------------------------------------------------ paged cache --
+// A pool of K/V pages shared by many sequences (paged_*.cu).  Row r of page p
+// of kv head g starts at k + p*page_stride + g*head_stride + r*row_stride
+// (elements; the same offsets from v); table[seq][i] is the page that holds
+// the sequence's positions [i * page_size, (i + 1) * page_size).
+struct PagedView {
+    uint16_t *k, *v;
+    const int32_t* table;
+    int n_pages, page_shift, NKV, D, n_seqs, width;
+    long long page_stride, head_stride, row_stride;
+    bool bf16;                   // element type: bf16, else f16
+};
+
+// Per-head RMSNorm (optional) and RoPE of q and k, rounding, and the store of
+// the K/V rows into their pages.  src: 0 f32, 1 bf16, 2 f16.
+struct PagedAppendArgs {
+    PagedView c;
+    const void *q, *k, *v;       // [n] rows of NH*D / NKV*D / NKV*D elements (q may be null)
+    int src;
+    long long ld_q, ld_k, ld_v;
+    int n, NH;
+    const int32_t *seqs, *positions;
+    const uint16_t *q_norm, *k_norm;   // [D] bf16 bits, or nullptr
+    float eps;
+    const float *cos_t, *sin_t;  // [n_pos][D/2]
+    int n_pos;
+    uint16_t* q_out;             // [n][ld_out]
+    long long ld_out;
+    int* status;
+};
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
+
+// Attention of one query token per sequence (its last position) over the
+// paged cache.
+struct PagedDecodeArgs {
+    PagedView c;
+    const uint16_t* q;           // [B][ld_q], NH*D used
+    long long ld_q;
+    int B, NH;
+    const int32_t* seqs;         // [B] rows of the table, or nullptr (row b)
+    const int32_t* lens;         // [B] keys of the sequence, the query's own among them
+    int window, sinks;
+    float scale;
+    uint16_t* out;               // [B][ld_out]
+    long long ld_out;
+    float* lse;                  // [B][NH] or nullptr
+    float* ws;                   // partials, paged_decode_ws floats
+    int* status;
+};
+size_t paged_decode_ws(int NKV, int G, int D, int sms);   // bytes
+cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int sms, cudaStream_t s);
+
+// Attention of the last cu[b + 1] - cu[b] positions of each sequence.
+struct PagedPrefillArgs {
+    PagedView c;
+    const uint16_t* q;           // [n][ld_q]
+    long long ld_q;
+    int n, B, NH;
+    const int32_t* seqs;
+    const int32_t* cu;           // [B + 1] first query row of each sequence
+    const int32_t* lens;
+    int window, sinks;
+    float scale;
+    uint16_t* out;
+    long long ld_out;
+    float* lse;                  // [n][NH] or nullptr
+    int* status;
+};
+cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, int sms, cudaStream_t s);
 
 // out[c][r] = in[r][c] for 16-bit elements
 void launch_transpose16(const uint16_t* in, uint16_t* out, int rows, int cols, cudaStream_t s);

@@ -1,0 +1,76 @@
+// paged.cuh -- device helpers shared by the paged-cache kernels: element
+// types, cp.async copies with zero fill, warp matrix products on bf16 or f16
+// operands, and which keys of a paged sequence a query sees.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "mma_common.cuh"
+
+namespace ember {
+
+// Cache element types.  Values are computed in f32 and rounded once, to
+// nearest even, when they are stored.
+struct ElemBf16 {
+    static constexpr bool bf16 = true;
+    __device__ __forceinline__ static uint32_t pack(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    __device__ __forceinline__ static float lo(uint32_t u) { return bf16_lo(u); }
+    __device__ __forceinline__ static float hi(uint32_t u) { return bf16_hi(u); }
+    // c += a (16x16) * b (16x8), f32 accumulators
+    __device__ __forceinline__ static void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+struct ElemF16 {
+    static constexpr bool bf16 = false;
+    __device__ __forceinline__ static uint32_t pack(float lo, float hi) { return pack_f16x2(lo, hi); }
+    __device__ __forceinline__ static float lo(uint32_t u) { return __half2float(__ushort_as_half((uint16_t)u)); }
+    __device__ __forceinline__ static float hi(uint32_t u) { return __half2float(__ushort_as_half((uint16_t)(u >> 16))); }
+    __device__ __forceinline__ static void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        mma16816(c, a, b0, b1);
+    }
+};
+
+// 16 bytes from global to shared memory, or 16 zero bytes when !valid (the
+// source is then not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Keys of one sequence that a query at position pos sees: all of [0, pos], or
+// under a window the last `window` of them and the first `sinks`.
+struct Visible {
+    int end;    // pos + 1: keys at or beyond it are hidden
+    int first;  // first key of the window (0 without one)
+    int sinks;  // keys below it are visible too
+    __device__ __forceinline__ Visible(int pos, int window, int n_sinks) {
+        end = pos + 1;
+        first = window > 0 ? max(0, end - window) : 0;
+        sinks = min(n_sinks, first);
+    }
+    __device__ __forceinline__ bool sees(int key) const { return key < end && (key >= first || key < sinks); }
+};
+
+// The scores' running maximum starts at a finite value below every score that
+// counts, so that a row which has seen no key yet (or only scores of -inf)
+// never forms inf - inf.
+constexpr float SOFTMAX_FLOOR = -3.0e38f;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+}  // namespace ember

@@ -49,6 +49,17 @@ class ember_weights(C.Structure):
                 ("layers", C.POINTER(ember_layer_weights))]
 
 
+# ember_dtype
+F32, BF16, F16 = 0, 1, 2
+
+
+class ember_paged_kv(C.Structure):
+    _fields_ = [("k", P), ("v", P), ("table", P), ("dtype", C.c_int32), ("n_pages", C.c_int32),
+                ("page_size", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("n_seqs", C.c_int32), ("table_width", C.c_int32), ("page_stride", C.c_int64),
+                ("head_stride", C.c_int64), ("row_stride", C.c_int64)]
+
+
 _lib = None
 
 
@@ -94,6 +105,13 @@ def load():
         "ember_gemv_argmax_noalloc": (st, [P, C.c_int32, C.c_int32, P, C.c_int32, P, P, P]),
         "ember_sample": (st, [P, C.c_int32, C.c_int32, C.c_int32, C.c_float, C.c_int32, C.c_float, P, P,
                               P]),
+        "ember_paged_append": (st, [P, P, P, P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_int32,
+                                    C.c_int32, P, P, P, P, C.c_float, P, P, C.c_int32, P, C.c_int64, P, P]),
+        "ember_paged_decode_workspace": (C.c_size_t, [P, C.c_int32, C.c_int32]),
+        "ember_paged_decode": (st, [P, P, C.c_int64, C.c_int32, C.c_int32, P, P, C.c_int32, C.c_int32,
+                                    C.c_float, P, C.c_int64, P, P, C.c_size_t, P, P]),
+        "ember_paged_prefill": (st, [P, P, C.c_int64, C.c_int32, C.c_int32, C.c_int32, P, P, P, C.c_int32,
+                                     C.c_int32, C.c_float, P, C.c_int64, P, P, P]),
         "ember_prefill_activations": (st, [P, P, C.c_int32, P, C.c_int32, C.c_int32, P, P, P, P]),
         "ember_mean_pooled_head": (st, [P, C.c_int32, C.c_int32, C.c_int32, P, P, C.c_int32, P, P]),
         "ember_test_bounded_wait": (st, [P, C.c_int32, C.c_int64, P]),
@@ -244,6 +262,28 @@ def ember_prefill_activations(m, kv, seq, ids, n, start_pos, acts, logits, argma
 
 def ember_mean_pooled_head(hidden, B, T, H, w, b, n_out, out, stream):
     return load().ember_mean_pooled_head(hidden, B, T, H, w, b, n_out, out, stream)
+
+
+def ember_paged_append(kv, q, k, v, src_dtype, ld_q, ld_k, ld_v, n, n_heads, seqs, positions, q_norm, k_norm,
+                       eps, cos_t, sin_t, n_pos, q_out, ld_out, status, stream):
+    return load().ember_paged_append(kv, q, k, v, src_dtype, ld_q, ld_k, ld_v, n, n_heads, seqs, positions,
+                                     q_norm, k_norm, eps, cos_t, sin_t, n_pos, q_out, ld_out, status, stream)
+
+
+def ember_paged_decode_workspace(kv, B, n_heads) -> int:
+    return int(load().ember_paged_decode_workspace(kv, B, n_heads))
+
+
+def ember_paged_decode(kv, q, ld_q, B, n_heads, seqs, lens, window, sinks, scale, out, ld_out, lse, workspace,
+                       workspace_bytes, status, stream):
+    return load().ember_paged_decode(kv, q, ld_q, B, n_heads, seqs, lens, window, sinks, scale, out, ld_out,
+                                     lse, workspace, workspace_bytes, status, stream)
+
+
+def ember_paged_prefill(kv, q, ld_q, n, B, n_heads, seqs, cu, lens, window, sinks, scale, out, ld_out, lse,
+                        status, stream):
+    return load().ember_paged_prefill(kv, q, ld_q, n, B, n_heads, seqs, cu, lens, window, sinks, scale, out,
+                                      ld_out, lse, status, stream)
 
 
 def ember_kernel_launches() -> int:

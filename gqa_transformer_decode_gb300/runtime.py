@@ -7,6 +7,7 @@ runs in libember.so.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 
 import numpy as np
@@ -140,6 +141,217 @@ class KVCache:
             self.close()
         except Exception:
             pass
+
+
+class PagedKV:
+    """The paged K/V cache operators on torch tensors (include/ember.h, "paged
+    key/value cache"): append new tokens' rows, attend with one token per
+    sequence (decode) or several (prefill).
+
+    k_pages, v_pages  bf16 or f16 [n_pages, n_kv_heads, page_size, head_dim]; any
+                      strides with head_dim contiguous, the same for both, so
+                      memory may also hold a row's heads side by side (a
+                      transposed view)
+    table             int32 [n_seqs, table_width], the sequences' pages
+
+    The tensors stay the caller's and may change between calls; the object
+    keeps references and one int32 status word.  Calls are asynchronous on
+    `stream` (default: the current stream of the pages' device); device-side
+    errors are read with sync_status().  Tensors that a call allocates are
+    allocated on that stream.
+    """
+
+    def __init__(self, k_pages, v_pages, table):
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+            raise ValueError("k_pages and v_pages must be alike: [n_pages, n_kv_heads, page_size, head_dim]")
+        if k_pages.dtype not in _PAGE_DTYPES or v_pages.dtype != k_pages.dtype:
+            raise TypeError("pages must be bfloat16 or float16")
+        if table.dim() != 2 or table.dtype != torch.int32 or not table.is_contiguous():
+            raise ValueError("table must be contiguous int32 [n_seqs, table_width]")
+        if not k_pages.is_cuda or v_pages.device != k_pages.device or table.device != k_pages.device:
+            raise ValueError("pages and table must be on one CUDA device")
+        # the stride of a dimension of one is never walked: any valid value will do
+        strides = [[t.stride(i) if t.shape[i] > 1 else t.shape[3] for i in range(3)] for t in (k_pages, v_pages)]
+        if strides[0] != strides[1] or k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
+            raise ValueError("pages must have the same strides and head_dim contiguous")
+        self.k_pages, self.v_pages, self.table = k_pages, v_pages, table
+        self.device, self.dtype = k_pages.device, k_pages.dtype
+        n_pages, self.n_kv_heads, page_size, self.head_dim = k_pages.shape
+        c = E.ember_paged_kv()
+        c.k, c.v, c.table = k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr()
+        c.dtype = _PAGE_DTYPES[k_pages.dtype]
+        c.n_pages, c.page_size, c.n_kv_heads, c.head_dim = n_pages, page_size, self.n_kv_heads, self.head_dim
+        c.n_seqs, c.table_width = table.shape
+        c.page_stride, c.head_stride, c.row_stride = strides[0]
+        self._c = c
+        self._kv = C.addressof(c)
+        self._lib = E.load()
+        with torch.cuda.device(self.device):
+            self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._status = self.status.data_ptr()
+        self._ws_bytes = {}
+
+    # -- checks ---------------------------------------------------------------
+    def _ints(self, t, n, what):
+        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != self.device or \
+                (n > 1 and t.stride(0) != 1):
+            raise ValueError(f"{what} must be contiguous int32 [{n}] on {self.device}")
+        return t.data_ptr()
+
+    def _rows(self, t, what, heads, dtype):
+        """[n, heads, head_dim] with a row's heads side by side -> (pointer, row stride)."""
+        D = self.head_dim
+        if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads) or t.dtype != dtype or \
+                t.device != self.device:
+            raise ValueError(f"{what} must be {dtype} [n, {heads or 'heads'}, {D}] on {self.device}")
+        st = t.stride()
+        if st[2] != 1 or (t.shape[1] > 1 and st[1] != D):
+            raise ValueError(f"{what}: a row's heads must lie side by side")
+        return t.data_ptr(), (st[0] if t.shape[0] > 1 else t.shape[1] * D)
+
+    def _run(self, stream):
+        """-> (raw stream, context that makes the device and the stream current)."""
+        if stream is None and torch.cuda.current_device() == self.device.index:
+            return torch.cuda.current_stream().cuda_stream, _NOTHING
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        if stream.device != self.device:
+            raise ValueError(f"the stream belongs to {stream.device}, the cache to {self.device}")
+        return stream.cuda_stream, torch.cuda.stream(stream)
+
+    # -- operators ------------------------------------------------------------
+    def append(self, k, v, seqs, positions, cos, sin, q=None, q_norm=None, k_norm=None, eps=1e-6, q_out=None,
+               stream=None):
+        """Norm (optional), rotate and store the K/V rows of new tokens.
+
+        k, v [n, n_kv_heads, head_dim] and q [n, n_heads, head_dim] (optional) of
+        one type, f32, bf16 or f16; seqs, positions int32 [n]; cos, sin f32
+        [n_pos, head_dim / 2]; q_norm, k_norm bf16 [head_dim].  Returns the
+        rotated queries in the cache's type (q_out where given), or None."""
+        src = _SRC_DTYPES.get(k.dtype)
+        if src is None:
+            raise TypeError("q, k and v must be float32, bfloat16 or float16")
+        n = k.shape[0]
+        kp, ldk = self._rows(k, "k", self.n_kv_heads, k.dtype)
+        vp, ldv = self._rows(v, "v", self.n_kv_heads, k.dtype)
+        if v.shape[0] != n or (q is not None and q.shape[0] != n):
+            raise ValueError("q, k and v must have the same rows")
+        sp, pp = self._ints(seqs, n, "seqs"), self._ints(positions, n, "positions")
+        half = self.head_dim // 2
+        for t in (cos, sin):
+            if t.dtype != torch.float32 or t.dim() != 2 or t.shape != (cos.shape[0], half) or \
+                    not t.is_contiguous() or t.device != self.device:
+                raise ValueError(f"cos and sin must be contiguous f32 [n_pos, {half}] on {self.device}")
+        norms = []
+        for t in (q_norm, k_norm):
+            if t is not None and (t.dtype != torch.bfloat16 or t.shape != (self.head_dim,) or
+                                  not t.is_contiguous() or t.device != self.device):
+                raise ValueError(f"q_norm and k_norm must be contiguous bf16 [{self.head_dim}] on {self.device}")
+            norms.append(None if t is None else t.data_ptr())
+        raw, ctx = self._run(stream)
+        with ctx:
+            qp, ldq, op, ldo, heads = None, 0, None, 0, 0
+            if q is not None:
+                heads = q.shape[1]
+                qp, ldq = self._rows(q, "q", heads, k.dtype)
+                if q_out is None:
+                    q_out = torch.empty((n, heads, self.head_dim), dtype=self.dtype, device=self.device)
+                elif q_out.shape != q.shape:
+                    raise ValueError("q_out must have q's shape")
+                op, ldo = self._rows(q_out, "q_out", heads, self.dtype)
+            elif q_out is not None:
+                raise ValueError("q_out without q")
+            if n:
+                st = self._lib.ember_paged_append(self._kv, qp, kp, vp, src, ldq, ldk, ldv, n, heads, sp, pp,
+                                                  norms[0], norms[1], eps, cos.data_ptr(), sin.data_ptr(),
+                                                  cos.shape[0], op, ldo, self._status, raw)
+                if st:
+                    E.check(st, "ember_paged_append")
+        return q_out
+
+    def decode(self, q, lens, seqs=None, window=0, sinks=0, scale=None, out=None, lse=None, return_lse=False,
+               workspace=None, stream=None):
+        """Attention of one token per sequence: q [B, n_heads, head_dim], lens
+        int32 [B] (keys of each sequence, the token's own among them), seqs
+        int32 [B] (default: sequence b).  scale defaults to head_dim ** -0.5.
+        Returns out, or (out, lse) with return_lse or lse.  workspace: a uint8
+        tensor of at least workspace_bytes(B, n_heads) (default: allocated)."""
+        B, heads = q.shape[0], q.shape[1]
+        qp, ldq = self._rows(q, "q", None, self.dtype)
+        lp = self._ints(lens, B, "lens")
+        sp = None if seqs is None else self._ints(seqs, B, "seqs")
+        raw, ctx = self._run(stream)
+        with ctx:
+            out, lse, op, ldo, ep = self._outputs(q, out, lse, return_lse)
+            if B:
+                need = self.workspace_bytes(B, heads)
+                if workspace is None:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+                elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+                        workspace.device != self.device:
+                    raise ValueError(f"workspace must be contiguous uint8 on {self.device}")
+                st = self._lib.ember_paged_decode(self._kv, qp, ldq, B, heads, sp, lp, window, sinks,
+                                                  self.head_dim ** -0.5 if scale is None else scale, op, ldo, ep,
+                                                  workspace.data_ptr(), workspace.numel(), self._status, raw)
+                if st:
+                    E.check(st, "ember_paged_decode")
+        return out if lse is None else (out, lse)
+
+    def prefill(self, q, cu, lens, seqs=None, window=0, sinks=0, scale=None, out=None, lse=None, return_lse=False,
+                stream=None):
+        """Attention of several tokens per sequence: rows cu[b] .. cu[b + 1] - 1
+        of q [n, n_heads, head_dim] are the last positions of sequence b (or
+        seqs[b]), which holds lens[b] keys.  cu int32 [B + 1], lens int32 [B]."""
+        n, heads, B = q.shape[0], q.shape[1], lens.shape[0]
+        qp, ldq = self._rows(q, "q", None, self.dtype)
+        lp, cp = self._ints(lens, B, "lens"), self._ints(cu, B + 1, "cu")
+        sp = None if seqs is None else self._ints(seqs, B, "seqs")
+        raw, ctx = self._run(stream)
+        with ctx:
+            out, lse, op, ldo, ep = self._outputs(q, out, lse, return_lse)
+            if n and B:
+                st = self._lib.ember_paged_prefill(self._kv, qp, ldq, n, B, heads, sp, cp, lp, window, sinks,
+                                                   self.head_dim ** -0.5 if scale is None else scale, op, ldo, ep,
+                                                   self._status, raw)
+                if st:
+                    E.check(st, "ember_paged_prefill")
+        return out if lse is None else (out, lse)
+
+    def _outputs(self, q, out, lse, return_lse):
+        if out is None:
+            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if lse is None and return_lse:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device)
+        elif lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or
+                                  not lse.is_contiguous() or lse.device != self.device):
+            raise ValueError("lse must be contiguous f32 [rows, n_heads]")
+        op, ldo = self._rows(out, "out", q.shape[1], self.dtype)
+        return out, lse, op, ldo, None if lse is None else lse.data_ptr()
+
+    def workspace_bytes(self, B: int, n_heads: int) -> int:
+        """Bytes of decode's workspace for B sequences of n_heads query heads."""
+        n = self._ws_bytes.get((B, n_heads))
+        if n is None:
+            with torch.cuda.device(self.device):
+                n = E.ember_paged_decode_workspace(self._kv, B, n_heads)
+            self._ws_bytes[(B, n_heads)] = n
+        return n
+
+    def sync_status(self, stream=None) -> int:
+        """Wait for the stream, return and clear the first device-side error (0: none)."""
+        (torch.cuda.current_stream(self.device) if stream is None else stream).synchronize()
+        st = int(self.status.item())
+        if st:
+            self.status.zero_()
+            torch.cuda.synchronize(self.device)
+        return st
+
+
+_PAGE_DTYPES = {torch.bfloat16: E.BF16, torch.float16: E.F16}
+_SRC_DTYPES = {torch.float32: E.F32, torch.bfloat16: E.BF16, torch.float16: E.F16}
+_NOTHING = contextlib.nullcontext()
 
 
 def _wrap_device(ptr: int, nbytes: int, device) -> torch.Tensor:

@@ -287,6 +287,112 @@ ember_status ember_sample(const float *logits, int32_t B, int32_t V, int32_t ldl
                           int32_t top_k, float top_p, const float *r, int32_t *out,
                           ember_stream_t stream);
 
+/* ---- paged key/value cache ------------------------------------------------ */
+
+/* Three operators on one pool of K/V pages that many sequences share, for a
+ * serving loop whose sequences grow, end and are replaced: new tokens' rows go
+ * in with ember_paged_append, and ember_paged_decode / ember_paged_prefill
+ * attend over them.  They are stateless like ember_sample: the pool, the page
+ * table and every other buffer are the caller's, nothing is kept, and they
+ * compose on one stream with any other call.  (The cache of ember_kv_alloc --
+ * "ember internals", "kv cache" -- is one block of max_len rows per sequence;
+ * the same operations on it are inside ember_prefill / ember_decode_step.)
+ *
+ * Common rules:
+ *   - Row r of page p of kv head g starts at k + p*page_stride +
+ *     g*head_stride + r*row_stride elements, the same for v, and holds
+ *     head_dim elements; so pages may hold a head's rows together or a row's
+ *     heads together.  Position i of sequence s lies in page
+ *     table[s*table_width + i / page_size], row i % page_size.
+ *   - head_dim is 16, 32, 64 or 128; page_size a power of two from 16 to 1024;
+ *     n_heads / n_kv_heads at most 16; table_width * page_size at most 2^30.
+ *   - All element pointers are 16-byte aligned; strides and row lengths (ld_*,
+ *     in elements) are multiples of 8.  q / out rows hold the heads side by
+ *     side, head_dim apart.
+ *   - seqs[i] < 0 marks a padding token or row: it is skipped and what it
+ *     would write stays as it was.
+ *   - Errors that depend on device data raise the first code into *status (a
+ *     device int32 that the caller zeroes and reads; NULL: not reported):
+ *     INVALID_ARG for a seqs entry >= n_seqs, a cu entry out of order or a page
+ *     outside [0, n_pages); CAPACITY for a position or length outside
+ *     [0, table_width*page_size] or, in append, beyond the RoPE table.  The token,
+ *     or the sequence's rows, are then skipped; of a bad page met by attention
+ *     the keys read as zeros.  Nothing outside the buffers is touched.
+ *   - Table entries of pages that hold no visible key are not read, nor are
+ *     rows of a page that no query of the call sees: they may hold anything.
+ *   - Buffers and the stream belong to the current device; buffers may not
+ *     overlap, except that pages may be shared by the tables of sequences
+ *     that only read them. */
+typedef enum ember_dtype { EMBER_F32 = 0, EMBER_BF16 = 1, EMBER_F16 = 2 } ember_dtype;
+
+typedef struct ember_paged_kv {
+    void *k, *v;                 /* the pages, elements of `dtype`              */
+    const int32_t *table;        /* [n_seqs][table_width] page numbers          */
+    int32_t dtype;               /* EMBER_BF16 or EMBER_F16                     */
+    int32_t n_pages, page_size;  /* pages of the pool, rows of a page           */
+    int32_t n_kv_heads, head_dim;
+    int32_t n_seqs, table_width;
+    int64_t page_stride, head_stride, row_stride; /* elements                   */
+} ember_paged_kv;
+
+/* Append n tokens: token t of sequence seqs[t] at position positions[t].  Per
+ * head, q and k are RMS-normed over head_dim (q_norm / k_norm, bf16 bits
+ * [head_dim], NULL: not normed; PII-Tracer forward(): before RoPE), rotated by
+ * row positions[t] of the f32 tables cos_t / sin_t [n_pos][head_dim/2] (ember
+ * reference_forward.py rope(), rotate-half) and rounded once to the cache's
+ * type; k and v go to their page row, q to q_out.  All arithmetic is f32; the
+ * rotation is that of ember_rope_store, bit for bit.
+ *   q [n] rows of n_heads*head_dim, k, v [n] rows of n_kv_heads*head_dim, of
+ *   src_dtype (F32, BF16 or F16), ld_* apart; slices of one fused q|k|v buffer
+ *   fit.  q and q_out may both be NULL (n_heads is then not used).
+ *   q_out [n] rows of n_heads*head_dim elements of the cache's type.
+ * The (sequence, position) pairs of a call must be distinct: of two tokens at
+ * one place each 16-byte piece is one or the other's.
+ * Host errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ember_status ember_paged_append(const ember_paged_kv *kv, const void *q, const void *k,
+                                const void *v, int32_t src_dtype, int64_t ld_q, int64_t ld_k,
+                                int64_t ld_v, int32_t n, int32_t n_heads, const int32_t *seqs,
+                                const int32_t *positions, const uint16_t *q_norm,
+                                const uint16_t *k_norm, float eps, const float *cos_t,
+                                const float *sin_t, int32_t n_pos, void *q_out, int64_t ld_out,
+                                int32_t *status, ember_stream_t stream);
+
+/* Attention of one token per sequence, its last: row b stands at position
+ * lens[b] - 1 of sequence seqs[b] (NULL: sequence b) and sees key j when
+ * j < lens[b] and, for window > 0, j >= lens[b] - window or j < sinks.
+ *   out[b] = sum_j p_j v_j,  p = softmax over the visible j of scale q . k_j
+ *   (ember reference_forward.py forward(), the grouped-query head loop)
+ *   lse[b][h] = log sum_j exp(scale q . k_j)   (f32 [B][n_heads], nullable)
+ * lens[b] == 0 gives out 0 and lse -inf.  q, out: [B] rows of
+ * n_heads*head_dim elements of the cache's type.
+ *   workspace: ember_paged_decode_workspace bytes, 16-byte aligned, of any
+ *   content; used until the call's kernels end, so calls that may overlap
+ *   (other streams, graphs that run at once) need one each.
+ * The result depends on the inputs and the device only (no atomics).
+ * Host errors: INVALID_ARG, UNSUPPORTED, CAPACITY (workspace too small), CUDA. */
+size_t ember_paged_decode_workspace(const ember_paged_kv *kv, int32_t B, int32_t n_heads);
+ember_status ember_paged_decode(const ember_paged_kv *kv, const void *q, int64_t ld_q, int32_t B,
+                                int32_t n_heads, const int32_t *seqs, const int32_t *lens,
+                                int32_t window, int32_t sinks, float scale, void *out,
+                                int64_t ld_out, float *lse, void *workspace,
+                                size_t workspace_bytes, int32_t *status, ember_stream_t stream);
+
+/* Attention of several tokens per sequence: rows cu[b] .. cu[b+1] - 1 of q
+ * (device int32 [B+1], 0 <= cu[b] <= cu[b+1] <= n) are the last positions of
+ * sequence seqs[b] (NULL: sequence b), which holds lens[b] keys with theirs: row
+ * cu[b] + i stands at p = lens[b] - (cu[b+1] - cu[b]) + i and sees key j when
+ * j <= p and, for window > 0, j > p - window or j < sinks.  A row with p < 0
+ * gives out 0 and lse -inf; rows outside every sequence stay as they were.
+ * out, lse [n][n_heads], window, sinks and scale as in ember_paged_decode.
+ * A K or V value that is not finite makes not only the rows that see its key
+ * but also others of their tile not finite, as a product with zero does.
+ * Host errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ember_status ember_paged_prefill(const ember_paged_kv *kv, const void *q, int64_t ld_q, int32_t n,
+                                 int32_t B, int32_t n_heads, const int32_t *seqs,
+                                 const int32_t *cu, const int32_t *lens, int32_t window,
+                                 int32_t sinks, float scale, void *out, int64_t ld_out, float *lse,
+                                 int32_t *status, ember_stream_t stream);
+
 /* ---- kernel-level entry points used by the parity tests ------------------ */
 
 /* The RoPE-and-store step of the K cache write, alone: for each of n_tok rows
