@@ -4,20 +4,29 @@
 // tokens), and optionally lse = log sum_j exp(scale q . k_j).
 //
 // Bound: the bytes of the visible K and V rows, each read once for the G query
-// heads that share a kv head.  So the heads of a group are the rows of one
-// 16-row matrix product (rows >= G are zero) and a warp takes 16 keys at a
-// time: S = Q K^T, one pass with the running maximum and sum of each row, and
-// O += P V, all in registers (mma.m16n8k16, f32 accumulators).
+// heads that share a kv head.  So the heads of a group are the 8 (or 2 x 8)
+// columns of the products and 16 keys, or 16 dimensions, their rows: S^T = K Q^T,
+// one pass with a running maximum and sum per head, O^T += V^T P^T, all in
+// registers (mma.m16n8k16, f32 accumulators; P^T becomes an operand by
+// movmatrix).  With the heads as the 16 rows half the work was on rows that most
+// groups lack.  The maximum that scores are taken against moves (and O, l are
+// rescaled) only when a score passes it by more than 2^8, so that most blocks
+// need one vote instead of a reduction over the lanes.
 //
-// Work split: the visible keys of every (sequence, kv head) form a list of
-// 16-key blocks, the lists of all sequences stand one behind the other, and
-// CTA c takes the c-th equal share of that whole line, so a ragged batch and
-// one long sequence both keep every SM busy to the end.  A CTA's warps take
-// its blocks in turn; each warp streams its own blocks through a ring of
-// cp.async copies that runs on across sequence boundaries.  A (sequence, kv
-// head) whose blocks lie in one CTA is finished there; otherwise its CTAs leave
-// (m, l, O) partials that a second small kernel joins in CTA order, so the
-// result depends on the lengths and the device only.
+// Work split, two ways:
+//   line     the visible keys of every (sequence, kv head) form a list of blocks,
+//            the lists of all sequences stand one behind the other, and CTA c
+//            takes the c-th equal share of that whole line, so a ragged batch
+//            and one long sequence both keep every SM busy to the end.  A CTA's
+//            warps take its blocks in turn; each warp streams its own blocks
+//            through a ring of cp.async copies that runs on across sequence
+//            boundaries.  A (sequence, kv head) whose blocks lie in one CTA is
+//            finished there; otherwise its CTAs leave (m, l, O) partials that a
+//            second small kernel joins in CTA order.
+//   cluster  for few, short sequences: the CTAs of one thread-block cluster share
+//            one (sequence, kv head) and join through distributed shared memory,
+//            with no scan of the lengths, no workspace and no second kernel.
+// Either way the result depends on the inputs, the form and the device only.
 //
 // Blocks start at multiples of 16 keys and pages hold a multiple of 16 rows,
 // so a block lies in one page.  Rows that the query does not see are filled
@@ -37,19 +46,25 @@ namespace {
 
 constexpr int PD_WARPS = 4;
 constexpr int PD_THREADS = PD_WARPS * 32;
-constexpr int PD_KEYS = 16;          // keys of a block
-constexpr int PD_STAGES = 3;         // ring stages of a warp
+constexpr int PD_STAGES = 2;         // ring stages of a warp
 constexpr int PD_MIN_BLOCKS = 8;     // blocks of a CTA at least (two per warp)
-constexpr int PD_CTAS_PER_SM = 2;
+constexpr int pd_ctas_per_sm(int ht) { return ht == 1 ? 3 : 2; }   // registers: 168 or 255 a thread
+constexpr int PD_MAX_CLUSTER = 8;     // CTAs of a cluster (a power of two)
+constexpr int PD_CLUSTER_BLOCKS = 8;  // blocks of a warp in cluster form at most
+constexpr int PD_MAX_CTAS = 1024;    // grid at most (the join's weights stand in shared memory)
+// Keys of a block: 8 KB of K and V rows either way.
+template <int DP>
+constexpr int PD_KEYS = DP == 64 ? 32 : 16;
 
 // Blocks of one sequence: [0, ns) hold its sinks, the rest its window.
 struct SeqBlocks {
     int n, ns, wb;       // blocks, blocks of the sinks, first block of the window
     int end, first, sinks;
     bool zero;           // nothing visible: the output is zero
-    __device__ __forceinline__ int key0(int i) const { return PD_KEYS * (i < ns ? i : wb + i - ns); }
+    __device__ __forceinline__ int index(int i) const { return i < ns ? i : wb + i - ns; }
 };
 
+template <int KEYS>
 __device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int b, bool report) {
     SeqBlocks r;
     r.n = 0;
@@ -74,49 +89,72 @@ __device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int b,
     r.end = v.end;
     r.first = v.first;
     r.sinks = v.sinks;
-    r.ns = (v.sinks + PD_KEYS - 1) / PD_KEYS;
-    r.wb = max(v.first / PD_KEYS, r.ns);
-    r.n = r.ns + (v.end + PD_KEYS - 1) / PD_KEYS - r.wb;
+    r.ns = (v.sinks + KEYS - 1) / KEYS;
+    r.wb = max(v.first / KEYS, r.ns);
+    r.n = r.ns + (v.end + KEYS - 1) / KEYS - r.wb;
     return r;
 }
 
-// Sum over the block's threads and exclusive prefix (s holds PD_WARPS + 1 ints).
-__device__ __forceinline__ int block_scan(int v, int* s, int& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = v;
+// Blocks of the whole line divided over `ctas` CTAs: CTA c takes [lo(c), lo(c + 1)).
+// (The launcher keeps the line below 2^30 blocks.)
+struct Shares {
+    unsigned total, ctas, each;
+    __device__ __forceinline__ Shares(unsigned t, unsigned grid) {
+        total = t;
+        const unsigned most = (t + PD_MIN_BLOCKS - 1) / PD_MIN_BLOCKS;
+        each = (t + min(grid, most) - 1) / min(grid, most);
+        ctas = (t + each - 1) / each;
+    }
+    __device__ __forceinline__ unsigned lo(unsigned c) const { return min(total, c * each); }
+};
+
+// Every warp by itself: the line's length, and in which sequence block `x`
+// (known once the length is: at(total)) lies.  Four sequences a lane, 128 at a time.
+constexpr int PD_SCAN = 4;
+template <int KEYS>
+__device__ __forceinline__ unsigned scan_chunk(const PagedDecodeArgs& a, int b0, bool report, int (&n)[PD_SCAN],
+                                               unsigned& before) {
+    const int lane = threadIdx.x & 31;
+    unsigned own = 0;
+#pragma unroll
+    for (int e = 0; e < PD_SCAN; ++e) {
+        const int b = b0 + PD_SCAN * lane + e;
+        n[e] = b < a.B ? seq_blocks<KEYS>(a, b, report).n : 0;
+        own += n[e];
+    }
+    unsigned incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(FULL_MASK, incl, o);
+        const unsigned y = __shfl_up_sync(FULL_MASK, incl, o);
         if (lane >= o) incl += y;
     }
-    __syncthreads();
-    if (lane == 31) s[warp] = incl;
-    __syncthreads();
-    int base = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < PD_WARPS; ++w) {
-        if (w < warp) base += s[w];
-        total += s[w];
-    }
-    return base + incl - v;
+    before = incl - own;
+    return __shfl_sync(FULL_MASK, incl, 31);
 }
 
-// Blocks of the whole line divided over `ctas` CTAs: CTA c takes [lo(c), lo(c + 1)).
-struct Shares {
-    long long total;     // blocks of all (sequence, kv head)s
-    int ctas;            // CTAs that take part
-    __device__ __forceinline__ Shares(long long t, int grid) {
-        total = t;
-        const long long most = (t + PD_MIN_BLOCKS - 1) / PD_MIN_BLOCKS;
-        ctas = (int)min((long long)grid, max(1ll, most));
-    }
-    __device__ __forceinline__ long long lo(int c) const { return total * c / ctas; }
-    // the CTA whose share holds block x
-    __device__ __forceinline__ int holder(long long x) const {
-        return (int)(((x + 1) * ctas - 1) / total);
-    }
-};
+// The workspace: a record for each CTA of the grid, then two partials for each.
+__device__ __forceinline__ float* partials(const PagedDecodeArgs& a, int grid) { return a.ws + 4 * (size_t)grid; }
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .u32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
+                 : "=f"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr, uint32_t rank) {
+    float2 v;
+    asm volatile(
+        "{\n\t.reg .u32 r;\n\tmapa.shared::cluster.u32 r, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [r];\n\t}"
+        : "=f"(v.x), "=f"(v.y)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // A place in the line: block `i` of kv head g of sequence b.
 struct Place {
@@ -124,72 +162,102 @@ struct Place {
     SeqBlocks s;
 };
 
-template <int DP>
+template <int DP, int HT>
 struct PdSmem {
-    static constexpr int TILE = PD_KEYS * DP * 2;                // one K (or V) block
+    static constexpr int TILE = PD_KEYS<DP> * DP * 2;             // one K (or V) block
     static constexpr int RING = PD_WARPS * PD_STAGES * 2 * TILE;
-    static constexpr int SCR = 16 * DP * 4;                       // the merge's O rows
+    static constexpr int ROW = DP + 4;                            // a head's O row in the merge: no bank conflicts
+    static constexpr int SCR = 2 * 8 * HT * ROW * 4;              // O of two warps
     static constexpr int TOTAL = RING + SCR;
 };
 
-template <class E, int DP>
-__global__ void __launch_bounds__(PD_THREADS, PD_CTAS_PER_SM) k_paged_decode(PagedDecodeArgs a) {
-    constexpr int KS = DP / 16, NT = DP / 8, C8 = DP / 8;
-    using L = PdSmem<DP>;
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// HT: tiles of 8 query heads (1 up to G = 8, else 2)
+template <class E, int DP, int HT, bool CLUSTER>
+__global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode(PagedDecodeArgs a) {
+    constexpr int KEYS = PD_KEYS<DP>, NSUB = KEYS / 16;
+    constexpr int KS = DP / 16, C8 = DP / 8;
+    using L = PdSmem<DP, HT>;
     extern __shared__ __align__(1024) uint8_t sm[];
-    __shared__ int s_scan[PD_WARPS];
-    __shared__ int s_find[4];
-    __shared__ float s_m[PD_WARPS][16], s_l[PD_WARPS][16];
+    __shared__ float s_m[PD_WARPS][8 * HT], s_l[PD_WARPS][8 * HT], s_M[8 * HT], s_L[8 * HT];
     float* s_o = reinterpret_cast<float*>(sm + L::RING);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g4 = lane >> 2, q4 = lane & 3;
     const int D = a.c.D, NKV = a.c.NKV, G = a.NH / NKV;
     pdl_wait();
-    pdl_trigger();   // after the wait: the join kernel may then read the caller's lengths at once
 
-    // ---- the whole line's length, and this CTA's first place in it ----
-    long long line = 0;
-    for (int b0 = 0; b0 < a.B; b0 += PD_THREADS) {
-        const int b = b0 + tid;
-        int n = 0, total;
-        if (b < a.B) n = seq_blocks(a, b, blockIdx.x == 0).n;
-        block_scan(n, s_scan, total);
-        line += total;
-    }
-    line *= NKV;
-    // rows of sequences without keys
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-        if (seq_blocks(a, b, false).zero) {
-            uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (long long)b * a.ld_out);
-            for (int e = tid; e < a.NH * D / 2; e += PD_THREADS) o[e] = 0u;
-            if (a.lse)
-                for (int e = tid; e < a.NH; e += PD_THREADS) a.lse[(long long)b * a.NH + e] = -INFINITY;
-        }
-    if (line == 0) return;
-    const Shares share(line, gridDim.x);
-    if ((int)blockIdx.x >= share.ctas) return;
-    const long long lo = share.lo(blockIdx.x), hi = share.lo(blockIdx.x + 1);
-    {
-        long long run = 0;
-        for (int b0 = 0; b0 < a.B; b0 += PD_THREADS) {
-            const int b = b0 + tid;
-            int n = 0, total;
-            if (b < a.B) n = seq_blocks(a, b, false).n;
-            const long long at = run + (long long)block_scan(n, s_scan, total) * NKV;
-            if (n > 0 && at <= lo && lo < at + (long long)n * NKV) {
-                s_find[0] = b;
-                s_find[1] = (int)((lo - at) / n);
-                s_find[2] = (int)((lo - at) % n);
-            }
-            run += (long long)total * NKV;
-        }
-        __syncthreads();
-    }
+    auto zero_row = [&](int b, int h0, int h1) {       // heads [h0, h1) of a sequence without keys
+        uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (long long)b * a.ld_out);
+        for (int e = h0 * D / 2 + tid; e < h1 * D / 2; e += PD_THREADS) o[e] = 0u;
+        if (a.lse)
+            for (int e = h0 + tid; e < h1; e += PD_THREADS) a.lse[(long long)b * a.NH + e] = -INFINITY;
+    };
+
+    // ---- this CTA's blocks [lo, hi) and the first one's place ----
+    unsigned lo, hi;
     Place cur;
-    cur.b = s_find[0];
-    cur.g = s_find[1];
-    cur.i = s_find[2];
-    cur.s = seq_blocks(a, cur.b, false);
+    if (CLUSTER) {
+        cur.b = blockIdx.z;
+        cur.g = blockIdx.y;
+        cur.s = seq_blocks<KEYS>(a, cur.b, blockIdx.x == 0 && cur.g == 0 && tid == 0);
+        if (cur.s.n == 0) {                            // so for the whole cluster
+            if (cur.s.zero && blockIdx.x == 0) zero_row(cur.b, cur.g * G, (cur.g + 1) * G);
+            return;
+        }
+        // a block for each warp at least; CTAs left over join in with nothing, so that a
+        // smaller cluster (a table with room for fewer blocks) gives the same bits
+        const unsigned each = max(PD_WARPS, (cur.s.n + PD_MAX_CLUSTER - 1) / PD_MAX_CLUSTER);
+        lo = min((unsigned)cur.s.n, blockIdx.x * each);
+        hi = min((unsigned)cur.s.n, lo + each);
+        cur.i = (int)lo;
+    } else {
+        int n[PD_SCAN];
+        unsigned line = 0, before = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32 * PD_SCAN) line += scan_chunk<KEYS>(a, b0, blockIdx.x == 0 && warp == 0, n, before);
+        line *= NKV;
+        int4* record = reinterpret_cast<int4*>(a.ws) + blockIdx.x;   // what the join finds of this CTA's last segment
+        const Shares share(max(1u, line), gridDim.x);
+        if (line == 0 || blockIdx.x >= share.ctas) {
+            pdl_trigger();
+            if (tid == 0) *record = make_int4(0, 0, 0, 0);
+            for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+                if (seq_blocks<KEYS>(a, b, false).zero) zero_row(b, 0, a.NH);
+            return;
+        }
+        lo = share.lo(blockIdx.x);
+        hi = share.lo(blockIdx.x + 1);
+        unsigned run = 0;
+        for (int b0 = 0;; b0 += 32 * PD_SCAN) {
+            // one chunk: its counts are still in the registers
+            const unsigned total = a.B <= 32 * PD_SCAN ? line / NKV : scan_chunk<KEYS>(a, b0, false, n, before);
+            if (lo < run + total * NKV) {
+                unsigned at = run + before * NKV;
+                int b = -1;
+                unsigned first = 0;
+#pragma unroll
+                for (int e = 0; e < PD_SCAN; ++e) {
+                    if (lo >= at && lo < at + (unsigned)n[e] * NKV) {
+                        b = b0 + PD_SCAN * lane + e;
+                        first = at;
+                    }
+                    at += (unsigned)n[e] * NKV;
+                }
+                const int src = __ffs(__ballot_sync(FULL_MASK, b >= 0)) - 1;
+                cur.b = __shfl_sync(FULL_MASK, b, src);
+                cur.s = seq_blocks<KEYS>(a, cur.b, false);
+                const unsigned x = lo - __shfl_sync(FULL_MASK, first, src);
+                cur.g = (int)(x / (unsigned)cur.s.n);
+                cur.i = (int)(x - (unsigned)cur.g * (unsigned)cur.s.n);
+                break;
+            }
+            run += total * NKV;
+        }
+    }
 
     auto advance = [&](Place& p, int by) {   // to the block `by` further on (inside the line)
         p.i += by;
@@ -197,47 +265,59 @@ __global__ void __launch_bounds__(PD_THREADS, PD_CTAS_PER_SM) k_paged_decode(Pag
             p.i -= p.s.n;
             if (++p.g == NKV) {
                 p.g = 0;
-                do p.s = seq_blocks(a, ++p.b, false);
+                do p.s = seq_blocks<KEYS>(a, ++p.b, false);
                 while (p.s.n == 0 && p.b + 1 < a.B);
             }
         }
     };
 
     // ---- copies: warp w takes blocks lo + w, lo + w + PD_WARPS, ... ----
-    const int mine = (int)max(0ll, (hi - lo - warp + PD_WARPS - 1) / PD_WARPS);
+    const int mine = ((int)(hi - lo) - warp + PD_WARPS - 1) / PD_WARPS;
     uint8_t* ring = sm + warp * (PD_STAGES * 2 * L::TILE);
     const uint32_t ring_u = sa_u32(ring);
     Place ld = cur;
-    int ld_page = 0;
-    auto page_of = [&](const Place& p) {
-        const int seq = a.seqs ? a.seqs[p.b] : p.b;
-        return a.c.table[(size_t)seq * a.c.width + (p.s.key0(p.i) >> a.c.page_shift)];
+    int ld_page[NSUB];                       // pages of its 16-key parts, looked up one block ahead
+    auto look_up = [&]() {
+        const int seq = a.seqs ? a.seqs[ld.b] : ld.b;
+        const int key0 = KEYS * ld.s.index(ld.i);
+#pragma unroll
+        for (int u = 0; u < NSUB; ++u) {
+            const int k0 = key0 + 16 * u;    // a part that nobody sees has no page
+            const bool any = k0 < ld.s.end && (k0 + 16 > ld.s.first || k0 < ld.s.sinks);
+            ld_page[u] = any ? a.c.table[(size_t)seq * a.c.width + (k0 >> a.c.page_shift)] : 0;
+        }
     };
     if (mine > 0) {
         advance(ld, warp);
-        ld_page = page_of(ld);
+        look_up();
     }
     auto issue = [&](int j) {                // the warp's j-th block -> stage j % PD_STAGES
         if (j < mine) {
             const uint32_t kd = ring_u + (uint32_t)(j % PD_STAGES) * 2 * L::TILE, vd = kd + L::TILE;
-            const int key0 = ld.s.key0(ld.i);
-            const bool ok = ld_page >= 0 && ld_page < a.c.n_pages;   // a bad page reads as zeros
-            if (!ok && lane == 0) raise_status(a.status, EMBER_ERR_INVALID_ARG);
-            const long long base = ok ? (long long)ld_page * a.c.page_stride + (long long)ld.g * a.c.head_stride +
-                                            (long long)(key0 & ((1 << a.c.page_shift) - 1)) * a.c.row_stride
-                                      : 0;
+            const int key0 = KEYS * ld.s.index(ld.i);
             const int c = lane % C8;
 #pragma unroll
-            for (int r = lane / C8; r < PD_KEYS; r += 32 / C8) {
-                const int key = key0 + r;
-                const bool in = ok && c * 8 < D && key < ld.s.end && (key >= ld.s.first || key < ld.s.sinks);
-                const long long off = in ? base + (long long)r * a.c.row_stride + c * 8 : 0;
-                cp_async16(kd + q_off<DP>(r, c), a.c.k + off, in);
-                cp_async16(vd + q_off<DP>(r, c), a.c.v + off, in);
+            for (int u = 0; u < NSUB; ++u) {
+                const int k0 = key0 + 16 * u;
+                const bool ok = ld_page[u] >= 0 && ld_page[u] < a.c.n_pages;   // a bad page reads as zeros
+                if (!ok && lane == 0) raise_status(a.status, EMBER_ERR_INVALID_ARG);
+                const long long base =
+                    ok ? (long long)ld_page[u] * a.c.page_stride + (long long)ld.g * a.c.head_stride +
+                             (long long)(k0 & ((1 << a.c.page_shift) - 1)) * a.c.row_stride + c * 8
+                       : 0;
+#pragma unroll
+                for (int i = 0; i < 16 * C8 / 32; ++i) {
+                    const int r = lane / C8 + i * (32 / C8);
+                    const int key = k0 + r;
+                    const bool in = ok && c * 8 < D && key < ld.s.end && (key >= ld.s.first || key < ld.s.sinks);
+                    const long long off = in ? base + (long long)r * a.c.row_stride : 0;
+                    cp_async16(kd + q_off<DP>(16 * u + r, c), a.c.k + off, in);
+                    cp_async16(vd + q_off<DP>(16 * u + r, c), a.c.v + off, in);
+                }
             }
             if (j + 1 < mine) {
                 advance(ld, PD_WARPS);
-                ld_page = page_of(ld);
+                look_up();
             }
         }
         cp_async_commit();
@@ -248,250 +328,389 @@ __global__ void __launch_bounds__(PD_THREADS, PD_CTAS_PER_SM) k_paged_decode(Pag
     // ---- segments: the CTA's blocks of one (sequence, kv head) after another ----
     const float sc = a.scale * LOG2E;
     int j = 0;                               // the warp's next block
-    long long at = lo;                       // the line's block at the segment's start
-    while (at < hi) {
-        const int seg = (int)min((long long)(cur.s.n - cur.i), hi - at);   // its blocks in this CTA
-        // q of the group's heads as A fragments (rows >= G zero)
-        uint32_t qa[KS][4];
+    unsigned at = lo;                        // the line's block at the segment's start
+    do {
+        const int seg = min(cur.s.n - cur.i, (int)(hi - at));   // its blocks in this CTA (0: a cluster's CTA without work)
+        // q of the group's heads as B fragments (columns >= G zero)
+        uint32_t qb[HT][KS][2];
         const uint16_t* q = a.q + (long long)cur.b * a.ld_q + (long long)cur.g * G * D;
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk)
+        for (int t = 0; t < HT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = g4 + (e & 1) * 8, col = 16 * kk + (e >> 1) * 8 + 2 * q4;
-                qa[kk][e] = row < G && col < D ? *reinterpret_cast<const uint32_t*>(q + row * D + col) : 0u;
-            }
-        float o[NT][4];
+            for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-        for (int dn = 0; dn < NT; ++dn) o[dn][0] = o[dn][1] = o[dn][2] = o[dn][3] = 0.f;
-        float m0 = SOFTMAX_FLOOR, m1 = SOFTMAX_FLOOR, l0 = 0.f, l1 = 0.f;   // rows g4, g4 + 8
-        const long long seg_end = at + seg;
-        for (; lo + warp + (long long)j * PD_WARPS < seg_end; ++j) {
-            const int blk = cur.i + (int)(lo + warp + (long long)j * PD_WARPS - at);
+                for (int e = 0; e < 2; ++e) {
+                    const int h = 8 * t + g4, col = 16 * kk + 8 * e + 2 * q4;
+                    qb[t][kk][e] = h < G && col < D ? *reinterpret_cast<const uint32_t*>(q + h * D + col) : 0u;
+                }
+        // O^T: rows (dimensions) 16 i + g4 and + 8, columns (heads) 8 t + 2 q4 and + 1
+        float o[HT][KS][4];
+        float m[HT][2], l[HT][2];            // of heads 8 t + 2 q4 + e; l over this lane's keys
+#pragma unroll
+        for (int t = 0; t < HT; ++t) {
+#pragma unroll
+            for (int i = 0; i < KS; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+            m[t][0] = m[t][1] = SOFTMAX_FLOOR;
+            l[t][0] = l[t][1] = 0.f;
+        }
+        const unsigned seg_end = at + seg;
+        for (; lo + warp + j * PD_WARPS < seg_end; ++j) {
+            const int blk = cur.i + (int)(lo + warp + j * PD_WARPS - at);
             issue(j + PD_STAGES - 1);
             cp_async_wait<PD_STAGES - 1>();
             __syncwarp();
             const uint32_t kt = ring_u + (uint32_t)(j % PD_STAGES) * 2 * L::TILE, vt = kt + L::TILE;
-            const int key0 = cur.s.key0(blk);
-            float s[2][4];
+            const int key0 = KEYS * cur.s.index(blk);
+            const int mi = lane >> 3, r8 = lane & 7;
+            float s[NSUB][HT][4];            // S^T: keys g4 and g4 + 8 of each 16
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-            const int mi = lane >> 3;
+            for (int u = 0; u < NSUB; ++u)
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                uint32_t b0, b1, b2, b3;
-                ldsm4(kt + q_off<DP>((mi >> 1) * 8 + (lane & 7), 2 * kk + (mi & 1)), b0, b1, b2, b3);
-                E::mma(s[0], qa[kk], b0, b1);
-                E::mma(s[1], qa[kk], b2, b3);
-            }
-            float mx0 = m0, mx1 = m1;
+                for (int t = 0; t < HT; ++t) s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+                for (int u = 0; u < NSUB; ++u) {
+                    uint32_t ka[4];
+                    ldsm4(kt + q_off<DP>(16 * u + (mi & 1) * 8 + r8, 2 * kk + (mi >> 1)), ka[0], ka[1], ka[2], ka[3]);
+#pragma unroll
+                    for (int t = 0; t < HT; ++t) E::mma(s[u][t], ka, qb[t][kk][0], qb[t][kk][1]);
+                }
             // every key of the block visible: below the end, and all in the window or all among the sinks
-            const bool whole = key0 + PD_KEYS <= cur.s.end && (key0 >= cur.s.first || key0 + PD_KEYS <= cur.s.sinks);
+            const bool whole = key0 + KEYS <= cur.s.end && (key0 >= cur.s.first || key0 + KEYS <= cur.s.sinks);
+            bool up = false;
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int u = 0; u < NSUB; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    s[nt][i] *= sc;
+                    bool in = true;
                     if (!whole) {
-                        const int key = key0 + nt * 8 + 2 * q4 + (i & 1);
-                        if (key >= cur.s.end || (key < cur.s.first && key >= cur.s.sinks)) s[nt][i] = -INFINITY;
+                        const int key = key0 + 16 * u + g4 + 8 * (i >> 1);
+                        in = key < cur.s.end && (key >= cur.s.first || key < cur.s.sinks);
                     }
-                    if (i < 2) mx0 = fmaxf(mx0, s[nt][i]);
-                    else mx1 = fmaxf(mx1, s[nt][i]);
+#pragma unroll
+                    for (int t = 0; t < HT; ++t) {
+                        s[u][t][i] = in ? s[u][t][i] * sc : -INFINITY;
+                        up |= s[u][t][i] > m[t][i & 1] + 8.f;
+                    }
                 }
-            mx0 = fmaxf(mx0, __shfl_xor_sync(FULL_MASK, mx0, 1));
-            mx0 = fmaxf(mx0, __shfl_xor_sync(FULL_MASK, mx0, 2));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, 1));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, 2));
-            const float sc0 = ex2(m0 - mx0), sc1 = ex2(m1 - mx1);
-            float p[2][4];
+            if (__any_sync(FULL_MASK, up)) {
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+                for (int t = 0; t < HT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[nt][i] = ex2(s[nt][i] - (i < 2 ? mx0 : mx1));
-            l0 = l0 * sc0 + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
-            l1 = l1 * sc1 + ((p[0][2] + p[0][3]) + (p[1][2] + p[1][3]));
-            m0 = mx0;
-            m1 = mx1;
+                    for (int e = 0; e < 2; ++e) {
+                        float x = m[t][e];
 #pragma unroll
-            for (int dn = 0; dn < NT; ++dn) {
-                o[dn][0] *= sc0; o[dn][1] *= sc0;
-                o[dn][2] *= sc1; o[dn][3] *= sc1;
-            }
-            const uint32_t pa[4] = {E::pack(p[0][0], p[0][1]), E::pack(p[0][2], p[0][3]), E::pack(p[1][0], p[1][1]),
-                                    E::pack(p[1][2], p[1][3])};
-            uint32_t pr[4];
-            if (E::bf16) {                   // what the first rounding left
+                        for (int u = 0; u < NSUB; ++u) x = fmaxf(x, fmaxf(s[u][t][e], s[u][t][e + 2]));
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    pr[i] = E::pack(p[i >> 1][2 * (i & 1)] - E::lo(pa[i]), p[i >> 1][2 * (i & 1) + 1] - E::hi(pa[i]));
+                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, d));
+                        const float f = ex2(m[t][e] - x);
+                        m[t][e] = x;
+                        l[t][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < KS; ++i) {
+                            o[t][i][e] *= f;
+                            o[t][i][e + 2] *= f;
+                        }
+                    }
             }
 #pragma unroll
-            for (int dn = 0; dn < NT; dn += 2) {
-                uint32_t r0, r1, r2, r3;
-                ldsm4t(vt + q_off<DP>((mi & 1) * 8 + (lane & 7), dn + (mi >> 1)), r0, r1, r2, r3);
-                E::mma(o[dn], pa, r0, r1);
-                E::mma(o[dn + 1], pa, r2, r3);
-                if (E::bf16) {
-                    E::mma(o[dn], pr, r0, r1);
-                    E::mma(o[dn + 1], pr, r2, r3);
+            for (int u = 0; u < NSUB; ++u) {
+                uint32_t pb[HT][2], pr[HT][2];   // P^T as B fragments: keys 2 q4, + 1 (and + 8) of head g4
+#pragma unroll
+                for (int t = 0; t < HT; ++t) {
+                    float (&p)[4] = s[u][t];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = ex2(p[i] - m[t][i & 1]);
+                    l[t][0] += p[0] + p[2];
+                    l[t][1] += p[1] + p[3];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t x = E::pack(p[2 * e], p[2 * e + 1]);
+                        pb[t][e] = transpose8x8(x);
+                        if (E::bf16)             // what the rounding left
+                            pr[t][e] = transpose8x8(E::pack(p[2 * e] - E::lo(x), p[2 * e + 1] - E::hi(x)));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    uint32_t va[4];
+                    ldsm4t(vt + q_off<DP>(16 * u + (mi >> 1) * 8 + r8, 2 * i + (mi & 1)), va[0], va[1], va[2], va[3]);
+#pragma unroll
+                    for (int t = 0; t < HT; ++t) {
+                        E::mma(o[t][i], va, pb[t][0], pb[t][1]);
+                        if (E::bf16) E::mma(o[t][i], va, pr[t][0], pr[t][1]);
+                    }
                 }
             }
             __syncwarp();                    // the stage is read: the next copy may fill it
         }
 
-        // ---- merge the warps' states, in warp order ----
-        l0 += __shfl_xor_sync(FULL_MASK, l0, 1);
-        l0 += __shfl_xor_sync(FULL_MASK, l0, 2);
-        l1 += __shfl_xor_sync(FULL_MASK, l1, 1);
-        l1 += __shfl_xor_sync(FULL_MASK, l1, 2);
-        __syncthreads();                     // the previous segment's merge is read
-        if (q4 == 0) {
-            s_m[warp][g4] = m0;
-            s_m[warp][g4 + 8] = m1;
-            s_l[warp][g4] = l0;
-            s_l[warp][g4 + 8] = l1;
+        // ---- merge the warps' states: 2 and 3 into 0 and 1, then 1 into 0 ----
+#pragma unroll
+        for (int t = 0; t < HT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(FULL_MASK, l[t][e], d);
+        __syncthreads();                     // the previous segment's output is written
+        if (g4 == 0) {
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    s_m[warp][8 * t + 2 * q4 + e] = m[t][e];
+                    s_l[warp][8 * t + 2 * q4 + e] = l[t][e];
+                }
         }
         __syncthreads();
-        float M0 = SOFTMAX_FLOOR, M1 = SOFTMAX_FLOOR, L0 = 0.f, L1 = 0.f;
 #pragma unroll
-        for (int v = 0; v < PD_WARPS; ++v) {
-            M0 = fmaxf(M0, s_m[v][g4]);
-            M1 = fmaxf(M1, s_m[v][g4 + 8]);
-        }
+        for (int t = 0; t < HT; ++t)
 #pragma unroll
-        for (int v = 0; v < PD_WARPS; ++v) {
-            L0 += s_l[v][g4] * ex2(s_m[v][g4] - M0);
-            L1 += s_l[v][g4 + 8] * ex2(s_m[v][g4 + 8] - M1);
-        }
-        const float f0 = ex2(m0 - M0), f1 = ex2(m1 - M1);
-        for (int v = 0; v < PD_WARPS; ++v) {
-            if (warp == v) {
+            for (int e = 0; e < 2; ++e) {
+                const int h = 8 * t + 2 * q4 + e;
+                float M = s_m[0][h];
 #pragma unroll
-                for (int dn = 0; dn < NT; ++dn)
+                for (int v = 1; v < PD_WARPS; ++v) M = fmaxf(M, s_m[v][h]);
+                const float f = ex2(m[t][e] - M);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int row = g4 + 8 * h;
-                        if (row < G) {
-                            float2* d = reinterpret_cast<float2*>(s_o + row * DP + dn * 8 + 2 * q4);
-                            float2 x = v ? *d : make_float2(0.f, 0.f);
-                            x.x = fmaf(o[dn][2 * h], h ? f1 : f0, x.x);
-                            x.y = fmaf(o[dn][2 * h + 1], h ? f1 : f0, x.y);
-                            *d = x;
-                        }
-                    }
+                for (int i = 0; i < KS; ++i) {
+                    o[t][i][e] *= f;
+                    o[t][i][e + 2] *= f;
+                }
             }
-            __syncthreads();
+        auto store_o = [&](int buf) {
+            float* d = s_o + buf * 8 * HT * L::ROW;
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        d[(8 * t + 2 * q4 + (e & 1)) * L::ROW + 16 * i + g4 + 8 * (e >> 1)] = o[t][i][e];
+        };
+        auto add_o = [&](int buf) {
+            const float* d = s_o + buf * 8 * HT * L::ROW;
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[t][i][e] += d[(8 * t + 2 * q4 + (e & 1)) * L::ROW + 16 * i + g4 + 8 * (e >> 1)];
+        };
+        if (warp >= 2) store_o(warp - 2);
+        __syncthreads();
+        if (warp < 2) add_o(warp);
+        if (warp == 1) store_o(1);
+        __syncthreads();
+        if (warp == 0) {
+            add_o(1);
+            store_o(0);
         }
-        const bool complete = seg == cur.s.n;
-        if (warp == 0 && q4 == 0) {          // the rows' m and l of the whole segment
-            s_m[0][g4] = M0;
-            s_m[0][g4 + 8] = M1;
-            s_l[0][g4] = L0;
-            s_l[0][g4 + 8] = L1;
+        if (warp == 1 && lane < 8 * HT) {    // the heads' m and l of the whole segment
+            float M = s_m[0][lane], S = 0.f;
+#pragma unroll
+            for (int v = 1; v < PD_WARPS; ++v) M = fmaxf(M, s_m[v][lane]);
+#pragma unroll
+            for (int v = 0; v < PD_WARPS; ++v) S += s_l[v][lane] * ex2(s_m[v][lane] - M);
+            s_M[lane] = M;
+            s_L[lane] = S;
         }
         __syncthreads();
+        if (CLUSTER) break;
+        const bool complete = seg == cur.s.n;
         if (complete) {
             uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (long long)cur.b * a.ld_out + (long long)cur.g * G * D);
             for (int e = tid; e < G * D / 2; e += PD_THREADS) {
                 const int row = e / (D / 2), d = 2 * (e - row * (D / 2));
-                const float l = s_l[0][row];
+                const float l = s_L[row];
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                out[e] = E::pack(s_o[row * DP + d] * inv, s_o[row * DP + d + 1] * inv);
+                out[e] = E::pack(s_o[row * L::ROW + d] * inv, s_o[row * L::ROW + d + 1] * inv);
             }
             if (a.lse && tid < G)
                 a.lse[(long long)cur.b * a.NH + cur.g * G + tid] =
-                    s_l[0][tid] == 0.f ? -INFINITY : s_m[0][tid] * LN2 + logf(s_l[0][tid]);
+                    s_L[tid] == 0.f ? -INFINITY : s_M[tid] * LN2 + logf(s_L[tid]);
         } else {
             // slot 0: the segment reaches back to the CTA's first block, slot 1: it begins inside
-            float* ws = a.ws + (size_t)(2 * blockIdx.x + (at == lo ? 0 : 1)) * G * (D + 2);
+            float* ws = partials(a, gridDim.x) + (size_t)(2 * blockIdx.x + (at == lo ? 0 : 1)) * G * (D + 2);
             for (int e = tid; e < G * (D + 2); e += PD_THREADS) {
                 const int row = e / (D + 2), d = e - row * (D + 2);
-                ws[e] = d == 0 ? s_m[0][row] : d == 1 ? s_l[0][row] : s_o[row * DP + d - 2];
+                ws[e] = d == 0 ? s_M[row] : d == 1 ? s_L[row] : s_o[row * L::ROW + d - 2];
             }
         }
+        if (tid == 0 && seg_end == hi) {     // does a segment begin here that later CTAs go on with?
+            const bool begins = cur.i == 0 && !complete;
+            const int parts = begins ? (int)((at + cur.s.n - 1) / (hi - lo)) - (int)blockIdx.x + 1 : 0;
+            reinterpret_cast<int4*>(a.ws)[blockIdx.x] = make_int4(cur.b, cur.g, parts, at == lo ? 0 : 1);
+        }
         at = seg_end;
-        if (at < hi) advance(cur, seg);      // on to the next (sequence, kv head)
-    }
+        if (at >= hi) break;
+        advance(cur, seg);                   // on to the next (sequence, kv head)
+    } while (true);
     cp_async_wait<0>();
+    pdl_trigger();                           // late: the join's blocks would take issue slots meanwhile
+    if (!CLUSTER) {
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+            if (seq_blocks<KEYS>(a, b, false).zero) zero_row(b, 0, a.NH);
+        return;
+    }
+
+    // ---- cluster: every CTA joins a share of the group's output ----
+    cluster_sync_all();
+    const uint32_t um = sa_u32(s_M), ul = sa_u32(s_L), uo = sa_u32(s_o);
+    const unsigned C = gridDim.x;
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (long long)cur.b * a.ld_out + (long long)cur.g * G * D);
+    for (int e = blockIdx.x * PD_THREADS + tid; e < G * D / 2; e += C * PD_THREADS) {
+        const int row = e / (D / 2), d = 2 * (e - row * (D / 2));
+        float cm[PD_MAX_CLUSTER], cl[PD_MAX_CLUSTER], M = SOFTMAX_FLOOR, S = 0.f;
+        float2 co[PD_MAX_CLUSTER], x = make_float2(0.f, 0.f);
+#pragma unroll
+        for (unsigned r = 0; r < PD_MAX_CLUSTER; ++r)
+            if (r < C) {
+                cm[r] = ld_cluster(um + 4 * row, r);
+                cl[r] = ld_cluster(ul + 4 * row, r);
+                co[r] = ld_cluster2(uo + 4 * (row * L::ROW + d), r);
+            }
+#pragma unroll
+        for (unsigned r = 0; r < PD_MAX_CLUSTER; ++r)
+            if (r < C) M = fmaxf(M, cm[r]);
+#pragma unroll
+        for (unsigned r = 0; r < PD_MAX_CLUSTER; ++r)
+            if (r < C) {
+                const float f = ex2(cm[r] - M);
+                S = fmaf(cl[r], f, S);
+                x.x = fmaf(co[r].x, f, x.x);
+                x.y = fmaf(co[r].y, f, x.y);
+            }
+        const float inv = S == 0.f ? 0.f : 1.f / S;
+        out[e] = E::pack(x.x * inv, x.y * inv);
+        if (a.lse && d == 0)
+            a.lse[(long long)cur.b * a.NH + cur.g * G + row] = S == 0.f ? -INFINITY : M * LN2 + logf(S);
+    }
+    cluster_sync_all();                      // no CTA leaves while another reads its shared memory
 }
 
-// Joins the partials of each (sequence, kv head) that several CTAs share:
-// block (g, b), in CTA order.
+// Joins the partials of each (sequence, kv head) that several CTAs share, in
+// CTA order.  Block (c, h) reads CTA c's record and, when a segment begins in
+// that CTA and goes on in later ones, joins head h of its group.  Threads take
+// four dimensions each and the partials in turn; the weights of all partials
+// are found at once before.
+constexpr int PJ_WARPS = 8;
+constexpr int PJ_THREADS = PJ_WARPS * 32;
+
 template <class E>
-__global__ void __launch_bounds__(PD_THREADS) k_paged_join(PagedDecodeArgs a, int grid) {
-    __shared__ int s_scan[PD_WARPS];
-    __shared__ float s_M[16], s_L[16];
-    const int g = blockIdx.x, b = blockIdx.y;
-    const int tid = threadIdx.x;
-    const int D = a.c.D, NKV = a.c.NKV, G = a.NH / NKV;
-    // The first kernel triggers after its own wait, so what the caller passed
-    // is complete here; its partials are after pdl_wait.
-    long long before = 0, line = 0;
-    for (int b0 = 0; b0 < a.B; b0 += PD_THREADS) {
-        const int x = b0 + tid;
-        const int n = x < a.B ? seq_blocks(a, x, false).n : 0;
-        int total, upto;
-        block_scan(x < b ? n : 0, s_scan, upto);
-        block_scan(n, s_scan, total);
-        before += upto;
-        line += total;
-    }
-    pdl_wait();                              // on every path: what follows in the stream waits for this kernel only
+__global__ void __launch_bounds__(PJ_THREADS) k_paged_join(PagedDecodeArgs a, int grid) {
+    __shared__ float s_w[PD_MAX_CTAS], s_red[2 * PJ_WARPS];
+    __shared__ float4 s_o[PJ_THREADS];
+    const int c0 = blockIdx.x, h = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int D = a.c.D, G = a.NH / a.c.NKV;
+    pdl_wait();
     pdl_trigger();
-    const int n = seq_blocks(a, b, false).n;
-    if (n == 0) return;
-    const Shares share(line * NKV, grid);
-    const long long s0 = before * NKV + (long long)g * n, s1 = s0 + n;
-    const int c0 = share.holder(s0), c1 = share.holder(s1 - 1);
-    if (c0 == c1) return;                    // finished by that CTA
-    auto slot = [&](int c) {
-        return a.ws + (size_t)(2 * c + (s0 <= share.lo(c) ? 0 : 1)) * G * (D + 2);
-    };
-    if (tid < G) {
-        float M = SOFTMAX_FLOOR, L = 0.f;
-        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(slot(c) + tid * (D + 2)));
-        for (int c = c0; c <= c1; ++c) {
-            const float* p = slot(c) + tid * (D + 2);
-            L += __ldcg(p + 1) * ex2(__ldcg(p) - M);
+    const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.ws) + c0);
+    const int b = rec.x, g = rec.y, parts = rec.z;
+    if (parts == 0) return;
+    // partial i: slot 0 of its CTA, but slot 1 of the first when the segment begins inside it
+    const float* base = partials(a, grid) + (size_t)h * (D + 2);
+    const size_t slot = (size_t)G * (D + 2);
+    auto part = [&](int i) { return base + (2 * (size_t)(c0 + i) + (i == 0 ? rec.w : 0)) * slot; };
+    float M = SOFTMAX_FLOOR, m0 = SOFTMAX_FLOOR, l0 = 0.f;
+    for (int i = tid; i < parts; i += PJ_THREADS) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i)));
+        if (i == tid) {
+            m0 = ml.x;
+            l0 = ml.y;
         }
-        s_M[tid] = M;
-        s_L[tid] = L;
+        s_w[i] = ml.x;
+        M = fmaxf(M, ml.x);
     }
+    M = warp_max(M);
+    if (lane == 0) s_red[warp] = M;
     __syncthreads();
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (long long)b * a.ld_out + (long long)g * G * D);
-    for (int e = tid; e < G * D / 2; e += PD_THREADS) {
-        const int row = e / (D / 2), d = 2 * (e - row * (D / 2));
-        float x = 0.f, y = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const float* p = slot(c) + row * (D + 2);
-            const float f = ex2(__ldcg(p) - s_M[row]);
-            x = fmaf(__ldcg(p + 2 + d), f, x);
-            y = fmaf(__ldcg(p + 3 + d), f, y);
-        }
-        const float inv = s_L[row] == 0.f ? 0.f : 1.f / s_L[row];
-        out[e] = E::pack(x * inv, y * inv);
+#pragma unroll
+    for (int w = 0; w < PJ_WARPS; ++w) M = fmaxf(M, s_red[w]);
+    float L = 0.f;
+    for (int i = tid; i < parts; i += PJ_THREADS) {
+        const float f = ex2((i == tid ? m0 : s_w[i]) - M);
+        s_w[i] = f;
+        L += (i == tid ? l0 : __ldcg(part(i) + 1)) * f;
     }
-    if (a.lse && tid < G)
-        a.lse[(long long)b * a.NH + g * G + tid] = s_L[tid] == 0.f ? -INFINITY : s_M[tid] * LN2 + logf(s_L[tid]);
+    L = warp_sum(L);
+    if (lane == 0) s_red[PJ_WARPS + warp] = L;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < PJ_WARPS; ++w) L += s_red[PJ_WARPS + w];
+    const int quads = D / 4, turns = PJ_THREADS / quads;   // threads of a partial, partials at a time
+    const int d = 4 * (tid % quads), t0 = tid / quads;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = t0; i < parts; i += turns) {
+        const float2* p = reinterpret_cast<const float2*>(part(i) + 2 + d);
+        const float2 u = __ldcg(p), v = __ldcg(p + 1);
+        const float f = s_w[i];
+        o.x = fmaf(u.x, f, o.x);
+        o.y = fmaf(u.y, f, o.y);
+        o.z = fmaf(v.x, f, o.z);
+        o.w = fmaf(v.y, f, o.w);
+    }
+    s_o[tid] = o;
+    __syncthreads();
+    if (tid < quads) {
+        for (int t = 1; t < turns; ++t) {
+            const float4 y = s_o[tid + t * quads];
+            o.x += y.x;
+            o.y += y.y;
+            o.z += y.z;
+            o.w += y.w;
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        uint2* out = reinterpret_cast<uint2*>(a.out + (long long)b * a.ld_out + (long long)(g * G + h) * D + d);
+        *out = make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
+        if (a.lse && tid == 0)
+            a.lse[(long long)b * a.NH + g * G + h] = L == 0.f ? -INFINITY : M * LN2 + logf(L);
+    }
+}
+
+int pd_grid_full(int sms, int G) { return min(PD_MAX_CTAS, sms * pd_ctas_per_sm(G <= 8 ? 1 : 2)); }
+
+template <class E, int DP, int HT>
+cudaError_t launch_ht(const PagedDecodeArgs& a, int sms, cudaStream_t s) {
+    constexpr int SMEM = PdSmem<DP, HT>::TOTAL;
+    const int G = a.NH / a.c.NKV;
+    // the most blocks that the table allows a sequence
+    const long long keys = (long long)a.c.width << a.c.page_shift;
+    const long long seen = a.window > 0 ? min(keys, (long long)a.window + a.sinks + 2 * PD_KEYS<DP>) : keys;
+    const long long blocks = (seen + PD_KEYS<DP> - 1) / PD_KEYS<DP>;
+    const long long pairs = (long long)a.B * a.c.NKV;
+    int C = 1;
+    while (C < PD_MAX_CLUSTER && C * PD_WARPS < blocks) C *= 2;
+    if (pairs * C <= pd_grid_full(sms, G) && blocks <= C * PD_WARPS * PD_CLUSTER_BLOCKS) {
+        auto k = k_paged_decode<E, DP, HT, true>;
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        return launch_cluster_k(k, dim3(C, a.c.NKV, a.B), dim3(PD_THREADS), SMEM, C, s, a);
+    }
+    auto k = k_paged_decode<E, DP, HT, false>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    const int grid = (int)min((long long)pd_grid_full(sms, G), (blocks * pairs + PD_MIN_BLOCKS - 1) / PD_MIN_BLOCKS);
+    const cudaError_t r = launch_k(k, dim3(grid), dim3(PD_THREADS), SMEM, s, a);
+    if (r != cudaSuccess || grid == 1) return r;
+    return launch_k(k_paged_join<E>, dim3(grid - 1, G), dim3(PJ_THREADS), 0, s, a, grid);
 }
 
 template <class E, int DP>
 cudaError_t launch_dp(const PagedDecodeArgs& a, int sms, cudaStream_t s) {
-    const cudaError_t e = cudaFuncSetAttribute(k_paged_decode<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               PdSmem<DP>::TOTAL);
-    if (e != cudaSuccess) return e;
-    const int grid = sms * PD_CTAS_PER_SM;
-    const cudaError_t r = launch_k(k_paged_decode<E, DP>, dim3(grid), dim3(PD_THREADS), PdSmem<DP>::TOTAL, s, a);
-    if (r != cudaSuccess) return r;
-    return launch_k(k_paged_join<E>, dim3(a.c.NKV, a.B), dim3(PD_THREADS), 0, s, a, grid);
+    return a.NH / a.c.NKV <= 8 ? launch_ht<E, DP, 1>(a, sms, s) : launch_ht<E, DP, 2>(a, sms, s);
 }
 
 }  // namespace
 
 size_t paged_decode_ws(int NKV, int G, int D, int sms) {
     (void)NKV;
-    return (size_t)sms * PD_CTAS_PER_SM * 2 * G * (D + 2) * sizeof(float);
+    return (size_t)pd_grid_full(sms, G) * (4 + 2 * (size_t)G * (D + 2)) * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int sms, cudaStream_t s) {

@@ -177,6 +177,9 @@ ember_status ember_paged_decode(const ember_paged_kv* kv, const void* q, int64_t
     if (B == 0) return EMBER_OK;
     if (B > 65535) PG_FAIL(EMBER_ERR_UNSUPPORTED, "B > 65535");
     if (!seqs && B > kv->n_seqs) PG_FAIL(EMBER_ERR_INVALID_ARG, "B > n_seqs without seqs");
+    if (kv->n_kv_heads > 65535 ||
+        (double)B * kv->n_kv_heads * ((double)kv->table_width * kv->page_size / 16) > (double)(1 << 30))
+        PG_FAIL(EMBER_ERR_UNSUPPORTED, "B * n_kv_heads * table_width * page_size > 2^34");
     int sms = 0;
     cudaError_t e = device_sms(&sms);
     if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "no device: %s", cudaGetErrorString(e));
