@@ -508,7 +508,12 @@ struct PagedPrefillArgs {
     float* lse;                  // [n][NH] or nullptr
     int* status;
 };
-cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, cudaStream_t s);
+// The same on tcgen05 (paged_prefill_tc.cu), through TMA maps over the pages
+// (paged_prefill_maps; false if the driver rejects the layout).
+// launch_paged_prefill picks it for calls with rows enough.
+bool paged_prefill_maps(const PagedView& c, void* mk, void* mv);
+cudaError_t launch_paged_prefill_tc(const PagedPrefillArgs& a, const void* mk, const void* mv, cudaStream_t s);
 
 // out[c][r] = in[r][c] for 16-bit elements
 void launch_transpose16(const uint16_t* in, uint16_t* out, int rows, int cols, cudaStream_t s);

@@ -73,4 +73,59 @@ constexpr float SOFTMAX_FLOOR = -3.0e38f;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
+// ---- prefill: query rows of a ragged batch ----
+// One sequence's query rows and keys; nq == 0 when it has none or is invalid.
+struct SeqRows {
+    int row0, nq, len, seq;
+};
+__device__ __forceinline__ SeqRows seq_rows(const PagedPrefillArgs& a, int b, bool report) {
+    SeqRows r{0, 0, 0, 0};
+    r.seq = a.seqs ? a.seqs[b] : b;
+    if (r.seq < 0) return r;
+    const int r0 = a.cu[b], r1 = a.cu[b + 1];
+    const int len = a.lens[b];
+    int err = 0;
+    if (r.seq >= a.c.n_seqs || r0 < 0 || r1 < r0 || r1 > a.n) err = EMBER_ERR_INVALID_ARG;
+    else if (len < 0 || len > ((long long)a.c.width << a.c.page_shift)) err = EMBER_ERR_CAPACITY;
+    if (err) {
+        if (report) raise_status(a.status, err);
+        return r;
+    }
+    r.row0 = r0;
+    r.nq = r1 - r0;
+    r.len = len;
+    return r;
+}
+
+// The x-th tile of `tokens` query tokens over all sequences: its sequence and
+// its number there (sequence -1: there are fewer tiles).  Every warp finds it by
+// itself, 32 sequences at a time.
+struct RowTile {
+    int b, i;
+};
+__device__ __forceinline__ RowTile find_row_tile(const PagedPrefillArgs& a, int tokens, int x, bool report) {
+    const int lane = threadIdx.x & 31;
+    RowTile r{-1, 0};
+    long long run = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int n = b0 + lane < a.B ? (seq_rows(a, b0 + lane, report).nq + tokens - 1) / tokens : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL_MASK, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const long long at = run + incl - n;
+        const unsigned hit = __ballot_sync(FULL_MASK, n > 0 && at <= x && x < at + n);
+        if (hit && r.b < 0) {
+            const int src = __ffs(hit) - 1;
+            r.b = b0 + src;
+            r.i = __shfl_sync(FULL_MASK, (int)(x - at), src);
+            if (!report) break;              // the reporting warp looks at every sequence
+        }
+        run += __shfl_sync(FULL_MASK, incl, 31);
+    }
+    return r;
+}
+
 }  // namespace ember

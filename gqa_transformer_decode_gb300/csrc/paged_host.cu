@@ -219,9 +219,6 @@ ember_status ember_paged_prefill(const ember_paged_kv* kv, const void* q, int64_
     if (!cu) PG_FAIL(EMBER_ERR_INVALID_ARG, "cu is NULL");
     if (B > (1 << 20) || kv->n_kv_heads > 65535) PG_FAIL(EMBER_ERR_UNSUPPORTED, "B > 2^20 or n_kv_heads > 65535");
     if (!seqs && B > kv->n_seqs) PG_FAIL(EMBER_ERR_INVALID_ARG, "B > n_seqs without seqs");
-    int sms = 0;
-    cudaError_t e = device_sms(&sms);
-    if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "no device: %s", cudaGetErrorString(e));
     a.q = static_cast<const uint16_t*>(q);
     a.ld_q = ld_q;
     a.n = n;
@@ -237,7 +234,7 @@ ember_status ember_paged_prefill(const ember_paged_kv* kv, const void* q, int64_
     a.ld_out = ld_out;
     a.lse = lse;
     a.status = status;
-    e = launch_paged_prefill(a, sms, (cudaStream_t)stream);
+    const cudaError_t e = launch_paged_prefill(a, (cudaStream_t)stream);
     if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "prefill launch failed: %s", cudaGetErrorString(e));
     return EMBER_OK;
 }

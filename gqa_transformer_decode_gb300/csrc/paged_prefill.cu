@@ -16,29 +16,7 @@ namespace {
 constexpr int PP_THREADS = 128;
 constexpr int PP_ROWS = 64;
 constexpr int PP_KEYS = 64;
-
-// One sequence's query rows and keys; nq == 0 when it has none or is invalid.
-struct SeqRows {
-    int row0, nq, len, seq;
-};
-__device__ __forceinline__ SeqRows seq_rows(const PagedPrefillArgs& a, int b, bool report) {
-    SeqRows r{0, 0, 0, 0};
-    r.seq = a.seqs ? a.seqs[b] : b;
-    if (r.seq < 0) return r;
-    const int r0 = a.cu[b], r1 = a.cu[b + 1];
-    const int len = a.lens[b];
-    int err = 0;
-    if (r.seq >= a.c.n_seqs || r0 < 0 || r1 < r0 || r1 > a.n) err = EMBER_ERR_INVALID_ARG;
-    else if (len < 0 || len > ((long long)a.c.width << a.c.page_shift)) err = EMBER_ERR_CAPACITY;
-    if (err) {
-        if (report) raise_status(a.status, err);
-        return r;
-    }
-    r.row0 = r0;
-    r.nq = r1 - r0;
-    r.len = len;
-    return r;
-}
+constexpr int PP_TC_ROWS = 256;   // (token, head) rows per kv head of a call from which the tcgen05 kernel runs
 
 template <int DP>
 struct PpSmem {
@@ -51,7 +29,6 @@ __global__ void __launch_bounds__(PP_THREADS) k_paged_prefill(PagedPrefillArgs a
     constexpr int KS = DP / 16, NT = DP / 8, C8 = DP / 8;
     using L = PpSmem<DP>;
     extern __shared__ __align__(1024) uint8_t sm[];
-    __shared__ int s_scan[4], s_find[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g4 = lane >> 2, q4 = lane & 3;
     const int D = a.c.D, NKV = a.c.NKV, G = a.NH / NKV, g = blockIdx.y;
@@ -59,39 +36,11 @@ __global__ void __launch_bounds__(PP_THREADS) k_paged_prefill(PagedPrefillArgs a
     pdl_wait();
     pdl_trigger();
 
-    // ---- which sequence and tile ----
-    if (tid == 0) s_find[0] = -1;
-    __syncthreads();
-    int run = 0;
-    for (int b0 = 0; b0 < a.B; b0 += PP_THREADS) {
-        const int b = b0 + tid;
-        const int n = b < a.B ? (seq_rows(a, b, blockIdx.x == 0 && g == 0).nq + QT - 1) / QT : 0;
-        int incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(FULL_MASK, incl, o);
-            if (lane >= o) incl += y;
-        }
-        __syncthreads();
-        if (lane == 31) s_scan[warp] = incl;
-        __syncthreads();
-        int base = run, total = 0;
-        for (int w = 0; w < 4; ++w) {
-            if (w < warp) base += s_scan[w];
-            total += s_scan[w];
-        }
-        const int at = base + incl - n;
-        if (n > 0 && at <= (int)blockIdx.x && (int)blockIdx.x < at + n) {
-            s_find[0] = b;
-            s_find[1] = (int)blockIdx.x - at;
-        }
-        run += total;
-    }
-    __syncthreads();
-    const int b = s_find[0];
+    const RowTile tile = find_row_tile(a, QT, (int)blockIdx.x, blockIdx.x == 0 && g == 0 && warp == 0);
+    const int b = tile.b;
     if (b < 0) return;
     const SeqRows sr = seq_rows(a, b, false);
-    const int i0 = s_find[1] * QT;                       // first token of the tile
+    const int i0 = tile.i * QT;                       // first token of the tile
     const int tokens = min(QT, sr.nq - i0);
     const int pos0 = sr.len - sr.nq + i0;                // its position (negative: sees nothing)
     const int pos1 = pos0 + tokens - 1;
@@ -259,8 +208,10 @@ cudaError_t launch_dp(const PagedPrefillArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, int sms, cudaStream_t s) {
-    (void)sms;
+cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, cudaStream_t s) {
+    alignas(64) unsigned char mk[128], mv[128];
+    if ((long long)a.n * (a.NH / a.c.NKV) >= PP_TC_ROWS && paged_prefill_maps(a.c, mk, mv))
+        return launch_paged_prefill_tc(a, mk, mv, s);
     if (a.c.bf16) return a.c.D <= 64 ? launch_dp<ElemBf16, 64>(a, s) : launch_dp<ElemBf16, 128>(a, s);
     return a.c.D <= 64 ? launch_dp<ElemF16, 64>(a, s) : launch_dp<ElemF16, 128>(a, s);
 }
