@@ -26,10 +26,13 @@
 // sum over keys of mixed sign is about the output's own rounding; l is summed
 // from the unrounded weights in f32.
 //
-// Warp 0: TMA producer; warp 1: TMEM allocation, edge rows, MMA issue; warps
-// 2-5: tile A; warps 6-9: tile B (a warp reads the TMEM lanes of its index mod
-// 4).  Every mbarrier wait is bounded; a timeout raises EMBER_ERR_TIMEOUT, the
-// CTA drains its copies and frees TMEM.
+// Warps 0-3: tile A; warps 4-7: tile B (a warp reads the TMEM lanes of its index
+// mod 4); warp 8: TMA producer; warp 9: TMEM allocation, edge rows, MMA issue;
+// warps 10 and 11 only complete the warpgroup that gives up registers.  A row's
+// 128 scores stand in registers at once: their maximum, then one fused
+// multiply-add and one exponential each, so a thread needs more registers (200)
+// than the other warps (104).  Every mbarrier wait is bounded; a timeout raises
+// EMBER_ERR_TIMEOUT, the CTA drains its copies and frees TMEM.
 #include <cudaTypedefs.h>
 
 #include "paged.cuh"
@@ -39,7 +42,9 @@ namespace ember {
 
 namespace {
 
-constexpr int PT_THREADS = 320;
+constexpr int PT_THREADS = 384;
+constexpr int PT_TMA = 8, PT_MMA = 9;   // warps
+constexpr int PT_REGS_ROW = 200, PT_REGS_REST = 104;   // 256 * 200 + 128 * 104 = 384 * 168, the launch's share
 constexpr int PT_ROWS = 128;   // rows of a query tile
 constexpr int PT_KEYS = 128;   // keys of a tile
 
@@ -99,6 +104,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     int* sflag = reinterpret_cast<int*>(bar + 8);   // [0] failed, [1] tiles issued, [2] tiles consumed
     uint64_t* kv_full = bar + 10;   // [NSTG]
     uint64_t* kv_empty = bar + 16;  // [NSTG]
+    uint64_t* s_free = bar + 22;    // [2] the row values of S are in registers (P beside S only)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int D = a.c.D, G = a.NH / a.c.NKV, g = blockIdx.y;
@@ -126,6 +132,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 128);
+            mbar_init(&s_free[t], 128);
             mbar_init(&o_full[t], 1);
         }
         for (int s = 0; s < NSTG; ++s) {
@@ -138,7 +145,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 1) {
+    if (warp == PT_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(512u));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -148,7 +155,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 0) {   // ------------------------------------------ TMA producer
+    if (warp >= PT_TMA) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PT_REGS_REST));
+    if (warp == PT_TMA) {   // ------------------------------------- TMA producer
         const int P = 1 << a.c.page_shift;
         const int box = min(P, PT_KEYS);               // rows of a box
         const int boxes = PT_KEYS / box;               // of a tile: lane i < boxes copies box i
@@ -187,7 +196,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             if (fail) sflag[0] = 1;
             sflag[1] = issued;
         }
-    } else if (warp == 1) {   // ----------------------------------- MMA issuer
+    } else if (warp == PT_MMA) {   // ------------------------------ MMA issuer
         constexpr uint32_t type = E::bf16 ? idesc_bf16(0, 0) : idesc_f16(0, 0);
         constexpr uint32_t idS = type | idesc_f16(PT_ROWS, PT_KEYS);
         constexpr uint32_t idO = type | idesc_f16(PT_ROWS, DP) | IDESC_B_MN;
@@ -241,55 +250,93 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             const int s = j % NSTG;
             const bool more = j + 1 < nkt;
             const int s1 = (j + 1) % NSTG;
-            // S_t(j + 1) may overwrite S_t(j): p_full[t] says that its row
-            // values have all been read.  With P over S, P . V(j) goes first.
-            bool in = mbar_wait(&p_full[0], (uint32_t)j & 1u);
-            if (!__all_sync(FULL_MASK, in)) break;
-            if (L::ALIAS && lane == 0) {
-                tc_fence_after();
-                mma_pv(0, s, j > 0);
-            }
-            __syncwarp();
-            if (more) {
-                in = kv_ready(j + 1);
+            bool in = true;
+            if (L::ALIAS) {
+                // P lies over S: P . V(j) of a query tile goes before its S(j + 1)
+                // (MMAs of one thread run in the order of issue)
+                in = mbar_wait(&p_full[0], (uint32_t)j & 1u);
+                if (!__all_sync(FULL_MASK, in)) break;
+                if (lane == 0) {
+                    tc_fence_after();
+                    mma_pv(0, s, j > 0);
+                }
+                __syncwarp();
+                if (more) {
+                    in = kv_ready(j + 1);
+                    if (!__all_sync(FULL_MASK, in)) break;
+                    if (lane == 0) {
+                        tc_fence_after();
+                        mma_s(0, s1);
+                    }
+                    __syncwarp();
+                }
+                in = mbar_wait(&p_full[1], (uint32_t)j & 1u);
+                if (!__all_sync(FULL_MASK, in)) break;
+                if (lane == 0) {
+                    tc_fence_after();
+                    mma_pv(1, s, j > 0);
+                    if (more) mma_s(1, s1);
+                }
+            } else {
+                // S(j + 1) as soon as the rows of S(j) are in registers, while they
+                // are exponentiated
+                if (more) {
+                    in = kv_ready(j + 1);
+                    if (!__all_sync(FULL_MASK, in)) break;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        in = in && mbar_wait(&s_free[t], (uint32_t)j & 1u);
+                        if (!__all_sync(FULL_MASK, in)) break;
+                        if (lane == 0) {
+                            tc_fence_after();
+                            mma_s(t, s1);
+                        }
+                        __syncwarp();
+                    }
+                    if (!__all_sync(FULL_MASK, in)) break;
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    in = in && mbar_wait(&p_full[t], (uint32_t)j & 1u);
+                    if (!__all_sync(FULL_MASK, in)) break;
+                    if (lane == 0) {
+                        tc_fence_after();
+                        mma_pv(t, s, j > 0);
+                    }
+                    __syncwarp();
+                }
                 if (!__all_sync(FULL_MASK, in)) break;
             }
-            if (lane == 0) {
-                tc_fence_after();
-                if (more) mma_s(0, s1);
-                if (!L::ALIAS) mma_pv(0, s, j > 0);
-            }
-            __syncwarp();
-            in = mbar_wait(&p_full[1], (uint32_t)j & 1u);
-            if (!__all_sync(FULL_MASK, in)) break;
-            if (lane == 0) {
-                tc_fence_after();
-                if (L::ALIAS) mma_pv(1, s, j > 0);
-                if (more) mma_s(1, s1);
-                if (!L::ALIAS) mma_pv(1, s, j > 0);
-                umma_commit(&kv_empty[s]);
-            }
+            if (lane == 0) umma_commit(&kv_empty[s]);
             __syncwarp();
         }
         if (lane == 0) {
             if (!ok || j < nkt) sflag[0] = 1;
             sflag[2] = j;
         }
-    } else {   // ------------------------------------------------ softmax warps
+    }
+    } else {   // -------------------------------------------------- softmax warps
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PT_REGS_ROW));
         constexpr float RESCALE = 8.f;
-        const int t = (warp - 2) >> 2;                // query tile: 0 = A, 1 = B
+        const int t = warp >> 2;                      // query tile: 0 = A, 1 = B
         const int qw = warp & 3;                      // TMEM lane quarter of this warp
         const int r = qw * 32 + lane;                 // row within the tile
         const int tok = t * QT + r / G, h = r % G;    // token of the pair, head of the group
         const bool live = r < QT * G && tok < tokens;
         const int qp = pos0 + min(tok, tokens - 1);   // its position (rows that are not live: the last one's)
         const long long row = sr.row0 + i0 + tok;
-        {   // the row's q into its swizzled tile (rows that are not live: zeros)
+        {   // the row's q into its swizzled tile (rows that are not live: zeros); a
+            // negative scale becomes its sign, so that the largest score is the largest product
+            const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
             const uint4* q = reinterpret_cast<const uint4*>(a.q + row * a.ld_q + (long long)(g * G + h) * D);
             uint8_t* d = sm + L::OFF_Q + t * L::TILE + r * 128;
 #pragma unroll
             for (int c = 0; c < DP / 8; ++c) {
-                const uint4 v = live && c * 8 < D ? __ldcg(q + c) : make_uint4(0u, 0u, 0u, 0u);
+                uint4 v = live && c * 8 < D ? __ldcg(q + c) : make_uint4(0u, 0u, 0u, 0u);
+                v.x ^= sign;
+                v.y ^= sign;
+                v.z ^= sign;
+                v.w ^= sign;
                 *reinterpret_cast<uint4*>(d + (c >> 3) * 128 * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -299,77 +346,59 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const uint32_t tS = tmem + L::COL_S + t * 128 + lane_off;
         const uint32_t tO = tmem + L::COL_O + t * DP + lane_off;
         const uint32_t tP = tmem + L::col_p(t) + lane_off;
-        const float sc = a.scale * LOG2E;
-        float m = SOFTMAX_FLOOR, l = 0.f;
+        const float sc = fabsf(a.scale) * LOG2E;
+        float m = SOFTMAX_FLOOR, l = 0.f;             // reference maximum (of s * sc), sum of 2^(s sc - m)
         bool ok = true;
-        // p = 2^(s - m) of the row's 128 scores (masked: 0), packed as pairs
-        // into pk (keys 2c, 2c + 1 in pk[c]); returns their sum, mt = the
-        // largest visible score.  Column c is visible when c < hi and (c >= lo or
-        // c < sk); `masked` is warp-uniform: false when every row sees all.
-        auto emit = [&](float mr, int lo, int hi, int sk, bool masked, float& mt, uint32_t (&pk)[64]) -> float {
-            float rs = 0.f;
-#pragma unroll
-            for (int c0 = 0; c0 < 128; c0 += 64) {
-                uint32_t v[64];
-                tmem_ld32(tS + c0, v);
-                tmem_ld32(tS + c0 + 32, v + 32);
-                tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 64; c += 2) {
-                    float x0 = __uint_as_float(v[c]) * sc, x1 = __uint_as_float(v[c + 1]) * sc;
-                    if (masked) {
-                        const int k = c0 + c;
-                        x0 = k < hi && (k >= lo || k < sk) ? x0 : -INFINITY;
-                        x1 = k + 1 < hi && (k + 1 >= lo || k + 1 < sk) ? x1 : -INFINITY;
-                    }
-                    mt = fmaxf(mt, fmaxf(x0, x1));
-                    const float p0 = ex2(x0 - mr), p1 = ex2(x1 - mr);
-                    rs += p0 + p1;
-                    pk[(c0 + c) / 2] = E::pack(p0, p1);
-                }
-            }
-            return rs;
-        };
         for (int j = 0; j < nkt; ++j) {
             if (!mbar_wait(&s_full[t], (uint32_t)j & 1u)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
+            uint32_t v[PT_KEYS];                      // the row's products, then its weights
+#pragma unroll
+            for (int c = 0; c < PT_KEYS; c += 32) tmem_ld32(tS + c, v + c);
+            tmem_ld_wait();
+            if (!L::ALIAS) {
+                tc_fence_before();
+                mbar_arrive(&s_free[t]);
+            }
+            // column c is visible when c < hi and (c >= lo or c < sk)
             const int key0 = key0_of(j);
             const int hi = qp - key0 + 1;
             const int lo = a.window > 0 ? qp - a.window + 1 - key0 : 0;
             const int sk = a.sinks - key0;
-            const bool masked = !__all_sync(FULL_MASK, hi >= PT_KEYS && (lo <= 0 || sk >= PT_KEYS));
-            if (j == 0) {   // the first tile sets the reference maximum
-                float mt = SOFTMAX_FLOOR;
+            if (!__all_sync(FULL_MASK, hi >= PT_KEYS && (lo <= 0 || sk >= PT_KEYS))) {
 #pragma unroll
-                for (int c0 = 0; c0 < 128; c0 += 64) {
-                    uint32_t v[64];
-                    tmem_ld32(tS + c0, v);
-                    tmem_ld32(tS + c0 + 32, v + 32);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        const int k = c0 + i;
-                        if (!masked || (k < hi && (k >= lo || k < sk))) mt = fmaxf(mt, __uint_as_float(v[i]) * sc);
-                    }
-                }
-                m = mt;
+                for (int c = 0; c < PT_KEYS; ++c)
+                    if (!(c < hi && (c >= lo || c < sk))) v[c] = 0xff800000u;   // -inf
             }
-            uint32_t pk[64];
-            float mt = SOFTMAX_FLOOR;
-            float rs = emit(m, lo, hi, sk, masked, mt, pk);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < PT_KEYS; c += 8)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mx[i] = fmaxf(mx[i], fmaxf(__uint_as_float(v[c + 2 * i]), __uint_as_float(v[c + 2 * i + 1])));
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+            // the reference moves (and O, l are rescaled) only when the tile's
+            // maximum passes it by more than RESCALE (log2 units): weights stay
+            // below 2^RESCALE
             const bool move = mt > m + RESCALE;
             const bool any_move = __any_sync(FULL_MASK, move);
             float corr = 1.f;
             if (any_move) {
                 const float mnew = move ? mt : m;
-                corr = move ? ex2(m - mnew) : 1.f;
-                float mt2 = SOFTMAX_FLOOR;
-                rs = emit(mnew, lo, hi, sk, masked, mt2, pk);
+                corr = ex2(m - mnew);
                 l *= corr;
                 m = mnew;
+            }
+            float rs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < PT_KEYS; c += 2) {
+                const float p0 = ex2(fmaf(__uint_as_float(v[c]), sc, -m));
+                const float p1 = ex2(fmaf(__uint_as_float(v[c + 1]), sc, -m));
+                rs[(c >> 1) & 3] += p0 + p1;
+                v[c >> 1] = E::pack(p0, p1);
             }
             if (j > 0) {   // P . V(j - 1) must be complete before O is touched or P is rewritten
                 if (!mbar_wait(&o_full[t], (uint32_t)(j - 1) & 1u)) {
@@ -390,11 +419,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 }
             }
 #pragma unroll
-            for (int c = 0; c < 64; c += 16) tmem_st16(tP + c, pk + c);
+            for (int c = 0; c < PT_KEYS / 2; c += 16) tmem_st16(tP + c, v + c);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&p_full[t]);
-            l += rs;
+            l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
         }
         if (ok && nkt > 0 && !mbar_wait(&o_full[t], (uint32_t)(nkt - 1) & 1u)) ok = false;
         if (!ok) sflag[0] = 1;
@@ -432,11 +461,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     __syncthreads();
     pdl_trigger();
     if (threadIdx.x == 0 && sflag[0]) raise_status(a.status, EMBER_ERR_TIMEOUT);
-    if (warp == 0 && lane == 0 && sflag[0]) {
+    if (warp == PT_TMA && lane == 0 && sflag[0]) {
         // drain K/V copies issued but never consumed by the MMA warp
         for (int j = sflag[2]; j < sflag[1]; ++j) (void)mbar_wait(&kv_full[j % NSTG], (uint32_t)(j / NSTG) & 1u);
     }
-    if (warp == 1) {
+    if (warp == PT_MMA) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
     }
