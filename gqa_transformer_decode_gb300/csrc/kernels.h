@@ -509,11 +509,14 @@ struct PagedPrefillArgs {
     int* status;
 };
 cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, cudaStream_t s);
-// The same on tcgen05 (paged_prefill_tc.cu), through TMA maps over the pages
-// (paged_prefill_maps; false if the driver rejects the layout).
+// The same on tcgen05 (paged_prefill_tc.cu; scale > 0), through TMA maps over the
+// queries and the pages (paged_prefill_maps; false if the driver rejects one).
 // launch_paged_prefill picks it for calls with rows enough.
-bool paged_prefill_maps(const PagedView& c, void* mk, void* mv);
-cudaError_t launch_paged_prefill_tc(const PagedPrefillArgs& a, const void* mk, const void* mv, cudaStream_t s);
+struct PagedPrefillMaps {
+    alignas(64) unsigned char q[128], k[128], v[128];
+};
+bool paged_prefill_maps(const PagedPrefillArgs& a, PagedPrefillMaps& m);
+cudaError_t launch_paged_prefill_tc(const PagedPrefillArgs& a, const PagedPrefillMaps& m, cudaStream_t s);
 
 // out[c][r] = in[r][c] for 16-bit elements
 void launch_transpose16(const uint16_t* in, uint16_t* out, int rows, int cols, cudaStream_t s);

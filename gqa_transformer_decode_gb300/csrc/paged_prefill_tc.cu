@@ -52,10 +52,10 @@ template <int DP>
 struct PtSmem {
     static constexpr int KB = DP / 64;                    // 64-element blocks of a row
     static constexpr int TILE = KB * 128 * 128;           // Q tile, K tile or V tile
-    static constexpr int NSTG = DP == 64 ? 4 : 2;
-    static constexpr int OFF_Q = 0;
-    static constexpr int OFF_KV = 2 * TILE;               // stage: K tile, V tile
-    static constexpr int OFF_BAR = OFF_KV + NSTG * 2 * TILE;
+    static constexpr int NS = DP == 64 ? 10 : 5;          // ring slots, a K or a V tile each
+    static constexpr int OFF_Q = 0;                       // Q of tile A, of tile B; at the end the output rows
+    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_BAR = OFF_KV + NS * TILE;
     static constexpr int TOTAL = OFF_BAR + 256 + 1024;    // + barriers, + alignment slack
     // TMEM columns: S_A, S_B (128 f32 each), O_A, O_B (DP f32 each); P (128
     // values, two to a column) in its own columns for DP 64, over S for DP 128
@@ -87,12 +87,38 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, in
         : "memory");
 }
 
+// two f32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    uint64_t r, u, v, w;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(x.x), "f"(x.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(y.x), "f"(y.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(z.x), "f"(z.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(u), "l"(v), "l"(w));
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    uint64_t r, u, v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(x.x), "f"(x.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(y.x), "f"(y.y));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u), "l"(v));
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 template <class E, int DP>
 __global__ void __launch_bounds__(PT_THREADS, 1)
-    k_paged_prefill_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+    k_paged_prefill_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        PagedPrefillArgs a) {
     using L = PtSmem<DP>;
-    constexpr int NSTG = L::NSTG;
+    constexpr int NS = L::NS;
     extern __shared__ uint8_t pt_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pt_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
@@ -101,19 +127,47 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     uint64_t* p_full = bar + 3;     // [2]
     uint64_t* o_full = bar + 5;     // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 7);
-    int* sflag = reinterpret_cast<int*>(bar + 8);   // [0] failed, [1] tiles issued, [2] tiles consumed
-    uint64_t* kv_full = bar + 10;   // [NSTG]
-    uint64_t* kv_empty = bar + 16;  // [NSTG]
-    uint64_t* s_free = bar + 22;    // [2] the row values of S are in registers (P beside S only)
+    int* sflag = reinterpret_cast<int*>(bar + 8);   // failed
+    uint64_t* s_free = bar + 9;     // [2] the row values of S are in registers (P beside S only)
+    uint64_t* kv_full = bar + 11;   // [NS]: slot i % NS holds K (i even) or V (i odd) of key tile i / 2
+    uint64_t* kv_empty = bar + 21;  // [NS]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int D = a.c.D, G = a.NH / a.c.NKV, g = blockIdx.y;
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 128);
+            mbar_init(&s_free[t], 128);
+            mbar_init(&o_full[t], 1);
+        }
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        sflag[0] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == PT_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(512u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    const int D = a.c.D, G = a.NH / a.c.NKV;
     const int QT = PT_ROWS / G;                        // tokens of a query tile
+    // the last tiles see the most keys: those of all kv heads go first
+    const int x = (int)(gridDim.x - 1 - blockIdx.x) / a.c.NKV, g = (int)(gridDim.x - 1 - blockIdx.x) % a.c.NKV;
     pdl_wait();
-    // the last tiles see the most keys: they go first
-    const int x = (int)(gridDim.x - 1 - blockIdx.x);
     const RowTile tile = find_row_tile(a, 2 * QT, x, x == 0 && g == 0 && warp == 0);
-    if (tile.b < 0) return;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (tile.b < 0) {
+        if (warp == PT_MMA) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+        return;
+    }
     const SeqRows sr = seq_rows(a, tile.b, false);
     const int i0 = tile.i * 2 * QT;                    // first token of tile A
     const int tokens = min(2 * QT, sr.nq - i0);
@@ -127,40 +181,19 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     const int nkt = end <= 0 ? 0 : ns + max(0, (end + PT_KEYS - 1) / PT_KEYS - wb);
     auto key0_of = [&](int j) { return PT_KEYS * (j < ns ? j : wb + j - ns); };
 
-    if (threadIdx.x == 0) {
-        mbar_init(q_full, 256);
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], 128);
-            mbar_init(&s_free[t], 128);
-            mbar_init(&o_full[t], 1);
-        }
-        for (int s = 0; s < NSTG; ++s) {
-            mbar_init(&kv_full[s], 1);
-            mbar_init(&kv_empty[s], 1);
-        }
-        sflag[0] = 0;
-        sflag[1] = 0;
-        sflag[2] = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
-    if (warp == PT_MMA) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(512u));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-
     if (warp >= PT_TMA) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PT_REGS_REST));
     if (warp == PT_TMA) {   // ------------------------------------- TMA producer
         const int P = 1 << a.c.page_shift;
         const int box = min(P, PT_KEYS);               // rows of a box
         const int boxes = PT_KEYS / box;               // of a tile: lane i < boxes copies box i
+        if (lane == 0 && nkt > 0) {                    // tokens beyond the sequence's: whatever follows, or zeros
+            mbar_expect_tx(q_full, 2 * L::KB * QT * G * 128);
+            for (int t = 0; t < 2; ++t)
+                for (int kb = 0; kb < L::KB; ++kb)
+                    tma_load_3d(sm + L::OFF_Q + t * L::TILE + kb * 128 * 128, &tmQ, kb * 64, g * G,
+                                sr.row0 + i0 + t * QT, q_full);
+        }
         auto look_up = [&](int j) {                    // the lane's page of tile j; n_pages reads as zeros
             const int k0 = key0_of(j) + lane * box;
             if (lane >= boxes || k0 >= end || (k0 + box <= first && k0 >= sinks)) return a.c.n_pages;
@@ -169,40 +202,42 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             raise_status(a.status, EMBER_ERR_INVALID_ARG);
             return a.c.n_pages;
         };
-        int page = nkt > 0 ? look_up(0) : 0;
+        int page = nkt > 0 ? look_up(0) : 0, next = 0;
         int issued = 0;
         bool fail = false;
-        for (; issued < nkt; ++issued) {
-            const int s = issued % NSTG;
-            if (issued >= NSTG && !mbar_wait(&kv_empty[s], (uint32_t)(issued / NSTG - 1) & 1u)) fail = true;
+        for (; issued < 2 * nkt; ++issued) {
+            const int s = issued % NS, j = issued >> 1;
+            const bool is_v = issued & 1;
+            if (!is_v && j + 1 < nkt) next = look_up(j + 1);
+            if (issued >= NS && !mbar_wait(&kv_empty[s], (uint32_t)(issued / NS - 1) & 1u)) fail = true;
             if (__any_sync(FULL_MASK, fail)) {
                 fail = true;
                 break;
             }
-            if (lane == 0) mbar_expect_tx(&kv_full[s], 2 * L::TILE);
+            if (lane == 0) mbar_expect_tx(&kv_full[s], L::TILE);
             __syncwarp();
             if (lane < boxes) {
-                const int row = (key0_of(issued) + lane * box) & (P - 1);
-                uint8_t* kd = sm + L::OFF_KV + s * 2 * L::TILE + lane * box * 128;
+                const int row = (key0_of(j) + lane * box) & (P - 1);
+                uint8_t* d = sm + L::OFF_KV + s * L::TILE + lane * box * 128;
 #pragma unroll
-                for (int kb = 0; kb < L::KB; ++kb) {
-                    tma_load_4d(kd + kb * 128 * 128, &tmK, kb * 64, row, g, page, &kv_full[s]);
-                    tma_load_4d(kd + L::TILE + kb * 128 * 128, &tmV, kb * 64, row, g, page, &kv_full[s]);
-                }
+                for (int kb = 0; kb < L::KB; ++kb)
+                    tma_load_4d(d + kb * 128 * 128, is_v ? &tmV : &tmK, kb * 64, row, g, page, &kv_full[s]);
             }
-            if (issued + 1 < nkt) page = look_up(issued + 1);
+            if (is_v) page = next;
         }
-        if (lane == 0) {
-            if (fail) sflag[0] = 1;
-            sflag[1] = issued;
+        if (fail && lane == 0) {
+            sflag[0] = 1;
+            // the copies in flight land before the block ends (none waits for more than the last NS)
+            (void)mbar_wait(q_full, 0);
+            for (int i = max(0, issued - NS); i < issued; ++i) (void)mbar_wait(&kv_full[i % NS], (uint32_t)(i / NS) & 1u);
         }
     } else if (warp == PT_MMA) {   // ------------------------------ MMA issuer
         constexpr uint32_t type = E::bf16 ? idesc_bf16(0, 0) : idesc_f16(0, 0);
         constexpr uint32_t idS = type | idesc_f16(PT_ROWS, PT_KEYS);
         constexpr uint32_t idO = type | idesc_f16(PT_ROWS, DP) | IDESC_B_MN;
-        auto mma_s = [&](int t, int s) {   // S_t = Q_t . K(stage s)^T
+        auto mma_s = [&](int t, int i) {   // S_t = Q_t . K(slot of i)^T
             const uint32_t q0 = smem_u32(sm + L::OFF_Q + t * L::TILE);
-            const uint32_t k0 = smem_u32(sm + L::OFF_KV + s * 2 * L::TILE);
+            const uint32_t k0 = smem_u32(sm + L::OFF_KV + (i % NS) * L::TILE);
 #pragma unroll
             for (int kb = 0; kb < L::KB; ++kb)
 #pragma unroll
@@ -211,21 +246,25 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                               sdesc_sw128(k0 + kb * 128 * 128 + k * 32), idS, (kb | k) ? 1u : 0u);
             umma_commit(&s_full[t]);
         };
-        auto mma_pv = [&](int t, int s, bool acc) {   // O_t += P_t (TMEM) . V(stage s)
-            const uint32_t v0 = smem_u32(sm + L::OFF_KV + s * 2 * L::TILE + L::TILE);
+        auto mma_pv = [&](int t, int i, bool acc) {   // O_t += P_t (TMEM) . V(slot of i)
+            const uint32_t v0 = smem_u32(sm + L::OFF_KV + (i % NS) * L::TILE);
 #pragma unroll
             for (int k = 0; k < PT_KEYS / 16; ++k)
                 umma_f16_ts(tmem + L::COL_O + t * DP, tmem + L::col_p(t) + k * 8,
                             sdesc_mn_sw128(v0 + k * 16 * 128, 128 * 128), idO, (acc || k) ? 1u : 0u);
             umma_commit(&o_full[t]);
         };
-        // waits for K and V of tile j; V rows that nobody sees become zeros
-        auto kv_ready = [&](int j) {
-            const int s = j % NSTG;
-            if (!mbar_wait(&kv_full[s], (uint32_t)(j / NSTG) & 1u)) return false;
+        auto wait_all = [&](uint64_t* b, int parity) {
+            return __all_sync(FULL_MASK, mbar_wait(b, (uint32_t)parity & 1u)) != 0;
+        };
+        auto k_ready = [&](int j) { return wait_all(&kv_full[2 * j % NS], 2 * j / NS); };
+        // V of tile j; rows that nobody sees become zeros
+        auto v_ready = [&](int j) {
+            const int s = (2 * j + 1) % NS;
+            if (!wait_all(&kv_full[s], (2 * j + 1) / NS)) return false;
             const int key0 = key0_of(j);
             if (key0 + PT_KEYS > end || (key0 < first && key0 + PT_KEYS > sinks)) {
-                uint8_t* v = sm + L::OFF_KV + s * 2 * L::TILE + L::TILE;
+                uint8_t* v = sm + L::OFF_KV + s * L::TILE;
                 for (int i = lane; i < PT_KEYS * 8 * L::KB; i += 32) {   // a 16-byte piece of a row each
                     const int r = i / (8 * L::KB), c = i % (8 * L::KB), key = key0 + r;
                     if (key >= end || (key < first && key >= sinks))
@@ -237,83 +276,65 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             }
             return true;
         };
-        bool ok = mbar_wait(q_full, 0) && (nkt == 0 || kv_ready(0));
-        ok = __all_sync(FULL_MASK, ok);
+        // lane 0 issues f() after everything the warp has waited for
+        auto issue = [&](auto f) {
+            if (lane == 0) {
+                tc_fence_after();
+                f();
+            }
+            __syncwarp();
+        };
         int j = 0;
-        if (ok && nkt > 0 && lane == 0) {
-            tc_fence_after();
-            mma_s(0, 0);
-            mma_s(1, 0);
-        }
-        __syncwarp();
+        bool ok = nkt == 0 || (wait_all(q_full, 0) && k_ready(0));
+        if (ok && nkt > 0)
+            issue([&] {
+                mma_s(0, 0);
+                mma_s(1, 0);
+                umma_commit(&kv_empty[0]);
+            });
         for (; ok && j < nkt; ++j) {
-            const int s = j % NSTG;
             const bool more = j + 1 < nkt;
-            const int s1 = (j + 1) % NSTG;
-            bool in = true;
+            const int iv = 2 * j + 1, ik = 2 * j + 2;   // V(j), K(j + 1)
             if (L::ALIAS) {
                 // P lies over S: P . V(j) of a query tile goes before its S(j + 1)
                 // (MMAs of one thread run in the order of issue)
-                in = mbar_wait(&p_full[0], (uint32_t)j & 1u);
-                if (!__all_sync(FULL_MASK, in)) break;
-                if (lane == 0) {
-                    tc_fence_after();
-                    mma_pv(0, s, j > 0);
-                }
-                __syncwarp();
+                if (!(ok = v_ready(j) && wait_all(&p_full[0], j))) break;
+                issue([&] { mma_pv(0, iv, j > 0); });
                 if (more) {
-                    in = kv_ready(j + 1);
-                    if (!__all_sync(FULL_MASK, in)) break;
-                    if (lane == 0) {
-                        tc_fence_after();
-                        mma_s(0, s1);
+                    if (!(ok = k_ready(j + 1))) break;
+                    issue([&] { mma_s(0, ik); });
+                }
+                if (!(ok = wait_all(&p_full[1], j))) break;
+                issue([&] {
+                    mma_pv(1, iv, j > 0);
+                    umma_commit(&kv_empty[iv % NS]);
+                    if (more) {
+                        mma_s(1, ik);
+                        umma_commit(&kv_empty[ik % NS]);
                     }
-                    __syncwarp();
-                }
-                in = mbar_wait(&p_full[1], (uint32_t)j & 1u);
-                if (!__all_sync(FULL_MASK, in)) break;
-                if (lane == 0) {
-                    tc_fence_after();
-                    mma_pv(1, s, j > 0);
-                    if (more) mma_s(1, s1);
-                }
+                });
             } else {
                 // S(j + 1) as soon as the rows of S(j) are in registers, while they
                 // are exponentiated
                 if (more) {
-                    in = kv_ready(j + 1);
-                    if (!__all_sync(FULL_MASK, in)) break;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        in = in && mbar_wait(&s_free[t], (uint32_t)j & 1u);
-                        if (!__all_sync(FULL_MASK, in)) break;
-                        if (lane == 0) {
-                            tc_fence_after();
-                            mma_s(t, s1);
-                        }
-                        __syncwarp();
-                    }
-                    if (!__all_sync(FULL_MASK, in)) break;
+                    if (!(ok = k_ready(j + 1) && wait_all(&s_free[0], j))) break;
+                    issue([&] { mma_s(0, ik); });
+                    if (!(ok = wait_all(&s_free[1], j))) break;
+                    issue([&] {
+                        mma_s(1, ik);
+                        umma_commit(&kv_empty[ik % NS]);
+                    });
                 }
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    in = in && mbar_wait(&p_full[t], (uint32_t)j & 1u);
-                    if (!__all_sync(FULL_MASK, in)) break;
-                    if (lane == 0) {
-                        tc_fence_after();
-                        mma_pv(t, s, j > 0);
-                    }
-                    __syncwarp();
-                }
-                if (!__all_sync(FULL_MASK, in)) break;
+                if (!(ok = v_ready(j) && wait_all(&p_full[0], j))) break;
+                issue([&] { mma_pv(0, iv, j > 0); });
+                if (!(ok = wait_all(&p_full[1], j))) break;
+                issue([&] {
+                    mma_pv(1, iv, j > 0);
+                    umma_commit(&kv_empty[iv % NS]);
+                });
             }
-            if (lane == 0) umma_commit(&kv_empty[s]);
-            __syncwarp();
         }
-        if (lane == 0) {
-            if (!ok || j < nkt) sflag[0] = 1;
-            sflag[2] = j;
-        }
+        if (!ok && lane == 0) sflag[0] = 1;
     }
     } else {   // -------------------------------------------------- softmax warps
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PT_REGS_ROW));
@@ -325,28 +346,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const bool live = r < QT * G && tok < tokens;
         const int qp = pos0 + min(tok, tokens - 1);   // its position (rows that are not live: the last one's)
         const long long row = sr.row0 + i0 + tok;
-        {   // the row's q into its swizzled tile (rows that are not live: zeros); a
-            // negative scale becomes its sign, so that the largest score is the largest product
-            const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
-            const uint4* q = reinterpret_cast<const uint4*>(a.q + row * a.ld_q + (long long)(g * G + h) * D);
-            uint8_t* d = sm + L::OFF_Q + t * L::TILE + r * 128;
-#pragma unroll
-            for (int c = 0; c < DP / 8; ++c) {
-                uint4 v = live && c * 8 < D ? __ldcg(q + c) : make_uint4(0u, 0u, 0u, 0u);
-                v.x ^= sign;
-                v.y ^= sign;
-                v.z ^= sign;
-                v.w ^= sign;
-                *reinterpret_cast<uint4*>(d + (c >> 3) * 128 * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(q_full);
-        }
         const uint32_t lane_off = (uint32_t)(qw * 32) << 16;
         const uint32_t tS = tmem + L::COL_S + t * 128 + lane_off;
         const uint32_t tO = tmem + L::COL_O + t * DP + lane_off;
         const uint32_t tP = tmem + L::col_p(t) + lane_off;
-        const float sc = fabsf(a.scale) * LOG2E;
+        const float sc = a.scale * LOG2E;             // > 0
         float m = SOFTMAX_FLOOR, l = 0.f;             // reference maximum (of s * sc), sum of 2^(s sc - m)
         bool ok = true;
         for (int j = 0; j < nkt; ++j) {
@@ -378,8 +382,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             for (int c = 0; c < PT_KEYS; c += 8)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    mx[i] = fmaxf(mx[i], fmaxf(__uint_as_float(v[c + 2 * i]), __uint_as_float(v[c + 2 * i + 1])));
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                    mx[i] = max3(mx[i], __uint_as_float(v[c + 2 * i]), __uint_as_float(v[c + 2 * i + 1]));
+            const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
             // the reference moves (and O, l are rescaled) only when the tile's
             // maximum passes it by more than RESCALE (log2 units): weights stay
             // below 2^RESCALE
@@ -392,13 +396,17 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 l *= corr;
                 m = mnew;
             }
-            float rs[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
+            float2 rs[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rs[i] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < PT_KEYS; c += 2) {
-                const float p0 = ex2(fmaf(__uint_as_float(v[c]), sc, -m));
-                const float p1 = ex2(fmaf(__uint_as_float(v[c + 1]), sc, -m));
-                rs[(c >> 1) & 3] += p0 + p1;
-                v[c >> 1] = E::pack(p0, p1);
+                float2 p = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, m2);
+                p.x = ex2(p.x);
+                p.y = ex2(p.y);
+                rs[(c >> 1) & 3] = add2(rs[(c >> 1) & 3], p);
+                v[c >> 1] = E::pack(p.x, p.y);
             }
             if (j > 0) {   // P . V(j - 1) must be complete before O is touched or P is rewritten
                 if (!mbar_wait(&o_full[t], (uint32_t)(j - 1) & 1u)) {
@@ -423,35 +431,44 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&p_full[t]);
-            l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+            const float2 r2 = add2(add2(rs[0], rs[1]), add2(rs[2], rs[3]));
+            l += r2.x + r2.y;
         }
         if (ok && nkt > 0 && !mbar_wait(&o_full[t], (uint32_t)(nkt - 1) & 1u)) ok = false;
         if (!ok) sflag[0] = 1;
         tc_fence_after();
         if (ok) {
+            // through the row's own part of the Q tile (no product reads it any more)
+            // into whole rows: neighbouring lanes write neighbouring 16 bytes
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint16_t* out = a.out + row * a.ld_out + (long long)(g * G + h) * D;
+            uint8_t* d = sm + L::OFF_Q + t * L::TILE + qw * (32 * DP * 2);
 #pragma unroll
             for (int c0 = 0; c0 < DP; c0 += 32) {
-                if (c0 >= D) break;
                 uint32_t o[32];
                 if (nkt > 0) {
                     tmem_ld32(tO + c0, o);
                     tmem_ld_wait();
                 }
-                if (live) {
 #pragma unroll
-                    for (int d = 0; d < 32; d += 8) {
-                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                        if (nkt > 0 && l != 0.f) {
-                            w.x = E::pack(__uint_as_float(o[d]) * inv, __uint_as_float(o[d + 1]) * inv);
-                            w.y = E::pack(__uint_as_float(o[d + 2]) * inv, __uint_as_float(o[d + 3]) * inv);
-                            w.z = E::pack(__uint_as_float(o[d + 4]) * inv, __uint_as_float(o[d + 5]) * inv);
-                            w.w = E::pack(__uint_as_float(o[d + 6]) * inv, __uint_as_float(o[d + 7]) * inv);
-                        }
-                        if (c0 + d < D) *reinterpret_cast<uint4*>(out + c0 + d) = w;
+                for (int e = 0; e < 32; e += 8) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (nkt > 0 && l != 0.f) {
+                        w.x = E::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                        w.y = E::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                        w.z = E::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                        w.w = E::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
                     }
+                    *reinterpret_cast<uint4*>(d + q_off<DP>(lane, (c0 + e) / 8)) = w;
                 }
+            }
+            uint16_t* own = live ? a.out + row * a.ld_out + (long long)(g * G + h) * D : nullptr;
+            __syncwarp();
+#pragma unroll 4
+            for (int i = 0; i < DP / 8; ++i) {         // 32 pieces at a time
+                const int piece = i * 32 + lane, rr = piece / (DP / 8), c = piece % (DP / 8);
+                uint16_t* out = reinterpret_cast<uint16_t*>(__shfl_sync(FULL_MASK, (unsigned long long)own, rr));
+                if (out && c * 8 < D)
+                    *reinterpret_cast<uint4*>(out + c * 8) = *reinterpret_cast<const uint4*>(d + q_off<DP>(rr, c));
             }
             if (a.lse && live) a.lse[row * a.NH + g * G + h] = l == 0.f ? -INFINITY : m * LN2 + logf(l);
         }
@@ -461,10 +478,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     __syncthreads();
     pdl_trigger();
     if (threadIdx.x == 0 && sflag[0]) raise_status(a.status, EMBER_ERR_TIMEOUT);
-    if (warp == PT_TMA && lane == 0 && sflag[0]) {
-        // drain K/V copies issued but never consumed by the MMA warp
-        for (int j = sflag[2]; j < sflag[1]; ++j) (void)mbar_wait(&kv_full[j % NSTG], (uint32_t)(j / NSTG) & 1u);
-    }
     if (warp == PT_MMA) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
@@ -472,28 +485,35 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 }
 
 template <class E, int DP>
-cudaError_t launch_dp(const void* mk, const void* mv, const PagedPrefillArgs& a, cudaStream_t s) {
+cudaError_t launch_dp(const PagedPrefillMaps& m, const PagedPrefillArgs& a, cudaStream_t s) {
     auto k = k_paged_prefill_tc<E, DP>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PtSmem<DP>::TOTAL);
     if (e != cudaSuccess) return e;
     const int per = 2 * (PT_ROWS / (a.NH / a.c.NKV));
-    const dim3 grid((unsigned)(((long long)a.n + per - 1) / per + a.B), a.c.NKV);
-    return launch_k(k, grid, dim3(PT_THREADS), PtSmem<DP>::TOTAL, s, *reinterpret_cast<const CUtensorMap*>(mk),
-                    *reinterpret_cast<const CUtensorMap*>(mv), a);
+    const dim3 grid((unsigned)((((long long)a.n + per - 1) / per + a.B) * a.c.NKV));
+    return launch_k(k, grid, dim3(PT_THREADS), PtSmem<DP>::TOTAL, s, *reinterpret_cast<const CUtensorMap*>(m.q),
+                    *reinterpret_cast<const CUtensorMap*>(m.k), *reinterpret_cast<const CUtensorMap*>(m.v), a);
 }
 
 }  // namespace
 
-bool paged_prefill_maps(const PagedView& c, void* mk, void* mv) {
+bool paged_prefill_maps(const PagedPrefillArgs& a, PagedPrefillMaps& m) {
+    const PagedView& c = a.c;
+    const int G = a.NH / c.NKV, per = 2 * (PT_ROWS / G);
+    if ((((long long)a.n + per - 1) / per + a.B) * c.NKV > 0x7fffffffll) return false;   // the grid
+    const uint64_t qd[3] = {(uint64_t)c.D, (uint64_t)a.NH, (uint64_t)a.n};
+    const uint64_t qs[2] = {(uint64_t)c.D * 2, (uint64_t)a.ld_q * 2};
+    const uint32_t qb[3] = {64u, (uint32_t)G, (uint32_t)(PT_ROWS / G)};
     const uint64_t dims[4] = {(uint64_t)c.D, 1ull << c.page_shift, (uint64_t)c.NKV, (uint64_t)c.n_pages};
     const uint64_t strides[3] = {(uint64_t)c.row_stride * 2, (uint64_t)c.head_stride * 2, (uint64_t)c.page_stride * 2};
     const uint32_t box[4] = {64u, (1u << c.page_shift) < 128u ? 1u << c.page_shift : 128u, 1u, 1u};
-    return encode_map_bf16(mk, c.k, 4, dims, strides, box) && encode_map_bf16(mv, c.v, 4, dims, strides, box);
+    return encode_map_bf16(m.q, a.q, 3, qd, qs, qb) && encode_map_bf16(m.k, c.k, 4, dims, strides, box) &&
+           encode_map_bf16(m.v, c.v, 4, dims, strides, box);
 }
 
-cudaError_t launch_paged_prefill_tc(const PagedPrefillArgs& a, const void* mk, const void* mv, cudaStream_t s) {
-    if (a.c.bf16) return a.c.D <= 64 ? launch_dp<ElemBf16, 64>(mk, mv, a, s) : launch_dp<ElemBf16, 128>(mk, mv, a, s);
-    return a.c.D <= 64 ? launch_dp<ElemF16, 64>(mk, mv, a, s) : launch_dp<ElemF16, 128>(mk, mv, a, s);
+cudaError_t launch_paged_prefill_tc(const PagedPrefillArgs& a, const PagedPrefillMaps& m, cudaStream_t s) {
+    if (a.c.bf16) return a.c.D <= 64 ? launch_dp<ElemBf16, 64>(m, a, s) : launch_dp<ElemBf16, 128>(m, a, s);
+    return a.c.D <= 64 ? launch_dp<ElemF16, 64>(m, a, s) : launch_dp<ElemF16, 128>(m, a, s);
 }
 
 }  // namespace ember
