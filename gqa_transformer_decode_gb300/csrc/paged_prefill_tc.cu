@@ -107,6 +107,8 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
     return o;
 }
+// bits 0 .. n - 1
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -374,8 +376,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             const int sk = a.sinks - key0;
             if (!__all_sync(FULL_MASK, hi >= PT_KEYS && (lo <= 0 || sk >= PT_KEYS))) {
 #pragma unroll
-                for (int c = 0; c < PT_KEYS; ++c)
-                    if (!(c < hi && (c >= lo || c < sk))) v[c] = 0xff800000u;   // -inf
+                for (int k = 0; k < PT_KEYS / 32; ++k) {   // a bit a column: no branches
+                    const uint32_t see = below(hi - 32 * k) & (~below(lo - 32 * k) | below(sk - 32 * k));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[32 * k + i] = (see >> i) & 1u ? v[32 * k + i] : 0xff800000u;   // -inf
+                }
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
