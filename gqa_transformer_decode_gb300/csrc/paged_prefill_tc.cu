@@ -26,6 +26,12 @@
 // sum over keys of mixed sign is about the output's own rounding; l is summed
 // from the unrounded weights in f32.
 //
+// CTAs are persistent: one whose last copies are issued asks the hardware to
+// cancel a CTA that has not started yet (clusterlaunchcontrol) and takes over
+// that one's tiles, so the next pair's Q, K and first products run under this
+// one's epilogue, and the pairs still go to whichever SM is free.  Barrier phases
+// and ring slots count on across the pairs.
+//
 // Warps 0-3: tile A; warps 4-7: tile B (a warp reads the TMEM lanes of its index
 // mod 4); warp 8: TMA producer; warp 9: TMEM allocation, edge rows, MMA issue;
 // warps 10 and 11 only complete the warpgroup that gives up registers.  A row's
@@ -53,10 +59,10 @@ struct PtSmem {
     static constexpr int KB = DP / 64;                    // 64-element blocks of a row
     static constexpr int TILE = KB * 128 * 128;           // Q tile, K tile or V tile
     static constexpr int NS = DP == 64 ? 10 : 5;          // ring slots, a K or a V tile each
-    static constexpr int OFF_Q = 0;                       // Q of tile A, of tile B; at the end the output rows
+    static constexpr int OFF_Q = 0;                       // Q of tile A, of tile B
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_BAR = OFF_KV + NS * TILE;
-    static constexpr int TOTAL = OFF_BAR + 256 + 1024;    // + barriers, + alignment slack
+    static constexpr int TOTAL = OFF_BAR + 512 + 1024;    // + barriers, + alignment slack
     // TMEM columns: S_A, S_B (128 f32 each), O_A, O_B (DP f32 each); P (128
     // values, two to a column) in its own columns for DP 64, over S for DP 128
     static constexpr bool ALIAS = DP == 128;
@@ -115,34 +121,97 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return r;
 }
 
+// What one CTA index stands for: the pair of query tiles of one kv head.
+struct PtPair {
+    int g, seq, row0, tokens, pos0;   // kv head, table row, first query row, tokens, position of the first
+    int end, first, sinks;            // keys that some row sees: [first, end) and [0, sinks)
+    int ns, wb, nkt;                  // key tiles: of the sinks, first of the window, in all (-1: no such pair)
+    __device__ __forceinline__ int key0(int j) const { return PT_KEYS * (j < ns ? j : wb + j - ns); }
+};
+__device__ __forceinline__ PtPair pt_pair(const PagedPrefillArgs& a, int QT, unsigned cta, bool reporter) {
+    PtPair p;
+    // the last tiles see the most keys: those of all kv heads go first
+    const int x = (int)(gridDim.x - 1 - cta) / a.c.NKV;
+    p.g = (int)(gridDim.x - 1 - cta) % a.c.NKV;
+    p.nkt = -1;
+    const RowTile tile = find_row_tile(a, 2 * QT, x, reporter && x == 0 && p.g == 0);
+    if (tile.b < 0) return p;
+    const SeqRows sr = seq_rows(a, tile.b, false);
+    const int i0 = tile.i * 2 * QT;
+    p.seq = sr.seq;
+    p.row0 = sr.row0 + i0;
+    p.tokens = min(2 * QT, sr.nq - i0);
+    p.pos0 = sr.len - sr.nq + i0;                      // negative: sees nothing
+    p.end = p.pos0 + p.tokens;
+    p.first = a.window > 0 ? max(0, p.pos0 + 1 - a.window) : 0;
+    p.sinks = min(a.sinks, p.first);
+    p.ns = (p.sinks + PT_KEYS - 1) / PT_KEYS;
+    p.wb = max(p.first / PT_KEYS, p.ns);
+    p.nkt = p.end <= 0 ? 0 : p.ns + max(0, (p.end + PT_KEYS - 1) / PT_KEYS - p.wb);
+    return p;
+}
+
+// Asks for a CTA that has not started; 16 bytes of answer, counted on bar.
+__device__ __forceinline__ void try_cancel(uint32_t answer, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     answer),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The answer: whether there was one, and its index in the grid.
+__device__ __forceinline__ bool cancelled(uint32_t answer, unsigned& cta) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    cta = x;
+    return ok != 0;
+}
+
 template <class E, int DP>
 __global__ void __launch_bounds__(PT_THREADS, 1)
-    k_paged_prefill_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                       PagedPrefillArgs a) {
+    k_paged_prefill_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, PagedPrefillArgs a) {
     using L = PtSmem<DP>;
     constexpr int NS = L::NS;
     extern __shared__ uint8_t pt_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pt_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
-    uint64_t* q_full = bar + 0;
-    uint64_t* s_full = bar + 1;     // [2] per query tile
-    uint64_t* p_full = bar + 3;     // [2]
-    uint64_t* o_full = bar + 5;     // [2]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 7);
-    int* sflag = reinterpret_cast<int*>(bar + 8);   // failed
-    uint64_t* s_free = bar + 9;     // [2] the row values of S are in registers (P beside S only)
-    uint64_t* kv_full = bar + 11;   // [NS]: slot i % NS holds K (i even) or V (i odd) of key tile i / 2
-    uint64_t* kv_empty = bar + 21;  // [NS]
+    uint64_t* s_full = bar + 0;     // [2] per query tile
+    uint64_t* p_full = bar + 2;     // [2]
+    uint64_t* o_full = bar + 4;     // [2]
+    uint64_t* s_free = bar + 6;     // [2] the row values of S are in registers (P beside S only)
+    uint64_t* o_free = bar + 8;     // [2] O of a finished pair is in registers
+    uint64_t* q_full = bar + 10;
+    uint64_t* q_empty = bar + 11;
+    uint64_t* next_full = bar + 12;   // [2] answer of the it-th request in answers[it % 2]
+    uint64_t* next_empty = bar + 14;  // [2]
+    uint64_t* answers = bar + 16;     // [2] of 16 bytes
+    uint64_t* kv_full = bar + 20;     // [NS]: slot i % NS holds K (i even) or V (i odd) of the (i / 2)-th key tile
+    uint64_t* kv_empty = bar + 30;    // [NS]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 40);
+    int* sflag = reinterpret_cast<int*>(bar + 41);   // failed
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 128);
-            mbar_init(&s_free[t], 128);
             mbar_init(&o_full[t], 1);
+            mbar_init(&s_free[t], 128);
+            mbar_init(&o_free[t], 128);
+            mbar_init(&next_full[t], 1);
+            mbar_init(&next_empty[t], 10);   // the warps that read the answer
         }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         for (int i = 0; i < NS; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
@@ -158,30 +227,27 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     }
     const int D = a.c.D, G = a.NH / a.c.NKV;
     const int QT = PT_ROWS / G;                        // tokens of a query tile
-    // the last tiles see the most keys: those of all kv heads go first
-    const int x = (int)(gridDim.x - 1 - blockIdx.x) / a.c.NKV, g = (int)(gridDim.x - 1 - blockIdx.x) % a.c.NKV;
     pdl_wait();
-    const RowTile tile = find_row_tile(a, 2 * QT, x, x == 0 && g == 0 && warp == 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (tile.b < 0) {
-        if (warp == PT_MMA) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
-        return;
-    }
-    const SeqRows sr = seq_rows(a, tile.b, false);
-    const int i0 = tile.i * 2 * QT;                    // first token of tile A
-    const int tokens = min(2 * QT, sr.nq - i0);
-    const int pos0 = sr.len - sr.nq + i0;              // its position (negative: sees nothing)
-    // keys that some row sees: [first, end) and [0, sinks); in tiles of 128
-    const int end = pos0 + tokens;
-    const int first = a.window > 0 ? max(0, pos0 + 1 - a.window) : 0;
-    const int sinks = min(a.sinks, first);
-    const int ns = (sinks + PT_KEYS - 1) / PT_KEYS;
-    const int wb = max(first / PT_KEYS, ns);
-    const int nkt = end <= 0 ? 0 : ns + max(0, (end + PT_KEYS - 1) / PT_KEYS - wb);
-    auto key0_of = [&](int j) { return PT_KEYS * (j < ns ? j : wb + j - ns); };
+
+    auto wait_all = [&](uint64_t* b, int parity) {     // by a whole warp
+        return __all_sync(FULL_MASK, mbar_wait(b, (uint32_t)parity & 1u)) != 0;
+    };
+    // the CTA index after the it-th pair's: false when there is none left (or, ok = false, no answer)
+    auto take_next = [&](int it, unsigned& cta, bool& ok) {
+        if (!wait_all(&next_full[it & 1], it >> 1)) {
+            ok = false;
+            return false;
+        }
+        const bool got = cancelled(smem_u32(answers + 2 * (it & 1)), cta);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&next_empty[it & 1]);
+        return got;
+    };
 
     if (warp >= PT_TMA) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PT_REGS_REST));
@@ -189,48 +255,68 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const int P = 1 << a.c.page_shift;
         const int box = min(P, PT_KEYS);               // rows of a box
         const int boxes = PT_KEYS / box;               // of a tile: lane i < boxes copies box i
-        if (lane == 0 && nkt > 0) {                    // tokens beyond the sequence's: whatever follows, or zeros
-            mbar_expect_tx(q_full, 2 * L::KB * QT * G * 128);
-            for (int t = 0; t < 2; ++t)
-                for (int kb = 0; kb < L::KB; ++kb)
-                    tma_load_3d(sm + L::OFF_Q + t * L::TILE + kb * 128 * 128, &tmQ, kb * 64, g * G,
-                                sr.row0 + i0 + t * QT, q_full);
-        }
-        auto look_up = [&](int j) {                    // the lane's page of tile j; n_pages reads as zeros
-            const int k0 = key0_of(j) + lane * box;
-            if (lane >= boxes || k0 >= end || (k0 + box <= first && k0 >= sinks)) return a.c.n_pages;
-            const int page = a.c.table[(size_t)sr.seq * a.c.width + (k0 >> a.c.page_shift)];
-            if (page >= 0 && page < a.c.n_pages) return page;
-            raise_status(a.status, EMBER_ERR_INVALID_ARG);
-            return a.c.n_pages;
-        };
-        int page = nkt > 0 ? look_up(0) : 0, next = 0;
-        int issued = 0;
-        bool fail = false;
-        for (; issued < 2 * nkt; ++issued) {
-            const int s = issued % NS, j = issued >> 1;
-            const bool is_v = issued & 1;
-            if (!is_v && j + 1 < nkt) next = look_up(j + 1);
-            if (issued >= NS && !mbar_wait(&kv_empty[s], (uint32_t)(issued / NS - 1) & 1u)) fail = true;
-            if (__any_sync(FULL_MASK, fail)) {
-                fail = true;
-                break;
-            }
-            if (lane == 0) mbar_expect_tx(&kv_full[s], L::TILE);
-            __syncwarp();
-            if (lane < boxes) {
-                const int row = (key0_of(j) + lane * box) & (P - 1);
-                uint8_t* d = sm + L::OFF_KV + s * L::TILE + lane * box * 128;
+        unsigned cta = blockIdx.x;
+        int issued = 0, pairs = 0, it = 0;             // slots and pairs with keys so far
+        bool ok = true, asked = false;
+        for (;; ++it) {
+            const PtPair p = pt_pair(a, QT, cta, true);
+            if (p.nkt > 0) {
+                auto look_up = [&](int j) {            // the lane's page of tile j; n_pages reads as zeros
+                    const int k0 = p.key0(j) + lane * box;
+                    if (lane >= boxes || k0 >= p.end || (k0 + box <= p.first && k0 >= p.sinks)) return a.c.n_pages;
+                    const int page = a.c.table[(size_t)p.seq * a.c.width + (k0 >> a.c.page_shift)];
+                    if (page >= 0 && page < a.c.n_pages) return page;
+                    raise_status(a.status, EMBER_ERR_INVALID_ARG);
+                    return a.c.n_pages;
+                };
+                int page = look_up(0), next = 0;
+                ok = pairs == 0 || wait_all(q_empty, pairs - 1);
+                if (!ok) break;
+                if (lane == 0) {                       // tokens beyond the sequence's: whatever follows, or zeros
+                    mbar_expect_tx(q_full, 2 * L::KB * QT * G * 128);
+                    for (int t = 0; t < 2; ++t)
+                        for (int kb = 0; kb < L::KB; ++kb)
+                            tma_load_3d(sm + L::OFF_Q + t * L::TILE + kb * 128 * 128, &tmQ, kb * 64, p.g * G,
+                                        p.row0 + t * QT, q_full);
+                }
+                ++pairs;
+                for (int i = 0; i < 2 * p.nkt; ++i, ++issued) {
+                    const int s = issued % NS, j = i >> 1;
+                    const bool is_v = i & 1;
+                    if (!is_v && j + 1 < p.nkt) next = look_up(j + 1);
+                    ok = issued < NS || wait_all(&kv_empty[s], issued / NS - 1);
+                    if (!ok) break;
+                    if (lane == 0) mbar_expect_tx(&kv_full[s], L::TILE);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const int row = (p.key0(j) + lane * box) & (P - 1);
+                        uint8_t* d = sm + L::OFF_KV + s * L::TILE + lane * box * 128;
 #pragma unroll
-                for (int kb = 0; kb < L::KB; ++kb)
-                    tma_load_4d(d + kb * 128 * 128, is_v ? &tmV : &tmK, kb * 64, row, g, page, &kv_full[s]);
+                        for (int kb = 0; kb < L::KB; ++kb)
+                            tma_load_4d(d + kb * 128 * 128, is_v ? &tmV : &tmK, kb * 64, row, p.g, page, &kv_full[s]);
+                    }
+                    if (is_v) page = next;
+                }
+                if (!ok) break;
             }
-            if (is_v) page = next;
+            // asked for only now, a ring's worth of tiles before the pair ends: a CTA
+            // that asked at its start would hold work that another could begin first
+            ok = it < 2 || wait_all(&next_empty[it & 1], (it >> 1) - 1);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_expect_tx(&next_full[it & 1], 16);
+                try_cancel(smem_u32(answers + 2 * (it & 1)), &next_full[it & 1]);
+            }
+            __syncwarp();
+            asked = true;
+            if (!take_next(it, cta, ok)) break;
+            asked = false;
         }
-        if (fail && lane == 0) {
+        if (!ok && lane == 0) {
             sflag[0] = 1;
-            // the copies in flight land before the block ends (none waits for more than the last NS)
-            (void)mbar_wait(q_full, 0);
+            // what is in flight lands before the block ends
+            if (asked) (void)mbar_wait(&next_full[it & 1], (uint32_t)(it >> 1) & 1u);
+            if (pairs) (void)mbar_wait(q_full, (uint32_t)(pairs - 1) & 1u);
             for (int i = max(0, issued - NS); i < issued; ++i) (void)mbar_wait(&kv_full[i % NS], (uint32_t)(i / NS) & 1u);
         }
     } else if (warp == PT_MMA) {   // ------------------------------ MMA issuer
@@ -256,23 +342,23 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                             sdesc_mn_sw128(v0 + k * 16 * 128, 128 * 128), idO, (acc || k) ? 1u : 0u);
             umma_commit(&o_full[t]);
         };
-        auto wait_all = [&](uint64_t* b, int parity) {
-            return __all_sync(FULL_MASK, mbar_wait(b, (uint32_t)parity & 1u)) != 0;
-        };
-        auto k_ready = [&](int j) { return wait_all(&kv_full[2 * j % NS], 2 * j / NS); };
-        // V of tile j; rows that nobody sees become zeros
-        auto v_ready = [&](int j) {
-            const int s = (2 * j + 1) % NS;
-            if (!wait_all(&kv_full[s], (2 * j + 1) / NS)) return false;
-            const int key0 = key0_of(j);
-            if (key0 + PT_KEYS > end || (key0 < first && key0 + PT_KEYS > sinks)) {
-                uint8_t* v = sm + L::OFF_KV + s * L::TILE;
-                for (int i = lane; i < PT_KEYS * 8 * L::KB; i += 32) {   // a 16-byte piece of a row each
-                    const int r = i / (8 * L::KB), c = i % (8 * L::KB), key = key0 + r;
-                    if (key >= end || (key < first && key >= sinks))
-                        *reinterpret_cast<uint4*>(v + (c >> 3) * 128 * 128 + r * 128 + (c & 7) * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                }
+        auto k_ready = [&](int i) { return wait_all(&kv_full[i % NS], i / NS); };
+        // V of tile j in slot i; rows that nobody sees become zeros
+        auto v_ready = [&](const PtPair& p, int j, int i) {
+            if (!wait_all(&kv_full[i % NS], i / NS)) return false;
+            const int key0 = p.key0(j);
+            if (key0 + PT_KEYS > p.end || (key0 < p.first && key0 + PT_KEYS > p.sinks)) {
+                const uint32_t v = smem_u32(sm + L::OFF_KV + (i % NS) * L::TILE);
+                auto zero = [&](int r0, int r1) {       // rows [r0, r1): 16 bytes a lane
+#pragma unroll 4
+                    for (int e = max(r0, 0) * 8 * L::KB + lane; e < min(r1, PT_KEYS) * 8 * L::KB; e += 32)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         v + (L::KB == 1 ? e * 16 : ((e >> 3) & 1) * (128 * 128) + (e >> 4) * 128 + (e & 7) * 16)),
+                                     "r"(0)
+                                     : "memory");
+                };
+                zero(p.sinks - key0, p.first - key0);
+                zero(p.end - key0, PT_KEYS);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             }
@@ -286,55 +372,74 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             }
             __syncwarp();
         };
-        int j = 0;
-        bool ok = nkt == 0 || (wait_all(q_full, 0) && k_ready(0));
-        if (ok && nkt > 0)
-            issue([&] {
-                mma_s(0, 0);
-                mma_s(1, 0);
-                umma_commit(&kv_empty[0]);
-            });
-        for (; ok && j < nkt; ++j) {
-            const bool more = j + 1 < nkt;
-            const int iv = 2 * j + 1, ik = 2 * j + 2;   // V(j), K(j + 1)
-            if (L::ALIAS) {
-                // P lies over S: P . V(j) of a query tile goes before its S(j + 1)
-                // (MMAs of one thread run in the order of issue)
-                if (!(ok = v_ready(j) && wait_all(&p_full[0], j))) break;
-                issue([&] { mma_pv(0, iv, j > 0); });
-                if (more) {
-                    if (!(ok = k_ready(j + 1))) break;
-                    issue([&] { mma_s(0, ik); });
-                }
-                if (!(ok = wait_all(&p_full[1], j))) break;
+        unsigned cta = blockIdx.x;
+        int base = 0, pairs = 0;   // key tiles and pairs with keys so far
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            const PtPair p = pt_pair(a, QT, cta, false);
+            const int nkt = max(0, p.nkt);
+            int j = 0;
+            if (nkt > 0) {
+                ok = wait_all(q_full, pairs) && k_ready(2 * base);
+                if (!ok) break;
                 issue([&] {
-                    mma_pv(1, iv, j > 0);
-                    umma_commit(&kv_empty[iv % NS]);
-                    if (more) {
-                        mma_s(1, ik);
-                        umma_commit(&kv_empty[ik % NS]);
-                    }
-                });
-            } else {
-                // S(j + 1) as soon as the rows of S(j) are in registers, while they
-                // are exponentiated
-                if (more) {
-                    if (!(ok = k_ready(j + 1) && wait_all(&s_free[0], j))) break;
-                    issue([&] { mma_s(0, ik); });
-                    if (!(ok = wait_all(&s_free[1], j))) break;
-                    issue([&] {
-                        mma_s(1, ik);
-                        umma_commit(&kv_empty[ik % NS]);
-                    });
-                }
-                if (!(ok = v_ready(j) && wait_all(&p_full[0], j))) break;
-                issue([&] { mma_pv(0, iv, j > 0); });
-                if (!(ok = wait_all(&p_full[1], j))) break;
-                issue([&] {
-                    mma_pv(1, iv, j > 0);
-                    umma_commit(&kv_empty[iv % NS]);
+                    mma_s(0, 2 * base);
+                    mma_s(1, 2 * base);
+                    umma_commit(&kv_empty[2 * base % NS]);
+                    if (nkt == 1) umma_commit(q_empty);
                 });
             }
+            for (; j < nkt; ++j) {
+                const int n = base + j;                        // tiles so far: phases
+                const bool more = j + 1 < nkt, last_s = j + 2 == nkt;
+                const int iv = 2 * n + 1, ik = 2 * n + 2;      // V(j), K(j + 1)
+                // the first P . V of a pair overwrites O of the pair before
+                auto o_ready = [&](int t) { return j > 0 || pairs == 0 || wait_all(&o_free[t], pairs - 1); };
+                if (L::ALIAS) {
+                    // P lies over S: P . V(j) of a query tile goes before its S(j + 1)
+                    // (MMAs of one thread run in the order of issue)
+                    if (!(ok = v_ready(p, j, iv) && wait_all(&p_full[0], n) && o_ready(0))) break;
+                    issue([&] { mma_pv(0, iv, j > 0); });
+                    if (more) {
+                        if (!(ok = k_ready(ik))) break;
+                        issue([&] { mma_s(0, ik); });
+                    }
+                    if (!(ok = wait_all(&p_full[1], n) && o_ready(1))) break;
+                    issue([&] {
+                        mma_pv(1, iv, j > 0);
+                        umma_commit(&kv_empty[iv % NS]);
+                        if (more) {
+                            mma_s(1, ik);
+                            umma_commit(&kv_empty[ik % NS]);
+                            if (last_s) umma_commit(q_empty);
+                        }
+                    });
+                } else {
+                    // S(j + 1) as soon as the rows of S(j) are in registers, while they
+                    // are exponentiated
+                    if (more) {
+                        if (!(ok = k_ready(ik) && wait_all(&s_free[0], n))) break;
+                        issue([&] { mma_s(0, ik); });
+                        if (!(ok = wait_all(&s_free[1], n))) break;
+                        issue([&] {
+                            mma_s(1, ik);
+                            umma_commit(&kv_empty[ik % NS]);
+                            if (last_s) umma_commit(q_empty);
+                        });
+                    }
+                    if (!(ok = v_ready(p, j, iv) && wait_all(&p_full[0], n) && o_ready(0))) break;
+                    issue([&] { mma_pv(0, iv, j > 0); });
+                    if (!(ok = wait_all(&p_full[1], n) && o_ready(1))) break;
+                    issue([&] {
+                        mma_pv(1, iv, j > 0);
+                        umma_commit(&kv_empty[iv % NS]);
+                    });
+                }
+            }
+            if (!ok) break;
+            base += nkt;
+            pairs += nkt > 0;
+            if (!take_next(it, cta, ok)) break;
         }
         if (!ok && lane == 0) sflag[0] = 1;
     }
@@ -345,23 +450,27 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const int qw = warp & 3;                      // TMEM lane quarter of this warp
         const int r = qw * 32 + lane;                 // row within the tile
         const int tok = t * QT + r / G, h = r % G;    // token of the pair, head of the group
-        const bool live = r < QT * G && tok < tokens;
-        const int qp = pos0 + min(tok, tokens - 1);   // its position (rows that are not live: the last one's)
-        const long long row = sr.row0 + i0 + tok;
         const uint32_t lane_off = (uint32_t)(qw * 32) << 16;
         const uint32_t tS = tmem + L::COL_S + t * 128 + lane_off;
         const uint32_t tO = tmem + L::COL_O + t * DP + lane_off;
         const uint32_t tP = tmem + L::col_p(t) + lane_off;
         const float sc = a.scale * LOG2E;             // > 0
-        float m = SOFTMAX_FLOOR, l = 0.f;             // reference maximum (of s * sc), sum of 2^(s sc - m)
+        unsigned cta = blockIdx.x;
+        int base = 0;                                 // key tiles so far
         bool ok = true;
+        for (int it = 0; ok; ++it) {
+        const PtPair p = pt_pair(a, QT, cta, false);
+        const int nkt = max(0, p.nkt);
+        const bool live = p.nkt >= 0 && r < QT * G && tok < p.tokens;
+        const int qp = p.pos0 + min(tok, p.tokens - 1);   // its position (rows that are not live: the last one's)
+        float m = SOFTMAX_FLOOR, l = 0.f;             // reference maximum (of s * sc), sum of 2^(s sc - m)
+        uint32_t v[PT_KEYS];                          // the row's products, then its weights; at the end its O
         for (int j = 0; j < nkt; ++j) {
-            if (!mbar_wait(&s_full[t], (uint32_t)j & 1u)) {
+            if (!wait_all(&s_full[t], base + j)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            uint32_t v[PT_KEYS];                      // the row's products, then its weights
 #pragma unroll
             for (int c = 0; c < PT_KEYS; c += 32) tmem_ld32(tS + c, v + c);
             tmem_ld_wait();
@@ -370,7 +479,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 mbar_arrive(&s_free[t]);
             }
             // column c is visible when c < hi and (c >= lo or c < sk)
-            const int key0 = key0_of(j);
+            const int key0 = p.key0(j);
             const int hi = qp - key0 + 1;
             const int lo = a.window > 0 ? qp - a.window + 1 - key0 : 0;
             const int sk = a.sinks - key0;
@@ -408,27 +517,28 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             for (int i = 0; i < 4; ++i) rs[i] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < PT_KEYS; c += 2) {
-                float2 p = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, m2);
-                p.x = ex2(p.x);
-                p.y = ex2(p.y);
-                rs[(c >> 1) & 3] = add2(rs[(c >> 1) & 3], p);
-                v[c >> 1] = E::pack(p.x, p.y);
+                float2 w = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, m2);
+                w.x = ex2(w.x);
+                w.y = ex2(w.y);
+                rs[(c >> 1) & 3] = add2(rs[(c >> 1) & 3], w);
+                v[c >> 1] = E::pack(w.x, w.y);
             }
             if (j > 0) {   // P . V(j - 1) must be complete before O is touched or P is rewritten
-                if (!mbar_wait(&o_full[t], (uint32_t)(j - 1) & 1u)) {
+                if (!wait_all(&o_full[t], base + j - 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (any_move) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < DP; c0 += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(tO + c0, o);
+                    for (int c0 = 0; c0 < DP; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + c0, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
                         tmem_st16(tO + c0, o);
+                        tmem_st16(tO + c0 + 16, o + 16);
                     }
                 }
             }
@@ -440,49 +550,74 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             const float2 r2 = add2(add2(rs[0], rs[1]), add2(rs[2], rs[3]));
             l += r2.x + r2.y;
         }
-        if (ok && nkt > 0 && !mbar_wait(&o_full[t], (uint32_t)(nkt - 1) & 1u)) ok = false;
-        if (!ok) sflag[0] = 1;
-        tc_fence_after();
-        if (ok) {
-            // through the row's own part of the Q tile (no product reads it any more)
-            // into whole rows: neighbouring lanes write neighbouring 16 bytes
+        if (ok && nkt > 0) {
+            ok = wait_all(&o_full[t], base + nkt - 1);
+            tc_fence_after();
+            if (ok) {
+#pragma unroll
+                for (int c = 0; c < DP; c += 32) tmem_ld32(tO + c, v + c);
+                tmem_ld_wait();
+                tc_fence_before();
+                mbar_arrive(&o_free[t]);
+            }
+        }
+        if (!ok) break;
+        {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint8_t* d = sm + L::OFF_Q + t * L::TILE + qw * (32 * DP * 2);
+            const long long row = p.row0 + tok;
+            uint16_t* own = live ? a.out + row * a.ld_out + (long long)(p.g * G + h) * D : nullptr;
+            // four neighbouring lanes exchange 16-byte pieces, so that together they
+            // write 64 bytes of one row after another instead of 16 of four rows each
+            uint16_t* rows[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                rows[i] = reinterpret_cast<uint16_t*>(__shfl_sync(FULL_MASK, (unsigned long long)own, (lane & ~3) | i));
+            const bool odd = lane & 1, high = lane & 2;
 #pragma unroll
             for (int c0 = 0; c0 < DP; c0 += 32) {
-                uint32_t o[32];
-                if (nkt > 0) {
-                    tmem_ld32(tO + c0, o);
-                    tmem_ld_wait();
-                }
+                if (c0 >= D) break;
+                uint4 w[4];
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                    if (nkt > 0 && l != 0.f) {
-                        w.x = E::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                        w.y = E::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                        w.z = E::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                        w.w = E::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                for (int i = 0; i < 4; ++i) {
+                    const int c = c0 + 8 * i;
+                    w[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (l != 0.f) {
+                        w[i].x = E::pack(__uint_as_float(v[c]) * inv, __uint_as_float(v[c + 1]) * inv);
+                        w[i].y = E::pack(__uint_as_float(v[c + 2]) * inv, __uint_as_float(v[c + 3]) * inv);
+                        w[i].z = E::pack(__uint_as_float(v[c + 4]) * inv, __uint_as_float(v[c + 5]) * inv);
+                        w[i].w = E::pack(__uint_as_float(v[c + 6]) * inv, __uint_as_float(v[c + 7]) * inv);
                     }
-                    *reinterpret_cast<uint4*>(d + q_off<DP>(lane, (c0 + e) / 8)) = w;
                 }
+                auto swap = [&](uint4& x, uint4& y, bool upper, int d) {   // lanes d apart: my y for its x
+                    const uint4 give = upper ? x : y;
+                    uint4 got;
+                    got.x = __shfl_xor_sync(FULL_MASK, give.x, d);
+                    got.y = __shfl_xor_sync(FULL_MASK, give.y, d);
+                    got.z = __shfl_xor_sync(FULL_MASK, give.z, d);
+                    got.w = __shfl_xor_sync(FULL_MASK, give.w, d);
+                    if (upper) x = got;
+                    else y = got;
+                };
+                swap(w[0], w[1], odd, 1);
+                swap(w[2], w[3], odd, 1);
+                swap(w[0], w[2], high, 2);
+                swap(w[1], w[3], high, 2);
+                // now w[i] is piece lane % 4 of row i of the four
+                const int c = c0 + 8 * (lane & 3);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (rows[i] && c < D) *reinterpret_cast<uint4*>(rows[i] + c) = w[i];
             }
-            uint16_t* own = live ? a.out + row * a.ld_out + (long long)(g * G + h) * D : nullptr;
-            __syncwarp();
-#pragma unroll 4
-            for (int i = 0; i < DP / 8; ++i) {         // 32 pieces at a time
-                const int piece = i * 32 + lane, rr = piece / (DP / 8), c = piece % (DP / 8);
-                uint16_t* out = reinterpret_cast<uint16_t*>(__shfl_sync(FULL_MASK, (unsigned long long)own, rr));
-                if (out && c * 8 < D)
-                    *reinterpret_cast<uint4*>(out + c * 8) = *reinterpret_cast<const uint4*>(d + q_off<DP>(rr, c));
-            }
-            if (a.lse && live) a.lse[row * a.NH + g * G + h] = l == 0.f ? -INFINITY : m * LN2 + logf(l);
+            if (a.lse && live) a.lse[row * a.NH + p.g * G + h] = l == 0.f ? -INFINITY : m * LN2 + logf(l);
         }
+        base += nkt;
+        if (!take_next(it, cta, ok)) break;
+        }
+        if (!ok) sflag[0] = 1;
     }
 
     tc_fence_before();
     __syncthreads();
-    pdl_trigger();
     if (threadIdx.x == 0 && sflag[0]) raise_status(a.status, EMBER_ERR_TIMEOUT);
     if (warp == PT_MMA) {
         tc_fence_after();
