@@ -6,12 +6,16 @@
 // query heads of a kv head share its keys, so a tile's rows are (token, head)
 // pairs, row r = token r / G, head r % G: a tile spans 128 / G tokens, so little
 // of its last key tile lies beyond the causal border, and each K / V tile that
-// TMA brings serves all heads of the group.  Per key tile of 128 keys and query
+// TMA brings serves all heads of the group.  Per key tile of 64 keys and query
 // tile: S = Q K^T into TMEM, one thread per row takes p = 2^(s - m) and writes P
 // (bf16 / f16) back to TMEM, O += P V accumulates there.  The reference maximum m
 // moves (and O, l are rescaled) only when a tile's maximum passes it by more than
-// 2^8.  While one tile's rows are exponentiated the tensor cores work for the
-// other.
+// 2^8.  S has two buffers for each query tile, so the products of the next key
+// tile are ready before a row's thread asks for them, and the two query tiles'
+// threads and the tensor cores wait for one another only when one of them has
+// fallen a whole tile behind.  (With one buffer of 128 keys, P over it, a step
+// was the sum of both products and the exponentials, 3.8 k cycles for 128 keys; a
+// product of 64 columns takes 45 cycles, of 128 columns 64.)
 //
 // K and V tiles are read from the pages as they lie, one TMA box (64 elements x
 // up to 128 rows of a page) at a time, 128-byte swizzled: as K-major operand of
@@ -35,9 +39,8 @@
 // Warps 0-3: tile A; warps 4-7: tile B (a warp reads the TMEM lanes of its index
 // mod 4); warp 8: TMA producer; warp 9: TMEM allocation, edge rows, MMA issue;
 // warps 10 and 11 only complete the warpgroup that gives up registers.  A row's
-// 128 scores stand in registers at once: their maximum, then one fused
-// multiply-add and one exponential each, so a thread needs more registers (200)
-// than the other warps (104).  Every mbarrier wait is bounded; a timeout raises
+// 64 scores, and at the end its output, stand in registers at once, so a row's
+// thread needs more of them (200) than the other warps (104).  Every mbarrier wait is bounded; a timeout raises
 // EMBER_ERR_TIMEOUT, the CTA drains its copies and frees TMEM.
 #include <cudaTypedefs.h>
 
@@ -52,36 +55,54 @@ constexpr int PT_THREADS = 384;
 constexpr int PT_TMA = 8, PT_MMA = 9;   // warps
 constexpr int PT_REGS_ROW = 200, PT_REGS_REST = 104;   // 256 * 200 + 128 * 104 = 384 * 168, the launch's share
 constexpr int PT_ROWS = 128;   // rows of a query tile
-constexpr int PT_KEYS = 128;   // keys of a tile
+constexpr int PT_KEYS = 64;    // keys of a tile
 
 template <int DP>
 struct PtSmem {
     static constexpr int KB = DP / 64;                    // 64-element blocks of a row
-    static constexpr int TILE = KB * 128 * 128;           // Q tile, K tile or V tile
-    static constexpr int NS = DP == 64 ? 10 : 5;          // ring slots, a K or a V tile each
+    static constexpr int QTILE = KB * PT_ROWS * 128;      // a Q tile
+    static constexpr int TILE = KB * PT_KEYS * 128;       // a K or V tile
+    static constexpr int NS = DP == 64 ? 16 : 10;         // ring slots, a K or a V tile each
     static constexpr int OFF_Q = 0;                       // Q of tile A, of tile B
-    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_KV = 2 * QTILE;
     static constexpr int OFF_BAR = OFF_KV + NS * TILE;
     static constexpr int TOTAL = OFF_BAR + 512 + 1024;    // + barriers, + alignment slack
-    // TMEM columns: S_A, S_B (128 f32 each), O_A, O_B (DP f32 each); P (128
-    // values, two to a column) in its own columns for DP 64, over S for DP 128
-    static constexpr bool ALIAS = DP == 128;
-    static constexpr uint32_t COL_S = 0, COL_O = 256;
-    static constexpr uint32_t col_p(int t) { return ALIAS ? COL_S + t * 128 : 384 + t * 64; }
+    static_assert(TOTAL <= 232448, "shared memory of a CTA");
+    // TMEM columns: two S buffers of 64 f32 for each query tile, the weights P (64
+    // values, two to a column) over the first half of theirs; O_A, O_B (DP f32 each)
+    static constexpr uint32_t col_s(int t, int b) { return t * 128 + b * 64; }
+    static constexpr uint32_t col_o(int t) { return 256 + t * DP; }
 };
 
-// Descriptor of an MN-major operand written by TMA with the 128-byte swizzle:
-// 64 elements of M/N to a 128-byte row, 8-row groups of K 1024 bytes apart
-// (stride offset), the next 64 elements `lead` bytes further (leading offset).
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lead) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3ffffu) >> 4);
-    d |= (uint64_t)(lead >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// Low words of the operands' descriptors (the high word is the same for all:
+// 8-row groups 1024 bytes apart, version 1, 128-byte swizzle).  K-major: rows of
+// 128 bytes along K.  MN-major: 64 elements of M/N to a 128-byte row, the next 64
+// `lead` bytes further.  Steps along K are added to the low word.
+constexpr uint32_t DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr & 0x3ffffu) >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t lead) {
+    return (saddr & 0x3ffffu) >> 4 | (lead >> 4) << 16;
 }
+// D (+)= A B^T, A in shared memory or in tensor memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"((uint32_t)acc), "n"(DESC_HI));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"((uint32_t)acc), "n"(DESC_HI));
+}
+// one lane of the warp, the same one each time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(FULL_MASK, x, 0); }
 constexpr uint32_t IDESC_B_MN = 1u << 16;   // B is MN-major
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, int c0, int c1, int c2, int c3,
@@ -184,28 +205,28 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     extern __shared__ uint8_t pt_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pt_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
-    uint64_t* s_full = bar + 0;     // [2] per query tile
-    uint64_t* p_full = bar + 2;     // [2]
-    uint64_t* o_full = bar + 4;     // [2]
-    uint64_t* s_free = bar + 6;     // [2] the row values of S are in registers (P beside S only)
-    uint64_t* o_free = bar + 8;     // [2] O of a finished pair is in registers
-    uint64_t* q_full = bar + 10;
-    uint64_t* q_empty = bar + 11;
-    uint64_t* next_full = bar + 12;   // [2] answer of the it-th request in answers[it % 2]
-    uint64_t* next_empty = bar + 14;  // [2]
-    uint64_t* answers = bar + 16;     // [2] of 16 bytes
-    uint64_t* kv_full = bar + 20;     // [NS]: slot i % NS holds K (i even) or V (i odd) of the (i / 2)-th key tile
-    uint64_t* kv_empty = bar + 30;    // [NS]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 40);
-    int* sflag = reinterpret_cast<int*>(bar + 41);   // failed
+    uint64_t* s_full = bar + 0;     // [query tile][buffer]
+    uint64_t* p_full = bar + 4;     // [query tile][buffer]
+    uint64_t* o_full = bar + 8;     // [query tile]
+    uint64_t* o_free = bar + 10;    // [query tile] O of a finished pair is in registers
+    uint64_t* q_full = bar + 12;
+    uint64_t* q_empty = bar + 13;
+    uint64_t* next_full = bar + 14;   // [2] answer of the it-th request in answers[it % 2]
+    uint64_t* next_empty = bar + 16;  // [2]
+    uint64_t* answers = bar + 18;     // [2] of 16 bytes
+    uint64_t* kv_full = bar + 22;     // [NS]: slot i % NS holds K (i even) or V (i odd) of the (i / 2)-th key tile
+    uint64_t* kv_empty = bar + 38;    // [NS]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 54);
+    int* sflag = reinterpret_cast<int*>(bar + 55);   // failed
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+        }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], 128);
             mbar_init(&o_full[t], 1);
-            mbar_init(&s_free[t], 128);
             mbar_init(&o_free[t], 128);
             mbar_init(&next_full[t], 1);
             mbar_init(&next_empty[t], 10);   // the warps that read the answer
@@ -276,7 +297,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     mbar_expect_tx(q_full, 2 * L::KB * QT * G * 128);
                     for (int t = 0; t < 2; ++t)
                         for (int kb = 0; kb < L::KB; ++kb)
-                            tma_load_3d(sm + L::OFF_Q + t * L::TILE + kb * 128 * 128, &tmQ, kb * 64, p.g * G,
+                            tma_load_3d(sm + L::OFF_Q + t * L::QTILE + kb * PT_ROWS * 128, &tmQ, kb * 64, p.g * G,
                                         p.row0 + t * QT, q_full);
                 }
                 ++pairs;
@@ -293,7 +314,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                         uint8_t* d = sm + L::OFF_KV + s * L::TILE + lane * box * 128;
 #pragma unroll
                         for (int kb = 0; kb < L::KB; ++kb)
-                            tma_load_4d(d + kb * 128 * 128, is_v ? &tmV : &tmK, kb * 64, row, p.g, page, &kv_full[s]);
+                            tma_load_4d(d + kb * PT_KEYS * 128, is_v ? &tmV : &tmK, kb * 64, row, p.g, page, &kv_full[s]);
                     }
                     if (is_v) page = next;
                 }
@@ -323,25 +344,28 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         constexpr uint32_t type = E::bf16 ? idesc_bf16(0, 0) : idesc_f16(0, 0);
         constexpr uint32_t idS = type | idesc_f16(PT_ROWS, PT_KEYS);
         constexpr uint32_t idO = type | idesc_f16(PT_ROWS, DP) | IDESC_B_MN;
-        auto mma_s = [&](int t, int i) {   // S_t = Q_t . K(slot of i)^T
-            const uint32_t q0 = smem_u32(sm + L::OFF_Q + t * L::TILE);
-            const uint32_t k0 = smem_u32(sm + L::OFF_KV + (i % NS) * L::TILE);
+        // Issuing is the tensor pipe's pace-maker when a product takes 45 to 64 cycles:
+        // operands are warp-uniform, descriptors one addition each.
+        const uint32_t tm = uniform(tmem);
+        const uint32_t dq = uniform(desc_k(smem_u32(sm + L::OFF_Q)));
+        const uint32_t kv0 = uniform(smem_u32(sm + L::OFF_KV));
+        auto mma_s = [&](int t, uint32_t buf, uint32_t dk) {   // S_t = Q_t . K^T
 #pragma unroll
             for (int kb = 0; kb < L::KB; ++kb)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    umma_bf16(tmem + L::COL_S + t * 128, sdesc_sw128(q0 + kb * 128 * 128 + k * 32),
-                              sdesc_sw128(k0 + kb * 128 * 128 + k * 32), idS, (kb | k) ? 1u : 0u);
-            umma_commit(&s_full[t]);
+                    mma_ss(tm + L::col_s(t, 0) + buf * 64, dq + ((t * L::QTILE + kb * PT_ROWS * 128 + k * 32) >> 4),
+                           dk + ((kb * PT_KEYS * 128 + k * 32) >> 4), idS, kb | k);
+            umma_commit(&s_full[2 * t + buf]);
         };
-        auto mma_pv = [&](int t, int i, bool acc) {   // O_t += P_t (TMEM) . V(slot of i)
-            const uint32_t v0 = smem_u32(sm + L::OFF_KV + (i % NS) * L::TILE);
+        auto mma_pv = [&](int t, uint32_t buf, uint32_t dv, bool acc) {   // O_t += P_t (TMEM) . V
 #pragma unroll
             for (int k = 0; k < PT_KEYS / 16; ++k)
-                umma_f16_ts(tmem + L::COL_O + t * DP, tmem + L::col_p(t) + k * 8,
-                            sdesc_mn_sw128(v0 + k * 16 * 128, 128 * 128), idO, (acc || k) ? 1u : 0u);
+                mma_ts(tm + L::col_o(t), tm + L::col_s(t, 0) + buf * 64 + k * 8, dv + ((k * 16 * 128) >> 4), idO, acc || k);
             umma_commit(&o_full[t]);
         };
+        auto slot_k = [&](int n) { return uniform(desc_k(kv0 + (2 * n % NS) * L::TILE)); };
+        auto slot_v = [&](int n) { return uniform(desc_mn(kv0 + ((2 * n + 1) % NS) * L::TILE, PT_KEYS * 128)); };
         auto k_ready = [&](int i) { return wait_all(&kv_full[i % NS], i / NS); };
         // V of tile j in slot i; rows that nobody sees become zeros
         auto v_ready = [&](const PtPair& p, int j, int i) {
@@ -353,7 +377,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 #pragma unroll 4
                     for (int e = max(r0, 0) * 8 * L::KB + lane; e < min(r1, PT_KEYS) * 8 * L::KB; e += 32)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         v + (L::KB == 1 ? e * 16 : ((e >> 3) & 1) * (128 * 128) + (e >> 4) * 128 + (e & 7) * 16)),
+                                         v + (L::KB == 1 ? e * 16 : ((e >> 3) & 1) * (PT_KEYS * 128) + (e >> 4) * 128 + (e & 7) * 16)),
                                      "r"(0)
                                      : "memory");
                 };
@@ -364,9 +388,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             }
             return true;
         };
-        // lane 0 issues f() after everything the warp has waited for
+        // one lane issues f() after everything the warp has waited for
         auto issue = [&](auto f) {
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
                 f();
             }
@@ -378,63 +402,52 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         for (int it = 0; ok; ++it) {
             const PtPair p = pt_pair(a, QT, cta, false);
             const int nkt = max(0, p.nkt);
-            int j = 0;
-            if (nkt > 0) {
-                ok = wait_all(q_full, pairs) && k_ready(2 * base);
-                if (!ok) break;
+            // both query tiles' S of key tile j; then K (after the last one Q) is free
+            auto first_s = [&](int j) {
+                const int n = base + j;
+                const uint32_t buf = uniform(n & 1), dk = slot_k(n);
                 issue([&] {
-                    mma_s(0, 2 * base);
-                    mma_s(1, 2 * base);
-                    umma_commit(&kv_empty[2 * base % NS]);
-                    if (nkt == 1) umma_commit(q_empty);
+                    mma_s(0, buf, dk);
+                    mma_s(1, buf, dk);
+                    umma_commit(&kv_empty[2 * n % NS]);
+                    if (j + 1 == nkt) umma_commit(q_empty);
                 });
+            };
+            if (nkt > 0) {
+                if (!(ok = wait_all(q_full, pairs) && k_ready(2 * base))) break;
+                first_s(0);
             }
-            for (; j < nkt; ++j) {
-                const int n = base + j;                        // tiles so far: phases
-                const bool more = j + 1 < nkt, last_s = j + 2 == nkt;
-                const int iv = 2 * n + 1, ik = 2 * n + 2;      // V(j), K(j + 1)
+            if (nkt > 1) {
+                if (!(ok = k_ready(2 * base + 2))) break;
+                first_s(1);
+            }
+            for (int j = 0; j < nkt; ++j) {
+                // P . V(j) frees the buffer that S(j + 2) takes (MMAs of one thread run
+                // in the order of issue), and S(j + 1) is there already
+                const int n = base + j;
+                const bool more = j + 2 < nkt;
                 // the first P . V of a pair overwrites O of the pair before
-                auto o_ready = [&](int t) { return j > 0 || pairs == 0 || wait_all(&o_free[t], pairs - 1); };
-                if (L::ALIAS) {
-                    // P lies over S: P . V(j) of a query tile goes before its S(j + 1)
-                    // (MMAs of one thread run in the order of issue)
-                    if (!(ok = v_ready(p, j, iv) && wait_all(&p_full[0], n) && o_ready(0))) break;
-                    issue([&] { mma_pv(0, iv, j > 0); });
-                    if (more) {
-                        if (!(ok = k_ready(ik))) break;
-                        issue([&] { mma_s(0, ik); });
-                    }
-                    if (!(ok = wait_all(&p_full[1], n) && o_ready(1))) break;
-                    issue([&] {
-                        mma_pv(1, iv, j > 0);
-                        umma_commit(&kv_empty[iv % NS]);
-                        if (more) {
-                            mma_s(1, ik);
-                            umma_commit(&kv_empty[ik % NS]);
-                            if (last_s) umma_commit(q_empty);
-                        }
-                    });
-                } else {
-                    // S(j + 1) as soon as the rows of S(j) are in registers, while they
-                    // are exponentiated
-                    if (more) {
-                        if (!(ok = k_ready(ik) && wait_all(&s_free[0], n))) break;
-                        issue([&] { mma_s(0, ik); });
-                        if (!(ok = wait_all(&s_free[1], n))) break;
-                        issue([&] {
-                            mma_s(1, ik);
-                            umma_commit(&kv_empty[ik % NS]);
-                            if (last_s) umma_commit(q_empty);
-                        });
-                    }
-                    if (!(ok = v_ready(p, j, iv) && wait_all(&p_full[0], n) && o_ready(0))) break;
-                    issue([&] { mma_pv(0, iv, j > 0); });
-                    if (!(ok = wait_all(&p_full[1], n) && o_ready(1))) break;
-                    issue([&] {
-                        mma_pv(1, iv, j > 0);
-                        umma_commit(&kv_empty[iv % NS]);
-                    });
+                auto p_ready = [&](int t) {
+                    return wait_all(&p_full[2 * t + (n & 1)], n >> 1) &&
+                           (j > 0 || pairs == 0 || wait_all(&o_free[t], pairs - 1));
+                };
+                const uint32_t buf = uniform(n & 1), dv = slot_v(n), dk = slot_k(n + 2);
+                if (!(ok = v_ready(p, j, 2 * n + 1) && p_ready(0))) break;
+                issue([&] { mma_pv(0, buf, dv, j > 0); });
+                if (more) {
+                    if (!(ok = k_ready(2 * n + 4))) break;
+                    issue([&] { mma_s(0, buf, dk); });
                 }
+                if (!(ok = p_ready(1))) break;
+                issue([&] {
+                    mma_pv(1, buf, dv, j > 0);
+                    umma_commit(&kv_empty[(2 * n + 1) % NS]);
+                    if (more) {
+                        mma_s(1, buf, dk);
+                        umma_commit(&kv_empty[(2 * n + 4) % NS]);
+                        if (j + 3 == nkt) umma_commit(q_empty);
+                    }
+                });
             }
             if (!ok) break;
             base += nkt;
@@ -451,9 +464,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const int r = qw * 32 + lane;                 // row within the tile
         const int tok = t * QT + r / G, h = r % G;    // token of the pair, head of the group
         const uint32_t lane_off = (uint32_t)(qw * 32) << 16;
-        const uint32_t tS = tmem + L::COL_S + t * 128 + lane_off;
-        const uint32_t tO = tmem + L::COL_O + t * DP + lane_off;
-        const uint32_t tP = tmem + L::col_p(t) + lane_off;
+        const uint32_t tO = tmem + L::col_o(t) + lane_off;
         const float sc = a.scale * LOG2E;             // > 0
         unsigned cta = blockIdx.x;
         int base = 0;                                 // key tiles so far
@@ -464,9 +475,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const bool live = p.nkt >= 0 && r < QT * G && tok < p.tokens;
         const int qp = p.pos0 + min(tok, p.tokens - 1);   // its position (rows that are not live: the last one's)
         float m = SOFTMAX_FLOOR, l = 0.f;             // reference maximum (of s * sc), sum of 2^(s sc - m)
-        uint32_t v[PT_KEYS];                          // the row's products, then its weights; at the end its O
         for (int j = 0; j < nkt; ++j) {
-            if (!wait_all(&s_full[t], base + j)) {
+            const int n = base + j;
+            const uint32_t tS = tmem + L::col_s(t, n & 1) + lane_off;
+            uint32_t v[PT_KEYS];                      // the row's products, then its weights
+            if (!wait_all(&s_full[2 * t + (n & 1)], n >> 1)) {
                 ok = false;
                 break;
             }
@@ -474,10 +487,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 #pragma unroll
             for (int c = 0; c < PT_KEYS; c += 32) tmem_ld32(tS + c, v + c);
             tmem_ld_wait();
-            if (!L::ALIAS) {
-                tc_fence_before();
-                mbar_arrive(&s_free[t]);
-            }
             // column c is visible when c < hi and (c >= lo or c < sk)
             const int key0 = p.key0(j);
             const int hi = qp - key0 + 1;
@@ -523,47 +532,58 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 rs[(c >> 1) & 3] = add2(rs[(c >> 1) & 3], w);
                 v[c >> 1] = E::pack(w.x, w.y);
             }
-            if (j > 0) {   // P . V(j - 1) must be complete before O is touched or P is rewritten
-                if (!wait_all(&o_full[t], base + j - 1)) {
+            if (any_move && j > 0) {   // O is touched: P . V(j - 1) must be complete
+                if (!wait_all(&o_full[t], n - 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (any_move) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < DP; c0 += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + c0, o);
-                        tmem_ld_wait();
+                for (int c0 = 0; c0 < DP; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + c0, o);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-                        tmem_st16(tO + c0, o);
-                        tmem_st16(tO + c0 + 16, o + 16);
-                    }
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+                    tmem_st16(tO + c0, o);
+                    tmem_st16(tO + c0 + 16, o + 16);
                 }
             }
+            // over S(j), all of it read; P . V(j - 2), the last reader here, was issued before S(j)
 #pragma unroll
-            for (int c = 0; c < PT_KEYS / 2; c += 16) tmem_st16(tP + c, v + c);
+            for (int c = 0; c < PT_KEYS / 2; c += 16) tmem_st16(tS + c, v + c);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&p_full[t]);
+            mbar_arrive(&p_full[2 * t + (n & 1)]);
             const float2 r2 = add2(add2(rs[0], rs[1]), add2(rs[2], rs[3]));
             l += r2.x + r2.y;
         }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint32_t w[DP / 2];                           // the row of the output
+#pragma unroll
+        for (int c = 0; c < DP / 2; ++c) w[c] = 0u;
         if (ok && nkt > 0) {
-            ok = wait_all(&o_full[t], base + nkt - 1);
+            // one phase after the other: S(last) only says that P . V(last - 2) is complete
+            ok = (nkt == 1 || wait_all(&o_full[t], base + nkt - 2)) && wait_all(&o_full[t], base + nkt - 1);
             tc_fence_after();
             if (ok) {
 #pragma unroll
-                for (int c = 0; c < DP; c += 32) tmem_ld32(tO + c, v + c);
-                tmem_ld_wait();
+                for (int c = 0; c < DP; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t x = E::pack(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                        w[c / 2 + i] = l == 0.f ? 0u : x;
+                    }
+                }
                 tc_fence_before();
                 mbar_arrive(&o_free[t]);
             }
         }
         if (!ok) break;
         {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
             const long long row = p.row0 + tok;
             uint16_t* own = live ? a.out + row * a.ld_out + (long long)(p.g * G + h) * D : nullptr;
             // four neighbouring lanes exchange 16-byte pieces, so that together they
@@ -576,17 +596,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 #pragma unroll
             for (int c0 = 0; c0 < DP; c0 += 32) {
                 if (c0 >= D) break;
-                uint4 w[4];
+                uint4 q[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int c = c0 + 8 * i;
-                    w[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (l != 0.f) {
-                        w[i].x = E::pack(__uint_as_float(v[c]) * inv, __uint_as_float(v[c + 1]) * inv);
-                        w[i].y = E::pack(__uint_as_float(v[c + 2]) * inv, __uint_as_float(v[c + 3]) * inv);
-                        w[i].z = E::pack(__uint_as_float(v[c + 4]) * inv, __uint_as_float(v[c + 5]) * inv);
-                        w[i].w = E::pack(__uint_as_float(v[c + 6]) * inv, __uint_as_float(v[c + 7]) * inv);
-                    }
+                    const uint32_t* x = w + c0 / 2 + 4 * i;
+                    q[i] = make_uint4(x[0], x[1], x[2], x[3]);
                 }
                 auto swap = [&](uint4& x, uint4& y, bool upper, int d) {   // lanes d apart: my y for its x
                     const uint4 give = upper ? x : y;
@@ -598,15 +612,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     if (upper) x = got;
                     else y = got;
                 };
-                swap(w[0], w[1], odd, 1);
-                swap(w[2], w[3], odd, 1);
-                swap(w[0], w[2], high, 2);
-                swap(w[1], w[3], high, 2);
-                // now w[i] is piece lane % 4 of row i of the four
+                swap(q[0], q[1], odd, 1);
+                swap(q[2], q[3], odd, 1);
+                swap(q[0], q[2], high, 2);
+                swap(q[1], q[3], high, 2);
+                // now q[i] is piece lane % 4 of row i of the four
                 const int c = c0 + 8 * (lane & 3);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (rows[i] && c < D) *reinterpret_cast<uint4*>(rows[i] + c) = w[i];
+                    if (rows[i] && c < D) *reinterpret_cast<uint4*>(rows[i] + c) = q[i];
             }
             if (a.lse && live) a.lse[row * a.NH + p.g * G + h] = l == 0.f ? -INFINITY : m * LN2 + logf(l);
         }
@@ -647,7 +661,7 @@ bool paged_prefill_maps(const PagedPrefillArgs& a, PagedPrefillMaps& m) {
     const uint32_t qb[3] = {64u, (uint32_t)G, (uint32_t)(PT_ROWS / G)};
     const uint64_t dims[4] = {(uint64_t)c.D, 1ull << c.page_shift, (uint64_t)c.NKV, (uint64_t)c.n_pages};
     const uint64_t strides[3] = {(uint64_t)c.row_stride * 2, (uint64_t)c.head_stride * 2, (uint64_t)c.page_stride * 2};
-    const uint32_t box[4] = {64u, (1u << c.page_shift) < 128u ? 1u << c.page_shift : 128u, 1u, 1u};
+    const uint32_t box[4] = {64u, (1u << c.page_shift) < (unsigned)PT_KEYS ? 1u << c.page_shift : (unsigned)PT_KEYS, 1u, 1u};
     return encode_map_bf16(m.q, a.q, 3, qd, qs, qb) && encode_map_bf16(m.k, c.k, 4, dims, strides, box) &&
            encode_map_bf16(m.v, c.v, 4, dims, strides, box);
 }
