@@ -23,7 +23,7 @@
 // transposed copy).  Boxes of pages that no row sees point beyond the pool, which
 // TMA fills with zeros without reading anything; so does a bad page number.  In
 // the tiles at the edges (the last one, the ends of the sinks and the window's
-// start) the MMA warp zeroes the V rows that no row sees, since 0 * NaN from a
+// start) a warp zeroes the V rows that no row sees, since 0 * NaN from a
 // stale row would not be 0.
 //
 // P is rounded to the cache's type, bf16 2^-9 of each weight at most, which in a
@@ -37,11 +37,12 @@
 // and ring slots count on across the pairs.
 //
 // Warps 0-3: tile A; warps 4-7: tile B (a warp reads the TMEM lanes of its index
-// mod 4); warp 8: TMA producer; warp 9: TMEM allocation, edge rows, MMA issue;
-// warps 10 and 11 only complete the warpgroup that gives up registers.  A row's
-// 64 scores, and at the end its output, stand in registers at once, so a row's
-// thread needs more of them (200) than the other warps (104).  Every mbarrier wait is bounded; a timeout raises
-// EMBER_ERR_TIMEOUT, the CTA drains its copies and frees TMEM.
+// mod 4); warp 8: TMA producer; warp 9: TMEM allocation; warps
+// 9 and 10: MMA issue for tile A and for tile B, so that neither's waiting holds
+// up the other's products; warp 11: edge rows.  A row's 64 scores, and at the end
+// its output, stand in registers at once, so a row's thread needs more of them
+// (200) than the other warps (104).  Every mbarrier wait is bounded; a timeout
+// raises EMBER_ERR_TIMEOUT, the CTA drains its copies and frees TMEM.
 #include <cudaTypedefs.h>
 
 #include "paged.cuh"
@@ -52,7 +53,7 @@ namespace ember {
 namespace {
 
 constexpr int PT_THREADS = 384;
-constexpr int PT_TMA = 8, PT_MMA = 9;   // warps
+constexpr int PT_TMA = 8, PT_MMA = 9, PT_EDGE = 11;   // warps (PT_MMA and the one after it: tiles A and B)
 constexpr int PT_REGS_ROW = 200, PT_REGS_REST = 104;   // 256 * 200 + 128 * 104 = 384 * 168, the launch's share
 constexpr int PT_ROWS = 128;   // rows of a query tile
 constexpr int PT_KEYS = 64;    // keys of a tile
@@ -66,7 +67,7 @@ struct PtSmem {
     static constexpr int OFF_Q = 0;                       // Q of tile A, of tile B
     static constexpr int OFF_KV = 2 * QTILE;
     static constexpr int OFF_BAR = OFF_KV + NS * TILE;
-    static constexpr int TOTAL = OFF_BAR + 512 + 1024;    // + barriers, + alignment slack
+    static constexpr int TOTAL = OFF_BAR + 640 + 1024;    // + barriers, + alignment slack
     static_assert(TOTAL <= 232448, "shared memory of a CTA");
     // TMEM columns: two S buffers of 64 f32 for each query tile, the weights P (64
     // values, two to a column) over the first half of theirs; O_A, O_B (DP f32 each)
@@ -207,35 +208,39 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
     uint64_t* s_full = bar + 0;     // [query tile][buffer]
     uint64_t* p_full = bar + 4;     // [query tile][buffer]
-    uint64_t* o_full = bar + 8;     // [query tile]
-    uint64_t* o_free = bar + 10;    // [query tile] O of a finished pair is in registers
-    uint64_t* q_full = bar + 12;
-    uint64_t* q_empty = bar + 13;
-    uint64_t* next_full = bar + 14;   // [2] answer of the it-th request in answers[it % 2]
-    uint64_t* next_empty = bar + 16;  // [2]
-    uint64_t* answers = bar + 18;     // [2] of 16 bytes
-    uint64_t* kv_full = bar + 22;     // [NS]: slot i % NS holds K (i even) or V (i odd) of the (i / 2)-th key tile
-    uint64_t* kv_empty = bar + 38;    // [NS]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 54);
-    int* sflag = reinterpret_cast<int*>(bar + 55);   // failed
+    uint64_t* o_full = bar + 8;     // [query tile][buffer]: P . V of that buffer's tile is complete
+    uint64_t* o_free = bar + 12;    // [query tile] O of a finished pair is in registers
+    uint64_t* q_full = bar + 14;
+    uint64_t* q_empty = bar + 15;
+    uint64_t* next_full = bar + 16;   // [2] answer of the it-th request in answers[it % 2]
+    uint64_t* next_empty = bar + 18;  // [2]
+    uint64_t* answers = bar + 20;     // [2] of 16 bytes
+    uint64_t* kv_full = bar + 24;     // [NS]: slot i % NS holds K (i even) or V (i odd) of the (i / 2)-th key tile
+    uint64_t* kv_empty = bar + 40;    // [NS]
+    uint64_t* v_raw = bar + 56;       // [NS / 2] V as it came, before the edge warp has seen it
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 64);
+    int* sflag = reinterpret_cast<int*>(bar + 65);   // failed
+    // A wait names a phase by its parity, so whoever waits on a barrier sees every
+    // one of its phases in turn.
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 128);
+            mbar_init(&o_full[i], 1);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&o_full[t], 1);
             mbar_init(&o_free[t], 128);
             mbar_init(&next_full[t], 1);
-            mbar_init(&next_empty[t], 10);   // the warps that read the answer
+            mbar_init(&next_empty[t], 12);   // the warps that read the answer
         }
         mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
+        mbar_init(q_empty, 2);               // both MMA warps
         for (int i = 0; i < NS; ++i) {
             mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
+            mbar_init(&kv_empty[i], 2);
+            if (i & 1) mbar_init(&v_raw[i >> 1], 1);
         }
         sflag[0] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -307,14 +312,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     if (!is_v && j + 1 < p.nkt) next = look_up(j + 1);
                     ok = issued < NS || wait_all(&kv_empty[s], issued / NS - 1);
                     if (!ok) break;
-                    if (lane == 0) mbar_expect_tx(&kv_full[s], L::TILE);
+                    uint64_t* full = is_v ? &v_raw[s >> 1] : &kv_full[s];   // (NS is even)
+                    if (lane == 0) mbar_expect_tx(full, L::TILE);
                     __syncwarp();
                     if (lane < boxes) {
                         const int row = (p.key0(j) + lane * box) & (P - 1);
                         uint8_t* d = sm + L::OFF_KV + s * L::TILE + lane * box * 128;
 #pragma unroll
                         for (int kb = 0; kb < L::KB; ++kb)
-                            tma_load_4d(d + kb * PT_KEYS * 128, is_v ? &tmV : &tmK, kb * 64, row, p.g, page, &kv_full[s]);
+                            tma_load_4d(d + kb * PT_KEYS * 128, is_v ? &tmV : &tmK, kb * 64, row, p.g, page, full);
                     }
                     if (is_v) page = next;
                 }
@@ -338,56 +344,70 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             // what is in flight lands before the block ends
             if (asked) (void)mbar_wait(&next_full[it & 1], (uint32_t)(it >> 1) & 1u);
             if (pairs) (void)mbar_wait(q_full, (uint32_t)(pairs - 1) & 1u);
-            for (int i = max(0, issued - NS); i < issued; ++i) (void)mbar_wait(&kv_full[i % NS], (uint32_t)(i / NS) & 1u);
+            for (int i = max(0, issued - NS); i < issued; ++i)
+                (void)mbar_wait(i & 1 ? &v_raw[i % NS >> 1] : &kv_full[i % NS], (uint32_t)(i / NS) & 1u);
         }
-    } else if (warp == PT_MMA) {   // ------------------------------ MMA issuer
+    } else if (warp == PT_EDGE) {   // ----------------------------- V rows that nobody sees become zeros
+        unsigned cta = blockIdx.x;
+        int base = 0;
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            const PtPair p = pt_pair(a, QT, cta, false);
+            const int nkt = max(0, p.nkt);
+            for (int j = 0; ok && j < nkt; ++j) {
+                const int i = 2 * (base + j) + 1, s = i % NS, key0 = p.key0(j);
+                ok = wait_all(&v_raw[s >> 1], i / NS);
+                if (ok && (key0 + PT_KEYS > p.end || (key0 < p.first && key0 + PT_KEYS > p.sinks))) {
+                    const uint32_t v = smem_u32(sm + L::OFF_KV + s * L::TILE);
+                    auto zero = [&](int r0, int r1) {   // rows [r0, r1): 16 bytes a lane
+#pragma unroll 4
+                        for (int e = max(r0, 0) * 8 * L::KB + lane; e < min(r1, PT_KEYS) * 8 * L::KB; e += 32)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             v + (L::KB == 1 ? e * 16
+                                                             : ((e >> 3) & 1) * (PT_KEYS * 128) + (e >> 4) * 128 + (e & 7) * 16)),
+                                         "r"(0)
+                                         : "memory");
+                    };
+                    zero(p.sinks - key0, p.first - key0);
+                    zero(p.end - key0, PT_KEYS);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                if (ok && lane == 0) mbar_arrive(&kv_full[s]);
+            }
+            if (!ok) break;
+            base += nkt;
+            if (!take_next(it, cta, ok)) break;
+        }
+        if (!ok && lane == 0) sflag[0] = 1;
+    } else {   // -------------------------------------------------- MMA issuers, one for each query tile
+        const int t = warp - PT_MMA;
         constexpr uint32_t type = E::bf16 ? idesc_bf16(0, 0) : idesc_f16(0, 0);
         constexpr uint32_t idS = type | idesc_f16(PT_ROWS, PT_KEYS);
         constexpr uint32_t idO = type | idesc_f16(PT_ROWS, DP) | IDESC_B_MN;
         // Issuing is the tensor pipe's pace-maker when a product takes 45 to 64 cycles:
         // operands are warp-uniform, descriptors one addition each.
         const uint32_t tm = uniform(tmem);
-        const uint32_t dq = uniform(desc_k(smem_u32(sm + L::OFF_Q)));
         const uint32_t kv0 = uniform(smem_u32(sm + L::OFF_KV));
-        auto mma_s = [&](int t, uint32_t buf, uint32_t dk) {   // S_t = Q_t . K^T
+        const uint32_t col_s = tm + uniform(t * 128), col_o = tm + uniform(L::col_o(t));
+        const uint32_t dq = uniform(desc_k(smem_u32(sm + L::OFF_Q + t * L::QTILE)));
+        auto mma_s = [&](uint32_t buf, uint32_t dk) {   // S = Q . K^T
 #pragma unroll
             for (int kb = 0; kb < L::KB; ++kb)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_ss(tm + L::col_s(t, 0) + buf * 64, dq + ((t * L::QTILE + kb * PT_ROWS * 128 + k * 32) >> 4),
+                    mma_ss(col_s + buf * 64, dq + ((kb * PT_ROWS * 128 + k * 32) >> 4),
                            dk + ((kb * PT_KEYS * 128 + k * 32) >> 4), idS, kb | k);
             umma_commit(&s_full[2 * t + buf]);
         };
-        auto mma_pv = [&](int t, uint32_t buf, uint32_t dv, bool acc) {   // O_t += P_t (TMEM) . V
+        auto mma_pv = [&](uint32_t buf, uint32_t dv, bool acc) {   // O += P (TMEM) . V
 #pragma unroll
             for (int k = 0; k < PT_KEYS / 16; ++k)
-                mma_ts(tm + L::col_o(t), tm + L::col_s(t, 0) + buf * 64 + k * 8, dv + ((k * 16 * 128) >> 4), idO, acc || k);
-            umma_commit(&o_full[t]);
+                mma_ts(col_o, col_s + buf * 64 + k * 8, dv + ((k * 16 * 128) >> 4), idO, acc || k);
+            umma_commit(&o_full[2 * t + buf]);
         };
         auto slot_k = [&](int n) { return uniform(desc_k(kv0 + (2 * n % NS) * L::TILE)); };
         auto slot_v = [&](int n) { return uniform(desc_mn(kv0 + ((2 * n + 1) % NS) * L::TILE, PT_KEYS * 128)); };
-        auto k_ready = [&](int i) { return wait_all(&kv_full[i % NS], i / NS); };
-        // V of tile j in slot i; rows that nobody sees become zeros
-        auto v_ready = [&](const PtPair& p, int j, int i) {
-            if (!wait_all(&kv_full[i % NS], i / NS)) return false;
-            const int key0 = p.key0(j);
-            if (key0 + PT_KEYS > p.end || (key0 < p.first && key0 + PT_KEYS > p.sinks)) {
-                const uint32_t v = smem_u32(sm + L::OFF_KV + (i % NS) * L::TILE);
-                auto zero = [&](int r0, int r1) {       // rows [r0, r1): 16 bytes a lane
-#pragma unroll 4
-                    for (int e = max(r0, 0) * 8 * L::KB + lane; e < min(r1, PT_KEYS) * 8 * L::KB; e += 32)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         v + (L::KB == 1 ? e * 16 : ((e >> 3) & 1) * (PT_KEYS * 128) + (e >> 4) * 128 + (e & 7) * 16)),
-                                     "r"(0)
-                                     : "memory");
-                };
-                zero(p.sinks - key0, p.first - key0);
-                zero(p.end - key0, PT_KEYS);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-            }
-            return true;
-        };
         // one lane issues f() after everything the warp has waited for
         auto issue = [&](auto f) {
             if (elect_one()) {
@@ -402,48 +422,50 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         for (int it = 0; ok; ++it) {
             const PtPair p = pt_pair(a, QT, cta, false);
             const int nkt = max(0, p.nkt);
-            // both query tiles' S of key tile j; then K (after the last one Q) is free
+            auto slot_full = [&](int i) { return &kv_full[i % NS]; };
+            // S of the pair's key tile j; then K (after the last one Q) is free
             auto first_s = [&](int j) {
                 const int n = base + j;
+                if (!(ok = wait_all(slot_full(2 * n), 2 * n / NS))) return;
                 const uint32_t buf = uniform(n & 1), dk = slot_k(n);
                 issue([&] {
-                    mma_s(0, buf, dk);
-                    mma_s(1, buf, dk);
+                    mma_s(buf, dk);
                     umma_commit(&kv_empty[2 * n % NS]);
                     if (j + 1 == nkt) umma_commit(q_empty);
                 });
             };
             if (nkt > 0) {
-                if (!(ok = wait_all(q_full, pairs) && k_ready(2 * base))) break;
+                if (!(ok = wait_all(q_full, pairs))) break;
                 first_s(0);
             }
-            if (nkt > 1) {
-                if (!(ok = k_ready(2 * base + 2))) break;
-                first_s(1);
-            }
+            if (ok && nkt > 1) first_s(1);
+            if (!ok) break;
             for (int j = 0; j < nkt; ++j) {
                 // P . V(j) frees the buffer that S(j + 2) takes (MMAs of one thread run
                 // in the order of issue), and S(j + 1) is there already
                 const int n = base + j;
                 const bool more = j + 2 < nkt;
-                // the first P . V of a pair overwrites O of the pair before
-                auto p_ready = [&](int t) {
-                    return wait_all(&p_full[2 * t + (n & 1)], n >> 1) &&
-                           (j > 0 || pairs == 0 || wait_all(&o_free[t], pairs - 1));
-                };
                 const uint32_t buf = uniform(n & 1), dv = slot_v(n), dk = slot_k(n + 2);
-                if (!(ok = v_ready(p, j, 2 * n + 1) && p_ready(0))) break;
-                issue([&] { mma_pv(0, buf, dv, j > 0); });
-                if (more) {
-                    if (!(ok = k_ready(2 * n + 4))) break;
-                    issue([&] { mma_s(0, buf, dk); });
+                // P(j), V(j), K(j + 2) and, before a pair's first P . V, the end of the
+                // pair before's use of O: a lane each, so that one poll sees them all
+                uint64_t* b = &p_full[2 * t + (n & 1)];
+                int parity = n >> 1;
+                if ((lane & 3) == 1) {
+                    b = slot_full(2 * n + 1);
+                    parity = (2 * n + 1) / NS;
+                } else if ((lane & 3) == 2 && more) {
+                    b = slot_full(2 * n + 4);
+                    parity = (2 * n + 4) / NS;
+                } else if ((lane & 3) == 3 && j == 0 && pairs > 0) {
+                    b = &o_free[t];
+                    parity = pairs - 1;
                 }
-                if (!(ok = p_ready(1))) break;
+                if (!(ok = wait_all(b, parity))) break;
                 issue([&] {
-                    mma_pv(1, buf, dv, j > 0);
+                    mma_pv(buf, dv, j > 0);
                     umma_commit(&kv_empty[(2 * n + 1) % NS]);
                     if (more) {
-                        mma_s(1, buf, dk);
+                        mma_s(buf, dk);
                         umma_commit(&kv_empty[(2 * n + 4) % NS]);
                         if (j + 3 == nkt) umma_commit(q_empty);
                     }
@@ -479,7 +501,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             const int n = base + j;
             const uint32_t tS = tmem + L::col_s(t, n & 1) + lane_off;
             uint32_t v[PT_KEYS];                      // the row's products, then its weights
-            if (!wait_all(&s_full[2 * t + (n & 1)], n >> 1)) {
+            // S(n); and P . V(n - 2), complete before it, for its phase to be seen
+            const bool odd_lane = n >= 2 && (lane & 1);
+            if (!wait_all((odd_lane ? o_full : s_full) + 2 * t + (n & 1), odd_lane ? (n >> 1) - 1 : n >> 1)) {
                 ok = false;
                 break;
             }
@@ -533,7 +557,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 v[c >> 1] = E::pack(w.x, w.y);
             }
             if (any_move && j > 0) {   // O is touched: P . V(j - 1) must be complete
-                if (!wait_all(&o_full[t], n - 1)) {
+                if (!wait_all(&o_full[2 * t + ((n - 1) & 1)], (n - 1) >> 1)) {
                     ok = false;
                     break;
                 }
@@ -563,8 +587,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 #pragma unroll
         for (int c = 0; c < DP / 2; ++c) w[c] = 0u;
         if (ok && nkt > 0) {
-            // one phase after the other: S(last) only says that P . V(last - 2) is complete
-            ok = (nkt == 1 || wait_all(&o_full[t], base + nkt - 2)) && wait_all(&o_full[t], base + nkt - 1);
+            const int last = base + nkt - 1;
+            ok = wait_all(&o_full[2 * t + (last & 1)], last >> 1);
             tc_fence_after();
             if (ok) {
 #pragma unroll
