@@ -486,10 +486,11 @@ struct PagedDecodeArgs {
     uint16_t* out;               // [B][ld_out]
     long long ld_out;
     float* lse;                  // [B][NH] or nullptr
-    float* ws;                   // partials, paged_decode_ws floats
+    float* ws;                   // records and partials, paged_decode_ws bytes
     int* status;
 };
-size_t paged_decode_ws(int NKV, int G, int D, int sms);   // bytes
+// bytes of ws that the call's split needs (a window only ever lowers them)
+size_t paged_decode_ws(const PagedView& c, int B, int NH, int window, int sinks, int sms);
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int sms, cudaStream_t s);
 
 // Attention of the last cu[b + 1] - cu[b] positions of each sequence.

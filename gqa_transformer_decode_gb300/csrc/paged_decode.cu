@@ -675,30 +675,39 @@ __global__ void __launch_bounds__(PJ_THREADS) k_paged_join(PagedDecodeArgs a, in
 
 int pd_grid_full(int sms, int G) { return min(PD_MAX_CTAS, sms * pd_ctas_per_sm(G <= 8 ? 1 : 2)); }
 
+// How a call is split: by the most blocks that its table and window allow.
+struct PdPlan {
+    int cluster;   // CTAs of a cluster, 0 for the line
+    int grid;      // the line's CTAs
+};
+PdPlan pd_plan(const PagedView& c, int B, int NH, int window, int sinks, int sms) {
+    const int G = NH / c.NKV, KEYS = c.D <= 64 ? PD_KEYS<64> : PD_KEYS<128>;
+    const long long keys = (long long)c.width << c.page_shift;
+    // (a window's blocks: its own, one more at each end that it cuts, one that the sinks cut)
+    const long long seen = window > 0 ? min(keys, (long long)window + sinks + 3 * KEYS) : keys;
+    const long long blocks = (seen + KEYS - 1) / KEYS, pairs = (long long)B * c.NKV;
+    int C = 1;
+    while (C < PD_MAX_CLUSTER && C * PD_WARPS < blocks) C *= 2;
+    if (pairs * C <= pd_grid_full(sms, G) && blocks <= C * PD_WARPS * PD_CLUSTER_BLOCKS) return {C, 0};
+    return {0, (int)min((long long)pd_grid_full(sms, G), (blocks * pairs + PD_MIN_BLOCKS - 1) / PD_MIN_BLOCKS)};
+}
+
 template <class E, int DP, int HT>
 cudaError_t launch_ht(const PagedDecodeArgs& a, int sms, cudaStream_t s) {
     constexpr int SMEM = PdSmem<DP, HT>::TOTAL;
-    const int G = a.NH / a.c.NKV;
-    // the most blocks that the table allows a sequence
-    const long long keys = (long long)a.c.width << a.c.page_shift;
-    const long long seen = a.window > 0 ? min(keys, (long long)a.window + a.sinks + 2 * PD_KEYS<DP>) : keys;
-    const long long blocks = (seen + PD_KEYS<DP> - 1) / PD_KEYS<DP>;
-    const long long pairs = (long long)a.B * a.c.NKV;
-    int C = 1;
-    while (C < PD_MAX_CLUSTER && C * PD_WARPS < blocks) C *= 2;
-    if (pairs * C <= pd_grid_full(sms, G) && blocks <= C * PD_WARPS * PD_CLUSTER_BLOCKS) {
+    const PdPlan plan = pd_plan(a.c, a.B, a.NH, a.window, a.sinks, sms);
+    if (plan.cluster) {
         auto k = k_paged_decode<E, DP, HT, true>;
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (e != cudaSuccess) return e;
-        return launch_cluster_k(k, dim3(C, a.c.NKV, a.B), dim3(PD_THREADS), SMEM, C, s, a);
+        return launch_cluster_k(k, dim3(plan.cluster, a.c.NKV, a.B), dim3(PD_THREADS), SMEM, plan.cluster, s, a);
     }
     auto k = k_paged_decode<E, DP, HT, false>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    const int grid = (int)min((long long)pd_grid_full(sms, G), (blocks * pairs + PD_MIN_BLOCKS - 1) / PD_MIN_BLOCKS);
-    const cudaError_t r = launch_k(k, dim3(grid), dim3(PD_THREADS), SMEM, s, a);
-    if (r != cudaSuccess || grid == 1) return r;
-    return launch_k(k_paged_join<E>, dim3(grid - 1, G), dim3(PJ_THREADS), 0, s, a, grid);
+    const cudaError_t r = launch_k(k, dim3(plan.grid), dim3(PD_THREADS), SMEM, s, a);
+    if (r != cudaSuccess || plan.grid == 1) return r;
+    return launch_k(k_paged_join<E>, dim3(plan.grid - 1, a.NH / a.c.NKV), dim3(PJ_THREADS), 0, s, a, plan.grid);
 }
 
 template <class E, int DP>
@@ -708,9 +717,9 @@ cudaError_t launch_dp(const PagedDecodeArgs& a, int sms, cudaStream_t s) {
 
 }  // namespace
 
-size_t paged_decode_ws(int NKV, int G, int D, int sms) {
-    (void)NKV;
-    return (size_t)pd_grid_full(sms, G) * (4 + 2 * (size_t)G * (D + 2)) * sizeof(float);
+size_t paged_decode_ws(const PagedView& c, int B, int NH, int window, int sinks, int sms) {
+    const PdPlan plan = pd_plan(c, B, NH, window, sinks, sms);
+    return plan.cluster ? 0 : (size_t)plan.grid * (4 + 2 * (size_t)(NH / c.NKV) * (c.D + 2)) * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int sms, cudaStream_t s) {

@@ -156,13 +156,14 @@ ember_status ember_paged_append(const ember_paged_kv* kv, const void* q, const v
 }
 
 size_t ember_paged_decode_workspace(const ember_paged_kv* kv, int32_t B, int32_t n_heads) {
-    if (!kv || B <= 0 || n_heads <= 0 || kv->n_kv_heads <= 0 || n_heads % kv->n_kv_heads || kv->head_dim <= 0) return 0;
+    PagedView c;
     int sms = 0;
+    if (B <= 0 || B > 65535 || check_cache(kv, c) != EMBER_OK || check_heads(kv, n_heads) != EMBER_OK) return 0;
     if (device_sms(&sms) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
-    return paged_decode_ws(kv->n_kv_heads, n_heads / kv->n_kv_heads, kv->head_dim, sms);
+    return paged_decode_ws(c, B, n_heads, 0, 0, sms);
 }
 
 ember_status ember_paged_decode(const ember_paged_kv* kv, const void* q, int64_t ld_q, int32_t B, int32_t n_heads,
@@ -183,9 +184,10 @@ ember_status ember_paged_decode(const ember_paged_kv* kv, const void* q, int64_t
     int sms = 0;
     cudaError_t e = device_sms(&sms);
     if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "no device: %s", cudaGetErrorString(e));
-    if (!workspace || !aligned16(workspace)) PG_FAIL(EMBER_ERR_INVALID_ARG, "workspace must be given and 16-byte aligned");
-    if (workspace_bytes < paged_decode_ws(kv->n_kv_heads, n_heads / kv->n_kv_heads, kv->head_dim, sms))
-        PG_FAIL(EMBER_ERR_CAPACITY, "workspace smaller than ember_paged_decode_workspace");
+    const size_t need = paged_decode_ws(a.c, B, n_heads, window, sinks, sms);
+    if ((need && !workspace) || !aligned16(workspace))
+        PG_FAIL(EMBER_ERR_INVALID_ARG, "workspace must be given and 16-byte aligned");
+    if (workspace_bytes < need) PG_FAIL(EMBER_ERR_CAPACITY, "workspace smaller than ember_paged_decode_workspace");
     a.q = static_cast<const uint16_t*>(q);
     a.ld_q = ld_q;
     a.B = B;

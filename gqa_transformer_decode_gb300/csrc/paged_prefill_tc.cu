@@ -227,11 +227,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 128);
+            mbar_init(&p_full[i], 4);    // the warps of a query tile
             mbar_init(&o_full[i], 1);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&o_free[t], 128);
+            mbar_init(&o_free[t], 4);
             mbar_init(&next_full[t], 1);
             mbar_init(&next_empty[t], 12);   // the warps that read the answer
         }
@@ -578,7 +578,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             for (int c = 0; c < PT_KEYS / 2; c += 16) tmem_st16(tS + c, v + c);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&p_full[2 * t + (n & 1)]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * t + (n & 1)]);
             const float2 r2 = add2(add2(rs[0], rs[1]), add2(rs[2], rs[3]));
             l += r2.x + r2.y;
         }
@@ -603,7 +604,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(&o_free[t]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_free[t]);
             }
         }
         if (!ok) break;

@@ -186,34 +186,40 @@ class PagedKV:
         self._c = c
         self._kv = C.addressof(c)
         self._lib = E.load()
+        self._index = self.k_pages.get_device()
         with torch.cuda.device(self.device):
             self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+            torch.cuda.current_stream().synchronize()   # zero before any stream uses it
         self._status = self.status.data_ptr()
         self._ws_bytes = {}
 
-    # -- checks ---------------------------------------------------------------
+    # -- checks (written for few calls into torch: they are most of a small call's cost) --
     def _ints(self, t, n, what):
-        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != self.device or \
-                (n > 1 and t.stride(0) != 1):
+        if t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != self._index or not t.is_contiguous():
             raise ValueError(f"{what} must be contiguous int32 [{n}] on {self.device}")
         return t.data_ptr()
 
-    def _rows(self, t, what, heads, dtype):
+    def _rows(self, t, what, n, heads, dtype):
         """[n, heads, head_dim] with a row's heads side by side -> (pointer, row stride)."""
         D = self.head_dim
-        if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads) or t.dtype != dtype or \
-                t.device != self.device:
-            raise ValueError(f"{what} must be {dtype} [n, {heads or 'heads'}, {D}] on {self.device}")
-        st = t.stride()
-        if st[2] != 1 or (t.shape[1] > 1 and st[1] != D):
+        if t.shape != (n, heads, D) or t.dtype is not dtype or t.get_device() != self._index:
+            raise ValueError(f"{what} must be {dtype} [{n}, {heads}, {D}] on {self.device}, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+        row, head, one = t.stride()
+        if one != 1 or (head != D and heads > 1):
             raise ValueError(f"{what}: a row's heads must lie side by side")
-        return t.data_ptr(), (st[0] if t.shape[0] > 1 else t.shape[1] * D)
+        return t.data_ptr(), (row if n > 1 else heads * D)
+
+    def _table(self, t, what, shape, dtype):
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != self._index or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous {dtype} {list(shape)} on {self.device}")
+        return t.data_ptr()
 
     def _run(self, stream):
         """-> (raw stream, context that makes the device and the stream current)."""
-        if stream is None and torch.cuda.current_device() == self.device.index:
-            return torch.cuda.current_stream().cuda_stream, _NOTHING
         if stream is None:
+            if torch.cuda.current_device() == self._index:
+                return _raw_stream(self._index), _NOTHING
             stream = torch.cuda.current_stream(self.device)
         if stream.device != self.device:
             raise ValueError(f"the stream belongs to {stream.device}, the cache to {self.device}")
@@ -228,43 +234,35 @@ class PagedKV:
         one type, f32, bf16 or f16; seqs, positions int32 [n]; cos, sin f32
         [n_pos, head_dim / 2]; q_norm, k_norm bf16 [head_dim].  Returns the
         rotated queries in the cache's type (q_out where given), or None."""
-        src = _SRC_DTYPES.get(k.dtype)
+        dt, n, heads, D = k.dtype, k.shape[0], 0, self.head_dim
+        src = _SRC_DTYPES.get(dt)
         if src is None:
             raise TypeError("q, k and v must be float32, bfloat16 or float16")
-        n = k.shape[0]
-        kp, ldk = self._rows(k, "k", self.n_kv_heads, k.dtype)
-        vp, ldv = self._rows(v, "v", self.n_kv_heads, k.dtype)
-        if v.shape[0] != n or (q is not None and q.shape[0] != n):
-            raise ValueError("q, k and v must have the same rows")
+        kp, ldk = self._rows(k, "k", n, self.n_kv_heads, dt)
+        vp, ldv = self._rows(v, "v", n, self.n_kv_heads, dt)
         sp, pp = self._ints(seqs, n, "seqs"), self._ints(positions, n, "positions")
-        half = self.head_dim // 2
-        for t in (cos, sin):
-            if t.dtype != torch.float32 or t.dim() != 2 or t.shape != (cos.shape[0], half) or \
-                    not t.is_contiguous() or t.device != self.device:
-                raise ValueError(f"cos and sin must be contiguous f32 [n_pos, {half}] on {self.device}")
-        norms = []
-        for t in (q_norm, k_norm):
-            if t is not None and (t.dtype != torch.bfloat16 or t.shape != (self.head_dim,) or
-                                  not t.is_contiguous() or t.device != self.device):
-                raise ValueError(f"q_norm and k_norm must be contiguous bf16 [{self.head_dim}] on {self.device}")
-            norms.append(None if t is None else t.data_ptr())
+        half = (cos.shape[0], D // 2)
+        cp, np_ = self._table(cos, "cos", half, torch.float32), self._table(sin, "sin", half, torch.float32)
+        qn = None if q_norm is None else self._table(q_norm, "q_norm", (D,), torch.bfloat16)
+        kn = None if k_norm is None else self._table(k_norm, "k_norm", (D,), torch.bfloat16)
+        qp = op = None
+        ldq = ldo = 0
+        if q is not None:
+            heads = q.shape[1]
+            qp, ldq = self._rows(q, "q", n, heads, dt)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
         raw, ctx = self._run(stream)
         with ctx:
-            qp, ldq, op, ldo, heads = None, 0, None, 0, 0
             if q is not None:
-                heads = q.shape[1]
-                qp, ldq = self._rows(q, "q", heads, k.dtype)
                 if q_out is None:
-                    q_out = torch.empty((n, heads, self.head_dim), dtype=self.dtype, device=self.device)
-                elif q_out.shape != q.shape:
-                    raise ValueError("q_out must have q's shape")
-                op, ldo = self._rows(q_out, "q_out", heads, self.dtype)
-            elif q_out is not None:
-                raise ValueError("q_out without q")
+                    q_out = torch.empty((n, heads, D), dtype=self.dtype, device=self.device)
+                    op, ldo = q_out.data_ptr(), heads * D
+                else:
+                    op, ldo = self._rows(q_out, "q_out", n, heads, self.dtype)
             if n:
                 st = self._lib.ember_paged_append(self._kv, qp, kp, vp, src, ldq, ldk, ldv, n, heads, sp, pp,
-                                                  norms[0], norms[1], eps, cos.data_ptr(), sin.data_ptr(),
-                                                  cos.shape[0], op, ldo, self._status, raw)
+                                                  qn, kn, eps, cp, np_, half[0], op, ldo, self._status, raw)
                 if st:
                     E.check(st, "ember_paged_append")
         return q_out
@@ -276,23 +274,29 @@ class PagedKV:
         int32 [B] (default: sequence b).  scale defaults to head_dim ** -0.5.
         Returns out, or (out, lse) with return_lse or lse.  workspace: a uint8
         tensor of at least workspace_bytes(B, n_heads) (default: allocated)."""
-        B, heads = q.shape[0], q.shape[1]
-        qp, ldq = self._rows(q, "q", None, self.dtype)
+        B, heads, D = q.shape
+        qp, ldq = self._rows(q, "q", B, heads, self.dtype)
         lp = self._ints(lens, B, "lens")
         sp = None if seqs is None else self._ints(seqs, B, "seqs")
         raw, ctx = self._run(stream)
         with ctx:
-            out, lse, op, ldo, ep = self._outputs(q, out, lse, return_lse)
+            out, lse, op, ldo, ep = self._outputs(B, heads, out, lse, return_lse)
             if B:
-                need = self.workspace_bytes(B, heads)
-                if workspace is None:
+                need = self._ws_bytes.get((B, heads))
+                if need is None:
+                    need = self.workspace_bytes(B, heads)
+                wp = None
+                if workspace is not None:
+                    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+                            workspace.get_device() != self._index:
+                        raise ValueError(f"workspace must be contiguous uint8 on {self.device}")
+                    wp, need = workspace.data_ptr(), workspace.numel()
+                elif need:
                     workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-                elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
-                        workspace.device != self.device:
-                    raise ValueError(f"workspace must be contiguous uint8 on {self.device}")
+                    wp = workspace.data_ptr()
                 st = self._lib.ember_paged_decode(self._kv, qp, ldq, B, heads, sp, lp, window, sinks,
-                                                  self.head_dim ** -0.5 if scale is None else scale, op, ldo, ep,
-                                                  workspace.data_ptr(), workspace.numel(), self._status, raw)
+                                                  D ** -0.5 if scale is None else scale, op, ldo, ep, wp, need,
+                                                  self._status, raw)
                 if st:
                     E.check(st, "ember_paged_decode")
         return out if lse is None else (out, lse)
@@ -302,36 +306,39 @@ class PagedKV:
         """Attention of several tokens per sequence: rows cu[b] .. cu[b + 1] - 1
         of q [n, n_heads, head_dim] are the last positions of sequence b (or
         seqs[b]), which holds lens[b] keys.  cu int32 [B + 1], lens int32 [B]."""
-        n, heads, B = q.shape[0], q.shape[1], lens.shape[0]
-        qp, ldq = self._rows(q, "q", None, self.dtype)
+        n, heads, D = q.shape
+        B = lens.shape[0]
+        qp, ldq = self._rows(q, "q", n, heads, self.dtype)
         lp, cp = self._ints(lens, B, "lens"), self._ints(cu, B + 1, "cu")
         sp = None if seqs is None else self._ints(seqs, B, "seqs")
         raw, ctx = self._run(stream)
         with ctx:
-            out, lse, op, ldo, ep = self._outputs(q, out, lse, return_lse)
+            out, lse, op, ldo, ep = self._outputs(n, heads, out, lse, return_lse)
             if n and B:
                 st = self._lib.ember_paged_prefill(self._kv, qp, ldq, n, B, heads, sp, cp, lp, window, sinks,
-                                                   self.head_dim ** -0.5 if scale is None else scale, op, ldo, ep,
+                                                   D ** -0.5 if scale is None else scale, op, ldo, ep,
                                                    self._status, raw)
                 if st:
                     E.check(st, "ember_paged_prefill")
         return out if lse is None else (out, lse)
 
-    def _outputs(self, q, out, lse, return_lse):
+    def _outputs(self, n, heads, out, lse, return_lse):
         if out is None:
-            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
-        elif out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        if lse is None and return_lse:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device)
-        elif lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or
-                                  not lse.is_contiguous() or lse.device != self.device):
-            raise ValueError("lse must be contiguous f32 [rows, n_heads]")
-        op, ldo = self._rows(out, "out", q.shape[1], self.dtype)
-        return out, lse, op, ldo, None if lse is None else lse.data_ptr()
+            out = torch.empty((n, heads, self.head_dim), dtype=self.dtype, device=self.device)
+            op, ldo = out.data_ptr(), heads * self.head_dim
+        else:
+            op, ldo = self._rows(out, "out", n, heads, self.dtype)
+        if lse is not None:
+            ep = self._table(lse, "lse", (n, heads), torch.float32)
+        elif return_lse:
+            lse = torch.empty((n, heads), dtype=torch.float32, device=self.device)
+            ep = lse.data_ptr()
+        else:
+            ep = None
+        return out, lse, op, ldo, ep
 
     def workspace_bytes(self, B: int, n_heads: int) -> int:
-        """Bytes of decode's workspace for B sequences of n_heads query heads."""
+        """Bytes of decode's workspace for B sequences of n_heads query heads (0: none is needed)."""
         n = self._ws_bytes.get((B, n_heads))
         if n is None:
             with torch.cuda.device(self.device):
@@ -352,6 +359,9 @@ class PagedKV:
 _PAGE_DTYPES = {torch.bfloat16: E.BF16, torch.float16: E.F16}
 _SRC_DTYPES = {torch.float32: E.F32, torch.bfloat16: E.BF16, torch.float16: E.F16}
 _NOTHING = contextlib.nullcontext()
+# the current stream's handle of a device, without the Stream object where torch has the shorter way
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _wrap_device(ptr: int, nbytes: int, device) -> torch.Tensor:

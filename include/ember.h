@@ -365,10 +365,13 @@ ember_status ember_paged_append(const ember_paged_kv *kv, const void *q, const v
  *   lse[b][h] = log sum_j exp(scale q . k_j)   (f32 [B][n_heads], nullable)
  * lens[b] == 0 gives out 0 and lse -inf.  q, out: [B] rows of
  * n_heads*head_dim elements of the cache's type.
- *   workspace: ember_paged_decode_workspace bytes, 16-byte aligned, of any
- *   content; used until the call's kernels end, so calls that may overlap
- *   (other streams, graphs that run at once) need one each.
- * The result depends on the inputs and the device only (no atomics).
+ *   workspace: ember_paged_decode_workspace bytes (which may be 0: then NULL
+ *   will do), 16-byte aligned, of any content; used until the call's kernels
+ *   end, so calls that may overlap (other streams, graphs that run at once) need
+ *   one each.
+ * How the keys are split, and with it the rounding, depends on B, the head
+ * counts, the window, lens, the table's width and the device; there are no
+ * atomics, so equal calls give equal bits.
  * Host errors: INVALID_ARG, UNSUPPORTED, CAPACITY (workspace too small), CUDA. */
 size_t ember_paged_decode_workspace(const ember_paged_kv *kv, int32_t B, int32_t n_heads);
 ember_status ember_paged_decode(const ember_paged_kv *kv, const void *q, int64_t ld_q, int32_t B,

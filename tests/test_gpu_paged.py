@@ -254,8 +254,8 @@ def test_decode_many_short_sequences():
     check_decode(p, q, out, lse)
 
 
-def test_decode_captured_replayed_and_on_other_streams():
-    lens = [300, 1000]
+@pytest.mark.parametrize("lens", [[300, 1000], [9000, 700]])   # joined in a cluster; over the workspace
+def test_decode_captured_replayed_and_on_other_streams(lens):
     p = Pool(19, lens, 2, 64, 16)
     q = p.queries(2, 14)
     ln = ints(lens)
@@ -285,10 +285,13 @@ def test_decode_captured_replayed_and_on_other_streams():
     q.copy_(p.queries(2, 14))
     graphs[0][0].replay()
     check_decode(p, q, graphs[0][1], None, lens=[17, 444])
-    ws = torch.empty(p.cache.workspace_bytes(2, 14), dtype=torch.uint8, device="cuda")
+    need = p.cache.workspace_bytes(2, 14)
+    assert (need > 0) == (lens[0] == 9000)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")      # NaN: any content will do
     assert torch.equal(graphs[0][1], p.cache.decode(q, ln, workspace=ws))
-    with pytest.raises(RuntimeError, match="workspace"):
-        p.cache.decode(q, ln, workspace=ws[:-16])
+    if need:
+        with pytest.raises(RuntimeError, match="workspace"):
+            p.cache.decode(q, ln, workspace=ws[:-16])
 
 
 def test_page_numbers_and_offsets_beyond_32_bits():
