@@ -51,7 +51,8 @@ constexpr int PD_MIN_BLOCKS = 8;     // blocks of a CTA at least (two per warp)
 constexpr int pd_ctas_per_sm(int ht) { return ht == 1 ? 3 : 2; }   // registers: 168 or 255 a thread
 constexpr int PD_MAX_CLUSTER = 8;     // CTAs of a cluster (a power of two)
 constexpr int PD_CLUSTER_BLOCKS = 8;  // blocks of a warp in cluster form at most
-constexpr int PD_MAX_CTAS = 1024;    // grid at most (the join's weights stand in shared memory)
+constexpr int PJ_PARTS = 8;           // partials of a (sequence, kv head) from which a block joins a single head
+constexpr int PD_MAX_CTAS = 512;     // grid at most (the join's weights stand in shared memory)
 // Keys of a block: 8 KB of K and V rows either way.
 template <int DP>
 constexpr int PD_KEYS = DP == 64 ? 32 : 16;
@@ -592,18 +593,19 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
 }
 
 // Joins the partials of each (sequence, kv head) that several CTAs share, in
-// CTA order.  Block (c, h) reads CTA c's record and, when a segment begins in
-// that CTA and goes on in later ones, joins head h of its group.  Threads take
-// four dimensions each and the partials in turn; the weights of all partials
-// are found at once before.
+// CTA order.  Block (c, y) reads CTA c's record and, when a segment begins in
+// that CTA and goes on in later ones, joins heads [y * heads, (y + 1) * heads) of
+// its group.  A warp finds the weights of a head's partials; then threads take
+// four dimensions each and the partials in turn.
 constexpr int PJ_WARPS = 8;
 constexpr int PJ_THREADS = PJ_WARPS * 32;
 
 template <class E>
-__global__ void __launch_bounds__(PJ_THREADS) k_paged_join(PagedDecodeArgs a, int grid) {
-    __shared__ float s_w[PD_MAX_CTAS], s_red[2 * PJ_WARPS];
+__global__ void __launch_bounds__(PJ_THREADS) k_paged_join(PagedDecodeArgs a, int grid, int heads) {
+    __shared__ float s_w[16][PD_MAX_CTAS];                 // [head][partial]
+    __shared__ float s_inv[16];
     __shared__ float4 s_o[PJ_THREADS];
-    const int c0 = blockIdx.x, h = blockIdx.y;
+    const int c0 = blockIdx.x, h0 = blockIdx.y * heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = a.c.D, G = a.NH / a.c.NKV;
     pdl_wait();
@@ -612,64 +614,71 @@ __global__ void __launch_bounds__(PJ_THREADS) k_paged_join(PagedDecodeArgs a, in
     const int b = rec.x, g = rec.y, parts = rec.z;
     if (parts == 0) return;
     // partial i: slot 0 of its CTA, but slot 1 of the first when the segment begins inside it
-    const float* base = partials(a, grid) + (size_t)h * (D + 2);
+    const float* base = partials(a, grid) + (size_t)h0 * (D + 2);
     const size_t slot = (size_t)G * (D + 2);
-    auto part = [&](int i) { return base + (2 * (size_t)(c0 + i) + (i == 0 ? rec.w : 0)) * slot; };
-    float M = SOFTMAX_FLOOR, m0 = SOFTMAX_FLOOR, l0 = 0.f;
-    for (int i = tid; i < parts; i += PJ_THREADS) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i)));
-        if (i == tid) {
-            m0 = ml.x;
-            l0 = ml.y;
+    auto part = [&](int h, int i) {
+        return base + (2 * (size_t)(c0 + i) + (i == 0 ? rec.w : 0)) * slot + (size_t)h * (D + 2);
+    };
+    for (int h = warp; h < heads; h += PJ_WARPS) {
+        float M = SOFTMAX_FLOOR, m0 = SOFTMAX_FLOOR, l0 = 0.f;
+        for (int i = lane; i < parts; i += 32) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(h, i)));
+            if (i == lane) {
+                m0 = ml.x;
+                l0 = ml.y;
+            }
+            s_w[h][i] = ml.x;
+            M = fmaxf(M, ml.x);
         }
-        s_w[i] = ml.x;
-        M = fmaxf(M, ml.x);
+        M = warp_max(M);
+        float L = 0.f;
+        for (int i = lane; i < parts; i += 32) {
+            const float f = ex2((i == lane ? m0 : s_w[h][i]) - M);
+            s_w[h][i] = f;
+            L += (i == lane ? l0 : __ldcg(part(h, i) + 1)) * f;
+        }
+        L = warp_sum(L);
+        if (lane == 0) {
+            s_inv[h] = L == 0.f ? 0.f : 1.f / L;
+            if (a.lse) a.lse[(long long)b * a.NH + g * G + h0 + h] = L == 0.f ? -INFINITY : M * LN2 + logf(L);
+        }
     }
-    M = warp_max(M);
-    if (lane == 0) s_red[warp] = M;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < PJ_WARPS; ++w) M = fmaxf(M, s_red[w]);
-    float L = 0.f;
-    for (int i = tid; i < parts; i += PJ_THREADS) {
-        const float f = ex2((i == tid ? m0 : s_w[i]) - M);
-        s_w[i] = f;
-        L += (i == tid ? l0 : __ldcg(part(i) + 1)) * f;
-    }
-    L = warp_sum(L);
-    if (lane == 0) s_red[PJ_WARPS + warp] = L;
-    __syncthreads();
-    L = 0.f;
-#pragma unroll
-    for (int w = 0; w < PJ_WARPS; ++w) L += s_red[PJ_WARPS + w];
-    const int quads = D / 4, turns = PJ_THREADS / quads;   // threads of a partial, partials at a time
-    const int d = 4 * (tid % quads), t0 = tid / quads;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int quads = heads * (D / 4);                      // four dimensions of a head each
+    const int turns = max(1, PJ_THREADS / quads);           // partials at a time
+    for (int q0 = 0; q0 < quads; q0 += PJ_THREADS) {
+        const int q = q0 + tid % min(quads, PJ_THREADS), t0 = tid / min(quads, PJ_THREADS);
+        const int h = q / (D / 4), d = 4 * (q - h * (D / 4));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q < quads && t0 < turns) {
 #pragma unroll 8
-    for (int i = t0; i < parts; i += turns) {
-        const float2* p = reinterpret_cast<const float2*>(part(i) + 2 + d);
-        const float2 u = __ldcg(p), v = __ldcg(p + 1);
-        const float f = s_w[i];
-        o.x = fmaf(u.x, f, o.x);
-        o.y = fmaf(u.y, f, o.y);
-        o.z = fmaf(v.x, f, o.z);
-        o.w = fmaf(v.y, f, o.w);
-    }
-    s_o[tid] = o;
-    __syncthreads();
-    if (tid < quads) {
-        for (int t = 1; t < turns; ++t) {
-            const float4 y = s_o[tid + t * quads];
-            o.x += y.x;
-            o.y += y.y;
-            o.z += y.z;
-            o.w += y.w;
+            for (int i = t0; i < parts; i += turns) {
+                const float2* p = reinterpret_cast<const float2*>(part(h, i) + 2 + d);
+                const float2 u = __ldcg(p), v = __ldcg(p + 1);
+                const float f = s_w[h][i];
+                o.x = fmaf(u.x, f, o.x);
+                o.y = fmaf(u.y, f, o.y);
+                o.z = fmaf(v.x, f, o.z);
+                o.w = fmaf(v.y, f, o.w);
+            }
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        uint2* out = reinterpret_cast<uint2*>(a.out + (long long)b * a.ld_out + (long long)(g * G + h) * D + d);
-        *out = make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
-        if (a.lse && tid == 0)
-            a.lse[(long long)b * a.NH + g * G + h] = L == 0.f ? -INFINITY : M * LN2 + logf(L);
+        if (turns > 1) {
+            s_o[tid] = o;
+            __syncthreads();
+            if (t0 == 0)
+                for (int t = 1; t < turns; ++t) {
+                    const float4 y = s_o[tid + t * quads];
+                    o.x += y.x;
+                    o.y += y.y;
+                    o.z += y.z;
+                    o.w += y.w;
+                }
+        }
+        if (q < quads && t0 == 0) {
+            const float inv = s_inv[h];
+            uint2* out = reinterpret_cast<uint2*>(a.out + (long long)b * a.ld_out + (long long)(g * G + h0 + h) * D + d);
+            *out = make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
+        }
     }
 }
 
@@ -707,7 +716,10 @@ cudaError_t launch_ht(const PagedDecodeArgs& a, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const cudaError_t r = launch_k(k, dim3(plan.grid), dim3(PD_THREADS), SMEM, s, a);
     if (r != cudaSuccess || plan.grid == 1) return r;
-    return launch_k(k_paged_join<E>, dim3(plan.grid - 1, a.NH / a.c.NKV), dim3(PJ_THREADS), 0, s, a, plan.grid);
+    // A block joins a group's heads, since every CTA of the grid has a block and most
+    // find nothing to do; but one head where few (sequence, kv head)s have many partials.
+    const int G = a.NH / a.c.NKV, heads = (long long)a.B * a.c.NKV * PJ_PARTS < plan.grid ? 1 : G;
+    return launch_k(k_paged_join<E>, dim3(plan.grid - 1, G / heads), dim3(PJ_THREADS), 0, s, a, plan.grid, heads);
 }
 
 template <class E, int DP>
