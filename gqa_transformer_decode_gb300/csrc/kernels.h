@@ -508,8 +508,9 @@ struct PagedPrefillArgs {
     long long ld_out;
     float* lse;                  // [n][NH] or nullptr
     int* status;
+    int parts;                   // set by launch_paged_prefill_tc: CTAs that share a tile pair's keys
 };
-cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, cudaStream_t s);
+cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, int sms, cudaStream_t s);
 // The same on tcgen05 (paged_prefill_tc.cu; scale > 0), through TMA maps over the
 // queries and the pages (paged_prefill_maps; false if the driver rejects one).
 // launch_paged_prefill picks it for calls with rows enough.
@@ -517,7 +518,7 @@ struct PagedPrefillMaps {
     alignas(64) unsigned char q[128], k[128], v[128];
 };
 bool paged_prefill_maps(const PagedPrefillArgs& a, PagedPrefillMaps& m);
-cudaError_t launch_paged_prefill_tc(const PagedPrefillArgs& a, const PagedPrefillMaps& m, cudaStream_t s);
+cudaError_t launch_paged_prefill_tc(const PagedPrefillArgs& a, const PagedPrefillMaps& m, int sms, cudaStream_t s);
 
 // out[c][r] = in[r][c] for 16-bit elements
 void launch_transpose16(const uint16_t* in, uint16_t* out, int rows, int cols, cudaStream_t s);

@@ -136,27 +136,6 @@ __device__ __forceinline__ unsigned scan_chunk(const PagedDecodeArgs& a, int b0,
 // The workspace: a record for each CTA of the grid, then two partials for each.
 __device__ __forceinline__ float* partials(const PagedDecodeArgs& a, int grid) { return a.ws + 4 * (size_t)grid; }
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-    float v;
-    asm volatile("{\n\t.reg .u32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
-                 : "=f"(v)
-                 : "r"(addr), "r"(rank)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr, uint32_t rank) {
-    float2 v;
-    asm volatile(
-        "{\n\t.reg .u32 r;\n\tmapa.shared::cluster.u32 r, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [r];\n\t}"
-        : "=f"(v.x), "=f"(v.y)
-        : "r"(addr), "r"(rank)
-        : "memory");
-    return v;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // A place in the line: block `i` of kv head g of sequence b.
 struct Place {
     int b, g, i;

@@ -236,7 +236,10 @@ ember_status ember_paged_prefill(const ember_paged_kv* kv, const void* q, int64_
     a.ld_out = ld_out;
     a.lse = lse;
     a.status = status;
-    const cudaError_t e = launch_paged_prefill(a, (cudaStream_t)stream);
+    int sms = 0;
+    cudaError_t e = device_sms(&sms);
+    if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "no device: %s", cudaGetErrorString(e));
+    e = launch_paged_prefill(a, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "prefill launch failed: %s", cudaGetErrorString(e));
     return EMBER_OK;
 }

@@ -208,11 +208,11 @@ cudaError_t launch_dp(const PagedPrefillArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, cudaStream_t s) {
+cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, int sms, cudaStream_t s) {
     PagedPrefillMaps maps;
     // (the tcgen05 kernel takes the largest product for the largest score: scale > 0)
     if ((long long)a.n * (a.NH / a.c.NKV) >= PP_TC_ROWS && a.scale > 0.f && paged_prefill_maps(a, maps))
-        return launch_paged_prefill_tc(a, maps, s);
+        return launch_paged_prefill_tc(a, maps, sms, s);
     if (a.c.bf16) return a.c.D <= 64 ? launch_dp<ElemBf16, 64>(a, s) : launch_dp<ElemBf16, 128>(a, s);
     return a.c.D <= 64 ? launch_dp<ElemF16, 64>(a, s) : launch_dp<ElemF16, 128>(a, s);
 }

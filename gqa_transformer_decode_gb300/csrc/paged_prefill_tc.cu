@@ -36,6 +36,10 @@
 // one's epilogue, and the pairs still go to whichever SM is free.  Barrier phases
 // and ring slots count on across the pairs.
 //
+// A call with few pairs splits their keys instead (SPLIT): the CTAs of a cluster
+// share a pair's key tiles, leave (m, l, O) of its rows in their shared memory and
+// join a share of the rows each through distributed shared memory.
+//
 // Warps 0-3: tile A; warps 4-7: tile B (a warp reads the TMEM lanes of its index
 // mod 4); warp 8: TMA producer; warp 9: TMEM allocation; warps
 // 9 and 10: MMA issue for tile A and for tile B, so that neither's waiting holds
@@ -57,6 +61,7 @@ constexpr int PT_TMA = 8, PT_MMA = 9, PT_EDGE = 11;   // warps (PT_MMA and the o
 constexpr int PT_REGS_ROW = 200, PT_REGS_REST = 104;   // 256 * 200 + 128 * 104 = 384 * 168, the launch's share
 constexpr int PT_ROWS = 128;   // rows of a query tile
 constexpr int PT_KEYS = 64;    // keys of a tile
+constexpr int PT_PARTS = 8;    // CTAs of a cluster at most
 
 template <int DP>
 struct PtSmem {
@@ -69,6 +74,7 @@ struct PtSmem {
     static constexpr int OFF_BAR = OFF_KV + NS * TILE;
     static constexpr int TOTAL = OFF_BAR + 640 + 1024;    // + barriers, + alignment slack
     static_assert(TOTAL <= 232448, "shared memory of a CTA");
+    static_assert(2 * PT_ROWS * (DP * 4 + 8) <= OFF_BAR, "the split form's rows");
     // TMEM columns: two S buffers of 64 f32 for each query tile, the weights P (64
     // values, two to a column) over the first half of theirs; O_A, O_B (DP f32 each)
     static constexpr uint32_t col_s(int t, int b) { return t * 128 + b * 64; }
@@ -147,15 +153,18 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 struct PtPair {
     int g, seq, row0, tokens, pos0;   // kv head, table row, first query row, tokens, position of the first
     int end, first, sinks;            // keys that some row sees: [first, end) and [0, sinks)
-    int ns, wb, nkt;                  // key tiles: of the sinks, first of the window, in all (-1: no such pair)
-    __device__ __forceinline__ int key0(int j) const { return PT_KEYS * (j < ns ? j : wb + j - ns); }
+    int ns, wb, j0, nkt;              // key tiles: of the sinks, first of the window; this CTA's first and number (-1: no such pair)
+    __device__ __forceinline__ int key0(int j) const { return PT_KEYS * (j0 + j < ns ? j0 + j : wb + j0 + j - ns); }
 };
-__device__ __forceinline__ PtPair pt_pair(const PagedPrefillArgs& a, int QT, unsigned cta, bool reporter) {
+// pair: its number among `pairs`; the keys in `parts` shares, of which the part-th.
+__device__ __forceinline__ PtPair pt_pair(const PagedPrefillArgs& a, int QT, unsigned pair, unsigned pairs, int part,
+                                          int parts, bool reporter) {
     PtPair p;
     // the last tiles see the most keys: those of all kv heads go first
-    const int x = (int)(gridDim.x - 1 - cta) / a.c.NKV;
-    p.g = (int)(gridDim.x - 1 - cta) % a.c.NKV;
+    const int x = (int)(pairs - 1 - pair) / a.c.NKV;
+    p.g = (int)(pairs - 1 - pair) % a.c.NKV;
     p.nkt = -1;
+    p.tokens = 0;
     const RowTile tile = find_row_tile(a, 2 * QT, x, reporter && x == 0 && p.g == 0);
     if (tile.b < 0) return p;
     const SeqRows sr = seq_rows(a, tile.b, false);
@@ -169,7 +178,9 @@ __device__ __forceinline__ PtPair pt_pair(const PagedPrefillArgs& a, int QT, uns
     p.sinks = min(a.sinks, p.first);
     p.ns = (p.sinks + PT_KEYS - 1) / PT_KEYS;
     p.wb = max(p.first / PT_KEYS, p.ns);
-    p.nkt = p.end <= 0 ? 0 : p.ns + max(0, (p.end + PT_KEYS - 1) / PT_KEYS - p.wb);
+    const int all = p.end <= 0 ? 0 : p.ns + max(0, (p.end + PT_KEYS - 1) / PT_KEYS - p.wb);
+    p.j0 = (int)((long long)all * part / parts);
+    p.nkt = (int)((long long)all * (part + 1) / parts) - p.j0;
     return p;
 }
 
@@ -197,7 +208,7 @@ __device__ __forceinline__ bool cancelled(uint32_t answer, unsigned& cta) {
     return ok != 0;
 }
 
-template <class E, int DP>
+template <class E, int DP, bool SPLIT>
 __global__ void __launch_bounds__(PT_THREADS, 1)
     k_paged_prefill_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, PagedPrefillArgs a) {
@@ -253,6 +264,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     }
     const int D = a.c.D, G = a.NH / a.c.NKV;
     const int QT = PT_ROWS / G;                        // tokens of a query tile
+    const int parts = SPLIT ? a.parts : 1, part = SPLIT ? (int)(blockIdx.x % parts) : 0;   // (a cluster's CTAs)
+    const unsigned first_pair = blockIdx.x / parts, pairs_all = gridDim.x / parts;
     pdl_wait();
     tc_fence_before();
     __syncthreads();
@@ -264,6 +277,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     };
     // the CTA index after the it-th pair's: false when there is none left (or, ok = false, no answer)
     auto take_next = [&](int it, unsigned& cta, bool& ok) {
+        if (SPLIT) return false;
         if (!wait_all(&next_full[it & 1], it >> 1)) {
             ok = false;
             return false;
@@ -281,11 +295,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const int P = 1 << a.c.page_shift;
         const int box = min(P, PT_KEYS);               // rows of a box
         const int boxes = PT_KEYS / box;               // of a tile: lane i < boxes copies box i
-        unsigned cta = blockIdx.x;
+        unsigned cta = first_pair;
         int issued = 0, pairs = 0, it = 0;             // slots and pairs with keys so far
         bool ok = true, asked = false;
         for (;; ++it) {
-            const PtPair p = pt_pair(a, QT, cta, true);
+            const PtPair p = pt_pair(a, QT, cta, pairs_all, part, parts, part == 0);
             if (p.nkt > 0) {
                 auto look_up = [&](int j) {            // the lane's page of tile j; n_pages reads as zeros
                     const int k0 = p.key0(j) + lane * box;
@@ -328,14 +342,16 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             }
             // asked for only now, a ring's worth of tiles before the pair ends: a CTA
             // that asked at its start would hold work that another could begin first
-            ok = it < 2 || wait_all(&next_empty[it & 1], (it >> 1) - 1);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_expect_tx(&next_full[it & 1], 16);
-                try_cancel(smem_u32(answers + 2 * (it & 1)), &next_full[it & 1]);
+            if (!SPLIT) {
+                ok = it < 2 || wait_all(&next_empty[it & 1], (it >> 1) - 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_expect_tx(&next_full[it & 1], 16);
+                    try_cancel(smem_u32(answers + 2 * (it & 1)), &next_full[it & 1]);
+                }
+                __syncwarp();
+                asked = true;
             }
-            __syncwarp();
-            asked = true;
             if (!take_next(it, cta, ok)) break;
             asked = false;
         }
@@ -348,11 +364,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 (void)mbar_wait(i & 1 ? &v_raw[i % NS >> 1] : &kv_full[i % NS], (uint32_t)(i / NS) & 1u);
         }
     } else if (warp == PT_EDGE) {   // ----------------------------- V rows that nobody sees become zeros
-        unsigned cta = blockIdx.x;
+        unsigned cta = first_pair;
         int base = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            const PtPair p = pt_pair(a, QT, cta, false);
+            const PtPair p = pt_pair(a, QT, cta, pairs_all, part, parts, false);
             const int nkt = max(0, p.nkt);
             for (int j = 0; ok && j < nkt; ++j) {
                 const int i = 2 * (base + j) + 1, s = i % NS, key0 = p.key0(j);
@@ -416,11 +432,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             }
             __syncwarp();
         };
-        unsigned cta = blockIdx.x;
+        unsigned cta = first_pair;
         int base = 0, pairs = 0;   // key tiles and pairs with keys so far
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            const PtPair p = pt_pair(a, QT, cta, false);
+            const PtPair p = pt_pair(a, QT, cta, pairs_all, part, parts, false);
             const int nkt = max(0, p.nkt);
             auto slot_full = [&](int i) { return &kv_full[i % NS]; };
             // S of the pair's key tile j; then K (after the last one Q) is free
@@ -488,11 +504,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const uint32_t lane_off = (uint32_t)(qw * 32) << 16;
         const uint32_t tO = tmem + L::col_o(t) + lane_off;
         const float sc = a.scale * LOG2E;             // > 0
-        unsigned cta = blockIdx.x;
+        unsigned cta = first_pair;
         int base = 0;                                 // key tiles so far
         bool ok = true;
+        PtPair pair;                                  // (SPLIT: the one pair)
         for (int it = 0; ok; ++it) {
-        const PtPair p = pt_pair(a, QT, cta, false);
+        const PtPair p = pt_pair(a, QT, cta, pairs_all, part, parts, false);
         const int nkt = max(0, p.nkt);
         const bool live = p.nkt >= 0 && r < QT * G && tok < p.tokens;
         const int qp = p.pos0 + min(tok, p.tokens - 1);   // its position (rows that are not live: the last one's)
@@ -583,6 +600,32 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             const float2 r2 = add2(add2(rs[0], rs[1]), add2(rs[2], rs[3]));
             l += r2.x + r2.y;
         }
+        if (SPLIT) {   // the rows as they are into shared memory; joined below
+            if (ok && nkt > 0) {
+                const int last = base + nkt - 1;
+                ok = wait_all(&o_full[2 * t + (last & 1)], last >> 1);
+                tc_fence_after();
+            }
+            // both query tiles' products are complete: nothing reads Q, K or V any more
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            const int at = t * PT_ROWS + r;
+            float* mine = reinterpret_cast<float*>(sm) + at * DP;
+#pragma unroll
+            for (int c = 0; c < DP; c += 32) {
+                uint32_t o[32];
+                if (nkt > 0) {
+                    tmem_ld32(tO + c, o);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<uint4*>(mine + 4 * (((c + i) / 4) ^ (r & 7))) =
+                        nkt > 0 ? make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            reinterpret_cast<float2*>(sm + 2 * PT_ROWS * DP * 4)[at] = make_float2(m, l);
+            pair = p;
+            break;
+        }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         uint32_t w[DP / 2];                           // the row of the output
 #pragma unroll
@@ -654,6 +697,54 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         if (!take_next(it, cta, ok)) break;
         }
         if (!ok) sflag[0] = 1;
+        if (SPLIT) {
+            cluster_sync_all();
+            // rows [part, part + 1) * 256 / parts, eight dimensions a thread
+            const uint32_t o_at = smem_u32(sm), ml_at = o_at + 2 * PT_ROWS * DP * 4;
+            const int rows = 2 * PT_ROWS / parts;
+            for (int e = threadIdx.x; e < rows * (DP / 8); e += 256) {
+                const int at = part * rows + e / (DP / 8), c = e % (DP / 8), rr = at % PT_ROWS;
+                const int tk = at / PT_ROWS * QT + rr / G, hh = rr % G;
+                if (rr >= QT * G || tk >= pair.tokens || c * 8 >= D) continue;
+                float mx = SOFTMAX_FLOOR, sum = 0.f, acc[8];
+                float2 ml[PT_PARTS];
+#pragma unroll
+                for (int i = 0; i < PT_PARTS; ++i)
+                    if (i < parts) {
+                        ml[i] = ld_cluster2(ml_at + at * 8, i);
+                        mx = fmaxf(mx, ml[i].x);
+                    }
+#pragma unroll
+                for (int d = 0; d < 8; ++d) acc[d] = 0.f;
+#pragma unroll
+                for (int i = 0; i < PT_PARTS; ++i)
+                    if (i < parts) {
+                        const float f = ex2(ml[i].x - mx);
+                        sum = fmaf(ml[i].y, f, sum);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const float4 x = ld_cluster4(o_at + (at * DP + 4 * ((2 * c + q) ^ (rr & 7))) * 4, i);
+                            acc[4 * q] = fmaf(x.x, f, acc[4 * q]);
+                            acc[4 * q + 1] = fmaf(x.y, f, acc[4 * q + 1]);
+                            acc[4 * q + 2] = fmaf(x.z, f, acc[4 * q + 2]);
+                            acc[4 * q + 3] = fmaf(x.w, f, acc[4 * q + 3]);
+                        }
+                    }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                for (int d = 0; d < 8; ++d) acc[d] = sum == 0.f ? 0.f : acc[d] * inv;
+                const long long row = pair.row0 + tk;
+                *reinterpret_cast<uint4*>(a.out + row * a.ld_out + (long long)(pair.g * G + hh) * D + c * 8) =
+                    make_uint4(E::pack(acc[0], acc[1]), E::pack(acc[2], acc[3]), E::pack(acc[4], acc[5]), E::pack(acc[6], acc[7]));
+                if (a.lse && c == 0)
+                    a.lse[row * a.NH + pair.g * G + hh] = sum == 0.f ? -INFINITY : mx * LN2 + logf(sum);
+            }
+            cluster_sync_all();                       // no CTA leaves while another reads its shared memory
+        }
+    }
+    if (SPLIT && warp >= PT_TMA) {
+        cluster_sync_all();
+        cluster_sync_all();
     }
 
     tc_fence_before();
@@ -666,14 +757,28 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 }
 
 template <class E, int DP>
-cudaError_t launch_dp(const PagedPrefillMaps& m, const PagedPrefillArgs& a, cudaStream_t s) {
-    auto k = k_paged_prefill_tc<E, DP>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PtSmem<DP>::TOTAL);
-    if (e != cudaSuccess) return e;
+cudaError_t launch_dp(const PagedPrefillMaps& m, PagedPrefillArgs a, int sms, cudaStream_t s) {
+    constexpr int SMEM = PtSmem<DP>::TOTAL;
     const int per = 2 * (PT_ROWS / (a.NH / a.c.NKV));
-    const dim3 grid((unsigned)((((long long)a.n + per - 1) / per + a.B) * a.c.NKV));
-    return launch_k(k, grid, dim3(PT_THREADS), PtSmem<DP>::TOTAL, s, *reinterpret_cast<const CUtensorMap*>(m.q),
-                    *reinterpret_cast<const CUtensorMap*>(m.k), *reinterpret_cast<const CUtensorMap*>(m.v), a);
+    const unsigned pairs = (unsigned)((((long long)a.n + per - 1) / per + a.B) * a.c.NKV);
+    // CTAs of a cluster that share a pair's keys: as many as leave every one an SM and two key tiles
+    const long long keys = (long long)a.c.width << a.c.page_shift;
+    const long long seen = a.window > 0 ? min(keys, (long long)a.window + a.sinks + per) : keys;
+    a.parts = 1;
+    while (a.parts < PT_PARTS && pairs * a.parts * 2 <= (unsigned)sms && seen >= 4ll * a.parts * PT_KEYS) a.parts *= 2;
+    const auto& mq = *reinterpret_cast<const CUtensorMap*>(m.q);
+    const auto& mk = *reinterpret_cast<const CUtensorMap*>(m.k);
+    const auto& mv = *reinterpret_cast<const CUtensorMap*>(m.v);
+    if (a.parts > 1) {
+        auto k = k_paged_prefill_tc<E, DP, true>;
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        return launch_cluster_k(k, dim3(pairs * a.parts), dim3(PT_THREADS), SMEM, a.parts, s, mq, mk, mv, a);
+    }
+    auto k = k_paged_prefill_tc<E, DP, false>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_k(k, dim3(pairs), dim3(PT_THREADS), SMEM, s, mq, mk, mv, a);
 }
 
 }  // namespace
@@ -692,9 +797,9 @@ bool paged_prefill_maps(const PagedPrefillArgs& a, PagedPrefillMaps& m) {
            encode_map_bf16(m.v, c.v, 4, dims, strides, box);
 }
 
-cudaError_t launch_paged_prefill_tc(const PagedPrefillArgs& a, const PagedPrefillMaps& m, cudaStream_t s) {
-    if (a.c.bf16) return a.c.D <= 64 ? launch_dp<ElemBf16, 64>(m, a, s) : launch_dp<ElemBf16, 128>(m, a, s);
-    return a.c.D <= 64 ? launch_dp<ElemF16, 64>(m, a, s) : launch_dp<ElemF16, 128>(m, a, s);
+cudaError_t launch_paged_prefill_tc(const PagedPrefillArgs& a, const PagedPrefillMaps& m, int sms, cudaStream_t s) {
+    if (a.c.bf16) return a.c.D <= 64 ? launch_dp<ElemBf16, 64>(m, a, sms, s) : launch_dp<ElemBf16, 128>(m, a, sms, s);
+    return a.c.D <= 64 ? launch_dp<ElemF16, 64>(m, a, sms, s) : launch_dp<ElemF16, 128>(m, a, sms, s);
 }
 
 }  // namespace ember
