@@ -3,10 +3,13 @@
 // positions, each sees the keys at or before it (or a window of them and a few
 // first tokens), out = softmax(scale Q K^T) V and lse = log sum exp.
 //
-// The G query heads of a kv head share its keys, so a tile's rows are (token,
-// head) pairs: row r = token r / G, head r % G.  One CTA holds 64 rows of one
-// kv head, 16 to a warp, and walks the keys in tiles of 64 that cp.async copies
-// (zero fill for keys no row sees) stage two deep in shared memory.
+// This kernel serves short sequences, and what the tcgen05 kernel
+// (paged_prefill_tc.cu) does not take: a scale that is not positive.  The G query
+// heads of a kv head share its keys, so a tile's rows are (token, head) pairs: row
+// r = token r / G, head r % G.  One CTA holds 64 rows of one kv head, 16 to a
+// warp, and walks the keys in tiles of 64 that cp.async copies (zero fill for keys
+// no row sees) stage two deep in shared memory.  Bound by latency: 4 sequences
+// of 9 new tokens, 14 heads on 2, in 4.5 us.
 #include "paged.cuh"
 
 namespace ember {
@@ -16,7 +19,8 @@ namespace {
 constexpr int PP_THREADS = 128;
 constexpr int PP_ROWS = 64;
 constexpr int PP_KEYS = 64;
-constexpr int PP_TC_ROWS = 256;   // (token, head) rows per kv head of a call from which the tcgen05 kernel runs
+constexpr int PP_SMALL_KEYS = 128;   // keys that the table holds for a sequence
+constexpr int PP_SMALL_ROWS = 64;    // new tokens of a sequence, on average
 
 template <int DP>
 struct PpSmem {
@@ -209,10 +213,15 @@ cudaError_t launch_dp(const PagedPrefillArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, int sms, cudaStream_t s) {
+    // Short sequences only, where filling the tcgen05 kernel's pipeline costs more than
+    // the whole attention: 20 new tokens each of 256 sequences 58 us here and 85 there,
+    // 4 sequences of 9 tokens 4.5 and 6.3 us; but 100 of 64 sequences 32 and 27 us, and
+    // with keys for more than two of its tiles the other kernel wins at any size (2
+    // tokens on 200 keys 9.4 and 8.8 us, on 1000 keys 52 and 26 us).
+    const bool small = ((long long)a.c.width << a.c.page_shift) <= PP_SMALL_KEYS && a.n <= PP_SMALL_ROWS * (long long)a.B;
     PagedPrefillMaps maps;
     // (the tcgen05 kernel takes the largest product for the largest score: scale > 0)
-    if ((long long)a.n * (a.NH / a.c.NKV) >= PP_TC_ROWS && a.scale > 0.f && paged_prefill_maps(a, maps))
-        return launch_paged_prefill_tc(a, maps, sms, s);
+    if (!small && a.scale > 0.f && paged_prefill_maps(a, maps)) return launch_paged_prefill_tc(a, maps, sms, s);
     if (a.c.bf16) return a.c.D <= 64 ? launch_dp<ElemBf16, 64>(a, s) : launch_dp<ElemBf16, 128>(a, s);
     return a.c.D <= 64 ? launch_dp<ElemF16, 64>(a, s) : launch_dp<ElemF16, 128>(a, s);
 }
