@@ -451,6 +451,19 @@ def test_prefill_captured_and_on_another_stream():
     assert torch.equal(want, out)
 
 
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-4])
+def test_other_scales(scale):
+    lens, new = [300, 70], [130, 20]
+    p = Pool(67, lens, 2, 64, 16)
+    q = p.queries(2, 8, 2.0)
+    out, lse = p.cache.decode(q, ints(lens), window=100, sinks=3, scale=scale, return_lse=True)
+    check_decode(p, q, out, lse, window=100, sinks=3, scale=scale)
+    cu = [0, 130, 150]
+    q = p.queries(150, 8, 2.0)
+    out, lse = p.cache.prefill(q, ints(cu), ints(lens), window=100, sinks=3, scale=scale, return_lse=True)
+    check_prefill(p, q, out, lse, cu, lens, window=100, sinks=3, scale=scale, rows=20)
+
+
 def test_one_row_of_prefill_is_decode():
     lens = [1, 64, 300]
     p = Pool(41, lens, 2, 128, 32, "f16")
