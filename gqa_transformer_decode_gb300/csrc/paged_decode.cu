@@ -66,18 +66,16 @@ struct SeqBlocks {
 };
 
 template <int KEYS>
-__device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int b, bool report) {
+__device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int seq, int len, bool report) {
     SeqBlocks r;
     r.n = 0;
     r.ns = r.wb = r.end = r.first = r.sinks = 0;
     r.zero = false;
-    const int seq = a.seqs ? a.seqs[b] : b;
     if (seq < 0) return r;                                   // padding: the row is left as it is
     if (seq >= a.c.n_seqs) {
         if (report) raise_status(a.status, EMBER_ERR_INVALID_ARG);
         return r;
     }
-    const int len = a.lens[b];
     if (len < 0 || len > ((long long)a.c.width << a.c.page_shift)) {
         if (report) raise_status(a.status, EMBER_ERR_CAPACITY);
         return r;
@@ -94,6 +92,11 @@ __device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int b,
     r.wb = max(v.first / KEYS, r.ns);
     r.n = r.ns + (v.end + KEYS - 1) / KEYS - r.wb;
     return r;
+}
+
+template <int KEYS>
+__device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int b, bool report) {
+    return seq_blocks<KEYS>(a, a.seqs ? a.seqs[b] : b, a.lens[b], report);
 }
 
 // Blocks of the whole line divided over `ctas` CTAs: CTA c takes [lo(c), lo(c + 1)).
@@ -117,10 +120,16 @@ __device__ __forceinline__ unsigned scan_chunk(const PagedDecodeArgs& a, int b0,
                                                unsigned& before) {
     const int lane = threadIdx.x & 31;
     unsigned own = 0;
+    int seq[PD_SCAN], len[PD_SCAN];
 #pragma unroll
     for (int e = 0; e < PD_SCAN; ++e) {
         const int b = b0 + PD_SCAN * lane + e;
-        n[e] = b < a.B ? seq_blocks<KEYS>(a, b, report).n : 0;
+        seq[e] = b >= a.B ? -1 : a.seqs ? a.seqs[b] : b;
+        len[e] = b >= a.B ? 0 : a.lens[b];
+    }
+#pragma unroll
+    for (int e = 0; e < PD_SCAN; ++e) {
+        n[e] = seq_blocks<KEYS>(a, seq[e], len[e], report).n;
         own += n[e];
     }
     unsigned incl = own;
@@ -178,6 +187,19 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
             for (int e = h0 + tid; e < h1; e += PD_THREADS) a.lse[(long long)b * a.NH + e] = -INFINITY;
     };
 
+    // What the join finds: a record of each (sequence, kv head) or, where these are
+    // more than the CTAs, of each CTA's last one: {b, g, partials (0: nothing to
+    // join), first CTA * 2 + its slot}.
+    int4* record = reinterpret_cast<int4*>(a.ws);
+    auto no_keys = [&]() {                             // sequences without blocks, shared out over the CTAs
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            const SeqBlocks s = seq_blocks<KEYS>(a, b, false);
+            if (s.zero) zero_row(b, 0, a.NH);
+            if (a.by_pair && s.n == 0)
+                for (int g = tid; g < NKV; g += PD_THREADS) record[b * NKV + g] = make_int4(0, 0, 0, 0);
+        }
+    };
+
     // ---- this CTA's blocks [lo, hi) and the first one's place ----
     unsigned lo, hi;
     Place cur;
@@ -200,13 +222,11 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
         unsigned line = 0, before = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32 * PD_SCAN) line += scan_chunk<KEYS>(a, b0, blockIdx.x == 0 && warp == 0, n, before);
         line *= NKV;
-        int4* record = reinterpret_cast<int4*>(a.ws) + blockIdx.x;   // what the join finds of this CTA's last segment
         const Shares share(max(1u, line), gridDim.x);
         if (line == 0 || blockIdx.x >= share.ctas) {
             pdl_trigger();
-            if (tid == 0) *record = make_int4(0, 0, 0, 0);
-            for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-                if (seq_blocks<KEYS>(a, b, false).zero) zero_row(b, 0, a.NH);
+            if (!a.by_pair && tid == 0) record[blockIdx.x] = make_int4(0, 0, 0, 0);
+            no_keys();
             return;
         }
         lo = share.lo(blockIdx.x);
@@ -519,10 +539,13 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
                 ws[e] = d == 0 ? s_M[row] : d == 1 ? s_L[row] : s_o[row * L::ROW + d - 2];
             }
         }
-        if (tid == 0 && seg_end == hi) {     // does a segment begin here that later CTAs go on with?
-            const bool begins = cur.i == 0 && !complete;
-            const int parts = begins ? (int)((at + cur.s.n - 1) / (hi - lo)) - (int)blockIdx.x + 1 : 0;
-            reinterpret_cast<int4*>(a.ws)[blockIdx.x] = make_int4(cur.b, cur.g, parts, at == lo ? 0 : 1);
+        // a segment that begins here and that later CTAs go on with is this CTA's last
+        // (hi - lo is then every CTA's share)
+        if (tid == 0 && (a.by_pair ? cur.i == 0 : seg_end == hi)) {
+            const int parts =
+                cur.i == 0 && !complete ? (int)((at + cur.s.n - 1) / (hi - lo)) - (int)blockIdx.x + 1 : 0;
+            record[a.by_pair ? cur.b * NKV + cur.g : blockIdx.x] =
+                make_int4(cur.b, cur.g, parts, 2 * blockIdx.x + (at == lo ? 0 : 1));
         }
         at = seg_end;
         if (at >= hi) break;
@@ -531,8 +554,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
     cp_async_wait<0>();
     pdl_trigger();                           // late: the join's blocks would take issue slots meanwhile
     if (!CLUSTER) {
-        for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-            if (seq_blocks<KEYS>(a, b, false).zero) zero_row(b, 0, a.NH);
+        no_keys();
         return;
     }
 
@@ -572,49 +594,62 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
 }
 
 // Joins the partials of each (sequence, kv head) that several CTAs share, in
-// CTA order.  Block (c, y) reads CTA c's record and, when a segment begins in
-// that CTA and goes on in later ones, joins heads [y * heads, (y + 1) * heads) of
-// its group.  A warp finds the weights of a head's partials; then threads take
-// four dimensions each and the partials in turn.
+// CTA order.  Block (r, y) reads record r and joins heads [y * heads, (y + 1) *
+// heads) of its group.  Threads take four dimensions each and the partials in
+// turn; they ask for their first values together with the (m, l) of all partials,
+// of which a warp for each head then finds the weights.
 constexpr int PJ_WARPS = 8;
 constexpr int PJ_THREADS = PJ_WARPS * 32;
+constexpr int PJ_AHEAD = 4;
 
 template <class E>
 __global__ void __launch_bounds__(PJ_THREADS) k_paged_join(PagedDecodeArgs a, int grid, int heads) {
     __shared__ float s_w[16][PD_MAX_CTAS];                 // [head][partial]
     __shared__ float s_inv[16];
     __shared__ float4 s_o[PJ_THREADS];
-    const int c0 = blockIdx.x, h0 = blockIdx.y * heads;
+    const int h0 = blockIdx.y * heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = a.c.D, G = a.NH / a.c.NKV;
     pdl_wait();
     pdl_trigger();
-    const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.ws) + c0);
-    const int b = rec.x, g = rec.y, parts = rec.z;
+    const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.ws) + blockIdx.x);
+    const int b = rec.x, g = rec.y, parts = rec.z, c0 = rec.w >> 1;
     if (parts == 0) return;
     // partial i: slot 0 of its CTA, but slot 1 of the first when the segment begins inside it
     const float* base = partials(a, grid) + (size_t)h0 * (D + 2);
     const size_t slot = (size_t)G * (D + 2);
     auto part = [&](int h, int i) {
-        return base + (2 * (size_t)(c0 + i) + (i == 0 ? rec.w : 0)) * slot + (size_t)h * (D + 2);
+        return base + (2 * (size_t)(c0 + i) + (i == 0 ? rec.w & 1 : 0)) * slot + (size_t)h * (D + 2);
     };
+    const int quads = heads * (D / 4);                      // four dimensions of a head each
+    const int wide = min(quads, PJ_THREADS), turns = PJ_THREADS / wide;   // threads of a partial, partials at a time
+    const int t0 = tid / wide;
+    auto value = [&](int q, int i) {
+        const int h = q / (D / 4), d = 4 * (q - h * (D / 4));
+        const float2* p = reinterpret_cast<const float2*>(part(h, i) + 2 + d);
+        const float2 u = __ldcg(p), v = __ldcg(p + 1);
+        return make_float4(u.x, u.y, v.x, v.y);
+    };
+    float4 ahead[PJ_AHEAD];
+#pragma unroll
+    for (int k = 0; k < PJ_AHEAD; ++k)
+        if (t0 < turns && t0 + k * turns < parts) ahead[k] = value(tid % wide, t0 + k * turns);
     for (int h = warp; h < heads; h += PJ_WARPS) {
-        float M = SOFTMAX_FLOOR, m0 = SOFTMAX_FLOOR, l0 = 0.f;
-        for (int i = lane; i < parts; i += 32) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(h, i)));
-            if (i == lane) {
-                m0 = ml.x;
-                l0 = ml.y;
-            }
-            s_w[h][i] = ml.x;
-            M = fmaxf(M, ml.x);
+        float M = SOFTMAX_FLOOR;
+        float2 ml[2];                                       // the lane's first two partials
+        for (int i = lane, k = 0; i < parts; i += 32, ++k) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(part(h, i)));
+            if (k == 0) ml[0] = x;
+            if (k == 1) ml[1] = x;
+            M = fmaxf(M, x.x);
         }
         M = warp_max(M);
         float L = 0.f;
-        for (int i = lane; i < parts; i += 32) {
-            const float f = ex2((i == lane ? m0 : s_w[h][i]) - M);
+        for (int i = lane, k = 0; i < parts; i += 32, ++k) {
+            const float2 x = k == 0 ? ml[0] : k == 1 ? ml[1] : __ldcg(reinterpret_cast<const float2*>(part(h, i)));
+            const float f = ex2(x.x - M);
             s_w[h][i] = f;
-            L += (i == lane ? l0 : __ldcg(part(h, i) + 1)) * f;
+            L += x.y * f;
         }
         L = warp_sum(L);
         if (lane == 0) {
@@ -623,30 +658,29 @@ __global__ void __launch_bounds__(PJ_THREADS) k_paged_join(PagedDecodeArgs a, in
         }
     }
     __syncthreads();
-    const int quads = heads * (D / 4);                      // four dimensions of a head each
-    const int turns = max(1, PJ_THREADS / quads);           // partials at a time
     for (int q0 = 0; q0 < quads; q0 += PJ_THREADS) {
-        const int q = q0 + tid % min(quads, PJ_THREADS), t0 = tid / min(quads, PJ_THREADS);
-        const int h = q / (D / 4), d = 4 * (q - h * (D / 4));
+        const int q = q0 + tid % wide, h = q / (D / 4), d = 4 * (q - h * (D / 4));
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](const float4& x, int i) {
+            const float f = s_w[h][i];
+            o.x = fmaf(x.x, f, o.x);
+            o.y = fmaf(x.y, f, o.y);
+            o.z = fmaf(x.z, f, o.z);
+            o.w = fmaf(x.w, f, o.w);
+        };
         if (q < quads && t0 < turns) {
-#pragma unroll 8
-            for (int i = t0; i < parts; i += turns) {
-                const float2* p = reinterpret_cast<const float2*>(part(h, i) + 2 + d);
-                const float2 u = __ldcg(p), v = __ldcg(p + 1);
-                const float f = s_w[h][i];
-                o.x = fmaf(u.x, f, o.x);
-                o.y = fmaf(u.y, f, o.y);
-                o.z = fmaf(v.x, f, o.z);
-                o.w = fmaf(v.y, f, o.w);
-            }
+#pragma unroll
+            for (int k = 0; k < PJ_AHEAD; ++k)
+                if (t0 + k * turns < parts) add(q0 == 0 ? ahead[k] : value(q, t0 + k * turns), t0 + k * turns);
+#pragma unroll 4
+            for (int i = t0 + PJ_AHEAD * turns; i < parts; i += turns) add(value(q, i), i);
         }
         if (turns > 1) {
             s_o[tid] = o;
             __syncthreads();
             if (t0 == 0)
                 for (int t = 1; t < turns; ++t) {
-                    const float4 y = s_o[tid + t * quads];
+                    const float4 y = s_o[tid + t * wide];
                     o.x += y.x;
                     o.y += y.y;
                     o.z += y.z;
@@ -681,7 +715,7 @@ PdPlan pd_plan(const PagedView& c, int B, int NH, int window, int sinks, int sms
 }
 
 template <class E, int DP, int HT>
-cudaError_t launch_ht(const PagedDecodeArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_ht(PagedDecodeArgs a, int sms, cudaStream_t s) {
     constexpr int SMEM = PdSmem<DP, HT>::TOTAL;
     const PdPlan plan = pd_plan(a.c, a.B, a.NH, a.window, a.sinks, sms);
     if (plan.cluster) {
@@ -693,12 +727,14 @@ cudaError_t launch_ht(const PagedDecodeArgs& a, int sms, cudaStream_t s) {
     auto k = k_paged_decode<E, DP, HT, false>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
+    a.by_pair = (long long)a.B * a.c.NKV < plan.grid;
     const cudaError_t r = launch_k(k, dim3(plan.grid), dim3(PD_THREADS), SMEM, s, a);
     if (r != cudaSuccess || plan.grid == 1) return r;
-    // A block joins a group's heads, since every CTA of the grid has a block and most
-    // find nothing to do; but one head where few (sequence, kv head)s have many partials.
-    const int G = a.NH / a.c.NKV, heads = (long long)a.B * a.c.NKV * PJ_PARTS < plan.grid ? 1 : G;
-    return launch_k(k_paged_join<E>, dim3(plan.grid - 1, G / heads), dim3(PJ_THREADS), 0, s, a, plan.grid, heads);
+    // A block joins a group's heads, since most records say that there is nothing to
+    // do; but one head where few (sequence, kv head)s have many partials.
+    const int G = a.NH / a.c.NKV, records = a.by_pair ? a.B * a.c.NKV : plan.grid - 1;
+    const int heads = (long long)a.B * a.c.NKV * PJ_PARTS < plan.grid ? 1 : G;
+    return launch_k(k_paged_join<E>, dim3(records, G / heads), dim3(PJ_THREADS), 0, s, a, plan.grid, heads);
 }
 
 template <class E, int DP>
