@@ -710,8 +710,14 @@ PdPlan pd_plan(const PagedView& c, int B, int NH, int window, int sinks, int sms
     const long long blocks = (seen + KEYS - 1) / KEYS, pairs = (long long)B * c.NKV;
     int C = 1;
     while (C < PD_MAX_CLUSTER && C * PD_WARPS < blocks) C *= 2;
-    if (pairs * C <= pd_grid_full(sms, G) && blocks <= C * PD_WARPS * PD_CLUSTER_BLOCKS) return {C, 0};
-    return {0, (int)min((long long)pd_grid_full(sms, G), (blocks * pairs + PD_MIN_BLOCKS - 1) / PD_MIN_BLOCKS)};
+    // A cluster has no second kernel, but only its own CTAs: 14 heads on 2 of 64,
+    // cluster and line, 4.5 and 8.6 us for 500 keys, 7.4 and 10.5 for 4000, 11.4 and
+    // 10.8 for 8000, 19.2 and 11.6 for 16000.  With clusters on most of the chip the
+    // line's even shares win earlier: 28 sequences of 2000 keys 12.1 and 13.8 us, of
+    // 4000 keys 20.5 and 19.8, of 8000 keys 32.5 and 28.6.
+    const int full = pd_grid_full(sms, G), per_warp = pairs * C * 2 <= full ? PD_CLUSTER_BLOCKS : PD_CLUSTER_BLOCKS / 2;
+    if (pairs * C <= full && blocks <= C * PD_WARPS * per_warp) return {C, 0};
+    return {0, (int)min((long long)full, (blocks * pairs + PD_MIN_BLOCKS - 1) / PD_MIN_BLOCKS)};
 }
 
 template <class E, int DP, int HT>
