@@ -1,7 +1,10 @@
-"""Build the CUDA library in-tree: csrc/*.cu -> _build/libember.so (sm_103a).
+"""Build the CUDA library in-tree: csrc/*.cu -> _build/libember.so (sm_103a), and
+the torch side of the paged-cache operators: csrc/paged_torch.cpp ->
+_build/paged_torch<suffix> (a Python extension against the installed torch).
 
-Each translation unit compiles in parallel with nvcc, then one nvcc -shared
-link.  Used by __graft_entry__.build() and by the Python binding on first use.
+Each translation unit compiles in parallel with nvcc (g++ for the extension),
+then one nvcc -shared link.  Used by __graft_entry__.build() and by the Python
+binding on first use.
 """
 from __future__ import annotations
 
@@ -10,11 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libember.so")
+TORCH_SRC = os.path.join(CSRC, "paged_torch.cpp")
+TORCH_EXT = os.path.join(OUT, "paged_torch" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 
@@ -46,8 +52,35 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def ext_up_to_date() -> bool:
+    deps = (TORCH_SRC, os.path.join(INCLUDE, "ember.h"))
+    return os.path.exists(TORCH_EXT) and all(os.path.getmtime(p) <= os.path.getmtime(TORCH_EXT) for p in deps)
+
+
+def build_ext(force: bool = False) -> str:
+    """Compile the torch extension (marshalling only; every kernel is in libember.so)."""
+    if not force and ext_up_to_date():
+        return TORCH_EXT
+    import torch
+    from torch.utils import cpp_extension as cpp
+    os.makedirs(OUT, exist_ok=True)
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [*cpp.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    tmp = TORCH_EXT + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + i for i in inc), TORCH_SRC,
+           "-o", tmp, "-L" + torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("torch extension failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+    os.replace(tmp, TORCH_EXT)
+    return TORCH_EXT
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and up_to_date():
+        build_ext()
         return LIB
     os.makedirs(OUT, exist_ok=True)
     nvcc = _nvcc()
@@ -64,7 +97,9 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        ext = ex.submit(build_ext, force)
         objs = list(ex.map(compile_one, sources()))
+        ext.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

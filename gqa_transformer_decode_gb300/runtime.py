@@ -7,8 +7,8 @@ runs in libember.so.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
+import importlib.util
 
 import numpy as np
 import torch
@@ -183,47 +183,16 @@ class PagedKV:
         c.n_pages, c.page_size, c.n_kv_heads, c.head_dim = n_pages, page_size, self.n_kv_heads, self.head_dim
         c.n_seqs, c.table_width = table.shape
         c.page_stride, c.head_stride, c.row_stride = strides[0]
-        self._c = c
-        self._kv = C.addressof(c)
-        self._lib = E.load()
-        self._index = self.k_pages.get_device()
         with torch.cuda.device(self.device):
             self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
             torch.cuda.current_stream().synchronize()   # zero before any stream uses it
-        self._status = self.status.data_ptr()
-        self._ws_bytes = {}
+        self._t = _paged_torch()
+        self._cache = self._t.cache(C.addressof(c), self.status.data_ptr(), k_pages.get_device())
 
-    # -- checks (written for few calls into torch: they are most of a small call's cost) --
-    def _ints(self, t, n, what):
-        if t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != self._index or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous int32 [{n}] on {self.device}")
-        return t.data_ptr()
-
-    def _rows(self, t, what, n, heads, dtype):
-        """[n, heads, head_dim] with a row's heads side by side -> (pointer, row stride)."""
-        D = self.head_dim
-        if t.shape != (n, heads, D) or t.dtype is not dtype or t.get_device() != self._index:
-            raise ValueError(f"{what} must be {dtype} [{n}, {heads}, {D}] on {self.device}, "
-                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
-        row, head, one = t.stride()
-        if one != 1 or (head != D and heads > 1):
-            raise ValueError(f"{what}: a row's heads must lie side by side")
-        return t.data_ptr(), (row if n > 1 else heads * D)
-
-    def _table(self, t, what, shape, dtype):
-        if t.shape != shape or t.dtype is not dtype or t.get_device() != self._index or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous {dtype} {list(shape)} on {self.device}")
-        return t.data_ptr()
-
-    def _run(self, stream):
-        """-> (raw stream, context that makes the device and the stream current)."""
-        if stream is None:
-            if torch.cuda.current_device() == self._index:
-                return _raw_stream(self._index), _NOTHING
-            stream = torch.cuda.current_stream(self.device)
+    def _on(self, stream):
         if stream.device != self.device:
             raise ValueError(f"the stream belongs to {stream.device}, the cache to {self.device}")
-        return stream.cuda_stream, torch.cuda.stream(stream)
+        return torch.cuda.stream(stream)
 
     # -- operators ------------------------------------------------------------
     def append(self, k, v, seqs, positions, cos, sin, q=None, q_norm=None, k_norm=None, eps=1e-6, q_out=None,
@@ -234,38 +203,10 @@ class PagedKV:
         one type, f32, bf16 or f16; seqs, positions int32 [n]; cos, sin f32
         [n_pos, head_dim / 2]; q_norm, k_norm bf16 [head_dim].  Returns the
         rotated queries in the cache's type (q_out where given), or None."""
-        dt, n, heads, D = k.dtype, k.shape[0], 0, self.head_dim
-        src = _SRC_DTYPES.get(dt)
-        if src is None:
-            raise TypeError("q, k and v must be float32, bfloat16 or float16")
-        kp, ldk = self._rows(k, "k", n, self.n_kv_heads, dt)
-        vp, ldv = self._rows(v, "v", n, self.n_kv_heads, dt)
-        sp, pp = self._ints(seqs, n, "seqs"), self._ints(positions, n, "positions")
-        half = (cos.shape[0], D // 2)
-        cp, np_ = self._table(cos, "cos", half, torch.float32), self._table(sin, "sin", half, torch.float32)
-        qn = None if q_norm is None else self._table(q_norm, "q_norm", (D,), torch.bfloat16)
-        kn = None if k_norm is None else self._table(k_norm, "k_norm", (D,), torch.bfloat16)
-        qp = op = None
-        ldq = ldo = 0
-        if q is not None:
-            heads = q.shape[1]
-            qp, ldq = self._rows(q, "q", n, heads, dt)
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        raw, ctx = self._run(stream)
-        with ctx:
-            if q is not None:
-                if q_out is None:
-                    q_out = torch.empty((n, heads, D), dtype=self.dtype, device=self.device)
-                    op, ldo = q_out.data_ptr(), heads * D
-                else:
-                    op, ldo = self._rows(q_out, "q_out", n, heads, self.dtype)
-            if n:
-                st = self._lib.ember_paged_append(self._kv, qp, kp, vp, src, ldq, ldk, ldv, n, heads, sp, pp,
-                                                  qn, kn, eps, cp, np_, half[0], op, ldo, self._status, raw)
-                if st:
-                    E.check(st, "ember_paged_append")
-        return q_out
+        if stream is not None:
+            with self._on(stream):
+                return self.append(k, v, seqs, positions, cos, sin, q, q_norm, k_norm, eps, q_out)
+        return self._t.append(self._cache, k, v, seqs, positions, cos, sin, q, q_norm, k_norm, eps, q_out)
 
     def decode(self, q, lens, seqs=None, window=0, sinks=0, scale=None, out=None, lse=None, return_lse=False,
                workspace=None, stream=None):
@@ -274,77 +215,24 @@ class PagedKV:
         int32 [B] (default: sequence b).  scale defaults to head_dim ** -0.5.
         Returns out, or (out, lse) with return_lse or lse.  workspace: a uint8
         tensor of at least workspace_bytes(B, n_heads) (default: allocated)."""
-        B, heads, D = q.shape
-        qp, ldq = self._rows(q, "q", B, heads, self.dtype)
-        lp = self._ints(lens, B, "lens")
-        sp = None if seqs is None else self._ints(seqs, B, "seqs")
-        raw, ctx = self._run(stream)
-        with ctx:
-            out, lse, op, ldo, ep = self._outputs(B, heads, out, lse, return_lse)
-            if B:
-                need = self._ws_bytes.get((B, heads))
-                if need is None:
-                    need = self.workspace_bytes(B, heads)
-                wp = None
-                if workspace is not None:
-                    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
-                            workspace.get_device() != self._index:
-                        raise ValueError(f"workspace must be contiguous uint8 on {self.device}")
-                    wp, need = workspace.data_ptr(), workspace.numel()
-                elif need:
-                    workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-                    wp = workspace.data_ptr()
-                st = self._lib.ember_paged_decode(self._kv, qp, ldq, B, heads, sp, lp, window, sinks,
-                                                  D ** -0.5 if scale is None else scale, op, ldo, ep, wp, need,
-                                                  self._status, raw)
-                if st:
-                    E.check(st, "ember_paged_decode")
-        return out if lse is None else (out, lse)
+        if stream is not None:
+            with self._on(stream):
+                return self.decode(q, lens, seqs, window, sinks, scale, out, lse, return_lse, workspace)
+        return self._t.decode(self._cache, q, lens, seqs, window, sinks, scale, out, lse, return_lse, workspace)
 
     def prefill(self, q, cu, lens, seqs=None, window=0, sinks=0, scale=None, out=None, lse=None, return_lse=False,
                 stream=None):
         """Attention of several tokens per sequence: rows cu[b] .. cu[b + 1] - 1
         of q [n, n_heads, head_dim] are the last positions of sequence b (or
         seqs[b]), which holds lens[b] keys.  cu int32 [B + 1], lens int32 [B]."""
-        n, heads, D = q.shape
-        B = lens.shape[0]
-        qp, ldq = self._rows(q, "q", n, heads, self.dtype)
-        lp, cp = self._ints(lens, B, "lens"), self._ints(cu, B + 1, "cu")
-        sp = None if seqs is None else self._ints(seqs, B, "seqs")
-        raw, ctx = self._run(stream)
-        with ctx:
-            out, lse, op, ldo, ep = self._outputs(n, heads, out, lse, return_lse)
-            if n and B:
-                st = self._lib.ember_paged_prefill(self._kv, qp, ldq, n, B, heads, sp, cp, lp, window, sinks,
-                                                   D ** -0.5 if scale is None else scale, op, ldo, ep,
-                                                   self._status, raw)
-                if st:
-                    E.check(st, "ember_paged_prefill")
-        return out if lse is None else (out, lse)
-
-    def _outputs(self, n, heads, out, lse, return_lse):
-        if out is None:
-            out = torch.empty((n, heads, self.head_dim), dtype=self.dtype, device=self.device)
-            op, ldo = out.data_ptr(), heads * self.head_dim
-        else:
-            op, ldo = self._rows(out, "out", n, heads, self.dtype)
-        if lse is not None:
-            ep = self._table(lse, "lse", (n, heads), torch.float32)
-        elif return_lse:
-            lse = torch.empty((n, heads), dtype=torch.float32, device=self.device)
-            ep = lse.data_ptr()
-        else:
-            ep = None
-        return out, lse, op, ldo, ep
+        if stream is not None:
+            with self._on(stream):
+                return self.prefill(q, cu, lens, seqs, window, sinks, scale, out, lse, return_lse)
+        return self._t.prefill(self._cache, q, cu, lens, seqs, window, sinks, scale, out, lse, return_lse)
 
     def workspace_bytes(self, B: int, n_heads: int) -> int:
         """Bytes of decode's workspace for B sequences of n_heads query heads (0: none is needed)."""
-        n = self._ws_bytes.get((B, n_heads))
-        if n is None:
-            with torch.cuda.device(self.device):
-                n = E.ember_paged_decode_workspace(self._kv, B, n_heads)
-            self._ws_bytes[(B, n_heads)] = n
-        return n
+        return self._t.workspace_bytes(self._cache, B, n_heads)
 
     def sync_status(self, stream=None) -> int:
         """Wait for the stream, return and clear the first device-side error (0: none)."""
@@ -357,11 +245,23 @@ class PagedKV:
 
 
 _PAGE_DTYPES = {torch.bfloat16: E.BF16, torch.float16: E.F16}
-_SRC_DTYPES = {torch.float32: E.F32, torch.bfloat16: E.BF16, torch.float16: E.F16}
-_NOTHING = contextlib.nullcontext()
-# the current stream's handle of a device, without the Stream object where torch has the shorter way
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_torch_side = None
+
+
+def _paged_torch():
+    """The compiled marshalling (csrc/paged_torch.cpp), on the loaded library's entry points."""
+    global _torch_side
+    if _torch_side is None:
+        lib = E.load()
+        path = E._build.build_ext()
+        spec = importlib.util.spec_from_file_location("paged_torch", path)
+        t = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(t)
+        t.entries(*(C.cast(getattr(lib, n), C.c_void_p).value for n in
+                    ("ember_paged_append", "ember_paged_decode", "ember_paged_decode_workspace",
+                     "ember_paged_prefill", "ember_last_error")), E.EmberError)
+        _torch_side = t
+    return _torch_side
 
 
 def _wrap_device(ptr: int, nbytes: int, device) -> torch.Tensor:

@@ -113,3 +113,31 @@ def test_calls_without_rows_do_nothing():
 def test_the_workspace_query_answers_zero_for_bad_arguments():
     f = E.ember_paged_decode_workspace
     assert f(None, 1, 4) == 0 and f(C.byref(cache()), 0, 4) == 0 and f(C.byref(cache()), 2, 3) == 0
+
+
+def torch_side():
+    """The compiled marshalling over a cache that is never reached."""
+    from gqa_transformer_decode_gb300 import runtime
+    t = runtime._paged_torch()
+    return t, t.cache(C.addressof(cache()), A, 0)
+
+
+def test_the_torch_side_refuses_before_any_device_work():
+    import torch
+    t, c = torch_side()
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    lens = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(TypeError, match="arguments"):
+        t.decode(c, q)
+    with pytest.raises(TypeError, match="q must be a tensor"):
+        t.decode(c, 3, lens, None, 0, 0, None, None, None, False, None)
+    with pytest.raises(ValueError, match="q must be on cuda:0, not cpu"):
+        t.decode(c, q, lens, None, 0, 0, None, None, None, False, None)
+    with pytest.raises(TypeError, match="float32, bfloat16 or float16"):
+        t.append(c, lens, lens, lens, lens, q, q, None, None, None, 1e-6, None)
+    with pytest.raises(ValueError, match="k must be on cuda"):
+        t.append(c, q, q, lens, lens, q, q, None, None, None, 1e-6, None)
+    with pytest.raises(TypeError, match="lens must be a tensor"):
+        t.prefill(c, q, lens, None, None, 0, 0, None, None, None, False)
+    with pytest.raises(ValueError):
+        t.decode("no cache", q, lens, None, 0, 0, None, None, None, False, None)
