@@ -34,6 +34,12 @@
 // sequence's end, NaN among it, has no effect, and table entries of pages
 // without a visible key are not looked at.
 //
+// Measured: 64 sequences of 64 to 4096 keys, 32 heads on 8 of 64 (269 MB of K and V
+// rows), 55 us, 4.9 TB/s; one of 131071 keys, 32 on 8 of 128, f16 (537 MB), 89 us, 6.0
+// TB/s (a copy moves 6.7).  Of the 55 us the first data arrive 5 us after the start
+// (lengths, page numbers and rows are three loads that depend on one another), the
+// CTAs end between 34 and 48 us, and the join with its launch takes 5.
+//
 // P is the second product's operand.  For f16 it is rounded to f16 (2^-12
 // relative).  bf16 would cost 2^-9, as much as the output's own rounding, so
 // there P goes in as the sum of two bf16 values: the products are far from

@@ -40,6 +40,15 @@
 // share a pair's key tiles, leave (m, l, O) of its rows in their shared memory and
 // join a share of the rows each through distributed shared memory.
 //
+// Measured: a 2048-token prompt, 32 heads on 8 of 64, 29 us (590 TFLOP/s of the
+// products it cannot do without); five chunks of up to 1000 tokens on up to 5000
+// keys, 16 on 8 of 128, f16, 94 us (850); 8192 tokens under a window of 1024, 78 us
+// (830).  For 64 keys and both query tiles the products take 1250 cycles at
+// head_dim 128 and 770 at 64, the exponentials 560 and the row threads' other
+// instructions about as much again; a step takes 1780 and 1310, since each waits
+// for the others at times.  The tensor pipe is active for 48 % of the cycles in the
+// chunks, whose longest tile pairs (94 steps) set the time, and 27 % in the prompt.
+//
 // Warps 0-3: tile A; warps 4-7: tile B (a warp reads the TMEM lanes of its index
 // mod 4); warp 8: TMA producer; warp 9: TMEM allocation; warps
 // 9 and 10: MMA issue for tile A and for tile B, so that neither's waiting holds
