@@ -9,8 +9,8 @@
 // TMA brings serves all heads of the group.  Per key tile of 64 keys and query
 // tile: S = Q K^T into TMEM, one thread per row takes p = 2^(s - m) and writes P
 // (bf16 / f16) back to TMEM, O += P V accumulates there.  The reference maximum m
-// moves (and O, l are rescaled) only when a tile's maximum passes it by more than
-// 2^8.  S has two buffers for each query tile, so the products of the next key
+// moves (and O, l are rescaled, the tile done again) only when a row's weights of a
+// tile sum to more than 2^15, so that most tiles need no maximum at all.  S has two buffers for each query tile, so the products of the next key
 // tile are ready before a row's thread asks for them, and the two query tiles'
 // threads and the tensor cores wait for one another only when one of them has
 // fallen a whole tile behind.  (With one buffer of 128 keys, P over it, a step
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     }
     } else {   // -------------------------------------------------- softmax warps
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PT_REGS_ROW));
-        constexpr float RESCALE = 8.f;
+        constexpr float MOST = 32768.f;               // f16 weights stay finite
         const int t = warp >> 2;                      // query tile: 0 = A, 1 = B
         const int qw = warp & 3;                      // TMEM lane quarter of this warp
         const int r = qw * 32 + lane;                 // row within the tile
@@ -534,53 +534,69 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 break;
             }
             tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < PT_KEYS; c += 32) tmem_ld32(tS + c, v + c);
-            tmem_ld_wait();
             // column c is visible when c < hi and (c >= lo or c < sk)
             const int key0 = p.key0(j);
             const int hi = qp - key0 + 1;
             const int lo = a.window > 0 ? qp - a.window + 1 - key0 : 0;
             const int sk = a.sinks - key0;
-            if (!__all_sync(FULL_MASK, hi >= PT_KEYS && (lo <= 0 || sk >= PT_KEYS))) {
+            const bool whole = __all_sync(FULL_MASK, hi >= PT_KEYS && (lo <= 0 || sk >= PT_KEYS));
+            auto scores = [&]() {                     // the row's products, -inf where hidden
 #pragma unroll
-                for (int k = 0; k < PT_KEYS / 32; ++k) {   // a bit a column: no branches
-                    const uint32_t see = below(hi - 32 * k) & (~below(lo - 32 * k) | below(sk - 32 * k));
+                for (int c = 0; c < PT_KEYS; c += 32) tmem_ld32(tS + c, v + c);
+                tmem_ld_wait();
+                if (!whole) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[32 * k + i] = (see >> i) & 1u ? v[32 * k + i] : 0xff800000u;   // -inf
+                    for (int k = 0; k < PT_KEYS / 32; ++k) {   // a bit a column: no branches
+                        const uint32_t see = below(hi - 32 * k) & (~below(lo - 32 * k) | below(sk - 32 * k));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[32 * k + i] = (see >> i) & 1u ? v[32 * k + i] : 0xff800000u;
+                    }
                 }
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            };
+            auto largest = [&]() {                    // of the row's scores
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < PT_KEYS; c += 8)
+                for (int c = 0; c < PT_KEYS; c += 8)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mx[i] = max3(mx[i], __uint_as_float(v[c + 2 * i]), __uint_as_float(v[c + 2 * i + 1]));
-            const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
-            // the reference moves (and O, l are rescaled) only when the tile's
-            // maximum passes it by more than RESCALE (log2 units): weights stay
-            // below 2^RESCALE
-            const bool move = mt > m + RESCALE;
+                    for (int i = 0; i < 4; ++i)
+                        mx[i] = max3(mx[i], __uint_as_float(v[c + 2 * i]), __uint_as_float(v[c + 2 * i + 1]));
+                return max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
+            };
+            auto weigh = [&]() {                      // scores -> weights, packed; their sum
+                const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
+                float2 rs[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) rs[i] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < PT_KEYS; c += 2) {
+                    float2 w = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, m2);
+                    w.x = ex2(w.x);
+                    w.y = ex2(w.y);
+                    rs[(c >> 1) & 3] = add2(rs[(c >> 1) & 3], w);
+                    v[c >> 1] = E::pack(w.x, w.y);
+                }
+                const float2 r2 = add2(add2(rs[0], rs[1]), add2(rs[2], rs[3]));
+                return r2.x + r2.y;
+            };
+            // The reference maximum is looked for only while a row has none, and when the
+            // tile's weights against the old one sum to more than MOST: until then every
+            // weight is exact to the same relative rounding, and within f16's range.
+            // (Rows that are not live hold anything and ask for nothing.)
+            scores();
+            const bool look = live && m == SOFTMAX_FLOOR;
+            if (__any_sync(FULL_MASK, look)) m = look ? fmaxf(m, largest()) : m;
+            float sum = weigh();
+            const bool move = live && !(sum <= MOST);
             const bool any_move = __any_sync(FULL_MASK, move);
             float corr = 1.f;
             if (any_move) {
-                const float mnew = move ? mt : m;
+                scores();                             // (S is whole until P is stored)
+                const float mnew = move ? fmaxf(m, largest()) : m;
                 corr = ex2(m - mnew);
                 l *= corr;
                 m = mnew;
-            }
-            const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
-            float2 rs[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rs[i] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < PT_KEYS; c += 2) {
-                float2 w = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, m2);
-                w.x = ex2(w.x);
-                w.y = ex2(w.y);
-                rs[(c >> 1) & 3] = add2(rs[(c >> 1) & 3], w);
-                v[c >> 1] = E::pack(w.x, w.y);
+                sum = weigh();
             }
             if (any_move && j > 0) {   // O is touched: P . V(j - 1) must be complete
                 if (!wait_all(&o_full[2 * t + ((n - 1) & 1)], (n - 1) >> 1)) {
@@ -606,8 +622,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[2 * t + (n & 1)]);
-            const float2 r2 = add2(add2(rs[0], rs[1]), add2(rs[2], rs[3]));
-            l += r2.x + r2.y;
+            l += sum;
         }
         if (SPLIT) {   // the rows as they are into shared memory; joined below
             if (ok && nkt > 0) {
