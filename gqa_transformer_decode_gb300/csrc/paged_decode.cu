@@ -40,10 +40,9 @@
 // (lengths, page numbers and rows are three loads that depend on one another), the
 // CTAs end between 34 and 48 us, and the join with its launch takes 5.
 //
-// P is the second product's operand.  For f16 it is rounded to f16 (2^-12
-// relative).  bf16 would cost 2^-9, as much as the output's own rounding, so
-// there P goes in as the sum of two bf16 values: the products are far from
-// bounding this kernel.
+// P, the second product's operand, goes in as the sum of two values of the cache's
+// type (bf16 2^-16 relative, f16 2^-22): one would add as much error as the output's
+// own rounding, and the products are far from bounding this kernel.
 #include "paged.cuh"
 
 namespace ember {
@@ -434,8 +433,8 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t x = E::pack(p[2 * e], p[2 * e + 1]);
                         pb[t][e] = transpose8x8(x);
-                        if (E::bf16)             // what the rounding left
-                            pr[t][e] = transpose8x8(E::pack(p[2 * e] - E::lo(x), p[2 * e + 1] - E::hi(x)));
+                        // what the rounding left
+                        pr[t][e] = transpose8x8(E::pack(p[2 * e] - E::lo(x), p[2 * e + 1] - E::hi(x)));
                     }
                 }
 #pragma unroll
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
 #pragma unroll
                     for (int t = 0; t < HT; ++t) {
                         E::mma(o[t][i], va, pb[t][0], pb[t][1]);
-                        if (E::bf16) E::mma(o[t][i], va, pr[t][0], pr[t][1]);
+                        E::mma(o[t][i], va, pr[t][0], pr[t][1]);
                     }
                 }
             }

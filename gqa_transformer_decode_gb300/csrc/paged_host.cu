@@ -219,7 +219,7 @@ ember_status ember_paged_prefill(const ember_paged_kv* kv, const void* q, int64_
     if (st != EMBER_OK) return st;
     if (n == 0 || B == 0) return EMBER_OK;
     if (!cu) PG_FAIL(EMBER_ERR_INVALID_ARG, "cu is NULL");
-    if (B > (1 << 20) || kv->n_kv_heads > 65535) PG_FAIL(EMBER_ERR_UNSUPPORTED, "B > 2^20 or n_kv_heads > 65535");
+    if (B > 65535 || kv->n_kv_heads > 65535) PG_FAIL(EMBER_ERR_UNSUPPORTED, "B > 65535 or n_kv_heads > 65535");
     if (!seqs && B > kv->n_seqs) PG_FAIL(EMBER_ERR_INVALID_ARG, "B > n_seqs without seqs");
     a.q = static_cast<const uint16_t*>(q);
     a.ld_q = ld_q;

@@ -443,58 +443,67 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         };
         unsigned cta = first_pair;
         int base = 0, pairs = 0;   // key tiles and pairs with keys so far
+        int mine = 0, with = 0;    // those in which this query tile has tokens
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const PtPair p = pt_pair(a, QT, cta, pairs_all, part, parts, false);
             const int nkt = max(0, p.nkt);
             auto slot_full = [&](int i) { return &kv_full[i % NS]; };
-            // S of the pair's key tile j; then K (after the last one Q) is free
-            auto first_s = [&](int j) {
-                const int n = base + j;
-                if (!(ok = wait_all(slot_full(2 * n), 2 * n / NS))) return;
-                const uint32_t buf = uniform(n & 1), dk = slot_k(n);
-                issue([&] {
-                    mma_s(buf, dk);
-                    umma_commit(&kv_empty[2 * n % NS]);
-                    if (j + 1 == nkt) umma_commit(q_empty);
-                });
-            };
-            if (nkt > 0) {
-                if (!(ok = wait_all(q_full, pairs))) break;
-                first_s(0);
-            }
-            if (ok && nkt > 1) first_s(1);
-            if (!ok) break;
-            for (int j = 0; j < nkt; ++j) {
-                // P . V(j) frees the buffer that S(j + 2) takes (MMAs of one thread run
-                // in the order of issue), and S(j + 1) is there already
-                const int n = base + j;
-                const bool more = j + 2 < nkt;
-                const uint32_t buf = uniform(n & 1), dv = slot_v(n), dk = slot_k(n + 2);
-                // P(j), V(j), K(j + 2) and, before a pair's first P . V, the end of the
-                // pair before's use of O: a lane each, so that one poll sees them all
-                uint64_t* b = &p_full[2 * t + (n & 1)];
-                int parity = n >> 1;
-                if ((lane & 3) == 1) {
-                    b = slot_full(2 * n + 1);
-                    parity = (2 * n + 1) / NS;
-                } else if ((lane & 3) == 2 && more) {
-                    b = slot_full(2 * n + 4);
-                    parity = (2 * n + 4) / NS;
-                } else if ((lane & 3) == 3 && j == 0 && pairs > 0) {
-                    b = &o_free[t];
-                    parity = pairs - 1;
+            if (nkt > 0 && !(ok = wait_all(q_full, pairs))) break;
+            if (t * QT >= p.tokens) {
+                // no tokens: the other tile alone, this warp only hands its half of the slots back
+                for (int i = 2 * base; ok && i < 2 * (base + nkt); ++i) {
+                    ok = wait_all(slot_full(i), i / NS);
+                    if (ok && lane == 0) mbar_arrive(&kv_empty[i % NS]);
                 }
-                if (!(ok = wait_all(b, parity))) break;
-                issue([&] {
-                    mma_pv(buf, dv, j > 0);
-                    umma_commit(&kv_empty[(2 * n + 1) % NS]);
-                    if (more) {
+                if (ok && nkt > 0 && lane == 0) mbar_arrive(q_empty);
+            } else {
+                // S of the pair's key tile j; then K (after the last one Q) is free
+                auto first_s = [&](int j) {
+                    const int n = base + j;
+                    if (!(ok = wait_all(slot_full(2 * n), 2 * n / NS))) return;
+                    const uint32_t buf = uniform((mine + j) & 1), dk = slot_k(n);
+                    issue([&] {
                         mma_s(buf, dk);
-                        umma_commit(&kv_empty[(2 * n + 4) % NS]);
-                        if (j + 3 == nkt) umma_commit(q_empty);
+                        umma_commit(&kv_empty[2 * n % NS]);
+                        if (j + 1 == nkt) umma_commit(q_empty);
+                    });
+                };
+                if (nkt > 0) first_s(0);
+                if (ok && nkt > 1) first_s(1);
+                for (int j = 0; ok && j < nkt; ++j) {
+                    // P . V(j) frees the buffer that S(j + 2) takes (MMAs of one thread run
+                    // in the order of issue), and S(j + 1) is there already
+                    const int n = base + j, m = mine + j;
+                    const bool more = j + 2 < nkt;
+                    const uint32_t buf = uniform(m & 1), dv = slot_v(n), dk = slot_k(n + 2);
+                    // P(j), V(j), K(j + 2) and, before a pair's first P . V, the end of the
+                    // pair before's use of O: a lane each, so that one poll sees them all
+                    uint64_t* b = &p_full[2 * t + (m & 1)];
+                    int parity = m >> 1;
+                    if ((lane & 3) == 1) {
+                        b = slot_full(2 * n + 1);
+                        parity = (2 * n + 1) / NS;
+                    } else if ((lane & 3) == 2 && more) {
+                        b = slot_full(2 * n + 4);
+                        parity = (2 * n + 4) / NS;
+                    } else if ((lane & 3) == 3 && j == 0 && with > 0) {
+                        b = &o_free[t];
+                        parity = with - 1;
                     }
-                });
+                    if (!(ok = wait_all(b, parity))) break;
+                    issue([&] {
+                        mma_pv(buf, dv, j > 0);
+                        umma_commit(&kv_empty[(2 * n + 1) % NS]);
+                        if (more) {
+                            mma_s(buf, dk);
+                            umma_commit(&kv_empty[(2 * n + 4) % NS]);
+                            if (j + 3 == nkt) umma_commit(q_empty);
+                        }
+                    });
+                }
+                mine += nkt;
+                with += nkt > 0;
             }
             if (!ok) break;
             base += nkt;
@@ -519,7 +528,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         PtPair pair;                                  // (SPLIT: the one pair)
         for (int it = 0; ok; ++it) {
         const PtPair p = pt_pair(a, QT, cta, pairs_all, part, parts, false);
-        const int nkt = max(0, p.nkt);
+        const int nkt = t * QT < p.tokens ? max(0, p.nkt) : 0;   // (without tokens the tile has no products either)
         const bool live = p.nkt >= 0 && r < QT * G && tok < p.tokens;
         const int qp = p.pos0 + min(tok, p.tokens - 1);   // its position (rows that are not live: the last one's)
         float m = SOFTMAX_FLOOR, l = 0.f;             // reference maximum (of s * sc), sum of 2^(s sc - m)
@@ -785,11 +794,13 @@ cudaError_t launch_dp(const PagedPrefillMaps& m, PagedPrefillArgs a, int sms, cu
     constexpr int SMEM = PtSmem<DP>::TOTAL;
     const int per = 2 * (PT_ROWS / (a.NH / a.c.NKV));
     const unsigned pairs = (unsigned)((((long long)a.n + per - 1) / per + a.B) * a.c.NKV);
-    // CTAs of a cluster that share a pair's keys: as many as leave every one an SM and two key tiles
+    // CTAs of a cluster that share a pair's keys: as many as leave every one an SM and
+    // two key tiles.  (`pairs` is the most there can be; about B / 2 of them are not.)
+    const long long about = max((long long)a.B, a.n / per + a.B / 2ll) * a.c.NKV;
     const long long keys = (long long)a.c.width << a.c.page_shift;
     const long long seen = a.window > 0 ? min(keys, (long long)a.window + a.sinks + per) : keys;
     a.parts = 1;
-    while (a.parts < PT_PARTS && pairs * a.parts * 2 <= (unsigned)sms && seen >= 4ll * a.parts * PT_KEYS) a.parts *= 2;
+    while (a.parts < PT_PARTS && about * a.parts * 2 <= sms && seen >= 4ll * a.parts * PT_KEYS) a.parts *= 2;
     const auto& mq = *reinterpret_cast<const CUtensorMap*>(m.q);
     const auto& mk = *reinterpret_cast<const CUtensorMap*>(m.k);
     const auto& mv = *reinterpret_cast<const CUtensorMap*>(m.v);

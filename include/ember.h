@@ -320,6 +320,10 @@ ember_status ember_sample(const float *logits, int32_t B, int32_t V, int32_t ldl
  *     the keys read as zeros.  Nothing outside the buffers is touched.
  *   - Table entries of pages that hold no visible key are not read, nor are
  *     rows of a page that no query of the call sees: they may hold anything.
+ *   - Products are taken on the cache's type and summed in f32, softmax weights
+ *     against a maximum that may lag behind the true one by up to 2^15: keys and
+ *     values stay below about 1e33 in magnitude (bf16; f16 always does).
+ *   - B is at most 65535.  No operator has a gradient.
  *   - Buffers and the stream belong to the current device; buffers may not
  *     overlap, except that pages may be shared by the tables of sequences
  *     that only read them. */

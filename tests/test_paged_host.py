@@ -101,6 +101,7 @@ def test_batches_beyond_the_table_are_refused():
     assert decode(B=5) == INVALID and "n_seqs" in E.last_error()
     assert prefill(B=5) == INVALID and "n_seqs" in E.last_error()
     assert decode(B=-1) == INVALID and decode(B=70000, seqs=A) == UNSUPPORTED
+    assert prefill(n=70000, B=70000, seqs=A) == UNSUPPORTED
     assert prefill(n=-1) == INVALID and prefill(B=-1) == INVALID and prefill(cu=None) == INVALID
 
 
