@@ -488,7 +488,9 @@ struct PagedDecodeArgs {
     float* lse;                  // [B][NH] or nullptr
     float* ws;                   // records and partials, paged_decode_ws bytes
     int* status;
-    int by_pair;                 // set by launch_paged_decode: records stand by (sequence, kv head)
+    // set by launch_paged_decode:
+    int split;                   // CTAs that share a long sequence in cluster form
+    int by_pair;                 // records stand by (sequence, kv head)
 };
 // bytes of ws that the call's split needs (a window only ever lowers them)
 size_t paged_decode_ws(const PagedView& c, int B, int NH, int window, int sinks, int sms);

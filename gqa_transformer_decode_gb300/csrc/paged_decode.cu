@@ -23,9 +23,9 @@
 //            boundaries.  A (sequence, kv head) whose blocks lie in one CTA is
 //            finished there; otherwise its CTAs leave (m, l, O) partials that a
 //            second small kernel joins in CTA order.
-//   cluster  for few, short sequences: the CTAs of one thread-block cluster share
-//            one (sequence, kv head) and join through distributed shared memory,
-//            with no scan of the lengths, no workspace and no second kernel.
+//   cluster  for short sequences (few ones: longer): the CTAs of one thread-block
+//            cluster share one (sequence, kv head) and join through distributed shared
+//            memory, with no scan of the lengths, no workspace and no second kernel.
 // Either way the result depends on the inputs, the form and the device only.
 //
 // Blocks start at multiples of 16 keys and pages hold a multiple of 16 rows,
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
         }
         // a block for each warp at least; CTAs left over join in with nothing, so that a
         // smaller cluster (a table with room for fewer blocks) gives the same bits
-        const unsigned each = max(PD_WARPS, (cur.s.n + PD_MAX_CLUSTER - 1) / PD_MAX_CLUSTER);
+        const unsigned each = max(PD_WARPS, (cur.s.n + a.split - 1) / a.split);
         lo = min((unsigned)cur.s.n, blockIdx.x * each);
         hi = min((unsigned)cur.s.n, lo + each);
         cur.i = (int)lo;
@@ -704,8 +704,8 @@ int pd_grid_full(int sms, int G) { return min(PD_MAX_CTAS, sms * pd_ctas_per_sm(
 
 // How a call is split: by the most blocks that its table and window allow.
 struct PdPlan {
-    int cluster;   // CTAs of a cluster, 0 for the line
-    int grid;      // the line's CTAs
+    int cluster, split;   // CTAs of a cluster (0: the line), and that share a long sequence
+    int grid;             // the line's CTAs
 };
 PdPlan pd_plan(const PagedView& c, int B, int NH, int window, int sinks, int sms) {
     const int G = NH / c.NKV, KEYS = c.D <= 64 ? PD_KEYS<64> : PD_KEYS<128>;
@@ -713,22 +713,31 @@ PdPlan pd_plan(const PagedView& c, int B, int NH, int window, int sinks, int sms
     // (a window's blocks: its own, one more at each end that it cuts, one that the sinks cut)
     const long long seen = window > 0 ? min(keys, (long long)window + sinks + 3 * KEYS) : keys;
     const long long blocks = (seen + KEYS - 1) / KEYS, pairs = (long long)B * c.NKV;
-    int C = 1;
-    while (C < PD_MAX_CLUSTER && C * PD_WARPS < blocks) C *= 2;
     // A cluster has no second kernel, but only its own CTAs: 14 heads on 2 of 64,
     // cluster and line, 4.5 and 8.6 us for 500 keys, 7.4 and 10.5 for 4000, 11.4 and
     // 10.8 for 8000, 19.2 and 11.6 for 16000.  With clusters on most of the chip the
     // line's even shares win earlier: 28 sequences of 2000 keys 12.1 and 13.8 us, of
-    // 4000 keys 20.5 and 19.8, of 8000 keys 32.5 and 28.6.
-    const int full = pd_grid_full(sms, G), per_warp = pairs * C * 2 <= full ? PD_CLUSTER_BLOCKS : PD_CLUSTER_BLOCKS / 2;
-    if (pairs * C <= full && blocks <= C * PD_WARPS * per_warp) return {C, 0};
-    return {0, (int)min((long long)full, (blocks * pairs + PD_MIN_BLOCKS - 1) / PD_MIN_BLOCKS)};
+    // 4000 keys 20.5 and 19.8, of 8000 keys 32.5 and 28.6.  Past a full chip a sequence
+    // has one CTA, for as many blocks as in the full one: 400 sequences of 100 keys 11.7
+    // and 13.5 us, 800 25.3 and 29.3, 1600 44.8 and 47.7, 900 of 480 keys 50.3 and 49.3;
+    // 200 sequences of 250 keys on 8 kv heads 23.8 and 34.3.
+    const int full = pd_grid_full(sms, G);
+    int split = PD_MAX_CLUSTER;
+    while (split > 1 && pairs * split > full) split /= 2;
+    const int per_warp = pairs * split * 2 <= full ? PD_CLUSTER_BLOCKS : PD_CLUSTER_BLOCKS / 2;
+    if (blocks <= split * PD_WARPS * per_warp) {
+        int C = 1;
+        while (C < split && C * PD_WARPS < blocks) C *= 2;
+        return {C, split, 0};
+    }
+    return {0, 0, (int)min((long long)full, (blocks * pairs + PD_MIN_BLOCKS - 1) / PD_MIN_BLOCKS)};
 }
 
 template <class E, int DP, int HT>
 cudaError_t launch_ht(PagedDecodeArgs a, int sms, cudaStream_t s) {
     constexpr int SMEM = PdSmem<DP, HT>::TOTAL;
     const PdPlan plan = pd_plan(a.c, a.B, a.NH, a.window, a.sinks, sms);
+    a.split = plan.split;
     if (plan.cluster) {
         auto k = k_paged_decode<E, DP, HT, true>;
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);

@@ -10,12 +10,13 @@
 // tile: S = Q K^T into TMEM, one thread per row takes p = 2^(s - m) and writes P
 // (bf16 / f16) back to TMEM, O += P V accumulates there.  The reference maximum m
 // moves (and O, l are rescaled, the tile done again) only when a row's weights of a
-// tile sum to more than 2^15, so that most tiles need no maximum at all.  S has two buffers for each query tile, so the products of the next key
-// tile are ready before a row's thread asks for them, and the two query tiles'
-// threads and the tensor cores wait for one another only when one of them has
-// fallen a whole tile behind.  (With one buffer of 128 keys, P over it, a step
-// was the sum of both products and the exponentials, 3.8 k cycles for 128 keys; a
-// product of 64 columns takes 45 cycles, of 128 columns 64.)
+// tile sum to more than 2^15, so that most tiles need no maximum at all.  S has two
+// buffers for each query tile, so the products of the next key tile are ready before
+// a row's thread asks for them, and the two query tiles' threads and the tensor
+// cores wait for one another only when one of them has fallen a whole tile behind.
+// (With one buffer of 128 keys, P over it, a step was the sum of both products and
+// the exponentials, 3.8 k cycles for 128 keys; a product of 64 columns takes 45
+// cycles, of 128 columns 64.)
 //
 // K and V tiles are read from the pages as they lie, one TMA box (64 elements x
 // up to 128 rows of a page) at a time, 128-byte swizzled: as K-major operand of
@@ -26,9 +27,10 @@
 // start) a warp zeroes the V rows that no row sees, since 0 * NaN from a
 // stale row would not be 0.
 //
-// P is rounded to the cache's type, bf16 2^-9 of each weight at most, which in a
-// sum over keys of mixed sign is about the output's own rounding; l is summed
-// from the unrounded weights in f32.
+// P is rounded to the cache's type, bf16 by 2^-8 of each weight at most, which in a
+// sum over keys of mixed sign is about the output's own rounding (error against 64
+// bits 0.0022, the bare rounding's 0.0016); l is summed from the unrounded weights
+// in f32.
 //
 // CTAs are persistent: one whose last copies are issued asks the hardware to
 // cancel a CTA that has not started yet (clusterlaunchcontrol) and takes over
@@ -40,10 +42,10 @@
 // share a pair's key tiles, leave (m, l, O) of its rows in their shared memory and
 // join a share of the rows each through distributed shared memory.
 //
-// Measured: a 2048-token prompt, 32 heads on 8 of 64, 29 us (590 TFLOP/s of the
-// products it cannot do without); five chunks of up to 1000 tokens on up to 5000
-// keys, 16 on 8 of 128, f16, 94 us (850); 8192 tokens under a window of 1024, 78 us
-// (830).  For 64 keys and both query tiles the products take 1250 cycles at
+// Measured: a 2048-token prompt, 32 heads on 8 of 64, 28.5 us (603 TFLOP/s of
+// the products it cannot do without); five chunks of up to 1000 tokens on up to 5000
+// keys, 16 on 8 of 128, f16, 93 us (860); 8192 tokens under a window of 1024, 75 us
+// (860).  For 64 keys and both query tiles the products take 1250 cycles at
 // head_dim 128 and 770 at 64, the exponentials 560 and the row threads' other
 // instructions about as much again; a step takes 1780 and 1310, since each waits
 // for the others at times.  The tensor pipe is active for 48 % of the cycles in the

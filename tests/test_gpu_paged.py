@@ -254,6 +254,42 @@ def test_decode_many_short_sequences():
     check_decode(p, q, out, lse)
 
 
+@pytest.mark.parametrize("B,most,NH,NKV,D", [
+    (40, 900, 4, 2, 64), (90, 400, 2, 2, 64), (130, 330, 12, 1, 128), (260, 480, 2, 2, 64), (500, 250, 3, 1, 128),
+])
+def test_decode_batches_of_every_size_of_cluster(B, most, NH, NKV, D):
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, most, B)]
+    lens[0], lens[1] = most, most - 15
+    p = Pool(B, lens, NKV, D, 16)
+    q = p.queries(B, NH, 2.0)
+    out, lse = p.cache.decode(q, ints(lens), return_lse=True)
+    check_decode(p, q, out, lse)
+    assert torch.equal(out, p.cache.decode(q, ints(lens)))
+    out, lse = p.cache.decode(q, ints(lens), window=70, sinks=5, return_lse=True)
+    check_decode(p, q, out, lse, window=70, sinks=5)
+
+
+@pytest.mark.parametrize("at", [0, 151, 299])
+def test_decode_one_long_sequence_among_many_short_ones(at):
+    rng = np.random.default_rng(at)
+    lens = [int(x) for x in rng.integers(0, 40, 300)]
+    lens[at] = 6000
+    p = Pool(at + 23, lens, 2, 64, 16)
+    q = p.queries(300, 4, 2.0)
+    seqs = [b if b % 7 != 3 or b == at else -1 for b in range(300)]
+    buf = torch.full((300, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    bad = list(lens)
+    bad[5] = 10 ** 6
+    out, lse = p.cache.decode(q, ints(bad), seqs=ints(seqs), out=buf, return_lse=True)
+    assert p.cache.sync_status() == 2
+    seqs[5] = -1
+    check_decode(p, q, out, lse, seqs=seqs)
+    for b in range(300):
+        if seqs[b] < 0:
+            assert (buf[b] == 7).all()
+
+
 @pytest.mark.parametrize("lens", [[300, 1000], [9000, 700]])   # joined in a cluster; over the workspace
 def test_decode_captured_replayed_and_on_other_streams(lens):
     p = Pool(19, lens, 2, 64, 16)
