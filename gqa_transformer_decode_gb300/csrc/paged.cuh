@@ -12,8 +12,13 @@ namespace ember {
 
 // Cache element types.  Values are computed in f32 and rounded once, to
 // nearest even, when they are stored.
+// LIFT: softmax weights go into the second product as 2^(s - max + LIFT).  Below 2^-14
+// an f16 has a fixed step of 2^-24, so without a lift 250000 keys of weight 2^-25.1
+// each, 0.7 % of the sum beside one key of weight 1, would round to nothing; lifted,
+// a weight is off by at most 2^-32 of the largest one.
 struct ElemBf16 {
     static constexpr bool bf16 = true;
+    static constexpr float LIFT = 0.f;
     __device__ __forceinline__ static uint32_t pack(float lo, float hi) {
         uint32_t r;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -32,6 +37,7 @@ struct ElemBf16 {
 };
 struct ElemF16 {
     static constexpr bool bf16 = false;
+    static constexpr float LIFT = 7.f;
     __device__ __forceinline__ static uint32_t pack(float lo, float hi) { return pack_f16x2(lo, hi); }
     __device__ __forceinline__ static float lo(uint32_t u) { return __half2float(__ushort_as_half((uint16_t)u)); }
     __device__ __forceinline__ static float hi(uint32_t u) { return __half2float(__ushort_as_half((uint16_t)(u >> 16))); }

@@ -41,7 +41,7 @@
 // CTAs end between 34 and 48 us, and the join with its launch takes 5.
 //
 // P, the second product's operand, goes in as the sum of two values of the cache's
-// type (bf16 2^-16 relative, f16 2^-22): one would add as much error as the output's
+// type (bf16 2^-16 relative, f16 2^-22 or 2^-32 of the largest): one would add as much error as the output's
 // own rounding, and the products are far from bounding this kernel.
 #include "paged.cuh"
 
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
                 }
         // O^T: rows (dimensions) 16 i + g4 and + 8, columns (heads) 8 t + 2 q4 and + 1
         float o[HT][KS][4];
-        float m[HT][2], l[HT][2];            // of heads 8 t + 2 q4 + e; l over this lane's keys
+        float m[HT][2], l[HT][2];            // of heads 8 t + 2 q4 + e, m less LIFT; l over this lane's keys
 #pragma unroll
         for (int t = 0; t < HT; ++t) {
 #pragma unroll
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
 #pragma unroll
                     for (int t = 0; t < HT; ++t) {
                         s[u][t][i] = in ? s[u][t][i] * sc : -INFINITY;
-                        up |= s[u][t][i] > m[t][i & 1] + 8.f;
+                        up |= s[u][t][i] > m[t][i & 1] + (8.f + E::LIFT);
                     }
                 }
             if (__any_sync(FULL_MASK, up)) {
@@ -404,11 +404,12 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
                 for (int t = 0; t < HT; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = m[t][e];
+                        float x = -INFINITY;
 #pragma unroll
                         for (int u = 0; u < NSUB; ++u) x = fmaxf(x, fmaxf(s[u][t][e], s[u][t][e + 2]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, d));
+                        x = fmaxf(m[t][e], x - E::LIFT);
                         const float f = ex2(m[t][e] - x);
                         m[t][e] = x;
                         l[t][e] *= f;

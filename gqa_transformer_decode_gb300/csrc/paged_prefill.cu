@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(PP_THREADS) k_paged_prefill(PagedPrefillArgs a
                 E::mma(s[nt], qa[kk], b0, b1);
                 E::mma(s[nt + 1], qa[kk], b2, b3);
             }
-        float mx[2] = {m[0], m[1]};
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(PP_THREADS) k_paged_prefill(PagedPrefillArgs a
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(FULL_MASK, mx[h], 1));
-            mx[h] = fmaxf(mx[h], __shfl_xor_sync(FULL_MASK, mx[h], 2));
+            mx[h] = fmaxf(m[h], fmaxf(mx[h], __shfl_xor_sync(FULL_MASK, mx[h], 2)) - E::LIFT);
             f[h] = ex2(m[h] - mx[h]);
             m[h] = mx[h];
             l[h] *= f[h];

@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const int nkt = t * QT < p.tokens ? max(0, p.nkt) : 0;   // (without tokens the tile has no products either)
         const bool live = p.nkt >= 0 && r < QT * G && tok < p.tokens;
         const int qp = p.pos0 + min(tok, p.tokens - 1);   // its position (rows that are not live: the last one's)
-        float m = SOFTMAX_FLOOR, l = 0.f;             // reference maximum (of s * sc), sum of 2^(s sc - m)
+        float m = SOFTMAX_FLOOR, l = 0.f;             // reference maximum (of s * sc) less LIFT, sum of 2^(s sc - m)
         for (int j = 0; j < nkt; ++j) {
             const int n = base + j;
             const uint32_t tS = tmem + L::col_s(t, n & 1) + lane_off;
@@ -596,14 +596,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             // (Rows that are not live hold anything and ask for nothing.)
             scores();
             const bool look = live && m == SOFTMAX_FLOOR;
-            if (__any_sync(FULL_MASK, look)) m = look ? fmaxf(m, largest()) : m;
+            if (__any_sync(FULL_MASK, look)) m = look ? fmaxf(m, largest() - E::LIFT) : m;
             float sum = weigh();
             const bool move = live && !(sum <= MOST);
             const bool any_move = __any_sync(FULL_MASK, move);
             float corr = 1.f;
             if (any_move) {
                 scores();                             // (S is whole until P is stored)
-                const float mnew = move ? fmaxf(m, largest()) : m;
+                const float mnew = move ? fmaxf(m, largest() - E::LIFT) : m;
                 corr = ex2(m - mnew);
                 l *= corr;
                 m = mnew;

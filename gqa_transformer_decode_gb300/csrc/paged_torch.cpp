@@ -101,6 +101,11 @@ int32_t number(PyObject* o, const char* what) {
     if (v < INT_MIN || v > INT_MAX) bad(std::string(what) + " is beyond 32 bits");
     return (int32_t)v;
 }
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw python_error();
+    return v;
+}
 double real(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -248,7 +253,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         const int32_t window = number(a[4], "window"), sinks = number(a[5], "sinks");
         const double scale = given(a[6]) ? real(a[6]) : 1.0 / std::sqrt((double)c.kv.head_dim);
         const c10::cuda::OptionalCUDAGuard on(c10::Device(at::kCUDA, c.device));
-        Outputs o = outputs(c, B, heads, a[7], a[8], PyObject_IsTrue(a[9]) == 1);
+        Outputs o = outputs(c, B, heads, a[7], a[8], truth(a[9]));
         if (B > 0) {
             Tensor ws;
             void* wp = nullptr;
@@ -284,7 +289,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         const int32_t window = number(a[5], "window"), sinks = number(a[6], "sinks");
         const double scale = given(a[7]) ? real(a[7]) : 1.0 / std::sqrt((double)c.kv.head_dim);
         const c10::cuda::OptionalCUDAGuard on(c10::Device(at::kCUDA, c.device));
-        Outputs o = outputs(c, n, heads, a[8], a[9], PyObject_IsTrue(a[10]) == 1);
+        Outputs o = outputs(c, n, heads, a[8], a[9], truth(a[10]));
         if (n > 0 && B > 0)
             check(f_prefill(&c.kv, qr.p, qr.ld, count(n, "q"), count(B, "lens"), count(heads, "q"), seqs, cu, lens, window, sinks,
                             (float)scale, o.r.p, o.r.ld, o.lse_p, c.status, stream_of(c)),

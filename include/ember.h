@@ -322,7 +322,9 @@ ember_status ember_sample(const float *logits, int32_t B, int32_t V, int32_t ldl
  *     rows of a page that no query of the call sees: they may hold anything.
  *   - Products are taken on the cache's type and summed in f32, softmax weights
  *     against a maximum that may lag behind the true one by up to 2^15: keys and
- *     values stay below about 1e33 in magnitude (bf16; f16 always does).
+ *     values stay below about 1e33 in magnitude (bf16; f16 always does).  A weight's
+ *     rounding for the second product is relative, but f16's at least 2^-32 of the
+ *     largest weight of its row.
  *   - B is at most 65535.  No operator has a gradient.
  *   - Buffers and the stream belong to the current device; buffers may not
  *     overlap, except that pages may be shared by the tables of sequences

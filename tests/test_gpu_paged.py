@@ -500,6 +500,43 @@ def test_other_scales(scale):
     check_prefill(p, q, out, lse, cu, lens, window=100, sinks=3, scale=scale, rows=20)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("form", ["decode", "prefill", "prefill with scale < 0", "prefill at the end"])
+def test_many_small_weights_beside_a_large_one(form, dtype):
+    """250000 keys of weight 2^-25.1 with value 1 beside one of weight 1 with value
+    0: out is what the small ones sum to, 0.7 %.  Each weight may be off by u_P of
+    itself and, for f16, whose step is fixed below a point, by 2^-32 of the largest
+    one, which with n keys of |v| <= 1 is n 2^-32 in out and in lse."""
+    n = 250000
+    p = Pool(3, [n], 1, 16, 1024, dtype)
+    sign = -1.0 if "scale" in form else 1.0
+    p.k[...] = 0
+    p.k[..., 0] = -25.1 * np.log(2.0) * sign
+    p.v[...] = 1
+    at = (n - 1 if "end" in form else 1234)
+    p.k[int(p.table_np[0, at // 1024]), 0, at % 1024, 0] = 0
+    p.v[int(p.table_np[0, at // 1024]), 0, at % 1024] = 0
+    new = 1 if form == "decode" else 3 if "end" not in form else 200
+    q = torch.zeros((new, 2, 16), dtype=p.k.dtype, device="cuda")
+    q[..., 0] = 1
+    if form == "decode":
+        out, lse = p.cache.decode(q, ints([n]), scale=1.0, return_lse=True)
+        u_p = 2.0 ** -16 if dtype == "bf16" else 2.0 ** -22
+    else:
+        out, lse = p.cache.prefill(q, ints([0, new]), ints([n]), scale=sign, return_lse=True)
+        u_p = U[dtype]
+    k, v = p.f64()
+    pos = list(range(n - new, n))
+    want = O.attend(q.double().cpu().numpy(), k, v, p.table_np[0], n, pos, 0, 0, sign)
+    flush = n * 2.0 ** -32 if dtype == "f16" else 0.0
+    ex, _, mean, big = want
+    ds, sums = 20 * 2.0 ** -23 * big, (n / 16 + 64) * 2.0 ** -23
+    tol = mean * (2 * ds + 2.0 ** -21 + u_p + sums) + flush + U[dtype] * np.abs(ex) + 2.0 ** -25
+    err = np.abs(out.double().cpu().numpy() - ex)
+    assert (err <= tol).all(), (err / tol).max()
+    assert np.abs(lse.double().cpu().numpy() - want[1]).max() <= (ds + 2.0 ** -21 + sums + 2.0 ** -22 * np.abs(want[1])).max()
+
+
 def test_one_row_of_prefill_is_decode():
     lens = [1, 64, 300]
     p = Pool(41, lens, 2, 128, 32, "f16")
