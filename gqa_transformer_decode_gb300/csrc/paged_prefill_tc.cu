@@ -283,9 +283,17 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    auto wait_all = [&](uint64_t* b, int parity) {     // by a whole warp
-        return __all_sync(FULL_MASK, mbar_wait(b, (uint32_t)parity & 1u)) != 0;
+    // By a whole warp: true once every lane's barrier has completed its phase, false after
+    // the bounded time.  (The first try, nearly always the last, is a poll and a vote: a
+    // loop of each lane's own took 300 cycles of a step's 2000.)
+    auto wait_at = [&](uint32_t addr, uint32_t parity) {
+        if (__all_sync(FULL_MASK, mbar_try_wait(addr, parity))) return true;
+        const long long t0 = clock64();
+        while (!__all_sync(FULL_MASK, mbar_try_wait(addr, parity)))
+            if (__any_sync(FULL_MASK, clock64() - t0 > TC_WAIT_CYCLES)) return false;
+        return true;
     };
+    auto wait_all = [&](uint64_t* b, int parity) { return wait_at(smem_u32(b), (uint32_t)parity & 1u); };
     // the CTA index after the it-th pair's: false when there is none left (or, ok = false, no answer)
     auto take_next = [&](int it, unsigned& cta, bool& ok) {
         if (SPLIT) return false;
@@ -418,23 +426,23 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const uint32_t kv0 = uniform(smem_u32(sm + L::OFF_KV));
         const uint32_t col_s = tm + uniform(t * 128), col_o = tm + uniform(L::col_o(t));
         const uint32_t dq = uniform(desc_k(smem_u32(sm + L::OFF_Q + t * L::QTILE)));
-        auto mma_s = [&](uint32_t buf, uint32_t dk) {   // S = Q . K^T
+        const uint32_t dk0 = uniform(desc_k(kv0)), dv0 = uniform(desc_mn(kv0, PT_KEYS * 128));
+        const uint32_t p_at = smem_u32(&p_full[2 * t]), o_at = smem_u32(&o_full[2 * t]), s_at = smem_u32(&s_full[2 * t]);
+        const uint32_t free_at = smem_u32(&o_free[t]), full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
+        auto commit = [](uint32_t at) {
+            asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(at) : "memory");
+        };
+        auto mma_s = [&](uint32_t c, uint32_t dk) {   // S = Q . K^T
 #pragma unroll
             for (int kb = 0; kb < L::KB; ++kb)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_ss(col_s + buf * 64, dq + ((kb * PT_ROWS * 128 + k * 32) >> 4),
-                           dk + ((kb * PT_KEYS * 128 + k * 32) >> 4), idS, kb | k);
-            umma_commit(&s_full[2 * t + buf]);
+                    mma_ss(c, dq + ((kb * PT_ROWS * 128 + k * 32) >> 4), dk + ((kb * PT_KEYS * 128 + k * 32) >> 4), idS, kb | k);
         };
-        auto mma_pv = [&](uint32_t buf, uint32_t dv, bool acc) {   // O += P (TMEM) . V
+        auto mma_pv = [&](uint32_t c, uint32_t dv, bool acc) {   // O += P (TMEM) . V
 #pragma unroll
-            for (int k = 0; k < PT_KEYS / 16; ++k)
-                mma_ts(col_o, col_s + buf * 64 + k * 8, dv + ((k * 16 * 128) >> 4), idO, acc || k);
-            umma_commit(&o_full[2 * t + buf]);
+            for (int k = 0; k < PT_KEYS / 16; ++k) mma_ts(col_o, c + k * 8, dv + ((k * 16 * 128) >> 4), idO, acc || k);
         };
-        auto slot_k = [&](int n) { return uniform(desc_k(kv0 + (2 * n % NS) * L::TILE)); };
-        auto slot_v = [&](int n) { return uniform(desc_mn(kv0 + ((2 * n + 1) % NS) * L::TILE, PT_KEYS * 128)); };
         // one lane issues f() after everything the warp has waited for
         auto issue = [&](auto f) {
             if (elect_one()) {
@@ -464,45 +472,50 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 auto first_s = [&](int j) {
                     const int n = base + j;
                     if (!(ok = wait_all(slot_full(2 * n), 2 * n / NS))) return;
-                    const uint32_t buf = uniform((mine + j) & 1), dk = slot_k(n);
+                    const uint32_t b = uniform((mine + j) & 1), dk = dk0 + uniform(2 * n % NS) * (L::TILE >> 4);
                     issue([&] {
-                        mma_s(buf, dk);
+                        mma_s(col_s + b * 64, dk);
+                        commit(s_at + b * 8);
                         umma_commit(&kv_empty[2 * n % NS]);
                         if (j + 1 == nkt) umma_commit(q_empty);
                     });
                 };
                 if (nkt > 0) first_s(0);
                 if (ok && nkt > 1) first_s(1);
-                for (int j = 0; ok && j < nkt; ++j) {
+                // What a step waits for and its operands are carried along, not computed: the
+                // pipe idles from the end of one step's issue to the start of the next.
+                int sv = (2 * base + 1) % NS, sk = (2 * base + 4) % NS;   // slots of V(j) and K(j + 2), their phases
+                uint32_t vp = (2 * base + 1) / NS & 1, kp = (2 * base + 4) / NS & 1, buf = mine & 1, pp = mine >> 1 & 1;
+                const int role = lane & 3;
+                for (int j = 0; j < nkt; ++j) {
                     // P . V(j) frees the buffer that S(j + 2) takes (MMAs of one thread run
                     // in the order of issue), and S(j + 1) is there already
-                    const int n = base + j, m = mine + j;
                     const bool more = j + 2 < nkt;
-                    const uint32_t buf = uniform(m & 1), dv = slot_v(n), dk = slot_k(n + 2);
                     // P(j), V(j), K(j + 2) and, before a pair's first P . V, the end of the
                     // pair before's use of O: a lane each, so that one poll sees them all
-                    uint64_t* b = &p_full[2 * t + (m & 1)];
-                    int parity = m >> 1;
-                    if ((lane & 3) == 1) {
-                        b = slot_full(2 * n + 1);
-                        parity = (2 * n + 1) / NS;
-                    } else if ((lane & 3) == 2 && more) {
-                        b = slot_full(2 * n + 4);
-                        parity = (2 * n + 4) / NS;
-                    } else if ((lane & 3) == 3 && j == 0 && with > 0) {
-                        b = &o_free[t];
-                        parity = with - 1;
-                    }
-                    if (!(ok = wait_all(b, parity))) break;
+                    uint32_t at = p_at + buf * 8, parity = pp;
+                    if (role == 1) at = full_at + sv * 8, parity = vp;
+                    if (role == 2 && more) at = full_at + sk * 8, parity = kp;
+                    if (role == 3 && j == 0 && with > 0) at = free_at, parity = (with - 1) & 1;
+                    const uint32_t c = col_s + uniform(buf) * 64, dv = dv0 + uniform(sv) * (L::TILE >> 4),
+                                   dk = dk0 + uniform(sk) * (L::TILE >> 4);
+                    const uint32_t o_bar = o_at + buf * 8, s_bar = s_at + buf * 8, v_bar = empty_at + sv * 8, k_bar = empty_at + sk * 8;
+                    if (!(ok = wait_at(at, parity))) break;
                     issue([&] {
-                        mma_pv(buf, dv, j > 0);
-                        umma_commit(&kv_empty[(2 * n + 1) % NS]);
+                        mma_pv(c, dv, j > 0);
+                        commit(o_bar);
+                        commit(v_bar);
                         if (more) {
-                            mma_s(buf, dk);
-                            umma_commit(&kv_empty[(2 * n + 4) % NS]);
+                            mma_s(c, dk);
+                            commit(s_bar);
+                            commit(k_bar);
                             if (j + 3 == nkt) umma_commit(q_empty);
                         }
                     });
+                    pp ^= buf;
+                    buf ^= 1;
+                    if ((sv += 2) >= NS) sv -= NS, vp ^= 1;
+                    if ((sk += 2) >= NS) sk -= NS, kp ^= 1;
                 }
                 mine += nkt;
                 with += nkt > 0;
