@@ -313,22 +313,36 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     if (warp == PT_TMA) {   // ------------------------------------- TMA producer
         const int P = 1 << a.c.page_shift;
         const int box = min(P, PT_KEYS);               // rows of a box
-        const int boxes = PT_KEYS / box;               // of a tile: lane i < boxes copies box i
+        const int boxes = PT_KEYS / box;               // of a tile: lane i < boxes looks up box i's page
         unsigned cta = first_pair;
         int issued = 0, pairs = 0, it = 0;             // slots and pairs with keys so far
+        // The slots of K(j) and V(j) are waited for together (a wait for the phase before a
+        // barrier's first passes), and one lane issues a tile's copies: with a wait, a page
+        // and a choice of map for each of the two, this warp's 2000 cycles a tile set the
+        // kernel's pace, the copies themselves take 330.
+        int slot = 0;
+        uint32_t empty = 1;
+        const uint32_t empty_at = smem_u32(kv_empty);
         bool ok = true, asked = false;
         for (;; ++it) {
             const PtPair p = pt_pair(a, QT, cta, pairs_all, part, parts, part == 0);
             if (p.nkt > 0) {
-                auto look_up = [&](int j) {            // the lane's page of tile j; n_pages reads as zeros
-                    const int k0 = p.key0(j) + lane * box;
-                    if (lane >= boxes || k0 >= p.end || (k0 + box <= p.first && k0 >= p.sinks)) return a.c.n_pages;
-                    const int page = a.c.table[(size_t)p.seq * a.c.width + (k0 >> a.c.page_shift)];
-                    if (page >= 0 && page < a.c.n_pages) return page;
-                    raise_status(a.status, EMBER_ERR_INVALID_ARG);
-                    return a.c.n_pages;
+                // The page of the lane's box of tile j, if some row sees its keys.  What it
+                // loads is looked at two tiles later, so that nothing waits for it.
+                struct Entry {
+                    int page;
+                    bool seen;
                 };
-                int page = look_up(0), next = 0;
+                auto look_up = [&](int j) {
+                    Entry e{0, false};
+                    if (j >= p.nkt) return e;
+                    const int k0 = p.key0(j) + lane * box;
+                    e.seen = lane < boxes && k0 < p.end && (k0 + box > p.first || k0 < p.sinks);
+                    if (e.seen) e.page = a.c.table[(size_t)p.seq * a.c.width + (k0 >> a.c.page_shift)];
+                    return e;
+                };
+                Entry e0 = look_up(0), e1 = look_up(1);
+                const int g = uniform(p.g);
                 ok = pairs == 0 || wait_all(q_empty, pairs - 1);
                 if (!ok) break;
                 if (lane == 0) {                       // tokens beyond the sequence's: whatever follows, or zeros
@@ -339,23 +353,38 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                                         p.row0 + t * QT, q_full);
                 }
                 ++pairs;
-                for (int i = 0; i < 2 * p.nkt; ++i, ++issued) {
-                    const int s = issued % NS, j = i >> 1;
-                    const bool is_v = i & 1;
-                    if (!is_v && j + 1 < p.nkt) next = look_up(j + 1);
-                    ok = issued < NS || wait_all(&kv_empty[s], issued / NS - 1);
-                    if (!ok) break;
-                    uint64_t* full = is_v ? &v_raw[s >> 1] : &kv_full[s];   // (NS is even)
-                    if (lane == 0) mbar_expect_tx(full, L::TILE);
-                    __syncwarp();
-                    if (lane < boxes) {
-                        const int row = (p.key0(j) + lane * box) & (P - 1);
-                        uint8_t* d = sm + L::OFF_KV + s * L::TILE + lane * box * 128;
+                for (int j = 0; j < p.nkt; ++j, issued += 2) {
+                    bool known = e0.page >= 0 && e0.page < a.c.n_pages;
+                    if (e0.seen && !known) raise_status(a.status, EMBER_ERR_INVALID_ARG);
+                    const int page = e0.seen && known ? e0.page : a.c.n_pages;   // n_pages reads as zeros
+                    e0 = e1;
+                    e1 = look_up(j + 2);
+                    int pages[PT_KEYS / 16];
 #pragma unroll
-                        for (int kb = 0; kb < L::KB; ++kb)
-                            tma_load_4d(d + kb * PT_KEYS * 128, is_v ? &tmV : &tmK, kb * 64, row, p.g, page, full);
+                    for (int i = 0; i < PT_KEYS / 16; ++i) pages[i] = __shfl_sync(FULL_MASK, page, i);
+                    const int s = uniform(slot), row = uniform(p.key0(j) & (P - 1));   // (0 where a tile has several boxes)
+                    if (!(ok = wait_at(empty_at + (s + (lane & 1)) * 8, empty))) break;
+                    if (elect_one()) {
+                        uint64_t *kf = &kv_full[s], *vf = &v_raw[s >> 1];
+                        uint8_t* d = sm + L::OFF_KV + s * L::TILE;
+                        mbar_expect_tx(kf, L::TILE);
+#pragma unroll
+                        for (int i = 0; i < PT_KEYS / 16; ++i)
+                            if (i < boxes)
+#pragma unroll
+                                for (int kb = 0; kb < L::KB; ++kb)
+                                    tma_load_4d(d + kb * PT_KEYS * 128 + i * box * 128, &tmK, kb * 64, row, g, pages[i], kf);
+                        mbar_expect_tx(vf, L::TILE);
+#pragma unroll
+                        for (int i = 0; i < PT_KEYS / 16; ++i)
+                            if (i < boxes)
+#pragma unroll
+                                for (int kb = 0; kb < L::KB; ++kb)
+                                    tma_load_4d(d + L::TILE + kb * PT_KEYS * 128 + i * box * 128, &tmV, kb * 64, row, g,
+                                                pages[i], vf);
                     }
-                    if (is_v) page = next;
+                    __syncwarp();
+                    if ((slot += 2) == NS) slot = 0, empty ^= 1;
                 }
                 if (!ok) break;
             }
