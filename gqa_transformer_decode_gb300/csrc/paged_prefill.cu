@@ -9,7 +9,7 @@
 // r = token r / G, head r % G.  One CTA holds 64 rows of one kv head, 16 to a
 // warp, and walks the keys in tiles of 64 that cp.async copies (zero fill for keys
 // no row sees) stage two deep in shared memory.  Bound by latency: 4 sequences
-// of 9 new tokens, 14 heads on 2, in 4.5 us.
+// of 9 new tokens, 14 heads on 2, in 4.3 us.
 #include "paged.cuh"
 
 namespace ember {
@@ -214,10 +214,12 @@ cudaError_t launch_dp(const PagedPrefillArgs& a, cudaStream_t s) {
 
 cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, int sms, cudaStream_t s) {
     // Short sequences only, where filling the tcgen05 kernel's pipeline costs more than
-    // the whole attention: 20 new tokens each of 256 sequences 58 us here and 85 there,
-    // 4 sequences of 9 tokens 4.5 and 6.3 us; but 100 of 64 sequences 32 and 27 us, and
-    // with keys for more than two of its tiles the other kernel wins at any size (2
-    // tokens on 200 keys 9.4 and 8.8 us, on 1000 keys 52 and 26 us).
+    // the whole attention.  14 heads on 2 of 64, here and there: 20 new tokens each of 256
+    // sequences 18.5 and 27.7 us, 4 sequences of 9 tokens 4.3 and 5.5, 60 of 64 sequences
+    // 10.1 and 11.4, but 100 of 64 sequences 14.0 and 13.7; 32 on 8: 20 of 256 sequences
+    // 68 and 91, 60 of 64 27.7 and 24.5, 100 of 64 55 and 38.  With keys for more than two
+    // of its tiles the other kernel wins at any size: 2 tokens on 200 keys 9.4 and 7.1 us,
+    // of 64 sequences on 1000 keys 33 and 15 us.
     const bool small = ((long long)a.c.width << a.c.page_shift) <= PP_SMALL_KEYS && a.n <= PP_SMALL_ROWS * (long long)a.B;
     PagedPrefillMaps maps;
     // (the tcgen05 kernel takes the largest product for the largest score: scale > 0)

@@ -42,14 +42,18 @@
 // share a pair's key tiles, leave (m, l, O) of its rows in their shared memory and
 // join a share of the rows each through distributed shared memory.
 //
-// Measured: a 2048-token prompt, 32 heads on 8 of 64, 28.5 us (603 TFLOP/s of
-// the products it cannot do without); five chunks of up to 1000 tokens on up to 5000
-// keys, 16 on 8 of 128, f16, 93 us (860); 8192 tokens under a window of 1024, 75 us
-// (860).  For 64 keys and both query tiles the products take 1250 cycles at
-// head_dim 128 and 770 at 64, the exponentials 560 and the row threads' other
-// instructions about as much again; a step takes 1780 and 1310, since each waits
-// for the others at times.  The tensor pipe is active for 48 % of the cycles in the
-// chunks, whose longest tile pairs (94 steps) set the time, and 27 % in the prompt.
+// Measured: a 2048-token prompt, 32 heads on 8 of 64, 27.4 us (627 TFLOP/s of
+// the products it cannot do without), one of 8000 tokens 296 us (885); five chunks of up
+// to 1000 tokens on up to 5000 keys, 16 on 8 of 128, f16, 67 us (1200); 8192 tokens
+// under a window of 1024, 68 us (945).  For 64 keys and both query tiles the products
+// take 1263 cycles at head_dim 128 and 640 at 64 with nothing else running, the
+// exponentials with their sums and rounding 540.  A step takes about 1330 at head_dim
+// 128: the products.  At 64 it takes 1370: a row's thread waits for its scores, loads
+// them (150 cycles each), works on them (under 900, two warps a scheduler) and hands
+// the weights over (150), one after the other.  The copy and MMA warps' own
+// instructions matter as much as the products: each must pass a tile in less than that.
+// The tensor pipe is active for 65 % of the cycles in the chunks, whose longest tile
+// pairs (94 steps) set the time, 52 % under the window and 27 % in the prompt.
 //
 // Warps 0-3: tile A; warps 4-7: tile B (a warp reads the TMEM lanes of its index
 // mod 4); warp 8: TMA producer; warp 9: TMEM allocation; warps
