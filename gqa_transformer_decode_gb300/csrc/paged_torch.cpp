@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -57,7 +58,10 @@ std::string describe(const Tensor& t) {
 
 const Tensor& tensor(PyObject* o, const char* what) {
     if (!THPVariable_Check(o)) throw Bad{PyExc_TypeError, std::string(what) + " must be a tensor"};
-    return THPVariable_Unpack(o);
+    const Tensor& t = THPVariable_Unpack(o);
+    if (t.requires_grad() && c10::GradMode::is_enabled())   // it would be lost without a word
+        bad(std::string(what) + " requires a gradient, which the paged operators do not have (torch.no_grad() to go without)");
+    return t;
 }
 bool given(PyObject* o) { return o != Py_None; }
 

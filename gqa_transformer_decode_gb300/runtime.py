@@ -158,7 +158,9 @@ class PagedKV:
     keeps references and one int32 status word.  Calls are asynchronous on
     `stream` (default: the current stream of the pages' device); device-side
     errors are read with sync_status().  Tensors that a call allocates are
-    allocated on that stream.
+    allocated on that stream, and hold anything in the rows that the call does
+    not write (padding, rows outside every sequence).  The operators have no
+    gradient: a tensor that requires one is refused unless gradients are off.
     """
 
     def __init__(self, k_pages, v_pages, table):

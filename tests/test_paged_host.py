@@ -142,3 +142,19 @@ def test_the_torch_side_refuses_before_any_device_work():
         t.prefill(c, q, lens, None, None, 0, 0, None, None, None, False)
     with pytest.raises(ValueError):
         t.decode("no cache", q, lens, None, 0, 0, None, None, None, False, None)
+
+
+def test_the_torch_side_refuses_to_lose_a_gradient():
+    import torch
+    t, c = torch_side()
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16, requires_grad=True)
+    x = q.detach()
+    lens = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="q requires a gradient"):
+        t.decode(c, q, lens, None, 0, 0, None, None, None, False, None)
+    with pytest.raises(ValueError, match="q requires a gradient"):
+        t.prefill(c, q * 2, lens, lens, None, 0, 0, None, None, None, False)
+    with pytest.raises(ValueError, match="v requires a gradient"):
+        t.append(c, x, q, lens, lens, x, x, None, None, None, 1e-6, None)
+    with torch.no_grad(), pytest.raises(ValueError, match="q must be on cuda:0, not cpu"):
+        t.decode(c, q, lens, None, 0, 0, None, None, None, False, None)
