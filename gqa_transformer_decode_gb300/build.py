@@ -2,9 +2,10 @@
 the torch side of the paged-cache operators: csrc/paged_torch.cpp ->
 _build/paged_torch<suffix> (a Python extension against the installed torch).
 
-Each translation unit compiles in parallel with nvcc (g++ for the extension),
-then one nvcc -shared link.  Used by __graft_entry__.build() and by the Python
-binding on first use.
+Each translation unit compiles in parallel with nvcc, then one nvcc -shared
+link.  The library needs neither torch nor a host C++ compiler beyond nvcc's, so
+build() leaves the extension alone; build_ext() (g++ and torch's headers) makes
+it when runtime.PagedKV is first used, build_all() both at once.
 """
 from __future__ import annotations
 
@@ -52,9 +53,21 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _torch_id() -> str:
+    """The torch that an extension is compiled against: another one may not load it, or load it and differ."""
+    import torch
+    return f"{torch.__version__} {torch.version.git_version} {os.path.dirname(torch.__file__)}"
+
+
 def ext_up_to_date() -> bool:
     deps = (TORCH_SRC, os.path.join(INCLUDE, "ember.h"))
-    return os.path.exists(TORCH_EXT) and all(os.path.getmtime(p) <= os.path.getmtime(TORCH_EXT) for p in deps)
+    made_for = TORCH_EXT + ".torch"
+    if not os.path.exists(TORCH_EXT) or not os.path.exists(made_for):
+        return False
+    with open(made_for) as f:
+        if f.read() != _torch_id():
+            return False
+    return all(os.path.getmtime(p) <= os.path.getmtime(TORCH_EXT) for p in deps)
 
 
 def build_ext(force: bool = False) -> str:
@@ -74,13 +87,25 @@ def build_ext(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("torch extension failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if os.path.exists(TORCH_EXT + ".torch"):
+        os.remove(TORCH_EXT + ".torch")      # never beside a binary that it does not speak of
     os.replace(tmp, TORCH_EXT)
+    with open(tmp, "w") as f:
+        f.write(_torch_id())
+    os.replace(tmp, TORCH_EXT + ".torch")
     return TORCH_EXT
+
+
+def build_all(force: bool = False) -> None:
+    """The library and the torch extension, side by side."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        ext = ex.submit(build_ext, force)
+        build(force)
+        ext.result()
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and up_to_date():
-        build_ext()
         return LIB
     os.makedirs(OUT, exist_ok=True)
     nvcc = _nvcc()
@@ -97,9 +122,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        ext = ex.submit(build_ext, force)
         objs = list(ex.map(compile_one, sources()))
-        ext.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
