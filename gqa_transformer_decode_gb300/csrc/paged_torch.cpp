@@ -38,6 +38,7 @@ struct Cache {
     int32_t* status;
     c10::DeviceIndex device;
     at::ScalarType dtype;
+    Tensor k_pages, v_pages;
     // decode's workspace of the last (B, heads): the query is a function of these
     int64_t ws_rows = -1, ws_heads = -1;
     size_t ws_bytes = 0;
@@ -56,11 +57,14 @@ std::string describe(const Tensor& t) {
     return s + "] on " + t.device().str();
 }
 
+void no_gradient(const Tensor& t, const char* what) {   // it would be lost without a word
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        bad(std::string(what) + " requires a gradient, which the paged operators do not have (torch.no_grad() to go without)");
+}
 const Tensor& tensor(PyObject* o, const char* what) {
     if (!THPVariable_Check(o)) throw Bad{PyExc_TypeError, std::string(what) + " must be a tensor"};
     const Tensor& t = THPVariable_Unpack(o);
-    if (t.requires_grad() && c10::GradMode::is_enabled())   // it would be lost without a word
-        bad(std::string(what) + " requires a gradient, which the paged operators do not have (torch.no_grad() to go without)");
+    no_gradient(t, what);
     return t;
 }
 bool given(PyObject* o) { return o != Py_None; }
@@ -136,6 +140,10 @@ void check(ember_status st, const char* where) {
 Cache& cache_of(PyObject* o) {
     auto* c = static_cast<Cache*>(PyCapsule_GetPointer(o, "ember.paged"));
     if (!c) throw python_error();
+    if (c->k_pages.defined()) {   // at every call: a tensor may be asked for its gradient at any time
+        no_gradient(c->k_pages, "k_pages");
+        no_gradient(c->v_pages, "v_pages");
+    }
     return *c;
 }
 
@@ -311,10 +319,14 @@ PyObject* workspace_bytes(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     });
 }
 
-// cache(address of an ember_paged_kv, address of the status word, device index)
+// cache(address of an ember_paged_kv, address of the status word, device index[, k_pages, v_pages])
 PyObject* cache(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-    return guarded(nargs, 3, [&]() -> PyObject* {
+    return guarded(nargs, nargs == 5 ? 5 : 3, [&]() -> PyObject* {
+        Tensor k_pages, v_pages;
+        if (nargs == 5) k_pages = tensor(a[3], "k_pages"), v_pages = tensor(a[4], "v_pages");
         auto* c = new Cache;
+        c->k_pages = k_pages;
+        c->v_pages = v_pages;
         c->kv = *static_cast<const ember_paged_kv*>(PyLong_AsVoidPtr(a[0]));
         c->status = static_cast<int32_t*>(PyLong_AsVoidPtr(a[1]));
         c->device = (c10::DeviceIndex)PyLong_AsLong(a[2]);

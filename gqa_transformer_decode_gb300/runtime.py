@@ -160,7 +160,8 @@ class PagedKV:
     errors are read with sync_status().  Tensors that a call allocates are
     allocated on that stream, and hold anything in the rows that the call does
     not write (padding, rows outside every sequence).  The operators have no
-    gradient: a tensor that requires one is refused unless gradients are off.
+    gradient: a tensor that requires one, the pages among them, is refused
+    unless gradients are off.
     """
 
     def __init__(self, k_pages, v_pages, table):
@@ -189,7 +190,7 @@ class PagedKV:
             self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
             torch.cuda.current_stream().synchronize()   # zero before any stream uses it
         self._t = _paged_torch()
-        self._cache = self._t.cache(C.addressof(c), self.status.data_ptr(), k_pages.get_device())
+        self._cache = self._t.cache(C.addressof(c), self.status.data_ptr(), k_pages.get_device(), k_pages, v_pages)
 
     def _on(self, stream):
         if stream.device != self.device:

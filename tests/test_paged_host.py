@@ -158,3 +158,27 @@ def test_the_torch_side_refuses_to_lose_a_gradient():
         t.append(c, x, q, lens, lens, x, x, None, None, None, 1e-6, None)
     with torch.no_grad(), pytest.raises(ValueError, match="q must be on cuda:0, not cpu"):
         t.decode(c, q, lens, None, 0, 0, None, None, None, False, None)
+
+
+def test_the_torch_side_refuses_pages_whose_gradient_would_be_lost():
+    import torch
+    from gqa_transformer_decode_gb300 import runtime
+    t = runtime._paged_torch()
+    k, v = (torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16) for _ in range(2))
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    x = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="v_pages requires a gradient"):
+        t.cache(C.addressof(cache()), A, 0, k, v.clone().requires_grad_())
+    c = t.cache(C.addressof(cache()), A, 0, k, v)
+    calls = [lambda: t.decode(c, q, x, None, 0, 0, None, None, None, False, None),
+             lambda: t.prefill(c, q, x, x, None, 0, 0, None, None, None, False),
+             lambda: t.append(c, q, q, x, x, q, q, None, None, None, 1e-6, None)]
+    for call in calls:
+        with pytest.raises(ValueError, match="must be on cuda:0, not cpu"):
+            call()
+    k.requires_grad_()                       # asked for after the cache was made
+    for call in calls:
+        with pytest.raises(ValueError, match="k_pages requires a gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="must be on cuda:0, not cpu"):
+            call()
