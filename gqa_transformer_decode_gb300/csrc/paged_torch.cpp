@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -60,6 +61,8 @@ std::string describe(const Tensor& t) {
 void no_gradient(const Tensor& t, const char* what) {   // it would be lost without a word
     if (t.requires_grad() && c10::GradMode::is_enabled())
         bad(std::string(what) + " requires a gradient, which the paged operators do not have (torch.no_grad() to go without)");
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+        bad(std::string(what) + " has a forward-mode tangent, which the paged operators do not carry on");
 }
 const Tensor& tensor(PyObject* o, const char* what) {
     if (!THPVariable_Check(o)) throw Bad{PyExc_TypeError, std::string(what) + " must be a tensor"};

@@ -161,7 +161,7 @@ class PagedKV:
     allocated on that stream, and hold anything in the rows that the call does
     not write (padding, rows outside every sequence).  The operators have no
     gradient: a tensor that requires one, the pages among them, is refused
-    unless gradients are off.
+    unless gradients are off, and so is one with a forward-mode tangent.
     """
 
     def __init__(self, k_pages, v_pages, table):

@@ -182,3 +182,33 @@ def test_the_torch_side_refuses_pages_whose_gradient_would_be_lost():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="must be on cuda:0, not cpu"):
             call()
+
+
+def test_the_torch_side_refuses_to_lose_a_forward_mode_tangent():
+    import torch
+    import torch.autograd.forward_ad as fw
+    from gqa_transformer_decode_gb300 import runtime
+    t = runtime._paged_torch()
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    x = torch.zeros(1, dtype=torch.int32)
+    pages = torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16)
+    _, c = torch_side()
+    with fw.dual_level():
+        d = fw.make_dual(q, torch.ones_like(q))
+        with pytest.raises(ValueError, match="q has a forward-mode tangent"):
+            t.decode(c, d, x, None, 0, 0, None, None, None, False, None)
+        with pytest.raises(ValueError, match="q has a forward-mode tangent"):
+            t.prefill(c, d * 2, x, x, None, 0, 0, None, None, None, False)
+        with pytest.raises(ValueError, match="v has a forward-mode tangent"):
+            t.append(c, q, d, x, x, q, q, None, None, None, 1e-6, None)
+        with pytest.raises(ValueError, match="k_pages has a forward-mode tangent"):
+            t.cache(C.addressof(cache()), A, 0, fw.make_dual(pages, pages + 1), pages)
+    with pytest.raises(ValueError, match="q must be on cuda:0, not cpu"):      # outside there is none
+        t.decode(c, q, x, None, 0, 0, None, None, None, False, None)
+
+    def through(x):                                                            # torch.func's own tensors
+        return t.decode(c, x, torch.zeros(1, dtype=torch.int32), None, 0, 0, None, None, None, False, None)
+    with pytest.raises((ValueError, RuntimeError)):
+        torch.func.jvp(through, (q,), (torch.ones_like(q),))
+    with pytest.raises((ValueError, RuntimeError)):
+        torch.func.vmap(through)(q[None])
