@@ -1,4 +1,4 @@
-"""Plain 64-bit restatement of the paged-cache operators (numpy), for the parity
+"""Plain 64-bit restatement of the paged-cache operators (numpy; attend_all: torch), for the parity
 tests: which keys a query sees, attention over a sequence's pages, and the
 append step (per-head RMS norm, rotate-half RoPE).  Shares nothing with the
 CUDA library.
@@ -10,6 +10,7 @@ norm before RoPE); ember internals, softmax.
 from __future__ import annotations
 
 import numpy as np
+import torch
 
 
 def visible(pos: int, n_keys: int, window: int = 0, sinks: int = 0) -> np.ndarray:
@@ -58,6 +59,41 @@ def attend(q, k_pages, v_pages, table_row, length, pos, window=0, sinks=0, scale
             lse[i, h] = m + np.log(total)
             out[i, h] = p @ vv[live] / total
             mean[i, h] = p @ np.abs(vv[live]) / total
+    return out, lse, mean, big
+
+
+def attend_all(q, k, v, pos, window=0, sinks=0, scale=None):
+    """The same for many rows at once, on torch f64 tensors of any device and with the
+    sequence's keys gathered: q [n, NH, D], k, v [length, NKV, D], pos [n].  Returns out,
+    lse, sum_j p_j |v_j| and, per row and head, the largest sum |q k| |scale| over the
+    keys that count."""
+    n, NH, D = q.shape
+    G = NH // k.shape[1]
+    scale = D ** -0.5 if scale is None else float(np.float32(scale))
+    key = torch.arange(k.shape[0], device=q.device)[None]
+    at = pos[:, None]
+    hidden = key > at
+    if window > 0:
+        hidden |= (key <= at - window) & (key >= sinks)
+    out, mean = torch.zeros_like(q), torch.zeros_like(q)
+    lse = torch.full((n, NH), -torch.inf, dtype=q.dtype, device=q.device)
+    big = torch.zeros_like(lse)
+    for h in range(NH):
+        kk, vv = k[:, h // G], v[:, h // G]
+        s = (q[:, h] @ kk.T * scale).masked_fill(hidden, -torch.inf)
+        live = s > -torch.inf                        # hidden, or without weight
+        m = s.amax(-1, keepdim=True).clamp(min=-1e300) if k.shape[0] else s.new_zeros(n, 1)
+        p = torch.where(live, (s - m).exp(), 0.0)
+        total = p.sum(-1, keepdim=True)
+        some = total > 0
+        p = p / torch.where(some, total, 1.0)
+        used = live.any(0)                           # what no row sees may hold anything
+        vv = torch.where(used[:, None], vv, 0.0)
+        out[:, h], mean[:, h] = p @ vv, p @ vv.abs()
+        lse[:, h] = torch.where(some, m + torch.where(some, total, 1.0).log(), -torch.inf)[:, 0]
+        if k.shape[0]:
+            size = q[:, h].abs() @ torch.where(used[:, None], kk, 0.0).abs().T * abs(scale)
+            big[:, h] = torch.where(live, size, 0.0).amax(-1)
     return out, lse, mean, big
 
 

@@ -60,3 +60,23 @@ def test_norm_and_rotation():
     y = O.norm_rope(x, w, 1e-6, np.ones((4, 5)), np.zeros((4, 5)))
     want = torch.nn.functional.rms_norm(torch.from_numpy(x), (10,), torch.from_numpy(w), 1e-6)
     np.testing.assert_allclose(y, want.numpy(), atol=1e-12)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (5, 3), (1, 0), (20, 60)])
+def test_all_rows_at_once_equals_row_by_row(window, sinks):
+    rng = np.random.default_rng(5)
+    NH, NKV, D, P, length = 6, 2, 16, 16, 50
+    k, v = pool(rng, 9, NKV, P, D)
+    table = np.array([7, 2, 5, 0, -1])
+    k[2, 0, 3] = -np.inf                      # scores of -inf and +inf from head 0's keys
+    q = rng.standard_normal((9, NH, D))
+    q[:, :3] = np.abs(q[:, :3])
+    pos = np.arange(-2, length, 6)
+    want = O.attend(q, k, v, table, length, pos, window, sinks)
+    kk, vv = (torch.from_numpy(O.gather(x, table, np.arange(length))) for x in (k, v))
+    got = O.attend_all(torch.from_numpy(q), kk, vv, torch.from_numpy(pos), window, sinks)
+    for a, b in zip(got[:3], want[:3]):
+        np.testing.assert_allclose(a.numpy(), b, rtol=0, atol=1e-12)
+    assert abs(got[3].max().item() - want[3]) < 1e-12 and (got[3][:1] == 0).all()
+    empty = O.attend_all(torch.from_numpy(q), kk[:0], vv[:0], torch.from_numpy(pos))
+    assert (empty[0] == 0).all() and torch.isneginf(empty[1]).all()
