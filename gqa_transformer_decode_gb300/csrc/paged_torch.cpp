@@ -140,6 +140,12 @@ void check(ember_status st, const char* where) {
     throw python_error();
 }
 
+// A tensor of the caller's that a kernel writes: autograd notices if an earlier
+// operation saved it.
+void written(const Tensor& t) {
+    if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 Cache& cache_of(PyObject* o) {
     auto* c = static_cast<Cache*>(PyCapsule_GetPointer(o, "ember.paged"));
     if (!c) throw python_error();
@@ -239,10 +245,14 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         } else if (given(a[11])) {
             bad("q_out without q");
         }
-        if (n > 0)
+        if (n > 0) {
             check(f_append(&c.kv, qr.p, kr.p, vr.p, src, qr.ld, kr.ld, vr.ld, count(n, "k"), count(heads, "q"), seqs, pos,
                            qn, kn, (float)eps, cp, sp, count(n_pos, "cos"), orow.p, orow.ld, c.status, stream_of(c)),
                   "ember_paged_append");
+            written(c.k_pages);
+            written(c.v_pages);
+            written(q_out);
+        }
         if (!q_out.defined()) Py_RETURN_NONE;
         return THPVariable_Wrap(q_out);
     });
@@ -286,6 +296,8 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
             check(f_decode(&c.kv, qr.p, qr.ld, count(B, "q"), count(heads, "q"), seqs, lens, window, sinks, (float)scale, o.r.p,
                            o.r.ld, o.lse_p, wp, bytes, c.status, stream_of(c)),
                   "ember_paged_decode");
+            written(o.out);
+            written(o.lse);
         }
         return answer(o);
     });
@@ -305,10 +317,13 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         const double scale = given(a[7]) ? real(a[7]) : 1.0 / std::sqrt((double)c.kv.head_dim);
         const c10::cuda::OptionalCUDAGuard on(c10::Device(at::kCUDA, c.device));
         Outputs o = outputs(c, n, heads, a[8], a[9], truth(a[10]));
-        if (n > 0 && B > 0)
+        if (n > 0 && B > 0) {
             check(f_prefill(&c.kv, qr.p, qr.ld, count(n, "q"), count(B, "lens"), count(heads, "q"), seqs, cu, lens, window, sinks,
                             (float)scale, o.r.p, o.r.ld, o.lse_p, c.status, stream_of(c)),
                   "ember_paged_prefill");
+            written(o.out);
+            written(o.lse);
+        }
         return answer(o);
     });
 }

@@ -1,0 +1,75 @@
+"""What runtime.PagedKV owes torch: version counters of what it writes, gradients refused, streams and
+the status word."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Small:
+    """One sequence of up to 64 keys on four pages; 2 kv heads, 4 query heads of 64."""
+
+    def __init__(self):
+        from gqa_transformer_decode_gb300 import runtime
+        self.k, self.v = (torch.randn(6, 2, 16, 64, device="cuda").bfloat16() for _ in range(2))
+        self.table = ints(3, 1, 0, 5)[None].contiguous()
+        self.cache = runtime.PagedKV(self.k, self.v, self.table)
+        self.cos, self.sin = torch.ones(64, 32, device="cuda"), torch.zeros(64, 32, device="cuda")
+        self.q = torch.randn(3, 4, 64, device="cuda").bfloat16()
+        self.x = torch.randn(3, 2, 64, device="cuda").bfloat16()
+
+    def append(self, **kw):
+        return self.cache.append(self.x, self.x, ints(0, 0, 0), ints(40, 41, 42), self.cos, self.sin, **kw)
+
+
+def test_writes_raise_the_version_counters():
+    s = Small()
+    versions = lambda *ts: [t._version for t in ts]  # noqa: E731
+    before = versions(s.k, s.v, s.q, s.x, s.table)
+    s.append()
+    assert versions(s.k, s.v, s.q, s.x, s.table) == [before[0] + 1, before[1] + 1, *before[2:]]
+    buf, lse = torch.zeros(3, 8, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, 4, device="cuda")
+    at = versions(buf, lse)
+    s.append(q=s.q, q_out=buf[:, 2:6])                   # a view counts with its base
+    s.cache.prefill(s.q, ints(0, 3), ints(43), out=buf[:, :4], lse=lse)
+    s.cache.decode(s.q[:1], ints(43), out=buf[:1, 4:], lse=lse[:1])
+    assert versions(buf, lse) == [at[0] + 3, at[1] + 2]
+    at = versions(s.k, buf)
+    s.cache.prefill(s.q[:0], ints(0), ints(), out=buf[:0, :4])   # nothing to do, nothing written
+    assert versions(s.k, buf) == at
+
+
+def test_autograd_notices_that_a_saved_tensor_was_overwritten():
+    s = Small()
+    w = torch.ones_like(s.k).requires_grad_()
+    y = (w * s.k).sum()                                  # saves the pages for w's gradient
+    s.append()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+
+
+def test_inference_tensors_are_written_too():
+    with torch.inference_mode():
+        s = Small()
+        out = torch.empty(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+        s.append(q=s.q, q_out=out)
+    assert torch.equal(out, s.q)
+    s.cache.prefill(s.q, ints(0, 3), ints(43), out=out)  # outside the mode as well
+    assert torch.equal(out, s.cache.prefill(s.q, ints(0, 3), ints(43)))
+
+
+def test_pages_that_require_a_gradient_are_refused():
+    from gqa_transformer_decode_gb300 import runtime
+    s = Small()
+    with pytest.raises(ValueError, match="k_pages requires a gradient"):
+        runtime.PagedKV(s.k.clone().requires_grad_(), s.v, s.table)
+    want = s.cache.decode(s.q[:1], ints(43))
+    s.v.requires_grad_()
+    with pytest.raises(ValueError, match="v_pages requires a gradient"):
+        s.cache.decode(s.q[:1], ints(43))
+    with torch.no_grad():
+        assert torch.equal(want, s.cache.decode(s.q[:1], ints(43)))
