@@ -2,6 +2,7 @@
 // argument checks before any device work, then one or two launches.
 #include <atomic>
 
+#include "common.cuh"
 #include "kernels.h"
 
 using namespace ember;
@@ -22,6 +23,11 @@ cudaError_t device_sms(int* sms) {
     e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess && dev < PG_MAX_DEVICES) known[dev].store(*sms, std::memory_order_relaxed);
     return e;
+}
+
+__global__ void k_take_status(int* status, int* taken) {
+    pdl_wait();
+    *taken = atomicExch(status, 0);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -241,6 +247,14 @@ ember_status ember_paged_prefill(const ember_paged_kv* kv, const void* q, int64_
     if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "no device: %s", cudaGetErrorString(e));
     e = launch_paged_prefill(a, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "prefill launch failed: %s", cudaGetErrorString(e));
+    return EMBER_OK;
+}
+
+ember_status ember_paged_take_status(int32_t* status, int32_t* taken, ember_stream_t stream) {
+    if (!status || !taken || (reinterpret_cast<uintptr_t>(status) & 3) || (reinterpret_cast<uintptr_t>(taken) & 3))
+        PG_FAIL(EMBER_ERR_INVALID_ARG, "status and taken must be given and 4-byte aligned");
+    const cudaError_t e = launch_k(k_take_status, dim3(1), dim3(1), 0, (cudaStream_t)stream, status, taken);
+    if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "status launch failed: %s", cudaGetErrorString(e));
     return EMBER_OK;
 }
 

@@ -112,6 +112,7 @@ def load():
                                     C.c_float, P, C.c_int64, P, P, C.c_size_t, P, P]),
         "ember_paged_prefill": (st, [P, P, C.c_int64, C.c_int32, C.c_int32, C.c_int32, P, P, P, C.c_int32,
                                      C.c_int32, C.c_float, P, C.c_int64, P, P, P]),
+        "ember_paged_take_status": (st, [P, P, P]),
         "ember_prefill_activations": (st, [P, P, C.c_int32, P, C.c_int32, C.c_int32, P, P, P, P]),
         "ember_mean_pooled_head": (st, [P, C.c_int32, C.c_int32, C.c_int32, P, P, C.c_int32, P, P]),
         "ember_test_bounded_wait": (st, [P, C.c_int32, C.c_int64, P]),
@@ -284,6 +285,10 @@ def ember_paged_prefill(kv, q, ld_q, n, B, n_heads, seqs, cu, lens, window, sink
                         status, stream):
     return load().ember_paged_prefill(kv, q, ld_q, n, B, n_heads, seqs, cu, lens, window, sinks, scale, out,
                                       ld_out, lse, status, stream)
+
+
+def ember_paged_take_status(status, taken, stream):
+    return load().ember_paged_take_status(status, taken, stream)
 
 
 def ember_kernel_launches() -> int:

@@ -238,13 +238,13 @@ class PagedKV:
         return self._t.workspace_bytes(self._cache, B, n_heads)
 
     def sync_status(self, stream=None) -> int:
-        """Wait for the stream, return and clear the first device-side error (0: none)."""
-        (torch.cuda.current_stream(self.device) if stream is None else stream).synchronize()
-        st = int(self.status.item())
-        if st:
-            self.status.zero_()
-            torch.cuda.synchronize(self.device)
-        return st
+        """Wait for the stream, return and clear the first device-side error (0: none).  What calls on
+        other streams raise meanwhile is returned now or by the next sync_status, never lost."""
+        stream = torch.cuda.current_stream(self.device) if stream is None else stream
+        with self._on(stream):
+            taken = torch.empty(1, dtype=torch.int32, device=self.device)
+            E.check(E.ember_paged_take_status(_ptr(self.status), _ptr(taken), _stream_ptr(stream)), "ember_paged_take_status")
+            return int(taken.item())
 
 
 _PAGE_DTYPES = {torch.bfloat16: E.BF16, torch.float16: E.F16}

@@ -402,6 +402,12 @@ ember_status ember_paged_prefill(const ember_paged_kv *kv, const void *q, int64_
                                  int32_t sinks, float scale, void *out, int64_t ld_out, float *lse,
                                  int32_t *status, ember_stream_t stream);
 
+/* Takes the status word of the operators above: *taken = *status and *status = 0
+ * (device int32s) in one atomic step on the stream, so that an error which a call on
+ * another stream raises meanwhile is either taken or kept for the next time.
+ * Host errors: INVALID_ARG (NULL or not 4-byte aligned), CUDA. */
+ember_status ember_paged_take_status(int32_t *status, int32_t *taken, ember_stream_t stream);
+
 /* ---- kernel-level entry points used by the parity tests ------------------ */
 
 /* The RoPE-and-store step of the K cache write, alone: for each of n_tok rows

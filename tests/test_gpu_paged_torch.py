@@ -73,3 +73,60 @@ def test_pages_that_require_a_gradient_are_refused():
         s.cache.decode(s.q[:1], ints(43))
     with torch.no_grad():
         assert torch.equal(want, s.cache.decode(s.q[:1], ints(43)))
+
+
+def test_an_error_raised_while_the_status_is_read_is_kept():
+    s = Small()
+    word = s.cache.status
+
+    class Raised:
+        """The status word; as soon as the host has read it, a call on another stream raises 2 (a length beyond
+        the table's)."""
+
+        def data_ptr(self):
+            return word.data_ptr()
+
+        def item(self):
+            got = word.item()
+            s.cache.decode(s.q[:1], ints(65))
+            torch.cuda.synchronize()
+            return got
+
+        def zero_(self):
+            word.zero_()
+
+    s.cache.decode(s.q[:1], ints(43), seqs=ints(9))      # raises 1
+    s.cache.status = Raised()
+    got = [s.cache.sync_status()]
+    if word.item() == 0:                                 # (where the word is taken on the device)
+        s.cache.decode(s.q[:1], ints(65))
+    s.cache.status = word
+    got.append(s.cache.sync_status())
+    assert got == [1, 2] and s.cache.sync_status() == 0
+
+
+def test_no_error_is_lost_between_streams():
+    """One stream raises an error again and again while another takes the word: whatever it takes is 0 or that
+    error, and the last one is still there at the end."""
+    s = Small()
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    bad, n = ints(65), ints(43)
+    with torch.cuda.stream(other):
+        for _ in range(300):
+            s.cache.decode(s.q[:1], bad)
+    got = [s.cache.sync_status() for _ in range(30)]
+    assert set(got) <= {0, 2}
+    other.synchronize()
+    with torch.cuda.stream(other):
+        s.cache.decode(s.q[:1], bad)
+    assert s.cache.sync_status(other) == 2 and s.cache.sync_status() == 0
+    s.cache.decode(s.q[:1], n)
+    assert s.cache.sync_status() == 0
+
+
+def test_the_status_of_a_cache_made_in_inference_mode():
+    with torch.inference_mode():
+        s = Small()
+    s.cache.decode(s.q[:1], ints(65))
+    assert s.cache.sync_status() == 2 and s.cache.sync_status() == 0

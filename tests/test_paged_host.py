@@ -212,3 +212,9 @@ def test_the_torch_side_refuses_to_lose_a_forward_mode_tangent():
         torch.func.jvp(through, (q,), (torch.ones_like(q),))
     with pytest.raises((ValueError, RuntimeError)):
         torch.func.vmap(through)(q[None])
+
+
+def test_the_status_word_is_taken_from_valid_pointers_only():
+    f = E.ember_paged_take_status
+    for a, b in ((None, A), (A, None), (A + 2, A), (A, A + 1)):
+        assert f(a, b, None) == INVALID and "4-byte" in E.last_error()
