@@ -78,6 +78,7 @@ def test_pages_that_require_a_gradient_are_refused():
 def test_an_error_raised_while_the_status_is_read_is_kept():
     s = Small()
     word = s.cache.status
+    raised = []
 
     class Raised:
         """The status word; as soon as the host has read it, a call on another stream raises 2 (a length beyond
@@ -89,6 +90,7 @@ def test_an_error_raised_while_the_status_is_read_is_kept():
         def item(self):
             got = word.item()
             s.cache.decode(s.q[:1], ints(65))
+            raised.append(2)
             torch.cuda.synchronize()
             return got
 
@@ -98,7 +100,7 @@ def test_an_error_raised_while_the_status_is_read_is_kept():
     s.cache.decode(s.q[:1], ints(43), seqs=ints(9))      # raises 1
     s.cache.status = Raised()
     got = [s.cache.sync_status()]
-    if word.item() == 0:                                 # (where the word is taken on the device)
+    if not raised:                                       # (where the word is taken on the device)
         s.cache.decode(s.q[:1], ints(65))
     s.cache.status = word
     got.append(s.cache.sync_status())
@@ -130,3 +132,47 @@ def test_the_status_of_a_cache_made_in_inference_mode():
         s = Small()
     s.cache.decode(s.q[:1], ints(65))
     assert s.cache.sync_status() == 2 and s.cache.sync_status() == 0
+
+
+def busy(stream):
+    """Work on the stream that outlasts the host's next calls."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(200_000_000)                   # a tenth of a second
+
+
+@pytest.mark.parametrize("op", ["decode", "prefill", "append"])
+def test_inputs_freed_after_a_call_on_another_stream_are_kept_for_it(op):
+    s = Small()
+    other = torch.cuda.Stream()
+    side = lambda *a, **k: getattr(s.cache, op)(*a, stream=other, **k)  # noqa: E731
+    n = {"decode": 1}.get(op, 3)
+    lens, cu, seqs, pos = ints(43), ints(0, 3), ints(0, 0, 0), ints(40, 41, 42)
+    call = {"decode": lambda q: side(q, lens), "prefill": lambda q: side(q, cu, lens),
+            "append": lambda q: side(s.x, s.x, seqs, pos, s.cos, s.sin, q=q)}[op]
+    data = torch.randn(n, 4, 64, device="cuda").bfloat16()
+    q = data.clone()
+    at = q.data_ptr()
+    other.wait_stream(torch.cuda.current_stream())
+    want = call(q).clone()
+    torch.cuda.synchronize()
+    busy(other)
+    got = call(q)
+    del q
+    new = [torch.full((n, 4, 64), 100.0, device="cuda").bfloat16() for _ in range(4)]   # into memory that is free
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all(t.data_ptr() != at for t in new)
+
+
+def test_the_status_word_outlives_its_cache_while_a_stream_may_raise_an_error():
+    s = Small()
+    at = s.cache.status.data_ptr()
+    k, v, table, q, bad = s.k, s.v, s.table, s.q[:1], ints(65)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    busy(other)
+    with torch.cuda.stream(other):
+        s.cache.decode(q, bad)
+    s.cache = None
+    words = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(64)]
+    torch.cuda.synchronize()
+    assert all(int(w) == 0 and w.data_ptr() != at for w in words) and k.is_cuda and v.is_cuda and table.is_cuda
