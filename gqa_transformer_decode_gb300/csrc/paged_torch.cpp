@@ -11,6 +11,7 @@
 #include <ATen/ATen.h>
 #include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -39,7 +40,8 @@ struct Cache {
     int32_t* status;
     c10::DeviceIndex device;
     at::ScalarType dtype;
-    Tensor k_pages, v_pages;
+    Tensor k_pages, v_pages, status_word;
+    ember_stream_t home = nullptr;   // the stream that status_word was allocated on
     // decode's workspace of the last (B, heads): the query is a function of these
     int64_t ws_rows = -1, ws_heads = -1;
     size_t ws_bytes = 0;
@@ -203,8 +205,14 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
     }
     END_HANDLE_TH_ERRORS
 }
+// The call's stream.  A kernel on another one than status_word's may still raise an
+// error when the cache is gone: the allocator keeps the word until then.
 ember_stream_t stream_of(const Cache& c) {
-    return reinterpret_cast<ember_stream_t>(c10::cuda::getCurrentCUDAStream(c.device).stream());
+    const c10::cuda::CUDAStream s = c10::cuda::getCurrentCUDAStream(c.device);
+    auto* p = reinterpret_cast<ember_stream_t>(s.stream());
+    if (c.status_word.defined() && p != c.home)
+        c10::cuda::CUDACachingAllocator::recordStream(c.status_word.storage().data_ptr(), s);
+    return p;
 }
 
 // append(cache, k, v, seqs, positions, cos, sin, q, q_norm, k_norm, eps, q_out)
@@ -337,18 +345,21 @@ PyObject* workspace_bytes(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     });
 }
 
-// cache(address of an ember_paged_kv, address of the status word, device index[, k_pages, v_pages])
+// cache(address of an ember_paged_kv, address of the status word, device index[, k_pages, v_pages[, status word]])
 PyObject* cache(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-    return guarded(nargs, nargs == 5 ? 5 : 3, [&]() -> PyObject* {
-        Tensor k_pages, v_pages;
-        if (nargs == 5) k_pages = tensor(a[3], "k_pages"), v_pages = tensor(a[4], "v_pages");
+    return guarded(nargs, nargs == 5 || nargs == 6 ? nargs : 3, [&]() -> PyObject* {
+        Tensor k_pages, v_pages, status_word;
+        if (nargs >= 5) k_pages = tensor(a[3], "k_pages"), v_pages = tensor(a[4], "v_pages");
+        if (nargs == 6) status_word = tensor(a[5], "status");
         auto* c = new Cache;
         c->k_pages = k_pages;
         c->v_pages = v_pages;
+        c->status_word = status_word;
         c->kv = *static_cast<const ember_paged_kv*>(PyLong_AsVoidPtr(a[0]));
         c->status = static_cast<int32_t*>(PyLong_AsVoidPtr(a[1]));
         c->device = (c10::DeviceIndex)PyLong_AsLong(a[2]);
         c->dtype = c->kv.dtype == EMBER_BF16 ? at::kBFloat16 : at::kHalf;
+        if (status_word.defined()) c->home = reinterpret_cast<ember_stream_t>(c10::cuda::getCurrentCUDAStream(c->device).stream());
         return PyCapsule_New(c, "ember.paged", [](PyObject* o) { delete static_cast<Cache*>(PyCapsule_GetPointer(o, "ember.paged")); });
     });
 }

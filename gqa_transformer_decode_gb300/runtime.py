@@ -157,10 +157,13 @@ class PagedKV:
     The tensors stay the caller's and may change between calls; the object
     keeps references and one int32 status word.  Calls are asynchronous on
     `stream` (default: the current stream of the pages' device); device-side
-    errors are read with sync_status().  Tensors that a call allocates are
-    allocated on that stream, and hold anything in the rows that the call does
-    not write (padding, rows outside every sequence).  The operators have no
-    gradient: a tensor that requires one, the pages among them, is refused
+    errors are read with sync_status().  A stream that is passed does not wait
+    for the current one: the caller orders it after whatever made the inputs
+    (wait_stream); the call keeps their memory, freed or not, until the stream is
+    done with it.  (A stream made current instead has torch's own rules:
+    record_stream is the caller's.)  Tensors that a call allocates are allocated
+    on the call's stream, and hold anything in the rows that the call does not
+    write (padding, rows outside every sequence).  The operators have no gradient: a tensor that requires one, the pages among them, is refused
     unless gradients are off, and so is one with a forward-mode tangent.
     """
 
@@ -190,12 +193,22 @@ class PagedKV:
             self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
             torch.cuda.current_stream().synchronize()   # zero before any stream uses it
         self._t = _paged_torch()
-        self._cache = self._t.cache(C.addressof(c), self.status.data_ptr(), k_pages.get_device(), k_pages, v_pages)
+        self._cache = self._t.cache(C.addressof(c), self.status.data_ptr(), k_pages.get_device(), k_pages, v_pages,
+                                    self.status)
 
     def _on(self, stream):
         if stream.device != self.device:
             raise ValueError(f"the stream belongs to {stream.device}, the cache to {self.device}")
         return torch.cuda.stream(stream)
+
+    def _call(self, stream, f, *args):
+        """f on another stream: what it reads and writes stays allocated until it has run there."""
+        with self._on(stream):
+            r = f(*args)
+        for t in (*args, self.k_pages, self.v_pages, self.table):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+        return r
 
     # -- operators ------------------------------------------------------------
     def append(self, k, v, seqs, positions, cos, sin, q=None, q_norm=None, k_norm=None, eps=1e-6, q_out=None,
@@ -207,8 +220,7 @@ class PagedKV:
         [n_pos, head_dim / 2]; q_norm, k_norm bf16 [head_dim].  Returns the
         rotated queries in the cache's type (q_out where given), or None."""
         if stream is not None:
-            with self._on(stream):
-                return self.append(k, v, seqs, positions, cos, sin, q, q_norm, k_norm, eps, q_out)
+            return self._call(stream, self.append, k, v, seqs, positions, cos, sin, q, q_norm, k_norm, eps, q_out)
         return self._t.append(self._cache, k, v, seqs, positions, cos, sin, q, q_norm, k_norm, eps, q_out)
 
     def decode(self, q, lens, seqs=None, window=0, sinks=0, scale=None, out=None, lse=None, return_lse=False,
@@ -219,8 +231,7 @@ class PagedKV:
         Returns out, or (out, lse) with return_lse or lse.  workspace: a uint8
         tensor of at least workspace_bytes(B, n_heads) (default: allocated)."""
         if stream is not None:
-            with self._on(stream):
-                return self.decode(q, lens, seqs, window, sinks, scale, out, lse, return_lse, workspace)
+            return self._call(stream, self.decode, q, lens, seqs, window, sinks, scale, out, lse, return_lse, workspace)
         return self._t.decode(self._cache, q, lens, seqs, window, sinks, scale, out, lse, return_lse, workspace)
 
     def prefill(self, q, cu, lens, seqs=None, window=0, sinks=0, scale=None, out=None, lse=None, return_lse=False,
@@ -229,8 +240,7 @@ class PagedKV:
         of q [n, n_heads, head_dim] are the last positions of sequence b (or
         seqs[b]), which holds lens[b] keys.  cu int32 [B + 1], lens int32 [B]."""
         if stream is not None:
-            with self._on(stream):
-                return self.prefill(q, cu, lens, seqs, window, sinks, scale, out, lse, return_lse)
+            return self._call(stream, self.prefill, q, cu, lens, seqs, window, sinks, scale, out, lse, return_lse)
         return self._t.prefill(self._cache, q, cu, lens, seqs, window, sinks, scale, out, lse, return_lse)
 
     def workspace_bytes(self, B: int, n_heads: int) -> int:
