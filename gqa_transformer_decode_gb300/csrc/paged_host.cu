@@ -32,6 +32,13 @@ __global__ void k_take_status(int* status, int* taken) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Index arrays, lse and the status word: loads and atomics of 4 bytes.
+template <class... P>
+ember_status check_words(const char* which, const P*... p) {
+    if (((reinterpret_cast<uintptr_t>(p) | ...) & 3) != 0) PG_FAIL(EMBER_ERR_INVALID_ARG, "%s must be 4-byte aligned", which);
+    return EMBER_OK;
+}
+
 // The checks every operator shares; fills the kernels' view of the cache.
 ember_status check_cache(const ember_paged_kv* kv, PagedView& c) {
     if (!kv) PG_FAIL(EMBER_ERR_INVALID_ARG, "kv is NULL");
@@ -122,6 +129,7 @@ ember_status ember_paged_append(const ember_paged_kv* kv, const void* q, const v
     if (n_pos <= 0) PG_FAIL(EMBER_ERR_INVALID_ARG, "n_pos must be > 0");
     if (n == 0) return EMBER_OK;
     if (!seqs || !positions) PG_FAIL(EMBER_ERR_INVALID_ARG, "seqs or positions is NULL");
+    if ((st = check_words("seqs, positions and status", seqs, positions, status)) != EMBER_OK) return st;
     if (!cos_t || !sin_t || !aligned16(cos_t) || !aligned16(sin_t))
         PG_FAIL(EMBER_ERR_INVALID_ARG, "cos_t and sin_t must be given and 16-byte aligned");
     if (!aligned16(q_norm) || !aligned16(k_norm))
@@ -184,6 +192,7 @@ ember_status ember_paged_decode(const ember_paged_kv* kv, const void* q, int64_t
     if (B == 0) return EMBER_OK;
     if (B > 65535) PG_FAIL(EMBER_ERR_UNSUPPORTED, "B > 65535");
     if (!seqs && B > kv->n_seqs) PG_FAIL(EMBER_ERR_INVALID_ARG, "B > n_seqs without seqs");
+    if ((st = check_words("seqs, lens, lse and status", seqs, lens, lse, status)) != EMBER_OK) return st;
     if (kv->n_kv_heads > 65535 ||
         (double)B * kv->n_kv_heads * ((double)kv->table_width * kv->page_size / 16) > (double)(1 << 30))
         PG_FAIL(EMBER_ERR_UNSUPPORTED, "B * n_kv_heads * table_width * page_size > 2^34");
@@ -227,6 +236,7 @@ ember_status ember_paged_prefill(const ember_paged_kv* kv, const void* q, int64_
     if (!cu) PG_FAIL(EMBER_ERR_INVALID_ARG, "cu is NULL");
     if (B > 65535 || kv->n_kv_heads > 65535) PG_FAIL(EMBER_ERR_UNSUPPORTED, "B > 65535 or n_kv_heads > 65535");
     if (!seqs && B > kv->n_seqs) PG_FAIL(EMBER_ERR_INVALID_ARG, "B > n_seqs without seqs");
+    if ((st = check_words("seqs, cu, lens, lse and status", seqs, cu, lens, lse, status)) != EMBER_OK) return st;
     a.q = static_cast<const uint16_t*>(q);
     a.ld_q = ld_q;
     a.n = n;
@@ -251,8 +261,9 @@ ember_status ember_paged_prefill(const ember_paged_kv* kv, const void* q, int64_
 }
 
 ember_status ember_paged_take_status(int32_t* status, int32_t* taken, ember_stream_t stream) {
-    if (!status || !taken || (reinterpret_cast<uintptr_t>(status) & 3) || (reinterpret_cast<uintptr_t>(taken) & 3))
-        PG_FAIL(EMBER_ERR_INVALID_ARG, "status and taken must be given and 4-byte aligned");
+    if (!status || !taken) PG_FAIL(EMBER_ERR_INVALID_ARG, "status or taken is NULL");
+    const ember_status st = check_words("status and taken", status, taken);
+    if (st != EMBER_OK) return st;
     const cudaError_t e = launch_k(k_take_status, dim3(1), dim3(1), 0, (cudaStream_t)stream, status, taken);
     if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "status launch failed: %s", cudaGetErrorString(e));
     return EMBER_OK;

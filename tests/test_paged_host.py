@@ -216,5 +216,23 @@ def test_the_torch_side_refuses_to_lose_a_forward_mode_tangent():
 
 def test_the_status_word_is_taken_from_valid_pointers_only():
     f = E.ember_paged_take_status
-    for a, b in ((None, A), (A, None), (A + 2, A), (A, A + 1)):
-        assert f(a, b, None) == INVALID and "4-byte" in E.last_error()
+    for a, b, msg in ((None, A, "NULL"), (A, None, "NULL"), (A + 2, A, "4-byte"), (A, A + 1, "4-byte")):
+        assert f(a, b, None) == INVALID and msg in E.last_error()
+
+
+def test_index_arrays_that_are_not_aligned_are_refused():
+    """They would be read by loads, and the status word by atomics, of 4 bytes."""
+    kv = C.byref(cache())
+    for over in (dict(seqs=A + 2), dict(positions=A + 1)):
+        assert append(**over) == INVALID and "4-byte" in E.last_error()
+    for over in (dict(seqs=A + 2), dict(lens=A + 3), dict(lse=A + 2)):
+        assert decode(**over) == INVALID and "4-byte" in E.last_error()
+    for over in (dict(seqs=A + 1), dict(cu=A + 2), dict(lens=A + 2), dict(lse=A + 1)):
+        assert prefill(**over) == INVALID and "4-byte" in E.last_error()
+    bad = A + 2                              # the status word
+    assert E.ember_paged_append(kv, None, A, A, E.F32, 0, 128, 128, 3, 0, A, A, None, None, 1e-6, A, A, 64, None, 0,
+                                bad, None) == INVALID and "4-byte" in E.last_error()
+    assert E.ember_paged_decode(kv, A, 256, 2, 4, None, A, 0, 0, 0.1, A, 256, None, A, 1 << 40, bad, None) == INVALID
+    assert "4-byte" in E.last_error()
+    assert E.ember_paged_prefill(kv, A, 256, 5, 2, 4, None, A, A, 0, 0, 0.1, A, 256, None, bad, None) == INVALID
+    assert "4-byte" in E.last_error()
