@@ -135,6 +135,7 @@ ember_status ember_paged_append(const ember_paged_kv* kv, const void* q, const v
     if (!aligned16(q_norm) || !aligned16(k_norm))
         PG_FAIL(EMBER_ERR_INVALID_ARG, "q_norm and k_norm must be 16-byte aligned");
     const int64_t kvd = (int64_t)kv->n_kv_heads * kv->head_dim;
+    if (kvd > (1 << 20)) PG_FAIL(EMBER_ERR_UNSUPPORTED, "n_kv_heads * head_dim > 2^20");   // (as n_heads with q)
     if ((st = check_rows("k", k, ld_k, kvd)) != EMBER_OK) return st;
     if ((st = check_rows("v", v, ld_v, kvd)) != EMBER_OK) return st;
     if ((q == nullptr) != (q_out == nullptr)) PG_FAIL(EMBER_ERR_INVALID_ARG, "q and q_out go together");

@@ -305,7 +305,9 @@ ember_status ember_sample(const float *logits, int32_t B, int32_t V, int32_t ldl
  *     heads together.  Position i of sequence s lies in page
  *     table[s*table_width + i / page_size], row i % page_size.
  *   - head_dim is 16, 32, 64 or 128; page_size a power of two from 16 to 1024;
- *     n_heads / n_kv_heads at most 16; table_width * page_size at most 2^30.
+ *     n_heads / n_kv_heads at most 16; table_width * page_size at most 2^30;
+ *     n_heads * head_dim (and n_kv_heads * head_dim) at most 2^20; in decode
+ *     B * n_kv_heads * table_width * page_size at most 2^34.
  *   - All element pointers are 16-byte aligned, lse and pointers to int32
  *     4-byte; strides and row lengths (ld_*, in elements) are multiples of 8.
  *     q / out rows hold the heads side by side, head_dim apart.

@@ -236,3 +236,14 @@ def test_index_arrays_that_are_not_aligned_are_refused():
     assert "4-byte" in E.last_error()
     assert E.ember_paged_prefill(kv, A, 256, 5, 2, 4, None, A, A, 0, 0, 0.1, A, 256, None, bad, None) == INVALID
     assert "4-byte" in E.last_error()
+
+
+def test_rows_too_long_for_32_bit_offsets_are_refused():
+    """Without q nothing else bounds the kv heads of a row: 2^25 heads of 64 pass 2^31 elements."""
+    for nkv in (1 << 25, (1 << 31) - 1, (1 << 14) + 1):
+        c = cache(n_kv_heads=nkv)
+        assert append(c, q=None, q_out=None, ld_k=64 * nkv, ld_v=64 * nkv) == UNSUPPORTED and "2^20" in E.last_error()
+    for call in (decode, prefill):
+        assert call(heads=1 << 15, ld_q=1 << 21, ld_out=1 << 21, c=cache(n_kv_heads=1 << 15)) == UNSUPPORTED
+    c = cache(n_kv_heads=1024, head_dim=16, n_seqs=70000, table_width=1 << 20)
+    assert decode(c, B=2048, heads=1024, ld_q=1 << 14, ld_out=1 << 14) == UNSUPPORTED and "2^34" in E.last_error()
