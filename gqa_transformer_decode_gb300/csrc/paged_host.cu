@@ -11,6 +11,13 @@ namespace {
 
 #define PG_FAIL(st, ...) return set_error(st, __VA_ARGS__)
 
+// Answers a CUDA error, and takes it off the thread's record: the next caller that
+// looks there would take it for its own.
+ember_status cuda_failed(const char* what, cudaError_t e) {
+    cudaGetLastError();
+    PG_FAIL(EMBER_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
 constexpr int PG_MAX_DEVICES = 64;
 
 // SMs of the current device (asked once per device).
@@ -166,7 +173,7 @@ ember_status ember_paged_append(const ember_paged_kv* kv, const void* q, const v
     a.ld_out = ld_out;
     a.status = status;
     const cudaError_t e = launch_paged_append(a, (cudaStream_t)stream);
-    if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "append launch failed: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return cuda_failed("append launch failed", e);
     return EMBER_OK;
 }
 
@@ -199,7 +206,7 @@ ember_status ember_paged_decode(const ember_paged_kv* kv, const void* q, int64_t
         PG_FAIL(EMBER_ERR_UNSUPPORTED, "B * n_kv_heads * table_width * page_size > 2^34");
     int sms = 0;
     cudaError_t e = device_sms(&sms);
-    if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "no device: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return cuda_failed("no device", e);
     const size_t need = paged_decode_ws(a.c, B, n_heads, window, sinks, sms);
     if ((need && !workspace) || !aligned16(workspace))
         PG_FAIL(EMBER_ERR_INVALID_ARG, "workspace must be given and 16-byte aligned");
@@ -219,7 +226,7 @@ ember_status ember_paged_decode(const ember_paged_kv* kv, const void* q, int64_t
     a.ws = static_cast<float*>(workspace);
     a.status = status;
     e = launch_paged_decode(a, sms, (cudaStream_t)stream);
-    if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "decode launch failed: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return cuda_failed("decode launch failed", e);
     return EMBER_OK;
 }
 
@@ -255,9 +262,9 @@ ember_status ember_paged_prefill(const ember_paged_kv* kv, const void* q, int64_
     a.status = status;
     int sms = 0;
     cudaError_t e = device_sms(&sms);
-    if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "no device: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return cuda_failed("no device", e);
     e = launch_paged_prefill(a, sms, (cudaStream_t)stream);
-    if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "prefill launch failed: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return cuda_failed("prefill launch failed", e);
     return EMBER_OK;
 }
 
@@ -266,7 +273,7 @@ ember_status ember_paged_take_status(int32_t* status, int32_t* taken, ember_stre
     const ember_status st = check_words("status and taken", status, taken);
     if (st != EMBER_OK) return st;
     const cudaError_t e = launch_k(k_take_status, dim3(1), dim3(1), 0, (cudaStream_t)stream, status, taken);
-    if (e != cudaSuccess) PG_FAIL(EMBER_ERR_CUDA, "status launch failed: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return cuda_failed("status launch failed", e);
     return EMBER_OK;
 }
 

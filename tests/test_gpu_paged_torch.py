@@ -176,3 +176,43 @@ def test_the_status_word_outlives_its_cache_while_a_stream_may_raise_an_error():
     words = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(64)]
     torch.cuda.synchronize()
     assert all(int(w) == 0 and w.data_ptr() != at for w in words) and k.is_cuda and v.is_cuda and table.is_cuda
+
+
+def test_a_launch_that_fails_leaves_no_error_behind():
+    """Launches into a capture that a synchronize has invalidated are refused by the runtime; the next caller's
+    check of the last error does not see it."""
+    import ctypes as C
+    from gqa_transformer_decode_gb300 import ember as E
+    with open("/proc/self/maps") as f:
+        rt = C.CDLL(next(line.split()[-1] for line in f if "libcudart" in line))
+    s = Small()
+    kv = E.ember_paged_kv(k=s.k.data_ptr(), v=s.v.data_ptr(), table=s.table.data_ptr(), dtype=E.BF16, n_pages=6,
+                          page_size=16, n_kv_heads=2, head_dim=64, n_seqs=1, table_width=4, page_stride=2 * 16 * 64,
+                          head_stride=16 * 64, row_stride=64)
+    zeros, lens, cu = ints(0, 0, 0), ints(43), ints(0, 3)
+    out = torch.empty_like(s.q)
+    p = lambda t: C.c_void_p(t.data_ptr())  # noqa: E731
+    torch.cuda.synchronize()
+    stream, graph = C.c_void_p(), C.c_void_p()
+    assert rt.cudaStreamCreate(C.byref(stream)) == 0
+    calls = [
+        lambda: E.ember_paged_append(C.byref(kv), None, p(s.x), p(s.x), E.BF16, 0, 128, 128, 3, 0, p(zeros), p(zeros),
+                                     None, None, 1e-6, p(s.cos), p(s.sin), 64, None, 0, None, stream),
+        lambda: E.ember_paged_decode(C.byref(kv), p(s.q), 256, 1, 4, None, p(lens), 0, 0, 0.1, p(out), 256, None, None,
+                                     0, None, stream),
+        lambda: E.ember_paged_prefill(C.byref(kv), p(s.q), 256, 3, 1, 4, None, p(cu), p(lens), 0, 0, 0.1, p(out), 256,
+                                      None, None, stream),
+        lambda: E.ember_paged_take_status(p(zeros), p(lens), stream)]
+    for call in calls:
+        assert rt.cudaStreamBeginCapture(stream, 2) == 0             # relaxed: only this stream's
+        assert rt.cudaStreamSynchronize(stream) != 0                 # not while it is captured: invalidates it
+        rt.cudaGetLastError()
+        assert call() == 6 and "launch failed" in E.last_error()
+        left = rt.cudaPeekAtLastError()
+        assert rt.cudaStreamEndCapture(stream, C.byref(graph)) != 0
+        rt.cudaGetLastError()
+        assert left == 0
+    assert rt.cudaStreamDestroy(stream) == 0
+    torch.cuda.synchronize()
+    s.cache.decode(s.q[:1], lens)                                    # all as before
+    assert s.cache.sync_status() == 0
