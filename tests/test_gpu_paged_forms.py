@@ -322,13 +322,11 @@ def test_decode_line_and_join_of_large_groups(count, NKV, D, G, dtype):
 
 # ---- weights whose rounding shows ------------------------------------------------------------------------------
 
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("n", [101, 9001])                          # in a cluster; along the line
-def test_decode_weights_keep_both_terms(n, dtype):
-    """Values +1 and -1 in equal numbers whose weights are so close that the sum nearly cancels, but round to
-    different values of the type: with one term a half step of the weight would remain, as large as A u."""
+def nearly_cancelling(n, dtype, wide=1):
+    """A sequence of n keys with values +1 and -1 in equal numbers, whose weights are so close that the sum nearly
+    cancels but round to different values of the type: with one term half a step of the weight would remain, A u / 2."""
     D, u = 16, U[dtype]
-    p = Held(n, [n], 1, D, 16, dtype)
+    p = Held(n, [n], 1, D, 16, dtype, wide=wide)
     k, v = p.keys[0], p.values[0]
     k.zero_()
     v.zero_()
@@ -346,8 +344,25 @@ def test_decode_weights_keep_both_terms(n, dtype):
     p.lay()
     q = torch.zeros(1, 2, D, dtype=DT[dtype], device="cuda")
     q[..., :3] = 1.0
+    return p, q
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [101, 9001])                          # in a cluster; along the line
+def test_decode_weights_keep_both_terms(n, dtype):
+    p, q = nearly_cancelling(n, dtype)
     out, lse = p.cache.decode(q, ints([n]), scale=1.0, return_lse=True)
     p.check(0, q, torch.tensor([n - 1], device="cuda"), out, lse, TWO[dtype], scale=1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n,sign", [(101, 1.0), (120, 1.0), (700, -1.0)])   # short; scale < 0 at any length
+def test_weights_of_warp_product_prefill_keep_both_terms(n, sign, dtype):
+    p, q = nearly_cancelling(n, dtype, wide=0)                       # tables of at most 128 keys: warp products
+    assert sign < 0 or p.table_np.shape[1] * p.P <= 128
+    q *= sign
+    out, lse = p.cache.prefill(q, ints([0, 1]), ints([n]), scale=sign, return_lse=True)
+    p.check(0, q, torch.tensor([n - 1], device="cuda"), out, lse, TWO[dtype], scale=sign)
 
 
 # ---- append: a token's heads in turn -----------------------------------------------------------------------------
