@@ -322,11 +322,18 @@ ember_status ember_sample(const float *logits, int32_t B, int32_t V, int32_t ldl
  *     the keys read as zeros.  Nothing outside the buffers is touched.
  *   - Table entries of pages that hold no visible key are not read, nor are
  *     rows of a page that no query of the call sees: they may hold anything.
- *   - Products are taken on the cache's type and summed in f32, softmax weights
- *     against a maximum that may lag behind the true one by up to 2^15: keys and
- *     values stay below about 1e33 in magnitude (bf16; f16 always does).  A weight's
- *     rounding for the second product is relative, but f16's at least 2^-32 of the
- *     largest weight of its row.
+ *   - Products are taken on the cache's type and summed in f32.  Softmax weights
+ *     are taken against a maximum that may lag behind the true one, so that a
+ *     row's weights sum to at most 2^9 for each of its keys (their number rounded
+ *     up to 64) before the division: bf16 values stay below 3.4e38 / (2^9 (keys +
+ *     63)) in magnitude, 1e32 at 5000 keys, 5e30 at 131072 (f16 always does).  A
+ *     score whose products sum beyond f32 counts as infinite; one below -3e38 /
+ *     log2(e) has no weight.
+ *   - A weight's rounding for the second product: decode, and prefill where tables
+ *     hold at most 128 keys or the scale is not positive, take it as the sum of two
+ *     values of the cache's type (2^-16 relative for bf16, 2^-22 for f16), other
+ *     prefill as one (2^-8, 2^-11: about the output's own rounding); f16's is at
+ *     least 2^-32 of the largest weight of its row.
  *   - B is at most 65535.  No operator has a gradient.
  *   - Buffers and the stream belong to the current device; buffers may not
  *     overlap, except that pages may be shared by the tables of sequences

@@ -301,6 +301,38 @@ def test_prefill_scores_of_minus_infinity(form, D):
     assert (out[:3] == 0).all() and torch.isneginf(lse[:3]).all() and torch.isfinite(lse[3:]).all()
 
 
+@pytest.mark.parametrize("above", [7.96875, 8.9375])                # just no move in decode, in prefill
+@pytest.mark.parametrize("form", [*FORMS, "decode", "decode in a cluster"])
+def test_values_as_large_as_a_lagging_maximum_allows(form, above):
+    """The first 64 keys score `above` (log2) below all others, which moves no maximum: weights of up to 2^9 for each
+    key meet values of 3.4e38 / (2^9 (keys + 63)), and nothing overflows."""
+    new, lens = FORMS.get(form, ([1], [9000 if form == "decode" else 700]))
+    if form in ("several rounds", "keys split"):
+        lens = [n + 4000 for n in lens]
+    NH, NKV, D = (16, 8, 64) if form == "several rounds" else (4, 2, 64)
+    p = Held(7, lens, NKV, D, 16, wide=0 if form == "warp products" else 1)
+    largest = torch.tensor(3.4e38 / (2.0 ** 9 * (max(lens) + 63))).bfloat16()
+    largest = (largest.float() * (1 - 2.0 ** -7)).bfloat16()         # (not above it after its rounding)
+    for k, v in zip(p.keys, p.values):
+        k.zero_()
+        k[64:, :, 0] = above
+        v.fill_(largest.item())
+        v[:, :, 1] *= -1
+    p.lay()
+    cu = cumulated(new)
+    q = torch.zeros(cu[-1], NH, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    scale = float(np.log(2.0))
+    if "decode" in form:
+        assert (p.cache.workspace_bytes(1, NH) > 0) == (form == "decode")
+        out, lse = p.cache.decode(q, ints(lens), scale=scale, return_lse=True)
+        p.check_decode(q, out, lse, scale=scale)
+    else:
+        out, lse = p.cache.prefill(q, ints(cu), ints(lens), scale=scale, return_lse=True)
+        p.check_prefill(q, cu, out, lse, scale=scale)
+    assert p.cache.sync_status() == 0
+
+
 # ---- decode along the line: groups of more than eight heads ---------------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
