@@ -620,7 +620,8 @@ __global__ void __launch_bounds__(PJ_THREADS) k_paged_join(PagedDecodeArgs a, in
     pdl_trigger();
     const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.ws) + blockIdx.x);
     const int b = rec.x, g = rec.y, parts = rec.z, c0 = rec.w >> 1;
-    if (parts == 0) return;
+    // (what another call wrote into a workspace that two share by mistake is not followed out of the buffers)
+    if (parts <= 0 || c0 < 0 || c0 >= grid || parts > grid - c0 || b < 0 || b >= a.B || g < 0 || g >= a.c.NKV) return;
     // partial i: slot 0 of its CTA, but slot 1 of the first when the segment begins inside it
     const float* base = partials(a, grid) + (size_t)h0 * (D + 2);
     const size_t slot = (size_t)G * (D + 2);

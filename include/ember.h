@@ -337,7 +337,8 @@ ember_status ember_sample(const float *logits, int32_t B, int32_t V, int32_t ldl
  *   - B is at most 65535.  No operator has a gradient.
  *   - Buffers and the stream belong to the current device; buffers may not
  *     overlap, except that pages may be shared by the tables of sequences
- *     that only read them. */
+ *     that only read them.  What a call reads is not to be written by others
+ *     until its kernels have ended (page rows that it does not see may be). */
 typedef enum ember_dtype { EMBER_F32 = 0, EMBER_BF16 = 1, EMBER_F16 = 2 } ember_dtype;
 
 typedef struct ember_paged_kv {
@@ -383,7 +384,7 @@ ember_status ember_paged_append(const ember_paged_kv *kv, const void *q, const v
  *   workspace: ember_paged_decode_workspace bytes (which may be 0: then NULL
  *   will do), 16-byte aligned, of any content; used until the call's kernels
  *   end, so calls that may overlap (other streams, graphs that run at once) need
- *   one each.
+ *   one each: sharing it makes their outputs wrong (nothing else is touched).
  * How the keys are split, and with it the rounding, depends on B, the head
  * counts, the window, lens, the table's width and the device; there are no
  * atomics, so equal calls give equal bits.

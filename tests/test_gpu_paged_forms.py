@@ -352,6 +352,29 @@ def test_decode_line_and_join_of_large_groups(count, NKV, D, G, dtype):
     assert torch.equal(out, p.cache.decode(q, ints(lens)))
 
 
+def test_a_workspace_shared_by_mistake_leads_out_of_no_buffer():
+    """Two calls of different sizes at once on one workspace: their rows may be wrong, all else stays as it was."""
+    many, few = Held(1, [int(x) for x in np.random.default_rng(1).integers(2000, 3000, 40)], 2, 64, 64), Held(2, [9001], 1, 64, 64)
+    ws = torch.empty(max(many.cache.workspace_bytes(40, 8), few.cache.workspace_bytes(1, 4)), dtype=torch.uint8, device="cuda")
+    jobs = []
+    for p, NH in ((many, 8), (few, 4)):
+        B = len(p.lens)
+        q, lens = p.normal(B, NH, 64), ints(p.lens)
+        room = torch.full((B + 80, NH, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        jobs.append((p, q, lens, room, room[40:40 + B], stream))
+    for _ in range(200):
+        for p, q, lens, _, out, stream in jobs:
+            p.cache.decode(q, lens, out=out, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for p, q, lens, room, out, _ in jobs:
+        B = len(p.lens)
+        assert (room[:40] == 7).all() and (room[40 + B:] == 7).all() and p.cache.sync_status() == 0
+        out, lse = p.cache.decode(q, lens, workspace=ws, return_lse=True)      # alone: right again
+        p.check_decode(q, out, lse)
+
+
 # ---- weights whose rounding shows ------------------------------------------------------------------------------
 
 def nearly_cancelling(n, dtype, wide=1):
