@@ -60,15 +60,20 @@ std::string describe(const Tensor& t) {
     return s + "] on " + t.device().str();
 }
 
-void no_gradient(const Tensor& t, const char* what) {   // it would be lost without a word
+// A gradient would be lost without a word.  (The modes are thread-local and so asked
+// for last: nearly no tensor here has either.)
+void no_gradient(const Tensor& t, const char* what) {
     if (t.requires_grad() && c10::GradMode::is_enabled())
         bad(std::string(what) + " requires a gradient, which the paged operators do not have (torch.no_grad() to go without)");
-    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+    if (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
         bad(std::string(what) + " has a forward-mode tangent, which the paged operators do not carry on");
 }
-const Tensor& tensor(PyObject* o, const char* what) {
+const Tensor& any_tensor(PyObject* o, const char* what) {
     if (!THPVariable_Check(o)) throw Bad{PyExc_TypeError, std::string(what) + " must be a tensor"};
-    const Tensor& t = THPVariable_Unpack(o);
+    return THPVariable_Unpack(o);
+}
+const Tensor& tensor(PyObject* o, const char* what) {
+    const Tensor& t = any_tensor(o, what);
     no_gradient(t, what);
     return t;
 }
@@ -90,7 +95,7 @@ void* flat(const Cache& c, const Tensor& t, const char* what, at::ScalarType dty
     return t.data_ptr();
 }
 int32_t* ints(const Cache& c, PyObject* o, const char* what, int64_t n) {
-    return static_cast<int32_t*>(flat(c, tensor(o, what), what, at::kInt, {n}));
+    return static_cast<int32_t*>(flat(c, any_tensor(o, what), what, at::kInt, {n}));
 }
 
 // [n, heads, head_dim] whose rows hold the heads side by side.
@@ -163,18 +168,23 @@ struct Outputs {
     Tensor out, lse;
     Rows r;
     float* lse_p = nullptr;
+    bool out_given = false, lse_given = false;
+    void done() const {
+        if (out_given) written(out);
+        if (lse_given) written(lse);
+    }
 };
 Outputs outputs(const Cache& c, int64_t n, int64_t heads, PyObject* out, PyObject* lse, bool want_lse) {
     Outputs o;
     const int64_t D = c.kv.head_dim;
-    if (given(out)) {
+    if ((o.out_given = given(out))) {
         o.out = tensor(out, "out");
         o.r = rows(c, o.out, "out", c.dtype, n, heads);
     } else {
         o.out = make(c, {n, heads, D}, c.dtype);
         o.r = {o.out.data_ptr(), heads * D};
     }
-    if (given(lse)) {
+    if ((o.lse_given = given(lse))) {
         o.lse = tensor(lse, "lse");
         o.lse_p = static_cast<float*>(flat(c, o.lse, "lse", at::kFloat, {n, heads}));
     } else if (want_lse) {
@@ -259,7 +269,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                   "ember_paged_append");
             written(c.k_pages);
             written(c.v_pages);
-            written(q_out);
+            if (given(a[11])) written(q_out);
         }
         if (!q_out.defined()) Py_RETURN_NONE;
         return THPVariable_Wrap(q_out);
@@ -304,8 +314,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
             check(f_decode(&c.kv, qr.p, qr.ld, count(B, "q"), count(heads, "q"), seqs, lens, window, sinks, (float)scale, o.r.p,
                            o.r.ld, o.lse_p, wp, bytes, c.status, stream_of(c)),
                   "ember_paged_decode");
-            written(o.out);
-            written(o.lse);
+            o.done();
         }
         return answer(o);
     });
@@ -329,8 +338,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
             check(f_prefill(&c.kv, qr.p, qr.ld, count(n, "q"), count(B, "lens"), count(heads, "q"), seqs, cu, lens, window, sinks,
                             (float)scale, o.r.p, o.r.ld, o.lse_p, c.status, stream_of(c)),
                   "ember_paged_prefill");
-            written(o.out);
-            written(o.lse);
+            o.done();
         }
         return answer(o);
     });
