@@ -27,10 +27,12 @@
 // start) a warp zeroes the V rows that no row sees, since 0 * NaN from a
 // stale row would not be 0.
 //
-// P is rounded to the cache's type, bf16 by 2^-8 of each weight at most, which in a
-// sum over keys of mixed sign is about the output's own rounding (error against 64
-// bits 0.0022, the bare rounding's 0.0016); l is summed from the unrounded weights
-// in f32.
+// P is rounded once to the cache's type, bf16 by 2^-8 of each weight at most, f16 by
+// 2^-11, which in a sum over keys of mixed sign is about the output's own rounding
+// (error against 64 bits 0.0022 and 0.00029, the bare rounding's 0.0016 and 0.00021).
+// A second term, as decode has it, would be another P V product: at head_dim 128, which
+// the tensor pipe bounds, 512 cycles more on the 1263 of a step.  l is summed from the
+// unrounded weights in f32.
 //
 // CTAs are persistent: one whose last copies are issued asks the hardware to
 // cancel a CTA that has not started yet (clusterlaunchcontrol) and takes over
@@ -53,7 +55,7 @@
 // the weights over (150), one after the other.  The copy and MMA warps' own
 // instructions matter as much as the products: each must pass a tile in less than that.
 // The tensor pipe is active for 65 % of the cycles in the chunks, whose longest tile
-// pairs (94 steps) set the time, 52 % under the window and 27 % in the prompt.
+// pairs (87 key tiles) set the time, 52 % under the window and 27 % in the prompt.
 //
 // Warps 0-3: tile A; warps 4-7: tile B (a warp reads the TMEM lanes of its index
 // mod 4); warp 8: TMA producer; warp 9: TMEM allocation; warps
