@@ -10,6 +10,7 @@ it when runtime.PagedKV is first used, build_all() both at once.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import os
 import shutil
 import subprocess
@@ -87,7 +88,7 @@ def build_ext(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("torch extension failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
-    if os.path.exists(TORCH_EXT + ".torch"):
+    with contextlib.suppress(FileNotFoundError):
         os.remove(TORCH_EXT + ".torch")      # never beside a binary that it does not speak of
     os.replace(tmp, TORCH_EXT)
     with open(tmp, "w") as f:

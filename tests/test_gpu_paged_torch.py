@@ -216,3 +216,22 @@ def test_a_launch_that_fails_leaves_no_error_behind():
     torch.cuda.synchronize()
     s.cache.decode(s.q[:1], lens)                                    # all as before
     assert s.cache.sync_status() == 0
+
+
+def test_a_stream_that_is_being_captured_can_be_passed():
+    s = Small()
+    lens, cu = ints(43), ints(0, 3)
+    want = s.cache.decode(s.q[:1], lens), s.cache.prefill(s.q, cu, lens)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        q = s.q.clone()                                  # of the graph's own memory, gone before its replay
+        got = s.cache.decode(q[:1], lens, stream=side), s.cache.prefill(q, cu, lens, stream=side)
+        del q
+    for t in got:
+        t.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and s.cache.sync_status(side) == 0
