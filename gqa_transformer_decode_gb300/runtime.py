@@ -163,8 +163,9 @@ class PagedKV:
     done with it.  (A stream made current instead has torch's own rules:
     record_stream is the caller's.)  Tensors that a call allocates are allocated
     on the call's stream, and hold anything in the rows that the call does not
-    write (padding, rows outside every sequence).  The operators have no gradient: a tensor that requires one, the pages among them, is refused
-    unless gradients are off, and so is one with a forward-mode tangent.
+    write (padding, rows outside every sequence).  The operators have no
+    gradient: a tensor that requires one, the pages among them, is refused unless
+    gradients are off, and so is one with a forward-mode tangent.
     """
 
     def __init__(self, k_pages, v_pages, table):

@@ -329,11 +329,12 @@ ember_status ember_sample(const float *logits, int32_t B, int32_t V, int32_t ldl
  *     63)) in magnitude, 1e32 at 5000 keys, 5e30 at 131072 (f16 always does).  A
  *     score whose products sum beyond f32 counts as infinite; one below -3e38 /
  *     log2(e) has no weight.
- *   - A weight's rounding for the second product: decode, and prefill where tables
- *     hold at most 128 keys or the scale is not positive, take it as the sum of two
- *     values of the cache's type (2^-16 relative for bf16, 2^-22 for f16), other
- *     prefill as one (2^-8, 2^-11: about the output's own rounding); f16's is at
- *     least 2^-32 of the largest weight of its row.
+ *   - A weight's rounding for the second product: decode, and prefill of short
+ *     sequences (tables of at most 128 keys, at most 64 rows a sequence on average)
+ *     or with a scale that is not positive, take it as the sum of two values of the
+ *     cache's type (2^-16 relative for bf16, 2^-22 for f16), other prefill as one
+ *     (2^-8, 2^-11: about the output's own rounding); f16's is at least 2^-32 of the
+ *     largest weight of its row.
  *   - B is at most 65535.  No operator has a gradient.
  *   - Buffers and the stream belong to the current device; buffers may not
  *     overlap, except that pages may be shared by the tables of sequences
