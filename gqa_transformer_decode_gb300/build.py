@@ -1,11 +1,12 @@
 """Build the CUDA library in-tree: csrc/*.cu -> _build/libember.so (sm_103a), and
-the torch side of the paged-cache operators: csrc/paged_torch.cpp ->
-_build/paged_torch<suffix> (a Python extension against the installed torch).
+the torch sides of the operators: csrc/paged_torch.cpp -> _build/paged_torch<suffix>
+and csrc/rows_torch.cpp -> _build/rows_torch<suffix> (Python extensions against the
+installed torch).
 
 Each translation unit compiles in parallel with nvcc, then one nvcc -shared
 link.  The library needs neither torch nor a host C++ compiler beyond nvcc's, so
-build() leaves the extension alone; build_ext() (g++ and torch's headers) makes
-it when runtime.PagedKV is first used, build_all() both at once.
+build() leaves the extensions alone; build_ext() and build_rows_ext() (g++ and
+torch's headers) make one when it is first used, build_all() all at once.
 """
 from __future__ import annotations
 
@@ -22,7 +23,9 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libember.so")
 TORCH_SRC = os.path.join(CSRC, "paged_torch.cpp")
-TORCH_EXT = os.path.join(OUT, "paged_torch" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+ROWS_SRC = os.path.join(CSRC, "rows_torch.cpp")
+_SUFFIX = sysconfig.get_config_var("EXT_SUFFIX") or ".so"
+TORCH_EXT = os.path.join(OUT, "paged_torch" + _SUFFIX)
 ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 
@@ -60,49 +63,63 @@ def _torch_id() -> str:
     return f"{torch.__version__} {torch.version.git_version} {os.path.dirname(torch.__file__)}"
 
 
-def ext_up_to_date() -> bool:
-    deps = (TORCH_SRC, os.path.join(INCLUDE, "ember.h"))
-    made_for = TORCH_EXT + ".torch"
-    if not os.path.exists(TORCH_EXT) or not os.path.exists(made_for):
+def _ext_up_to_date(src: str, ext: str) -> bool:
+    deps = (src, os.path.join(CSRC, "torch_args.h"), os.path.join(INCLUDE, "ember.h"))
+    made_for = ext + ".torch"
+    if not os.path.exists(ext) or not os.path.exists(made_for):
         return False
     with open(made_for) as f:
         if f.read() != _torch_id():
             return False
-    return all(os.path.getmtime(p) <= os.path.getmtime(TORCH_EXT) for p in deps)
+    return all(os.path.getmtime(p) <= os.path.getmtime(ext) for p in deps)
+
+
+def ext_up_to_date() -> bool:
+    return _ext_up_to_date(TORCH_SRC, TORCH_EXT)
 
 
 def build_ext(force: bool = False) -> str:
-    """Compile the torch extension (marshalling only; every kernel is in libember.so)."""
-    if not force and ext_up_to_date():
-        return TORCH_EXT
+    """Compile the torch extension of the paged-cache operators (marshalling only; every kernel is in libember.so)."""
+    return _build_ext(TORCH_SRC, TORCH_EXT, force)
+
+
+def build_rows_ext(force: bool = False) -> str:
+    """The same for the operators on rows."""
+    return _build_ext(ROWS_SRC, os.path.join(OUT, "rows_torch" + _SUFFIX), force)
+
+
+def _build_ext(src: str, ext: str, force: bool) -> str:
+    if not force and _ext_up_to_date(src, ext):
+        return ext
     import torch
     from torch.utils import cpp_extension as cpp
     os.makedirs(OUT, exist_ok=True)
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     inc = [*cpp.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
-    tmp = TORCH_EXT + f".tmp{os.getpid()}"
+    tmp = ext + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + i for i in inc), TORCH_SRC,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + i for i in inc), src,
            "-o", tmp, "-L" + torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("torch extension failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
     with contextlib.suppress(FileNotFoundError):
-        os.remove(TORCH_EXT + ".torch")      # never beside a binary that it does not speak of
-    os.replace(tmp, TORCH_EXT)
+        os.remove(ext + ".torch")      # never beside a binary that it does not speak of
+    os.replace(tmp, ext)
     with open(tmp, "w") as f:
         f.write(_torch_id())
-    os.replace(tmp, TORCH_EXT + ".torch")
-    return TORCH_EXT
+    os.replace(tmp, ext + ".torch")
+    return ext
 
 
 def build_all(force: bool = False) -> None:
-    """The library and the torch extension, side by side."""
-    with cf.ThreadPoolExecutor(max_workers=1) as ex:
-        ext = ex.submit(build_ext, force)
+    """The library and the torch extensions, side by side."""
+    with cf.ThreadPoolExecutor(max_workers=2) as ex:
+        exts = [ex.submit(build_ext, force), ex.submit(build_rows_ext, force)]
         build(force)
-        ext.result()
+        for e in exts:
+            e.result()
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:

@@ -440,6 +440,26 @@ struct SampleArgs {
 };
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
 
+// ------------------------------------------------------- log probabilities --
+// Per row of logits [n][ldl] (V used) at temperature t: the given token's log
+// probability and rank, the entropy, the `top` largest logits.  logprobs.cu.
+struct LogprobsArgs {
+    const void* logits;
+    int dtype;                   // ember_dtype
+    int n, V;
+    long long ldl;
+    float t;
+    const int32_t* ids;          // [n] or nullptr
+    int top;
+    float* logprob;              // [n] or nullptr
+    int32_t* rank;               // [n] or nullptr
+    float* entropy;              // [n] or nullptr
+    int32_t* top_ids;            // [n][top]
+    float* top_logprobs;
+    int cluster;                 // set by launch_logprobs: CTAs of a row
+};
+cudaError_t launch_logprobs(const LogprobsArgs& a, int sms, cudaStream_t s);
+
 // ------------------------------------------------------------ paged cache --
 // A pool of K/V pages shared by many sequences (paged_*.cu).  Row r of page p
 // of kv head g starts at k + p*page_stride + g*head_stride + r*row_stride

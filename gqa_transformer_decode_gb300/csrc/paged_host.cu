@@ -1,49 +1,14 @@
 // paged_host.cu -- the C entry points of the paged K/V cache operators:
 // argument checks before any device work, then one or two launches.
-#include <atomic>
-
-#include "common.cuh"
-#include "kernels.h"
+#include "entry.h"
 
 using namespace ember;
 
 namespace {
 
-#define PG_FAIL(st, ...) return set_error(st, __VA_ARGS__)
-
-// Answers a CUDA error, and takes it off the thread's record: the next caller that
-// looks there would take it for its own.
-ember_status cuda_failed(const char* what, cudaError_t e) {
-    cudaGetLastError();
-    PG_FAIL(EMBER_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-constexpr int PG_MAX_DEVICES = 64;
-
-// SMs of the current device (asked once per device).
-cudaError_t device_sms(int* sms) {
-    static std::atomic<int> known[PG_MAX_DEVICES];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < PG_MAX_DEVICES && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess && dev < PG_MAX_DEVICES) known[dev].store(*sms, std::memory_order_relaxed);
-    return e;
-}
-
 __global__ void k_take_status(int* status, int* taken) {
     pdl_wait();
     *taken = atomicExch(status, 0);
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// Index arrays, lse and the status word: loads and atomics of 4 bytes.
-template <class... P>
-ember_status check_words(const char* which, const P*... p) {
-    if (((reinterpret_cast<uintptr_t>(p) | ...) & 3) != 0) PG_FAIL(EMBER_ERR_INVALID_ARG, "%s must be 4-byte aligned", which);
-    return EMBER_OK;
 }
 
 // The checks every operator shares; fills the kernels' view of the cache.

@@ -6,33 +6,14 @@
 //
 // The entry points come as addresses from the loaded library, so that this module
 // serves whichever build of it ember.py loads.
-#include <Python.h>
-
-#include <ATen/ATen.h>
-#include <c10/core/AutogradState.h>
-#include <c10/core/GradMode.h>
-#include <c10/cuda/CUDACachingAllocator.h>
-#include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAStream.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <climits>
-#include <cmath>
-#include <string>
-
-#include "ember.h"
+#include "torch_args.h"
 
 namespace {
-
-using at::Tensor;
 
 decltype(&ember_paged_append) f_append = nullptr;
 decltype(&ember_paged_decode) f_decode = nullptr;
 decltype(&ember_paged_decode_workspace) f_workspace = nullptr;
 decltype(&ember_paged_prefill) f_prefill = nullptr;
-decltype(&ember_last_error) f_error = nullptr;
-PyObject* ember_error = nullptr;   // ember.EmberError
 
 // One PagedKV: the C view of the cache and where its status word lives.
 struct Cache {
@@ -47,57 +28,6 @@ struct Cache {
     size_t ws_bytes = 0;
 };
 
-struct Bad {   // a Python exception to raise
-    PyObject* type;
-    std::string text;
-};
-[[noreturn]] void bad(const std::string& text) { throw Bad{PyExc_ValueError, text}; }
-
-std::string describe(const Tensor& t) {
-    std::string s = c10::toString(t.scalar_type());
-    s += " [";
-    for (int64_t i = 0; i < t.dim(); ++i) s += (i ? ", " : "") + std::to_string(t.size(i));
-    return s + "] on " + t.device().str();
-}
-
-// A gradient would be lost without a word.  (The modes are thread-local and so asked
-// for last: nearly no tensor here has either.)
-void no_gradient(const Tensor& t, const char* what) {
-    if (t.requires_grad() && c10::GradMode::is_enabled())
-        bad(std::string(what) + " requires a gradient, which the paged operators do not have (torch.no_grad() to go without)");
-    if (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
-        bad(std::string(what) + " has a forward-mode tangent, which the paged operators do not carry on");
-}
-const Tensor& any_tensor(PyObject* o, const char* what) {
-    if (!THPVariable_Check(o)) throw Bad{PyExc_TypeError, std::string(what) + " must be a tensor"};
-    return THPVariable_Unpack(o);
-}
-const Tensor& tensor(PyObject* o, const char* what) {
-    const Tensor& t = any_tensor(o, what);
-    no_gradient(t, what);
-    return t;
-}
-bool given(PyObject* o) { return o != Py_None; }
-
-void on_device(const Cache& c, const Tensor& t, const char* what) {
-    if (!t.is_cuda() || t.device().index() != c.device)
-        bad(std::string(what) + " must be on cuda:" + std::to_string(c.device) + ", not " + t.device().str());
-}
-
-// Contiguous, of one type and shape.
-void* flat(const Cache& c, const Tensor& t, const char* what, at::ScalarType dtype, at::IntArrayRef shape) {
-    on_device(c, t, what);
-    if (t.scalar_type() != dtype || t.sizes() != shape || !t.is_contiguous()) {
-        std::string s;
-        for (size_t i = 0; i < shape.size(); ++i) s += (i ? ", " : "") + std::to_string(shape[i]);
-        bad(std::string(what) + " must be contiguous " + c10::toString(dtype) + " [" + s + "], not " + describe(t));
-    }
-    return t.data_ptr();
-}
-int32_t* ints(const Cache& c, PyObject* o, const char* what, int64_t n) {
-    return static_cast<int32_t*>(flat(c, any_tensor(o, what), what, at::kInt, {n}));
-}
-
 // [n, heads, head_dim] whose rows hold the heads side by side.
 struct Rows {
     void* p;
@@ -111,46 +41,6 @@ Rows rows(const Cache& c, const Tensor& t, const char* what, at::ScalarType dtyp
             std::to_string(heads) + ", " + std::to_string(D) + "], not " + describe(t));
     if (t.stride(2) != 1 || (heads > 1 && t.stride(1) != D)) bad(std::string(what) + ": a row's heads must lie side by side");
     return {t.data_ptr(), n > 1 ? t.stride(0) : heads * D};
-}
-
-int32_t number(PyObject* o, const char* what) {
-    const long v = PyLong_AsLong(o);
-    if (v == -1 && PyErr_Occurred()) throw python_error();
-    if (v < INT_MIN || v > INT_MAX) bad(std::string(what) + " is beyond 32 bits");
-    return (int32_t)v;
-}
-bool truth(PyObject* o) {
-    const int v = PyObject_IsTrue(o);
-    if (v < 0) throw python_error();
-    return v;
-}
-double real(PyObject* o) {
-    const double v = PyFloat_AsDouble(o);
-    if (v == -1.0 && PyErr_Occurred()) throw python_error();
-    return v;
-}
-int32_t count(int64_t n, const char* what) {
-    if (n > INT_MAX) bad(std::string(what) + " has too many rows");
-    return (int32_t)n;
-}
-
-Tensor make(const Cache& c, at::IntArrayRef shape, at::ScalarType dtype) {
-    return at::empty(shape, at::TensorOptions().dtype(dtype).device(at::kCUDA, c.device));
-}
-
-void check(ember_status st, const char* where) {
-    if (st == EMBER_OK) return;
-    if (PyObject* e = PyObject_CallFunction(ember_error, "iss", (int)st, where, f_error())) {
-        PyErr_SetObject(ember_error, e);
-        Py_DECREF(e);
-    }
-    throw python_error();
-}
-
-// A tensor of the caller's that a kernel writes: autograd notices if an earlier
-// operation saved it.
-void written(const Tensor& t) {
-    if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 Cache& cache_of(PyObject* o) {
@@ -202,19 +92,6 @@ PyObject* answer(Outputs& o) {
     return t;
 }
 
-// Runs f; nothing it throws leaves this module but as a Python exception.
-template <class F>
-PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
-    HANDLE_TH_ERRORS
-    try {
-        if (n != want) throw Bad{PyExc_TypeError, "wrong number of arguments"};
-        return f();
-    } catch (const Bad& b) {
-        PyErr_SetString(b.type, b.text.c_str());
-        return nullptr;
-    }
-    END_HANDLE_TH_ERRORS
-}
 // The call's stream.  A kernel on another one than status_word's may still raise an
 // error when the cache is gone: the allocator keeps the word until then.
 ember_stream_t stream_of(const Cache& c) {
@@ -386,7 +263,6 @@ PyObject* entries(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     });
 }
 
-#define FAST(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST("append", append), FAST("decode", decode), FAST("prefill", prefill),
                          FAST("workspace_bytes", workspace_bytes), FAST("cache", cache), FAST("entries", entries),
                          {nullptr, nullptr, 0, nullptr}};

@@ -51,6 +51,7 @@ class ember_weights(C.Structure):
 
 # ember_dtype
 F32, BF16, F16 = 0, 1, 2
+LOGPROBS_MAX_TOP = 32
 
 
 class ember_paged_kv(C.Structure):
@@ -105,6 +106,8 @@ def load():
         "ember_gemv_argmax_noalloc": (st, [P, C.c_int32, C.c_int32, P, C.c_int32, P, P, P]),
         "ember_sample": (st, [P, C.c_int32, C.c_int32, C.c_int32, C.c_float, C.c_int32, C.c_float, P, P,
                               P]),
+        "ember_logprobs": (st, [P, C.c_int32, C.c_int32, C.c_int32, C.c_int64, C.c_float, P, C.c_int32, P, P, P, P,
+                                P, P]),
         "ember_paged_append": (st, [P, P, P, P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_int32,
                                     C.c_int32, P, P, P, P, C.c_float, P, P, C.c_int32, P, C.c_int64, P, P]),
         "ember_paged_decode_workspace": (C.c_size_t, [P, C.c_int32, C.c_int32]),
@@ -255,6 +258,12 @@ def ember_gemv_q8_0(q, d, N, K, x, nb, y, stream):
 
 def ember_sample(logits, B, V, ldl, temperature, top_k, top_p, r, out, stream):
     return load().ember_sample(logits, B, V, ldl, temperature, top_k, top_p, r, out, stream)
+
+
+def ember_logprobs(logits, dtype, n, V, ldl, temperature, ids, top, logprob, rank, entropy, top_ids, top_logprobs,
+                   stream):
+    return load().ember_logprobs(logits, dtype, n, V, ldl, temperature, ids, top, logprob, rank, entropy, top_ids,
+                                 top_logprobs, stream)
 
 
 def ember_prefill_activations(m, kv, seq, ids, n, start_pos, acts, logits, argmax, stream):

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import importlib.util
+import typing
 
 import numpy as np
 import torch
@@ -206,9 +207,7 @@ class PagedKV:
         """f on another stream: what it reads and writes stays allocated until it has run there."""
         with self._on(stream):
             r = f(*args)
-        for t in (*args, self.k_pages, self.v_pages, self.table):
-            if isinstance(t, torch.Tensor):
-                t.record_stream(stream)
+        _keep_for(stream, *args, self.k_pages, self.v_pages, self.table)
         return r
 
     # -- operators ------------------------------------------------------------
@@ -258,24 +257,64 @@ class PagedKV:
             return int(taken.item())
 
 
+class Logprobs(typing.NamedTuple):
+    """What logprobs() returns, a row of logits each."""
+
+    logprob: torch.Tensor | None       # f32 [n]: of the given token (None without ids)
+    rank: torch.Tensor | None          # int32 [n]: tokens that stand before it
+    entropy: torch.Tensor              # f32 [n]
+    top_ids: torch.Tensor              # int32 [n, top]: the most probable tokens, the first first
+    top_logprobs: torch.Tensor         # f32 [n, top]
+
+
+def logprobs(logits, ids=None, top: int = 0, temperature: float = 1.0, stream=None) -> Logprobs:
+    """Log probabilities of given tokens with their ranks, the entropy, and the `top` (at most 32) most probable
+    tokens (include/ember.h, "log probabilities").
+
+    logits f32, bf16 or f16 [n, V], rows of any stride; ids int32 [n].  Tokens stand in the order of their logits,
+    equal ones in that of their indices.  Asynchronous on `stream` (default: the current stream of the logits'
+    device) under the rules of PagedKV.  It has no gradient: logits that require one are refused unless gradients
+    are off."""
+    if stream is not None:
+        if stream.device != logits.device:
+            raise ValueError(f"the stream belongs to {stream.device}, the logits to {logits.device}")
+        with torch.cuda.stream(stream):
+            r = logprobs(logits, ids, top, temperature)
+        _keep_for(stream, logits, ids)
+        return r
+    return Logprobs(*_rows_torch().logprobs(logits, ids, top, temperature))
+
+
+def _keep_for(stream, *args):
+    """What a call on another stream reads and writes stays allocated until it has run there."""
+    for t in args:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+
+
 _PAGE_DTYPES = {torch.bfloat16: E.BF16, torch.float16: E.F16}
-_torch_side = None
+_torch_sides = {}
+
+
+def _torch_side(name, build, entries):
+    """A compiled marshalling module (csrc/<name>.cpp), on the loaded library's entry points."""
+    if name not in _torch_sides:
+        lib = E.load()
+        spec = importlib.util.spec_from_file_location(name, build())
+        t = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(t)
+        t.entries(*(C.cast(getattr(lib, n), C.c_void_p).value for n in (*entries, "ember_last_error")), E.EmberError)
+        _torch_sides[name] = t
+    return _torch_sides[name]
 
 
 def _paged_torch():
-    """The compiled marshalling (csrc/paged_torch.cpp), on the loaded library's entry points."""
-    global _torch_side
-    if _torch_side is None:
-        lib = E.load()
-        path = E._build.build_ext()
-        spec = importlib.util.spec_from_file_location("paged_torch", path)
-        t = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(t)
-        t.entries(*(C.cast(getattr(lib, n), C.c_void_p).value for n in
-                    ("ember_paged_append", "ember_paged_decode", "ember_paged_decode_workspace",
-                     "ember_paged_prefill", "ember_last_error")), E.EmberError)
-        _torch_side = t
-    return _torch_side
+    return _torch_side("paged_torch", E._build.build_ext,
+                       ("ember_paged_append", "ember_paged_decode", "ember_paged_decode_workspace", "ember_paged_prefill"))
+
+
+def _rows_torch():
+    return _torch_side("rows_torch", E._build.build_rows_ext, ("ember_logprobs",))
 
 
 def _wrap_device(ptr: int, nbytes: int, device) -> torch.Tensor:

@@ -287,6 +287,37 @@ ember_status ember_sample(const float *logits, int32_t B, int32_t V, int32_t ldl
                           int32_t top_k, float top_p, const float *r, int32_t *out,
                           ember_stream_t stream);
 
+/* Element types of the operators below. */
+typedef enum ember_dtype { EMBER_F32 = 0, EMBER_BF16 = 1, EMBER_F16 = 2 } ember_dtype;
+
+/* ---- log probabilities ---------------------------------------------------- */
+
+/* What a row of logits l says of its tokens, with x = l / temperature and
+ * log p_i = x_i - log sum_j exp(x_j) (ember reference_forward.py forward()'s
+ * logits; "ember internals", softmax):
+ *   logprob [n]       log p of ids[r]
+ *   rank    [n]       how many tokens stand before it: larger logits, and equal
+ *                     ones of a lower index (0: it is the greedy token)
+ *   entropy [n]       -sum_i p_i log p_i
+ *   top_ids, top_logprobs [n][top]  the first `top` tokens in that order and
+ *                     their log p; top at most EMBER_LOGPROBS_MAX_TOP
+ *   logits [n] rows of V elements of `dtype` (F32, BF16, F16), ldl elements apart,
+ *   aligned to their elements; ids [n] int32.  logprob, rank and entropy may be
+ *   NULL, ids too (logprob and rank must then be); top may be 0.
+ * An id outside [0, V) gives logprob NaN and rank -1.  A logit of -inf has no
+ * weight; a row of nothing else is uniform, as in ember_sample.  In a row with a
+ * NaN or +inf every log probability and the entropy are NaN; NaN counts as the
+ * largest logit.  The order is that of the logits themselves, whatever the
+ * temperature (finite, above 0, not subnormal) rounds together.  Distances between
+ * logits beyond 1e30 count as 1e30.  Arithmetic is
+ * f32; equal calls give equal bits.  Asynchronous on `stream`; allocates nothing.
+ * Host errors: INVALID_ARG, UNSUPPORTED (top), CUDA. */
+#define EMBER_LOGPROBS_MAX_TOP 32
+ember_status ember_logprobs(const void *logits, int32_t dtype, int32_t n, int32_t V, int64_t ldl,
+                            float temperature, const int32_t *ids, int32_t top, float *logprob,
+                            int32_t *rank, float *entropy, int32_t *top_ids, float *top_logprobs,
+                            ember_stream_t stream);
+
 /* ---- paged key/value cache ------------------------------------------------ */
 
 /* Three operators on one pool of K/V pages that many sequences share, for a
@@ -340,8 +371,6 @@ ember_status ember_sample(const float *logits, int32_t B, int32_t V, int32_t ldl
  *     overlap, except that pages may be shared by the tables of sequences
  *     that only read them.  What a call reads is not to be written by others
  *     until its kernels have ended (page rows that it does not see may be). */
-typedef enum ember_dtype { EMBER_F32 = 0, EMBER_BF16 = 1, EMBER_F16 = 2 } ember_dtype;
-
 typedef struct ember_paged_kv {
     void *k, *v;                 /* the pages, elements of `dtype`              */
     const int32_t *table;        /* [n_seqs][table_width] page numbers          */
