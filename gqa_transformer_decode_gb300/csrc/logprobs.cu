@@ -10,12 +10,13 @@
 //
 // The largest `top` <= 32 come out of the same pass by a threshold that rises: the
 // threads form 32 groups, whose maxima so far are 32 different elements, so that the
-// top-th largest of these maxima is a lower bound of the top-th largest logit.  An
-// element at or above the bound goes into a list in shared memory (a few hundred of a
-// row of 150000 do), everything else costs nothing, since the maximum of a vector is
-// taken for m anyway.  The list is then ordered by counting.  Rows that overflow it
-// (thousands of equal largest logits) or hold a NaN are searched once for each of the
-// `top`, slowly but right.
+// top-th largest of these maxima is a lower bound of the top-th largest logit.  The
+// number of a 16-byte vector with an element at or above the bound goes into a list (a
+// few hundred of a row of 150000 do), everything else costs nothing, since the maximum of
+// a vector is taken for m anyway.  In the end these vectors are read again, and their
+// elements above the last bound ordered by counting.  Rows that overflow the list
+// (thousands of equal largest logits) or hold a NaN are searched value by value, slowly
+// but right.
 //
 // A row is split over the CTAs of a cluster while that leaves CTAs idle otherwise, and
 // joined through distributed shared memory: one launch, no workspace, no atomics on
@@ -33,37 +34,96 @@ constexpr int LP_GROUP = LP_THREADS / 32;       // lanes of a group: 32 groups
 constexpr int LP_AHEAD = 4;                     // vectors of 16 bytes in flight for each thread
 constexpr int LP_TOP = EMBER_LOGPROBS_MAX_TOP;
 constexpr int LP_CLUSTER = 8;                   // CTAs of a row at most
-// An empty group leaves no bound, but then fewer than LP_THREADS + 1 vectors of 8.
-constexpr int LP_LIST = 8 * (LP_THREADS + 1);
+constexpr int LP_HITS = 2048;                   // vectors looked at again at most
+// A group without elements leaves no bound, but then there are less than LP_THREADS vectors (of 8) and the ends.
+constexpr int LP_LIST = 8 * (LP_THREADS + 2);
 static_assert(LP_TOP == 32, "one group's maximum for each of the largest");
+// In the fast pass every logit counts as at least LP_LOW: -inf then has the weight 0 and
+// gives no inf - inf.  A row whose largest logit is not within +-LP_LOW goes the slow way.
+constexpr float LP_LOW = -1e30f;
 
-struct LogitF32 {
-    static constexpr int VEC = 4;
-    using T = float;
-    __device__ __forceinline__ static float one(float x) { return x; }
-    __device__ __forceinline__ static void unpack(const uint4& w, float* x) {
-        x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
-    }
-};
-struct LogitBf16 {
-    static constexpr int VEC = 8;
-    using T = uint16_t;
-    __device__ __forceinline__ static float one(uint16_t x) { return bf16_to_f32(x); }
-    __device__ __forceinline__ static void unpack(const uint4& w, float* x) { unpack8(w, x); }
-};
-struct LogitF16 {
-    static constexpr int VEC = 8;
-    using T = uint16_t;
-    __device__ __forceinline__ static float one(uint16_t x) { return __half2float(__ushort_as_half(x)); }
-    __device__ __forceinline__ static void unpack(const uint4& w, float* x) { unpack8_f16(w, x); }
-};
-
-// the larger of two, NaN if either is
+// the larger of two and of three, NaN if any is
 __device__ __forceinline__ float max_nan(float x, float y) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
+__device__ __forceinline__ float max_nan(float x, float y, float z) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+
+// Element types: a 16-byte vector as floats that are at least LP_LOW, and their largest.
+struct LogitF32 {
+    static constexpr int VEC = 4;
+    using T = float;
+    static constexpr uint32_t NONE = 0xff800000u;   // -inf
+    __device__ __forceinline__ static float one(float x) { return x; }
+    __device__ __forceinline__ static float unpack(const uint4& w, float* x) {
+        x[0] = max_nan(__uint_as_float(w.x), LP_LOW), x[1] = max_nan(__uint_as_float(w.y), LP_LOW);
+        x[2] = max_nan(__uint_as_float(w.z), LP_LOW), x[3] = max_nan(__uint_as_float(w.w), LP_LOW);
+        return max_nan(max_nan(x[0], x[1], x[2]), x[3]);
+    }
+};
+struct LogitBf16 {
+    static constexpr int VEC = 8;
+    using T = uint16_t;
+    static constexpr uint32_t NONE = 0xff80ff80u;
+    __device__ __forceinline__ static float one(uint16_t x) { return bf16_to_f32(x); }
+    __device__ __forceinline__ static float unpack(uint4 w, float* x) {
+        constexpr uint32_t low = 0xf14af14au;       // -1.0003e30: the largest bf16 that is not above LP_LOW
+        w = make_uint4(max_bf16x2(w.x, low), max_bf16x2(w.y, low), max_bf16x2(w.z, low), max_bf16x2(w.w, low));
+        unpack8(w, x);
+        const uint32_t m = max_bf16x2(max_bf16x2(w.x, w.y), max_bf16x2(w.z, w.w));
+        return max_nan(bf16_lo(m), bf16_hi(m));
+    }
+};
+struct LogitF16 {
+    static constexpr int VEC = 8;
+    using T = uint16_t;
+    static constexpr uint32_t NONE = 0xfc00fc00u;
+    __device__ __forceinline__ static float one(uint16_t x) { return __half2float(__ushort_as_half(x)); }
+    __device__ __forceinline__ static float unpack(const uint4& w, float* x) {
+        unpack8_f16(w, x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] = max_nan(x[e], LP_LOW);
+        return max_nan(max_nan(max_nan(x[0], x[1], x[2]), x[3], x[4]), max_nan(x[5], x[6], x[7]));
+    }
+};
+
+// two f32 operations in one instruction
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+
 // the value that argmax_key made the key's high word from (NaN for the highest)
 __device__ __forceinline__ float key_value(unsigned long long k) {
     const uint32_t u = (uint32_t)(k >> 32);
@@ -90,23 +150,151 @@ struct Sums {
     }
 };
 
+// The sums of `n` neighbouring lanes (a power of two) joined, in one order for all of them.
+template <int N>
+__device__ __forceinline__ Sums join_lanes(Sums q, float c2) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
+        Sums y;
+        y.m = __shfl_xor_sync(FULL_MASK, q.m, o);
+        y.s = __shfl_xor_sync(FULL_MASK, q.s, o);
+        y.u = __shfl_xor_sync(FULL_MASK, q.u, o);
+        y.above = __shfl_xor_sync(FULL_MASK, q.above, o);
+        if (threadIdx.x & o) {
+            const Sums t = q;
+            q = y;
+            y = t;
+        }
+        q.join(y, c2);
+    }
+    return q;
+}
+// Over the whole CTA (s_sums: LP_WARPS of them).
+__device__ __noinline__ Sums join_all(Sums q, float c2, Sums* s_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    q = join_lanes<32>(q, c2);
+    __syncthreads();
+    if (lane == 0) s_sums[warp] = q;
+    __syncthreads();
+    return join_lanes<LP_WARPS>(s_sums[lane % LP_WARPS], c2);
+}
+
+// A lower bound of the top-th largest logit from the groups' maxima as they are (each a
+// lower bound of what it will be); g: this thread's maximum.  By a whole warp.  The top-th
+// largest maximum is the best such bound; beyond the eighth the least of all, which takes one
+// reduction, costs less than the longer list it lets in.
+__device__ __noinline__ float raise_bound(float g, float* s_group, int top) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < LP_GROUP; o <<= 1) g = fmaxf(g, __shfl_xor_sync(FULL_MASK, g, o));
+    volatile float* group = s_group;
+    if (lane % LP_GROUP == 0) group[threadIdx.x / LP_GROUP] = g;
+    __syncwarp();
+    // the values' order as unsigned numbers, the lane below them (1: -inf or none)
+    uint32_t v = (uint32_t)(argmax_key(group[lane], 0u) >> 32);
+    uint32_t k = __reduce_min_sync(FULL_MASK, v);
+    if (top <= 8)
+        for (int i = 0; i < top; ++i) {
+            k = __reduce_max_sync(FULL_MASK, v);
+            const unsigned at = __ballot_sync(FULL_MASK, v == k);
+            if (lane == __ffs(at) - 1) v = 0;
+        }
+    return fmaxf(LP_LOW, __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k));
+}
+
+// Puts each key of s_keys[0 .. n) that is among the `top` largest into its place: the number of
+// larger ones (0: no key).
+__device__ __noinline__ void order_keys(const unsigned long long* s_keys, int n, int top, unsigned long long* s_top) {
+    for (int i = threadIdx.x; i < n; i += LP_THREADS) {
+        const unsigned long long x = s_keys[i];
+        int larger = 0;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) larger += s_keys[k] > x;
+        if (x != 0 && larger < top) s_top[larger] = x;
+    }
+}
+
+// The slow ways, over elements [i0, i1) of a row, by the whole CTA.
+struct Search {
+    unsigned long long best[LP_WARPS];
+    int found[LP_WARPS];
+};
+// Adds to s_top[have ..] the largest elements below the key `before` (first: there is none), in
+// order, until there are `top`: finds the largest, then in one walk all that equal it.
+template <class L>
+__device__ __noinline__ int take_largest(const typename L::T* row, int i0, int i1, unsigned long long before, bool first,
+                                         int have, int top, unsigned long long* s_top, Search& s) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    while (have < top) {
+        unsigned long long best = 0;
+        for (int i = i0 + tid; i < i1; i += LP_THREADS) {
+            const unsigned long long k = argmax_key(L::one(row[i]), (uint32_t)i);
+            if ((first || k < before) && k > best) best = k;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const unsigned long long y = __shfl_xor_sync(FULL_MASK, best, o);
+            best = y > best ? y : best;
+        }
+        __syncthreads();
+        if (lane == 0) s.best[warp] = best;
+        __syncthreads();
+        for (int w = 0; w < LP_WARPS; ++w) best = s.best[w] > best ? s.best[w] : best;
+        if (best == 0) return have;                  // no more of them (a key is never 0)
+        const uint32_t value = (uint32_t)(best >> 32);
+        for (int j = argmax_key_index(best); j < i1 && have < top; j += LP_THREADS) {
+            const int i = j + tid;
+            const unsigned long long k = i < i1 ? argmax_key(L::one(row[i]), (uint32_t)i) : 0ull;
+            const bool same = i < i1 && (uint32_t)(k >> 32) == value;
+            const unsigned m = __ballot_sync(FULL_MASK, same);
+            __syncthreads();
+            if (lane == 0) s.found[warp] = __popc(m);
+            __syncthreads();
+            int at = have + __popc(m & ((1u << lane) - 1u));
+            for (int w = 0; w < LP_WARPS; ++w) {
+                if (w < warp) at += s.found[w];
+                have += s.found[w];
+            }
+            if (same && at < top) s_top[at] = k;
+        }
+        before = (unsigned long long)value << 32;    // below all of this value
+        first = false;
+    }
+    return top;
+}
+// Sums of a row of any values; above: how many stand before element id, less id.
+template <class L>
+__device__ __noinline__ Sums sum_slowly(const typename L::T* row, int i0, int i1, int id, float xi, float c2, Sums* s_sums) {
+    Sums q{-INFINITY, 0.f, 0.f, 0};
+    const unsigned long long mine = id >= 0 ? argmax_key(xi, (uint32_t)id) : 0ull;
+    for (int i = i0 + (int)threadIdx.x; i < i1; i += LP_THREADS) {
+        const float x = L::one(row[i]);
+        if (id >= 0) q.above += (argmax_key(x, (uint32_t)i) > mine) - (i < id);
+        if (x > q.m) q.move(x, c2);
+        const float d = fmaxf(x - q.m, LP_LOW), p = x == -INFINITY ? 0.f : ex2(d * c2);
+        q.s += p;
+        q.u = fmaf(p, d, q.u);
+    }
+    return join_all(q, c2, s_sums);
+}
+
 template <class L>
 __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(LogprobsArgs a) {
     constexpr int VEC = L::VEC;
     using T = typename L::T;
     __shared__ unsigned long long s_list[LP_LIST];
-    __shared__ unsigned long long s_top[LP_TOP];
-    __shared__ unsigned long long s_all[LP_CLUSTER * LP_TOP];
+    __shared__ unsigned long long s_top[LP_TOP], s_all[LP_CLUSTER * LP_TOP];
     __shared__ float s_group[32];
     __shared__ Sums s_sums[LP_WARPS], s_part;
-    __shared__ int s_count, s_nan, s_kept;
-    __shared__ unsigned long long s_best[LP_WARPS];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int s_hit[LP_HITS], s_hits, s_count, s_nan;
+    __shared__ Search s_search;
+    const int tid = threadIdx.x, lane = tid & 31;
     const unsigned C = a.cluster, part = blockIdx.x % C;
     const long long r = blockIdx.x / C;
     const int top = a.top;
-    if (tid == 0) s_count = s_nan = s_kept = 0;
+    if (tid == 0) s_hits = s_count = s_nan = 0;
     if (tid < LP_TOP) s_top[tid] = 0;
+    if (tid < 32) s_group[tid] = -INFINITY;
     pdl_wait();
 
     // Vector j of the row holds elements first + j * VEC ..: the 0th ends where the row's
@@ -116,291 +304,216 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(LogprobsArgs a) {
     const int first = ahead - VEC;
     const int vectors = 1 + (int)(((long long)a.V - ahead + VEC - 1) / VEC);
     const int lo = (int)((long long)vectors * part / C), hi = (int)((long long)vectors * (part + 1) / C);
+    const int whole_lo = max(lo, 1), whole_hi = min(hi, 1 + (a.V - ahead) / VEC);   // (V < ahead: none)
+    const uint4* at = reinterpret_cast<const uint4*>(row + first);                 // vector 0
     const float c2 = LOG2E / a.t;
 
     const int id = a.ids ? a.ids[r] : -1;
     const bool given = id >= 0 && id < a.V;
     const float xi = given ? L::one(row[id]) : 0.f;
-    const int jid = given ? (id - first) / VEC : 0;
-
-    auto whole = [&](int j) { return j > 0 && first + (j + 1) * VEC <= a.V; };
-    auto fetch = [&](int j) {                    // its bits; elements outside are -inf
-        if (j < hi && whole(j)) return ld_stream(reinterpret_cast<const uint4*>(row + first + (long long)j * VEC));
-        constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : std::is_same<L, LogitF16>::value ? 0xfc00fc00u : 0xff80ff80u;
-        uint4 w = make_uint4(none, none, none, none);
-        if (j < hi) {
-            uint32_t b[4] = {none, none, none, none};
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int i = first + j * VEC + e;
-                if (i < 0 || i >= a.V) continue;
-                if constexpr (sizeof(T) == 4) b[e] = __float_as_uint(row[i]);
-                else b[e / 2] = e & 1 ? (b[e / 2] & 0xffffu) | (uint32_t)row[i] << 16 : (b[e / 2] & 0xffff0000u) | row[i];
-            }
-            w = make_uint4(b[0], b[1], b[2], b[3]);
-        }
-        return w;
-    };
+    const bool count_fast = given && xi > LP_LOW;
+    const int jid = given ? (id - first) / VEC : -1;                               // its vector
+    const float below_xi = nextafterf(xi, -INFINITY);
 
     Sums q{-INFINITY, 0.f, 0.f, 0};
     bool nan = false;
-    float bound = -INFINITY;                     // of the top-th largest logit, from below
-    // The bound from the groups' maxima as they are (each a lower bound of what it will be);
-    // g: this thread's maximum.
+    float bound = LP_LOW;                        // of the top-th largest logit, from below
+    // What a vector has to reach to be looked at by element: the bound, or the given token's logit.
+    float reach = count_fast ? (top > 0 ? LP_LOW : xi) : top > 0 ? LP_LOW : INFINITY;
     auto raise = [&](float g) {
+        bound = raise_bound(g, s_group, top);
+        reach = count_fast ? fminf(bound, xi) : bound;
+    };
+    // Lists element i of value x if it may be among the largest.
+    auto list = [&](float x, int i) {
+        if (!(x >= bound && x > LP_LOW)) return;
+        const int n = atomicAdd(&s_count, 1);
+        if (n < LP_LIST) s_list[n] = argmax_key(x, (uint32_t)i);
+    };
+    auto work = [&](const uint4& w, int j) {
+        float x[VEC];
+        float big = L::unpack(w, x);
+        if (!(big <= q.m)) {
+            if (big != big) {
+                nan = true;
+                big = q.m;
 #pragma unroll
-        for (int o = 1; o < LP_GROUP; o <<= 1) g = fmaxf(g, __shfl_xor_sync(FULL_MASK, g, o));
-        volatile float* group = s_group;
-        if (lane % LP_GROUP == 0) group[tid / LP_GROUP] = g;
-        __syncwarp();
-        const float v = group[lane];
-        int before = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float w = __shfl_sync(FULL_MASK, v, i);
-            before += w > v || (w == v && i < lane);
+                for (int e = 0; e < VEC; ++e) big = fmaxf(big, x[e]);
+            }
+            if (big > q.m) q.move(big, c2);
         }
-        const unsigned at = __ballot_sync(FULL_MASK, before == top - 1);
-        bound = __shfl_sync(FULL_MASK, v, __ffs(at) - 1);
+        bool listed = false;
+        if (big >= reach) {
+            if (count_fast) {                    // larger ones, before the given token equal ones too
+                const float than = j < jid ? below_xi : xi;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) q.above += x[e] > than;
+            }
+            if (count_fast && j == jid) {        // (read again: one vector of the row)
+#pragma unroll 1
+                for (int i = first + j * VEC; i < id; ++i) q.above += L::one(row[i]) == xi;
+            }
+            listed = top > 0 && big >= bound;
+            if (listed) {
+                const int n = atomicAdd(&s_hits, 1);
+                if (n < LP_HITS) s_hit[n] = j;
+            }
+        }
+        const uint64_t m2 = pair(-q.m, -q.m), k2 = pair(c2, c2);
+        uint64_t s = pair(q.s, 0.f), u = pair(q.u, 0.f);
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const uint64_t d = add2(pair(x[e], x[e + 1]), m2);
+            float2 p = halves(mul2(d, k2));
+            p.x = ex2(p.x);
+            p.y = ex2(p.y);
+            const uint64_t p2 = pair(p.x, p.y);
+            s = add2(s, p2);
+            u = fma2(p2, d, u);
+        }
+        const float2 s1 = halves(s), u1 = halves(u);
+        q.s = s1.x + s1.y;
+        q.u = u1.x + u1.y;
+        return listed;
     };
 
     uint4 next[LP_AHEAD];
+    const uint4 none = make_uint4(L::NONE, L::NONE, L::NONE, L::NONE);
 #pragma unroll
-    for (int k = 0; k < LP_AHEAD; ++k) next[k] = fetch(lo + tid + k * LP_THREADS);
-    if (tid < 32) s_group[tid] = -INFINITY;
+    for (int k = 0; k < LP_AHEAD; ++k) {
+        const int j = whole_lo + tid + k * LP_THREADS;
+        next[k] = j < whole_hi ? ld_stream(at + j) : none;
+    }
     __syncthreads();
     if (top > 0) {                               // a first bound before anything is listed
+        float g = -INFINITY;
 #pragma unroll
         for (int k = 0; k < LP_AHEAD; ++k) {
             float x[VEC];
-            L::unpack(next[k], x);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) q.m = fmaxf(q.m, x[e]);
+            const float big = L::unpack(next[k], x);
+            g = fmaxf(g, big);                   // (a NaN is left out here, and found below)
         }
-        raise(q.m);
+        raise(g);
         __syncthreads();
-        raise(q.m);
+        raise(g);
+        q.m = g > LP_LOW ? g : -INFINITY;
     }
-    for (int j0 = lo; j0 < hi; j0 += LP_AHEAD * LP_THREADS) {
+    for (int j0 = whole_lo; j0 < whole_hi; j0 += LP_AHEAD * LP_THREADS) {
         bool listed = false;
 #pragma unroll
         for (int k = 0; k < LP_AHEAD; ++k) {
-            const int j = j0 + tid + k * LP_THREADS;
+            const int j = j0 + tid + k * LP_THREADS, jn = j + LP_AHEAD * LP_THREADS;
             const uint4 w = next[k];
-            next[k] = fetch(j + LP_AHEAD * LP_THREADS);
-            if (j >= hi) continue;
-            float x[VEC];
-            L::unpack(w, x);
-            float big = x[0];
-#pragma unroll
-            for (int e = 1; e < VEC; ++e) big = max_nan(big, x[e]);
-            if (!(big <= q.m)) {
-                if (big != big) {
-                    nan = true;
-                    big = q.m;
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) big = fmaxf(big, x[e]);
-                }
-                if (big > q.m) q.move(big, c2);
-            }
-            if (top > 0 && big >= bound) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (x[e] >= bound && x[e] > -INFINITY) {
-                        const int at = atomicAdd(&s_count, 1);
-                        if (at < LP_LIST) s_list[at] = argmax_key(x[e], (uint32_t)(first + j * VEC + e));
-                        listed = true;
-                    }
-            }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                // (-inf has no weight, and -inf - -inf is not a number: both end at the floor)
-                const float d = fmaxf(x[e] - q.m, -1e30f);
-                const float p = ex2(d * c2);
-                q.s += p;
-                q.u = fmaf(p, d, q.u);
-            }
-            if (given) {                         // elements that stand before the given one: larger, or equal and earlier
-                if (j == jid || j == 0) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const int i = first + j * VEC + e;
-                        q.above += i < 0 || i >= a.V ? 0 : i < id ? -(x[e] < xi) : x[e] > xi;
-                    }
-                } else if (j < jid) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) q.above -= x[e] < xi;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) q.above += x[e] > xi;
-                }
-            }
+            if (jn < whole_hi) next[k] = ld_stream(at + jn);
+            if (j < whole_hi) listed |= work(w, j);
         }
         if (top > 0 && __any_sync(FULL_MASK, listed)) raise(q.m);
+    }
+    // the row's ends, an element a thread
+    if (tid < 2 * VEC) {
+        const int j = tid < VEC ? 0 : vectors - 1, i = first + j * VEC + tid % VEC;
+        if (j >= lo && j < hi && (j < whole_lo || j >= whole_hi) && (tid < VEC || j > 0) && i >= 0 && i < a.V) {
+            const float v = max_nan(L::one(row[i]), LP_LOW);
+            if (v != v) nan = true;
+            else if (v > q.m) q.move(v, c2);
+            if (count_fast) q.above += v > xi || (v == xi && i < id);
+            if (top > 0) list(v, i);
+            const float d = v - q.m, p = ex2(d * c2);
+            q.s += p;
+            q.u = fmaf(p, d, q.u);
+        }
     }
     if (nan) s_nan = 1;
     const float largest = q.m;                   // of this thread
     if (top > 0) raise(largest);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Sums y;
-        y.m = __shfl_xor_sync(FULL_MASK, q.m, o);
-        y.s = __shfl_xor_sync(FULL_MASK, q.s, o);
-        y.u = __shfl_xor_sync(FULL_MASK, q.u, o);
-        y.above = __shfl_xor_sync(FULL_MASK, q.above, o);
-        // in the same order on both sides, so that all lanes hold the same sum
-        if (lane & o) {
-            y.join(q, c2);
-            q = y;
-        } else {
-            q.join(y, c2);
-        }
-    }
-    if (lane == 0) s_sums[warp] = q;
-    __syncthreads();
-    q = s_sums[0];
-    for (int w = 1; w < LP_WARPS; ++w) q.join(s_sums[w], c2);
-    const bool has_nan = s_nan != 0;
+    q = join_all(q, c2, s_sums);
 
-    // every element of this part by its key, NaN above all others
-    auto each = [&](auto f) {
-        const int i0 = max(0, first + lo * VEC), i1 = (int)min((long long)a.V, first + (long long)hi * VEC);
-        for (int i = i0 + tid; i < i1; i += LP_THREADS) f(argmax_key(L::one(row[i]), (uint32_t)i));
-    };
-    if (given && (has_nan || xi != xi)) {        // the count by keys; id is added below
-        const unsigned long long mine = argmax_key(xi, (uint32_t)id);
-        int n = 0;
-        each([&](unsigned long long k) {
-            const int i = argmax_key_index(k);
-            n += (k > mine) - (i < id);
-        });
-        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(FULL_MASK, n, o);
+    // ---- this part's largest above LP_LOW, in order ----
+    const int i_lo = max(0, first + lo * VEC), i_hi = (int)min((long long)a.V, first + (long long)hi * VEC);
+    if (top > 0) {
+        raise(largest);
+        const int hits = s_hits;
+        if (hits <= LP_HITS)
+            for (int h = tid; h < hits; h += LP_THREADS) {
+                const int j = s_hit[h];
+                float x[VEC];
+                L::unpack(ld_stream(at + j), x);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) list(x[e], first + j * VEC + e);
+            }
         __syncthreads();
-        if (lane == 0) s_sums[warp].above = n;
-        __syncthreads();
-        q.above = 0;
-        for (int w = 0; w < LP_WARPS; ++w) q.above += s_sums[w].above;
+        const int listed = s_count;
+        if (s_nan || hits > LP_HITS || listed > LP_LIST) {
+            take_largest<L>(row, i_lo, i_hi, 0ull, true, 0, top, s_top, s_search);
+            __syncthreads();
+            if (tid < top && s_top[tid] <= argmax_key(LP_LOW, 0u)) s_top[tid] = 0;
+        } else {
+            order_keys(s_list, listed, top, s_top);
+        }
     }
     if (tid == 0) s_part = q;
-
-    // ---- this part's largest, in order, without -inf ----
-    if (top > 0) {
-        const int listed = s_count;
-        if (has_nan || listed > LP_LIST) {
-            unsigned long long before = ~0ull;
-            const unsigned long long least = argmax_key(-INFINITY, 0u);   // (0u: the highest key of -inf)
-            for (int k = 0; k < top; ++k) {
-                unsigned long long best = 0;
-                each([&](unsigned long long x) {
-                    if ((k == 0 || x < before) && x > least && x > best) best = x;
-                });
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const unsigned long long y = __shfl_xor_sync(FULL_MASK, best, o);
-                    best = y > best ? y : best;
-                }
-                __syncthreads();
-                if (lane == 0) s_best[warp] = best;
-                __syncthreads();
-                for (int w = 0; w < LP_WARPS; ++w) best = s_best[w] > best ? s_best[w] : best;
-                if (tid == 0) s_top[k] = best;
-                if (best == 0) break;            // no more of them (the same for all threads)
-                before = best;
-            }
-        } else {
-            // what lies below the last bound goes, then each element's place is the number of larger ones
-            // (the highest index has the lowest key of its value)
-            raise(largest);
-            const unsigned long long least = argmax_key(bound, 0xffffffffu);
-            unsigned long long keep[LP_LIST / LP_THREADS + 1];
-#pragma unroll
-            for (int k = 0; k < LP_LIST / LP_THREADS + 1; ++k) {
-                const int i = tid + k * LP_THREADS;
-                keep[k] = i < listed ? s_list[i] : 0ull;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < LP_LIST / LP_THREADS + 1; ++k)
-                if (keep[k] != 0 && keep[k] >= least) s_list[atomicAdd(&s_kept, 1)] = keep[k];
-            __syncthreads();
-            const int kept = s_kept;
-            for (int i = tid; i < kept; i += LP_THREADS) {
-                const unsigned long long x = s_list[i];
-                int larger = 0;
-                for (int k = 0; k < kept; ++k) larger += s_list[k] > x;
-                if (larger < top) s_top[larger] = x;
-            }
-        }
-    }
     pdl_trigger();
 
     // ---- the parts' joined in the first CTA ----
     if (C > 1) {
         cluster_sync_all();
         if (part == 0) {
-            const uint32_t at = sa_u32(&s_part), keys = sa_u32(s_top);
-            for (unsigned p = 1; p < C; ++p) {
-                Sums y;
-                y.m = ld_cluster(at, p);
-                y.s = ld_cluster(at + 4, p);
-                y.u = ld_cluster(at + 8, p);
-                y.above = __float_as_int(ld_cluster(at + 12, p));
-                q.join(y, c2);
+            const uint32_t sums = sa_u32(&s_part), keys = sa_u32(s_top);
+            Sums y{-INFINITY, 0.f, 0.f, 0};
+            if (lane < (int)C) {
+                y.m = ld_cluster(sums, lane);
+                y.s = ld_cluster(sums + 4, lane);
+                y.u = ld_cluster(sums + 8, lane);
+                y.above = __float_as_int(ld_cluster(sums + 12, lane));
             }
+            q = join_lanes<LP_CLUSTER>(y, c2);
+            q.m = __shfl_sync(FULL_MASK, q.m, 0);
+            q.s = __shfl_sync(FULL_MASK, q.s, 0);
+            q.u = __shfl_sync(FULL_MASK, q.u, 0);
+            q.above = __shfl_sync(FULL_MASK, q.above, 0);
             for (int i = tid; i < (int)C * top; i += LP_THREADS) {
                 const float2 k = ld_cluster2(keys + 8 * (i % top), i / top);
                 s_all[i] = (unsigned long long)__float_as_uint(k.y) << 32 | __float_as_uint(k.x);
             }
-            if (tid == 0)
-                for (unsigned p = 1; p < C; ++p)
-                    if (__float_as_int(ld_cluster(sa_u32(&s_nan), p)) != 0) s_nan = 1;
+            if (tid > 0 && tid < (int)C && __float_as_int(ld_cluster(sa_u32(&s_nan), tid)) != 0) s_nan = 1;
         }
         cluster_sync_all();                      // no CTA leaves while its shared memory is read
         if (part != 0) return;
         if (tid < top) s_top[tid] = 0;
         __syncthreads();
-        for (int i = tid; i < (int)C * top; i += LP_THREADS) {
-            const unsigned long long x = s_all[i];
-            if (x == 0) continue;
-            int larger = 0;
-            for (int k = 0; k < (int)C * top; ++k) larger += s_all[k] > x;
-            if (larger < top) s_top[larger] = x;
-        }
+        order_keys(s_all, (int)C * top, top, s_top);
     }
     __syncthreads();
 
+    // ---- what the fast pass leaves out ----
+    const bool has_nan = s_nan != 0;
+    if (has_nan || !(q.m > LP_LOW && q.m < -LP_LOW) || (given && !count_fast))
+        q = sum_slowly<L>(row, 0, a.V, given ? id : -1, xi, c2, s_sums);
+    else if (given)
+        q.above -= id;                           // (sum_slowly's count)
+    if (top > 0) {
+        const int have = __syncthreads_count(tid < top && s_top[min(tid, LP_TOP - 1)] != 0);
+        if (have < top) take_largest<L>(row, 0, a.V, have > 0 ? s_top[have - 1] : 0ull, have == 0, have, top, s_top, s_search);
+        __syncthreads();
+    }
+
     // ---- the row's outputs ----
-    const bool flat = q.m == -INFINITY && !s_nan;                  // every logit -inf: uniform, as the sampler has it
-    const bool bad = s_nan || q.m == INFINITY;                     // no distribution
+    const bool flat = q.m == -INFINITY && !has_nan;                // every logit -inf: uniform, as the sampler has it
+    const bool undefined = has_nan || q.m == INFINITY;
     const float log_s = flat ? logf((float)a.V) : logf(q.s);
     auto logprob = [&](float x) {
-        if (bad) return __int_as_float(0x7fffffff);
+        if (undefined) return __int_as_float(0x7fffffff);
         return flat ? -log_s : (x - q.m) / a.t - log_s;
     };
     if (tid == 0) {
         if (a.logprob) a.logprob[r] = given ? logprob(xi) : __int_as_float(0x7fffffff);
         if (a.rank) a.rank[r] = given ? q.above + id : -1;
-        if (a.entropy) a.entropy[r] = bad ? __int_as_float(0x7fffffff) : flat ? log_s : log_s - q.u / (q.s * a.t);
+        if (a.entropy) a.entropy[r] = undefined ? __int_as_float(0x7fffffff) : flat ? log_s : log_s - q.u / (q.s * a.t);
     }
-    if (warp == 0 && top > 0) {
-        const unsigned long long k = lane < top ? s_top[lane] : 0ull;
-        int have = __popc(__ballot_sync(FULL_MASK, k != 0));
-        if (k != 0) {
-            a.top_ids[r * top + lane] = argmax_key_index(k);
-            a.top_logprobs[r * top + lane] = logprob(key_value(k));
-        }
-        // fewer than `top` above -inf: the first of the others, which stand among the first 64
-        for (int i0 = 0; have < top && i0 < a.V; i0 += 32) {
-            const int i = i0 + lane;
-            const bool none = i < a.V && L::one(row[i]) == -INFINITY;
-            const unsigned m = __ballot_sync(FULL_MASK, none);
-            const int at = have + __popc(m & ((1u << lane) - 1u));
-            if (none && at < top) {
-                a.top_ids[r * top + at] = i;
-                a.top_logprobs[r * top + at] = logprob(-INFINITY);
-            }
-            have += __popc(m);
-        }
+    if (tid < top) {
+        const unsigned long long k = s_top[tid];
+        a.top_ids[r * top + tid] = argmax_key_index(k);
+        a.top_logprobs[r * top + tid] = logprob(key_value(k));
     }
 }
 

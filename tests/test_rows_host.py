@@ -21,7 +21,7 @@ def logprobs(**over):
     (dict(V=(1 << 30) + 1, ldl=1 << 31), INVALID, "V must"), (dict(ldl=99), INVALID, "ldl"),
     (dict(t=0.0), INVALID, "temperature"), (dict(t=-1.0), INVALID, "temperature"),
     (dict(t=float("nan")), INVALID, "temperature"), (dict(t=float("inf")), INVALID, "temperature"),
-    (dict(t=1e-39), INVALID, "temperature"), (dict(top=-1), INVALID, "top"), (dict(top=101), INVALID, "top"),
+    (dict(t=9e-7), INVALID, "temperature"), (dict(t=1.1e6), INVALID, "temperature"), (dict(top=-1), INVALID, "top"), (dict(top=101), INVALID, "top"),
     (dict(top=33), UNSUPPORTED, "top > 32"), (dict(top_ids=None), INVALID, "top_ids"),
     (dict(top_logprobs=None), INVALID, "top_ids"), (dict(ids=None), INVALID, "need ids"),
     (dict(logits=None), INVALID, "logits is NULL"), (dict(logits=A + 2), INVALID, "aligned"),
