@@ -1,0 +1,609 @@
+// adapters.cu -- a projection that all requests share, with the low-rank adapter of each
+// row's own beside it:  y_i = W x_i + bias + s_a B_a (A_a x_i),  a = ids[i].
+//
+// Bound: for few rows the bytes of W and of the adapters that the rows name, for many rows
+// the products.  Two launches: the first takes t_i = s_a A_a x_i (k_adapter<.., true>), the
+// second y (k_adapter<.., false>); the second starts with the first and streams W and x
+// meanwhile, and waits for t only when it has come to the adapters.
+//
+// Both are the same tcgen05 kernel.  A tile is 128 rows of W (or the R rows of one A_a) by
+// NT rows of x: the weights are the M = 128 operand, so that a few rows of x waste no
+// tensor work and W streams through at the memory's rate.  The adapters of a tile's rows
+// are further blocks along K: B_a's 128 rows against t, where t stands as zeros for the
+// rows that have another adapter.  Only the columns from an adapter's first to its last row
+// in the tile are multiplied, so rows of one request that stand together cost what they
+// must, and rows in any order are right.  Each adapter is read once a tile.
+//
+// t goes in as the sum of two values of x's type (bf16 2^-17 relative; f16 2^-22 or 2^-25
+// absolute), so that its rounding does not count beside the output's own; that costs a few
+// products of K = 16 more.
+//
+// Few tiles split K and the adapters over the CTAs of a cluster, which join their f32 sums
+// through distributed shared memory in rank order: no atomics, no workspace but t, equal
+// calls give equal bits.  Many tiles run persistently, one CTA an SM, the next tile's
+// products under the last one's output.
+//
+// Warp 0: copies; warp 1: TMEM and products; warps 2-5: output; warps 6 and 7: which adapters
+// a tile has, and t's tiles.  Every wait is bounded; a timeout raises EMBER_ERR_TIMEOUT, the
+// CTA drains its copies and frees TMEM.
+#include <cudaTypedefs.h>
+
+#include "paged.cuh"
+#include "tc_common.cuh"
+
+namespace ember {
+
+namespace {
+
+constexpr int AD_THREADS = 256;
+constexpr int AD_M = 128;                        // rows of W in a tile
+constexpr int AD_BK = 64;                        // K of a block
+constexpr int AD_BUILD = 64;                     // threads of the last two warps
+constexpr int AD_SLICE = 32;                     // rows of x that are put out at a time
+constexpr int AD_LD = AD_M + 4;                  // their distance in shared memory, floats
+
+template <int NT, bool LOW>
+struct AdSmem {
+    static constexpr int A_BYTES = AD_M * 128, X_BYTES = NT * 128, STAGE = A_BYTES + X_BYTES;
+    // a tile of few rows leaves room for the other launch's CTA on the same SM
+    static constexpr int STAGES = NT == 256 ? 4 : NT == 128 ? 6 : LOW ? 3 : 5;
+    static constexpr int OUT = AD_SLICE * AD_LD * 4;
+    static constexpr int OFF_OUT = STAGES * STAGE;
+    static constexpr int OFF_LIST = OFF_OUT + OUT;           // [2][NT] entries
+    static constexpr int OFF_IDS = OFF_LIST + 2 * NT * 8;    // [2][NT]
+    static constexpr int OFF_BAR = OFF_IDS + 2 * NT * 4;
+    static constexpr int TOTAL = OFF_BAR + 320 + 1024;       // + alignment slack
+    static_assert(TOTAL <= 232448, "shared memory of a CTA");
+    static_assert(STAGES * STAGE >= NT * AD_LD * 4, "the cluster's sums");
+};
+
+// An adapter of a tile and the columns [c0, c1) of the tile, multiples of 16, that hold its rows.
+struct AdEntry {
+    int adapter;
+    uint16_t c0, c1;
+};
+
+// The adapters of rows [row0, row0 + NT) of ids in rising order, by one warp; their number.
+template <int NT>
+__device__ int list_adapters(const AdapterArgs& a, int row0, AdEntry* list, int* s_ids) {
+    constexpr int PER = (NT + 31) / 32;
+    const int lane = threadIdx.x & 31;
+    uint32_t id[PER];                            // none: all bits
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int c = k * 32 + lane, row = row0 + c;
+        int x = c < NT && row < a.n ? a.ids[row] : -1;
+        if (x >= a.n_adapters) {
+            raise_status(a.status, EMBER_ERR_INVALID_ARG);
+            x = -1;
+        }
+        id[k] = (uint32_t)x;
+        if (c < NT) s_ids[c] = x;
+    }
+    int n = 0;
+    uint32_t from = 0;
+    while (true) {
+        uint32_t least = ~0u, lo = ~0u, hi = 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (id[k] >= from && (int)id[k] >= 0) least = min(least, id[k]);
+        least = __reduce_min_sync(FULL_MASK, least);
+        if (least == ~0u) break;
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (id[k] == least) {
+                lo = min(lo, (uint32_t)(k * 32 + lane));
+                hi = (uint32_t)(k * 32 + lane + 1);
+            }
+        lo = __reduce_min_sync(FULL_MASK, lo);
+        hi = __reduce_max_sync(FULL_MASK, hi);
+        if (lane == 0) list[n] = AdEntry{(int)least, (uint16_t)(lo & ~15u), (uint16_t)((hi + 15u) & ~15u)};
+        ++n;
+        from = least + 1;
+    }
+    __syncwarp();
+    return n;
+}
+
+// Eight sums of a row of x.  First launch: ranks r .. r + 7 of its adapter, as two terms (and
+// zeros for the ranks that fill up a product); second: outputs m .. m + 7.  True: beyond f16.
+template <class E>
+__device__ __forceinline__ bool store_low(const AdapterArgs& a, int row, int r, int adapter, float (&y)[8]) {
+    const int RP = (a.R + 15) & ~15;
+    const float scale = a.scale ? a.scale[adapter] : 1.f;
+    uint16_t* t = a.t + (long long)row * 2 * RP + r;
+    uint32_t hi[4], lo[4];
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float u = y[2 * j] * scale, v = y[2 * j + 1] * scale;
+        if (!E::bf16) bad |= f16_out_of_range(u) | f16_out_of_range(v);
+        hi[j] = E::pack(u, v);
+        lo[j] = E::pack(u - E::lo(hi[j]), v - E::hi(hi[j]));
+    }
+    *reinterpret_cast<uint4*>(t) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(t + RP) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (r + 8 == a.R && a.R < RP) {
+        *reinterpret_cast<uint4*>(t + 8) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(t + RP + 8) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    return bad;
+}
+template <class E>
+__device__ __forceinline__ void store_out(const AdapterArgs& a, int row, int m, const float (&y)[8]) {
+    if (m >= a.N) return;
+    if (a.out_f32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * a.ld_out + m);
+        o[0] = make_float4(y[0], y[1], y[2], y[3]);
+        o[1] = make_float4(y[4], y[5], y[6], y[7]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.ld_out + m) =
+            make_uint4(E::pack(y[0], y[1]), E::pack(y[2], y[3]), E::pack(y[4], y[5]), E::pack(y[6], y[7]));
+    }
+}
+
+// (Two CTAs to an SM where they have room: one of each launch.)
+template <class E, int NT, bool LOW>
+__global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
+    k_adapter(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+              const __grid_constant__ CUtensorMap tmB, AdapterArgs a) {
+    using L = AdSmem<NT, LOW>;
+    constexpr int S = L::STAGES;
+    constexpr uint32_t COLS = 2 * NT < 32 ? 32 : 2 * NT;     // of TMEM: two accumulators
+    extern __shared__ uint8_t ad_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ad_raw) + 1023) & ~uintptr_t(1023));
+    float* s_out = reinterpret_cast<float*>(sm + L::OFF_OUT);
+    AdEntry* s_list = reinterpret_cast<AdEntry*>(sm + L::OFF_LIST);
+    int* s_ids = reinterpret_cast<int*>(sm + L::OFF_IDS);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
+    uint64_t* full = bar;                // [S] a stage's copies have landed
+    uint64_t* empty = bar + S;           // [S] its products are done
+    uint64_t* t_go = bar + 2 * S;        // [S] t's tile may be written there
+    uint64_t* t_full = bar + 3 * S;      // [S] it is
+    uint64_t* acc_full = bar + 4 * S;    // [2]
+    uint64_t* acc_empty = acc_full + 2;  // [2]
+    uint64_t* list_full = acc_empty + 2; // [2]
+    uint64_t* list_empty = list_full + 2;
+    int* s_count = reinterpret_cast<int*>(list_empty + 2);   // [2] entries of the lists
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_count + 2);
+    int* sflag = reinterpret_cast<int*>(tmem_slot + 1);      // [0] failed, [1] stages issued, [2] consumed
+    static_assert((4 * S + 8) * 8 + 6 * 4 <= 320, "barriers");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int C = a.splits, part = C > 1 ? (int)(blockIdx.x % C) : 0;
+    const int nk = (a.K + AD_BK - 1) / AD_BK;
+    const int kb0 = (int)((long long)nk * part / C), kb1 = (int)((long long)nk * (part + 1) / C);
+    const int start = (int)blockIdx.x / C, stride = (int)gridDim.x / C;   // tiles start, start + stride, ..
+    const int RP = (a.R + 15) & ~15;                          // ranks with those that fill up a product
+    const bool both = a.R <= 32;                              // both terms of t fit one stage
+    const int blocks = both ? 1 : 2 * ((RP + 63) / 64);       // stages of an adapter
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&t_go[s], 1);
+            mbar_init(&t_full[s], 2);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 4);
+            mbar_init(&list_full[b], 1);
+            mbar_init(&list_empty[b], 3);
+        }
+        sflag[0] = sflag[1] = sflag[2] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(COLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    // The second launch starts once every CTA of the first has come past its wait: what came
+    // before both is complete for it too.
+    if (LOW) {
+        pdl_wait();
+        pdl_trigger();
+        if (warp == 6) {                         // the CTA's one row tile
+            const int n = list_adapters<NT>(a, start % a.row_tiles * NT, s_list, s_ids);
+            if (lane == 0) s_count[0] = n;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // Its tiles.  In the first launch one holds as many of the list's adapters as have room in
+    // 128 rows, and the CTA takes every step-th of its row tile.
+    const int P = LOW ? AD_M / a.R : 1;
+    const int step = LOW ? stride / a.row_tiles : 1;
+    const int tiles = LOW ? max(0, ((s_count[0] + P - 1) / P - start / a.row_tiles + step - 1) / step)
+                          : max(0, (a.row_tiles * a.col_tiles - start + stride - 1) / stride);
+    struct Tile {
+        int row0, m0, e0;                        // first row of x, first row of W, first entry (first launch)
+    };
+    auto tile_of = [&](int li) {
+        Tile t;
+        const int i = start + li * stride;
+        t.row0 = i % a.row_tiles * NT;
+        t.m0 = LOW ? 0 : i / a.row_tiles * AD_M;
+        t.e0 = LOW ? i / a.row_tiles * P : 0;
+        return t;
+    };
+    // Row m .. m + 7 of the tile's sums of row c of x, wherever they belong.
+    bool bad = false;                            // f16: t beyond its range
+    auto store = [&](const Tile& t, int c, int m, float (&y)[8]) {
+        if (LOW) {
+            const int e = t.e0 + m / a.R;
+            if (m < P * a.R && e < s_count[0] && s_list[e].adapter == s_ids[c])
+                bad |= store_low<E>(a, t.row0 + c, m % a.R, s_ids[c], y);
+        } else {
+            store_out<E>(a, t.row0 + c, t.m0 + m, y);
+        }
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {   // ---------------- copies
+            int g = 0;                           // stages so far
+            bool ok = true;
+            auto slot = [&](int& s) {
+                s = g % S;
+                ok = g < S || mbar_wait(&empty[s], ((uint32_t)(g / S) & 1u) ^ 1u);
+                return ok;
+            };
+            for (int li = 0; li < tiles && ok; ++li) {
+                const Tile t = tile_of(li);
+                int s;
+                for (int kb = kb0; kb < kb1 && slot(s); ++kb, ++g) {
+                    uint8_t* p = sm + s * L::STAGE;
+                    const int n = LOW ? min(P, s_count[0] - t.e0) : 0;
+                    mbar_expect_tx(&full[s], (LOW ? n * a.R * 128 : L::A_BYTES) + L::X_BYTES);
+                    if (!LOW) tma_load_2d(p, &tmW, kb * AD_BK, t.m0, &full[s]);
+                    for (int e = 0; e < n; ++e)
+                        tma_load_3d(p + e * a.R * 128, &tmW, kb * AD_BK, 0, s_list[t.e0 + e].adapter, &full[s]);
+                    tma_load_2d(p + L::A_BYTES, &tmX, kb * AD_BK, t.row0, &full[s]);
+                }
+                if (LOW || !ok) continue;
+                const int b = li & 1;
+                ok = mbar_wait(&list_full[b], (uint32_t)(li >> 1) & 1u);
+                const int n = s_count[b];
+                for (int e = part; e < n && ok; e += C)
+                    for (int k = 0; k < blocks && slot(s); ++k, ++g) {
+                        mbar_expect_tx(&full[s], L::A_BYTES);
+                        tma_load_3d(sm + s * L::STAGE, &tmB, both ? 0 : (k >> 1) * 64, t.m0, s_list[b * NT + e].adapter, &full[s]);
+                        mbar_arrive(&t_go[s]);
+                    }
+                if (ok) mbar_arrive(&list_empty[b]);
+            }
+            if (!ok) sflag[0] = 1;
+            sflag[1] = g;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {   // ---------------- products
+            constexpr uint32_t type = E::bf16 ? idesc_bf16(0, 0) : idesc_f16(0, 0);
+            int g = 0;
+            uint32_t t_phase = 0;                // of t_full, a bit a slot
+            bool ok = true;
+            for (int li = 0; li < tiles && ok; ++li) {
+                const int b = li & 1;
+                ok = li < 2 || mbar_wait(&acc_empty[b], ((uint32_t)(li >> 1) & 1u) ^ 1u);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + (uint32_t)(b * NT);
+                for (int kb = kb0; kb < kb1; ++kb, ++g) {
+                    const int s = g % S;
+                    if (!(ok = mbar_wait(&full[s], (uint32_t)(g / S) & 1u))) break;
+                    tc_fence_after();
+                    const uint32_t w = smem_u32(sm + s * L::STAGE), x = w + L::A_BYTES;
+#pragma unroll
+                    for (int k = 0; k < AD_BK / 16; ++k)
+                        umma_bf16(acc, sdesc_sw128(w + k * 32), sdesc_sw128(x + k * 32), type | idesc_f16(AD_M, NT),
+                                  kb > kb0 || k > 0);
+                    umma_commit(&empty[s]);
+                }
+                if (!LOW && ok) {
+                    ok = mbar_wait(&list_full[b], (uint32_t)(li >> 1) & 1u);
+                    const int n = s_count[b];
+                    for (int e = part; e < n && ok; e += C) {
+                        const AdEntry en = s_list[b * NT + e];
+                        const uint32_t id = type | idesc_f16(AD_M, en.c1 - en.c0);
+                        for (int k = 0; k < blocks; ++k, ++g) {
+                            const int s = g % S;
+                            ok = mbar_wait(&full[s], (uint32_t)(g / S) & 1u) && mbar_wait(&t_full[s], t_phase >> s & 1u);
+                            if (!ok) break;
+                            t_phase ^= 1u << s;
+                            tc_fence_after();
+                            const uint32_t w = smem_u32(sm + s * L::STAGE), t = w + L::A_BYTES + en.c0 * 128;
+                            const int steps = both ? RP / 16 : min(4, RP / 16 - (k >> 1) * 4);
+                            for (int q = 0; q < steps; ++q) {
+                                umma_bf16(acc + en.c0, sdesc_sw128(w + q * 32), sdesc_sw128(t + q * 32), id, 1);
+                                if (both) umma_bf16(acc + en.c0, sdesc_sw128(w + q * 32), sdesc_sw128(t + 64 + q * 32), id, 1);
+                            }
+                            umma_commit(&empty[s]);
+                        }
+                    }
+                    if (ok) mbar_arrive(&list_empty[b]);
+                }
+                if (ok) umma_commit(&acc_full[b]);
+            }
+            if (!ok) sflag[0] = 1;
+            sflag[2] = g;
+        }
+    } else if (warp >= 6) {
+        if (!LOW) {   // -------------- which adapters a tile has, and t's tiles
+            const int tid = threadIdx.x - (AD_THREADS - AD_BUILD);
+            int g = 0;
+            uint32_t go_phase = 0;
+            bool ok = true, waited = false;
+            for (int li = 0; li < tiles && ok; ++li) {
+                const int b = li & 1;
+                const Tile t = tile_of(li);
+                if (warp == 6) {
+                    ok = li < 2 || mbar_wait(&list_empty[b], ((uint32_t)(li >> 1) & 1u) ^ 1u);
+                    if (ok) {
+                        const int n = list_adapters<NT>(a, t.row0, s_list + b * NT, s_ids + b * NT);
+                        if (lane == 0) {
+                            s_count[b] = n;
+                            mbar_arrive(&list_full[b]);
+                        }
+                    }
+                }
+                // (both warps see the phase; after a failure neither goes on)
+                ok = ok && mbar_wait(&list_full[b], (uint32_t)(li >> 1) & 1u);
+                if (!ok) break;
+                const int n = s_count[b];
+                const int* ids = s_ids + b * NT;
+                g += kb1 - kb0;
+                if (!waited) {                   // t is the first launch's
+                    pdl_wait();
+                    waited = true;
+                }
+                for (int e = part; e < n && ok; e += C) {
+                    const AdEntry en = s_list[b * NT + e];
+                    for (int k = 0; k < blocks; ++k, ++g) {
+                        const int s = g % S;
+                        if (!(ok = mbar_wait(&t_go[s], go_phase >> s & 1u))) break;
+                        go_phase ^= 1u << s;
+                        uint8_t* dst = sm + s * L::STAGE + L::A_BYTES;
+                        // 16-byte pieces of the rows: both terms at 0 and 64, or one term's 64 ranks
+                        const int q0 = both ? 0 : (k >> 1) * 8;              // first piece of the term's row
+                        const int per = both ? RP / 8 : min(8, RP / 8 - q0); // pieces of a term
+                        const int each = both ? 2 * per : per, term0 = both ? 0 : k & 1;
+                        const int total = (en.c1 - en.c0) * each;
+                        for (int i = tid; i < total; i += AD_BUILD) {
+                            const int c = en.c0 + i / each, p = i % each, term = term0 + p / per, q = p % per;
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (ids[c] == en.adapter)
+                                v = __ldcg(reinterpret_cast<const uint4*>(a.t + ((long long)(t.row0 + c) * 2 + term) * RP) + q0 + q);
+                            const int at = both ? term * 4 + q : q;
+                            *reinterpret_cast<uint4*>(dst + c * 128 + ((at ^ (c & 7)) << 4)) = v;
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&t_full[s]);
+                    }
+                }
+                __syncwarp();
+                if (warp == 7 && lane == 0) mbar_arrive(&list_empty[b]);
+            }
+            if (!waited) pdl_wait();             // this grid ends after the first one, whatever happens
+            if (!ok) sflag[0] = 1;
+        }
+    } else {   // ---------------- output, warps 2..5
+        const int quad = warp & 3, tid = threadIdx.x - 64;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        for (int li = 0; li < tiles; ++li) {
+            const int b = li & 1;
+            const Tile t = tile_of(li);
+            bool ok = mbar_wait(&acc_full[b], (uint32_t)(li >> 1) & 1u);
+            uint32_t all;                        // the barriers below need all four warps
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                         : "=r"(all)
+                         : "r"((uint32_t)ok)
+                         : "memory");
+            if (!all) {
+                sflag[0] = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + (uint32_t)(b * NT) + lane_off;
+            const int rows = min(NT, a.n - t.row0);
+            if (C > 1) {                         // the whole tile, joined below
+                float* dst = reinterpret_cast<float*>(sm) + quad * 32 + lane;
+                for (int c = 0; c < rows; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(acc + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) dst[(c + i) * AD_LD] = __uint_as_float(r[i]);
+                }
+                break;
+            }
+            const int f = tid % 16 * 8;          // this thread's 8 rows of W
+            float add[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) add[i] = 0.f;
+            if (!LOW && a.bias && t.m0 + f < a.N) {
+                const uint4 w = *reinterpret_cast<const uint4*>(a.bias + t.m0 + f);
+                unpack8w<!E::bf16>(w, add);
+            }
+            for (int c = 0; c < rows; c += AD_SLICE) {
+                uint32_t r[AD_SLICE];
+                tmem_ld16(acc + c, r);
+                if (NT >= AD_SLICE) tmem_ld16(acc + c + 16, r + 16);
+                tmem_ld_wait();
+                if (c + AD_SLICE >= rows) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[b]);
+                }
+#pragma unroll
+                for (int i = 0; i < AD_SLICE; ++i)
+                    if (NT >= AD_SLICE || i < 16) s_out[i * AD_LD + quad * 32 + lane] = __uint_as_float(r[i]);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                for (int i = tid / 16; i < min(AD_SLICE, rows - c); i += 8) {
+                    const float4* p = reinterpret_cast<const float4*>(s_out + i * AD_LD + f);
+                    const float4 u = p[0], v = p[1];
+                    float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] += add[j];
+                    store(t, c + i, f, y);
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
+        }
+    }
+    __syncwarp();
+
+    if (C > 1) {   // ---------------- the cluster's sums, a share of the tile for each CTA
+        cluster_sync_all();
+        if (tiles > 0) {                         // (the same for all of them)
+            const Tile t = tile_of(0);
+            const int rows = min(NT, a.n - t.row0);
+            const uint32_t at = smem_u32(sm);
+            const int all = rows * (AD_M / 8), lo = (int)((long long)all * part / C), hi = (int)((long long)all * (part + 1) / C);
+            for (int i = lo + (int)threadIdx.x; i < hi; i += AD_THREADS) {
+                const int c = i / (AD_M / 8), f = i % (AD_M / 8) * 8;
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = 0.f;
+                for (int p = 0; p < C; ++p)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 v = ld_cluster4(at + (c * AD_LD + f + 4 * h) * 4, p);
+                        y[4 * h] += v.x;
+                        y[4 * h + 1] += v.y;
+                        y[4 * h + 2] += v.z;
+                        y[4 * h + 3] += v.w;
+                    }
+                if (!LOW && a.bias && t.m0 + f < a.N) {
+                    float add[8];
+                    unpack8w<!E::bf16>(*reinterpret_cast<const uint4*>(a.bias + t.m0 + f), add);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] += add[j];
+                }
+                store(t, c, f, y);
+            }
+        }
+        cluster_sync_all();                      // no CTA leaves while its shared memory is read
+    }
+    if (bad) raise_status(a.status, EMBER_ERR_RANGE);
+    if (!LOW) pdl_trigger();
+
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && sflag[0]) {
+        raise_status(a.status, EMBER_ERR_TIMEOUT);
+        for (int g = max(sflag[2], sflag[1] - S); g < sflag[1]; ++g)   // copies in flight
+            (void)mbar_wait(&full[g % S], (uint32_t)(g / S) & 1u);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(COLS));
+    }
+}
+
+template <class E, int NT, bool LOW>
+cudaError_t launch_nt(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const AdapterArgs& a, int grid,
+                      cudaStream_t s) {
+    constexpr int SMEM = AdSmem<NT, LOW>::TOTAL;
+    auto k = k_adapter<E, NT, LOW>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    if (a.splits > 1) return launch_cluster_k(k, dim3(grid), dim3(AD_THREADS), SMEM, a.splits, s, w, x, b, a);
+    return launch_k(k, dim3(grid), dim3(AD_THREADS), SMEM, s, w, x, b, a);
+}
+template <class E, bool LOW>
+cudaError_t launch_low(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const AdapterArgs& a, int nt, int grid,
+                       cudaStream_t s) {
+    switch (nt) {
+        case 16: return launch_nt<E, 16, LOW>(w, x, b, a, grid, s);
+        case 32: return launch_nt<E, 32, LOW>(w, x, b, a, grid, s);
+        case 64: return launch_nt<E, 64, LOW>(w, x, b, a, grid, s);
+        case 128: return launch_nt<E, 128, LOW>(w, x, b, a, grid, s);
+    }
+    if constexpr (!LOW) return launch_nt<E, 256, LOW>(w, x, b, a, grid, s);
+    return cudaErrorInvalidValue;
+}
+template <class E>
+cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& p, cudaStream_t s) {
+    const auto& mw = *reinterpret_cast<const CUtensorMap*>(m.w);
+    const auto& mx = *reinterpret_cast<const CUtensorMap*>(m.x);
+    const auto& ma = *reinterpret_cast<const CUtensorMap*>(m.a);
+    const auto& mb = *reinterpret_cast<const CUtensorMap*>(m.b);
+    const auto& mxl = *reinterpret_cast<const CUtensorMap*>(m.x_low);
+    a.row_tiles = p.low_row_tiles;
+    a.col_tiles = 1;
+    a.splits = p.low_splits;
+    const cudaError_t e = launch_low<E, true>(ma, mxl, ma, a, p.low_nt, p.low_grid, s);
+    if (e != cudaSuccess) return e;
+    a.row_tiles = p.row_tiles;
+    a.col_tiles = p.col_tiles;
+    a.splits = p.splits;
+    return launch_low<E, false>(mw, mx, mb, a, p.nt, p.grid, s);
+}
+
+// Cycles of a block's products: 4 of M = 128, N = nt, K = 16.
+constexpr int block_cycles(int nt) { return nt == 256 ? 700 : 450; }
+
+}  // namespace
+
+AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms) {
+    AdapterPlan p{};
+    const int nk = (K + AD_BK - 1) / AD_BK;
+    p.col_tiles = (N + AD_M - 1) / AD_M;
+    // Few rows: one row tile, K split until the SMs are full.  Many rows: the tile and the
+    // split that end first, by rounds of tiles over the SMs.
+    long long best = -1;
+    for (int nt = 16; nt <= 256; nt *= 2) {
+        const int rt = (n + nt - 1) / nt;
+        if (nt < 128 && rt > 1) continue;
+        for (int c = 1; c <= 8 && c <= nk; c *= 2) {
+            const long long tiles = (long long)rt * p.col_tiles;
+            if (c > 1 && tiles * c > sms) break;
+            const long long rounds = (tiles * c + sms - 1) / sms;
+            const long long cost = rounds * ((nk + c - 1) / c) * block_cycles(nt) + (c > 1 ? 3000 : 0) + nt;
+            if (best < 0 || cost < best) {
+                best = cost;
+                p.nt = nt;
+                p.splits = c;
+                p.row_tiles = rt;
+                p.grid = (int)(c > 1 ? tiles * c : min(tiles, (long long)sms));
+            }
+        }
+        if (rt == 1) break;
+    }
+    p.low_nt = min(p.nt, 128);
+    p.low_row_tiles = (n + p.low_nt - 1) / p.low_nt;
+    const int most = (min(n_adapters, p.low_nt) + AD_M / R - 1) / (AD_M / R);   // tiles of a row tile
+    // rows of many requests together hold few adapters a tile: two are reckoned with
+    const int likely = p.low_row_tiles > 1 ? min(most, 2) : most;
+    p.low_splits = 1;
+    while (p.low_splits < 8 && (long long)p.low_row_tiles * likely * p.low_splits * 2 <= sms && nk >= 4 * p.low_splits &&
+           (long long)p.low_row_tiles * most * p.low_splits * 2 <= 4 * sms)
+        p.low_splits *= 2;
+    const int wide = p.low_splits > 1 ? most : (int)min((long long)most, (2ll * sms + p.low_row_tiles - 1) / p.low_row_tiles);
+    p.low_grid = p.low_row_tiles * wide * p.low_splits;
+    return p;
+}
+
+size_t adapter_ws(int n, int R) { return (size_t)n * 2 * ((R + 15) & ~15) * sizeof(uint16_t); }
+
+bool adapter_maps(const AdapterArgs& a, const AdapterPlan& p, const void* x, long long ld_x, const void* w, const void* la,
+                  const void* lb, AdapterMaps& m) {
+    const uint64_t K = a.K, N = a.N, R = a.R, n = a.n;
+    const uint64_t wd[2] = {K, N}, xd[2] = {K, n}, ad[3] = {K, R, (uint64_t)a.n_adapters}, bd[3] = {R, N, (uint64_t)a.n_adapters};
+    const uint64_t ws[1] = {K * 2}, xs[1] = {(uint64_t)ld_x * 2}, as[2] = {K * 2, K * R * 2}, bs[2] = {R * 2, R * N * 2};
+    const uint32_t wb[2] = {AD_BK, AD_M}, xb[2] = {AD_BK, (uint32_t)p.nt}, xl[2] = {AD_BK, (uint32_t)p.low_nt};
+    const uint32_t ab[3] = {AD_BK, (uint32_t)a.R, 1}, bb[3] = {64, AD_M, 1};
+    return encode_map_bf16(m.w, w, 2, wd, ws, wb) && encode_map_bf16(m.x, x, 2, xd, xs, xb) &&
+           encode_map_bf16(m.x_low, x, 2, xd, xs, xl) && encode_map_bf16(m.a, la, 3, ad, as, ab) &&
+           encode_map_bf16(m.b, lb, 3, bd, bs, bb);
+}
+
+cudaError_t launch_adapter(const AdapterMaps& m, const AdapterArgs& a, const AdapterPlan& p, bool bf16, cudaStream_t s) {
+    return bf16 ? launch_type<ElemBf16>(m, a, p, s) : launch_type<ElemF16>(m, a, p, s);
+}
+
+}  // namespace ember

@@ -41,4 +41,11 @@ ember_status check_words(const char* which, const P*... p) {
     return EMBER_OK;
 }
 
+inline ember_status check_rows(const char* what, const void* p, int64_t ld, int64_t cols) {
+    if (!p) PG_FAIL(EMBER_ERR_INVALID_ARG, "%s is NULL", what);
+    if (!aligned16(p)) PG_FAIL(EMBER_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
+    if (ld < cols || ld % 8) PG_FAIL(EMBER_ERR_INVALID_ARG, "row stride of %s must be a multiple of 8 and cover a row", what);
+    return EMBER_OK;
+}
+
 }  // namespace ember

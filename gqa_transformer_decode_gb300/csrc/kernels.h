@@ -440,6 +440,37 @@ struct SampleArgs {
 };
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
 
+// ---------------------------------------------------------------- adapters --
+// y = W x + bias + s_a B_a (A_a x) for each row x of a batch, a = ids[row]
+// (negative: none).  adapters.cu.
+struct AdapterArgs {
+    const int32_t* ids;          // [n]
+    int n, N, K, R, n_adapters;
+    const float* scale;          // [n_adapters] or nullptr (1)
+    const uint16_t* bias;        // [N] or nullptr
+    uint16_t* t;                 // [n][2][R rounded up to 16]: s_a A_a x in two terms
+    void* out;                   // [n][ld_out], f32 or x's type
+    long long ld_out;
+    int out_f32;
+    int* status;
+    // set by launch_adapter:
+    int row_tiles, col_tiles, splits;
+};
+// How a call is split: rows of x in a tile, tiles, CTAs that share a tile's K (splits) and
+// the grid, of the second launch and of the first (low_).
+struct AdapterPlan {
+    int nt, row_tiles, col_tiles, splits, grid;
+    int low_nt, low_row_tiles, low_splits, low_grid;
+};
+struct AdapterMaps {
+    alignas(64) unsigned char w[128], x[128], x_low[128], a[128], b[128];
+};
+AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms);
+size_t adapter_ws(int n, int R);
+bool adapter_maps(const AdapterArgs& a, const AdapterPlan& p, const void* x, long long ld_x, const void* w, const void* la,
+                  const void* lb, AdapterMaps& m);
+cudaError_t launch_adapter(const AdapterMaps& m, const AdapterArgs& a, const AdapterPlan& p, bool bf16, cudaStream_t s);
+
 // ------------------------------------------------------- log probabilities --
 // Per row of logits [n][ldl] (V used) at temperature t: the given token's log
 // probability and rank, the entropy, the `top` largest logits.  logprobs.cu.

@@ -56,13 +56,6 @@ ember_status check_heads(const ember_paged_kv* kv, int32_t n_heads) {
     return EMBER_OK;
 }
 
-ember_status check_rows(const char* what, const void* p, int64_t ld, int64_t cols) {
-    if (!p) PG_FAIL(EMBER_ERR_INVALID_ARG, "%s is NULL", what);
-    if (!aligned16(p)) PG_FAIL(EMBER_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
-    if (ld < cols || ld % 8) PG_FAIL(EMBER_ERR_INVALID_ARG, "row stride of %s must be a multiple of 8 and cover a row", what);
-    return EMBER_OK;
-}
-
 // Checks that the two attentions share; window 0 when it hides nothing.
 ember_status check_attention(const ember_paged_kv* kv, int32_t rows, int32_t n_heads, const void* q, int64_t ld_q,
                              const void* out, int64_t ld_out, const int32_t* lens, int32_t& window, int32_t& sinks,

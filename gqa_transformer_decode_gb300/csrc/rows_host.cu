@@ -1,5 +1,6 @@
-// rows_host.cu -- the C entry points of the operators on rows that need no cache:
-// log probabilities.  Argument checks before any device work, then one launch.
+// rows_host.cu -- the C entry points of the operators on rows that need no cache: log
+// probabilities, projections with adapters.  Argument checks before any device work, then
+// one or two launches.
 #include "entry.h"
 
 using namespace ember;
@@ -44,6 +45,63 @@ ember_status ember_logprobs(const void* logits, int32_t dtype, int32_t n, int32_
     if (e != cudaSuccess) return cuda_failed("no device", e);
     e = launch_logprobs(a, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_failed("logprobs launch failed", e);
+    return EMBER_OK;
+}
+
+size_t ember_adapter_workspace(int32_t n, int32_t rank) {
+    if (n <= 0 || n > (1 << 30) || rank < 8 || rank > 128 || rank % 8) return 0;
+    return adapter_ws(n, rank);
+}
+
+ember_status ember_adapter_project(const ember_adapters* ad, const void* x, int64_t ld_x, const void* w, const void* bias,
+                                   int32_t dtype, int32_t n, int32_t N, int32_t K, const int32_t* ids, void* out,
+                                   int32_t out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes,
+                                   int32_t* status, ember_stream_t stream) {
+    if (!ad) PG_FAIL(EMBER_ERR_INVALID_ARG, "adapters is NULL");
+    if (dtype != EMBER_BF16 && dtype != EMBER_F16) PG_FAIL(EMBER_ERR_INVALID_ARG, "dtype must be EMBER_BF16 or EMBER_F16");
+    if (out_dtype != dtype && out_dtype != EMBER_F32) PG_FAIL(EMBER_ERR_INVALID_ARG, "out_dtype must be dtype or EMBER_F32");
+    if (n < 0 || n > (1 << 30)) PG_FAIL(EMBER_ERR_INVALID_ARG, "bad number of rows");
+    if (N <= 0 || K <= 0 || N % 8 || K % 8) PG_FAIL(EMBER_ERR_INVALID_ARG, "N and K must be positive multiples of 8");
+    if (N > (1 << 28) || K > (1 << 28)) PG_FAIL(EMBER_ERR_UNSUPPORTED, "N or K > 2^28");
+    if (ad->n_adapters <= 0) PG_FAIL(EMBER_ERR_INVALID_ARG, "n_adapters must be > 0");
+    if (ad->rank <= 0 || ad->rank % 8) PG_FAIL(EMBER_ERR_INVALID_ARG, "rank must be a positive multiple of 8");
+    if (ad->rank > 128) PG_FAIL(EMBER_ERR_UNSUPPORTED, "rank > 128");
+    if (n == 0) return EMBER_OK;
+    if (!ad->a || !ad->b || !aligned16(ad->a) || !aligned16(ad->b))
+        PG_FAIL(EMBER_ERR_INVALID_ARG, "a and b must be given and 16-byte aligned");
+    if (!w || !aligned16(w) || !aligned16(bias)) PG_FAIL(EMBER_ERR_INVALID_ARG, "w must be given, w and bias 16-byte aligned");
+    if (!ids) PG_FAIL(EMBER_ERR_INVALID_ARG, "ids is NULL");
+    ember_status st = check_words("scale, ids and status", ad->scale, ids, status);
+    if (st != EMBER_OK) return st;
+    if ((st = check_rows("x", x, ld_x, K)) != EMBER_OK) return st;
+    if ((st = check_rows("out", out, ld_out, N)) != EMBER_OK) return st;
+    if (ld_x > (1ll << 36)) PG_FAIL(EMBER_ERR_UNSUPPORTED, "row stride of x > 2^36");
+    if (!workspace || !aligned16(workspace)) PG_FAIL(EMBER_ERR_INVALID_ARG, "workspace must be given and 16-byte aligned");
+    if (workspace_bytes < adapter_ws(n, ad->rank))
+        PG_FAIL(EMBER_ERR_CAPACITY, "workspace smaller than ember_adapter_workspace");
+    int sms = 0;
+    cudaError_t e = device_sms(&sms);
+    if (e != cudaSuccess) return cuda_failed("no device", e);
+    AdapterArgs a{};
+    a.ids = ids;
+    a.n = n;
+    a.N = N;
+    a.K = K;
+    a.R = ad->rank;
+    a.n_adapters = ad->n_adapters;
+    a.scale = ad->scale;
+    a.bias = static_cast<const uint16_t*>(bias);
+    a.t = static_cast<uint16_t*>(workspace);
+    a.out = out;
+    a.ld_out = ld_out;
+    a.out_f32 = out_dtype == EMBER_F32;
+    a.status = status;
+    const AdapterPlan plan = adapter_plan(n, N, K, a.R, a.n_adapters, sms);
+    AdapterMaps maps;
+    if (!adapter_maps(a, plan, x, ld_x, w, ad->a, ad->b, maps))
+        PG_FAIL(EMBER_ERR_UNSUPPORTED, "the driver takes no tensor map of these sizes and strides");
+    e = launch_adapter(maps, a, plan, dtype == EMBER_BF16, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_failed("adapter launch failed", e);
     return EMBER_OK;
 }
 

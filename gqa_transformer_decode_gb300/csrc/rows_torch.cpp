@@ -1,11 +1,17 @@
-// rows_torch.cpp -- the torch side of runtime.logprobs: checks of the tensors, allocation
-// of the outputs, and the call of the C entry point (include/ember.h).  Marshalling only,
-// compiled for the reason that paged_torch.cpp gives.
+// rows_torch.cpp -- the torch side of runtime.logprobs and runtime.Adapters: checks of the
+// tensors, allocation of what the caller did not pass, and the calls of the C entry points
+// (include/ember.h).  Marshalling only, compiled for the reason that paged_torch.cpp gives.
 #include "torch_args.h"
+
+#include <torch/csrc/Dtype.h>
+
+#include <memory>
 
 namespace {
 
 decltype(&ember_logprobs) f_logprobs = nullptr;
+decltype(&ember_adapter_project) f_project = nullptr;
+decltype(&ember_adapter_workspace) f_workspace = nullptr;
 
 struct Place {   // where a call runs
     c10::DeviceIndex device;
@@ -70,18 +76,121 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     });
 }
 
-// entries(logprobs, last_error, EmberError)
+// One runtime.Adapters: the C view of them and where their status word lives.
+struct Adapters {
+    ember_adapters c;
+    c10::DeviceIndex device;
+    at::ScalarType dtype;
+    int64_t K, N;
+    Tensor a, b, scale, status;
+    ember_stream_t home;             // the stream that status was allocated on
+};
+Adapters& adapters_of(PyObject* o) {
+    auto* p = static_cast<Adapters*>(PyCapsule_GetPointer(o, "ember.adapters"));
+    if (!p) throw python_error();
+    no_gradient(p->a, "a");          // at every call: a tensor may be asked for its gradient at any time
+    no_gradient(p->b, "b");
+    if (p->scale.defined()) no_gradient(p->scale, "scale");
+    return *p;
+}
+
+// adapters(a, b, scale, status)
+PyObject* adapters(PyObject*, PyObject* const* x, Py_ssize_t nargs) {
+    return guarded(nargs, 4, [&]() -> PyObject* {
+        const Tensor &a = tensor(x[0], "a"), &b = tensor(x[1], "b");
+        if (!a.is_cuda()) bad("a must be on a CUDA device, not " + a.device().str());
+        if (type_of(a.scalar_type()) < EMBER_BF16) throw Bad{PyExc_TypeError, "a and b must be bfloat16 or float16"};
+        if (a.dim() != 3 || b.dim() != 3) bad("a must be [n_adapters, rank, K], b [n_adapters, N, rank], not " + describe(a) + " and " + describe(b));
+        auto made = std::make_unique<Adapters>();
+        Adapters& p = *made;
+        p.device = a.device().index();
+        p.dtype = a.scalar_type();
+        p.K = a.size(2);
+        p.N = b.size(1);
+        p.c.a = flat(p, a, "a", p.dtype, a.sizes());
+        p.c.b = flat(p, b, "b", p.dtype, {a.size(0), p.N, a.size(1)});
+        p.c.scale = given(x[2]) ? static_cast<const float*>(flat(p, tensor(x[2], "scale"), "scale", at::kFloat, {a.size(0)})) : nullptr;
+        p.c.n_adapters = count(a.size(0), "a");
+        p.c.rank = count(a.size(1), "a");
+        p.a = a;
+        p.b = b;
+        if (given(x[2])) p.scale = tensor(x[2], "scale");
+        p.status = tensor(x[3], "status");
+        (void)flat(p, p.status, "status", at::kInt, {1});
+        p.home = stream_of({p.device});
+        return PyCapsule_New(made.release(), "ember.adapters",
+                             [](PyObject* o) { delete static_cast<Adapters*>(PyCapsule_GetPointer(o, "ember.adapters")); });
+    });
+}
+
+// project(adapters, x, w, ids, bias, out, out_dtype (a torch.dtype or None), workspace)
+PyObject* project(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+    return guarded(nargs, 8, [&]() -> PyObject* {
+        const Adapters& p = adapters_of(a[0]);
+        const Tensor &x = tensor(a[1], "x"), &w = tensor(a[2], "w");
+        on_device(p, x, "x");
+        const int64_t ld_x = matrix(x, "x"), n = x.size(0);
+        if (x.scalar_type() != p.dtype || x.size(1) != p.K)
+            bad(std::string("x must be ") + c10::toString(p.dtype) + " [n, " + std::to_string(p.K) + "], not " + describe(x));
+        const void* wp = flat(p, w, "w", p.dtype, {p.N, p.K});
+        const int32_t* ids = ints(p, a[3], "ids", n);
+        const void* bias = given(a[4]) ? flat(p, tensor(a[4], "bias"), "bias", p.dtype, {p.N}) : nullptr;
+        at::ScalarType ot = p.dtype;
+        if (given(a[6])) {
+            if (!THPDtype_Check(a[6])) throw Bad{PyExc_TypeError, "out_dtype must be a torch.dtype"};
+            ot = reinterpret_cast<THPDtype*>(a[6])->scalar_type;
+            if (ot != p.dtype && ot != at::kFloat) bad("out_dtype must be the adapters' type or float32");
+        }
+        const c10::cuda::OptionalCUDAGuard on(c10::Device(at::kCUDA, p.device));
+        Tensor out, ws;
+        int64_t ld_out = p.N;
+        if (given(a[5])) {
+            out = tensor(a[5], "out");
+            on_device(p, out, "out");
+            if (!given(a[6])) ot = out.scalar_type();
+            ld_out = matrix(out, "out");
+            if (out.scalar_type() != ot || (ot != p.dtype && ot != at::kFloat) || out.size(0) != n || out.size(1) != p.N)
+                bad(std::string("out must be ") + c10::toString(p.dtype) + " or Float [" + std::to_string(n) + ", " + std::to_string(p.N) +
+                    "], not " + describe(out));
+        } else {
+            out = make(p, {n, p.N}, ot);
+        }
+        if (n > 0) {
+            const size_t need = f_workspace(count(n, "x"), p.c.rank);
+            if (given(a[7])) {
+                ws = tensor(a[7], "workspace");
+                on_device(p, ws, "workspace");
+                if (ws.scalar_type() != at::kByte || !ws.is_contiguous()) bad("workspace must be contiguous uint8");
+            } else {
+                ws = make(p, {(int64_t)need}, at::kByte);
+            }
+            const ember_stream_t s = stream_of({p.device});
+            if (s != p.home)   // a kernel may raise an error when the object is gone: the word stays until then
+                c10::cuda::CUDACachingAllocator::recordStream(p.status.storage().data_ptr(), c10::cuda::getCurrentCUDAStream(p.device));
+            check(f_project(&p.c, x.data_ptr(), ld_x, wp, bias, type_of(p.dtype), count(n, "x"), count(p.N, "w"), count(p.K, "w"), ids,
+                            out.data_ptr(), type_of(ot), ld_out, ws.numel() ? ws.data_ptr() : nullptr, (size_t)ws.numel(),
+                            static_cast<int32_t*>(p.status.data_ptr()), s),
+                  "ember_adapter_project");
+            if (given(a[5])) written(out);
+        }
+        return THPVariable_Wrap(out);
+    });
+}
+
+// entries(logprobs, project, adapter_workspace, last_error, EmberError)
 PyObject* entries(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-    return guarded(nargs, 3, [&]() -> PyObject* {
+    return guarded(nargs, 5, [&]() -> PyObject* {
         f_logprobs = reinterpret_cast<decltype(f_logprobs)>(PyLong_AsVoidPtr(a[0]));
-        f_error = reinterpret_cast<decltype(f_error)>(PyLong_AsVoidPtr(a[1]));
-        Py_INCREF(a[2]);
-        ember_error = a[2];
+        f_project = reinterpret_cast<decltype(f_project)>(PyLong_AsVoidPtr(a[1]));
+        f_workspace = reinterpret_cast<decltype(f_workspace)>(PyLong_AsVoidPtr(a[2]));
+        f_error = reinterpret_cast<decltype(f_error)>(PyLong_AsVoidPtr(a[3]));
+        Py_INCREF(a[4]);
+        ember_error = a[4];
         Py_RETURN_NONE;
     });
 }
 
-PyMethodDef methods[] = {FAST("logprobs", logprobs), FAST("entries", entries), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FAST("logprobs", logprobs), FAST("adapters", adapters), FAST("project", project), FAST("entries", entries), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "rows_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -61,6 +61,10 @@ class ember_paged_kv(C.Structure):
                 ("head_stride", C.c_int64), ("row_stride", C.c_int64)]
 
 
+class ember_adapters(C.Structure):
+    _fields_ = [("a", P), ("b", P), ("scale", P), ("n_adapters", C.c_int32), ("rank", C.c_int32)]
+
+
 _lib = None
 
 
@@ -106,6 +110,9 @@ def load():
         "ember_gemv_argmax_noalloc": (st, [P, C.c_int32, C.c_int32, P, C.c_int32, P, P, P]),
         "ember_sample": (st, [P, C.c_int32, C.c_int32, C.c_int32, C.c_float, C.c_int32, C.c_float, P, P,
                               P]),
+        "ember_adapter_workspace": (C.c_size_t, [C.c_int32, C.c_int32]),
+        "ember_adapter_project": (st, [P, P, C.c_int64, P, P, C.c_int32, C.c_int32, C.c_int32, C.c_int32, P, P,
+                                       C.c_int32, C.c_int64, P, C.c_size_t, P, P]),
         "ember_logprobs": (st, [P, C.c_int32, C.c_int32, C.c_int32, C.c_int64, C.c_float, P, C.c_int32, P, P, P, P,
                                 P, P]),
         "ember_paged_append": (st, [P, P, P, P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_int32,
@@ -258,6 +265,16 @@ def ember_gemv_q8_0(q, d, N, K, x, nb, y, stream):
 
 def ember_sample(logits, B, V, ldl, temperature, top_k, top_p, r, out, stream):
     return load().ember_sample(logits, B, V, ldl, temperature, top_k, top_p, r, out, stream)
+
+
+def ember_adapter_workspace(n, rank) -> int:
+    return int(load().ember_adapter_workspace(n, rank))
+
+
+def ember_adapter_project(ad, x, ld_x, w, bias, dtype, n, N, K, ids, out, out_dtype, ld_out, workspace, workspace_bytes,
+                          status, stream):
+    return load().ember_adapter_project(ad, x, ld_x, w, bias, dtype, n, N, K, ids, out, out_dtype, ld_out, workspace,
+                                        workspace_bytes, status, stream)
 
 
 def ember_logprobs(logits, dtype, n, V, ldl, temperature, ids, top, logprob, rank, entropy, top_ids, top_logprobs,

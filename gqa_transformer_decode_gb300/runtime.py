@@ -191,9 +191,7 @@ class PagedKV:
         c.n_pages, c.page_size, c.n_kv_heads, c.head_dim = n_pages, page_size, self.n_kv_heads, self.head_dim
         c.n_seqs, c.table_width = table.shape
         c.page_stride, c.head_stride, c.row_stride = strides[0]
-        with torch.cuda.device(self.device):
-            self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
-            torch.cuda.current_stream().synchronize()   # zero before any stream uses it
+        self.status = _status_word(self.device)
         self._t = _paged_torch()
         self._cache = self._t.cache(C.addressof(c), self.status.data_ptr(), k_pages.get_device(), k_pages, v_pages,
                                     self.status)
@@ -252,9 +250,70 @@ class PagedKV:
         other streams raise meanwhile is returned now or by the next sync_status, never lost."""
         stream = torch.cuda.current_stream(self.device) if stream is None else stream
         with self._on(stream):
-            taken = torch.empty(1, dtype=torch.int32, device=self.device)
-            E.check(E.ember_paged_take_status(_ptr(self.status), _ptr(taken), _stream_ptr(stream)), "ember_paged_take_status")
-            return int(taken.item())
+            return _take_status(self.status, stream)
+
+
+def _status_word(device):
+    """An int32 on the device, zero before any stream uses it."""
+    with torch.cuda.device(device):
+        status = torch.zeros(1, dtype=torch.int32, device=device)
+        torch.cuda.current_stream().synchronize()
+    return status
+
+
+def _take_status(status, stream) -> int:
+    taken = torch.empty(1, dtype=torch.int32, device=stream.device)
+    E.check(E.ember_paged_take_status(_ptr(status), _ptr(taken), _stream_ptr(stream)), "ember_paged_take_status")
+    return int(taken.item())
+
+
+class Adapters:
+    """Low-rank adapters of one projection, for batches whose rows name different ones (include/ember.h,
+    "projections with adapters").
+
+    a      bf16 or f16 [n_adapters, rank, K]; rank a multiple of 8 up to 128
+    b      the same type, [n_adapters, N, rank]
+    scale  f32 [n_adapters] (default: 1 each)
+
+    All contiguous and the caller's; they may change between calls.  Streams, gradients and errors as in PagedKV:
+    calls are asynchronous on `stream` (default: the current one), tensors that require a gradient are refused
+    unless gradients are off, device-side errors are read with sync_status().
+    """
+
+    def __init__(self, a, b, scale=None):
+        for t, what in ((a, "a"), (b, "b")):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise ValueError(f"{what} must be a tensor on a CUDA device")
+        self.a, self.b, self.scale, self.device = a, b, scale, a.device
+        self.status = _status_word(self.device)
+        self._t = _rows_torch()
+        with torch.cuda.device(self.device):
+            self._adapters = self._t.adapters(a, b, scale, self.status)
+
+    def project(self, x, w, ids, bias=None, out=None, out_dtype=None, workspace=None, stream=None):
+        """x [n, K] through the projection w [N, K] (+ bias [N]) with the adapter ids[i] of row i beside it (int32
+        [n]; negative: none).  x, w and bias have the adapters' type.  Returns out [n, N] of that type, or of
+        out_dtype = torch.float32.  workspace: a uint8 tensor of at least workspace_bytes(n) (default: allocated)."""
+        if stream is None:
+            return self._t.project(self._adapters, x, w, ids, bias, out, out_dtype, workspace)
+        if stream.device != self.device:
+            raise ValueError(f"the stream belongs to {stream.device}, the adapters to {self.device}")
+        with torch.cuda.stream(stream):
+            r = self._t.project(self._adapters, x, w, ids, bias, out, out_dtype, workspace)
+        _keep_for(stream, x, w, ids, bias, out, workspace, self.a, self.b, self.scale)
+        return r
+
+    def workspace_bytes(self, n: int) -> int:
+        """Bytes of project's workspace for n rows."""
+        return E.ember_adapter_workspace(n, self.a.shape[1])
+
+    def sync_status(self, stream=None) -> int:
+        """Wait for the stream, return and clear the first device-side error (0: none), as in PagedKV."""
+        stream = torch.cuda.current_stream(self.device) if stream is None else stream
+        if stream.device != self.device:
+            raise ValueError(f"the stream belongs to {stream.device}, the adapters to {self.device}")
+        with torch.cuda.stream(stream):
+            return _take_status(self.status, stream)
 
 
 class Logprobs(typing.NamedTuple):
@@ -314,7 +373,8 @@ def _paged_torch():
 
 
 def _rows_torch():
-    return _torch_side("rows_torch", E._build.build_rows_ext, ("ember_logprobs",))
+    return _torch_side("rows_torch", E._build.build_rows_ext,
+                       ("ember_logprobs", "ember_adapter_project", "ember_adapter_workspace"))
 
 
 def _wrap_device(ptr: int, nbytes: int, device) -> torch.Tensor:

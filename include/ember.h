@@ -318,6 +318,45 @@ ember_status ember_logprobs(const void *logits, int32_t dtype, int32_t n, int32_
                             int32_t *rank, float *entropy, int32_t *top_ids, float *top_logprobs,
                             ember_stream_t stream);
 
+/* ---- projections with adapters -------------------------------------------- */
+
+/* A projection that all rows share (ember reference_forward.py forward(): q = Wq x
+ * and the others) with a low-rank adapter of each row's own beside it:
+ *   out_i = W x_i + bias + s_a B_a (A_a x_i),   a = ids[i]   (negative: W x_i + bias)
+ * for a batch whose rows belong to requests with different adapters, in any order.
+ *   x    [n] rows of K elements of `dtype` (BF16 or F16), ld_x apart
+ *   w    [N][K], bias [N] or NULL, of dtype;  ids [n] int32
+ *   a    [n_adapters][rank][K], b [n_adapters][N][rank] of dtype, scale
+ *        [n_adapters] f32 or NULL (1).  Adapters of a lower rank are filled up with
+ *        zeros.  rank is a multiple of 8 up to 128; N and K are multiples of 8.
+ *   out  [n] rows of N elements of out_dtype (dtype or F32), ld_out apart
+ *   workspace: ember_adapter_workspace(n, rank) bytes, 16-byte aligned, of any
+ *        content; used until the call's kernels end, so calls that may overlap need
+ *        one each.
+ *   status: as for the paged operators below; INVALID_ARG for an id >= n_adapters
+ *        (the row then goes without adapter), RANGE for f16 where an element of
+ *        s_a A_a x lies beyond the type's range (its row is then not finite), TIMEOUT.
+ * Products are taken on the type and summed in f32; s_a A_a x is held as the sum of
+ * two values of the type (2^-17 relative for bf16, 2^-22 or 2^-25 absolute for f16).
+ * Element pointers are 16-byte aligned, scale, ids and status 4-byte; row strides
+ * multiples of 8 elements; buffers may not overlap.  A b that is not finite makes
+ * not finite not only the rows that name its adapter but also rows with others
+ * that stand between two of those, as a product with zero does.  No
+ * atomics: equal calls give equal bits.  Asynchronous on `stream`; no gradient.
+ * Host errors: INVALID_ARG, UNSUPPORTED, CAPACITY (workspace), CUDA. */
+typedef struct ember_adapters {
+    const void *a, *b;
+    const float *scale;
+    int32_t n_adapters, rank;
+} ember_adapters;
+size_t ember_adapter_workspace(int32_t n, int32_t rank);
+ember_status ember_adapter_project(const ember_adapters *ad, const void *x, int64_t ld_x,
+                                   const void *w, const void *bias, int32_t dtype, int32_t n,
+                                   int32_t N, int32_t K, const int32_t *ids, void *out,
+                                   int32_t out_dtype, int64_t ld_out, void *workspace,
+                                   size_t workspace_bytes, int32_t *status,
+                                   ember_stream_t stream);
+
 /* ---- paged key/value cache ------------------------------------------------ */
 
 /* Three operators on one pool of K/V pages that many sequences share, for a

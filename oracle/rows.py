@@ -33,3 +33,19 @@ def logprobs(logits, temperature=1.0):
         some = lp[r] > -np.inf
         entropy[r] = -(np.exp(lp[r][some]) * lp[r][some]).sum()
     return lp, entropy
+
+
+def project(x, w, a, b, scale, ids, bias=None):
+    """x [n, K] through w [N, K] with adapter ids[i] (a [A, R, K], b [A, N, R]) beside it.  Returns the outputs and,
+    for error bounds, sums of magnitudes: |w| |x|, |s| |b| |a| |x| and |s| |b| summed over ranks, all [n, N]."""
+    x, w, a, b = (np.asarray(t, np.float64) for t in (x, w, a, b))
+    y, size = x @ w.T, np.abs(x) @ np.abs(w).T
+    low, ranks = np.zeros_like(y), np.zeros_like(y)
+    for i, k in enumerate(np.asarray(ids)):
+        if not 0 <= k < len(a):
+            continue
+        s = 1.0 if scale is None else float(scale[k])
+        y[i] += b[k] @ (a[k] @ x[i]) * s
+        low[i] = np.abs(b[k]) @ (np.abs(a[k]) @ np.abs(x[i])) * abs(s)
+        ranks[i] = np.abs(b[k]).sum(-1)
+    return (y if bias is None else y + np.asarray(bias, np.float64)), size, low, ranks

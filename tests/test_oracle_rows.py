@@ -27,3 +27,15 @@ def test_uniform_and_undefined_rows():
 def test_order():
     assert O.order([1.0, np.nan, 3.0, 3.0, -np.inf, np.inf, np.nan]).tolist() == [1, 6, 5, 2, 3, 0, 4]
     assert O.order([0.0, -0.0, 0.0]).tolist() == [0, 1, 2]
+
+
+def test_project_against_torch():
+    g = torch.Generator().manual_seed(2)
+    x, w, a, b = (torch.randn(*s, generator=g, dtype=torch.float64) for s in ((6, 10), (7, 10), (3, 2, 10), (3, 7, 2)))
+    s, bias = torch.rand(3, generator=g).double(), torch.randn(7, generator=g).double()
+    ids = torch.tensor([0, 2, -1, 1, 2, 5])
+    y, size, low, ranks = O.project(x, w, a, b, s, ids, bias)
+    full = torch.stack([w + s[k] * b[k] @ a[k] if 0 <= k < 3 else w for k in ids.tolist()])
+    want = torch.einsum("nok,nk->no", full, x) + bias
+    assert np.allclose(y, want.numpy(), rtol=1e-12, atol=1e-12)
+    assert (size + low >= np.abs(y - bias.numpy()) - 1e-12).all() and (ranks[2] == 0).all() and (ranks[0] > 0).all()
