@@ -539,6 +539,10 @@ struct PagedDecodeArgs {
     float* lse;                  // [B][NH] or nullptr
     float* ws;                   // records and partials, paged_decode_ws bytes
     int* status;
+    // shared prefixes (groups nullptr: none): rows groups[i] .. groups[i + 1] - 1 read keys
+    // below shared[i] from table row prefixes[i]; no window then
+    const int32_t *groups, *shared, *prefixes;
+    int n_groups;
     // set by launch_paged_decode:
     int split;                   // CTAs that share a long sequence in cluster form
     int by_pair;                 // records stand by (sequence, kv head)

@@ -62,19 +62,40 @@ constexpr int PD_MAX_CTAS = 512;     // grid at most (the join's weights stand i
 template <int DP>
 constexpr int PD_KEYS = DP == 64 ? 32 : 16;
 
+// What a row's keys lie in: its own pages, or those of its group's prefix up to `from` and
+// its own from there on.
+enum PdShare : int { PD_OWN = 0, PD_SHARED = 1 };
+
 // Blocks of one sequence: [0, ns) hold its sinks, the rest its window.
 struct SeqBlocks {
     int n, ns, wb;       // blocks, blocks of the sinks, first block of the window
     int end, first, sinks;
+    int from, prefix;    // PD_SHARED: keys below `from` are those of table row `prefix`
     bool zero;           // nothing visible: the output is zero
     __device__ __forceinline__ int index(int i) const { return i < ns ? i : wb + i - ns; }
 };
 
-template <int KEYS>
-__device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int seq, int len, bool report) {
+// The group of row b, if it is in one and its prefix is valid: its shared keys and their table row.
+__device__ __forceinline__ int shared_prefix(const PagedDecodeArgs& a, int b, int& from, int& prefix) {
+    int lo = 0;
+    for (int hi = a.n_groups; hi - lo > 1;) {
+        const int mid = (lo + hi) / 2;
+        if (a.groups[mid] <= b) lo = mid;
+        else hi = mid;
+    }
+    if (a.groups[lo] > b || b >= a.groups[lo + 1]) return EMBER_ERR_INVALID_ARG;
+    from = a.shared[lo];
+    prefix = a.prefixes[lo];
+    if (prefix < 0 || prefix >= a.c.n_seqs) return EMBER_ERR_INVALID_ARG;
+    if (from < 0 || from > ((long long)a.c.width << a.c.page_shift)) return EMBER_ERR_CAPACITY;
+    return EMBER_OK;
+}
+
+template <int KEYS, int SHARE>
+__device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int b, int seq, int len, bool report) {
     SeqBlocks r;
     r.n = 0;
-    r.ns = r.wb = r.end = r.first = r.sinks = 0;
+    r.ns = r.wb = r.end = r.first = r.sinks = r.from = r.prefix = 0;
     r.zero = false;
     if (seq < 0) return r;                                   // padding: the row is left as it is
     if (seq >= a.c.n_seqs) {
@@ -84,6 +105,13 @@ __device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int se
     if (len < 0 || len > ((long long)a.c.width << a.c.page_shift)) {
         if (report) raise_status(a.status, EMBER_ERR_CAPACITY);
         return r;
+    }
+    if (SHARE != PD_OWN) {
+        const int e = shared_prefix(a, b, r.from, r.prefix);
+        if (e != EMBER_OK) {
+            if (report) raise_status(a.status, e);
+            return r;
+        }
     }
     if (len == 0) {
         r.zero = true;
@@ -99,9 +127,9 @@ __device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int se
     return r;
 }
 
-template <int KEYS>
+template <int KEYS, int SHARE>
 __device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int b, bool report) {
-    return seq_blocks<KEYS>(a, a.seqs ? a.seqs[b] : b, a.lens[b], report);
+    return seq_blocks<KEYS, SHARE>(a, b, a.seqs ? a.seqs[b] : b, a.lens[b], report);
 }
 
 // Blocks of the whole line divided over `ctas` CTAs: CTA c takes [lo(c), lo(c + 1)).
@@ -120,7 +148,7 @@ struct Shares {
 // Every warp by itself: the line's length, and in which sequence block `x`
 // (known once the length is: at(total)) lies.  Four sequences a lane, 128 at a time.
 constexpr int PD_SCAN = 4;
-template <int KEYS>
+template <int KEYS, int SHARE>
 __device__ __forceinline__ unsigned scan_chunk(const PagedDecodeArgs& a, int b0, bool report, int (&n)[PD_SCAN],
                                                unsigned& before) {
     const int lane = threadIdx.x & 31;
@@ -134,7 +162,7 @@ __device__ __forceinline__ unsigned scan_chunk(const PagedDecodeArgs& a, int b0,
     }
 #pragma unroll
     for (int e = 0; e < PD_SCAN; ++e) {
-        n[e] = seq_blocks<KEYS>(a, seq[e], len[e], report).n;
+        n[e] = seq_blocks<KEYS, SHARE>(a, b0 + PD_SCAN * lane + e, seq[e], len[e], report).n;
         own += n[e];
     }
     unsigned incl = own;
@@ -172,7 +200,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 // HT: tiles of 8 query heads (1 up to G = 8, else 2)
-template <class E, int DP, int HT, bool CLUSTER>
+template <class E, int DP, int HT, bool CLUSTER, int SHARE>
 __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode(PagedDecodeArgs a) {
     constexpr int KEYS = PD_KEYS<DP>, NSUB = KEYS / 16;
     constexpr int KS = DP / 16, C8 = DP / 8;
@@ -198,7 +226,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
     int4* record = reinterpret_cast<int4*>(a.ws);
     auto no_keys = [&]() {                             // sequences without blocks, shared out over the CTAs
         for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-            const SeqBlocks s = seq_blocks<KEYS>(a, b, false);
+            const SeqBlocks s = seq_blocks<KEYS, SHARE>(a, b, false);
             if (s.zero) zero_row(b, 0, a.NH);
             if (a.by_pair && s.n == 0)
                 for (int g = tid; g < NKV; g += PD_THREADS) record[b * NKV + g] = make_int4(0, 0, 0, 0);
@@ -211,7 +239,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
     if (CLUSTER) {
         cur.b = blockIdx.z;
         cur.g = blockIdx.y;
-        cur.s = seq_blocks<KEYS>(a, cur.b, blockIdx.x == 0 && cur.g == 0 && tid == 0);
+        cur.s = seq_blocks<KEYS, SHARE>(a, cur.b, blockIdx.x == 0 && cur.g == 0 && tid == 0);
         if (cur.s.n == 0) {                            // so for the whole cluster
             if (cur.s.zero && blockIdx.x == 0) zero_row(cur.b, cur.g * G, (cur.g + 1) * G);
             return;
@@ -225,7 +253,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
     } else {
         int n[PD_SCAN];
         unsigned line = 0, before = 0;
-        for (int b0 = 0; b0 < a.B; b0 += 32 * PD_SCAN) line += scan_chunk<KEYS>(a, b0, blockIdx.x == 0 && warp == 0, n, before);
+        for (int b0 = 0; b0 < a.B; b0 += 32 * PD_SCAN) line += scan_chunk<KEYS, SHARE>(a, b0, blockIdx.x == 0 && warp == 0, n, before);
         line *= NKV;
         const Shares share(max(1u, line), gridDim.x);
         if (line == 0 || blockIdx.x >= share.ctas) {
@@ -239,7 +267,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
         unsigned run = 0;
         for (int b0 = 0;; b0 += 32 * PD_SCAN) {
             // one chunk: its counts are still in the registers
-            const unsigned total = a.B <= 32 * PD_SCAN ? line / NKV : scan_chunk<KEYS>(a, b0, false, n, before);
+            const unsigned total = a.B <= 32 * PD_SCAN ? line / NKV : scan_chunk<KEYS, SHARE>(a, b0, false, n, before);
             if (lo < run + total * NKV) {
                 unsigned at = run + before * NKV;
                 int b = -1;
@@ -254,7 +282,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
                 }
                 const int src = __ffs(__ballot_sync(FULL_MASK, b >= 0)) - 1;
                 cur.b = __shfl_sync(FULL_MASK, b, src);
-                cur.s = seq_blocks<KEYS>(a, cur.b, false);
+                cur.s = seq_blocks<KEYS, SHARE>(a, cur.b, false);
                 const unsigned x = lo - __shfl_sync(FULL_MASK, first, src);
                 cur.g = (int)(x / (unsigned)cur.s.n);
                 cur.i = (int)(x - (unsigned)cur.g * (unsigned)cur.s.n);
@@ -270,7 +298,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
             p.i -= p.s.n;
             if (++p.g == NKV) {
                 p.g = 0;
-                do p.s = seq_blocks<KEYS>(a, ++p.b, false);
+                do p.s = seq_blocks<KEYS, SHARE>(a, ++p.b, false);
                 while (p.s.n == 0 && p.b + 1 < a.B);
             }
         }
@@ -282,6 +310,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
     const uint32_t ring_u = sa_u32(ring);
     Place ld = cur;
     int ld_page[NSUB];                       // pages of its 16-key parts, looked up one block ahead
+    int ld_before[NSUB];                     // PD_SHARED: those of the part's keys below `from`
     auto look_up = [&]() {
         const int seq = a.seqs ? a.seqs[ld.b] : ld.b;
         const int key0 = KEYS * ld.s.index(ld.i);
@@ -289,7 +318,10 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
         for (int u = 0; u < NSUB; ++u) {
             const int k0 = key0 + 16 * u;    // a part that nobody sees has no page
             const bool any = k0 < ld.s.end && (k0 + 16 > ld.s.first || k0 < ld.s.sinks);
-            ld_page[u] = any ? a.c.table[(size_t)seq * a.c.width + (k0 >> a.c.page_shift)] : 0;
+            const bool own = SHARE == PD_OWN || (k0 + 16 > ld.s.from && ld.s.end > ld.s.from);
+            ld_page[u] = any && own ? a.c.table[(size_t)seq * a.c.width + (k0 >> a.c.page_shift)] : 0;
+            if (SHARE == PD_SHARED)
+                ld_before[u] = any && k0 < ld.s.from ? a.c.table[(size_t)ld.s.prefix * a.c.width + (k0 >> a.c.page_shift)] : 0;
         }
     };
     if (mine > 0) {
@@ -306,16 +338,24 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
                 const int k0 = key0 + 16 * u;
                 const bool ok = ld_page[u] >= 0 && ld_page[u] < a.c.n_pages;   // a bad page reads as zeros
                 if (!ok && lane == 0) raise_status(a.status, EMBER_ERR_INVALID_ARG);
-                const long long base =
-                    ok ? (long long)ld_page[u] * a.c.page_stride + (long long)ld.g * a.c.head_stride +
-                             (long long)(k0 & ((1 << a.c.page_shift) - 1)) * a.c.row_stride + c * 8
-                       : 0;
+                const long long in_page =
+                    (long long)ld.g * a.c.head_stride + (long long)(k0 & ((1 << a.c.page_shift) - 1)) * a.c.row_stride + c * 8;
+                const long long base = ok ? (long long)ld_page[u] * a.c.page_stride + in_page : 0;
+                bool ok_before = true;
+                long long before = 0;
+                if (SHARE == PD_SHARED) {
+                    ok_before = ld_before[u] >= 0 && ld_before[u] < a.c.n_pages;
+                    if (!ok_before && lane == 0) raise_status(a.status, EMBER_ERR_INVALID_ARG);
+                    before = ok_before ? (long long)ld_before[u] * a.c.page_stride + in_page : 0;
+                }
 #pragma unroll
                 for (int i = 0; i < 16 * C8 / 32; ++i) {
                     const int r = lane / C8 + i * (32 / C8);
                     const int key = k0 + r;
-                    const bool in = ok && c * 8 < D && key < ld.s.end && (key >= ld.s.first || key < ld.s.sinks);
-                    const long long off = in ? base + (long long)r * a.c.row_stride : 0;
+                    const bool shared = SHARE == PD_SHARED && key < ld.s.from;
+                    const bool in =
+                        (shared ? ok_before : ok) && c * 8 < D && key < ld.s.end && (key >= ld.s.first || key < ld.s.sinks);
+                    const long long off = in ? (shared ? before : base) + (long long)r * a.c.row_stride : 0;
                     cp_async16(kd + q_off<DP>(16 * u + r, c), a.c.k + off, in);
                     cp_async16(vd + q_off<DP>(16 * u + r, c), a.c.v + off, in);
                 }
@@ -735,18 +775,18 @@ PdPlan pd_plan(const PagedView& c, int B, int NH, int window, int sinks, int sms
     return {0, 0, (int)min((long long)full, (blocks * pairs + PD_MIN_BLOCKS - 1) / PD_MIN_BLOCKS)};
 }
 
-template <class E, int DP, int HT>
+template <class E, int DP, int HT, int SHARE>
 cudaError_t launch_ht(PagedDecodeArgs a, int sms, cudaStream_t s) {
     constexpr int SMEM = PdSmem<DP, HT>::TOTAL;
     const PdPlan plan = pd_plan(a.c, a.B, a.NH, a.window, a.sinks, sms);
     a.split = plan.split;
     if (plan.cluster) {
-        auto k = k_paged_decode<E, DP, HT, true>;
+        auto k = k_paged_decode<E, DP, HT, true, SHARE>;
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (e != cudaSuccess) return e;
         return launch_cluster_k(k, dim3(plan.cluster, a.c.NKV, a.B), dim3(PD_THREADS), SMEM, plan.cluster, s, a);
     }
-    auto k = k_paged_decode<E, DP, HT, false>;
+    auto k = k_paged_decode<E, DP, HT, false, SHARE>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     a.by_pair = (long long)a.B * a.c.NKV < plan.grid;
@@ -761,7 +801,8 @@ cudaError_t launch_ht(PagedDecodeArgs a, int sms, cudaStream_t s) {
 
 template <class E, int DP>
 cudaError_t launch_dp(const PagedDecodeArgs& a, int sms, cudaStream_t s) {
-    return a.NH / a.c.NKV <= 8 ? launch_ht<E, DP, 1>(a, sms, s) : launch_ht<E, DP, 2>(a, sms, s);
+    if (a.groups) return a.NH / a.c.NKV <= 8 ? launch_ht<E, DP, 1, PD_SHARED>(a, sms, s) : launch_ht<E, DP, 2, PD_SHARED>(a, sms, s);
+    return a.NH / a.c.NKV <= 8 ? launch_ht<E, DP, 1, PD_OWN>(a, sms, s) : launch_ht<E, DP, 2, PD_OWN>(a, sms, s);
 }
 
 }  // namespace

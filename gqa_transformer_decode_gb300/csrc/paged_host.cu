@@ -74,6 +74,48 @@ ember_status check_attention(const ember_paged_kv* kv, int32_t rows, int32_t n_h
     return check_rows("out", out, ld_out, (int64_t)n_heads * kv->head_dim);
 }
 
+// Attention of one token per sequence; a.groups and what goes with it are set.
+ember_status decode(const ember_paged_kv* kv, PagedDecodeArgs& a, const void* q, int64_t ld_q, int32_t B, int32_t n_heads,
+                    const int32_t* seqs, const int32_t* lens, int32_t window, int32_t sinks, float scale, void* out,
+                    int64_t ld_out, float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                    ember_stream_t stream) {
+    ember_status st = check_cache(kv, a.c);
+    if (st != EMBER_OK) return st;
+    st = check_attention(kv, B, n_heads, q, ld_q, out, ld_out, lens, window, sinks, scale);
+    if (st != EMBER_OK) return st;
+    if (B == 0) return EMBER_OK;
+    if (B > 65535) PG_FAIL(EMBER_ERR_UNSUPPORTED, "B > 65535");
+    if (!seqs && B > kv->n_seqs) PG_FAIL(EMBER_ERR_INVALID_ARG, "B > n_seqs without seqs");
+    if ((st = check_words("seqs, lens, lse and status", seqs, lens, lse, status)) != EMBER_OK) return st;
+    if (kv->n_kv_heads > 65535 ||
+        (double)B * kv->n_kv_heads * ((double)kv->table_width * kv->page_size / 16) > (double)(1 << 30))
+        PG_FAIL(EMBER_ERR_UNSUPPORTED, "B * n_kv_heads * table_width * page_size > 2^34");
+    int sms = 0;
+    cudaError_t e = device_sms(&sms);
+    if (e != cudaSuccess) return cuda_failed("no device", e);
+    const size_t need = paged_decode_ws(a.c, B, n_heads, window, sinks, sms);
+    if ((need && !workspace) || !aligned16(workspace))
+        PG_FAIL(EMBER_ERR_INVALID_ARG, "workspace must be given and 16-byte aligned");
+    if (workspace_bytes < need) PG_FAIL(EMBER_ERR_CAPACITY, "workspace smaller than ember_paged_decode_workspace");
+    a.q = static_cast<const uint16_t*>(q);
+    a.ld_q = ld_q;
+    a.B = B;
+    a.NH = n_heads;
+    a.seqs = seqs;
+    a.lens = lens;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale = scale;
+    a.out = static_cast<uint16_t*>(out);
+    a.ld_out = ld_out;
+    a.lse = lse;
+    a.ws = static_cast<float*>(workspace);
+    a.status = status;
+    e = launch_paged_decode(a, sms, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_failed("decode launch failed", e);
+    return EMBER_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -151,41 +193,32 @@ ember_status ember_paged_decode(const ember_paged_kv* kv, const void* q, int64_t
                                 void* out, int64_t ld_out, float* lse, void* workspace, size_t workspace_bytes,
                                 int32_t* status, ember_stream_t stream) {
     PagedDecodeArgs a{};
-    ember_status st = check_cache(kv, a.c);
-    if (st != EMBER_OK) return st;
-    st = check_attention(kv, B, n_heads, q, ld_q, out, ld_out, lens, window, sinks, scale);
-    if (st != EMBER_OK) return st;
-    if (B == 0) return EMBER_OK;
-    if (B > 65535) PG_FAIL(EMBER_ERR_UNSUPPORTED, "B > 65535");
-    if (!seqs && B > kv->n_seqs) PG_FAIL(EMBER_ERR_INVALID_ARG, "B > n_seqs without seqs");
-    if ((st = check_words("seqs, lens, lse and status", seqs, lens, lse, status)) != EMBER_OK) return st;
-    if (kv->n_kv_heads > 65535 ||
-        (double)B * kv->n_kv_heads * ((double)kv->table_width * kv->page_size / 16) > (double)(1 << 30))
-        PG_FAIL(EMBER_ERR_UNSUPPORTED, "B * n_kv_heads * table_width * page_size > 2^34");
-    int sms = 0;
-    cudaError_t e = device_sms(&sms);
-    if (e != cudaSuccess) return cuda_failed("no device", e);
-    const size_t need = paged_decode_ws(a.c, B, n_heads, window, sinks, sms);
-    if ((need && !workspace) || !aligned16(workspace))
-        PG_FAIL(EMBER_ERR_INVALID_ARG, "workspace must be given and 16-byte aligned");
-    if (workspace_bytes < need) PG_FAIL(EMBER_ERR_CAPACITY, "workspace smaller than ember_paged_decode_workspace");
-    a.q = static_cast<const uint16_t*>(q);
-    a.ld_q = ld_q;
-    a.B = B;
-    a.NH = n_heads;
-    a.seqs = seqs;
-    a.lens = lens;
-    a.window = window;
-    a.sinks = sinks;
-    a.scale = scale;
-    a.out = static_cast<uint16_t*>(out);
-    a.ld_out = ld_out;
-    a.lse = lse;
-    a.ws = static_cast<float*>(workspace);
-    a.status = status;
-    e = launch_paged_decode(a, sms, (cudaStream_t)stream);
-    if (e != cudaSuccess) return cuda_failed("decode launch failed", e);
-    return EMBER_OK;
+    return decode(kv, a, q, ld_q, B, n_heads, seqs, lens, window, sinks, scale, out, ld_out, lse, workspace, workspace_bytes,
+                  status, stream);
+}
+
+size_t ember_paged_decode_shared_workspace(const ember_paged_kv* kv, int32_t B, int32_t n_heads, int32_t n_groups) {
+    return n_groups <= 0 || n_groups > B ? 0 : ember_paged_decode_workspace(kv, B, n_heads);
+}
+
+ember_status ember_paged_decode_shared(const ember_paged_kv* kv, const void* q, int64_t ld_q, int32_t B, int32_t n_heads,
+                                       const int32_t* seqs, const int32_t* lens, const int32_t* groups,
+                                       const int32_t* shared, const int32_t* prefixes, int32_t n_groups, float scale,
+                                       void* out, int64_t ld_out, float* lse, void* workspace, size_t workspace_bytes,
+                                       int32_t* status, ember_stream_t stream) {
+    PagedDecodeArgs a{};
+    if (B > 0) {
+        if (n_groups <= 0 || n_groups > B) PG_FAIL(EMBER_ERR_INVALID_ARG, "n_groups must be in [1, B]");
+        if (!groups || !shared || !prefixes) PG_FAIL(EMBER_ERR_INVALID_ARG, "groups, shared or prefixes is NULL");
+        const ember_status st = check_words("groups, shared and prefixes", groups, shared, prefixes);
+        if (st != EMBER_OK) return st;
+        a.groups = groups;
+        a.shared = shared;
+        a.prefixes = prefixes;
+        a.n_groups = n_groups;
+    }
+    return decode(kv, a, q, ld_q, B, n_heads, seqs, lens, 0, 0, scale, out, ld_out, lse, workspace, workspace_bytes, status,
+                  stream);
 }
 
 ember_status ember_paged_prefill(const ember_paged_kv* kv, const void* q, int64_t ld_q, int32_t n, int32_t B,

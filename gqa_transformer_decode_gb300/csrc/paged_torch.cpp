@@ -14,6 +14,8 @@ decltype(&ember_paged_append) f_append = nullptr;
 decltype(&ember_paged_decode) f_decode = nullptr;
 decltype(&ember_paged_decode_workspace) f_workspace = nullptr;
 decltype(&ember_paged_prefill) f_prefill = nullptr;
+decltype(&ember_paged_decode_shared) f_shared = nullptr;
+decltype(&ember_paged_decode_shared_workspace) f_shared_workspace = nullptr;
 
 // One PagedKV: the C view of the cache and where its status word lives.
 struct Cache {
@@ -26,6 +28,8 @@ struct Cache {
     // decode's workspace of the last (B, heads): the query is a function of these
     int64_t ws_rows = -1, ws_heads = -1;
     size_t ws_bytes = 0;
+    int64_t shared_rows = -1, shared_heads = -1, shared_groups = -1;   // decode_shared's likewise
+    size_t shared_bytes = 0;
 };
 
 // [n, heads, head_dim] whose rows hold the heads side by side.
@@ -162,6 +166,37 @@ size_t workspace_of(Cache& c, int64_t B, int64_t heads) {
     return c.ws_bytes;
 }
 
+size_t shared_workspace_of(Cache& c, int64_t B, int64_t heads, int64_t groups) {
+    if (c.shared_rows != B || c.shared_heads != heads || c.shared_groups != groups) {
+        c.shared_bytes = f_shared_workspace(&c.kv, count(B, "q"), count(heads, "q"), count(groups, "shared"));
+        c.shared_rows = B;
+        c.shared_heads = heads;
+        c.shared_groups = groups;
+    }
+    return c.shared_bytes;
+}
+
+// A workspace, given or made.
+struct Workspace {
+    Tensor t;
+    void* p = nullptr;
+    size_t bytes;
+};
+Workspace workspace(const Cache& c, PyObject* o, size_t need) {
+    Workspace w;
+    w.bytes = need;
+    if (given(o)) {
+        w.t = tensor(o, "workspace");
+        on_device(c, w.t, "workspace");
+        if (w.t.scalar_type() != at::kByte || !w.t.is_contiguous()) bad("workspace must be contiguous uint8");
+        w.bytes = (size_t)w.t.numel();
+    } else if (need) {
+        w.t = make(c, {(int64_t)need}, at::kByte);
+    }
+    if (w.bytes) w.p = w.t.data_ptr();
+    return w;
+}
+
 // decode(cache, q, lens, seqs, window, sinks, scale, out, lse, return_lse, workspace)
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return guarded(nargs, 11, [&]() -> PyObject* {
@@ -175,22 +210,35 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         const c10::cuda::OptionalCUDAGuard on(c10::Device(at::kCUDA, c.device));
         Outputs o = outputs(c, B, heads, a[7], a[8], truth(a[9]));
         if (B > 0) {
-            Tensor ws;
-            void* wp = nullptr;
-            size_t bytes = workspace_of(c, B, heads);
-            if (given(a[10])) {
-                ws = tensor(a[10], "workspace");
-                on_device(c, ws, "workspace");
-                if (ws.scalar_type() != at::kByte || !ws.is_contiguous()) bad("workspace must be contiguous uint8");
-                bytes = (size_t)ws.numel();
-                wp = bytes ? ws.data_ptr() : nullptr;
-            } else if (bytes) {
-                ws = make(c, {(int64_t)bytes}, at::kByte);
-                wp = ws.data_ptr();
-            }
+            const Workspace ws = workspace(c, a[10], workspace_of(c, B, heads));
             check(f_decode(&c.kv, qr.p, qr.ld, count(B, "q"), count(heads, "q"), seqs, lens, window, sinks, (float)scale, o.r.p,
-                           o.r.ld, o.lse_p, wp, bytes, c.status, stream_of(c)),
+                           o.r.ld, o.lse_p, ws.p, ws.bytes, c.status, stream_of(c)),
                   "ember_paged_decode");
+            o.done();
+        }
+        return answer(o);
+    });
+}
+
+// decode_shared(cache, q, lens, groups, shared, prefixes, seqs, scale, out, lse, return_lse, workspace)
+PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+    return guarded(nargs, 12, [&]() -> PyObject* {
+        Cache& c = cache_of(a[0]);
+        const Tensor &q = tensor(a[1], "q"), &st = any_tensor(a[4], "shared");
+        const int64_t B = q.dim() == 3 ? q.size(0) : 0, heads = q.dim() == 3 ? q.size(1) : 0;
+        const int64_t groups = st.dim() == 1 ? st.size(0) : 0;
+        const Rows qr = rows(c, q, "q", c.dtype, B, heads);
+        const int32_t *lens = ints(c, a[2], "lens", B), *cu = ints(c, a[3], "groups", groups + 1);
+        const int32_t *shared = ints(c, a[4], "shared", groups), *prefixes = ints(c, a[5], "prefixes", groups);
+        const int32_t* seqs = given(a[6]) ? ints(c, a[6], "seqs", B) : nullptr;
+        const double scale = given(a[7]) ? real(a[7]) : 1.0 / std::sqrt((double)c.kv.head_dim);
+        const c10::cuda::OptionalCUDAGuard on(c10::Device(at::kCUDA, c.device));
+        Outputs o = outputs(c, B, heads, a[8], a[9], truth(a[10]));
+        if (B > 0) {
+            const Workspace ws = workspace(c, a[11], shared_workspace_of(c, B, heads, groups));
+            check(f_shared(&c.kv, qr.p, qr.ld, count(B, "q"), count(heads, "q"), seqs, lens, cu, shared, prefixes,
+                           count(groups, "shared"), (float)scale, o.r.p, o.r.ld, o.lse_p, ws.p, ws.bytes, c.status, stream_of(c)),
+                  "ember_paged_decode_shared");
             o.done();
         }
         return answer(o);
@@ -230,6 +278,15 @@ PyObject* workspace_bytes(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     });
 }
 
+// shared_workspace_bytes(cache, B, heads, groups)
+PyObject* shared_workspace_bytes(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+    return guarded(nargs, 4, [&]() -> PyObject* {
+        Cache& c = cache_of(a[0]);
+        const c10::cuda::OptionalCUDAGuard on(c10::Device(at::kCUDA, c.device));
+        return PyLong_FromSize_t(shared_workspace_of(c, number(a[1], "B"), number(a[2], "n_heads"), number(a[3], "n_groups")));
+    });
+}
+
 // cache(address of an ember_paged_kv, address of the status word, device index[, k_pages, v_pages[, status word]])
 PyObject* cache(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return guarded(nargs, nargs == 5 || nargs == 6 ? nargs : 3, [&]() -> PyObject* {
@@ -249,22 +306,25 @@ PyObject* cache(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     });
 }
 
-// entries(append, decode, decode_workspace, prefill, last_error, EmberError)
+// entries(append, decode, decode_workspace, prefill, decode_shared, decode_shared_workspace, last_error, EmberError)
 PyObject* entries(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-    return guarded(nargs, 6, [&]() -> PyObject* {
+    return guarded(nargs, 8, [&]() -> PyObject* {
         f_append = reinterpret_cast<decltype(f_append)>(PyLong_AsVoidPtr(a[0]));
         f_decode = reinterpret_cast<decltype(f_decode)>(PyLong_AsVoidPtr(a[1]));
         f_workspace = reinterpret_cast<decltype(f_workspace)>(PyLong_AsVoidPtr(a[2]));
         f_prefill = reinterpret_cast<decltype(f_prefill)>(PyLong_AsVoidPtr(a[3]));
-        f_error = reinterpret_cast<decltype(f_error)>(PyLong_AsVoidPtr(a[4]));
-        Py_INCREF(a[5]);
-        ember_error = a[5];
+        f_shared = reinterpret_cast<decltype(f_shared)>(PyLong_AsVoidPtr(a[4]));
+        f_shared_workspace = reinterpret_cast<decltype(f_shared_workspace)>(PyLong_AsVoidPtr(a[5]));
+        f_error = reinterpret_cast<decltype(f_error)>(PyLong_AsVoidPtr(a[6]));
+        Py_INCREF(a[7]);
+        ember_error = a[7];
         Py_RETURN_NONE;
     });
 }
 
-PyMethodDef methods[] = {FAST("append", append), FAST("decode", decode), FAST("prefill", prefill),
-                         FAST("workspace_bytes", workspace_bytes), FAST("cache", cache), FAST("entries", entries),
+PyMethodDef methods[] = {FAST("append", append), FAST("decode", decode), FAST("decode_shared", decode_shared), FAST("prefill", prefill),
+                         FAST("workspace_bytes", workspace_bytes),
+                         FAST("shared_workspace_bytes", shared_workspace_bytes), FAST("cache", cache), FAST("entries", entries),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "paged_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -120,6 +120,9 @@ def load():
         "ember_paged_decode_workspace": (C.c_size_t, [P, C.c_int32, C.c_int32]),
         "ember_paged_decode": (st, [P, P, C.c_int64, C.c_int32, C.c_int32, P, P, C.c_int32, C.c_int32,
                                     C.c_float, P, C.c_int64, P, P, C.c_size_t, P, P]),
+        "ember_paged_decode_shared_workspace": (C.c_size_t, [P, C.c_int32, C.c_int32, C.c_int32]),
+        "ember_paged_decode_shared": (st, [P, P, C.c_int64, C.c_int32, C.c_int32, P, P, P, P, P, C.c_int32, C.c_float, P,
+                                           C.c_int64, P, P, C.c_size_t, P, P]),
         "ember_paged_prefill": (st, [P, P, C.c_int64, C.c_int32, C.c_int32, C.c_int32, P, P, P, C.c_int32,
                                      C.c_int32, C.c_float, P, C.c_int64, P, P, P]),
         "ember_paged_take_status": (st, [P, P, P]),
@@ -305,6 +308,16 @@ def ember_paged_decode(kv, q, ld_q, B, n_heads, seqs, lens, window, sinks, scale
                        workspace_bytes, status, stream):
     return load().ember_paged_decode(kv, q, ld_q, B, n_heads, seqs, lens, window, sinks, scale, out, ld_out,
                                      lse, workspace, workspace_bytes, status, stream)
+
+
+def ember_paged_decode_shared_workspace(kv, B, n_heads, n_groups) -> int:
+    return int(load().ember_paged_decode_shared_workspace(kv, B, n_heads, n_groups))
+
+
+def ember_paged_decode_shared(kv, q, ld_q, B, n_heads, seqs, lens, groups, shared, prefixes, n_groups, scale, out, ld_out,
+                              lse, workspace, workspace_bytes, status, stream):
+    return load().ember_paged_decode_shared(kv, q, ld_q, B, n_heads, seqs, lens, groups, shared, prefixes, n_groups, scale,
+                                            out, ld_out, lse, workspace, workspace_bytes, status, stream)
 
 
 def ember_paged_prefill(kv, q, ld_q, n, B, n_heads, seqs, cu, lens, window, sinks, scale, out, ld_out, lse,

@@ -232,6 +232,18 @@ class PagedKV:
             return self._call(stream, self.decode, q, lens, seqs, window, sinks, scale, out, lse, return_lse, workspace)
         return self._t.decode(self._cache, q, lens, seqs, window, sinks, scale, out, lse, return_lse, workspace)
 
+    def decode_shared(self, q, lens, groups, shared, prefixes, seqs=None, scale=None, out=None, lse=None,
+                      return_lse=False, workspace=None, stream=None):
+        """decode() for groups of sequences that share a long prefix, read once for all of a group: rows groups[i] ..
+        groups[i + 1] - 1 of q find their first shared[i] keys in the pages of table row prefixes[i] and the others in
+        their own (seqs[b], default b).  groups int32 [n_groups + 1], shared and prefixes int32 [n_groups]; lens counts
+        all keys of a row.  workspace: a uint8 tensor of at least shared_workspace_bytes(B, n_heads, n_groups)."""
+        if stream is not None:
+            return self._call(stream, self.decode_shared, q, lens, groups, shared, prefixes, seqs, scale, out, lse,
+                              return_lse, workspace)
+        return self._t.decode_shared(self._cache, q, lens, groups, shared, prefixes, seqs, scale, out, lse, return_lse,
+                                     workspace)
+
     def prefill(self, q, cu, lens, seqs=None, window=0, sinks=0, scale=None, out=None, lse=None, return_lse=False,
                 stream=None):
         """Attention of several tokens per sequence: rows cu[b] .. cu[b + 1] - 1
@@ -244,6 +256,10 @@ class PagedKV:
     def workspace_bytes(self, B: int, n_heads: int) -> int:
         """Bytes of decode's workspace for B sequences of n_heads query heads (0: none is needed)."""
         return self._t.workspace_bytes(self._cache, B, n_heads)
+
+    def shared_workspace_bytes(self, B: int, n_heads: int, n_groups: int) -> int:
+        """The same of decode_shared's."""
+        return self._t.shared_workspace_bytes(self._cache, B, n_heads, n_groups)
 
     def sync_status(self, stream=None) -> int:
         """Wait for the stream, return and clear the first device-side error (0: none).  What calls on
@@ -369,7 +385,8 @@ def _torch_side(name, build, entries):
 
 def _paged_torch():
     return _torch_side("paged_torch", E._build.build_ext,
-                       ("ember_paged_append", "ember_paged_decode", "ember_paged_decode_workspace", "ember_paged_prefill"))
+                       ("ember_paged_append", "ember_paged_decode", "ember_paged_decode_workspace", "ember_paged_prefill",
+                        "ember_paged_decode_shared", "ember_paged_decode_shared_workspace"))
 
 
 def _rows_torch():

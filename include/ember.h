@@ -465,6 +465,28 @@ ember_status ember_paged_decode(const ember_paged_kv *kv, const void *q, int64_t
                                 int64_t ld_out, float *lse, void *workspace,
                                 size_t workspace_bytes, int32_t *status, ember_stream_t stream);
 
+/* ember_paged_decode for groups of sequences that share a long prefix (a system
+ * prompt, a document), held once: rows groups[i] .. groups[i+1] - 1 (device int32
+ * [n_groups+1], groups[0] = 0, groups[n_groups] = B) find their keys j < shared[i] in
+ * the pages of table row prefixes[i] and the others, up to lens[b], in their own
+ * row's (seqs[b]).  shared [n_groups] is any number, whole pages or not, and may
+ * exceed a row's lens[b]; entries of a row's own pages that hold only shared keys
+ * are not read.  Every key is seen: there is no window.  What the rows of a group
+ * read together is read once for all of them; n_groups is at most B.
+ * A row outside every group, a prefixes entry outside [0, n_seqs) and a shared entry
+ * outside [0, table_width*page_size] raise INVALID_ARG and CAPACITY, and the rows
+ * are skipped.  All else as in ember_paged_decode, with
+ * ember_paged_decode_shared_workspace bytes of workspace. */
+size_t ember_paged_decode_shared_workspace(const ember_paged_kv *kv, int32_t B, int32_t n_heads,
+                                           int32_t n_groups);
+ember_status ember_paged_decode_shared(const ember_paged_kv *kv, const void *q, int64_t ld_q,
+                                       int32_t B, int32_t n_heads, const int32_t *seqs,
+                                       const int32_t *lens, const int32_t *groups,
+                                       const int32_t *shared, const int32_t *prefixes,
+                                       int32_t n_groups, float scale, void *out, int64_t ld_out,
+                                       float *lse, void *workspace, size_t workspace_bytes,
+                                       int32_t *status, ember_stream_t stream);
+
 /* Attention of several tokens per sequence: rows cu[b] .. cu[b+1] - 1 of q
  * (device int32 [B+1], 0 <= cu[b] <= cu[b+1] <= n) are the last positions of
  * sequence seqs[b] (NULL: sequence b), which holds lens[b] keys with theirs: row
