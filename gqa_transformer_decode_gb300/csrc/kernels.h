@@ -546,10 +546,14 @@ struct PagedDecodeArgs {
     // set by launch_paged_decode:
     int split;                   // CTAs that share a long sequence in cluster form
     int by_pair;                 // records stand by (sequence, kv head)
+    const float* prefix;         // PagedSharedWs, to be joined
+    int prefix_head, prefix_slots, prefix_rows;
 };
 // bytes of ws that the call's split needs (a window only ever lowers them)
 size_t paged_decode_ws(const PagedView& c, int B, int NH, int window, int sinks, int sms);
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int sms, cudaStream_t s);
+// The same of a call with shared prefixes, for any scale.
+size_t paged_decode_shared_ws(const PagedView& c, int B, int NH, int n_groups, int sms);
 
 // Attention of the last cu[b + 1] - cu[b] positions of each sequence.
 struct PagedPrefillArgs {
@@ -567,6 +571,11 @@ struct PagedPrefillArgs {
     float* lse;                  // [n][NH] or nullptr
     int* status;
     int parts;                   // set by launch_paged_prefill_tc: CTAs that share a tile pair's keys
+    // shared prefixes (launch_paged_shared): B groups of rows cu[g] .. cu[g + 1] - 1 read
+    // shared[g] keys of table row seqs[g], row i at most lens[i] of them; no out
+    const int32_t* shared;
+    float* ws;                   // PagedSharedWs
+    int ws_head, slots;
 };
 cudaError_t launch_paged_prefill(const PagedPrefillArgs& a, int sms, cudaStream_t s);
 // The same on tcgen05 (paged_prefill_tc.cu; scale > 0), through TMA maps over the
@@ -577,6 +586,19 @@ struct PagedPrefillMaps {
 };
 bool paged_prefill_maps(const PagedPrefillArgs& a, PagedPrefillMaps& m);
 cudaError_t launch_paged_prefill_tc(const PagedPrefillArgs& a, const PagedPrefillMaps& m, int sms, cudaStream_t s);
+
+// The partials that launch_paged_shared leaves: `head` floats (int2 {tiles of a CTA, tiles of
+// all}, then for each group {its first pair, its first tile}), [slots][256][D] sums, and
+// [slots][256] {m, l}.  A pair holds rows_per_pair rows of a group for one kv head, row
+// (i, h) of them at (i / (half) * 128 + i % half * G + h), half = rows_per_pair / 2;
+// pairs of a group stand by kv head, then by rows, each with ceil(shared / 64) tiles.  What
+// CTA c has of pair p lies in slot p + c.
+struct PagedSharedWs {
+    int head, slots, rows_per_pair;
+    size_t floats;
+};
+PagedSharedWs paged_shared_ws(int B, int n_groups, int NH, int NKV, int D, int sms);
+cudaError_t launch_paged_shared(const PagedPrefillArgs& a, const PagedPrefillMaps& m, int sms, cudaStream_t s);
 
 // out[c][r] = in[r][c] for 16-bit elements
 void launch_transpose16(const uint16_t* in, uint16_t* out, int rows, int cols, cudaStream_t s);

@@ -93,10 +93,11 @@ ember_status decode(const ember_paged_kv* kv, PagedDecodeArgs& a, const void* q,
     int sms = 0;
     cudaError_t e = device_sms(&sms);
     if (e != cudaSuccess) return cuda_failed("no device", e);
-    const size_t need = paged_decode_ws(a.c, B, n_heads, window, sinks, sms);
+    const size_t need = a.groups ? paged_decode_shared_ws(a.c, B, n_heads, a.n_groups, sms)
+                                 : paged_decode_ws(a.c, B, n_heads, window, sinks, sms);
     if ((need && !workspace) || !aligned16(workspace))
         PG_FAIL(EMBER_ERR_INVALID_ARG, "workspace must be given and 16-byte aligned");
-    if (workspace_bytes < need) PG_FAIL(EMBER_ERR_CAPACITY, "workspace smaller than ember_paged_decode_workspace");
+    if (workspace_bytes < need) PG_FAIL(EMBER_ERR_CAPACITY, "workspace smaller than its query answers");
     a.q = static_cast<const uint16_t*>(q);
     a.ld_q = ld_q;
     a.B = B;
@@ -198,7 +199,15 @@ ember_status ember_paged_decode(const ember_paged_kv* kv, const void* q, int64_t
 }
 
 size_t ember_paged_decode_shared_workspace(const ember_paged_kv* kv, int32_t B, int32_t n_heads, int32_t n_groups) {
-    return n_groups <= 0 || n_groups > B ? 0 : ember_paged_decode_workspace(kv, B, n_heads);
+    PagedView c;
+    int sms = 0;
+    if (B <= 0 || B > 65535 || n_groups <= 0 || n_groups > B || check_cache(kv, c) != EMBER_OK || check_heads(kv, n_heads) != EMBER_OK)
+        return 0;
+    if (device_sms(&sms) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return paged_decode_shared_ws(c, B, n_heads, n_groups, sms);
 }
 
 ember_status ember_paged_decode_shared(const ember_paged_kv* kv, const void* q, int64_t ld_q, int32_t B, int32_t n_heads,

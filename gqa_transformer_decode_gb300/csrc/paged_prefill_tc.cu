@@ -57,6 +57,12 @@
 // The tensor pipe is active for 65 % of the cycles in the chunks, whose longest tile
 // pairs (87 key tiles) set the time, 52 % under the window and 27 % in the prompt.
 //
+// The same kernel takes the shared prefixes of ember_paged_decode_shared (PT_SHARED): a
+// "sequence" is then a group of one-token rows, all of which see the group's prefix, and
+// the key tiles of all (pair, kv head)s form a line of which CTA c takes the c-th equal
+// share, as in paged_decode.cu.  What a CTA has of a pair it leaves as (m, l, O) of the
+// pair's rows, which paged_decode.cu joins with the rows' own keys.
+//
 // Warps 0-3: tile A; warps 4-7: tile B (a warp reads the TMEM lanes of its index
 // mod 4); warp 8: TMA producer; warp 9: TMEM allocation; warps
 // 9 and 10: MMA issue for tile A and for tile B, so that neither's waiting holds
@@ -79,6 +85,9 @@ constexpr int PT_REGS_ROW = 200, PT_REGS_REST = 104;   // 256 * 200 + 128 * 104 
 constexpr int PT_ROWS = 128;   // rows of a query tile
 constexpr int PT_KEYS = 64;    // keys of a tile
 constexpr int PT_PARTS = 8;    // CTAs of a cluster at most
+constexpr int PT_SHARE = 4;    // PT_SHARED: key tiles of a CTA at least
+// A pair's keys: by one CTA, or shared out over a cluster, or over the line.
+enum PtForm : int { PT_WHOLE = 0, PT_SPLIT = 1, PT_SHARED = 2 };
 
 template <int DP>
 struct PtSmem {
@@ -171,6 +180,7 @@ struct PtPair {
     int g, seq, row0, tokens, pos0;   // kv head, table row, first query row, tokens, position of the first
     int end, first, sinks;            // keys that some row sees: [first, end) and [0, sinks)
     int ns, wb, j0, nkt;              // key tiles: of the sinks, first of the window; this CTA's first and number (-1: no such pair)
+    int slot;                         // PT_SHARED: where its partials go
     __device__ __forceinline__ int key0(int j) const { return PT_KEYS * (j0 + j < ns ? j0 + j : wb + j0 + j - ns); }
 };
 // pair: its number among `pairs`; the keys in `parts` shares, of which the part-th.
@@ -201,6 +211,101 @@ __device__ __forceinline__ PtPair pt_pair(const PagedPrefillArgs& a, int QT, uns
     return p;
 }
 
+// ---- PT_SHARED ----
+// The rows of group g in pairs of tiles and its key tiles; none if it is invalid (paged_decode.cu
+// reports that) or has no prefix.
+struct PtGroup {
+    int row0, nq, keys, seq, nx, tiles;
+};
+__device__ __forceinline__ PtGroup pt_group(const PagedPrefillArgs& a, int g, int QT) {
+    PtGroup r{0, 0, 0, 0, 0, 0};
+    if (g >= a.B) return r;
+    const int r0 = a.cu[g], r1 = a.cu[g + 1], keys = a.shared[g], seq = a.seqs[g];
+    if (seq < 0 || seq >= a.c.n_seqs || r0 < 0 || r1 <= r0 || r1 > a.n || keys <= 0 ||
+        keys > ((long long)a.c.width << a.c.page_shift))
+        return r;
+    r.row0 = r0;
+    r.nq = r1 - r0;
+    r.keys = keys;
+    r.seq = seq;
+    r.nx = (r.nq + 2 * QT - 1) / (2 * QT);
+    r.tiles = (keys + PT_KEYS - 1) / PT_KEYS;
+    return r;
+}
+// Where 32 groups' pairs and key tiles begin, each lane its own group's, after those of `pairs` and `line`
+// before; both are moved on.
+__device__ __forceinline__ PtGroup pt_scan(const PagedPrefillArgs& a, int g0, int QT, unsigned& pairs, unsigned& line,
+                                           unsigned& pair0, unsigned& line0) {
+    const int lane = threadIdx.x & 31;
+    const PtGroup r = pt_group(a, g0 + lane, QT);
+    const unsigned np = (unsigned)r.nx * a.c.NKV, nl = np * (unsigned)r.tiles;
+    pair0 = np;
+    line0 = nl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(FULL_MASK, pair0, o), y = __shfl_up_sync(FULL_MASK, line0, o);
+        if (lane >= o) {
+            pair0 += x;
+            line0 += y;
+        }
+    }
+    const unsigned all_p = __shfl_sync(FULL_MASK, pair0, 31), all_l = __shfl_sync(FULL_MASK, line0, 31);
+    pair0 += pairs - np;
+    line0 += line - nl;
+    pairs += all_p;
+    line += all_l;
+    return r;
+}
+// The line's length and a CTA's share of it; one warp of the grid leaves what the join needs
+// to find a pair's partials: the share, then each group's first pair and place in the line.
+__device__ __forceinline__ void pt_line(const PagedPrefillArgs& a, int QT, bool leave, unsigned& each, unsigned& lo, unsigned& hi) {
+    unsigned pairs = 0, line = 0;
+    int2* head = reinterpret_cast<int2*>(a.ws);
+    for (int g0 = 0; g0 < a.B; g0 += 32) {
+        unsigned pair0, line0;
+        (void)pt_scan(a, g0, QT, pairs, line, pair0, line0);
+        const int g = g0 + (threadIdx.x & 31);
+        if (leave && g < a.B) head[1 + g] = make_int2((int)pair0, (int)line0);
+    }
+    each = max((unsigned)PT_SHARE, (line + gridDim.x - 1) / gridDim.x);
+    if (leave && (threadIdx.x & 31) == 0) head[0] = make_int2((int)each, (int)line);
+    lo = min(line, blockIdx.x * each);
+    hi = min(line, lo + each);
+}
+// The pair at place `at` of the line and the key tiles that the CTA has of it from there on.
+__device__ __forceinline__ PtPair pt_shared(const PagedPrefillArgs& a, int QT, unsigned at, unsigned hi) {
+    PtPair p;
+    p.nkt = -1;
+    p.tokens = 0;
+    if (at >= hi) return p;
+    unsigned pairs = 0, line = 0;
+    for (int g0 = 0; g0 < a.B; g0 += 32) {
+        unsigned pair0, line0;
+        const PtGroup mine = pt_scan(a, g0, QT, pairs, line, pair0, line0);
+        const unsigned hit =
+            __ballot_sync(FULL_MASK, at >= line0 && at - line0 < (unsigned)mine.nx * a.c.NKV * (unsigned)mine.tiles);
+        if (!hit) continue;
+        const int src = __ffs(hit) - 1;
+        const PtGroup r = pt_group(a, g0 + src, QT);
+        const unsigned off = at - __shfl_sync(FULL_MASK, line0, src);
+        // a kv head's pairs side by side: they read the same keys at about the same time
+        const int pi = (int)(off / (unsigned)r.tiles), x = pi % r.nx;
+        p.g = pi / r.nx;
+        p.seq = r.seq;
+        p.row0 = r.row0 + x * 2 * QT;
+        p.tokens = min(2 * QT, r.nq - x * 2 * QT);
+        p.pos0 = 0;
+        p.end = r.keys;
+        p.first = p.sinks = p.ns = p.wb = 0;
+        p.j0 = (int)(off % (unsigned)r.tiles);
+        p.nkt = (int)min((unsigned)(r.tiles - p.j0), hi - at);
+        // pairs and CTAs both only rise along the line, one of them at each step: no two share a slot
+        p.slot = (int)__shfl_sync(FULL_MASK, pair0, src) + pi + (int)blockIdx.x;
+        break;
+    }
+    return p;
+}
+
 // Asks for a CTA that has not started; 16 bytes of answer, counted on bar.
 __device__ __forceinline__ void try_cancel(uint32_t answer, uint64_t* bar) {
     asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
@@ -225,12 +330,13 @@ __device__ __forceinline__ bool cancelled(uint32_t answer, unsigned& cta) {
     return ok != 0;
 }
 
-template <class E, int DP, bool SPLIT>
+template <class E, int DP, int FORM>
 __global__ void __launch_bounds__(PT_THREADS, 1)
     k_paged_prefill_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, PagedPrefillArgs a) {
     using L = PtSmem<DP>;
     constexpr int NS = L::NS;
+    constexpr bool SPLIT = FORM == PT_SPLIT, SHARED = FORM == PT_SHARED;
     extern __shared__ uint8_t pt_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pt_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
@@ -282,8 +388,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     const int D = a.c.D, G = a.NH / a.c.NKV;
     const int QT = PT_ROWS / G;                        // tokens of a query tile
     const int parts = SPLIT ? a.parts : 1, part = SPLIT ? (int)(blockIdx.x % parts) : 0;   // (a cluster's CTAs)
-    const unsigned first_pair = blockIdx.x / parts, pairs_all = gridDim.x / parts;
+    unsigned first_pair = blockIdx.x / parts, pairs_all = gridDim.x / parts;
     pdl_wait();
+    if (SHARED) {   // (then these are the CTA's share of the line)
+        pdl_trigger();   // the rows' own keys do not need this grid's results
+        unsigned each;
+        pt_line(a, QT, blockIdx.x == 0 && warp == 0, each, first_pair, pairs_all);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -300,9 +411,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         return true;
     };
     auto wait_all = [&](uint64_t* b, int parity) { return wait_at(smem_u32(b), (uint32_t)parity & 1u); };
-    // the CTA index after the it-th pair's: false when there is none left (or, ok = false, no answer)
-    auto take_next = [&](int it, unsigned& cta, bool& ok) {
+    // the CTA index (SHARED: the place in the line) after the it-th pair's: false when there is none left (or, ok = false, no answer)
+    auto take_next = [&](int it, unsigned& cta, bool& ok, int nkt) {
         if (SPLIT) return false;
+        if (SHARED) {
+            cta += max(0, nkt);
+            return cta < pairs_all;
+        }
         if (!wait_all(&next_full[it & 1], it >> 1)) {
             ok = false;
             return false;
@@ -312,6 +427,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&next_empty[it & 1]);
         return got;
+    };
+
+    auto pair_at = [&](unsigned cta, bool reporter) {
+        if constexpr (SHARED) return pt_shared(a, QT, cta, pairs_all);
+        else return pt_pair(a, QT, cta, pairs_all, part, parts, reporter);
     };
 
     if (warp >= PT_TMA) {
@@ -331,7 +451,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const uint32_t empty_at = smem_u32(kv_empty);
         bool ok = true, asked = false;
         for (;; ++it) {
-            const PtPair p = pt_pair(a, QT, cta, pairs_all, part, parts, part == 0);
+            const PtPair p = pair_at(cta, part == 0);
             if (p.nkt > 0) {
                 // The page of the lane's box of tile j, if some row sees its keys.  What it
                 // loads is looked at two tiles later, so that nothing waits for it.
@@ -396,7 +516,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             }
             // asked for only now, a ring's worth of tiles before the pair ends: a CTA
             // that asked at its start would hold work that another could begin first
-            if (!SPLIT) {
+            if (FORM == PT_WHOLE) {
                 ok = it < 2 || wait_all(&next_empty[it & 1], (it >> 1) - 1);
                 if (!ok) break;
                 if (lane == 0) {
@@ -406,7 +526,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 __syncwarp();
                 asked = true;
             }
-            if (!take_next(it, cta, ok)) break;
+            if (!take_next(it, cta, ok, p.nkt)) break;
             asked = false;
         }
         if (!ok && lane == 0) {
@@ -422,7 +542,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         int base = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            const PtPair p = pt_pair(a, QT, cta, pairs_all, part, parts, false);
+            const PtPair p = pair_at(cta, false);
             const int nkt = max(0, p.nkt);
             for (int j = 0; ok && j < nkt; ++j) {
                 const int i = 2 * (base + j) + 1, s = i % NS, key0 = p.key0(j);
@@ -447,7 +567,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             }
             if (!ok) break;
             base += nkt;
-            if (!take_next(it, cta, ok)) break;
+            if (!take_next(it, cta, ok, p.nkt)) break;
         }
         if (!ok && lane == 0) sflag[0] = 1;
     } else {   // -------------------------------------------------- MMA issuers, one for each query tile
@@ -491,7 +611,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         int mine = 0, with = 0;    // those in which this query tile has tokens
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            const PtPair p = pt_pair(a, QT, cta, pairs_all, part, parts, false);
+            const PtPair p = pair_at(cta, false);
             const int nkt = max(0, p.nkt);
             auto slot_full = [&](int i) { return &kv_full[i % NS]; };
             if (nkt > 0 && !(ok = wait_all(q_full, pairs))) break;
@@ -558,7 +678,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             if (!ok) break;
             base += nkt;
             pairs += nkt > 0;
-            if (!take_next(it, cta, ok)) break;
+            if (!take_next(it, cta, ok, p.nkt)) break;
         }
         if (!ok && lane == 0) sflag[0] = 1;
     }
@@ -577,10 +697,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         bool ok = true;
         PtPair pair;                                  // (SPLIT: the one pair)
         for (int it = 0; ok; ++it) {
-        const PtPair p = pt_pair(a, QT, cta, pairs_all, part, parts, false);
+        const PtPair p = pair_at(cta, false);
         const int nkt = t * QT < p.tokens ? max(0, p.nkt) : 0;   // (without tokens the tile has no products either)
         const bool live = p.nkt >= 0 && r < QT * G && tok < p.tokens;
-        const int qp = p.pos0 + min(tok, p.tokens - 1);   // its position (rows that are not live: the last one's)
+        int qp = p.pos0 + min(tok, p.tokens - 1);         // its position (rows that are not live: the last one's)
+        if (SHARED && p.nkt >= 0) qp = min(p.end, a.lens[p.row0 + min(tok, p.tokens - 1)]) - 1;   // its last key here
         float m = SOFTMAX_FLOOR, l = 0.f;             // reference maximum (of s * sc) less LIFT, sum of 2^(s sc - m)
         for (int j = 0; j < nkt; ++j) {
             const int n = base + j;
@@ -709,6 +830,36 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             pair = p;
             break;
         }
+        if (SHARED) {   // the rows as they are; joined by another kernel
+            const bool store = live && p.slot < a.slots;
+            float* o_row = a.ws + a.ws_head + ((size_t)p.slot * (2 * PT_ROWS) + t * PT_ROWS + r) * D;
+            if (ok && nkt > 0) {
+                const int last = base + nkt - 1;
+                ok = wait_all(&o_full[2 * t + (last & 1)], last >> 1);
+                tc_fence_after();
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            if (store && c + i < D) *reinterpret_cast<uint4*>(o_row + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                    if (store)
+                        reinterpret_cast<float2*>(a.ws + a.ws_head + (size_t)a.slots * (2 * PT_ROWS) * D)[(size_t)p.slot * (2 * PT_ROWS) + t * PT_ROWS + r] =
+                            make_float2(m, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_free[t]);
+                }
+            }
+            if (!ok) break;
+            base += nkt;
+            if (!take_next(it, cta, ok, p.nkt)) break;
+            continue;
+        }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         uint32_t w[DP / 2];                           // the row of the output
 #pragma unroll
@@ -777,7 +928,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             if (a.lse && live) a.lse[row * a.NH + p.g * G + h] = l == 0.f ? -INFINITY : m * LN2 + logf(l);
         }
         base += nkt;
-        if (!take_next(it, cta, ok)) break;
+        if (!take_next(it, cta, ok, p.nkt)) break;
         }
         if (!ok) sflag[0] = 1;
         if (SPLIT) {
@@ -855,18 +1006,43 @@ cudaError_t launch_dp(const PagedPrefillMaps& m, PagedPrefillArgs a, int sms, cu
     const auto& mk = *reinterpret_cast<const CUtensorMap*>(m.k);
     const auto& mv = *reinterpret_cast<const CUtensorMap*>(m.v);
     if (a.parts > 1) {
-        auto k = k_paged_prefill_tc<E, DP, true>;
+        auto k = k_paged_prefill_tc<E, DP, PT_SPLIT>;
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (e != cudaSuccess) return e;
         return launch_cluster_k(k, dim3(pairs * a.parts), dim3(PT_THREADS), SMEM, a.parts, s, mq, mk, mv, a);
     }
-    auto k = k_paged_prefill_tc<E, DP, false>;
+    auto k = k_paged_prefill_tc<E, DP, PT_WHOLE>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     return launch_k(k, dim3(pairs), dim3(PT_THREADS), SMEM, s, mq, mk, mv, a);
 }
 
+template <class E, int DP>
+cudaError_t launch_shared(const PagedPrefillMaps& m, const PagedPrefillArgs& a, int sms, cudaStream_t s) {
+    constexpr int SMEM = PtSmem<DP>::TOTAL;
+    auto k = k_paged_prefill_tc<E, DP, PT_SHARED>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_k(k, dim3(sms), dim3(PT_THREADS), SMEM, s, *reinterpret_cast<const CUtensorMap*>(m.q),
+                    *reinterpret_cast<const CUtensorMap*>(m.k), *reinterpret_cast<const CUtensorMap*>(m.v), a);
+}
+
 }  // namespace
+
+PagedSharedWs paged_shared_ws(int B, int n_groups, int NH, int NKV, int D, int sms) {
+    const int per = 2 * (PT_ROWS / (NH / NKV));
+    PagedSharedWs w;
+    w.head = (2 * (1 + n_groups) + 3) & ~3;
+    w.slots = (B / per + n_groups) * NKV + sms;        // at most one more pair than full ones for each group
+    w.rows_per_pair = per;
+    w.floats = w.head + (size_t)w.slots * (2 * PT_ROWS) * (D + 2);
+    return w;
+}
+
+cudaError_t launch_paged_shared(const PagedPrefillArgs& a, const PagedPrefillMaps& m, int sms, cudaStream_t s) {
+    if (a.c.bf16) return a.c.D <= 64 ? launch_shared<ElemBf16, 64>(m, a, sms, s) : launch_shared<ElemBf16, 128>(m, a, sms, s);
+    return a.c.D <= 64 ? launch_shared<ElemF16, 64>(m, a, sms, s) : launch_shared<ElemF16, 128>(m, a, sms, s);
+}
 
 bool paged_prefill_maps(const PagedPrefillArgs& a, PagedPrefillMaps& m) {
     const PagedView& c = a.c;

@@ -91,6 +91,15 @@ def test_ragged_groups(NH, NKV, D, P, row_major, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("NH,NKV,D", HEADS)
+def test_ragged_groups_on_a_wide_table(NH, NKV, D, dtype):
+    """A table with room for many keys: the prefixes go by themselves, however short they are."""
+    p = Shared(RAGGED + [(1, [1, 2, 3]), (63, [70] * 3), (130, [128, 131, 500] * 20)], NKV, D, 16, dtype, extra_width=20000)
+    q = p.queries(NH)
+    p.check(q, *p.run(q, return_lse=True))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("NH,NKV,D,P,groups", [
     (14, 2, 64, 16, [(1000, [1001] * 5)]), (32, 8, 64, 32, [(2049, list(range(2050, 2050 + 70)))]),
     (16, 8, 128, 64, [(777, [800] * 20), (3000, [3001, 4100, 2900] * 9), (65, [66] * 3)]),
