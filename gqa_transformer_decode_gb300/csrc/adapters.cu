@@ -23,8 +23,8 @@
 // calls give equal bits.  Many tiles run persistently, one CTA an SM, the next tile's
 // products under the last one's output.
 //
-// Warp 0: copies; warp 1: TMEM and products; warps 2-5: output; warps 6 and 7: which adapters
-// a tile has, and t's tiles.  Every wait is bounded; a timeout raises EMBER_ERR_TIMEOUT, the
+// Warp 0: copies; warp 1: TMEM and products; warps 2-5: output; warp 6: which adapters a tile
+// has; warps 6-9: t's tiles.  Every wait is bounded; a timeout raises EMBER_ERR_TIMEOUT, the
 // CTA drains its copies and frees TMEM.
 #include <cudaTypedefs.h>
 
@@ -35,10 +35,10 @@ namespace ember {
 
 namespace {
 
-constexpr int AD_THREADS = 256;
+constexpr int AD_BUILDERS = 4;                   // warps that write t's tiles, a stage each
+constexpr int AD_THREADS = 192 + 32 * AD_BUILDERS;
 constexpr int AD_M = 128;                        // rows of W in a tile
 constexpr int AD_BK = 64;                        // K of a block
-constexpr int AD_BUILD = 64;                     // threads of the last two warps
 constexpr int AD_SLICE = 32;                     // rows of x that are put out at a time
 constexpr int AD_LD = AD_M + 4;                  // their distance in shared memory, floats
 
@@ -46,7 +46,7 @@ template <int NT, bool LOW>
 struct AdSmem {
     static constexpr int A_BYTES = AD_M * 128, X_BYTES = NT * 128, STAGE = A_BYTES + X_BYTES;
     // a tile of few rows leaves room for the other launch's CTA on the same SM
-    static constexpr int STAGES = NT == 256 ? 4 : NT == 128 ? 6 : LOW ? 3 : 5;
+    static constexpr int STAGES = NT == 256 ? 4 : NT == 128 ? 6 : LOW ? 4 : 5;
     static constexpr int OUT = AD_SLICE * AD_LD * 4;
     static constexpr int OFF_OUT = STAGES * STAGE;
     static constexpr int OFF_LIST = OFF_OUT + OUT;           // [2][NT] entries
@@ -183,13 +183,13 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&t_go[s], 1);
-            mbar_init(&t_full[s], 2);
+            mbar_init(&t_full[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 4);
             mbar_init(&list_full[b], 1);
-            mbar_init(&list_empty[b], 3);
+            mbar_init(&list_empty[b], 1 + AD_BUILDERS);   // copies, products, all builders but the one that lists
         }
         sflag[0] = sflag[1] = sflag[2] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -332,14 +332,14 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
         }
     } else if (warp >= 6) {
         if (!LOW) {   // -------------- which adapters a tile has, and t's tiles
-            const int tid = threadIdx.x - (AD_THREADS - AD_BUILD);
-            int g = 0;
+            const int builder = warp - 6;
+            int g = 0, x = 0;                    // stages so far; those with an adapter's products
             uint32_t go_phase = 0;
             bool ok = true, waited = false;
             for (int li = 0; li < tiles && ok; ++li) {
                 const int b = li & 1;
                 const Tile t = tile_of(li);
-                if (warp == 6) {
+                if (builder == 0) {
                     ok = li < 2 || mbar_wait(&list_empty[b], ((uint32_t)(li >> 1) & 1u) ^ 1u);
                     if (ok) {
                         const int n = list_adapters<NT>(a, t.row0, s_list + b * NT, s_ids + b * NT);
@@ -349,7 +349,6 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                         }
                     }
                 }
-                // (both warps see the phase; after a failure neither goes on)
                 ok = ok && mbar_wait(&list_full[b], (uint32_t)(li >> 1) & 1u);
                 if (!ok) break;
                 const int n = s_count[b];
@@ -361,23 +360,30 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                 }
                 for (int e = part; e < n && ok; e += C) {
                     const AdEntry en = s_list[b * NT + e];
-                    for (int k = 0; k < blocks; ++k, ++g) {
+                    for (int k = 0; k < blocks; ++k, ++g, ++x) {
                         const int s = g % S;
+                        // (every builder sees every phase: a wait names one by its parity alone)
                         if (!(ok = mbar_wait(&t_go[s], go_phase >> s & 1u))) break;
                         go_phase ^= 1u << s;
+                        if (x % AD_BUILDERS != builder) continue;
+                        // 16-byte pieces of a row: both terms, which lie side by side, at 0 and 64, or
+                        // 64 ranks of one term
+                        const int q0 = both ? 0 : (k >> 1) * 8, per = both ? RP / 8 : min(8, RP / 8 - q0);
+                        const int pieces = both ? 2 * per : per;
+                        const uint4* src = reinterpret_cast<const uint4*>(a.t + ((long long)t.row0 * 2 + (both ? 0 : k & 1)) * RP) + q0;
                         uint8_t* dst = sm + s * L::STAGE + L::A_BYTES;
-                        // 16-byte pieces of the rows: both terms at 0 and 64, or one term's 64 ranks
-                        const int q0 = both ? 0 : (k >> 1) * 8;              // first piece of the term's row
-                        const int per = both ? RP / 8 : min(8, RP / 8 - q0); // pieces of a term
-                        const int each = both ? 2 * per : per, term0 = both ? 0 : k & 1;
-                        const int total = (en.c1 - en.c0) * each;
-                        for (int i = tid; i < total; i += AD_BUILD) {
-                            const int c = en.c0 + i / each, p = i % each, term = term0 + p / per, q = p % per;
-                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                            if (ids[c] == en.adapter)
-                                v = __ldcg(reinterpret_cast<const uint4*>(a.t + ((long long)(t.row0 + c) * 2 + term) * RP) + q0 + q);
-                            const int at = both ? term * 4 + q : q;
-                            *reinterpret_cast<uint4*>(dst + c * 128 + ((at ^ (c & 7)) << 4)) = v;
+                        for (int c = en.c0 + lane; c < en.c1; c += 32) {
+                            const bool mine = ids[c] == en.adapter;
+                            const uint4* p = src + (long long)c * (RP / 4);
+                            uint4 v[8];
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                v[q] = mine && q < pieces ? __ldcg(p + q) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const int at = both && q >= per ? 4 + q - per : q;
+                                if (q < pieces) *reinterpret_cast<uint4*>(dst + c * 128 + ((at ^ (c & 7)) << 4)) = v[q];
+                            }
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
@@ -385,7 +391,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                     }
                 }
                 __syncwarp();
-                if (warp == 7 && lane == 0) mbar_arrive(&list_empty[b]);
+                if (builder != 0 && lane == 0) mbar_arrive(&list_empty[b]);
             }
             if (!waited) pdl_wait();             // this grid ends after the first one, whatever happens
             if (!ok) sflag[0] = 1;
