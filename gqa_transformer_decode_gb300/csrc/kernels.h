@@ -552,8 +552,9 @@ struct PagedDecodeArgs {
 // bytes of ws that the call's split needs (a window only ever lowers them)
 size_t paged_decode_ws(const PagedView& c, int B, int NH, int window, int sinks, int sms);
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int sms, cudaStream_t s);
-// The same of a call with shared prefixes, for any scale.
+// The same of a call with shared prefixes (paged_shared.cu).
 size_t paged_decode_shared_ws(const PagedView& c, int B, int NH, int n_groups, int sms);
+cudaError_t launch_paged_decode_shared(PagedDecodeArgs a, int sms, cudaStream_t s);
 
 // Attention of the last cu[b + 1] - cu[b] positions of each sequence.
 struct PagedPrefillArgs {

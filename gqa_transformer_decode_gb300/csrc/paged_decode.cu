@@ -43,102 +43,17 @@
 // P, the second product's operand, goes in as the sum of two values of the cache's
 // type (bf16 2^-16 relative, f16 2^-22 or 2^-32 of the largest): one would add as much error as the output's
 // own rounding, and the products are far from bounding this kernel.
-#include "paged.cuh"
+#include "paged_decode.cuh"
 
 namespace ember {
 
 namespace {
 
-constexpr int PD_WARPS = 4;
-constexpr int PD_THREADS = PD_WARPS * 32;
-constexpr int PD_STAGES = 2;         // ring stages of a warp
 constexpr int PD_MIN_BLOCKS = 8;     // blocks of a CTA at least (two per warp)
-constexpr int pd_ctas_per_sm(int ht) { return ht == 1 ? 3 : 2; }   // registers: 168 or 255 a thread
 constexpr int PD_MAX_CLUSTER = 8;     // CTAs of a cluster (a power of two)
 constexpr int PD_CLUSTER_BLOCKS = 8;  // blocks of a warp in cluster form at most
 constexpr int PJ_PARTS = 8;           // partials of a (sequence, kv head) from which a block joins a single head
 constexpr int PD_MAX_CTAS = 512;     // grid at most (the join's weights stand in shared memory)
-// Keys of a block: 8 KB of K and V rows either way.
-template <int DP>
-constexpr int PD_KEYS = DP == 64 ? 32 : 16;
-
-// What a row's keys lie in: its own pages, or those of its group's prefix up to `from` and
-// its own from there on, or its own from there on alone (the prefix is another kernel's).
-enum PdShare : int { PD_OWN = 0, PD_SHARED = 1, PD_TAIL = 2 };
-
-// Blocks of one sequence: [0, ns) hold its sinks, the rest its window.
-struct SeqBlocks {
-    int n, ns, wb;       // blocks, blocks of the sinks, first block of the window
-    int end, first, sinks;
-    int from, prefix;    // PD_SHARED: keys below `from` are those of table row `prefix`
-    bool zero;           // nothing visible: the output is zero (PD_TAIL: the row is valid)
-    __device__ __forceinline__ int index(int i) const { return i < ns ? i : wb + i - ns; }
-};
-
-// The group of row b, if it is in one and its prefix is valid: its shared keys and their table row.
-__device__ __forceinline__ int shared_prefix(const PagedDecodeArgs& a, int b, int& from, int& prefix) {
-    int lo = 0;
-    for (int hi = a.n_groups; hi - lo > 1;) {
-        const int mid = (lo + hi) / 2;
-        if (a.groups[mid] <= b) lo = mid;
-        else hi = mid;
-    }
-    if (a.groups[lo] < 0 || a.groups[lo] > b || b >= a.groups[lo + 1] || a.groups[lo + 1] > a.B) return EMBER_ERR_INVALID_ARG;
-    from = a.shared[lo];
-    prefix = a.prefixes[lo];
-    if (prefix < 0 || prefix >= a.c.n_seqs) return EMBER_ERR_INVALID_ARG;
-    if (from < 0 || from > ((long long)a.c.width << a.c.page_shift)) return EMBER_ERR_CAPACITY;
-    return EMBER_OK;
-}
-
-template <int KEYS, int SHARE>
-__device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int b, int seq, int len, bool report) {
-    SeqBlocks r;
-    r.n = 0;
-    r.ns = r.wb = r.end = r.first = r.sinks = r.from = r.prefix = 0;
-    r.zero = false;
-    if (seq < 0) return r;                                   // padding: the row is left as it is
-    if (seq >= a.c.n_seqs) {
-        if (report) raise_status(a.status, EMBER_ERR_INVALID_ARG);
-        return r;
-    }
-    if (len < 0 || len > ((long long)a.c.width << a.c.page_shift)) {
-        if (report) raise_status(a.status, EMBER_ERR_CAPACITY);
-        return r;
-    }
-    if (SHARE != PD_OWN) {
-        const int e = shared_prefix(a, b, r.from, r.prefix);
-        if (e != EMBER_OK) {
-            if (report) raise_status(a.status, e);
-            return r;
-        }
-    }
-    if (SHARE == PD_TAIL) {
-        r.zero = true;
-        r.end = len;
-        r.first = min(r.from, len);
-        r.wb = r.first / KEYS;
-        r.n = r.first < len ? (len + KEYS - 1) / KEYS - r.wb : 0;
-        return r;
-    }
-    if (len == 0) {
-        r.zero = true;
-        return r;
-    }
-    const Visible v(len - 1, a.window, a.sinks);
-    r.end = v.end;
-    r.first = v.first;
-    r.sinks = v.sinks;
-    r.ns = (v.sinks + KEYS - 1) / KEYS;
-    r.wb = max(v.first / KEYS, r.ns);
-    r.n = r.ns + (v.end + KEYS - 1) / KEYS - r.wb;
-    return r;
-}
-
-template <int KEYS, int SHARE>
-__device__ __forceinline__ SeqBlocks seq_blocks(const PagedDecodeArgs& a, int b, bool report) {
-    return seq_blocks<KEYS, SHARE>(a, b, a.seqs ? a.seqs[b] : b, a.lens[b], report);
-}
 
 // Blocks of the whole line divided over `ctas` CTAs: CTA c takes [lo(c), lo(c + 1)).
 // (The launcher keeps the line below 2^30 blocks.)
@@ -153,63 +68,8 @@ struct Shares {
     __device__ __forceinline__ unsigned lo(unsigned c) const { return min(total, c * each); }
 };
 
-// Every warp by itself: the line's length, and in which sequence block `x`
-// (known once the length is: at(total)) lies.  Four sequences a lane, 128 at a time.
-constexpr int PD_SCAN = 4;
-template <int KEYS, int SHARE>
-__device__ __forceinline__ unsigned scan_chunk(const PagedDecodeArgs& a, int b0, bool report, int (&n)[PD_SCAN],
-                                               unsigned& before) {
-    const int lane = threadIdx.x & 31;
-    unsigned own = 0;
-    int seq[PD_SCAN], len[PD_SCAN];
-#pragma unroll
-    for (int e = 0; e < PD_SCAN; ++e) {
-        const int b = b0 + PD_SCAN * lane + e;
-        seq[e] = b >= a.B ? -1 : a.seqs ? a.seqs[b] : b;
-        len[e] = b >= a.B ? 0 : a.lens[b];
-    }
-#pragma unroll
-    for (int e = 0; e < PD_SCAN; ++e) {
-        n[e] = seq_blocks<KEYS, SHARE>(a, b0 + PD_SCAN * lane + e, seq[e], len[e], report).n;
-        own += n[e];
-    }
-    unsigned incl = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned y = __shfl_up_sync(FULL_MASK, incl, o);
-        if (lane >= o) incl += y;
-    }
-    before = incl - own;
-    return __shfl_sync(FULL_MASK, incl, 31);
-}
-
-// The workspace: a record for each CTA of the grid, then two partials for each.  PD_TAIL: a
-// record for each (sequence, kv head), two partials for each CTA, one for each (sequence, kv head).
-template <int SHARE>
-__device__ __forceinline__ float* partials(const PagedDecodeArgs& a, int grid) {
-    return a.ws + 4 * (SHARE == PD_TAIL ? (size_t)a.B * a.c.NKV : (size_t)grid);
-}
-
-// A place in the line: block `i` of kv head g of sequence b.
-struct Place {
-    int b, g, i;
-    SeqBlocks s;
-};
-
-template <int DP, int HT>
-struct PdSmem {
-    static constexpr int TILE = PD_KEYS<DP> * DP * 2;             // one K (or V) block
-    static constexpr int RING = PD_WARPS * PD_STAGES * 2 * TILE;
-    static constexpr int ROW = DP + 4;                            // a head's O row in the merge: no bank conflicts
-    static constexpr int SCR = 2 * 8 * HT * ROW * 4;              // O of two warps
-    static constexpr int TOTAL = RING + SCR;
-};
-
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
+// The workspace: a record for each CTA of the grid, then two partials for each.
+__device__ __forceinline__ float* partials(const PagedDecodeArgs& a, int grid) { return a.ws + 4 * (size_t)grid; }
 
 // HT: tiles of 8 query heads (1 up to G = 8, else 2)
 template <class E, int DP, int HT, bool CLUSTER, int SHARE>
@@ -223,9 +83,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g4 = lane >> 2, q4 = lane & 3;
     const int D = a.c.D, NKV = a.c.NKV, G = a.NH / NKV;
-    // PD_TAIL starts with the prefixes' kernel, which waited for all before it, and needs
-    // none of its results; only its end waits, so that the join finds both complete.
-    if (SHARE != PD_TAIL) pdl_wait();
+    pdl_wait();
 
     auto zero_row = [&](int b, int h0, int h1) {       // heads [h0, h1) of a sequence without keys
         uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (long long)b * a.ld_out);
@@ -241,7 +99,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
     auto no_keys = [&]() {                             // sequences without blocks, shared out over the CTAs
         for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
             const SeqBlocks s = seq_blocks<KEYS, SHARE>(a, b, false);
-            if (SHARE != PD_TAIL && s.zero) zero_row(b, 0, a.NH);
+            if (s.zero) zero_row(b, 0, a.NH);
             if (a.by_pair && s.n == 0)
                 for (int g = tid; g < NKV; g += PD_THREADS) record[b * NKV + g] = make_int4(0, 0, 0, 0);
         }
@@ -274,7 +132,6 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
             pdl_trigger();
             if (!a.by_pair && tid == 0) record[blockIdx.x] = make_int4(0, 0, 0, 0);
             no_keys();
-            if (SHARE == PD_TAIL) pdl_wait();
             return;
         }
         lo = share.lo(blockIdx.x);
@@ -391,28 +248,10 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
     unsigned at = lo;                        // the line's block at the segment's start
     do {
         const int seg = min(cur.s.n - cur.i, (int)(hi - at));   // its blocks in this CTA (0: a cluster's CTA without work)
-        // q of the group's heads as B fragments (columns >= G zero)
-        uint32_t qb[HT][KS][2];
-        const uint16_t* q = a.q + (long long)cur.b * a.ld_q + (long long)cur.g * G * D;
-#pragma unroll
-        for (int t = 0; t < HT; ++t)
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int h = 8 * t + g4, col = 16 * kk + 8 * e + 2 * q4;
-                    qb[t][kk][e] = h < G && col < D ? *reinterpret_cast<const uint32_t*>(q + h * D + col) : 0u;
-                }
-        // O^T: rows (dimensions) 16 i + g4 and + 8, columns (heads) 8 t + 2 q4 and + 1
-        float o[HT][KS][4];
-        float m[HT][2], l[HT][2];            // of heads 8 t + 2 q4 + e, m less LIFT; l over this lane's keys
-#pragma unroll
-        for (int t = 0; t < HT; ++t) {
-#pragma unroll
-            for (int i = 0; i < KS; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
-            m[t][0] = m[t][1] = SOFTMAX_FLOOR;
-            l[t][0] = l[t][1] = 0.f;
-        }
+        PdState<E, DP, HT> st;
+        st.begin(a.q + (long long)cur.b * a.ld_q + (long long)cur.g * G * D, G, D);
+        auto &o = st.o;
+        auto &m = st.m, &l = st.l;
         const unsigned seg_end = at + seg;
         for (; lo + warp + j * PD_WARPS < seg_end; ++j) {
             const int blk = cur.i + (int)(lo + warp + j * PD_WARPS - at);
@@ -421,99 +260,12 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
             __syncwarp();
             const uint32_t kt = ring_u + (uint32_t)(j % PD_STAGES) * 2 * L::TILE, vt = kt + L::TILE;
             const int key0 = KEYS * cur.s.index(blk);
-            const int mi = lane >> 3, r8 = lane & 7;
-            float s[NSUB][HT][4];            // S^T: keys g4 and g4 + 8 of each 16
-#pragma unroll
-            for (int u = 0; u < NSUB; ++u)
-#pragma unroll
-                for (int t = 0; t < HT; ++t) s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-                for (int u = 0; u < NSUB; ++u) {
-                    uint32_t ka[4];
-                    ldsm4(kt + q_off<DP>(16 * u + (mi & 1) * 8 + r8, 2 * kk + (mi >> 1)), ka[0], ka[1], ka[2], ka[3]);
-#pragma unroll
-                    for (int t = 0; t < HT; ++t) E::mma(s[u][t], ka, qb[t][kk][0], qb[t][kk][1]);
-                }
-            // every key of the block visible: below the end, and all in the window or all among the sinks
-            const bool whole = key0 + KEYS <= cur.s.end && (key0 >= cur.s.first || key0 + KEYS <= cur.s.sinks);
-            bool up = false;
-#pragma unroll
-            for (int u = 0; u < NSUB; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    bool in = true;
-                    if (!whole) {
-                        const int key = key0 + 16 * u + g4 + 8 * (i >> 1);
-                        in = key < cur.s.end && (key >= cur.s.first || key < cur.s.sinks);
-                    }
-#pragma unroll
-                    for (int t = 0; t < HT; ++t) {
-                        s[u][t][i] = in ? s[u][t][i] * sc : -INFINITY;
-                        up |= s[u][t][i] > m[t][i & 1] + (8.f + E::LIFT);
-                    }
-                }
-            if (__any_sync(FULL_MASK, up)) {
-#pragma unroll
-                for (int t = 0; t < HT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = -INFINITY;
-#pragma unroll
-                        for (int u = 0; u < NSUB; ++u) x = fmaxf(x, fmaxf(s[u][t][e], s[u][t][e + 2]));
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, d));
-                        x = fmaxf(m[t][e], x - E::LIFT);
-                        const float f = ex2(m[t][e] - x);
-                        m[t][e] = x;
-                        l[t][e] *= f;
-#pragma unroll
-                        for (int i = 0; i < KS; ++i) {
-                            o[t][i][e] *= f;
-                            o[t][i][e + 2] *= f;
-                        }
-                    }
-            }
-#pragma unroll
-            for (int u = 0; u < NSUB; ++u) {
-                uint32_t pb[HT][2], pr[HT][2];   // P^T as B fragments: keys 2 q4, + 1 (and + 8) of head g4
-#pragma unroll
-                for (int t = 0; t < HT; ++t) {
-                    float (&p)[4] = s[u][t];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = ex2(p[i] - m[t][i & 1]);
-                    l[t][0] += p[0] + p[2];
-                    l[t][1] += p[1] + p[3];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t x = E::pack(p[2 * e], p[2 * e + 1]);
-                        pb[t][e] = transpose8x8(x);
-                        // what the rounding left
-                        pr[t][e] = transpose8x8(E::pack(p[2 * e] - E::lo(x), p[2 * e + 1] - E::hi(x)));
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    uint32_t va[4];
-                    ldsm4t(vt + q_off<DP>(16 * u + (mi >> 1) * 8 + r8, 2 * i + (mi & 1)), va[0], va[1], va[2], va[3]);
-#pragma unroll
-                    for (int t = 0; t < HT; ++t) {
-                        E::mma(o[t][i], va, pb[t][0], pb[t][1]);
-                        E::mma(o[t][i], va, pr[t][0], pr[t][1]);
-                    }
-                }
-            }
+            st.block(kt, vt, key0, cur.s, sc);
             __syncwarp();                    // the stage is read: the next copy may fill it
         }
 
         // ---- merge the warps' states: 2 and 3 into 0 and 1, then 1 into 0 ----
-#pragma unroll
-        for (int t = 0; t < HT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(FULL_MASK, l[t][e], d);
+        st.end();
         __syncthreads();                     // the previous segment's output is written
         if (g4 == 0) {
 #pragma unroll
@@ -581,7 +333,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
         __syncthreads();
         if (CLUSTER) break;
         const bool complete = seg == cur.s.n;
-        if (SHARE != PD_TAIL && complete) {
+        if (complete) {
             uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (long long)cur.b * a.ld_out + (long long)cur.g * G * D);
             for (int e = tid; e < G * D / 2; e += PD_THREADS) {
                 const int row = e / (D / 2), d = 2 * (e - row * (D / 2));
@@ -594,9 +346,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
                     s_L[tid] == 0.f ? -INFINITY : s_M[tid] * LN2 + logf(s_L[tid]);
         } else {
             // slot 0: the segment reaches back to the CTA's first block, slot 1: it begins inside
-            size_t slot = 2 * blockIdx.x + (at == lo ? 0 : 1);
-            if (SHARE == PD_TAIL && complete) slot = 2 * (size_t)gridDim.x + (size_t)cur.b * NKV + cur.g;
-            float* ws = partials<SHARE>(a, gridDim.x) + slot * G * (D + 2);
+            float* ws = partials(a, gridDim.x) + (size_t)(2 * blockIdx.x + (at == lo ? 0 : 1)) * G * (D + 2);
             for (int e = tid; e < G * (D + 2); e += PD_THREADS) {
                 const int row = e / (D + 2), d = e - row * (D + 2);
                 ws[e] = d == 0 ? s_M[row] : d == 1 ? s_L[row] : s_o[row * L::ROW + d - 2];
@@ -608,7 +358,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
             const int parts =
                 cur.i == 0 && !complete ? (int)((at + cur.s.n - 1) / (hi - lo)) - (int)blockIdx.x + 1 : 0;
             record[a.by_pair ? cur.b * NKV + cur.g : blockIdx.x] =
-                make_int4(cur.b, cur.g, SHARE == PD_TAIL && complete ? -1 : parts, 2 * blockIdx.x + (at == lo ? 0 : 1));
+                make_int4(cur.b, cur.g, parts, 2 * blockIdx.x + (at == lo ? 0 : 1));
         }
         at = seg_end;
         if (at >= hi) break;
@@ -618,7 +368,6 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_paged_decode
     pdl_trigger();                           // late: the join's blocks would take issue slots meanwhile
     if (!CLUSTER) {
         no_keys();
-        if (SHARE == PD_TAIL) pdl_wait();
         return;
     }
 
@@ -681,7 +430,7 @@ __global__ void __launch_bounds__(PJ_THREADS) k_paged_join(PagedDecodeArgs a, in
     // (what another call wrote into a workspace that two share by mistake is not followed out of the buffers)
     if (parts <= 0 || c0 < 0 || c0 >= grid || parts > grid - c0 || b < 0 || b >= a.B || g < 0 || g >= a.c.NKV) return;
     // partial i: slot 0 of its CTA, but slot 1 of the first when the segment begins inside it
-    const float* base = partials<PD_OWN>(a, grid) + (size_t)h0 * (D + 2);
+    const float* base = partials(a, grid) + (size_t)h0 * (D + 2);
     const size_t slot = (size_t)G * (D + 2);
     auto part = [&](int h, int i) {
         return base + (2 * (size_t)(c0 + i) + (i == 0 ? rec.w & 1 : 0)) * slot + (size_t)h * (D + 2);
@@ -760,122 +509,6 @@ __global__ void __launch_bounds__(PJ_THREADS) k_paged_join(PagedDecodeArgs a, in
     }
 }
 
-// Joins what the prefixes' kernel and PD_TAIL have left of a row's kv head: block (kv head, row).
-// Threads take four dimensions each and the partials in turn.
-constexpr int SJ_THREADS = 128;
-
-template <class E>
-__global__ void __launch_bounds__(SJ_THREADS) k_shared_join(PagedDecodeArgs a, int grid) {
-    constexpr int KEYS = 16;                               // (of no account here)
-    __shared__ float s_m[16], s_inv[16];
-    __shared__ float4 s_o[SJ_THREADS];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = blockIdx.x, b = blockIdx.y;
-    const int D = a.c.D, NKV = a.c.NKV, G = a.NH / NKV;
-    pdl_wait();
-    const SeqBlocks s = seq_blocks<KEYS, PD_TAIL>(a, b, false);
-    if (!s.zero) return;                                   // the row is left as it is
-    // the prefix's partials: CTAs c0 .. c0 + np - 1 of the pair that the row lies in
-    const int2* head = reinterpret_cast<const int2*>(a.prefix);
-    int np = 0, slot0 = 0, at = 0;                         // their number, the first one's slot, the row in it
-    if (s.from > 0) {
-        int lo = 0;
-        for (int hi = a.n_groups; hi - lo > 1;) {
-            const int mid = (lo + hi) / 2;
-            if (a.groups[mid] <= b) lo = mid;
-            else hi = mid;
-        }
-        const int row0 = a.groups[lo], nx = (a.groups[lo + 1] - row0 + a.prefix_rows - 1) / a.prefix_rows;
-        const int i = b - row0, x = i / a.prefix_rows, r = i % a.prefix_rows, half = a.prefix_rows / 2;
-        const int2 line = head[0], first = head[1 + lo];
-        const unsigned tiles = (unsigned)(s.from + 63) / 64, each = max(1, line.x), pi = (unsigned)(g * nx + x);
-        const unsigned p0 = (unsigned)first.y + pi * tiles, c0 = p0 / each;
-        np = (int)((p0 + tiles - 1) / each - c0) + 1;
-        slot0 = first.x + (int)pi + (int)c0;
-        at = r / half * 128 + r % half * G;
-        // (what another call wrote into a workspace that two share by mistake is not followed out of the buffers)
-        if (slot0 < 0 || np < 0 || np > PD_MAX_CTAS || slot0 + np > a.prefix_slots) np = 0;
-    }
-    // the row's own keys: one partial of its own, or those of CTAs in turn
-    const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.ws) + (size_t)b * NKV + g);
-    const size_t own_slot = (size_t)G * (D + 2);
-    int no = rec.z < 0 ? 1 : rec.z;
-    const int c0 = rec.w >> 1;
-    if (no > 0 && rec.z > 0 && (c0 < 0 || c0 >= grid || no > grid - c0)) no = 0;
-    const float* own = partials<PD_TAIL>(a, grid);
-    auto own_part = [&](int i) {
-        const size_t k = rec.z < 0 ? 2 * (size_t)grid + (size_t)b * NKV + g : 2 * (size_t)(c0 + i) + (i == 0 ? rec.w & 1 : 0);
-        return own + k * own_slot;
-    };
-    const float* sums = a.prefix + a.prefix_head;
-    const float2* ml = reinterpret_cast<const float2*>(sums + (size_t)a.prefix_slots * 256 * D);
-    const int parts = np + no;
-    auto state = [&](int h, int i) {
-        return i < np ? __ldcg(ml + (size_t)(slot0 + i) * 256 + at + h)
-                      : __ldcg(reinterpret_cast<const float2*>(own_part(i - np) + (size_t)h * (D + 2)));
-    };
-    for (int h = warp; h < G; h += SJ_THREADS / 32) {
-        float M = SOFTMAX_FLOOR;
-        for (int i = lane; i < parts; i += 32) M = fmaxf(M, state(h, i).x);
-        M = warp_max(M);
-        float L = 0.f;
-        for (int i = lane; i < parts; i += 32) {
-            const float2 x = state(h, i);
-            L += x.y * ex2(x.x - M);
-        }
-        L = warp_sum(L);
-        if (lane == 0) {
-            s_m[h] = M;
-            s_inv[h] = L == 0.f ? 0.f : 1.f / L;
-            if (a.lse) a.lse[(long long)b * a.NH + g * G + h] = L == 0.f ? -INFINITY : M * LN2 + logf(L);
-        }
-    }
-    __syncthreads();
-    const int quads = G * (D / 4), wide = min(quads, SJ_THREADS), turns = SJ_THREADS / wide, t0 = tid / wide;
-    for (int q0 = 0; q0 < quads; q0 += wide) {
-        const int q = q0 + tid % wide, h = q / (D / 4), d = 4 * (q - h * (D / 4));
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (q < quads && t0 < turns)
-#pragma unroll 4
-            for (int i = t0; i < parts; i += turns) {
-                float4 x;
-                if (i < np) {
-                    x = __ldcg(reinterpret_cast<const float4*>(sums + ((size_t)(slot0 + i) * 256 + at + h) * D + d));
-                } else {
-                    const float2* p = reinterpret_cast<const float2*>(own_part(i - np) + (size_t)h * (D + 2) + 2 + d);
-                    const float2 u = __ldcg(p), v = __ldcg(p + 1);
-                    x = make_float4(u.x, u.y, v.x, v.y);
-                }
-                const float f = ex2(state(h, i).x - s_m[h]);
-                o.x = fmaf(x.x, f, o.x);
-                o.y = fmaf(x.y, f, o.y);
-                o.z = fmaf(x.z, f, o.z);
-                o.w = fmaf(x.w, f, o.w);
-            }
-        if (turns > 1) {
-            __syncthreads();
-            s_o[tid] = o;
-            __syncthreads();
-            if (t0 == 0)
-                for (int t = 1; t < turns; ++t) {
-                    const float4 y = s_o[tid + t * wide];
-                    o.x += y.x;
-                    o.y += y.y;
-                    o.z += y.z;
-                    o.w += y.w;
-                }
-        }
-        if (q < quads && t0 == 0) {
-            const float inv = s_inv[h];
-            uint2* out = reinterpret_cast<uint2*>(a.out + (long long)b * a.ld_out + (long long)(g * G + h) * D + d);
-            *out = make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
-        }
-    }
-}
-
-// Bytes of keys and values, read once for each row, up to which a call with shared prefixes does just that.
-constexpr double PD_TOGETHER = 32e6;
-
 int pd_grid_full(int sms, int G) { return min(PD_MAX_CTAS, sms * pd_ctas_per_sm(G <= 8 ? 1 : 2)); }
 
 // How a call is split: by the most blocks that its table and window allow.
@@ -933,80 +566,8 @@ cudaError_t launch_ht(PagedDecodeArgs a, int sms, cudaStream_t s) {
     return launch_k(k_paged_join<E>, dim3(records, G / heads), dim3(PJ_THREADS), 0, s, a, plan.grid, heads);
 }
 
-// Shared prefixes by themselves (tcgen05), beside them the rows' own keys, then the join.
-struct SharedPlan {
-    bool apart;
-    int grid;                                  // PD_TAIL's
-    size_t tail_floats;
-    PagedSharedWs prefix;
-};
-SharedPlan shared_plan(const PagedView& c, int B, int NH, int n_groups, int sms) {
-    SharedPlan p{};
-    const int G = NH / c.NKV;
-    const long long keys = (long long)c.width << c.page_shift;
-    p.apart = (double)B * c.NKV * keys * c.D * 4 > PD_TOGETHER;
-    p.grid = pd_grid_full(sms, G);
-    p.tail_floats = 4 * (size_t)B * c.NKV + (2 * (size_t)p.grid + (size_t)B * c.NKV) * G * (c.D + 2);
-    p.tail_floats = (p.tail_floats + 3) & ~(size_t)3;
-    p.prefix = paged_shared_ws(B, n_groups, NH, c.NKV, c.D, sms);
-    return p;
-}
-
-template <class E, int DP, int HT>
-cudaError_t launch_apart(PagedDecodeArgs a, const PagedPrefillMaps& maps, const SharedPlan& plan, int sms, cudaStream_t s) {
-    constexpr int SMEM = PdSmem<DP, HT>::TOTAL;
-    PagedPrefillArgs p{};
-    p.c = a.c;
-    p.q = a.q;
-    p.ld_q = a.ld_q;
-    p.n = a.B;
-    p.B = a.n_groups;
-    p.NH = a.NH;
-    p.seqs = a.prefixes;
-    p.cu = a.groups;
-    p.lens = a.lens;
-    p.scale = a.scale;
-    p.status = a.status;
-    p.shared = a.shared;
-    p.ws = a.ws + plan.tail_floats;
-    p.ws_head = plan.prefix.head;
-    p.slots = plan.prefix.slots;
-    cudaError_t e = launch_paged_shared(p, maps, sms, s);
-    if (e != cudaSuccess) return e;
-    a.by_pair = 1;
-    a.prefix = p.ws;
-    a.prefix_head = plan.prefix.head;
-    a.prefix_slots = plan.prefix.slots;
-    a.prefix_rows = plan.prefix.rows_per_pair;
-    auto k = k_paged_decode<E, DP, HT, false, PD_TAIL>;
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (e != cudaSuccess) return e;
-    e = launch_k(k, dim3(plan.grid), dim3(PD_THREADS), SMEM, s, a);
-    if (e != cudaSuccess) return e;
-    return launch_k(k_shared_join<E>, dim3(a.c.NKV, a.B), dim3(SJ_THREADS), 0, s, a, plan.grid);
-}
-
-// Whether and with what maps a call's prefixes go by themselves.
-bool shared_apart(const PagedDecodeArgs& a, const SharedPlan& plan, PagedPrefillMaps& maps) {
-    if (!plan.apart || !(a.scale > 0.f)) return false;
-    PagedPrefillArgs p{};
-    p.c = a.c;
-    p.q = a.q;
-    p.ld_q = a.ld_q;
-    p.n = a.B;
-    p.B = a.n_groups;
-    p.NH = a.NH;
-    return paged_prefill_maps(p, maps);
-}
-
 template <class E, int DP>
 cudaError_t launch_dp(const PagedDecodeArgs& a, int sms, cudaStream_t s) {
-    if (a.groups) {
-        const SharedPlan plan = shared_plan(a.c, a.B, a.NH, a.n_groups, sms);
-        PagedPrefillMaps maps;
-        if (shared_apart(a, plan, maps))
-            return a.NH / a.c.NKV <= 8 ? launch_apart<E, DP, 1>(a, maps, plan, sms, s) : launch_apart<E, DP, 2>(a, maps, plan, sms, s);
-    }
     if (a.groups) return a.NH / a.c.NKV <= 8 ? launch_ht<E, DP, 1, PD_SHARED>(a, sms, s) : launch_ht<E, DP, 2, PD_SHARED>(a, sms, s);
     return a.NH / a.c.NKV <= 8 ? launch_ht<E, DP, 1, PD_OWN>(a, sms, s) : launch_ht<E, DP, 2, PD_OWN>(a, sms, s);
 }
@@ -1016,12 +577,6 @@ cudaError_t launch_dp(const PagedDecodeArgs& a, int sms, cudaStream_t s) {
 size_t paged_decode_ws(const PagedView& c, int B, int NH, int window, int sinks, int sms) {
     const PdPlan plan = pd_plan(c, B, NH, window, sinks, sms);
     return plan.cluster ? 0 : (size_t)plan.grid * (4 + 2 * (size_t)(NH / c.NKV) * (c.D + 2)) * sizeof(float);
-}
-
-size_t paged_decode_shared_ws(const PagedView& c, int B, int NH, int n_groups, int sms) {
-    const SharedPlan p = shared_plan(c, B, NH, n_groups, sms);
-    const size_t together = paged_decode_ws(c, B, NH, 0, 0, sms);   // (also for scales that are not positive)
-    return p.apart ? max(together, (p.tail_floats + p.prefix.floats) * sizeof(float)) : together;
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int sms, cudaStream_t s) {

@@ -112,7 +112,7 @@ ember_status decode(const ember_paged_kv* kv, PagedDecodeArgs& a, const void* q,
     a.lse = lse;
     a.ws = static_cast<float*>(workspace);
     a.status = status;
-    e = launch_paged_decode(a, sms, (cudaStream_t)stream);
+    e = a.groups ? launch_paged_decode_shared(a, sms, (cudaStream_t)stream) : launch_paged_decode(a, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_failed("decode launch failed", e);
     return EMBER_OK;
 }

@@ -1,0 +1,364 @@
+// paged_shared.cu -- attention of one new token per sequence where groups of sequences share a
+// long prefix: out = softmax over the prefix's keys and the row's own, each prefix read once for
+// all rows of its group.
+//
+// Softmax over two sets of keys is joined from each set's maximum, sum and weighted values.  So
+// three launches:
+//   k_paged_prefill_tc<.., PT_SHARED>   the prefixes: the group's (row, head) pairs are the rows
+//                    of matrix products on tcgen05, which is where the work is (4 D flops a key
+//                    for each query head, against 4 D bytes a key and kv head)
+//   k_shared_tail    the rows' own keys, as in paged_decode.cu, bound by their bytes
+//   k_shared_join    the two
+// The second needs nothing of the first and fills the SMs as that leaves them; it ends after it.
+// The third starts when the second is through.
+//
+// Tails are short and many (a few hundred keys for each of hundreds of rows and kv heads), so a
+// warp, not a CTA, is what takes a share of the line of blocks: it works on its blocks alone and
+// leaves what it has of a (row, kv head) as one partial, with no other warp to wait for, and the
+// join adds up the few partials of each.  With shares for CTAs, whose warps merge their states
+// once for each (row, kv head), 64 rows of one block each on 8 kv heads took as long as 64 of 256
+// keys.
+//
+// Calls of little work read each row's keys once for each row instead (paged_decode.cu,
+// PD_SHARED), which is one launch.
+#include "paged_decode.cuh"
+
+namespace ember {
+
+namespace {
+
+// The workspace of k_shared_tail: {first slot, partials} for each (row, kv head), then the
+// partials, [G][D + 2] floats each: m, l, sums.  What warp w has of pair p lies in slot p + w,
+// which no other has: along the line p and w only rise, one of them at each step.
+__device__ __forceinline__ float* tail_partials(const PagedDecodeArgs& a) { return a.ws + ((2 * (size_t)a.B * a.c.NKV + 3) & ~(size_t)3); }
+
+template <class E, int DP, int HT>
+__global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_shared_tail(PagedDecodeArgs a) {
+    constexpr int KEYS = PD_KEYS<DP>, NSUB = KEYS / 16, KS = DP / 16, C8 = DP / 8;
+    using L = PdSmem<DP, HT>;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g4 = lane >> 2, q4 = lane & 3;
+    const int D = a.c.D, NKV = a.c.NKV, G = a.NH / NKV;
+    const unsigned W = blockIdx.x * PD_WARPS + warp, NW = gridDim.x * PD_WARPS;
+    int2* record = reinterpret_cast<int2*>(a.ws);
+
+    // (no wait: this grid starts when all CTAs of the prefixes' are past theirs, and everything
+    // before that one is then complete)
+    int n[PD_SCAN];
+    unsigned line = 0, before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32 * PD_SCAN) line += scan_chunk<KEYS, PD_TAIL>(a, b0, W == 0, n, before);
+    line *= NKV;
+    const unsigned each = max(1u, (line + NW - 1) / NW);
+    const unsigned lo = min(line, W * each), hi = min(line, lo + each);
+    for (int b = W; b < a.B; b += NW)            // rows without blocks
+        if (seq_blocks<KEYS, PD_TAIL>(a, b, false).n == 0)
+            for (int g = lane; g < NKV; g += 32) record[(size_t)b * NKV + g] = make_int2(0, 0);
+
+    if (lo < hi) {
+        Place cur;
+        unsigned run = 0;
+        for (int b0 = 0;; b0 += 32 * PD_SCAN) {
+            // one chunk: its counts are still in the registers
+            const unsigned total = a.B <= 32 * PD_SCAN ? line / NKV : scan_chunk<KEYS, PD_TAIL>(a, b0, false, n, before);
+            if (lo < run + total * NKV) {
+                unsigned at = run + before * NKV, first = 0;
+                int b = -1;
+#pragma unroll
+                for (int e = 0; e < PD_SCAN; ++e) {
+                    if (lo >= at && lo < at + (unsigned)n[e] * NKV) {
+                        b = b0 + PD_SCAN * lane + e;
+                        first = at;
+                    }
+                    at += (unsigned)n[e] * NKV;
+                }
+                const int src = __ffs(__ballot_sync(FULL_MASK, b >= 0)) - 1;
+                cur.b = __shfl_sync(FULL_MASK, b, src);
+                cur.s = seq_blocks<KEYS, PD_TAIL>(a, cur.b, false);
+                const unsigned x = lo - __shfl_sync(FULL_MASK, first, src);
+                cur.g = (int)(x / (unsigned)cur.s.n);
+                cur.i = (int)(x - (unsigned)cur.g * (unsigned)cur.s.n);
+                break;
+            }
+            run += total * NKV;
+        }
+        auto next_pair = [&](Place& p) {         // (inside the line)
+            p.i = 0;
+            if (++p.g == NKV) {
+                p.g = 0;
+                do p.s = seq_blocks<KEYS, PD_TAIL>(a, ++p.b, false);
+                while (p.s.n == 0 && p.b + 1 < a.B);
+            }
+        };
+
+        // ---- copies, a block ahead ----
+        const int mine = (int)(hi - lo);
+        const uint32_t ring = sa_u32(sm + warp * (PD_STAGES * 2 * L::TILE));
+        Place ld = cur;
+        int page[NSUB];                          // of its 16-key parts, looked up one block ahead
+        auto look_up = [&]() {
+            const int seq = a.seqs ? a.seqs[ld.b] : ld.b;
+#pragma unroll
+            for (int u = 0; u < NSUB; ++u) {
+                const int k0 = KEYS * ld.s.index(ld.i) + 16 * u;
+                page[u] = k0 < ld.s.end && k0 + 16 > ld.s.first ? a.c.table[(size_t)seq * a.c.width + (k0 >> a.c.page_shift)] : 0;
+            }
+        };
+        look_up();
+        auto issue = [&](int j) {
+            if (j < mine) {
+                const uint32_t kd = ring + (uint32_t)(j % PD_STAGES) * 2 * L::TILE, vd = kd + L::TILE;
+                const int key0 = KEYS * ld.s.index(ld.i), c = lane % C8;
+#pragma unroll
+                for (int u = 0; u < NSUB; ++u) {
+                    const int k0 = key0 + 16 * u;
+                    const bool ok = page[u] >= 0 && page[u] < a.c.n_pages;   // a bad page reads as zeros
+                    if (!ok && lane == 0) raise_status(a.status, EMBER_ERR_INVALID_ARG);
+                    const long long base =
+                        ok ? (long long)page[u] * a.c.page_stride + (long long)ld.g * a.c.head_stride +
+                                 (long long)(k0 & ((1 << a.c.page_shift) - 1)) * a.c.row_stride + c * 8
+                           : 0;
+#pragma unroll
+                    for (int i = 0; i < 16 * C8 / 32; ++i) {
+                        const int r = lane / C8 + i * (32 / C8), key = k0 + r;
+                        const bool in = ok && c * 8 < D && key < ld.s.end && key >= ld.s.first;
+                        const long long off = in ? base + (long long)r * a.c.row_stride : 0;
+                        cp_async16(kd + q_off<DP>(16 * u + r, c), a.c.k + off, in);
+                        cp_async16(vd + q_off<DP>(16 * u + r, c), a.c.v + off, in);
+                    }
+                }
+                if (j + 1 < mine) {
+                    if (++ld.i >= ld.s.n) next_pair(ld);
+                    look_up();
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int j = 0; j < PD_STAGES - 1; ++j) issue(j);
+
+        // ---- the warp's blocks of one (row, kv head) after another ----
+        const float sc = a.scale * LOG2E;
+        PdState<E, DP, HT> st;
+        for (int j = 0; j < mine;) {
+            const int seg = min(cur.s.n - cur.i, mine - j);
+            st.begin(a.q + (long long)cur.b * a.ld_q + (long long)cur.g * G * D, G, D);
+            for (int e = 0; e < seg; ++e, ++j) {
+                issue(j + PD_STAGES - 1);
+                cp_async_wait<PD_STAGES - 1>();
+                __syncwarp();
+                const uint32_t kt = ring + (uint32_t)(j % PD_STAGES) * 2 * L::TILE;
+                st.block(kt, kt + L::TILE, KEYS * cur.s.index(cur.i + e), cur.s, sc);
+                __syncwarp();                    // the stage is read: the next copy may fill it
+            }
+            st.end();
+            const size_t pair = (size_t)cur.b * NKV + cur.g;
+            float* out = tail_partials(a) + (pair + W) * G * (D + 2);
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int h = 8 * t + 2 * q4 + e;
+                    if (h >= G) continue;
+                    if (g4 == 0) *reinterpret_cast<float2*>(out + h * (D + 2)) = make_float2(st.m[t][e], st.l[t][e]);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            if (16 * i + 8 * r < D) out[h * (D + 2) + 2 + 16 * i + g4 + 8 * r] = st.o[t][i][e + 2 * r];
+                }
+            // the pair's first warp knows how many there are: all have the same share
+            if (cur.i == 0 && lane == 0)
+                record[pair] = make_int2((int)(pair + W), (int)((lo + j - seg + cur.s.n - 1) / each) - (int)W + 1);
+            if (j < mine) next_pair(cur);
+        }
+        cp_async_wait<0>();
+    }
+    pdl_trigger();
+    pdl_wait();                                  // this grid ends after the prefixes'
+}
+
+// Joins what the two have left of a row's kv head: block (kv head, row).  Threads take four
+// dimensions each and the partials in turn.
+constexpr int SJ_THREADS = 256;
+
+template <class E>
+__global__ void __launch_bounds__(SJ_THREADS) k_shared_join(PagedDecodeArgs a, int warps) {
+    __shared__ float s_m[16], s_inv[16];
+    __shared__ float4 s_o[SJ_THREADS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = blockIdx.x, b = blockIdx.y;
+    const int D = a.c.D, NKV = a.c.NKV, G = a.NH / NKV;
+    // What the call got may be read before the wait (the kernels before began after it was complete).
+    const SeqBlocks s = seq_blocks<16, PD_TAIL>(a, b, false);
+    int pi = 0, at = 0, group = 0;               // the pair of row tiles among its group's, the row in it
+    if (s.zero && s.from > 0) {
+        int from, prefix;
+        shared_prefix(a, b, from, prefix, group);
+        const int row0 = a.groups[group], nx = (a.groups[group + 1] - row0 + a.prefix_rows - 1) / a.prefix_rows;
+        const int i = b - row0, r = i % a.prefix_rows, half = a.prefix_rows / 2;
+        pi = g * nx + i / a.prefix_rows;
+        at = r / half * 128 + r % half * G;
+    }
+    pdl_wait();
+    if (!s.zero) return;                         // the row is left as it is
+    const size_t pair = (size_t)b * NKV + g;
+    const int2* head = reinterpret_cast<const int2*>(a.prefix);
+    const int2 line = __ldcg(head), first = __ldcg(head + 1 + group), rec = __ldcg(reinterpret_cast<const int2*>(a.ws) + pair);
+    // (what another call wrote into a workspace that two share by mistake is not followed out of the buffers)
+    int np = 0, slot0 = 0;                       // the prefix's partials: those of neighbouring CTAs
+    if (s.from > 0) {
+        const unsigned tiles = (unsigned)(s.from + 63) / 64, each = max(1, line.x), p0 = (unsigned)first.y + (unsigned)pi * tiles;
+        np = (int)((p0 + tiles - 1) / each - p0 / each) + 1;
+        slot0 = first.x + pi + (int)(p0 / each);
+        if (slot0 < 0 || np < 0 || np > a.prefix_slots || slot0 > a.prefix_slots - np) np = 0;
+    }
+    int no = rec.y;                              // the row's own
+    const int slots = a.B * NKV + warps;
+    if (no < 0 || no > slots || rec.x < 0 || rec.x > slots - no) no = 0;
+    const float* own = tail_partials(a) + (size_t)rec.x * G * (D + 2);
+    const float* sums = a.prefix + a.prefix_head + ((size_t)slot0 * 256 + at) * D;
+    const float2* ml = reinterpret_cast<const float2*>(a.prefix + a.prefix_head + (size_t)a.prefix_slots * 256 * D) + (size_t)slot0 * 256 + at;
+    const int parts = np + no;
+    auto state = [&](int h, int i) {
+        return __ldcg(i < np ? ml + (size_t)i * 256 + h : reinterpret_cast<const float2*>(own + ((size_t)(i - np) * G + h) * (D + 2)));
+    };
+    for (int h = warp; h < G; h += SJ_THREADS / 32) {
+        float M = SOFTMAX_FLOOR, l = 0.f;
+        for (int i = lane; i < parts; i += 32) {
+            const float2 x = state(h, i);
+            const float to = fmaxf(M, x.x);
+            l = l * ex2(M - to) + x.y * ex2(x.x - to);
+            M = to;
+        }
+        const float top = warp_max(M);
+        l = warp_sum(l * ex2(M - top));
+        if (lane == 0) {
+            s_m[h] = top;
+            s_inv[h] = l == 0.f ? 0.f : 1.f / l;
+            if (a.lse) a.lse[(long long)b * a.NH + g * G + h] = l == 0.f ? -INFINITY : top * LN2 + logf(l);
+        }
+    }
+    __syncthreads();
+    const int quads = G * (D / 4), wide = min(quads, SJ_THREADS), turns = SJ_THREADS / wide, t0 = tid / wide;
+    for (int q0 = 0; q0 < quads; q0 += wide) {
+        const int q = q0 + tid % wide, h = q / (D / 4), d = 4 * (q - h * (D / 4));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q < quads && t0 < turns) {
+            const float m = s_m[h];
+#pragma unroll 4
+            for (int i = t0; i < parts; i += turns) {
+                float4 x;
+                if (i < np) {
+                    x = __ldcg(reinterpret_cast<const float4*>(sums + ((size_t)i * 256 + h) * D + d));
+                } else {
+                    const float2* p = reinterpret_cast<const float2*>(own + ((size_t)(i - np) * G + h) * (D + 2) + 2 + d);
+                    const float2 u = __ldcg(p), v = __ldcg(p + 1);
+                    x = make_float4(u.x, u.y, v.x, v.y);
+                }
+                const float f = ex2(state(h, i).x - m);
+                o.x = fmaf(x.x, f, o.x);
+                o.y = fmaf(x.y, f, o.y);
+                o.z = fmaf(x.z, f, o.z);
+                o.w = fmaf(x.w, f, o.w);
+            }
+        }
+        if (turns > 1) {
+            __syncthreads();
+            s_o[tid] = o;
+            __syncthreads();
+            if (t0 == 0)
+                for (int t = 1; t < turns; ++t) {
+                    const float4 y = s_o[tid + t * wide];
+                    o.x += y.x;
+                    o.y += y.y;
+                    o.z += y.z;
+                    o.w += y.w;
+                }
+        }
+        if (q < quads && t0 == 0) {
+            const float inv = s_inv[h];
+            uint2* out = reinterpret_cast<uint2*>(a.out + (long long)b * a.ld_out + (long long)(g * G + h) * D + d);
+            *out = make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
+        }
+    }
+}
+
+// Bytes of keys and values, read once for each row, up to which a call does just that.
+constexpr double PD_TOGETHER = 32e6;
+
+struct SharedPlan {
+    bool apart;                                  // the prefixes by themselves
+    int grid;                                    // k_shared_tail's
+    size_t tail_floats;
+    PagedSharedWs prefix;
+};
+SharedPlan shared_plan(const PagedView& c, int B, int NH, int n_groups, int sms) {
+    SharedPlan p{};
+    const int G = NH / c.NKV;
+    const long long keys = (long long)c.width << c.page_shift;
+    p.apart = (double)B * c.NKV * keys * c.D * 4 > PD_TOGETHER;
+    p.grid = sms * pd_ctas_per_sm(G <= 8 ? 1 : 2);
+    p.tail_floats = ((2 * (size_t)B * c.NKV + 3) & ~(size_t)3) + ((size_t)B * c.NKV + (size_t)p.grid * PD_WARPS) * G * (c.D + 2);
+    p.tail_floats = (p.tail_floats + 3) & ~(size_t)3;
+    p.prefix = paged_shared_ws(B, n_groups, NH, c.NKV, c.D, sms);
+    return p;
+}
+
+template <class E, int DP, int HT>
+cudaError_t launch_ht(PagedDecodeArgs a, const PagedPrefillArgs& p, const PagedPrefillMaps& maps, const SharedPlan& plan, int sms,
+                      cudaStream_t s) {
+    constexpr int SMEM = PdSmem<DP, HT>::RING;
+    cudaError_t e = launch_paged_shared(p, maps, sms, s);
+    if (e != cudaSuccess) return e;
+    auto k = k_shared_tail<E, DP, HT>;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    e = launch_k(k, dim3(plan.grid), dim3(PD_THREADS), SMEM, s, a);
+    if (e != cudaSuccess) return e;
+    return launch_k(k_shared_join<E>, dim3(a.c.NKV, a.B), dim3(SJ_THREADS), 0, s, a, plan.grid * PD_WARPS);
+}
+template <class E>
+cudaError_t launch_type(const PagedDecodeArgs& a, const PagedPrefillArgs& p, const PagedPrefillMaps& m, const SharedPlan& plan,
+                        int sms, cudaStream_t s) {
+    if (a.NH / a.c.NKV <= 8) return a.c.D <= 64 ? launch_ht<E, 64, 1>(a, p, m, plan, sms, s) : launch_ht<E, 128, 1>(a, p, m, plan, sms, s);
+    return a.c.D <= 64 ? launch_ht<E, 64, 2>(a, p, m, plan, sms, s) : launch_ht<E, 128, 2>(a, p, m, plan, sms, s);
+}
+
+}  // namespace
+
+size_t paged_decode_shared_ws(const PagedView& c, int B, int NH, int n_groups, int sms) {
+    const SharedPlan p = shared_plan(c, B, NH, n_groups, sms);
+    const size_t together = paged_decode_ws(c, B, NH, 0, 0, sms);   // (also for scales that are not positive)
+    return p.apart ? max(together, (p.tail_floats + p.prefix.floats) * sizeof(float)) : together;
+}
+
+cudaError_t launch_paged_decode_shared(PagedDecodeArgs a, int sms, cudaStream_t s) {
+    const SharedPlan plan = shared_plan(a.c, a.B, a.NH, a.n_groups, sms);
+    PagedPrefillArgs p{};
+    p.c = a.c;
+    p.q = a.q;
+    p.ld_q = a.ld_q;
+    p.n = a.B;
+    p.B = a.n_groups;
+    p.NH = a.NH;
+    PagedPrefillMaps maps;
+    // (the row threads of the prefixes' kernel take scores against a maximum of the products: scale > 0)
+    if (!plan.apart || !(a.scale > 0.f) || !paged_prefill_maps(p, maps)) return launch_paged_decode(a, sms, s);
+    p.seqs = a.prefixes;
+    p.cu = a.groups;
+    p.lens = a.lens;
+    p.scale = a.scale;
+    p.status = a.status;
+    p.shared = a.shared;
+    p.ws = a.ws + plan.tail_floats;
+    p.ws_head = plan.prefix.head;
+    p.slots = plan.prefix.slots;
+    a.prefix = p.ws;
+    a.prefix_head = plan.prefix.head;
+    a.prefix_slots = plan.prefix.slots;
+    a.prefix_rows = plan.prefix.rows_per_pair;
+    return a.c.bf16 ? launch_type<ElemBf16>(a, p, maps, plan, sms, s) : launch_type<ElemF16>(a, p, maps, plan, sms, s);
+}
+
+}  // namespace ember
