@@ -175,6 +175,34 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return r;
 }
 
+// Four neighbouring lanes exchange the four 16-byte pieces that each holds of its row, so that
+// together they write 64 bytes of one row after another instead of 16 of four rows each:
+// afterwards q[i] is piece lane % 4 of row i of the four.
+__device__ __forceinline__ void transpose_four(uint4 (&q)[4]) {
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+    auto swap = [&](uint4& x, uint4& y, bool upper, int d) {   // lanes d apart: my y for its x
+        const uint4 give = upper ? x : y;
+        uint4 got;
+        got.x = __shfl_xor_sync(FULL_MASK, give.x, d);
+        got.y = __shfl_xor_sync(FULL_MASK, give.y, d);
+        got.z = __shfl_xor_sync(FULL_MASK, give.z, d);
+        got.w = __shfl_xor_sync(FULL_MASK, give.w, d);
+        if (upper) x = got;
+        else y = got;
+    };
+    swap(q[0], q[1], odd, 1);
+    swap(q[2], q[3], odd, 1);
+    swap(q[0], q[2], high, 2);
+    swap(q[1], q[3], high, 2);
+}
+// The rows that those four lanes' pointers stand for.
+template <class T>
+__device__ __forceinline__ void rows_of_four(T* own, T* (&rows)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        rows[i] = reinterpret_cast<T*>(__shfl_sync(FULL_MASK, (unsigned long long)own, (threadIdx.x & 28) | i));
+}
+
 // What one CTA index stands for: the pair of query tiles of one kv head.
 struct PtPair {
     int g, seq, row0, tokens, pos0;   // kv head, table row, first query row, tokens, position of the first
@@ -832,20 +860,31 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         }
         if (SHARED) {   // the rows as they are; joined by another kernel
             const bool store = live && p.slot < a.slots;
-            float* o_row = a.ws + a.ws_head + ((size_t)p.slot * (2 * PT_ROWS) + t * PT_ROWS + r) * D;
+            float* own = store ? a.ws + a.ws_head + ((size_t)p.slot * (2 * PT_ROWS) + t * PT_ROWS + r) * D : nullptr;
             if (ok && nkt > 0) {
                 const int last = base + nkt - 1;
                 ok = wait_all(&o_full[2 * t + (last & 1)], last >> 1);
                 tc_fence_after();
                 if (ok) {
+                    // (16 bytes of 32 rows each at a time took 4 us for rows of 64, 8 us for 128)
+                    float* rows[4];
+                    rows_of_four(own, rows);
 #pragma unroll
                     for (int c = 0; c < DP; c += 32) {
                         uint32_t o[32];
                         tmem_ld32(tO + c, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            if (store && c + i < D) *reinterpret_cast<uint4*>(o_row + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        for (int i = 0; i < 32; i += 16) {
+                            uint4 q[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) q[k] = make_uint4(o[i + 4 * k], o[i + 4 * k + 1], o[i + 4 * k + 2], o[i + 4 * k + 3]);
+                            transpose_four(q);
+                            const int d = c + i + 4 * (lane & 3);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (rows[k] && d < D) *reinterpret_cast<uint4*>(rows[k] + d) = q[k];
+                        }
                     }
                     if (store)
                         reinterpret_cast<float2*>(a.ws + a.ws_head + (size_t)a.slots * (2 * PT_ROWS) * D)[(size_t)p.slot * (2 * PT_ROWS) + t * PT_ROWS + r] =
@@ -889,13 +928,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         {
             const long long row = p.row0 + tok;
             uint16_t* own = live ? a.out + row * a.ld_out + (long long)(p.g * G + h) * D : nullptr;
-            // four neighbouring lanes exchange 16-byte pieces, so that together they
-            // write 64 bytes of one row after another instead of 16 of four rows each
             uint16_t* rows[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                rows[i] = reinterpret_cast<uint16_t*>(__shfl_sync(FULL_MASK, (unsigned long long)own, (lane & ~3) | i));
-            const bool odd = lane & 1, high = lane & 2;
+            rows_of_four(own, rows);
 #pragma unroll
             for (int c0 = 0; c0 < DP; c0 += 32) {
                 if (c0 >= D) break;
@@ -905,21 +939,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     const uint32_t* x = w + c0 / 2 + 4 * i;
                     q[i] = make_uint4(x[0], x[1], x[2], x[3]);
                 }
-                auto swap = [&](uint4& x, uint4& y, bool upper, int d) {   // lanes d apart: my y for its x
-                    const uint4 give = upper ? x : y;
-                    uint4 got;
-                    got.x = __shfl_xor_sync(FULL_MASK, give.x, d);
-                    got.y = __shfl_xor_sync(FULL_MASK, give.y, d);
-                    got.z = __shfl_xor_sync(FULL_MASK, give.z, d);
-                    got.w = __shfl_xor_sync(FULL_MASK, give.w, d);
-                    if (upper) x = got;
-                    else y = got;
-                };
-                swap(q[0], q[1], odd, 1);
-                swap(q[2], q[3], odd, 1);
-                swap(q[0], q[2], high, 2);
-                swap(q[1], q[3], high, 2);
-                // now q[i] is piece lane % 4 of row i of the four
+                transpose_four(q);
                 const int c = c0 + 8 * (lane & 3);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
