@@ -7,7 +7,7 @@
 // meanwhile, and waits for t only when it has come to the adapters.
 //
 // Both are the same tcgen05 kernel.  A tile is 128 rows of W (or the R rows of one A_a) by
-// NT rows of x: the weights are the M = 128 operand, so that a few rows of x waste no
+// up to NT rows of x: the weights are the M = 128 operand, so that a few rows of x waste no
 // tensor work and W streams through at the memory's rate.  The adapters of a tile's rows
 // are further blocks along K: B_a's 128 rows against t, where t stands as zeros for the
 // rows that have another adapter.  Only the columns from an adapter's first to its last row
@@ -23,8 +23,8 @@
 // calls give equal bits.  Many tiles run persistently, one CTA an SM, the next tile's
 // products under the last one's output.
 //
-// Warp 0: copies; warp 1: TMEM and products; warps 2-5: output; warp 6: which adapters a tile
-// has; warps 6-9: t's tiles.  Every wait is bounded; a timeout raises EMBER_ERR_TIMEOUT, the
+// Warp 0: copies; warp 1: TMEM and products; warps 2-5: output; warps 6-9: which adapters a
+// tile has, and t's tiles.  Every wait is bounded; a timeout raises EMBER_ERR_TIMEOUT, the
 // CTA drains its copies and frees TMEM.
 #include <cudaTypedefs.h>
 
@@ -45,73 +45,99 @@ constexpr int AD_LD = AD_M + 4;                  // their distance in shared mem
 template <int NT, bool LOW>
 struct AdSmem {
     static constexpr int A_BYTES = AD_M * 128, X_BYTES = NT * 128, STAGE = A_BYTES + X_BYTES;
-    // a tile of few rows leaves room for the other launch's CTA on the same SM
-    static constexpr int STAGES = NT == 256 ? 4 : NT == 128 ? 6 : LOW ? 4 : 5;
+    // a tile of few rows leaves room for the other launch's CTA on the same SM, the first launch's
+    // wide tiles for a second one
+    static constexpr int STAGES = NT == 256 ? 4 : NT == 128 ? (LOW ? 3 : 6) : LOW ? 4 : 5;
+    // an adapter's block in a stage: 16 ranks of 128 rows of B, and both terms of t's
+    static constexpr int SLAB_A = AD_M * 32, SLAB_T = NT * 32, SLABS = STAGE / (SLAB_A + 2 * SLAB_T);
+    static constexpr int OFF_T = SLABS * SLAB_A;
     static constexpr int OUT = AD_SLICE * AD_LD * 4;
     static constexpr int OFF_OUT = STAGES * STAGE;
     static constexpr int OFF_LIST = OFF_OUT + OUT;           // [2][NT] entries
-    static constexpr int OFF_IDS = OFF_LIST + 2 * NT * 8;    // [2][NT]
-    static constexpr int OFF_BAR = OFF_IDS + 2 * NT * 4;
+    static constexpr int OFF_IDS = OFF_LIST + 2 * NT * 16;   // [2][NT]
+    static constexpr int OFF_FIRST = OFF_IDS + 2 * NT * 4;   // a bit for each row
+    static constexpr int OFF_BAR = OFF_FIRST + 32;
     static constexpr int TOTAL = OFF_BAR + 320 + 1024;       // + alignment slack
     static_assert(TOTAL <= 232448, "shared memory of a CTA");
     static_assert(STAGES * STAGE >= NT * AD_LD * 4, "the cluster's sums");
 };
 
 // An adapter of a tile and the columns [c0, c1) of the tile, multiples of 16, that hold its rows.
-struct AdEntry {
+struct alignas(16) AdEntry {
     int adapter;
     uint16_t c0, c1;
+    float scale;
 };
 
-// The adapters of rows [row0, row0 + NT) of ids in rising order, by one warp; their number.
+// Shared-memory descriptor of a K-major tile with the 32-byte swizzle: rows of 32 bytes (16
+// ranks), 8-row groups 256 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3ffffu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)6 << 61;
+}
+
+// The adapters of rows [row0, row0 + NT) of ids, in the order in which they come first, by the
+// AD_BUILDERS warps together; their number.  Each thread compares its rows' ids with all others:
+// NT broadcast reads, where a search for one adapter after another took 0.15 us for each.
 template <int NT>
-__device__ int list_adapters(const AdapterArgs& a, int row0, AdEntry* list, int* s_ids) {
-    constexpr int PER = (NT + 31) / 32;
-    const int lane = threadIdx.x & 31;
-    uint32_t id[PER];                            // none: all bits
+__device__ __forceinline__ int list_adapters(const AdapterArgs& a, int row0, AdEntry* list, int* s_ids, uint32_t* s_first) {
+    constexpr int T = 32 * AD_BUILDERS, PER = (NT + T - 1) / T;
+    const int tid = threadIdx.x - (AD_THREADS - T), lane = tid & 31;
+    auto sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(T) : "memory"); };
+    float scale[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        const int c = k * 32 + lane, row = row0 + c;
-        int x = c < NT && row < a.n ? a.ids[row] : -1;
+        const int c = k * T + tid, row = row0 + c;
+        int x = c < a.nt && row < a.n ? a.ids[row] : -1;
         if (x >= a.n_adapters) {
             raise_status(a.status, EMBER_ERR_INVALID_ARG);
             x = -1;
         }
-        id[k] = (uint32_t)x;
-        if (c < NT) s_ids[c] = x;
+        if (c < NT) s_ids[c] = max(x, -1);
+        scale[k] = x >= 0 && a.scale ? a.scale[x] : 1.f;
     }
-    int n = 0;
-    uint32_t from = 0;
-    while (true) {
-        uint32_t least = ~0u, lo = ~0u, hi = 0;
+    sync();
+    int last[PER];
+    bool first[PER];
 #pragma unroll
-        for (int k = 0; k < PER; ++k)
-            if (id[k] >= from && (int)id[k] >= 0) least = min(least, id[k]);
-        least = __reduce_min_sync(FULL_MASK, least);
-        if (least == ~0u) break;
-#pragma unroll
-        for (int k = 0; k < PER; ++k)
-            if (id[k] == least) {
-                lo = min(lo, (uint32_t)(k * 32 + lane));
-                hi = (uint32_t)(k * 32 + lane + 1);
+    for (int k = 0; k < PER; ++k) {
+        const int c = k * T + tid, x = c < NT ? s_ids[c] : -1;
+        last[k] = c;
+        first[k] = x >= 0;
+        if (x >= 0) {
+#pragma unroll 4
+            for (int j = 0; j < NT; j += 4) {
+                const int4 y = *reinterpret_cast<const int4*>(s_ids + j);
+                if (y.x == x) last[k] = max(last[k], j), first[k] = first[k] && j >= c;
+                if (y.y == x) last[k] = max(last[k], j + 1), first[k] = first[k] && j + 1 >= c;
+                if (y.z == x) last[k] = max(last[k], j + 2), first[k] = first[k] && j + 2 >= c;
+                if (y.w == x) last[k] = max(last[k], j + 3), first[k] = first[k] && j + 3 >= c;
             }
-        lo = __reduce_min_sync(FULL_MASK, lo);
-        hi = __reduce_max_sync(FULL_MASK, hi);
-        if (lane == 0) list[n] = AdEntry{(int)least, (uint16_t)(lo & ~15u), (uint16_t)((hi + 15u) & ~15u)};
-        ++n;
-        from = least + 1;
+        }
+        const unsigned m = __ballot_sync(FULL_MASK, first[k]);
+        if (lane == 0 && c < NT) s_first[c / 32] = m;
     }
-    __syncwarp();
+    sync();
+    int n = 0;
+    constexpr int WORDS = (NT + 31) / 32;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int c = k * T + tid;
+        if (!first[k]) continue;
+        int at = __popc(s_first[c / 32] & ((1u << lane) - 1u));
+        for (int w = 0; w < c / 32; ++w) at += __popc(s_first[w]);
+        list[at] = AdEntry{s_ids[c], (uint16_t)(c & ~15), (uint16_t)((last[k] + 16) & ~15), scale[k]};
+    }
+    for (int w = 0; w < WORDS; ++w) n += __popc(s_first[w]);
+    sync();
     return n;
 }
 
 // Eight sums of a row of x.  First launch: ranks r .. r + 7 of its adapter, as two terms (and
 // zeros for the ranks that fill up a product); second: outputs m .. m + 7.  True: beyond f16.
 template <class E>
-__device__ __forceinline__ bool store_low(const AdapterArgs& a, int row, int r, int adapter, float (&y)[8]) {
+__device__ __forceinline__ bool store_low(const AdapterArgs& a, int row, int r, float scale, float (&y)[8]) {
     const int RP = (a.R + 15) & ~15;
-    const float scale = a.scale ? a.scale[adapter] : 1.f;
-    uint16_t* t = a.t + (long long)row * 2 * RP + r;
+    uint16_t* t = a.t + (long long)row * 2 * RP + r / 16 * 32 + r % 16;   // both terms of 16 ranks side by side
     uint32_t hi[4], lo[4];
     bool bad = false;
 #pragma unroll
@@ -122,16 +148,15 @@ __device__ __forceinline__ bool store_low(const AdapterArgs& a, int row, int r, 
         lo[j] = E::pack(u - E::lo(hi[j]), v - E::hi(hi[j]));
     }
     *reinterpret_cast<uint4*>(t) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(t + RP) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(t + 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     if (r + 8 == a.R && a.R < RP) {
         *reinterpret_cast<uint4*>(t + 8) = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(t + RP + 8) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(t + 24) = make_uint4(0u, 0u, 0u, 0u);
     }
     return bad;
 }
 template <class E>
 __device__ __forceinline__ void store_out(const AdapterArgs& a, int row, int m, const float (&y)[8]) {
-    if (m >= a.N) return;
     if (a.out_f32) {
         float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * a.ld_out + m);
         o[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -155,6 +180,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     float* s_out = reinterpret_cast<float*>(sm + L::OFF_OUT);
     AdEntry* s_list = reinterpret_cast<AdEntry*>(sm + L::OFF_LIST);
     int* s_ids = reinterpret_cast<int*>(sm + L::OFF_IDS);
+    uint32_t* s_first = reinterpret_cast<uint32_t*>(sm + L::OFF_FIRST);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
     uint64_t* full = bar;                // [S] a stage's copies have landed
     uint64_t* empty = bar + S;           // [S] its products are done
@@ -170,13 +196,11 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     static_assert((4 * S + 8) * 8 + 6 * 4 <= 320, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int C = a.splits, part = C > 1 ? (int)(blockIdx.x % C) : 0;
+    const int CL = a.splits, rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;   // CTAs of a cluster
     const int nk = (a.K + AD_BK - 1) / AD_BK;
-    const int kb0 = (int)((long long)nk * part / C), kb1 = (int)((long long)nk * (part + 1) / C);
-    const int start = (int)blockIdx.x / C, stride = (int)gridDim.x / C;   // tiles start, start + stride, ..
+    const int start = (int)blockIdx.x / CL, stride = (int)gridDim.x / CL;
     const int RP = (a.R + 15) & ~15;                          // ranks with those that fill up a product
-    const bool both = a.R <= 32;                              // both terms of t fit one stage
-    const int blocks = both ? 1 : 2 * ((RP + 63) / 64);       // stages of an adapter
+    const int slabs = RP / 16;                                // blocks of an adapter
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -189,7 +213,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 4);
             mbar_init(&list_full[b], 1);
-            mbar_init(&list_empty[b], 1 + AD_BUILDERS);   // copies, products, all builders but the one that lists
+            mbar_init(&list_empty[b], 2 + AD_BUILDERS);   // copies, products, builders
         }
         sflag[0] = sflag[1] = sflag[2] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -205,42 +229,52 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     if (LOW) {
         pdl_wait();
         pdl_trigger();
-        if (warp == 6) {                         // the CTA's one row tile
-            const int n = list_adapters<NT>(a, start % a.row_tiles * NT, s_list, s_ids);
-            if (lane == 0) s_count[0] = n;
+        if (warp >= 6) {                         // the CTA's one row tile
+            const int n = list_adapters<NT>(a, start % a.row_tiles * a.nt, s_list, s_ids, s_first);
+            if (warp == 6 && lane == 0) s_count[0] = n;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // Its tiles.  In the first launch one holds as many of the list's adapters as have room in
-    // 128 rows, and the CTA takes every step-th of its row tile.
+    // Its tiles.  Second launch: the cluster's start, start + stride, ..; with a cluster of several
+    // it is one, whose K they share.  First launch: a tile holds as many of the list's adapters as
+    // have room in 128 rows, the cluster has every step-th of its row tile's, and as many CTAs as
+    // there are for each share one's K.
     const int P = LOW ? AD_M / a.R : 1;
-    const int step = LOW ? stride / a.row_tiles : 1;
-    const int tiles = LOW ? max(0, ((s_count[0] + P - 1) / P - start / a.row_tiles + step - 1) / step)
-                          : max(0, (a.row_tiles * a.col_tiles - start + stride - 1) / stride);
+    const int step = LOW ? stride / a.row_tiles : 1, first_tile = LOW ? start / a.row_tiles : 0;
+    const int have = LOW ? max(0, ((s_count[0] + P - 1) / P - first_tile + step - 1) / step)
+                         : max(0, (a.row_tiles * a.col_tiles - start + stride - 1) / stride);
+    int C = CL;                                  // CTAs that share a tile
+    if (LOW)
+        while (C > 1 && have * C > CL) C /= 2;
+    const int part = rank % C, first_of = rank / C, every = LOW ? CL / C : 1;
+    const int tiles = LOW ? max(0, (have - first_of + every - 1) / every) : have;
+    const int kb0 = (int)((long long)nk * part / C), kb1 = (int)((long long)nk * (part + 1) / C);
     struct Tile {
         int row0, m0, e0;                        // first row of x, first row of W, first entry (first launch)
     };
     auto tile_of = [&](int li) {
         Tile t;
         const int i = start + li * stride;
-        t.row0 = i % a.row_tiles * NT;
+        t.row0 = i % a.row_tiles * a.nt;
         t.m0 = LOW ? 0 : i / a.row_tiles * AD_M;
-        t.e0 = LOW ? i / a.row_tiles * P : 0;
+        t.e0 = LOW ? (first_tile + (first_of + li * every) * step) * P : 0;
         return t;
     };
-    // Row m .. m + 7 of the tile's sums of row c of x, wherever they belong.
+    // Stages of a tile's adapters that are this CTA's (entries part, part + C, ..): SLABS blocks each.
+    auto blocks_of = [&](int n) { return n > part ? (n - part + C - 1) / C * slabs : 0; };
+    // Sums m .. m + 7 of row c of x: whether anybody wants them, and where they go.
+    auto wanted = [&](const Tile& t, int c, int m) {
+        if (!LOW) return t.m0 + m < a.N;
+        const int e = t.e0 + m / a.R;
+        return m < P * a.R && e < s_count[0] && s_list[e].adapter == s_ids[c];
+    };
     bool bad = false;                            // f16: t beyond its range
     auto store = [&](const Tile& t, int c, int m, float (&y)[8]) {
-        if (LOW) {
-            const int e = t.e0 + m / a.R;
-            if (m < P * a.R && e < s_count[0] && s_list[e].adapter == s_ids[c])
-                bad |= store_low<E>(a, t.row0 + c, m % a.R, s_ids[c], y);
-        } else {
-            store_out<E>(a, t.row0 + c, t.m0 + m, y);
-        }
+        if (LOW) bad |= store_low<E>(a, t.row0 + c, m % a.R, s_list[t.e0 + m / a.R].scale, y);
+        else store_out<E>(a, t.row0 + c, t.m0 + m, y);
     };
 
     if (warp == 0) {
@@ -258,7 +292,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                 for (int kb = kb0; kb < kb1 && slot(s); ++kb, ++g) {
                     uint8_t* p = sm + s * L::STAGE;
                     const int n = LOW ? min(P, s_count[0] - t.e0) : 0;
-                    mbar_expect_tx(&full[s], (LOW ? n * a.R * 128 : L::A_BYTES) + L::X_BYTES);
+                    mbar_expect_tx(&full[s], (LOW ? n * a.R * 128 : L::A_BYTES) + a.nt * 128);
                     if (!LOW) tma_load_2d(p, &tmW, kb * AD_BK, t.m0, &full[s]);
                     for (int e = 0; e < n; ++e)
                         tma_load_3d(p + e * a.R * 128, &tmW, kb * AD_BK, 0, s_list[t.e0 + e].adapter, &full[s]);
@@ -267,13 +301,15 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                 if (LOW || !ok) continue;
                 const int b = li & 1;
                 ok = mbar_wait(&list_full[b], (uint32_t)(li >> 1) & 1u);
-                const int n = s_count[b];
-                for (int e = part; e < n && ok; e += C)
-                    for (int k = 0; k < blocks && slot(s); ++k, ++g) {
-                        mbar_expect_tx(&full[s], L::A_BYTES);
-                        tma_load_3d(sm + s * L::STAGE, &tmB, both ? 0 : (k >> 1) * 64, t.m0, s_list[b * NT + e].adapter, &full[s]);
-                        mbar_arrive(&t_go[s]);
-                    }
+                const int all = ok ? blocks_of(s_count[b]) : 0;
+                for (int f = 0; f < all && slot(s); f += L::SLABS, ++g) {
+                    const int m = min(L::SLABS, all - f);
+                    mbar_expect_tx(&full[s], m * L::SLAB_A);
+                    for (int i = 0; i < m; ++i)
+                        tma_load_3d(sm + s * L::STAGE + i * L::SLAB_A, &tmB, (f + i) % slabs * 16, t.m0,
+                                    s_list[b * NT + part + (f + i) / slabs * C].adapter, &full[s]);
+                    mbar_arrive(&t_go[s]);
+                }
                 if (ok) mbar_arrive(&list_empty[b]);
             }
             if (!ok) sflag[0] = 1;
@@ -282,6 +318,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     } else if (warp == 1) {
         if (lane == 0) {   // ---------------- products
             constexpr uint32_t type = E::bf16 ? idesc_bf16(0, 0) : idesc_f16(0, 0);
+            const uint32_t id_x = type | idesc_f16(AD_M, a.nt);
             int g = 0;
             uint32_t t_phase = 0;                // of t_full, a bit a slot
             bool ok = true;
@@ -298,30 +335,28 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                     const uint32_t w = smem_u32(sm + s * L::STAGE), x = w + L::A_BYTES;
 #pragma unroll
                     for (int k = 0; k < AD_BK / 16; ++k)
-                        umma_bf16(acc, sdesc_sw128(w + k * 32), sdesc_sw128(x + k * 32), type | idesc_f16(AD_M, NT),
-                                  kb > kb0 || k > 0);
+                        umma_bf16(acc, sdesc_sw128(w + k * 32), sdesc_sw128(x + k * 32), id_x, kb > kb0 || k > 0);
                     umma_commit(&empty[s]);
                 }
                 if (!LOW && ok) {
                     ok = mbar_wait(&list_full[b], (uint32_t)(li >> 1) & 1u);
-                    const int n = s_count[b];
-                    for (int e = part; e < n && ok; e += C) {
-                        const AdEntry en = s_list[b * NT + e];
-                        const uint32_t id = type | idesc_f16(AD_M, en.c1 - en.c0);
-                        for (int k = 0; k < blocks; ++k, ++g) {
-                            const int s = g % S;
-                            ok = mbar_wait(&full[s], (uint32_t)(g / S) & 1u) && mbar_wait(&t_full[s], t_phase >> s & 1u);
-                            if (!ok) break;
-                            t_phase ^= 1u << s;
-                            tc_fence_after();
-                            const uint32_t w = smem_u32(sm + s * L::STAGE), t = w + L::A_BYTES + en.c0 * 128;
-                            const int steps = both ? RP / 16 : min(4, RP / 16 - (k >> 1) * 4);
-                            for (int q = 0; q < steps; ++q) {
-                                umma_bf16(acc + en.c0, sdesc_sw128(w + q * 32), sdesc_sw128(t + q * 32), id, 1);
-                                if (both) umma_bf16(acc + en.c0, sdesc_sw128(w + q * 32), sdesc_sw128(t + 64 + q * 32), id, 1);
-                            }
-                            umma_commit(&empty[s]);
+                    const int all = ok ? blocks_of(s_count[b]) : 0;
+                    for (int f = 0; f < all; f += L::SLABS, ++g) {
+                        const int s = g % S;
+                        ok = mbar_wait(&full[s], (uint32_t)(g / S) & 1u) && mbar_wait(&t_full[s], t_phase >> s & 1u);
+                        if (!ok) break;
+                        t_phase ^= 1u << s;
+                        tc_fence_after();
+                        const uint32_t at = smem_u32(sm + s * L::STAGE);
+                        for (int i = 0; i < min(L::SLABS, all - f); ++i) {
+                            const AdEntry en = s_list[b * NT + part + (f + i) / slabs * C];
+                            const uint32_t id = type | idesc_f16(AD_M, en.c1 - en.c0);
+                            const uint64_t w = sdesc_sw32(at + i * L::SLAB_A);
+                            const uint32_t t = at + L::OFF_T + i * 2 * L::SLAB_T + en.c0 * 32;
+                            umma_bf16(acc + en.c0, w, sdesc_sw32(t), id, 1);
+                            umma_bf16(acc + en.c0, w, sdesc_sw32(t + L::SLAB_T), id, 1);
                         }
+                        umma_commit(&empty[s]);
                     }
                     if (ok) mbar_arrive(&list_empty[b]);
                 }
@@ -339,59 +374,69 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
             for (int li = 0; li < tiles && ok; ++li) {
                 const int b = li & 1;
                 const Tile t = tile_of(li);
-                if (builder == 0) {
-                    ok = li < 2 || mbar_wait(&list_empty[b], ((uint32_t)(li >> 1) & 1u) ^ 1u);
-                    if (ok) {
-                        const int n = list_adapters<NT>(a, t.row0, s_list + b * NT, s_ids + b * NT);
-                        if (lane == 0) {
-                            s_count[b] = n;
-                            mbar_arrive(&list_full[b]);
-                        }
-                    }
-                }
-                ok = ok && mbar_wait(&list_full[b], (uint32_t)(li >> 1) & 1u);
+                // (all of them see the phases: a wait names one by its parity alone)
+                ok = li < 2 || mbar_wait(&list_empty[b], ((uint32_t)(li >> 1) & 1u) ^ 1u);
+                int all_ok;
+                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 2, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                             : "=r"(all_ok)
+                             : "r"((uint32_t)ok), "n"(32 * AD_BUILDERS)
+                             : "memory");
+                ok = all_ok != 0;
                 if (!ok) break;
-                const int n = s_count[b];
+                const int n = list_adapters<NT>(a, t.row0, s_list + b * NT, s_ids + b * NT, s_first);
+                if (builder == 0 && lane == 0) {
+                    s_count[b] = n;
+                    mbar_arrive(&list_full[b]);
+                }
                 const int* ids = s_ids + b * NT;
                 g += kb1 - kb0;
                 if (!waited) {                   // t is the first launch's
                     pdl_wait();
                     waited = true;
                 }
-                for (int e = part; e < n && ok; e += C) {
-                    const AdEntry en = s_list[b * NT + e];
-                    for (int k = 0; k < blocks; ++k, ++g, ++x) {
-                        const int s = g % S;
-                        // (every builder sees every phase: a wait names one by its parity alone)
-                        if (!(ok = mbar_wait(&t_go[s], go_phase >> s & 1u))) break;
-                        go_phase ^= 1u << s;
-                        if (x % AD_BUILDERS != builder) continue;
-                        // 16-byte pieces of a row: both terms, which lie side by side, at 0 and 64, or
-                        // 64 ranks of one term
-                        const int q0 = both ? 0 : (k >> 1) * 8, per = both ? RP / 8 : min(8, RP / 8 - q0);
-                        const int pieces = both ? 2 * per : per;
-                        const uint4* src = reinterpret_cast<const uint4*>(a.t + ((long long)t.row0 * 2 + (both ? 0 : k & 1)) * RP) + q0;
-                        uint8_t* dst = sm + s * L::STAGE + L::A_BYTES;
-                        for (int c = en.c0 + lane; c < en.c1; c += 32) {
-                            const bool mine = ids[c] == en.adapter;
-                            const uint4* p = src + (long long)c * (RP / 4);
-                            uint4 v[8];
+                const int all = blocks_of(n);
+                for (int f = 0; f < all; f += L::SLABS, ++g, ++x) {
+                    const int s = g % S;
+                    if (!(ok = mbar_wait(&t_go[s], go_phase >> s & 1u))) break;
+                    go_phase ^= 1u << s;
+                    if (x % AD_BUILDERS != builder) continue;
+                    // Columns c0 .. of up to 32 rows a block, 16 ranks of both terms of each, or zeros; all
+                    // blocks' rows asked for together: rows in no order have one here and there.
+                    const int m = min(L::SLABS, all - f);
+                    AdEntry en[L::SLABS];
+                    int spans = 0;               // the widest block's
 #pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                v[q] = mine && q < pieces ? __ldcg(p + q) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                const int at = both && q >= per ? 4 + q - per : q;
-                                if (q < pieces) *reinterpret_cast<uint4*>(dst + c * 128 + ((at ^ (c & 7)) << 4)) = v[q];
-                            }
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&t_full[s]);
+                    for (int i = 0; i < L::SLABS; ++i) {
+                        en[i] = s_list[b * NT + part + (f + min(i, m - 1)) / slabs * C];
+                        if (i >= m) en[i].c1 = en[i].c0;
+                        spans = max(spans, en[i].c1 - en[i].c0);
                     }
+                    for (int c0 = 0; c0 < spans; c0 += 32) {
+                        uint4 v[L::SLABS][4];
+#pragma unroll
+                        for (int i = 0; i < L::SLABS; ++i) {
+                            const int c = en[i].c0 + c0 + lane;
+                            const bool mine = c < en[i].c1 && ids[c] == en[i].adapter;
+                            const uint4* p = reinterpret_cast<const uint4*>(a.t + (long long)(t.row0 + c) * 2 * RP + (f + i) % slabs * 32);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) v[i][q] = mine ? __ldcg(p + q) : make_uint4(0u, 0u, 0u, 0u);
+                        }
+#pragma unroll
+                        for (int i = 0; i < L::SLABS; ++i) {
+                            const int c = en[i].c0 + c0 + lane;
+                            uint8_t* dst = sm + s * L::STAGE + L::OFF_T + i * 2 * L::SLAB_T + c * 32;
+                            if (c < en[i].c1)
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    *reinterpret_cast<uint4*>(dst + (q >> 1) * L::SLAB_T + (((q & 1) ^ (c >> 2 & 1)) << 4)) = v[i][q];
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&t_full[s]);
                 }
                 __syncwarp();
-                if (builder != 0 && lane == 0) mbar_arrive(&list_empty[b]);
+                if (lane == 0) mbar_arrive(&list_empty[b]);
             }
             if (!waited) pdl_wait();             // this grid ends after the first one, whatever happens
             if (!ok) sflag[0] = 1;
@@ -414,7 +459,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
             }
             tc_fence_after();
             const uint32_t acc = tmem + (uint32_t)(b * NT) + lane_off;
-            const int rows = min(NT, a.n - t.row0);
+            const int rows = min(a.nt, a.n - t.row0);
             if (C > 1) {                         // the whole tile, joined below
                 float* dst = reinterpret_cast<float*>(sm) + quad * 32 + lane;
                 for (int c = 0; c < rows; c += 16) {
@@ -449,6 +494,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                     if (NT >= AD_SLICE || i < 16) s_out[i * AD_LD + quad * 32 + lane] = __uint_as_float(r[i]);
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 for (int i = tid / 16; i < min(AD_SLICE, rows - c); i += 8) {
+                    if (!wanted(t, c + i, f)) continue;
                     const float4* p = reinterpret_cast<const float4*>(s_out + i * AD_LD + f);
                     const float4 u = p[0], v = p[1];
                     float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
@@ -464,26 +510,35 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
 
     if (C > 1) {   // ---------------- the cluster's sums, a share of the tile for each CTA
         cluster_sync_all();
-        if (tiles > 0) {                         // (the same for all of them)
+        if (tiles > 0) {                         // (the same for all that share it)
             const Tile t = tile_of(0);
-            const int rows = min(NT, a.n - t.row0);
+            const int rows = min(a.nt, a.n - t.row0);
             const uint32_t at = smem_u32(sm);
             const int all = rows * (AD_M / 8), lo = (int)((long long)all * part / C), hi = (int)((long long)all * (part + 1) / C);
             for (int i = lo + (int)threadIdx.x; i < hi; i += AD_THREADS) {
                 const int c = i / (AD_M / 8), f = i % (AD_M / 8) * 8;
+                if (!wanted(t, c, f)) continue;  // (most of the first launch's)
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) y[j] = 0.f;
-                for (int p = 0; p < C; ++p)
+                float4 v[8][2];                  // asked for at once: one after another they took 0.3 us each
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float4 v = ld_cluster4(at + (c * AD_LD + f + 4 * h) * 4, p);
-                        y[4 * h] += v.x;
-                        y[4 * h + 1] += v.y;
-                        y[4 * h + 2] += v.z;
-                        y[4 * h + 3] += v.w;
+                for (int p = 0; p < 8; ++p)
+                    if (p < C) {
+                        v[p][0] = ld_cluster4(at + (c * AD_LD + f) * 4, rank - part + p);
+                        v[p][1] = ld_cluster4(at + (c * AD_LD + f + 4) * 4, rank - part + p);
                     }
-                if (!LOW && a.bias && t.m0 + f < a.N) {
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    if (p < C)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            y[4 * h] += v[p][h].x;
+                            y[4 * h + 1] += v[p][h].y;
+                            y[4 * h + 2] += v[p][h].z;
+                            y[4 * h + 3] += v[p][h].w;
+                        }
+                if (!LOW && a.bias) {
                     float add[8];
                     unpack8w<!E::bf16>(*reinterpret_cast<const uint4*>(a.bias + t.m0 + f), add);
 #pragma unroll
@@ -521,14 +576,11 @@ cudaError_t launch_nt(const CUtensorMap& w, const CUtensorMap& x, const CUtensor
     return launch_k(k, dim3(grid), dim3(AD_THREADS), SMEM, s, w, x, b, a);
 }
 template <class E, bool LOW>
-cudaError_t launch_low(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const AdapterArgs& a, int nt, int grid,
-                       cudaStream_t s) {
-    switch (nt) {
-        case 16: return launch_nt<E, 16, LOW>(w, x, b, a, grid, s);
-        case 32: return launch_nt<E, 32, LOW>(w, x, b, a, grid, s);
-        case 64: return launch_nt<E, 64, LOW>(w, x, b, a, grid, s);
-        case 128: return launch_nt<E, 128, LOW>(w, x, b, a, grid, s);
-    }
+cudaError_t launch_low(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const AdapterArgs& a, int grid, cudaStream_t s) {
+    if (a.nt <= 16) return launch_nt<E, 16, LOW>(w, x, b, a, grid, s);
+    if (a.nt <= 32) return launch_nt<E, 32, LOW>(w, x, b, a, grid, s);
+    if (a.nt <= 64) return launch_nt<E, 64, LOW>(w, x, b, a, grid, s);
+    if (a.nt <= 128) return launch_nt<E, 128, LOW>(w, x, b, a, grid, s);
     if constexpr (!LOW) return launch_nt<E, 256, LOW>(w, x, b, a, grid, s);
     return cudaErrorInvalidValue;
 }
@@ -542,16 +594,18 @@ cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& 
     a.row_tiles = p.low_row_tiles;
     a.col_tiles = 1;
     a.splits = p.low_splits;
-    const cudaError_t e = launch_low<E, true>(ma, mxl, ma, a, p.low_nt, p.low_grid, s);
+    a.nt = p.low_nt;
+    const cudaError_t e = launch_low<E, true>(ma, mxl, ma, a, p.low_grid, s);
     if (e != cudaSuccess) return e;
     a.row_tiles = p.row_tiles;
     a.col_tiles = p.col_tiles;
     a.splits = p.splits;
-    return launch_low<E, false>(mw, mx, mb, a, p.nt, p.grid, s);
+    a.nt = p.nt;
+    return launch_low<E, false>(mw, mx, mb, a, p.grid, s);
 }
 
-// Cycles of a block's products: 4 of M = 128, N = nt, K = 16.
-constexpr int block_cycles(int nt) { return nt == 256 ? 700 : 450; }
+// Cycles of a block's products, 4 of M = 128, N = nt, K = 16: no less than 112 each.
+int block_cycles(int nt) { return max(450, nt * 8 / 3); }
 
 }  // namespace
 
@@ -559,17 +613,18 @@ AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms) {
     AdapterPlan p{};
     const int nk = (K + AD_BK - 1) / AD_BK;
     p.col_tiles = (N + AD_M - 1) / AD_M;
-    // Few rows: one row tile, K split until the SMs are full.  Many rows: the tile and the
-    // split that end first, by rounds of tiles over the SMs.
+    // The tile and the split that end first, by rounds of tiles over the SMs.  Few rows: one row
+    // tile, K split until the SMs are full.  Many rows: any multiple of 16 rows up to 256, so that
+    // 4096 rows of 16 column tiles are 304 tiles of 224 rows, two rounds of 152, not 256 of 256.
     long long best = -1;
-    for (int nt = 16; nt <= 256; nt *= 2) {
+    for (int nt = min(256, (n + 15) & ~15); nt >= 16; nt -= 16) {
         const int rt = (n + nt - 1) / nt;
-        if (nt < 128 && rt > 1) continue;
+        if (rt > 1 && nt < 128) break;
         for (int c = 1; c <= 8 && c <= nk; c *= 2) {
             const long long tiles = (long long)rt * p.col_tiles;
             if (c > 1 && tiles * c > sms) break;
             const long long rounds = (tiles * c + sms - 1) / sms;
-            const long long cost = rounds * ((nk + c - 1) / c) * block_cycles(nt) + (c > 1 ? 3000 : 0) + nt;
+            const long long cost = rounds * ((nk + c - 1) / c) * block_cycles(nt) + rounds * 8 * nt + (c > 1 ? 2000 : 0);
             if (best < 0 || cost < best) {
                 best = cost;
                 p.nt = nt;
@@ -580,17 +635,14 @@ AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms) {
         }
         if (rt == 1) break;
     }
-    p.low_nt = min(p.nt, 128);
+    p.low_nt = min((n + 15) & ~15, 128);
     p.low_row_tiles = (n + p.low_nt - 1) / p.low_nt;
     const int most = (min(n_adapters, p.low_nt) + AD_M / R - 1) / (AD_M / R);   // tiles of a row tile
-    // rows of many requests together hold few adapters a tile: two are reckoned with
-    const int likely = p.low_row_tiles > 1 ? min(most, 2) : most;
     p.low_splits = 1;
-    while (p.low_splits < 8 && (long long)p.low_row_tiles * likely * p.low_splits * 2 <= sms && nk >= 4 * p.low_splits &&
-           (long long)p.low_row_tiles * most * p.low_splits * 2 <= 4 * sms)
-        p.low_splits *= 2;
-    const int wide = p.low_splits > 1 ? most : (int)min((long long)most, (2ll * sms + p.low_row_tiles - 1) / p.low_row_tiles);
-    p.low_grid = p.low_row_tiles * wide * p.low_splits;
+    while (p.low_splits < 8 && nk >= 2 * p.low_splits) p.low_splits *= 2;
+    // clusters of a row tile: how many adapters it has is known on the device
+    const int clusters = max(1, min(most, sms / (p.low_splits * p.low_row_tiles)));
+    p.low_grid = p.low_row_tiles * clusters * p.low_splits;
     return p;
 }
 
@@ -602,10 +654,10 @@ bool adapter_maps(const AdapterArgs& a, const AdapterPlan& p, const void* x, lon
     const uint64_t wd[2] = {K, N}, xd[2] = {K, n}, ad[3] = {K, R, (uint64_t)a.n_adapters}, bd[3] = {R, N, (uint64_t)a.n_adapters};
     const uint64_t ws[1] = {K * 2}, xs[1] = {(uint64_t)ld_x * 2}, as[2] = {K * 2, K * R * 2}, bs[2] = {R * 2, R * N * 2};
     const uint32_t wb[2] = {AD_BK, AD_M}, xb[2] = {AD_BK, (uint32_t)p.nt}, xl[2] = {AD_BK, (uint32_t)p.low_nt};
-    const uint32_t ab[3] = {AD_BK, (uint32_t)a.R, 1}, bb[3] = {64, AD_M, 1};
+    const uint32_t ab[3] = {AD_BK, (uint32_t)a.R, 1}, bb[3] = {16, AD_M, 1};
     return encode_map_bf16(m.w, w, 2, wd, ws, wb) && encode_map_bf16(m.x, x, 2, xd, xs, xb) &&
            encode_map_bf16(m.x_low, x, 2, xd, xs, xl) && encode_map_bf16(m.a, la, 3, ad, as, ab) &&
-           encode_map_bf16(m.b, lb, 3, bd, bs, bb);
+           encode_map_bf16_sw32(m.b, lb, 3, bd, bs, bb);
 }
 
 cudaError_t launch_adapter(const AdapterMaps& m, const AdapterArgs& a, const AdapterPlan& p, bool bf16, cudaStream_t s) {

@@ -261,7 +261,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 static bool encode_map_t(void* out, const void* ptr, CUtensorMapDataType dt, int rank, const uint64_t* dims,
-                         const uint64_t* strides, const uint32_t* box) {
+                         const uint64_t* strides, const uint32_t* box,
+                         CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     auto enc = encode_fn();
     if (!enc || rank < 2 || rank > 5) return false;
     if (reinterpret_cast<uintptr_t>(ptr) & 15) return false;
@@ -278,7 +279,7 @@ static bool encode_map_t(void* out, const void* ptr, CUtensorMapDataType dt, int
     }
     CUresult r = enc(reinterpret_cast<CUtensorMap*>(out), dt,
                      (cuuint32_t)rank, const_cast<void*>(ptr), d, st, bx, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
@@ -286,6 +287,11 @@ static bool encode_map_t(void* out, const void* ptr, CUtensorMapDataType dt, int
 bool encode_map_bf16(void* out, const void* ptr, int rank, const uint64_t* dims,
                      const uint64_t* strides, const uint32_t* box) {
     return encode_map_t(out, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, dims, strides, box);
+}
+
+bool encode_map_bf16_sw32(void* out, const void* ptr, int rank, const uint64_t* dims,
+                          const uint64_t* strides, const uint32_t* box) {
+    return encode_map_t(out, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
 bool make_out_map(void* out, const void* ptr, int rows, int cols, int ld, bool f16) {

@@ -298,6 +298,9 @@ void launch_gemm_persistent(const void* tmA, const void* tmB, int bn, int m_rows
 // are in bytes.  False if the driver rejects it.
 bool encode_map_bf16(void* out, const void* ptr, int rank, const uint64_t* dims,
                      const uint64_t* strides, const uint32_t* box);
+// The same with the 32-byte swizzle (boxes of 16 elements a row).
+bool encode_map_bf16_sw32(void* out, const void* ptr, int rank, const uint64_t* dims,
+                          const uint64_t* strides, const uint32_t* box);
 
 // m_rows: rows of A actually valid (<= p.M); the rest is ignored.
 void launch_gemm(const GemmPlan& p, int m_rows, const GemmEpilogue& e, int* status,
@@ -448,16 +451,16 @@ struct AdapterArgs {
     int n, N, K, R, n_adapters;
     const float* scale;          // [n_adapters] or nullptr (1)
     const uint16_t* bias;        // [N] or nullptr
-    uint16_t* t;                 // [n][2][R rounded up to 16]: s_a A_a x in two terms
+    uint16_t* t;                 // [n][R / 16 rounded up][2][16]: s_a A_a x in two terms
     void* out;                   // [n][ld_out], f32 or x's type
     long long ld_out;
     int out_f32;
     int* status;
     // set by launch_adapter:
-    int row_tiles, col_tiles, splits;
+    int nt, row_tiles, col_tiles, splits;
 };
-// How a call is split: rows of x in a tile, tiles, CTAs that share a tile's K (splits) and
-// the grid, of the second launch and of the first (low_).
+// How a call is split: rows of x in a tile, tiles, CTAs of a cluster (splits: of the second
+// launch they share a tile's K) and the grid, of the second launch and of the first (low_).
 struct AdapterPlan {
     int nt, row_tiles, col_tiles, splits, grid;
     int low_nt, low_row_tiles, low_splits, low_grid;
