@@ -45,9 +45,9 @@ constexpr int AD_LD = AD_M + 4;                  // their distance in shared mem
 template <int NT, bool LOW>
 struct AdSmem {
     static constexpr int A_BYTES = AD_M * 128, X_BYTES = NT * 128, STAGE = A_BYTES + X_BYTES;
-    // a tile of few rows leaves room for the other launch's CTA on the same SM, the first launch's
-    // wide tiles for a second one
-    static constexpr int STAGES = NT == 256 ? 4 : NT == 128 ? (LOW ? 3 : 6) : LOW ? 4 : 5;
+    // as many as fit, since W has to be on its way (five stages of 16 KB of W on 128 SMs, 2 us from
+    // asking to having: 5 TB/s); the first launch's leave room for a second CTA
+    static constexpr int STAGES = LOW ? (NT == 128 ? 3 : 4) : NT == 256 ? 4 : NT == 128 ? 6 : NT == 64 ? 8 : NT == 32 ? 9 : 10;
     // an adapter's block in a stage: 16 ranks of 128 rows of B, and both terms of t's
     static constexpr int SLAB_A = AD_M * 32, SLAB_T = NT * 32, SLABS = STAGE / (SLAB_A + 2 * SLAB_T);
     static constexpr int OFF_T = SLABS * SLAB_A;
@@ -55,9 +55,11 @@ struct AdSmem {
     static constexpr int OFF_OUT = STAGES * STAGE;
     static constexpr int OFF_LIST = OFF_OUT + OUT;           // [2][NT] entries
     static constexpr int OFF_IDS = OFF_LIST + 2 * NT * 16;   // [2][NT]
-    static constexpr int OFF_FIRST = OFF_IDS + 2 * NT * 4;   // a bit for each row
-    static constexpr int OFF_BAR = OFF_FIRST + 32;
-    static constexpr int TOTAL = OFF_BAR + 320 + 1024;       // + alignment slack
+    static constexpr int OFF_RUNS = OFF_IDS + 2 * NT * 4;    // [NT]
+    static constexpr int OFF_WORD = OFF_RUNS + NT * 16;      // a bit for each row
+    static constexpr int OFF_BAR = OFF_WORD + 32;
+    static constexpr int BARS = 32 * STAGES + 96;
+    static constexpr int TOTAL = OFF_BAR + BARS + 1024;      // + alignment slack
     static_assert(TOTAL <= 232448, "shared memory of a CTA");
     static_assert(STAGES * STAGE >= NT * AD_LD * 4, "the cluster's sums");
 };
@@ -75,15 +77,47 @@ __device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3ffffu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)6 << 61;
 }
 
-// The adapters of rows [row0, row0 + NT) of ids, in the order in which they come first, by the
-// AD_BUILDERS warps together; their number.  Each thread compares its rows' ids with all others:
-// NT broadcast reads, where a search for one adapter after another took 0.15 us for each.
+// The adapters of rows [row0, row0 + a.nt) of ids, in the order in which they come first, by the
+// AD_BUILDERS warps together; their number.  Neighbouring rows with one adapter are a run; each
+// thread compares its run with all others.  (A search for one adapter after another took 0.15 us
+// for each, a comparison of 256 rows with one another 8 us.)
+struct alignas(16) AdRun {
+    int adapter;
+    uint16_t c0, c1;                             // its rows
+    float scale;
+};
 template <int NT>
-__device__ __forceinline__ int list_adapters(const AdapterArgs& a, int row0, AdEntry* list, int* s_ids, uint32_t* s_first) {
-    constexpr int T = 32 * AD_BUILDERS, PER = (NT + T - 1) / T;
+__device__ __forceinline__ int list_adapters(const AdapterArgs& a, int row0, AdEntry* list, int* s_ids, AdRun* runs, uint32_t* s_word) {
+    constexpr int T = 32 * AD_BUILDERS, PER = (NT + T - 1) / T, WORDS = (NT + 31) / 32;
     const int tid = threadIdx.x - (AD_THREADS - T), lane = tid & 31;
     auto sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(T) : "memory"); };
+    // the place of this thread's k-th element among those whose flag is set, by a ballot a warp
+    auto count = [&](const bool (&flag)[PER], int (&at)[PER]) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const unsigned m = __ballot_sync(FULL_MASK, flag[k]);
+            if (lane == 0 && k * T + tid < NT) s_word[(k * T + tid) / 32] = m;
+        }
+        sync();
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) at[k] = 0;
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) {
+            const uint32_t m = s_word[w];
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int own = (k * T + tid) / 32;
+                at[k] += w < own ? __popc(m) : w == own ? __popc(m & ((1u << lane) - 1u)) : 0;
+            }
+            n += __popc(m);
+        }
+        sync();
+        return n;
+    };
     float scale[PER];
+    bool flag[PER];
+    int at[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int c = k * T + tid, row = row0 + c;
@@ -96,38 +130,45 @@ __device__ __forceinline__ int list_adapters(const AdapterArgs& a, int row0, AdE
         scale[k] = x >= 0 && a.scale ? a.scale[x] : 1.f;
     }
     sync();
-    int last[PER];
-    bool first[PER];
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int c = k * T + tid, x = c < NT ? s_ids[c] : -1;
-        last[k] = c;
-        first[k] = x >= 0;
-        if (x >= 0) {
-#pragma unroll 4
-            for (int j = 0; j < NT; j += 4) {
-                const int4 y = *reinterpret_cast<const int4*>(s_ids + j);
-                if (y.x == x) last[k] = max(last[k], j), first[k] = first[k] && j >= c;
-                if (y.y == x) last[k] = max(last[k], j + 1), first[k] = first[k] && j + 1 >= c;
-                if (y.z == x) last[k] = max(last[k], j + 2), first[k] = first[k] && j + 2 >= c;
-                if (y.w == x) last[k] = max(last[k], j + 3), first[k] = first[k] && j + 3 >= c;
-            }
-        }
-        const unsigned m = __ballot_sync(FULL_MASK, first[k]);
-        if (lane == 0 && c < NT) s_first[c / 32] = m;
-    }
-    sync();
-    int n = 0;
-    constexpr int WORDS = (NT + 31) / 32;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int c = k * T + tid;
-        if (!first[k]) continue;
-        int at = __popc(s_first[c / 32] & ((1u << lane) - 1u));
-        for (int w = 0; w < c / 32; ++w) at += __popc(s_first[w]);
-        list[at] = AdEntry{s_ids[c], (uint16_t)(c & ~15), (uint16_t)((last[k] + 16) & ~15), scale[k]};
+        flag[k] = c < NT && s_ids[c] >= 0 && (c == 0 || s_ids[c - 1] != s_ids[c]);
     }
-    for (int w = 0; w < WORDS; ++w) n += __popc(s_first[w]);
+    const int n_runs = count(flag, at);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int c = k * T + tid;
+        if (c >= NT || s_ids[c] < 0) continue;
+        if (flag[k]) {
+            runs[at[k]].adapter = s_ids[c];
+            runs[at[k]].c0 = (uint16_t)c;
+            runs[at[k]].scale = scale[k];
+        }
+        if (c + 1 == NT || s_ids[c + 1] != s_ids[c]) runs[at[k] + flag[k] - 1].c1 = (uint16_t)(c + 1);
+    }
+    sync();
+    int last[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int r = k * T + tid;
+        flag[k] = r < n_runs;
+        last[k] = 0;
+        if (!flag[k]) continue;
+        const int x = runs[r].adapter;
+        for (int q = 0; q < n_runs; ++q)
+            if (runs[q].adapter == x) {
+                flag[k] = flag[k] && q >= r;
+                last[k] = runs[q].c1;
+            }
+    }
+    const int n = count(flag, at);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (!flag[k]) continue;
+        const AdRun r = runs[k * T + tid];
+        list[at[k]] = AdEntry{r.adapter, (uint16_t)(r.c0 & ~15), (uint16_t)((last[k] + 15) & ~15), r.scale};
+    }
     sync();
     return n;
 }
@@ -180,7 +221,8 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     float* s_out = reinterpret_cast<float*>(sm + L::OFF_OUT);
     AdEntry* s_list = reinterpret_cast<AdEntry*>(sm + L::OFF_LIST);
     int* s_ids = reinterpret_cast<int*>(sm + L::OFF_IDS);
-    uint32_t* s_first = reinterpret_cast<uint32_t*>(sm + L::OFF_FIRST);
+    AdRun* s_runs = reinterpret_cast<AdRun*>(sm + L::OFF_RUNS);
+    uint32_t* s_word = reinterpret_cast<uint32_t*>(sm + L::OFF_WORD);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
     uint64_t* full = bar;                // [S] a stage's copies have landed
     uint64_t* empty = bar + S;           // [S] its products are done
@@ -193,7 +235,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     int* s_count = reinterpret_cast<int*>(list_empty + 2);   // [2] entries of the lists
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_count + 2);
     int* sflag = reinterpret_cast<int*>(tmem_slot + 1);      // [0] failed, [1] stages issued, [2] consumed
-    static_assert((4 * S + 8) * 8 + 6 * 4 <= 320, "barriers");
+    static_assert((4 * S + 8) * 8 + 6 * 4 <= L::BARS, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int CL = a.splits, rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;   // CTAs of a cluster
@@ -230,7 +272,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
         pdl_wait();
         pdl_trigger();
         if (warp >= 6) {                         // the CTA's one row tile
-            const int n = list_adapters<NT>(a, start % a.row_tiles * a.nt, s_list, s_ids, s_first);
+            const int n = list_adapters<NT>(a, start % a.row_tiles * a.nt, s_list, s_ids, s_runs, s_word);
             if (warp == 6 && lane == 0) s_count[0] = n;
         }
     }
@@ -383,7 +425,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                              : "memory");
                 ok = all_ok != 0;
                 if (!ok) break;
-                const int n = list_adapters<NT>(a, t.row0, s_list + b * NT, s_ids + b * NT, s_first);
+                const int n = list_adapters<NT>(a, t.row0, s_list + b * NT, s_ids + b * NT, s_runs, s_word);
                 if (builder == 0 && lane == 0) {
                     s_count[b] = n;
                     mbar_arrive(&list_full[b]);
@@ -395,6 +437,18 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                     waited = true;
                 }
                 const int all = blocks_of(n);
+                // One tile, and t's rows fit where its output will be staged: they are fetched at
+                // once, and writing a block is a matter of shared memory.
+                const uint4* rows_t = reinterpret_cast<const uint4*>(a.t + (long long)t.row0 * 2 * RP);
+                const int rows = min(a.nt, a.n - t.row0);
+                const bool kept = tiles == 1 && all > 0 && rows * RP * 4 <= L::OUT;
+                if (kept) {
+                    const int tid = threadIdx.x - (AD_THREADS - 32 * AD_BUILDERS);
+                    for (int i = tid; i < rows * (RP / 4); i += 32 * AD_BUILDERS)
+                        reinterpret_cast<uint4*>(s_out)[i] = __ldcg(rows_t + i);
+                    asm volatile("bar.sync 2, %0;" ::"n"(32 * AD_BUILDERS) : "memory");
+                    rows_t = reinterpret_cast<const uint4*>(s_out);
+                }
                 for (int f = 0; f < all; f += L::SLABS, ++g, ++x) {
                     const int s = g % S;
                     if (!(ok = mbar_wait(&t_go[s], go_phase >> s & 1u))) break;
@@ -417,9 +471,12 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                         for (int i = 0; i < L::SLABS; ++i) {
                             const int c = en[i].c0 + c0 + lane;
                             const bool mine = c < en[i].c1 && ids[c] == en[i].adapter;
-                            const uint4* p = reinterpret_cast<const uint4*>(a.t + (long long)(t.row0 + c) * 2 * RP + (f + i) % slabs * 32);
+                            const uint4* p = rows_t + (long long)c * (RP / 4) + (f + i) % slabs * 4;
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) v[i][q] = mine ? __ldcg(p + q) : make_uint4(0u, 0u, 0u, 0u);
+                            for (int q = 0; q < 4; ++q) {
+                                v[i][q] = make_uint4(0u, 0u, 0u, 0u);
+                                if (mine) v[i][q] = kept ? p[q] : __ldcg(p + q);
+                            }
                         }
 #pragma unroll
                         for (int i = 0; i < L::SLABS; ++i) {
@@ -640,7 +697,9 @@ AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms) {
     const int most = (min(n_adapters, p.low_nt) + AD_M / R - 1) / (AD_M / R);   // tiles of a row tile
     p.low_splits = 1;
     while (p.low_splits < 8 && nk >= 2 * p.low_splits) p.low_splits *= 2;
-    // clusters of a row tile: how many adapters it has is known on the device
+    // Clusters of a row tile: how many adapters it has is known on the device.  Few rows: no more
+    // CTAs than the second launch leaves SMs, which then starts at once.
+    while (p.low_splits > 2 && p.low_row_tiles * most * p.low_splits > sms - p.grid && p.low_row_tiles * most * 2 <= sms - p.grid) p.low_splits /= 2;
     const int clusters = max(1, min(most, sms / (p.low_splits * p.low_row_tiles)));
     p.low_grid = p.low_row_tiles * clusters * p.low_splits;
     return p;
