@@ -173,6 +173,20 @@ __device__ __forceinline__ int list_adapters(const AdapterArgs& a, int row0, AdE
     return n;
 }
 
+// The blocks of a CTA's entries one after another: 16 ranks of an entry, then the next 16, then
+// the entry `step` further on.  (Divisions took the thread that issues products longer than they.)
+struct Block {
+    const AdEntry* entry;
+    int slab, slabs, step;
+    __device__ __forceinline__ Block(const AdEntry* e, int n, int by) : entry(e), slab(0), slabs(n), step(by) {}
+    __device__ __forceinline__ void next() {
+        if (++slab == slabs) {
+            slab = 0;
+            entry += step;
+        }
+    }
+};
+
 // Eight sums of a row of x.  First launch: ranks r .. r + 7 of its adapter, as two terms (and
 // zeros for the ranks that fill up a product); second: outputs m .. m + 7.  True: beyond f16.
 template <class E>
@@ -344,12 +358,12 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                 const int b = li & 1;
                 ok = mbar_wait(&list_full[b], (uint32_t)(li >> 1) & 1u);
                 const int all = ok ? blocks_of(s_count[b]) : 0;
+                Block at(s_list + b * NT + part, slabs, C);
                 for (int f = 0; f < all && slot(s); f += L::SLABS, ++g) {
                     const int m = min(L::SLABS, all - f);
                     mbar_expect_tx(&full[s], m * L::SLAB_A);
-                    for (int i = 0; i < m; ++i)
-                        tma_load_3d(sm + s * L::STAGE + i * L::SLAB_A, &tmB, (f + i) % slabs * 16, t.m0,
-                                    s_list[b * NT + part + (f + i) / slabs * C].adapter, &full[s]);
+                    for (int i = 0; i < m; ++i, at.next())
+                        tma_load_3d(sm + s * L::STAGE + i * L::SLAB_A, &tmB, at.slab * 16, t.m0, at.entry->adapter, &full[s]);
                     mbar_arrive(&t_go[s]);
                 }
                 if (ok) mbar_arrive(&list_empty[b]);
@@ -383,20 +397,21 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                 if (!LOW && ok) {
                     ok = mbar_wait(&list_full[b], (uint32_t)(li >> 1) & 1u);
                     const int all = ok ? blocks_of(s_count[b]) : 0;
+                    Block next(s_list + b * NT + part, slabs, C);
                     for (int f = 0; f < all; f += L::SLABS, ++g) {
                         const int s = g % S;
                         ok = mbar_wait(&full[s], (uint32_t)(g / S) & 1u) && mbar_wait(&t_full[s], t_phase >> s & 1u);
                         if (!ok) break;
                         t_phase ^= 1u << s;
                         tc_fence_after();
-                        const uint32_t at = smem_u32(sm + s * L::STAGE);
-                        for (int i = 0; i < min(L::SLABS, all - f); ++i) {
-                            const AdEntry en = s_list[b * NT + part + (f + i) / slabs * C];
-                            const uint32_t id = type | idesc_f16(AD_M, en.c1 - en.c0);
-                            const uint64_t w = sdesc_sw32(at + i * L::SLAB_A);
-                            const uint32_t t = at + L::OFF_T + i * 2 * L::SLAB_T + en.c0 * 32;
-                            umma_bf16(acc + en.c0, w, sdesc_sw32(t), id, 1);
-                            umma_bf16(acc + en.c0, w, sdesc_sw32(t + L::SLAB_T), id, 1);
+                        const uint64_t w = sdesc_sw32(smem_u32(sm + s * L::STAGE)), u = sdesc_sw32(smem_u32(sm + s * L::STAGE + L::OFF_T));
+#pragma unroll 1
+                        for (int i = 0; i < min(L::SLABS, all - f); ++i, next.next()) {
+                            const int c0 = next.entry->c0;
+                            const uint32_t id = type | idesc_f16(AD_M, next.entry->c1 - c0);
+                            const uint64_t t = u + (i * 2 * L::SLAB_T >> 4) + c0 * 2;   // (rows of 32 bytes)
+                            umma_bf16(acc + c0, w + (i * L::SLAB_A >> 4), t, id, 1);
+                            umma_bf16(acc + c0, w + (i * L::SLAB_A >> 4), t + (L::SLAB_T >> 4), id, 1);
                         }
                         umma_commit(&empty[s]);
                     }
@@ -438,8 +453,10 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                 }
                 const int all = blocks_of(n);
                 // One tile, and t's rows fit where its output will be staged: they are fetched at
-                // once, and writing a block is a matter of shared memory.
+                // once, and writing a block is a matter of shared memory.  (The two places have a
+                // pointer each: a load that is of one space by name must never see the other's address.)
                 const uint4* rows_t = reinterpret_cast<const uint4*>(a.t + (long long)t.row0 * 2 * RP);
+                const uint4* kept_t = reinterpret_cast<const uint4*>(s_out);
                 const int rows = min(a.nt, a.n - t.row0);
                 const bool kept = tiles == 1 && all > 0 && rows * RP * 4 <= L::OUT;
                 if (kept) {
@@ -447,42 +464,54 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                     for (int i = tid; i < rows * (RP / 4); i += 32 * AD_BUILDERS)
                         reinterpret_cast<uint4*>(s_out)[i] = __ldcg(rows_t + i);
                     asm volatile("bar.sync 2, %0;" ::"n"(32 * AD_BUILDERS) : "memory");
-                    rows_t = reinterpret_cast<const uint4*>(s_out);
                 }
+                Block next(s_list + b * NT + part, slabs, C);
                 for (int f = 0; f < all; f += L::SLABS, ++g, ++x) {
-                    const int s = g % S;
-                    if (!(ok = mbar_wait(&t_go[s], go_phase >> s & 1u))) break;
-                    go_phase ^= 1u << s;
-                    if (x % AD_BUILDERS != builder) continue;
+                    const int s = g % S, m = min(L::SLABS, all - f);
+                    const bool mine = x % AD_BUILDERS == builder;
                     // Columns c0 .. of up to 32 rows a block, 16 ranks of both terms of each, or zeros; all
-                    // blocks' rows asked for together: rows in no order have one here and there.
-                    const int m = min(L::SLABS, all - f);
-                    AdEntry en[L::SLABS];
-                    int spans = 0;               // the widest block's
+                    // blocks' rows asked for together (rows in no order have one here and there), the
+                    // first ones before their stage is free.
+                    const AdEntry* en[L::SLABS];
+                    int slab[L::SLABS], wide = 0;
+                    uint4 v[L::SLABS][4];
 #pragma unroll
                     for (int i = 0; i < L::SLABS; ++i) {
-                        en[i] = s_list[b * NT + part + (f + min(i, m - 1)) / slabs * C];
-                        if (i >= m) en[i].c1 = en[i].c0;
-                        spans = max(spans, en[i].c1 - en[i].c0);
-                    }
-                    for (int c0 = 0; c0 < spans; c0 += 32) {
-                        uint4 v[L::SLABS][4];
-#pragma unroll
-                        for (int i = 0; i < L::SLABS; ++i) {
-                            const int c = en[i].c0 + c0 + lane;
-                            const bool mine = c < en[i].c1 && ids[c] == en[i].adapter;
-                            const uint4* p = rows_t + (long long)c * (RP / 4) + (f + i) % slabs * 4;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                v[i][q] = make_uint4(0u, 0u, 0u, 0u);
-                                if (mine) v[i][q] = kept ? p[q] : __ldcg(p + q);
-                            }
+                        en[i] = next.entry;
+                        slab[i] = next.slab;
+                        if (i < m) {
+                            wide = max(wide, en[i]->c1 - en[i]->c0);
+                            next.next();
                         }
+                    }
+                    auto ask = [&](int c0) {
 #pragma unroll
                         for (int i = 0; i < L::SLABS; ++i) {
-                            const int c = en[i].c0 + c0 + lane;
+                            const int c = i < m ? en[i]->c0 + c0 + lane : NT;
+                            const bool own = i < m && c < en[i]->c1 && ids[c] == en[i]->adapter;
+                            const int p = c * (RP / 4) + slab[i] * 4;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) v[i][q] = make_uint4(0u, 0u, 0u, 0u);
+                            if (own && kept)
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) v[i][q] = kept_t[p + q];
+                            if (own && !kept)
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) v[i][q] = __ldcg(rows_t + p + q);
+                        }
+                    };
+                    if (mine) ask(0);
+                    if (!(ok = mbar_wait(&t_go[s], go_phase >> s & 1u))) break;
+                    go_phase ^= 1u << s;
+                    if (!mine) continue;
+                    for (int c0 = 0; c0 < wide; c0 += 32) {
+                        if (c0 > 0) ask(c0);
+#pragma unroll
+                        for (int i = 0; i < L::SLABS; ++i) {
+                            if (i >= m) continue;
+                            const int c = en[i]->c0 + c0 + lane;
                             uint8_t* dst = sm + s * L::STAGE + L::OFF_T + i * 2 * L::SLAB_T + c * 32;
-                            if (c < en[i].c1)
+                            if (c < en[i]->c1)
 #pragma unroll
                                 for (int q = 0; q < 4; ++q)
                                     *reinterpret_cast<uint4*>(dst + (q >> 1) * L::SLAB_T + (((q & 1) ^ (c >> 2 & 1)) << 4)) = v[i][q];
@@ -622,6 +651,61 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     }
 }
 
+// The first launch for few rows: a CTA for eight ranks of a row, its warps for a part of K each.
+// No list of adapters, no tensor memory, no cluster: one row on rank 8 has t 2 us sooner, and what
+// it costs beyond that (A is read for each row that names it, from L2) few rows do not notice.
+constexpr int AR_WARPS = 4, AR_RANKS = 8;
+template <class E>
+__global__ void __launch_bounds__(AR_WARPS * 32) k_adapter_rows(AdapterArgs a, const uint16_t* x, long long ld_x, const uint16_t* la) {
+    __shared__ float s_sum[AR_WARPS][AR_RANKS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = blockIdx.x * AR_RANKS, row = blockIdx.y;
+    pdl_wait();
+    pdl_trigger();
+    const int id = a.ids[row];
+    if (id >= a.n_adapters && threadIdx.x == 0) raise_status(a.status, EMBER_ERR_INVALID_ARG);
+    if (id < 0 || id >= a.n_adapters) return;
+    const float scale = a.scale ? a.scale[id] : 1.f;
+    const uint4* xp = reinterpret_cast<const uint4*>(x + row * ld_x);
+    const uint4* ap = reinterpret_cast<const uint4*>(la + ((long long)id * a.R + r) * a.K);
+    float sum[AR_RANKS];
+#pragma unroll
+    for (int k = 0; k < AR_RANKS; ++k) sum[k] = 0.f;
+    const int pieces = a.K / 8;
+#pragma unroll 2
+    for (int i = warp * 32 + lane; i < pieces; i += AR_WARPS * 32) {
+        uint4 w[AR_RANKS];
+        const uint4 v = xp[i];
+#pragma unroll
+        for (int k = 0; k < AR_RANKS; ++k) w[k] = __ldg(ap + (long long)k * pieces + i);
+        float u[8];
+        unpack8w<!E::bf16>(v, u);
+#pragma unroll
+        for (int k = 0; k < AR_RANKS; ++k) {
+            float y[8];
+            unpack8w<!E::bf16>(w[k], y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[k] = fmaf(u[j], y[j], sum[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < AR_RANKS; ++k) sum[k] = warp_sum(sum[k]);
+    if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < AR_RANKS; ++k) s_sum[warp][k] = sum[k];
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float y[AR_RANKS];
+#pragma unroll
+        for (int k = 0; k < AR_RANKS; ++k) {
+            y[k] = 0.f;
+#pragma unroll
+            for (int w = 0; w < AR_WARPS; ++w) y[k] += s_sum[w][k];
+        }
+        if (store_low<E>(a, row, r, scale, y)) raise_status(a.status, EMBER_ERR_RANGE);
+    }
+}
+
 template <class E, int NT, bool LOW>
 cudaError_t launch_nt(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const AdapterArgs& a, int grid,
                       cudaStream_t s) {
@@ -642,7 +726,7 @@ cudaError_t launch_low(const CUtensorMap& w, const CUtensorMap& x, const CUtenso
     return cudaErrorInvalidValue;
 }
 template <class E>
-cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& p, cudaStream_t s) {
+cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& p, const AdapterRows& r, cudaStream_t s) {
     const auto& mw = *reinterpret_cast<const CUtensorMap*>(m.w);
     const auto& mx = *reinterpret_cast<const CUtensorMap*>(m.x);
     const auto& ma = *reinterpret_cast<const CUtensorMap*>(m.a);
@@ -652,7 +736,8 @@ cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& 
     a.col_tiles = 1;
     a.splits = p.low_splits;
     a.nt = p.low_nt;
-    const cudaError_t e = launch_low<E, true>(ma, mxl, ma, a, p.low_grid, s);
+    const cudaError_t e = p.low_grid ? launch_low<E, true>(ma, mxl, ma, a, p.low_grid, s)
+                                     : launch_k(k_adapter_rows<E>, dim3(a.R / AR_RANKS, a.n), dim3(AR_WARPS * 32), 0, s, a, r.x, r.ld_x, r.a);
     if (e != cudaSuccess) return e;
     a.row_tiles = p.row_tiles;
     a.col_tiles = p.col_tiles;
@@ -660,6 +745,8 @@ cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& 
     a.nt = p.nt;
     return launch_low<E, false>(mw, mx, mb, a, p.grid, s);
 }
+
+constexpr int AR_MOST = 1 << 23;                 // multiplications of k_adapter_rows at most
 
 // Cycles of a block's products, 4 of M = 128, N = nt, K = 16: no less than 112 each.
 int block_cycles(int nt) { return max(450, nt * 8 / 3); }
@@ -692,6 +779,8 @@ AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms) {
         }
         if (rt == 1) break;
     }
+    // One row at a time while that is little work: 64 rows of rank 16 on 2048 inputs.
+    if (n <= 64 && (double)n * R * K <= (double)AR_MOST) return p;
     p.low_nt = min((n + 15) & ~15, 128);
     p.low_row_tiles = (n + p.low_nt - 1) / p.low_nt;
     const int most = (min(n_adapters, p.low_nt) + AD_M / R - 1) / (AD_M / R);   // tiles of a row tile
@@ -707,20 +796,20 @@ AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms) {
 
 size_t adapter_ws(int n, int R) { return (size_t)n * 2 * ((R + 15) & ~15) * sizeof(uint16_t); }
 
-bool adapter_maps(const AdapterArgs& a, const AdapterPlan& p, const void* x, long long ld_x, const void* w, const void* la,
-                  const void* lb, AdapterMaps& m) {
+bool adapter_maps(const AdapterArgs& a, const AdapterPlan& p, const AdapterRows& r, AdapterMaps& m) {
     const uint64_t K = a.K, N = a.N, R = a.R, n = a.n;
     const uint64_t wd[2] = {K, N}, xd[2] = {K, n}, ad[3] = {K, R, (uint64_t)a.n_adapters}, bd[3] = {R, N, (uint64_t)a.n_adapters};
-    const uint64_t ws[1] = {K * 2}, xs[1] = {(uint64_t)ld_x * 2}, as[2] = {K * 2, K * R * 2}, bs[2] = {R * 2, R * N * 2};
+    const uint64_t ws[1] = {K * 2}, xs[1] = {(uint64_t)r.ld_x * 2}, as[2] = {K * 2, K * R * 2}, bs[2] = {R * 2, R * N * 2};
     const uint32_t wb[2] = {AD_BK, AD_M}, xb[2] = {AD_BK, (uint32_t)p.nt}, xl[2] = {AD_BK, (uint32_t)p.low_nt};
     const uint32_t ab[3] = {AD_BK, (uint32_t)a.R, 1}, bb[3] = {16, AD_M, 1};
-    return encode_map_bf16(m.w, w, 2, wd, ws, wb) && encode_map_bf16(m.x, x, 2, xd, xs, xb) &&
-           encode_map_bf16(m.x_low, x, 2, xd, xs, xl) && encode_map_bf16(m.a, la, 3, ad, as, ab) &&
-           encode_map_bf16_sw32(m.b, lb, 3, bd, bs, bb);
+    return encode_map_bf16(m.w, r.w, 2, wd, ws, wb) && encode_map_bf16(m.x, r.x, 2, xd, xs, xb) &&
+           encode_map_bf16_sw32(m.b, r.b, 3, bd, bs, bb) &&
+           (!p.low_grid || (encode_map_bf16(m.x_low, r.x, 2, xd, xs, xl) && encode_map_bf16(m.a, r.a, 3, ad, as, ab)));
 }
 
-cudaError_t launch_adapter(const AdapterMaps& m, const AdapterArgs& a, const AdapterPlan& p, bool bf16, cudaStream_t s) {
-    return bf16 ? launch_type<ElemBf16>(m, a, p, s) : launch_type<ElemF16>(m, a, p, s);
+cudaError_t launch_adapter(const AdapterMaps& m, const AdapterArgs& a, const AdapterPlan& p, const AdapterRows& r, bool bf16,
+                           cudaStream_t s) {
+    return bf16 ? launch_type<ElemBf16>(m, a, p, r, s) : launch_type<ElemF16>(m, a, p, r, s);
 }
 
 }  // namespace ember

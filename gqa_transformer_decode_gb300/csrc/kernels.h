@@ -460,7 +460,8 @@ struct AdapterArgs {
     int nt, row_tiles, col_tiles, splits;
 };
 // How a call is split: rows of x in a tile, tiles, CTAs of a cluster (splits: of the second
-// launch they share a tile's K) and the grid, of the second launch and of the first (low_).
+// launch they share a tile's K) and the grid, of the second launch and of the first (low_;
+// low_grid 0: row by row).
 struct AdapterPlan {
     int nt, row_tiles, col_tiles, splits, grid;
     int low_nt, low_row_tiles, low_splits, low_grid;
@@ -468,11 +469,15 @@ struct AdapterPlan {
 struct AdapterMaps {
     alignas(64) unsigned char w[128], x[128], x_low[128], a[128], b[128];
 };
+struct AdapterRows {
+    const uint16_t *x, *w, *a, *b;   // [n][ld_x], [N][K], [n_adapters][R][K], [n_adapters][N][R]
+    long long ld_x;
+};
 AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms);
 size_t adapter_ws(int n, int R);
-bool adapter_maps(const AdapterArgs& a, const AdapterPlan& p, const void* x, long long ld_x, const void* w, const void* la,
-                  const void* lb, AdapterMaps& m);
-cudaError_t launch_adapter(const AdapterMaps& m, const AdapterArgs& a, const AdapterPlan& p, bool bf16, cudaStream_t s);
+bool adapter_maps(const AdapterArgs& a, const AdapterPlan& p, const AdapterRows& r, AdapterMaps& m);
+cudaError_t launch_adapter(const AdapterMaps& m, const AdapterArgs& a, const AdapterPlan& p, const AdapterRows& r, bool bf16,
+                           cudaStream_t s);
 
 // ------------------------------------------------------- log probabilities --
 // Per row of logits [n][ldl] (V used) at temperature t: the given token's log

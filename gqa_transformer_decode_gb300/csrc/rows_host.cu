@@ -97,10 +97,12 @@ ember_status ember_adapter_project(const ember_adapters* ad, const void* x, int6
     a.out_f32 = out_dtype == EMBER_F32;
     a.status = status;
     const AdapterPlan plan = adapter_plan(n, N, K, a.R, a.n_adapters, sms);
+    const AdapterRows rows{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), static_cast<const uint16_t*>(ad->a),
+                           static_cast<const uint16_t*>(ad->b), ld_x};
     AdapterMaps maps;
-    if (!adapter_maps(a, plan, x, ld_x, w, ad->a, ad->b, maps))
+    if (!adapter_maps(a, plan, rows, maps))
         PG_FAIL(EMBER_ERR_UNSUPPORTED, "the driver takes no tensor map of these sizes and strides");
-    e = launch_adapter(maps, a, plan, dtype == EMBER_BF16, (cudaStream_t)stream);
+    e = launch_adapter(maps, a, plan, rows, dtype == EMBER_BF16, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_failed("adapter launch failed", e);
     return EMBER_OK;
 }
