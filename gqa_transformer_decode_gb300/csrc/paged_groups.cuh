@@ -1,0 +1,80 @@
+// paged_groups.cuh -- the line of key tiles of shared prefixes, as the prefixes' kernel
+// (paged_prefill_tc.cu, PT_SHARED) and the rows' own (paged_shared.cu) see it, and which SMs
+// take which.
+#pragma once
+
+#include "paged.cuh"
+
+namespace ember {
+
+namespace {
+
+constexpr int PT_KEYS = 64;    // keys of a tile
+constexpr int PT_SHARE = 4;    // key tiles of a CTA at least
+
+// Groups cu[g] .. cu[g + 1] - 1 of n rows that read keys[g] keys of table row seqs[g].
+struct PtGroups {
+    const int32_t *cu, *keys, *seqs, *lens;
+    int n_groups, n, n_seqs, NKV, rows_per_pair;
+    long long most;            // keys that the table has room for
+};
+// The rows of a group in pairs of tiles and its key tiles; none if it is invalid (the rows' own
+// kernel reports that) or has no prefix.
+struct PtGroup {
+    int row0, nq, keys, seq, nx, tiles;
+};
+__device__ __forceinline__ PtGroup pt_group(const PtGroups& a, int g) {
+    PtGroup r{0, 0, 0, 0, 0, 0};
+    if (g >= a.n_groups) return r;
+    const int r0 = a.cu[g], r1 = a.cu[g + 1], keys = a.keys[g], seq = a.seqs[g];
+    if (seq < 0 || seq >= a.n_seqs || r0 < 0 || r1 <= r0 || r1 > a.n || keys <= 0 || keys > a.most) return r;
+    r.row0 = r0;
+    r.nq = r1 - r0;
+    r.keys = keys;
+    r.seq = seq;
+    r.nx = (r.nq + a.rows_per_pair - 1) / a.rows_per_pair;
+    r.tiles = (keys + PT_KEYS - 1) / PT_KEYS;
+    return r;
+}
+// Where 32 groups' pairs and key tiles begin, each lane its own group's, after those of `pairs` and `line`
+// before; both are moved on.
+__device__ __forceinline__ PtGroup pt_scan(const PtGroups& a, int g0, unsigned& pairs, unsigned& line, unsigned& pair0,
+                                           unsigned& line0) {
+    const int lane = threadIdx.x & 31;
+    const PtGroup r = pt_group(a, g0 + lane);
+    const unsigned np = (unsigned)r.nx * a.NKV, nl = np * (unsigned)r.tiles;
+    pair0 = np;
+    line0 = nl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(FULL_MASK, pair0, o), y = __shfl_up_sync(FULL_MASK, line0, o);
+        if (lane >= o) {
+            pair0 += x;
+            line0 += y;
+        }
+    }
+    const unsigned all_p = __shfl_sync(FULL_MASK, pair0, 31), all_l = __shfl_sync(FULL_MASK, line0, 31);
+    pair0 += pairs - np;
+    line0 += line - nl;
+    pairs += all_p;
+    line += all_l;
+    return r;
+}
+
+// SMs for the prefixes' products; the others are for the rows' own keys, which then run beside
+// them.  That pays while both are short and made of latencies: 64 rows on 8192 keys and up to 512
+// of their own 20.5 us, one kernel after the other 23.  With more than PT_APART tiles an SM they
+// only contend for memory (128 rows on 32768 keys: 98 us beside each other, 90 after each other).
+// In proportion to what each would take one SM: a key tile of a pair 1350 cycles, a pair four
+// tiles more, and a CTA's SM reads 40 bytes a cycle when not all SMs do.
+constexpr unsigned PT_APART = 12;
+__device__ __forceinline__ int prefix_sms(unsigned tiles, unsigned pairs, float tail_bytes, int sms) {
+    if (tiles == 0) return 0;
+    if (!(tail_bytes > 0.f) || tiles > PT_APART * sms) return sms;
+    const float w1 = (tiles + 4.f * pairs) * 1350.f, w2 = tail_bytes * (1.f / 40.f);
+    return min(sms - 1, max(1, (int)(sms * (w1 / (w1 + w2)) + 0.5f)));
+}
+
+}  // namespace
+
+}  // namespace ember

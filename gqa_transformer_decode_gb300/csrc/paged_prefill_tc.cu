@@ -72,7 +72,7 @@
 // raises EMBER_ERR_TIMEOUT, the CTA drains its copies and frees TMEM.
 #include <cudaTypedefs.h>
 
-#include "paged.cuh"
+#include "paged_groups.cuh"
 #include "tc_common.cuh"
 
 namespace ember {
@@ -83,9 +83,7 @@ constexpr int PT_THREADS = 384;
 constexpr int PT_TMA = 8, PT_MMA = 9, PT_EDGE = 11;   // warps (PT_MMA and the one after it: tiles A and B)
 constexpr int PT_REGS_ROW = 200, PT_REGS_REST = 104;   // 256 * 200 + 128 * 104 = 384 * 168, the launch's share
 constexpr int PT_ROWS = 128;   // rows of a query tile
-constexpr int PT_KEYS = 64;    // keys of a tile
 constexpr int PT_PARTS = 8;    // CTAs of a cluster at most
-constexpr int PT_SHARE = 4;    // PT_SHARED: key tiles of a CTA at least
 // A pair's keys: by one CTA, or shared out over a cluster, or over the line.
 enum PtForm : int { PT_WHOLE = 0, PT_SPLIT = 1, PT_SHARED = 2 };
 
@@ -240,81 +238,46 @@ __device__ __forceinline__ PtPair pt_pair(const PagedPrefillArgs& a, int QT, uns
 }
 
 // ---- PT_SHARED ----
-// The rows of group g in pairs of tiles and its key tiles; none if it is invalid (paged_decode.cu
-// reports that) or has no prefix.
-struct PtGroup {
-    int row0, nq, keys, seq, nx, tiles;
-};
-__device__ __forceinline__ PtGroup pt_group(const PagedPrefillArgs& a, int g, int QT) {
-    PtGroup r{0, 0, 0, 0, 0, 0};
-    if (g >= a.B) return r;
-    const int r0 = a.cu[g], r1 = a.cu[g + 1], keys = a.shared[g], seq = a.seqs[g];
-    if (seq < 0 || seq >= a.c.n_seqs || r0 < 0 || r1 <= r0 || r1 > a.n || keys <= 0 ||
-        keys > ((long long)a.c.width << a.c.page_shift))
-        return r;
-    r.row0 = r0;
-    r.nq = r1 - r0;
-    r.keys = keys;
-    r.seq = seq;
-    r.nx = (r.nq + 2 * QT - 1) / (2 * QT);
-    r.tiles = (keys + PT_KEYS - 1) / PT_KEYS;
-    return r;
-}
-// Where 32 groups' pairs and key tiles begin, each lane its own group's, after those of `pairs` and `line`
-// before; both are moved on.
-__device__ __forceinline__ PtGroup pt_scan(const PagedPrefillArgs& a, int g0, int QT, unsigned& pairs, unsigned& line,
-                                           unsigned& pair0, unsigned& line0) {
-    const int lane = threadIdx.x & 31;
-    const PtGroup r = pt_group(a, g0 + lane, QT);
-    const unsigned np = (unsigned)r.nx * a.c.NKV, nl = np * (unsigned)r.tiles;
-    pair0 = np;
-    line0 = nl;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned x = __shfl_up_sync(FULL_MASK, pair0, o), y = __shfl_up_sync(FULL_MASK, line0, o);
-        if (lane >= o) {
-            pair0 += x;
-            line0 += y;
-        }
-    }
-    const unsigned all_p = __shfl_sync(FULL_MASK, pair0, 31), all_l = __shfl_sync(FULL_MASK, line0, 31);
-    pair0 += pairs - np;
-    line0 += line - nl;
-    pairs += all_p;
-    line += all_l;
-    return r;
+__device__ __forceinline__ PtGroups pt_groups(const PagedPrefillArgs& a, int QT) {
+    return PtGroups{a.cu, a.shared, a.seqs, a.lens, a.B, a.n, a.c.n_seqs, a.c.NKV, 2 * QT, (long long)a.c.width << a.c.page_shift};
 }
 // The line's length and a CTA's share of it; one warp of the grid leaves what the join needs
 // to find a pair's partials: the share, then each group's first pair and place in the line.
-__device__ __forceinline__ void pt_line(const PagedPrefillArgs& a, int QT, bool leave, unsigned& each, unsigned& lo, unsigned& hi) {
+__device__ __forceinline__ void pt_line(const PagedPrefillArgs& a, const PtGroups& gs, bool leave, unsigned& each, unsigned& lo, unsigned& hi) {
+    const int lane = threadIdx.x & 31;
     unsigned pairs = 0, line = 0;
     int2* head = reinterpret_cast<int2*>(a.ws);
+    float own = 0.f;           // the rows' own keys, about
+    for (int b = lane; b < a.n; b += 32) own += max(0, a.lens[b]);
     for (int g0 = 0; g0 < a.B; g0 += 32) {
         unsigned pair0, line0;
-        (void)pt_scan(a, g0, QT, pairs, line, pair0, line0);
-        const int g = g0 + (threadIdx.x & 31);
+        const PtGroup r = pt_scan(gs, g0, pairs, line, pair0, line0);
+        own -= (float)r.nq * r.keys;
+        const int g = g0 + lane;
         if (leave && g < a.B) head[1 + g] = make_int2((int)pair0, (int)line0);
     }
-    each = max((unsigned)PT_SHARE, (line + gridDim.x - 1) / gridDim.x);
-    if (leave && (threadIdx.x & 31) == 0) head[0] = make_int2((int)each, (int)line);
+    own = fmaxf(0.f, warp_sum(own));
+    const int sms = prefix_sms(line, pairs, own * a.c.NKV * a.c.D * 4.f, gridDim.x);
+    each = max((unsigned)PT_SHARE, (line + sms - 1) / max(1, sms));
+    if (leave && lane == 0) head[0] = make_int2((int)each, (int)line);
     lo = min(line, blockIdx.x * each);
     hi = min(line, lo + each);
 }
 // The pair at place `at` of the line and the key tiles that the CTA has of it from there on.
-__device__ __forceinline__ PtPair pt_shared(const PagedPrefillArgs& a, int QT, unsigned at, unsigned hi) {
+__device__ __forceinline__ PtPair pt_shared(const PtGroups& a, int QT, unsigned at, unsigned hi) {
     PtPair p;
     p.nkt = -1;
     p.tokens = 0;
     if (at >= hi) return p;
     unsigned pairs = 0, line = 0;
-    for (int g0 = 0; g0 < a.B; g0 += 32) {
+    for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
         unsigned pair0, line0;
-        const PtGroup mine = pt_scan(a, g0, QT, pairs, line, pair0, line0);
+        const PtGroup mine = pt_scan(a, g0, pairs, line, pair0, line0);
         const unsigned hit =
-            __ballot_sync(FULL_MASK, at >= line0 && at - line0 < (unsigned)mine.nx * a.c.NKV * (unsigned)mine.tiles);
+            __ballot_sync(FULL_MASK, at >= line0 && at - line0 < (unsigned)mine.nx * a.NKV * (unsigned)mine.tiles);
         if (!hit) continue;
         const int src = __ffs(hit) - 1;
-        const PtGroup r = pt_group(a, g0 + src, QT);
+        const PtGroup r = pt_group(a, g0 + src);
         const unsigned off = at - __shfl_sync(FULL_MASK, line0, src);
         // a kv head's pairs side by side: they read the same keys at about the same time
         const int pi = (int)(off / (unsigned)r.tiles), x = pi % r.nx;
@@ -421,7 +384,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     if (SHARED) {   // (then these are the CTA's share of the line)
         pdl_trigger();   // the rows' own keys do not need this grid's results
         unsigned each;
-        pt_line(a, QT, blockIdx.x == 0 && warp == 0, each, first_pair, pairs_all);
+        pt_line(a, pt_groups(a, QT), blockIdx.x == 0 && warp == 0, each, first_pair, pairs_all);
     }
     tc_fence_before();
     __syncthreads();
@@ -458,7 +421,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     };
 
     auto pair_at = [&](unsigned cta, bool reporter) {
-        if constexpr (SHARED) return pt_shared(a, QT, cta, pairs_all);
+        if constexpr (SHARED) return pt_shared(pt_groups(a, QT), QT, cta, pairs_all);
         else return pt_pair(a, QT, cta, pairs_all, part, parts, reporter);
     };
 

@@ -9,8 +9,9 @@
 //                    for each query head, against 4 D bytes a key and kv head)
 //   k_shared_tail    the rows' own keys, as in paged_decode.cu, bound by their bytes
 //   k_shared_join    the two
-// The second needs nothing of the first and fills the SMs as that leaves them; it ends after it.
-// The third starts when the second is through.
+// The second needs nothing of the first: it starts as the first one's CTAs leave their SMs, some
+// of them at once in small calls (paged_groups.cuh), and ends after it.  The third starts when the
+// second is through.
 //
 // Tails are short and many (a few hundred keys for each of hundreds of rows and kv heads), so a
 // warp, not a CTA, is what takes a share of the line of blocks: it works on its blocks alone and
@@ -22,6 +23,7 @@
 // Calls of little work read each row's keys once for each row instead (paged_decode.cu,
 // PD_SHARED), which is one launch.
 #include "paged_decode.cuh"
+#include "paged_groups.cuh"
 
 namespace ember {
 
@@ -40,7 +42,7 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_shared_tail(
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g4 = lane >> 2, q4 = lane & 3;
     const int D = a.c.D, NKV = a.c.NKV, G = a.NH / NKV;
-    const unsigned W = blockIdx.x * PD_WARPS + warp, NW = gridDim.x * PD_WARPS;
+    const unsigned W = blockIdx.x * PD_WARPS + warp;
     int2* record = reinterpret_cast<int2*>(a.ws);
 
     // (no wait: this grid starts when all CTAs of the prefixes' are past theirs, and everything
@@ -49,9 +51,20 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_shared_tail(
     unsigned line = 0, before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32 * PD_SCAN) line += scan_chunk<KEYS, PD_TAIL>(a, b0, W == 0, n, before);
     line *= NKV;
+    // as many CTAs as have room on the SMs that the prefixes leave
+    const PtGroups gs{a.groups, a.shared, a.prefixes, a.lens, a.n_groups, a.B, a.c.n_seqs, NKV, a.prefix_rows,
+                      (long long)a.c.width << a.c.page_shift};
+    unsigned pairs = 0, tiles = 0;
+    for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
+        unsigned pair0, line0;
+        (void)pt_scan(gs, g0, pairs, tiles, pair0, line0);
+    }
+    const int per_sm = pd_ctas_per_sm(HT), sms = (int)gridDim.x / per_sm;
+    const int beside = prefix_sms(tiles, pairs, (float)line * (KEYS * DP * 4), sms);
+    const unsigned NW = PD_WARPS * (unsigned)per_sm * (beside < sms ? sms - beside : sms);
     const unsigned each = max(1u, (line + NW - 1) / NW);
     const unsigned lo = min(line, W * each), hi = min(line, lo + each);
-    for (int b = W; b < a.B; b += NW)            // rows without blocks
+    for (int b = W; b < a.B; b += gridDim.x * PD_WARPS)   // rows without blocks
         if (seq_blocks<KEYS, PD_TAIL>(a, b, false).n == 0)
             for (int g = lane; g < NKV; g += 32) record[(size_t)b * NKV + g] = make_int2(0, 0);
 
@@ -180,13 +193,13 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_shared_tail(
 
 // Joins what the two have left of a row's kv head: block (kv head, row).  Threads take four
 // dimensions each and the partials in turn.
-constexpr int SJ_THREADS = 256;
+constexpr int SJ_AHEAD = 4;                      // partials asked for at a time
 
-template <class E>
+template <class E, int SJ_THREADS>
 __global__ void __launch_bounds__(SJ_THREADS) k_shared_join(PagedDecodeArgs a, int warps) {
-    __shared__ float s_m[16], s_inv[16];
     __shared__ float4 s_o[SJ_THREADS];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float2 s_ml[SJ_THREADS];
+    const int tid = threadIdx.x;
     const int g = blockIdx.x, b = blockIdx.y;
     const int D = a.c.D, NKV = a.c.NKV, G = a.NH / NKV;
     // What the call got may be read before the wait (the kernels before began after it was complete).
@@ -220,66 +233,74 @@ __global__ void __launch_bounds__(SJ_THREADS) k_shared_join(PagedDecodeArgs a, i
     const float* sums = a.prefix + a.prefix_head + ((size_t)slot0 * 256 + at) * D;
     const float2* ml = reinterpret_cast<const float2*>(a.prefix + a.prefix_head + (size_t)a.prefix_slots * 256 * D) + (size_t)slot0 * 256 + at;
     const int parts = np + no;
-    auto state = [&](int h, int i) {
-        return __ldcg(i < np ? ml + (size_t)i * 256 + h : reinterpret_cast<const float2*>(own + ((size_t)(i - np) * G + h) * (D + 2)));
-    };
-    for (int h = warp; h < G; h += SJ_THREADS / 32) {
-        float M = SOFTMAX_FLOOR, l = 0.f;
-        for (int i = lane; i < parts; i += 32) {
-            const float2 x = state(h, i);
-            const float to = fmaxf(M, x.x);
-            l = l * ex2(M - to) + x.y * ex2(x.x - to);
-            M = to;
-        }
-        const float top = warp_max(M);
-        l = warp_sum(l * ex2(M - top));
-        if (lane == 0) {
-            s_m[h] = top;
-            s_inv[h] = l == 0.f ? 0.f : 1.f / l;
-            if (a.lse) a.lse[(long long)b * a.NH + g * G + h] = l == 0.f ? -INFINITY : top * LN2 + logf(l);
-        }
-    }
-    __syncthreads();
+    // Each thread takes four dimensions of a head and every turns-th partial, four at a time, against
+    // a maximum of its own; the threads of one place are joined at the end.
     const int quads = G * (D / 4), wide = min(quads, SJ_THREADS), turns = SJ_THREADS / wide, t0 = tid / wide;
     for (int q0 = 0; q0 < quads; q0 += wide) {
         const int q = q0 + tid % wide, h = q / (D / 4), d = 4 * (q - h * (D / 4));
+        float M = SOFTMAX_FLOOR, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (q < quads && t0 < turns) {
-            const float m = s_m[h];
-#pragma unroll 4
-            for (int i = t0; i < parts; i += turns) {
-                float4 x;
-                if (i < np) {
-                    x = __ldcg(reinterpret_cast<const float4*>(sums + ((size_t)i * 256 + h) * D + d));
-                } else {
-                    const float2* p = reinterpret_cast<const float2*>(own + ((size_t)(i - np) * G + h) * (D + 2) + 2 + d);
-                    const float2 u = __ldcg(p), v = __ldcg(p + 1);
-                    x = make_float4(u.x, u.y, v.x, v.y);
+        auto add = [&](float f, const float4& x) {
+            o.x = fmaf(x.x, f, o.x);
+            o.y = fmaf(x.y, f, o.y);
+            o.z = fmaf(x.z, f, o.z);
+            o.w = fmaf(x.w, f, o.w);
+        };
+        auto move = [&](float to) {
+            const float f = ex2(M - to);
+            l *= f;
+            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+            M = to;
+        };
+        if (q < quads && t0 < turns)
+            for (int i0 = t0; i0 < parts; i0 += SJ_AHEAD * turns) {
+                float2 s2[SJ_AHEAD];
+                float4 x[SJ_AHEAD];
+                float top = M;
+#pragma unroll
+                for (int k = 0; k < SJ_AHEAD; ++k) {
+                    const int i = i0 + k * turns;
+                    s2[k] = make_float2(SOFTMAX_FLOOR, 0.f);
+                    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i < np) {
+                        s2[k] = __ldcg(ml + (size_t)i * 256 + h);
+                        x[k] = __ldcg(reinterpret_cast<const float4*>(sums + ((size_t)i * 256 + h) * D + d));
+                    } else if (i < parts) {
+                        const float2* p = reinterpret_cast<const float2*>(own + ((size_t)(i - np) * G + h) * (D + 2));
+                        const float2 u = __ldcg(p + 1 + d / 2), v = __ldcg(p + 2 + d / 2);
+                        s2[k] = __ldcg(p);
+                        x[k] = make_float4(u.x, u.y, v.x, v.y);
+                    }
                 }
-                const float f = ex2(state(h, i).x - m);
-                o.x = fmaf(x.x, f, o.x);
-                o.y = fmaf(x.y, f, o.y);
-                o.z = fmaf(x.z, f, o.z);
-                o.w = fmaf(x.w, f, o.w);
+#pragma unroll
+                for (int k = 0; k < SJ_AHEAD; ++k) top = fmaxf(top, s2[k].x);
+                if (top > M) move(top);
+#pragma unroll
+                for (int k = 0; k < SJ_AHEAD; ++k) {
+                    const float f = ex2(s2[k].x - M);
+                    l = fmaf(s2[k].y, f, l);
+                    add(f, x[k]);
+                }
             }
-        }
         if (turns > 1) {
             __syncthreads();
             s_o[tid] = o;
+            s_ml[tid] = make_float2(M, l);
             __syncthreads();
             if (t0 == 0)
                 for (int t = 1; t < turns; ++t) {
-                    const float4 y = s_o[tid + t * wide];
-                    o.x += y.x;
-                    o.y += y.y;
-                    o.z += y.z;
-                    o.w += y.w;
+                    const float2 y = s_ml[tid + t * wide];
+                    if (y.x > M) move(y.x);
+                    const float f = ex2(y.x - M);
+                    l = fmaf(y.y, f, l);
+                    add(f, s_o[tid + t * wide]);
                 }
         }
         if (q < quads && t0 == 0) {
-            const float inv = s_inv[h];
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             uint2* out = reinterpret_cast<uint2*>(a.out + (long long)b * a.ld_out + (long long)(g * G + h) * D + d);
             *out = make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
+            if (a.lse && d == 0) a.lse[(long long)b * a.NH + g * G + h] = l == 0.f ? -INFINITY : M * LN2 + logf(l);
         }
     }
 }
@@ -316,7 +337,10 @@ cudaError_t launch_ht(PagedDecodeArgs a, const PagedPrefillArgs& p, const PagedP
     if (e != cudaSuccess) return e;
     e = launch_k(k, dim3(plan.grid), dim3(PD_THREADS), SMEM, s, a);
     if (e != cudaSuccess) return e;
-    return launch_k(k_shared_join<E>, dim3(a.c.NKV, a.B), dim3(SJ_THREADS), 0, s, a, plan.grid * PD_WARPS);
+    // all blocks at once: 1024 of 256 threads take two rounds of 4 us
+    const dim3 grid(a.c.NKV, a.B);
+    if ((long long)a.c.NKV * a.B <= 4 * sms) return launch_k(k_shared_join<E, 256>, grid, dim3(256), 0, s, a, plan.grid * PD_WARPS);
+    return launch_k(k_shared_join<E, 128>, grid, dim3(128), 0, s, a, plan.grid * PD_WARPS);
 }
 template <class E>
 cudaError_t launch_type(const PagedDecodeArgs& a, const PagedPrefillArgs& p, const PagedPrefillMaps& m, const SharedPlan& plan,
