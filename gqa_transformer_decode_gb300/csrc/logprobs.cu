@@ -28,15 +28,16 @@ namespace ember {
 
 namespace {
 
-constexpr int LP_THREADS = 512;
-constexpr int LP_WARPS = LP_THREADS / 32;
-constexpr int LP_GROUP = LP_THREADS / 32;       // lanes of a group: 32 groups
+// Threads of a CTA, T: 512 while the rows are few, whose ends (joining, ordering) then take half the
+// time (64 rows of 128256 f32, top 20: 23 and 29 us), else 256, whose rows end one under another's
+// loads (2048 rows of 151936 bf16, top 10: 237 and 215 us).  1024 threads of an SM either way.
+constexpr int lp_per_sm(int T) { return 1024 / T; }
 constexpr int LP_AHEAD = 4;                     // vectors of 16 bytes in flight for each thread
 constexpr int LP_TOP = EMBER_LOGPROBS_MAX_TOP;
 constexpr int LP_CLUSTER = 8;                   // CTAs of a row at most
 constexpr int LP_HITS = 2048;                   // vectors looked at again at most
-// A group without elements leaves no bound, but then there are less than LP_THREADS vectors (of 8) and the ends.
-constexpr int LP_LIST = 8 * (LP_THREADS + 2);
+// A group (T / 32 lanes) without elements leaves no bound, but then there are less than T vectors (of 8) and the ends.
+constexpr int lp_list(int T) { return 8 * (T + 2); }
 static_assert(LP_TOP == 32, "one group's maximum for each of the largest");
 // In the fast pass every logit counts as at least LP_LOW: -inf then has the weight 0 and
 // gives no inf - inf.  A row whose largest logit is not within +-LP_LOW goes the slow way.
@@ -169,31 +170,34 @@ __device__ __forceinline__ Sums join_lanes(Sums q, float c2) {
     }
     return q;
 }
-// Over the whole CTA (s_sums: LP_WARPS of them).
+// Over the whole CTA (s_sums: one a warp).
+template <int T>
 __device__ __noinline__ Sums join_all(Sums q, float c2, Sums* s_sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     q = join_lanes<32>(q, c2);
     __syncthreads();
     if (lane == 0) s_sums[warp] = q;
     __syncthreads();
-    return join_lanes<LP_WARPS>(s_sums[lane % LP_WARPS], c2);
+    return join_lanes<T / 32>(s_sums[lane % (T / 32)], c2);
 }
 
 // A lower bound of the top-th largest logit from the groups' maxima as they are (each a
 // lower bound of what it will be); g: this thread's maximum.  By a whole warp.  The top-th
-// largest maximum is the best such bound; beyond the eighth the least of all, which takes one
-// reduction, costs less than the longer list it lets in.
-__device__ __noinline__ float raise_bound(float g, float* s_group, int top) {
+// largest maximum is the best such bound; on the way, beyond the eighth, the least of all, which
+// takes one reduction, costs less than the longer list that it lets in.
+template <int T>
+__device__ __noinline__ float raise_bound(float g, float* s_group, int top, bool best) {
+    constexpr int GROUP = T / 32;
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 1; o < LP_GROUP; o <<= 1) g = fmaxf(g, __shfl_xor_sync(FULL_MASK, g, o));
+    for (int o = 1; o < GROUP; o <<= 1) g = fmaxf(g, __shfl_xor_sync(FULL_MASK, g, o));
     volatile float* group = s_group;
-    if (lane % LP_GROUP == 0) group[threadIdx.x / LP_GROUP] = g;
+    if (lane % GROUP == 0) group[threadIdx.x / GROUP] = g;
     __syncwarp();
     // the values' order as unsigned numbers, the lane below them (1: -inf or none)
     uint32_t v = (uint32_t)(argmax_key(group[lane], 0u) >> 32);
     uint32_t k = __reduce_min_sync(FULL_MASK, v);
-    if (top <= 8)
+    if (top <= 8 || (best && top < 32))
         for (int i = 0; i < top; ++i) {
             k = __reduce_max_sync(FULL_MASK, v);
             const unsigned at = __ballot_sync(FULL_MASK, v == k);
@@ -203,31 +207,35 @@ __device__ __noinline__ float raise_bound(float g, float* s_group, int top) {
 }
 
 // Puts each key of s_keys[0 .. n) that is among the `top` largest into its place: the number of
-// larger ones (0: no key).
+// larger ones (0: no key).  Four lanes count for a key.
+template <int T>
 __device__ __noinline__ void order_keys(const unsigned long long* s_keys, int n, int top, unsigned long long* s_top) {
-    for (int i = threadIdx.x; i < n; i += LP_THREADS) {
-        const unsigned long long x = s_keys[i];
+    for (int i0 = 0; i0 < n; i0 += T / 4) {
+        const int i = i0 + (int)threadIdx.x / 4;
+        const unsigned long long x = i < n ? s_keys[i] : 0ull;
         int larger = 0;
 #pragma unroll 4
-        for (int k = 0; k < n; ++k) larger += s_keys[k] > x;
-        if (x != 0 && larger < top) s_top[larger] = x;
+        for (int k = threadIdx.x & 3; k < n; k += 4) larger += s_keys[k] > x;
+        larger += __shfl_xor_sync(FULL_MASK, larger, 1);
+        larger += __shfl_xor_sync(FULL_MASK, larger, 2);
+        if (x != 0 && larger < top && (threadIdx.x & 3) == 0) s_top[larger] = x;
     }
 }
 
 // The slow ways, over elements [i0, i1) of a row, by the whole CTA.
 struct Search {
-    unsigned long long best[LP_WARPS];
-    int found[LP_WARPS];
+    unsigned long long best[32];
+    int found[32];
 };
 // Adds to s_top[have ..] the largest elements below the key `before` (first: there is none), in
 // order, until there are `top`: finds the largest, then in one walk all that equal it.
-template <class L>
+template <class L, int T>
 __device__ __noinline__ int take_largest(const typename L::T* row, int i0, int i1, unsigned long long before, bool first,
                                          int have, int top, unsigned long long* s_top, Search& s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     while (have < top) {
         unsigned long long best = 0;
-        for (int i = i0 + tid; i < i1; i += LP_THREADS) {
+        for (int i = i0 + tid; i < i1; i += T) {
             const unsigned long long k = argmax_key(L::one(row[i]), (uint32_t)i);
             if ((first || k < before) && k > best) best = k;
         }
@@ -239,10 +247,10 @@ __device__ __noinline__ int take_largest(const typename L::T* row, int i0, int i
         __syncthreads();
         if (lane == 0) s.best[warp] = best;
         __syncthreads();
-        for (int w = 0; w < LP_WARPS; ++w) best = s.best[w] > best ? s.best[w] : best;
+        for (int w = 0; w < (T / 32); ++w) best = s.best[w] > best ? s.best[w] : best;
         if (best == 0) return have;                  // no more of them (a key is never 0)
         const uint32_t value = (uint32_t)(best >> 32);
-        for (int j = argmax_key_index(best); j < i1 && have < top; j += LP_THREADS) {
+        for (int j = argmax_key_index(best); j < i1 && have < top; j += T) {
             const int i = j + tid;
             const unsigned long long k = i < i1 ? argmax_key(L::one(row[i]), (uint32_t)i) : 0ull;
             const bool same = i < i1 && (uint32_t)(k >> 32) == value;
@@ -251,7 +259,7 @@ __device__ __noinline__ int take_largest(const typename L::T* row, int i0, int i
             if (lane == 0) s.found[warp] = __popc(m);
             __syncthreads();
             int at = have + __popc(m & ((1u << lane) - 1u));
-            for (int w = 0; w < LP_WARPS; ++w) {
+            for (int w = 0; w < (T / 32); ++w) {
                 if (w < warp) at += s.found[w];
                 have += s.found[w];
             }
@@ -263,11 +271,11 @@ __device__ __noinline__ int take_largest(const typename L::T* row, int i0, int i
     return top;
 }
 // Sums of a row of any values; above: how many stand before element id, less id.
-template <class L>
+template <class L, int T>
 __device__ __noinline__ Sums sum_slowly(const typename L::T* row, int i0, int i1, int id, float xi, float c2, Sums* s_sums) {
     Sums q{-INFINITY, 0.f, 0.f, 0};
     const unsigned long long mine = id >= 0 ? argmax_key(xi, (uint32_t)id) : 0ull;
-    for (int i = i0 + (int)threadIdx.x; i < i1; i += LP_THREADS) {
+    for (int i = i0 + (int)threadIdx.x; i < i1; i += T) {
         const float x = L::one(row[i]);
         if (id >= 0) q.above += (argmax_key(x, (uint32_t)i) > mine) - (i < id);
         if (x > q.m) q.move(x, c2);
@@ -275,17 +283,17 @@ __device__ __noinline__ Sums sum_slowly(const typename L::T* row, int i0, int i1
         q.s += p;
         q.u = fmaf(p, d, q.u);
     }
-    return join_all(q, c2, s_sums);
+    return join_all<T>(q, c2, s_sums);
 }
 
-template <class L>
-__global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(LogprobsArgs a) {
-    constexpr int VEC = L::VEC;
-    using T = typename L::T;
+template <class L, int T>
+__global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
+    constexpr int VEC = L::VEC, LP_LIST = lp_list(T);
+    using Elem = typename L::T;
     __shared__ unsigned long long s_list[LP_LIST];
     __shared__ unsigned long long s_top[LP_TOP], s_all[LP_CLUSTER * LP_TOP];
     __shared__ float s_group[32];
-    __shared__ Sums s_sums[LP_WARPS], s_part;
+    __shared__ Sums s_sums[T / 32], s_part;
     __shared__ int s_hit[LP_HITS], s_hits, s_count, s_nan;
     __shared__ Search s_search;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -299,8 +307,8 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(LogprobsArgs a) {
 
     // Vector j of the row holds elements first + j * VEC ..: the 0th ends where the row's
     // memory is aligned, so it and the last one may be partly or wholly outside.
-    const T* row = static_cast<const T*>(a.logits) + r * a.ldl;
-    const int ahead = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T);   // elements before it
+    const Elem* row = static_cast<const Elem*>(a.logits) + r * a.ldl;
+    const int ahead = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(Elem);   // elements before it
     const int first = ahead - VEC;
     const int vectors = 1 + (int)(((long long)a.V - ahead + VEC - 1) / VEC);
     const int lo = (int)((long long)vectors * part / C), hi = (int)((long long)vectors * (part + 1) / C);
@@ -320,8 +328,8 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(LogprobsArgs a) {
     float bound = LP_LOW;                        // of the top-th largest logit, from below
     // What a vector has to reach to be looked at by element: the bound, or the given token's logit.
     float reach = count_fast ? (top > 0 ? LP_LOW : xi) : top > 0 ? LP_LOW : INFINITY;
-    auto raise = [&](float g) {
-        bound = raise_bound(g, s_group, top);
+    auto raise = [&](float g, bool best) {
+        bound = raise_bound<T>(g, s_group, top, best);
         reach = count_fast ? fminf(bound, xi) : bound;
     };
     // Lists element i of value x if it may be among the largest.
@@ -381,7 +389,7 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(LogprobsArgs a) {
     const uint4 none = make_uint4(L::NONE, L::NONE, L::NONE, L::NONE);
 #pragma unroll
     for (int k = 0; k < LP_AHEAD; ++k) {
-        const int j = whole_lo + tid + k * LP_THREADS;
+        const int j = whole_lo + tid + k * T;
         next[k] = j < whole_hi ? ld_stream(at + j) : none;
     }
     __syncthreads();
@@ -393,21 +401,21 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(LogprobsArgs a) {
             const float big = L::unpack(next[k], x);
             g = fmaxf(g, big);                   // (a NaN is left out here, and found below)
         }
-        raise(g);
+        raise(g, false);
         __syncthreads();
-        raise(g);
+        raise(g, false);
         q.m = g > LP_LOW ? g : -INFINITY;
     }
-    for (int j0 = whole_lo; j0 < whole_hi; j0 += LP_AHEAD * LP_THREADS) {
+    for (int j0 = whole_lo; j0 < whole_hi; j0 += LP_AHEAD * T) {
         bool listed = false;
 #pragma unroll
         for (int k = 0; k < LP_AHEAD; ++k) {
-            const int j = j0 + tid + k * LP_THREADS, jn = j + LP_AHEAD * LP_THREADS;
+            const int j = j0 + tid + k * T, jn = j + LP_AHEAD * T;
             const uint4 w = next[k];
             if (jn < whole_hi) next[k] = ld_stream(at + jn);
             if (j < whole_hi) listed |= work(w, j);
         }
-        if (top > 0 && __any_sync(FULL_MASK, listed)) raise(q.m);
+        if (top > 0 && __any_sync(FULL_MASK, listed)) raise(q.m, false);
     }
     // the row's ends, an element a thread
     if (tid < 2 * VEC) {
@@ -425,16 +433,16 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(LogprobsArgs a) {
     }
     if (nan) s_nan = 1;
     const float largest = q.m;                   // of this thread
-    if (top > 0) raise(largest);
-    q = join_all(q, c2, s_sums);
+    if (top > 0) raise(largest, false);
+    q = join_all<T>(q, c2, s_sums);
 
     // ---- this part's largest above LP_LOW, in order ----
     const int i_lo = max(0, first + lo * VEC), i_hi = (int)min((long long)a.V, first + (long long)hi * VEC);
     if (top > 0) {
-        raise(largest);
+        raise(largest, true);
         const int hits = s_hits;
         if (hits <= LP_HITS)
-            for (int h = tid; h < hits; h += LP_THREADS) {
+            for (int h = tid; h < hits; h += T) {
                 const int j = s_hit[h];
                 float x[VEC];
                 L::unpack(ld_stream(at + j), x);
@@ -444,11 +452,11 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(LogprobsArgs a) {
         __syncthreads();
         const int listed = s_count;
         if (s_nan || hits > LP_HITS || listed > LP_LIST) {
-            take_largest<L>(row, i_lo, i_hi, 0ull, true, 0, top, s_top, s_search);
+            take_largest<L, T>(row, i_lo, i_hi, 0ull, true, 0, top, s_top, s_search);
             __syncthreads();
             if (tid < top && s_top[tid] <= argmax_key(LP_LOW, 0u)) s_top[tid] = 0;
         } else {
-            order_keys(s_list, listed, top, s_top);
+            order_keys<T>(s_list, listed, top, s_top);
         }
     }
     if (tid == 0) s_part = q;
@@ -471,29 +479,35 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(LogprobsArgs a) {
             q.s = __shfl_sync(FULL_MASK, q.s, 0);
             q.u = __shfl_sync(FULL_MASK, q.u, 0);
             q.above = __shfl_sync(FULL_MASK, q.above, 0);
-            for (int i = tid; i < (int)C * top; i += LP_THREADS) {
+            for (int i = tid; i < (int)C * top; i += T) {
                 const float2 k = ld_cluster2(keys + 8 * (i % top), i / top);
                 s_all[i] = (unsigned long long)__float_as_uint(k.y) << 32 | __float_as_uint(k.x);
             }
             if (tid > 0 && tid < (int)C && __float_as_int(ld_cluster(sa_u32(&s_nan), tid)) != 0) s_nan = 1;
         }
-        cluster_sync_all();                      // no CTA leaves while its shared memory is read
-        if (part != 0) return;
+        // no CTA leaves while its shared memory is read
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        if (part != 0) {
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            return;
+        }
+        __syncthreads();
         if (tid < top) s_top[tid] = 0;
         __syncthreads();
-        order_keys(s_all, (int)C * top, top, s_top);
+        order_keys<T>(s_all, (int)C * top, top, s_top);
     }
     __syncthreads();
 
     // ---- what the fast pass leaves out ----
     const bool has_nan = s_nan != 0;
     if (has_nan || !(q.m > LP_LOW && q.m < -LP_LOW) || (given && !count_fast))
-        q = sum_slowly<L>(row, 0, a.V, given ? id : -1, xi, c2, s_sums);
+        q = sum_slowly<L, T>(row, 0, a.V, given ? id : -1, xi, c2, s_sums);
     else if (given)
         q.above -= id;                           // (sum_slowly's count)
     if (top > 0) {
         const int have = __syncthreads_count(tid < top && s_top[min(tid, LP_TOP - 1)] != 0);
-        if (have < top) take_largest<L>(row, 0, a.V, have > 0 ? s_top[have - 1] : 0ull, have == 0, have, top, s_top, s_search);
+        if (have < top) take_largest<L, T>(row, 0, a.V, have > 0 ? s_top[have - 1] : 0ull, have == 0, have, top, s_top, s_search);
         __syncthreads();
     }
 
@@ -515,18 +529,25 @@ __global__ void __launch_bounds__(LP_THREADS, 2) k_logprobs(LogprobsArgs a) {
         a.top_ids[r * top + tid] = argmax_key_index(k);
         a.top_logprobs[r * top + tid] = logprob(key_value(k));
     }
+    if (C > 1) {
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
 }
 
-template <class L>
-cudaError_t launch_type(LogprobsArgs a, int sms, cudaStream_t s) {
-    // As many CTAs of a row as leave every one its place (two on an SM) and a first batch.
+template <class L, int T>
+cudaError_t launch_threads(LogprobsArgs a, int sms, cudaStream_t s) {
+    // As many CTAs of a row as leave every one its place and a first batch.
     a.cluster = 1;
-    while (a.cluster < LP_CLUSTER && (long long)a.n * a.cluster * 2 <= 2 * sms &&
-           a.V >= 2 * a.cluster * L::VEC * LP_THREADS)
+    while (a.cluster < LP_CLUSTER && (long long)a.n * a.cluster * 2 <= lp_per_sm(T) * sms && a.V >= 2 * a.cluster * L::VEC * T)
         a.cluster *= 2;
     const dim3 grid((unsigned)(a.n * (long long)a.cluster));
-    if (a.cluster > 1) return launch_cluster_k(k_logprobs<L>, grid, dim3(LP_THREADS), 0, a.cluster, s, a);
-    return launch_k(k_logprobs<L>, grid, dim3(LP_THREADS), 0, s, a);
+    if (a.cluster > 1) return launch_cluster_k(k_logprobs<L, T>, grid, dim3(T), 0, a.cluster, s, a);
+    return launch_k(k_logprobs<L, T>, grid, dim3(T), 0, s, a);
+}
+template <class L>
+cudaError_t launch_type(const LogprobsArgs& a, int sms, cudaStream_t s) {
+    return a.n <= sms ? launch_threads<L, 512>(a, sms, s) : launch_threads<L, 256>(a, sms, s);
 }
 
 }  // namespace
