@@ -60,16 +60,31 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t x, uint32_t y) {
     return r;
 }
 
-// Element types: a 16-byte vector as floats that are at least LP_LOW, and their largest.
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+
+// Element types.  largest: of a 16-byte vector, at least LP_LOW, NaN if one is; unpack: its
+// elements as floats that are at least LP_LOW; above: how many are larger than x (EQUAL: or equal),
+// x of the type, in pairs (1.0 for each; with conversions first it took twice as long).
 struct LogitF32 {
     static constexpr int VEC = 4;
     using T = float;
     static constexpr uint32_t NONE = 0xff800000u;   // -inf
     __device__ __forceinline__ static float one(float x) { return x; }
-    __device__ __forceinline__ static float unpack(const uint4& w, float* x) {
+    __device__ __forceinline__ static float largest(const uint4& w) {
+        return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z)), __uint_as_float(w.w), LP_LOW);
+    }
+    __device__ __forceinline__ static void unpack(const uint4& w, float* x) {
         x[0] = max_nan(__uint_as_float(w.x), LP_LOW), x[1] = max_nan(__uint_as_float(w.y), LP_LOW);
         x[2] = max_nan(__uint_as_float(w.z), LP_LOW), x[3] = max_nan(__uint_as_float(w.w), LP_LOW);
-        return max_nan(max_nan(x[0], x[1], x[2]), x[3]);
+    }
+    template <bool EQUAL>
+    __device__ __forceinline__ static int above(const uint4& w, float x) {
+        auto one = [&](uint32_t u) { return (int)(EQUAL ? __uint_as_float(u) >= x : __uint_as_float(u) > x); };
+        return one(w.x) + one(w.y) + one(w.z) + one(w.w);
     }
 };
 struct LogitBf16 {
@@ -77,12 +92,23 @@ struct LogitBf16 {
     using T = uint16_t;
     static constexpr uint32_t NONE = 0xff80ff80u;
     __device__ __forceinline__ static float one(uint16_t x) { return bf16_to_f32(x); }
-    __device__ __forceinline__ static float unpack(uint4 w, float* x) {
-        constexpr uint32_t low = 0xf14af14au;       // -1.0003e30: the largest bf16 that is not above LP_LOW
-        w = make_uint4(max_bf16x2(w.x, low), max_bf16x2(w.y, low), max_bf16x2(w.z, low), max_bf16x2(w.w, low));
-        unpack8(w, x);
+    __device__ __forceinline__ static float largest(const uint4& w) {
         const uint32_t m = max_bf16x2(max_bf16x2(w.x, w.y), max_bf16x2(w.z, w.w));
-        return max_nan(bf16_lo(m), bf16_hi(m));
+        return max_nan(bf16_lo(m), bf16_hi(m), LP_LOW);
+    }
+    __device__ __forceinline__ static void unpack(uint4 w, float* x) {
+        constexpr uint32_t low = 0xf14af14au;       // -1.0003e30: the largest bf16 that is not above LP_LOW
+        unpack8(make_uint4(max_bf16x2(w.x, low), max_bf16x2(w.y, low), max_bf16x2(w.z, low), max_bf16x2(w.w, low)), x);
+    }
+    template <bool EQUAL>
+    __device__ __forceinline__ static int above(const uint4& w, float x) {
+        const __nv_bfloat162 t = __float2bfloat162_rn(x);
+        auto two = [&](uint32_t u) {
+            const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&u);
+            return EQUAL ? __hge2(v, t) : __hgt2(v, t);
+        };
+        const __nv_bfloat162 n = __hadd2(__hadd2(two(w.x), two(w.y)), __hadd2(two(w.z), two(w.w)));
+        return (int)(__low2float(n) + __high2float(n));
     }
 };
 struct LogitF16 {
@@ -90,11 +116,24 @@ struct LogitF16 {
     using T = uint16_t;
     static constexpr uint32_t NONE = 0xfc00fc00u;
     __device__ __forceinline__ static float one(uint16_t x) { return __half2float(__ushort_as_half(x)); }
-    __device__ __forceinline__ static float unpack(const uint4& w, float* x) {
+    __device__ __forceinline__ static float largest(const uint4& w) {
+        const uint32_t m = max_f16x2(max_f16x2(w.x, w.y), max_f16x2(w.z, w.w));
+        return max_nan(one((uint16_t)m), one((uint16_t)(m >> 16)), LP_LOW);
+    }
+    __device__ __forceinline__ static void unpack(const uint4& w, float* x) {
         unpack8_f16(w, x);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) x[e] = max_nan(x[e], LP_LOW);
-        return max_nan(max_nan(max_nan(x[0], x[1], x[2]), x[3], x[4]), max_nan(x[5], x[6], x[7]));
+    }
+    template <bool EQUAL>
+    __device__ __forceinline__ static int above(const uint4& w, float x) {
+        const __half2 t = __float2half2_rn(x);
+        auto two = [&](uint32_t u) {
+            const __half2 v = *reinterpret_cast<const __half2*>(&u);
+            return EQUAL ? __hge2(v, t) : __hgt2(v, t);
+        };
+        const __half2 n = __hadd2(__hadd2(two(w.x), two(w.y)), __hadd2(two(w.z), two(w.w)));
+        return (int)(__low2float(n) + __high2float(n));
     }
 };
 
@@ -137,36 +176,26 @@ struct Sums {
     float m, s, u;
     int above;
     __device__ __forceinline__ void move(float to, float c2) {   // to a larger maximum
-        const float f = m == -INFINITY ? 0.f : ex2((m - to) * c2);
+        const float f = ex2((m - to) * c2);
         u = f == 0.f ? 0.f : f * fmaf(s, m - to, u);   // (without weight m - to may be of any size)
         s *= f;
         m = to;
     }
-    __device__ __forceinline__ void join(Sums o, float c2) {
-        if (o.m > m) move(o.m, c2);
-        else if (m > o.m) o.move(m, c2);
-        s += o.s;
-        u += o.u;
-        above += o.above;
-    }
 };
 
-// The sums of `n` neighbouring lanes (a power of two) joined, in one order for all of them.
+// The sums of N neighbouring lanes joined: all to the largest maximum first, then plain sums, in
+// one order for all of them.
 template <int N>
 __device__ __forceinline__ Sums join_lanes(Sums q, float c2) {
+    float m = q.m;
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
+    if (m > q.m) q.move(m, c2);
 #pragma unroll
     for (int o = N / 2; o > 0; o >>= 1) {
-        Sums y;
-        y.m = __shfl_xor_sync(FULL_MASK, q.m, o);
-        y.s = __shfl_xor_sync(FULL_MASK, q.s, o);
-        y.u = __shfl_xor_sync(FULL_MASK, q.u, o);
-        y.above = __shfl_xor_sync(FULL_MASK, q.above, o);
-        if (threadIdx.x & o) {
-            const Sums t = q;
-            q = y;
-            y = t;
-        }
-        q.join(y, c2);
+        q.s += __shfl_xor_sync(FULL_MASK, q.s, o);
+        q.u += __shfl_xor_sync(FULL_MASK, q.u, o);
+        q.above += __shfl_xor_sync(FULL_MASK, q.above, o);
     }
     return q;
 }
@@ -321,70 +350,29 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
     const float xi = given ? L::one(row[id]) : 0.f;
     const bool count_fast = given && xi > LP_LOW;
     const int jid = given ? (id - first) / VEC : -1;                               // its vector
-    const float below_xi = nextafterf(xi, -INFINITY);
 
-    Sums q{-INFINITY, 0.f, 0.f, 0};
+    Sums q{LP_LOW, 0.f, 0.f, 0};
     bool nan = false;
     float bound = LP_LOW;                        // of the top-th largest logit, from below
-    // What a vector has to reach to be looked at by element: the bound, or the given token's logit.
-    float reach = count_fast ? (top > 0 ? LP_LOW : xi) : top > 0 ? LP_LOW : INFINITY;
-    auto raise = [&](float g, bool best) {
-        bound = raise_bound<T>(g, s_group, top, best);
-        reach = count_fast ? fminf(bound, xi) : bound;
-    };
+    auto raise = [&](float g, bool best) { bound = raise_bound<T>(g, s_group, top, best); };
     // Lists element i of value x if it may be among the largest.
     auto list = [&](float x, int i) {
         if (!(x >= bound && x > LP_LOW)) return;
         const int n = atomicAdd(&s_count, 1);
         if (n < LP_LIST) s_list[n] = argmax_key(x, (uint32_t)i);
     };
-    auto work = [&](const uint4& w, int j) {
-        float x[VEC];
-        float big = L::unpack(w, x);
-        if (!(big <= q.m)) {
-            if (big != big) {
-                nan = true;
-                big = q.m;
+    // The same in the batch that the given token's vector lies in or stands between.
+    auto count_around = [&](const uint4 (&w)[LP_AHEAD], int j) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) big = fmaxf(big, x[e]);
-            }
-            if (big > q.m) q.move(big, c2);
-        }
-        bool listed = false;
-        if (big >= reach) {
-            if (count_fast) {                    // larger ones, before the given token equal ones too
-                const float than = j < jid ? below_xi : xi;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) q.above += x[e] > than;
-            }
-            if (count_fast && j == jid) {        // (read again: one vector of the row)
-#pragma unroll 1
-                for (int i = first + j * VEC; i < id; ++i) q.above += L::one(row[i]) == xi;
-            }
-            listed = top > 0 && big >= bound;
-            if (listed) {
-                const int n = atomicAdd(&s_hits, 1);
-                if (n < LP_HITS) s_hit[n] = j;
-            }
-        }
-        const uint64_t m2 = pair(-q.m, -q.m), k2 = pair(c2, c2);
-        uint64_t s = pair(q.s, 0.f), u = pair(q.u, 0.f);
-#pragma unroll
-        for (int e = 0; e < VEC; e += 2) {
-            const uint64_t d = add2(pair(x[e], x[e + 1]), m2);
-            float2 p = halves(mul2(d, k2));
-            p.x = ex2(p.x);
-            p.y = ex2(p.y);
-            const uint64_t p2 = pair(p.x, p.y);
-            s = add2(s, p2);
-            u = fma2(p2, d, u);
-        }
-        const float2 s1 = halves(s), u1 = halves(u);
-        q.s = s1.x + s1.y;
-        q.u = u1.x + u1.y;
-        return listed;
+        for (int k = 0; k < LP_AHEAD; ++k) q.above += j + k * T < jid ? L::template above<true>(w[k], xi) : L::template above<false>(w[k], xi);
+        if ((jid - j) % T == 0 && jid >= whole_lo && jid < whole_hi)   // its own vector: equal ones before it (read again)
+            for (int i = first + jid * VEC; i < id; ++i) q.above += L::one(row[i]) == xi;
     };
-
+    // the row's ends, an element for each of the first threads
+    const int j_end = tid < VEC ? 0 : vectors - 1, i_end = first + j_end * VEC + tid % VEC;
+    const bool has_end = tid < 2 * VEC && j_end >= lo && j_end < hi && (j_end < whole_lo || j_end >= whole_hi) &&
+                         (tid < VEC || j_end > 0) && i_end >= 0 && i_end < a.V;
+    const float x_end = has_end ? L::one(row[i_end]) : 0.f;
     uint4 next[LP_AHEAD];
     const uint4 none = make_uint4(L::NONE, L::NONE, L::NONE, L::NONE);
 #pragma unroll
@@ -394,42 +382,88 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
     }
     __syncthreads();
     if (top > 0) {                               // a first bound before anything is listed
-        float g = -INFINITY;
+        float g = LP_LOW;
 #pragma unroll
-        for (int k = 0; k < LP_AHEAD; ++k) {
-            float x[VEC];
-            const float big = L::unpack(next[k], x);
-            g = fmaxf(g, big);                   // (a NaN is left out here, and found below)
-        }
+        for (int k = 0; k < LP_AHEAD; ++k) g = fmaxf(g, L::largest(next[k]));   // (a NaN is left out here, and found below)
         raise(g, false);
         __syncthreads();
         raise(g, false);
-        q.m = g > LP_LOW ? g : -INFINITY;
+        q.m = g;
     }
+    const uint64_t k2 = pair(c2, c2);
     for (int j0 = whole_lo; j0 < whole_hi; j0 += LP_AHEAD * T) {
-        bool listed = false;
+        // what has to be decided once for a batch, then its exponentials without a branch; vectors
+        // beyond the part are -inf
+        uint4 w[LP_AHEAD];
+        float big[LP_AHEAD];
 #pragma unroll
         for (int k = 0; k < LP_AHEAD; ++k) {
-            const int j = j0 + tid + k * T, jn = j + LP_AHEAD * T;
-            const uint4 w = next[k];
-            if (jn < whole_hi) next[k] = ld_stream(at + jn);
-            if (j < whole_hi) listed |= work(w, j);
+            const int jn = j0 + tid + (k + LP_AHEAD) * T;
+            w[k] = next[k];
+            next[k] = jn < whole_hi ? ld_stream(at + jn) : none;
+            big[k] = L::largest(w[k]);
         }
+        float most = max_nan(max_nan(big[0], big[1], big[2]), big[3]);
+        static_assert(LP_AHEAD == 4, "the batch's largest");
+        if (!(most <= q.m)) {
+            if (most != most) {
+                nan = true;
+                most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));   // (the row goes the slow way)
+            }
+            if (most > q.m) q.move(most, c2);
+        }
+        const int j = j0 + tid;
+        if (count_fast && most >= xi) {          // larger ones, before the given token equal ones too
+            if (j + (LP_AHEAD - 1) * T < jid) {
+#pragma unroll
+                for (int k = 0; k < LP_AHEAD; ++k) q.above += L::template above<true>(w[k], xi);
+            } else if (j > jid) {
+#pragma unroll
+                for (int k = 0; k < LP_AHEAD; ++k) q.above += L::template above<false>(w[k], xi);
+            } else {
+                count_around(w, j);
+            }
+        }
+        bool listed = false;
+        if (top > 0 && most >= bound)
+#pragma unroll
+            for (int k = 0; k < LP_AHEAD; ++k)
+                if (big[k] >= bound && big[k] > LP_LOW) {   // (beyond the part all are LP_LOW)
+                    const int n = atomicAdd(&s_hits, 1);
+                    if (n < LP_HITS) s_hit[n] = j + k * T;
+                    listed = true;
+                }
+        const uint64_t m2 = pair(-q.m, -q.m);
+        uint64_t s = 0ull, u = 0ull;
+#pragma unroll
+        for (int k = 0; k < LP_AHEAD; ++k) {
+            float x[VEC];
+            L::unpack(w[k], x);
+#pragma unroll
+            for (int e = 0; e < VEC; e += 2) {
+                const uint64_t d = add2(pair(x[e], x[e + 1]), m2);
+                float2 p = halves(mul2(d, k2));
+                p.x = ex2(p.x);
+                p.y = ex2(p.y);
+                const uint64_t p2 = pair(p.x, p.y);
+                s = add2(s, p2);
+                u = fma2(p2, d, u);
+            }
+        }
+        const float2 s1 = halves(s), u1 = halves(u);
+        q.s += s1.x + s1.y;
+        q.u += u1.x + u1.y;
         if (top > 0 && __any_sync(FULL_MASK, listed)) raise(q.m, false);
     }
-    // the row's ends, an element a thread
-    if (tid < 2 * VEC) {
-        const int j = tid < VEC ? 0 : vectors - 1, i = first + j * VEC + tid % VEC;
-        if (j >= lo && j < hi && (j < whole_lo || j >= whole_hi) && (tid < VEC || j > 0) && i >= 0 && i < a.V) {
-            const float v = max_nan(L::one(row[i]), LP_LOW);
-            if (v != v) nan = true;
-            else if (v > q.m) q.move(v, c2);
-            if (count_fast) q.above += v > xi || (v == xi && i < id);
-            if (top > 0) list(v, i);
-            const float d = v - q.m, p = ex2(d * c2);
-            q.s += p;
-            q.u = fmaf(p, d, q.u);
-        }
+    if (has_end) {
+        const float v = max_nan(x_end, LP_LOW);
+        if (v != v) nan = true;
+        else if (v > q.m) q.move(v, c2);
+        if (count_fast) q.above += v > xi || (v == xi && i_end < id);
+        if (top > 0) list(v, i_end);
+        const float d = v - q.m, p = ex2(d * c2);
+        q.s += p;
+        q.u = fmaf(p, d, q.u);
     }
     if (nan) s_nan = 1;
     const float largest = q.m;                   // of this thread
@@ -467,7 +501,7 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
         cluster_sync_all();
         if (part == 0) {
             const uint32_t sums = sa_u32(&s_part), keys = sa_u32(s_top);
-            Sums y{-INFINITY, 0.f, 0.f, 0};
+            Sums y{LP_LOW, 0.f, 0.f, 0};
             if (lane < (int)C) {
                 y.m = ld_cluster(sums, lane);
                 y.s = ld_cluster(sums + 4, lane);
