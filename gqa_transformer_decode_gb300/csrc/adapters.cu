@@ -35,7 +35,7 @@ namespace ember {
 
 namespace {
 
-constexpr int AD_BUILDERS = 4;                   // warps that write t's tiles, a stage each
+constexpr int AD_BUILDERS = 4;                   // warps that write t's tiles
 constexpr int AD_THREADS = 192 + 32 * AD_BUILDERS;
 constexpr int AD_M = 128;                        // rows of W in a tile
 constexpr int AD_BK = 64;                        // K of a block
@@ -226,7 +226,7 @@ __device__ __forceinline__ void store_out(const AdapterArgs& a, int row, int m, 
 template <class E, int NT, bool LOW>
 __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     k_adapter(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-              const __grid_constant__ CUtensorMap tmB, AdapterArgs a) {
+              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmOut, AdapterArgs a) {
     using L = AdSmem<NT, LOW>;
     constexpr int S = L::STAGES;
     constexpr uint32_t COLS = 2 * NT < 32 ? 32 : 2 * NT;     // of TMEM: two accumulators
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&t_go[s], 1);
-            mbar_init(&t_full[s], 1);
+            mbar_init(&t_full[s], AD_BUILDERS);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     } else if (warp >= 6) {
         if (!LOW) {   // -------------- which adapters a tile has, and t's tiles
             const int builder = warp - 6;
-            int g = 0, x = 0;                    // stages so far; those with an adapter's products
+            int g = 0;                           // stages so far
             uint32_t go_phase = 0;
             bool ok = true, waited = false;
             for (int li = 0; li < tiles && ok; ++li) {
@@ -466,56 +466,52 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                     asm volatile("bar.sync 2, %0;" ::"n"(32 * AD_BUILDERS) : "memory");
                 }
                 Block next(s_list + b * NT + part, slabs, C);
-                for (int f = 0; f < all; f += L::SLABS, ++g, ++x) {
+                for (int f = 0; f < all; f += L::SLABS, ++g) {
                     const int s = g % S, m = min(L::SLABS, all - f);
-                    const bool mine = x % AD_BUILDERS == builder;
-                    // Columns c0 .. of up to 32 rows a block, 16 ranks of both terms of each, or zeros; all
-                    // blocks' rows asked for together (rows in no order have one here and there), the
-                    // first ones before their stage is free.
-                    const AdEntry* en[L::SLABS];
-                    int slab[L::SLABS], wide = 0;
-                    uint4 v[L::SLABS][4];
-#pragma unroll
-                    for (int i = 0; i < L::SLABS; ++i) {
-                        en[i] = next.entry;
-                        slab[i] = next.slab;
-                        if (i < m) {
-                            wide = max(wide, en[i]->c1 - en[i]->c0);
-                            next.next();
+                    // Pieces of 32 rows of a block, 16 ranks of both terms of each row, or zeros: the
+                    // builders' in turn, the first one asked for before the stage is free.
+                    int p = builder, i = 0, c = 0;   // this builder's piece: of block i, column c
+                    const AdEntry* en = nullptr;
+                    int slab = 0;
+                    auto find = [&] {                // false: there is none
+                        for (; i < m; ++i, next.next()) {
+                            const int wide = (next.entry->c1 - next.entry->c0 + 31) / 32;
+                            if (p < wide) {
+                                en = next.entry;
+                                slab = next.slab;
+                                c = en->c0 + 32 * p + lane;
+                                return true;
+                            }
+                            p -= wide;
                         }
-                    }
-                    auto ask = [&](int c0) {
-#pragma unroll
-                        for (int i = 0; i < L::SLABS; ++i) {
-                            const int c = i < m ? en[i]->c0 + c0 + lane : NT;
-                            const bool own = i < m && c < en[i]->c1 && ids[c] == en[i]->adapter;
-                            const int p = c * (RP / 4) + slab[i] * 4;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) v[i][q] = make_uint4(0u, 0u, 0u, 0u);
-                            if (own && kept)
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) v[i][q] = kept_t[p + q];
-                            if (own && !kept)
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) v[i][q] = __ldcg(rows_t + p + q);
-                        }
+                        return false;
                     };
-                    if (mine) ask(0);
+                    uint4 v[4];
+                    auto ask = [&] {
+                        const bool own = c < en->c1 && ids[c] == en->adapter;
+                        const int from = c * (RP / 4) + slab * 4;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[q] = make_uint4(0u, 0u, 0u, 0u);
+                        if (own && kept)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) v[q] = kept_t[from + q];
+                        if (own && !kept)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) v[q] = __ldcg(rows_t + from + q);
+                    };
+                    bool some = find();
+                    if (some) ask();
                     if (!(ok = mbar_wait(&t_go[s], go_phase >> s & 1u))) break;
                     go_phase ^= 1u << s;
-                    if (!mine) continue;
-                    for (int c0 = 0; c0 < wide; c0 += 32) {
-                        if (c0 > 0) ask(c0);
+                    while (some) {
+                        uint8_t* dst = sm + s * L::STAGE + L::OFF_T + i * 2 * L::SLAB_T + c * 32;
+                        if (c < en->c1)
 #pragma unroll
-                        for (int i = 0; i < L::SLABS; ++i) {
-                            if (i >= m) continue;
-                            const int c = en[i]->c0 + c0 + lane;
-                            uint8_t* dst = sm + s * L::STAGE + L::OFF_T + i * 2 * L::SLAB_T + c * 32;
-                            if (c < en[i]->c1)
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    *reinterpret_cast<uint4*>(dst + (q >> 1) * L::SLAB_T + (((q & 1) ^ (c >> 2 & 1)) << 4)) = v[i][q];
-                        }
+                            for (int q = 0; q < 4; ++q)
+                                *reinterpret_cast<uint4*>(dst + (q >> 1) * L::SLAB_T + (((q & 1) ^ (c >> 2 & 1)) << 4)) = v[q];
+                        p += AD_BUILDERS;
+                        some = find();
+                        if (some) ask();
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
@@ -530,6 +526,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     } else {   // ---------------- output, warps 2..5
         const int quad = warp & 3, tid = threadIdx.x - 64;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        int slice = 0;
         for (int li = 0; li < tiles; ++li) {
             const int b = li & 1;
             const Tile t = tile_of(li);
@@ -557,14 +554,41 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                 }
                 break;
             }
-            const int f = tid % 16 * 8;          // this thread's 8 rows of W
-            float add[8];
+            if (!LOW) {   // slices of 16 rows of x through shared memory and TMA, two in turn
+                const int m = t.m0 + quad * 32 + lane;   // this thread's row of W
+                float add = 0.f;
+                if (a.bias && m < a.N) add = E::bf16 ? bf16_to_f32(a.bias[m]) : __half2float(__ushort_as_half(a.bias[m]));
+                for (int c = 0; c < rows; c += 16, ++slice) {
+                    uint32_t r[16];
+                    tmem_ld16(acc + c, r);
+                    tmem_ld_wait();
+                    if (c + 16 >= rows) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acc_empty[b]);
+                    }
+                    uint8_t* buf = sm + L::OFF_OUT + (slice & 1) * (16 * AD_M * 4);
+                    if (tid == 0) bulk_wait_read<1>();   // the slice before the last one has left
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (a.out_f32) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) add[i] = 0.f;
-            if (!LOW && a.bias && t.m0 + f < a.N) {
-                const uint4 w = *reinterpret_cast<const uint4*>(a.bias + t.m0 + f);
-                unpack8w<!E::bf16>(w, add);
+                        for (int i = 0; i < 16; ++i)
+                            reinterpret_cast<float*>(buf)[i * AD_M + quad * 32 + lane] = __uint_as_float(r[i]) + add;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            reinterpret_cast<uint16_t*>(buf)[i * AD_M + quad * 32 + lane] = (uint16_t)E::pack(__uint_as_float(r[i]) + add, 0.f);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (tid == 0) {
+                        tma_store_2d(&tmOut, buf, t.m0, t.row0 + c);   // (clipped to what there is)
+                        bulk_commit();
+                    }
+                }
+                continue;
             }
+            const int f = tid % 16 * 8;          // this thread's 8 ranks
             for (int c = 0; c < rows; c += AD_SLICE) {
                 uint32_t r[AD_SLICE];
                 tmem_ld16(acc + c, r);
@@ -584,13 +608,12 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                     const float4* p = reinterpret_cast<const float4*>(s_out + i * AD_LD + f);
                     const float4 u = p[0], v = p[1];
                     float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] += add[j];
                     store(t, c + i, f, y);
                 }
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
         }
+        if (!LOW && tid == 0) bulk_wait<0>();    // every output copy complete before the end
     }
     __syncwarp();
 
@@ -707,23 +730,31 @@ __global__ void __launch_bounds__(AR_WARPS * 32) k_adapter_rows(AdapterArgs a, c
 }
 
 template <class E, int NT, bool LOW>
-cudaError_t launch_nt(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const AdapterArgs& a, int grid,
-                      cudaStream_t s) {
+cudaError_t launch_nt(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const CUtensorMap& o, const AdapterArgs& a,
+                      int grid, cudaStream_t s) {
     constexpr int SMEM = AdSmem<NT, LOW>::TOTAL;
     auto k = k_adapter<E, NT, LOW>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    if (a.splits > 1) return launch_cluster_k(k, dim3(grid), dim3(AD_THREADS), SMEM, a.splits, s, w, x, b, a);
-    return launch_k(k, dim3(grid), dim3(AD_THREADS), SMEM, s, w, x, b, a);
+    if (a.splits > 1) return launch_cluster_k(k, dim3(grid), dim3(AD_THREADS), SMEM, a.splits, s, w, x, b, o, a);
+    return launch_k(k, dim3(grid), dim3(AD_THREADS), SMEM, s, w, x, b, o, a);
 }
 template <class E, bool LOW>
-cudaError_t launch_low(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const AdapterArgs& a, int grid, cudaStream_t s) {
-    if (a.nt <= 16) return launch_nt<E, 16, LOW>(w, x, b, a, grid, s);
-    if (a.nt <= 32) return launch_nt<E, 32, LOW>(w, x, b, a, grid, s);
-    if (a.nt <= 64) return launch_nt<E, 64, LOW>(w, x, b, a, grid, s);
-    if (a.nt <= 128) return launch_nt<E, 128, LOW>(w, x, b, a, grid, s);
-    if constexpr (!LOW) return launch_nt<E, 256, LOW>(w, x, b, a, grid, s);
+cudaError_t launch_low(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const CUtensorMap& o, const AdapterArgs& a,
+                       int grid, cudaStream_t s) {
+    if (a.nt <= 16) return launch_nt<E, 16, LOW>(w, x, b, o, a, grid, s);
+    if (a.nt <= 32) return launch_nt<E, 32, LOW>(w, x, b, o, a, grid, s);
+    if (a.nt <= 64) return launch_nt<E, 64, LOW>(w, x, b, o, a, grid, s);
+    if (a.nt <= 128) return launch_nt<E, 128, LOW>(w, x, b, o, a, grid, s);
+    if constexpr (!LOW) return launch_nt<E, 256, LOW>(w, x, b, o, a, grid, s);
     return cudaErrorInvalidValue;
+}
+template <class E>
+cudaError_t launch_rows(const AdapterArgs& a, const AdapterRows& r, cudaStream_t s) {
+    // an SM set to little shared memory takes no CTA of the second launch before this one's are gone
+    const cudaError_t e = cudaFuncSetAttribute(k_adapter_rows<E>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    return launch_k(k_adapter_rows<E>, dim3(a.R / AR_RANKS, a.n), dim3(AR_WARPS * 32), 0, s, a, r.x, r.ld_x, r.a);
 }
 template <class E>
 cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& p, const AdapterRows& r, cudaStream_t s) {
@@ -732,18 +763,19 @@ cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& 
     const auto& ma = *reinterpret_cast<const CUtensorMap*>(m.a);
     const auto& mb = *reinterpret_cast<const CUtensorMap*>(m.b);
     const auto& mxl = *reinterpret_cast<const CUtensorMap*>(m.x_low);
+    const auto& mo = *reinterpret_cast<const CUtensorMap*>(m.out);
     a.row_tiles = p.low_row_tiles;
     a.col_tiles = 1;
     a.splits = p.low_splits;
     a.nt = p.low_nt;
-    const cudaError_t e = p.low_grid ? launch_low<E, true>(ma, mxl, ma, a, p.low_grid, s)
-                                     : launch_k(k_adapter_rows<E>, dim3(a.R / AR_RANKS, a.n), dim3(AR_WARPS * 32), 0, s, a, r.x, r.ld_x, r.a);
+    const cudaError_t e = p.low_grid ? launch_low<E, true>(ma, mxl, ma, ma, a, p.low_grid, s)
+                                     : launch_rows<E>(a, r, s);
     if (e != cudaSuccess) return e;
     a.row_tiles = p.row_tiles;
     a.col_tiles = p.col_tiles;
     a.splits = p.splits;
     a.nt = p.nt;
-    return launch_low<E, false>(mw, mx, mb, a, p.grid, s);
+    return launch_low<E, false>(mw, mx, mb, mo, a, p.grid, s);
 }
 
 constexpr int AR_MOST = 1 << 23;                 // multiplications of k_adapter_rows at most
@@ -803,7 +835,7 @@ bool adapter_maps(const AdapterArgs& a, const AdapterPlan& p, const AdapterRows&
     const uint32_t wb[2] = {AD_BK, AD_M}, xb[2] = {AD_BK, (uint32_t)p.nt}, xl[2] = {AD_BK, (uint32_t)p.low_nt};
     const uint32_t ab[3] = {AD_BK, (uint32_t)a.R, 1}, bb[3] = {16, AD_M, 1};
     return encode_map_bf16(m.w, r.w, 2, wd, ws, wb) && encode_map_bf16(m.x, r.x, 2, xd, xs, xb) &&
-           encode_map_bf16_sw32(m.b, r.b, 3, bd, bs, bb) &&
+           encode_map_bf16_sw32(m.b, r.b, 3, bd, bs, bb) && encode_map_rows(m.out, a.out, a.out_f32, N, n, a.ld_out, AD_M, 16) &&
            (!p.low_grid || (encode_map_bf16(m.x_low, r.x, 2, xd, xs, xl) && encode_map_bf16(m.a, r.a, 3, ad, as, ab)));
 }
 

@@ -294,6 +294,14 @@ bool encode_map_bf16_sw32(void* out, const void* ptr, int rank, const uint64_t* 
     return encode_map_t(out, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
+bool encode_map_rows(void* out, const void* ptr, bool f32, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_cols,
+                     uint32_t box_rows) {
+    const uint64_t dims[2] = {cols, rows}, strides[1] = {ld * (f32 ? 4 : 2)};
+    const uint32_t box[2] = {box_cols, box_rows};
+    return encode_map_t(out, ptr, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dims, strides, box,
+                        CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 bool make_out_map(void* out, const void* ptr, int rows, int cols, int ld, bool f16) {
     if (rows <= 0 || cols <= 0 || cols > ld) return false;
     const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};

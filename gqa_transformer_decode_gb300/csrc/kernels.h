@@ -301,6 +301,9 @@ bool encode_map_bf16(void* out, const void* ptr, int rank, const uint64_t* dims,
 // The same with the 32-byte swizzle (boxes of 16 elements a row).
 bool encode_map_bf16_sw32(void* out, const void* ptr, int rank, const uint64_t* dims,
                           const uint64_t* strides, const uint32_t* box);
+// Rows of f32 or 16-bit elements, ld apart, not swizzled.
+bool encode_map_rows(void* out, const void* ptr, bool f32, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_cols,
+                     uint32_t box_rows);
 
 // m_rows: rows of A actually valid (<= p.M); the rest is ignored.
 void launch_gemm(const GemmPlan& p, int m_rows, const GemmEpilogue& e, int* status,
@@ -467,7 +470,7 @@ struct AdapterPlan {
     int low_nt, low_row_tiles, low_splits, low_grid;
 };
 struct AdapterMaps {
-    alignas(64) unsigned char w[128], x[128], x_low[128], a[128], b[128];
+    alignas(64) unsigned char w[128], x[128], x_low[128], a[128], b[128], out[128];
 };
 struct AdapterRows {
     const uint16_t *x, *w, *a, *b;   // [n][ld_x], [N][K], [n_adapters][R][K], [n_adapters][N][R]

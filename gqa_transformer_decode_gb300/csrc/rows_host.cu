@@ -75,7 +75,7 @@ ember_status ember_adapter_project(const ember_adapters* ad, const void* x, int6
     if (st != EMBER_OK) return st;
     if ((st = check_rows("x", x, ld_x, K)) != EMBER_OK) return st;
     if ((st = check_rows("out", out, ld_out, N)) != EMBER_OK) return st;
-    if (ld_x > (1ll << 36)) PG_FAIL(EMBER_ERR_UNSUPPORTED, "row stride of x > 2^36");
+    if (ld_x > (1ll << 36) || ld_out > (1ll << 36)) PG_FAIL(EMBER_ERR_UNSUPPORTED, "row stride of x or out > 2^36");
     if (!workspace || !aligned16(workspace)) PG_FAIL(EMBER_ERR_INVALID_ARG, "workspace must be given and 16-byte aligned");
     if (workspace_bytes < adapter_ws(n, ad->rank))
         PG_FAIL(EMBER_ERR_CAPACITY, "workspace smaller than ember_adapter_workspace");
