@@ -61,7 +61,7 @@ struct AdSmem {
     static constexpr int BARS = 32 * STAGES + 96;
     static constexpr int TOTAL = OFF_BAR + BARS + 1024;      // + alignment slack
     static_assert(TOTAL <= 232448, "shared memory of a CTA");
-    static_assert(STAGES * STAGE >= NT * AD_LD * 4, "the cluster's sums");
+    static_assert(STAGES * STAGE >= NT * AD_LD * 4, "the cluster's sums, the last tile's output");
 };
 
 // An adapter of a tile and the columns [c0, c1) of the tile, multiples of 16, that hold its rows.
@@ -526,7 +526,6 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     } else {   // ---------------- output, warps 2..5
         const int quad = warp & 3, tid = threadIdx.x - 64;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-        int slice = 0;
         for (int li = 0; li < tiles; ++li) {
             const int b = li & 1;
             const Tile t = tile_of(li);
@@ -554,11 +553,19 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                 }
                 break;
             }
-            if (!LOW) {   // slices of 16 rows of x through shared memory and TMA, two in turn
+            if (!LOW) {
+                // Through shared memory and TMA: while other tiles follow, slices of 16 rows of x, two
+                // in turn; the last tile at once over the stages, which nothing needs any more.
                 const int m = t.m0 + quad * 32 + lane;   // this thread's row of W
+                const bool last = li + 1 == tiles;
+                const int row_bytes = AD_M * (a.out_f32 ? 4 : 2);
                 float add = 0.f;
                 if (a.bias && m < a.N) add = E::bf16 ? bf16_to_f32(a.bias[m]) : __half2float(__ushort_as_half(a.bias[m]));
-                for (int c = 0; c < rows; c += 16, ++slice) {
+                auto put_out = [&](const uint8_t* buf, int c) {   // (clipped to what there is)
+                    tma_store_2d(&tmOut, buf, t.m0, t.row0 + c);
+                    bulk_commit();
+                };
+                for (int c = 0; c < rows; c += 16) {
                     uint32_t r[16];
                     tmem_ld16(acc + c, r);
                     tmem_ld_wait();
@@ -567,9 +574,11 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&acc_empty[b]);
                     }
-                    uint8_t* buf = sm + L::OFF_OUT + (slice & 1) * (16 * AD_M * 4);
-                    if (tid == 0) bulk_wait_read<1>();   // the slice before the last one has left
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    uint8_t* buf = last ? sm + c * row_bytes : sm + L::OFF_OUT + (c >> 4 & 1) * (16 * AD_M * 4);
+                    if (!last) {
+                        if (tid == 0) bulk_wait_read<1>();   // the slice before the last one has left
+                        asm volatile("bar.sync 1, 128;" ::: "memory");
+                    }
                     if (a.out_f32) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -579,12 +588,19 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                         for (int i = 0; i < 16; ++i)
                             reinterpret_cast<uint16_t*>(buf)[i * AD_M + quad * 32 + lane] = (uint16_t)E::pack(__uint_as_float(r[i]) + add, 0.f);
                     }
+                    if (!last) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        asm volatile("bar.sync 1, 128;" ::: "memory");
+                        if (tid == 0) put_out(buf, c);
+                    }
+                }
+                if (last) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     asm volatile("bar.sync 1, 128;" ::: "memory");
-                    if (tid == 0) {
-                        tma_store_2d(&tmOut, buf, t.m0, t.row0 + c);   // (clipped to what there is)
-                        bulk_commit();
-                    }
+                    if (tid == 0)
+                        for (int c = 0; c < rows; c += 16) put_out(sm + c * row_bytes, c);
+                } else if (tid == 0) {
+                    bulk_wait_read<0>();         // the next tile begins with the first slice's place again
                 }
                 continue;
             }
@@ -734,7 +750,8 @@ cudaError_t launch_nt(const CUtensorMap& w, const CUtensorMap& x, const CUtensor
                       int grid, cudaStream_t s) {
     constexpr int SMEM = AdSmem<NT, LOW>::TOTAL;
     auto k = k_adapter<E, NT, LOW>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    static OncePerDevice once;
+    const cudaError_t e = once([&] { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); });
     if (e != cudaSuccess) return e;
     if (a.splits > 1) return launch_cluster_k(k, dim3(grid), dim3(AD_THREADS), SMEM, a.splits, s, w, x, b, o, a);
     return launch_k(k, dim3(grid), dim3(AD_THREADS), SMEM, s, w, x, b, o, a);
@@ -752,7 +769,10 @@ cudaError_t launch_low(const CUtensorMap& w, const CUtensorMap& x, const CUtenso
 template <class E>
 cudaError_t launch_rows(const AdapterArgs& a, const AdapterRows& r, cudaStream_t s) {
     // an SM set to little shared memory takes no CTA of the second launch before this one's are gone
-    const cudaError_t e = cudaFuncSetAttribute(k_adapter_rows<E>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    static OncePerDevice once;
+    const cudaError_t e = once([] {
+        return cudaFuncSetAttribute(k_adapter_rows<E>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    });
     if (e != cudaSuccess) return e;
     return launch_k(k_adapter_rows<E>, dim3(a.R / AR_RANKS, a.n), dim3(AR_WARPS * 32), 0, s, a, r.x, r.ld_x, r.a);
 }
@@ -835,7 +855,7 @@ bool adapter_maps(const AdapterArgs& a, const AdapterPlan& p, const AdapterRows&
     const uint32_t wb[2] = {AD_BK, AD_M}, xb[2] = {AD_BK, (uint32_t)p.nt}, xl[2] = {AD_BK, (uint32_t)p.low_nt};
     const uint32_t ab[3] = {AD_BK, (uint32_t)a.R, 1}, bb[3] = {16, AD_M, 1};
     return encode_map_bf16(m.w, r.w, 2, wd, ws, wb) && encode_map_bf16(m.x, r.x, 2, xd, xs, xb) &&
-           encode_map_bf16_sw32(m.b, r.b, 3, bd, bs, bb) && encode_map_rows(m.out, a.out, a.out_f32, N, n, a.ld_out, AD_M, 16) &&
+           encode_map_bf16_sw32(m.b, r.b, 3, bd, bs, bb) && (p.splits > 1 || encode_map_rows(m.out, a.out, a.out_f32, N, n, a.ld_out, AD_M, 16)) &&
            (!p.low_grid || (encode_map_bf16(m.x_low, r.x, 2, xd, xs, xl) && encode_map_bf16(m.a, r.a, 3, ad, as, ab)));
 }
 

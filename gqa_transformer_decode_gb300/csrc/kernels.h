@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ember.h"
 
 namespace ember {
@@ -61,6 +63,25 @@ inline cudaError_t launch_cluster_k(void (*kern)(KArgs...), dim3 grid, dim3 bloc
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
+
+// Runs f, a setting of a kernel's, for the current device unless it has succeeded there before
+// (0.3 us a call otherwise).
+class OncePerDevice {
+    std::atomic<uint64_t> done_{0};
+
+public:
+    template <class F>
+    cudaError_t operator()(F f) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+        if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = f();
+        if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 // ---------------------------------------------------------------- embedding --
 // x[t] = f32(E[ids[t]]) and the per-token argument checks of a decode step

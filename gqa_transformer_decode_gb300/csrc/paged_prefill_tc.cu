@@ -1004,7 +1004,8 @@ template <class E, int DP>
 cudaError_t launch_shared(const PagedPrefillMaps& m, const PagedPrefillArgs& a, int sms, cudaStream_t s) {
     constexpr int SMEM = PtSmem<DP>::TOTAL;
     auto k = k_paged_prefill_tc<E, DP, PT_SHARED>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    static OncePerDevice once;
+    const cudaError_t e = once([&] { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); });
     if (e != cudaSuccess) return e;
     return launch_k(k, dim3(sms), dim3(PT_THREADS), SMEM, s, *reinterpret_cast<const CUtensorMap*>(m.q),
                     *reinterpret_cast<const CUtensorMap*>(m.k), *reinterpret_cast<const CUtensorMap*>(m.v), a);

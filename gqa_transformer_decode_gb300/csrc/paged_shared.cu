@@ -333,7 +333,8 @@ cudaError_t launch_ht(PagedDecodeArgs a, const PagedPrefillArgs& p, const PagedP
     cudaError_t e = launch_paged_shared(p, maps, sms, s);
     if (e != cudaSuccess) return e;
     auto k = k_shared_tail<E, DP, HT>;
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    static OncePerDevice once;
+    e = once([&] { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); });
     if (e != cudaSuccess) return e;
     e = launch_k(k, dim3(plan.grid), dim3(PD_THREADS), SMEM, s, a);
     if (e != cudaSuccess) return e;
