@@ -46,8 +46,8 @@ template <int NT, bool LOW>
 struct AdSmem {
     static constexpr int A_BYTES = AD_M * 128, X_BYTES = NT * 128, STAGE = A_BYTES + X_BYTES;
     // as many as fit, since W has to be on its way (five stages of 16 KB of W on 128 SMs, 2 us from
-    // asking to having: 5 TB/s); the first launch's leave room for a second CTA
-    static constexpr int STAGES = LOW ? (NT == 128 ? 3 : 4) : NT == 256 ? 4 : NT == 128 ? 6 : NT == 64 ? 8 : NT == 32 ? 9 : 10;
+    // asking to having: 5 TB/s); the first launch's small ones leave room for other CTAs
+    static constexpr int STAGES = LOW ? (NT == 128 ? 6 : 4) : NT == 256 ? 4 : NT == 128 ? 6 : NT == 64 ? 8 : NT == 32 ? 9 : 10;
     // an adapter's block in a stage: 16 ranks of 128 rows of B, and both terms of t's
     static constexpr int SLAB_A = AD_M * 32, SLAB_T = NT * 32, SLABS = STAGE / (SLAB_A + 2 * SLAB_T);
     static constexpr int OFF_T = SLABS * SLAB_A;
@@ -836,12 +836,13 @@ AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms) {
     p.low_nt = min((n + 15) & ~15, 128);
     p.low_row_tiles = (n + p.low_nt - 1) / p.low_nt;
     const int most = (min(n_adapters, p.low_nt) + AD_M / R - 1) / (AD_M / R);   // tiles of a row tile
+    // A CTA for each SM, but few rows' on those that the second launch leaves, since its CTAs then
+    // start at once.  How many adapters a row tile has is known on the device: its clusters share
+    // them out.
+    const int left = sms - p.grid, room = p.low_row_tiles == 1 && left >= 8 ? left : sms;
     p.low_splits = 1;
-    while (p.low_splits < 8 && nk >= 2 * p.low_splits) p.low_splits *= 2;
-    // Clusters of a row tile: how many adapters it has is known on the device.  Few rows: no more
-    // CTAs than the second launch leaves SMs, which then starts at once.
-    while (p.low_splits > 2 && p.low_row_tiles * most * p.low_splits > sms - p.grid && p.low_row_tiles * most * 2 <= sms - p.grid) p.low_splits /= 2;
-    const int clusters = max(1, min(most, sms / (p.low_splits * p.low_row_tiles)));
+    while (p.low_splits < 8 && nk >= 2 * p.low_splits && p.low_row_tiles * p.low_splits * 2 <= room) p.low_splits *= 2;
+    const int clusters = max(1, min(most, room / (p.low_splits * p.low_row_tiles)));
     p.low_grid = p.low_row_tiles * clusters * p.low_splits;
     return p;
 }
