@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             break;
         }
         if (SHARED) {   // the rows as they are; joined by another kernel
-            const bool store = live && p.slot < a.slots;
+            const bool store = live && (unsigned)p.slot < (unsigned)a.slots;
             float* own = store ? a.ws + a.ws_head + ((size_t)p.slot * (2 * PT_ROWS) + t * PT_ROWS + r) * D : nullptr;
             if (ok && nkt > 0) {
                 const int last = base + nkt - 1;

@@ -20,8 +20,8 @@
 // once for each (row, kv head), 64 rows of one block each on 8 kv heads took as long as 64 of 256
 // keys.
 //
-// Calls of little work read each row's keys once for each row instead (paged_decode.cu,
-// PD_SHARED), which is one launch.
+// Calls of little work, or of groups of one or two rows, read each row's keys once for each row
+// instead (paged_decode.cu, PD_SHARED), which is one launch.
 #include "paged_decode.cuh"
 #include "paged_groups.cuh"
 
@@ -49,7 +49,29 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_shared_tail(
     // before that one is then complete)
     int n[PD_SCAN];
     unsigned line = 0, before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32 * PD_SCAN) line += scan_chunk<KEYS, PD_TAIL>(a, b0, W == 0, n, before);
+    constexpr int CHUNK = 32 * PD_SCAN;
+    // One chunk of rows each warp scans for itself; of more, the warps take turns and hand each
+    // other the totals (1024 rows in 64 groups on 2 kv heads of 64: 35 us; all by itself 63).
+    const bool one = a.B <= CHUNK;
+    unsigned* totals = reinterpret_cast<unsigned*>(sm);
+    static_assert(4 * (65536 / CHUNK) <= L::RING, "65535 rows");
+    for (int c = one ? 0 : warp; c * CHUNK < a.B; c += PD_WARPS) {
+        // one warp of the grid: errors, and rows without blocks
+        const bool report = c % gridDim.x == blockIdx.x && (!one || warp == 0);
+        const unsigned t = scan_chunk<KEYS, PD_TAIL>(a, c * CHUNK, report, n, before);
+        if (one) line = t;
+        else if (lane == 0) totals[c] = t;
+        for (int e = 0; report && e < PD_SCAN; ++e) {
+            const int b = c * CHUNK + PD_SCAN * lane + e;
+            if (b < a.B && n[e] == 0)
+                for (int g = 0; g < NKV; ++g) record[(size_t)b * NKV + g] = make_int2(0, 0);
+        }
+    }
+    if (!one) {
+        __syncthreads();
+        for (int c = lane; c * CHUNK < a.B; c += 32) line += totals[c];
+        line = __reduce_add_sync(FULL_MASK, line);
+    }
     line *= NKV;
     // as many CTAs as have room on the SMs that the prefixes leave
     const PtGroups gs{a.groups, a.shared, a.prefixes, a.lens, a.n_groups, a.B, a.c.n_seqs, NKV, a.prefix_rows,
@@ -64,36 +86,34 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_shared_tail(
     const unsigned NW = PD_WARPS * (unsigned)per_sm * (beside < sms ? sms - beside : sms);
     const unsigned each = max(1u, (line + NW - 1) / NW);
     const unsigned lo = min(line, W * each), hi = min(line, lo + each);
-    for (int b = W; b < a.B; b += gridDim.x * PD_WARPS)   // rows without blocks
-        if (seq_blocks<KEYS, PD_TAIL>(a, b, false).n == 0)
-            for (int g = lane; g < NKV; g += 32) record[(size_t)b * NKV + g] = make_int2(0, 0);
-
+    int chunk = 0;                               // that the warp's share begins in
+    unsigned run = 0;
+    if (!one) {
+        if (lo < hi)
+            while (lo >= run + totals[chunk] * NKV) run += totals[chunk++] * NKV;
+        __syncthreads();                         // the ring may be filled
+    }
     if (lo < hi) {
         Place cur;
-        unsigned run = 0;
-        for (int b0 = 0;; b0 += 32 * PD_SCAN) {
-            // one chunk: its counts are still in the registers
-            const unsigned total = a.B <= 32 * PD_SCAN ? line / NKV : scan_chunk<KEYS, PD_TAIL>(a, b0, false, n, before);
-            if (lo < run + total * NKV) {
-                unsigned at = run + before * NKV, first = 0;
-                int b = -1;
+        if (!one)                                // (else its counts are still in the registers)
+            (void)scan_chunk<KEYS, PD_TAIL>(a, chunk * CHUNK, false, n, before);
+        {
+            unsigned at = run + before * NKV, first = 0;
+            int b = -1;
 #pragma unroll
-                for (int e = 0; e < PD_SCAN; ++e) {
-                    if (lo >= at && lo < at + (unsigned)n[e] * NKV) {
-                        b = b0 + PD_SCAN * lane + e;
-                        first = at;
-                    }
-                    at += (unsigned)n[e] * NKV;
+            for (int e = 0; e < PD_SCAN; ++e) {
+                if (lo >= at && lo < at + (unsigned)n[e] * NKV) {
+                    b = chunk * CHUNK + PD_SCAN * lane + e;
+                    first = at;
                 }
-                const int src = __ffs(__ballot_sync(FULL_MASK, b >= 0)) - 1;
-                cur.b = __shfl_sync(FULL_MASK, b, src);
-                cur.s = seq_blocks<KEYS, PD_TAIL>(a, cur.b, false);
-                const unsigned x = lo - __shfl_sync(FULL_MASK, first, src);
-                cur.g = (int)(x / (unsigned)cur.s.n);
-                cur.i = (int)(x - (unsigned)cur.g * (unsigned)cur.s.n);
-                break;
+                at += (unsigned)n[e] * NKV;
             }
-            run += total * NKV;
+            const int src = __ffs(__ballot_sync(FULL_MASK, b >= 0)) - 1;
+            cur.b = __shfl_sync(FULL_MASK, b, src);
+            cur.s = seq_blocks<KEYS, PD_TAIL>(a, cur.b, false);
+            const unsigned x = lo - __shfl_sync(FULL_MASK, first, src);
+            cur.g = (int)(x / (unsigned)cur.s.n);
+            cur.i = (int)(x - (unsigned)cur.g * (unsigned)cur.s.n);
         }
         auto next_pair = [&](Place& p) {         // (inside the line)
             p.i = 0;
@@ -203,11 +223,12 @@ __global__ void __launch_bounds__(SJ_THREADS) k_shared_join(PagedDecodeArgs a, i
     const int g = blockIdx.x, b = blockIdx.y;
     const int D = a.c.D, NKV = a.c.NKV, G = a.NH / NKV;
     // What the call got may be read before the wait (the kernels before began after it was complete).
-    const SeqBlocks s = seq_blocks<16, PD_TAIL>(a, b, false);
-    int pi = 0, at = 0, group = 0;               // the pair of row tiles among its group's, the row in it
+    int row[1] = {b}, of[1];
+    find_groups(a, row, of);
+    const int group = of[0];
+    const SeqBlocks s = seq_blocks<16, PD_TAIL>(a, b, a.seqs ? a.seqs[b] : b, a.lens[b], group, false);
+    int pi = 0, at = 0;                          // the pair of row tiles among its group's, the row in it
     if (s.zero && s.from > 0) {
-        int from, prefix;
-        shared_prefix(a, b, from, prefix, group);
         const int row0 = a.groups[group], nx = (a.groups[group + 1] - row0 + a.prefix_rows - 1) / a.prefix_rows;
         const int i = b - row0, r = i % a.prefix_rows, half = a.prefix_rows / 2;
         pi = g * nx + i / a.prefix_rows;
@@ -305,8 +326,13 @@ __global__ void __launch_bounds__(SJ_THREADS) k_shared_join(PagedDecodeArgs a, i
     }
 }
 
-// Bytes of keys and values, read once for each row, up to which a call does just that.
+// A call reads each row's keys once for each row (paged_decode.cu, PD_SHARED) up to so many bytes of
+// keys and values, and with fewer than three rows a group on average: 64 rows of 4096 shared and
+// 200 own keys on 8 kv heads of 128 take 150 us so, apart 108 in groups of 2 and 81 in groups of 3;
+// but 1024 rows of 256 and 64 keys 258 so, apart 413 in groups of 2, 234 of 3 and 190 of 4, with a
+// gigabyte of partials.
 constexpr double PD_TOGETHER = 32e6;
+constexpr int PD_APART_ROWS = 3;
 
 struct SharedPlan {
     bool apart;                                  // the prefixes by themselves
@@ -318,7 +344,7 @@ SharedPlan shared_plan(const PagedView& c, int B, int NH, int n_groups, int sms)
     SharedPlan p{};
     const int G = NH / c.NKV;
     const long long keys = (long long)c.width << c.page_shift;
-    p.apart = (double)B * c.NKV * keys * c.D * 4 > PD_TOGETHER;
+    p.apart = (double)B * c.NKV * keys * c.D * 4 > PD_TOGETHER && n_groups <= B / PD_APART_ROWS;
     p.grid = sms * pd_ctas_per_sm(G <= 8 ? 1 : 2);
     p.tail_floats = ((2 * (size_t)B * c.NKV + 3) & ~(size_t)3) + ((size_t)B * c.NKV + (size_t)p.grid * PD_WARPS) * G * (c.D + 2);
     p.tail_floats = (p.tail_floats + 3) & ~(size_t)3;

@@ -308,9 +308,9 @@ typedef enum ember_dtype { EMBER_F32 = 0, EMBER_BF16 = 1, EMBER_F16 = 2 } ember_
  * weight; a row of nothing else is uniform, as in ember_sample.  In a row with a
  * NaN or +inf every log probability and the entropy are NaN; NaN counts as the
  * largest logit.  The order is that of the logits themselves, whatever the
- * temperature (1e-6 to 1e6) rounds together.  Distances between logits beyond 1e30
- * count as 1e30.  Arithmetic is
- * f32; equal calls give equal bits.  Asynchronous on `stream`; allocates nothing.
+ * temperature (1e-6 to 1e6) rounds together.  For the entropy distances between
+ * logits beyond 1e30 count as 1e30; a log probability beyond f32's range is -inf.
+ * Arithmetic is f32; equal calls give equal bits.  Asynchronous on `stream`; allocates nothing.
  * Host errors: INVALID_ARG, UNSUPPORTED (top), CUDA. */
 #define EMBER_LOGPROBS_MAX_TOP 32
 ember_status ember_logprobs(const void *logits, int32_t dtype, int32_t n, int32_t V, int64_t ldl,

@@ -219,3 +219,42 @@ def test_refusals():
         c.run()
     with torch.no_grad():
         c.run()
+
+
+def test_offsets_beyond_2_31():
+    """Rows far apart, in x and in out: 64-bit offsets in both launches and every form of the output."""
+    for n, R in ((3, 16), (200, 64)):
+        far = (1 << 31) // n + 64
+        far -= far % 8
+        c = Case(n, 136, 64, R, 3)
+        base = torch.empty((n - 1) * far + 200, dtype=torch.bfloat16, device="cuda")
+        x = torch.as_strided(base, (n, 64), (far, 1))
+        x.copy_(c.x)
+        out = torch.as_strided(base, (n, 136), (far, 1), 64)
+        want = c.run()
+        c.x = x
+        assert torch.equal(c.run(out=out), want)
+
+
+def test_calls_that_share_a_workspace_in_turn():
+    c, d = Case(20, 256, 512, 16, 4), Case(300, 256, 512, 16, 4, seed=9)
+    ws = torch.empty(d.ad.workspace_bytes(300), dtype=torch.uint8, device="cuda").fill_(0x7f)
+    want = [c.run(), d.run()]
+    for _ in range(10):
+        assert torch.equal(c.run(workspace=ws), want[0]) and torch.equal(d.run(workspace=ws), want[1])
+
+
+def test_status_word_and_inputs_outlive_a_call_on_another_stream():
+    c = Case(64, 512, 512, 16, 4)
+    want = c.run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    x, ids = c.x.clone(), c.ids.clone()
+    torch.cuda.current_stream().synchronize()
+    y = c.ad.project(x, c.w, ids, stream=side)
+    del x, ids
+    junk = [torch.full((64, 512), 9.0, device="cuda").bfloat16() for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and len(junk) == 4

@@ -42,6 +42,8 @@ def check(logits, ids, top, t, got):
 
         def near(a, want, tol):
             a = float(a)
+            if abs(want) > 2.0 ** 128:  # beyond f32, whose nearest value is infinite: a lowest logit at a temperature below 1
+                want = np.copysign(np.inf, want)
             if not np.isfinite(want):
                 assert (np.isnan(a) and np.isnan(want)) or a == want, (r, a, want)
             else:
@@ -209,3 +211,29 @@ def test_refusals():
             bad()
     with torch.no_grad():
         logprobs(x.clone().requires_grad_(), ids)
+
+
+def test_rows_beyond_2_31_elements():
+    """Offsets of 64 bits: the last of 16800 rows of 128256 bf16 (4.3 GB)."""
+    n, V = 16800, 128256
+    x = torch.empty(n, V, dtype=torch.bfloat16, device="cuda").fill_(-3.0)
+    few, ids = rows(3, V, "bf16", 8)
+    x[-3:] = few
+    all_ids = torch.zeros(n, dtype=torch.int32, device="cuda")
+    all_ids[-3:] = ids
+    got = logprobs(x, all_ids, top=5)
+    check(few, ids, 5, 1.0, type(got)(*(y[-3:] for y in got)))
+    assert got.top_ids[0].tolist() == [0, 1, 2, 3, 4] and got.entropy[7].item() == pytest.approx(np.log(V), rel=1e-6)
+
+
+def test_masks_of_the_types_lowest_value():
+    """A grammar's mask: a handful of tokens, all others at the type's lowest value or -inf, in one call with open rows."""
+    for dtype in TYPES:
+        x, ids = rows(40, 32000, dtype, 6)
+        for r in range(0, 40, 3):
+            keep = torch.randperm(32000, generator=torch.Generator().manual_seed(r))[:1 + r // 3].cuda()
+            kept = x[r, keep].clone()
+            x[r] = torch.finfo(x.dtype).min if r % 2 else float("-inf")
+            x[r, keep] = kept
+        check(x, ids, 20, 1.0, logprobs(x, ids, top=20))
+        check(x, ids, 3, 0.5, logprobs(x, ids, top=3, temperature=0.5))

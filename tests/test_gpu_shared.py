@@ -269,3 +269,37 @@ def test_refusals():
         with pytest.raises((ValueError, TypeError, RuntimeError), match=err):
             bad()
     assert run(q[:0], lens[:0], ints([0]), shared[:0], prefixes[:0]).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("NH,NKV,D,n_groups,per", [(14, 2, 64, 100, 13), (8, 8, 128, 40, 33), (4, 2, 64, 700, 2)])
+def test_many_rows_in_many_groups(NH, NKV, D, n_groups, per):
+    """Batches of several chunks of rows, groups found among many; two rows a group read their keys each for itself."""
+    g = np.random.default_rng(n_groups)
+    groups = []
+    for i in range(n_groups):
+        s = int(g.integers(0, 300))
+        groups.append((s, [int(s + g.integers(-s // 4, 60)) if g.random() < 0.9 else 0 for _ in range(int(g.integers(0, 2 * per + 1)))]))
+    p = Shared([(s, [max(0, n) for n in lens]) for s, lens in groups], NKV, D, 16, extra_width=40)
+    q = p.queries(NH)
+    out, lse = p.run(q, return_lse=True)
+    n = len(p.lens)
+    p.check(q, out, lse, rows=set(range(0, n, max(1, n // 150))) | {n - 1})
+    minus, lse = p.run(q, return_lse=True, scale=-0.2)
+    p.check(q, minus, lse, rows=set(range(0, n, max(1, n // 40))), scale=-0.2)
+
+
+def test_groups_out_of_order_touch_nothing():
+    """What the header forbids and only the device can see: no row outside the call's buffers is written, and rows of
+    groups that are in order before it are right."""
+    p = Shared([(200, [220 + i for i in range(60)]), (300, [310 + i for i in range(90)]), (64, [70] * 50)], 2, 64, 16, extra_width=4000)
+    q = p.queries(8)
+    lens, cu, sh, pre = p.args
+    n = len(p.lens)
+    buf = torch.full((n + 2, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    for bad in ([0, 60, 20, 200], [0, 60, 900, 200], [0, -5, 150, 200], [5, 60, 150, 200], [0, 60, 150, 180]):
+        ws = torch.full((p.cache.shared_workspace_bytes(n, 8, 3) + 256,), 0x5a, dtype=torch.uint8, device="cuda")
+        p.cache.decode_shared(q, lens, ints(bad), sh, pre, seqs=p.seqs, out=buf[1:-1], workspace=ws[:-256])
+        assert (buf[0] == 7).all() and (buf[-1] == 7).all() and (ws[-256:] == 0x5a).all()
+        assert p.cache.sync_status() == 1
+    out = p.run(q)
+    p.check(q, out, None, rows={0, 61, n - 1})
