@@ -258,3 +258,13 @@ def test_status_word_and_inputs_outlive_a_call_on_another_stream():
     junk = [torch.full((64, 512), 9.0, device="cuda").bfloat16() for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(y, want) and len(junk) == 4
+
+
+def test_forms_of_the_first_launch():
+    """A x of few rows with and without tensor cores (n rank K either side of 2^23), more adapters than rows, rows of a
+    tile that all name different adapters, one adapter for all of many rows."""
+    for n, N, K, R, A in ((64, 128, 2048, 64, 3), (64, 128, 2056, 64, 3), (65, 128, 64, 8, 200), (300, 264, 512, 8, 300),
+                          (257, 128, 4096, 32, 1), (16, 1024, 8192, 128, 16), (33, 8, 8, 8, 40)):
+        c = Case(n, N, K, R, A, ids=np.random.default_rng(n).permutation(max(n, A))[:n] % A)
+        c.check(c.run())
+        c.check(c.run(out_dtype=torch.float32))
