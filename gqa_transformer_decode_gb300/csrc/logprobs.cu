@@ -210,29 +210,28 @@ __device__ __noinline__ Sums join_all(Sums q, float c2, Sums* s_sums) {
     return join_lanes<T / 32>(s_sums[lane % (T / 32)], c2);
 }
 
-// A lower bound of the top-th largest logit from the groups' maxima as they are (each a
-// lower bound of what it will be); g: this thread's maximum.  By a whole warp.  The top-th
-// largest maximum is the best such bound; on the way, beyond the eighth, the least of all, which
-// takes one reduction, costs less than the longer list that it lets in.
+// Leaves the maximum of this thread's group so far, from g, the thread's.
 template <int T>
-__device__ __noinline__ float raise_bound(float g, float* s_group, int top, bool best) {
+__device__ __forceinline__ void leave_maximum(float g, float* s_group) {
     constexpr int GROUP = T / 32;
-    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < GROUP; o <<= 1) g = fmaxf(g, __shfl_xor_sync(FULL_MASK, g, o));
-    volatile float* group = s_group;
-    if (lane % GROUP == 0) group[threadIdx.x / GROUP] = g;
-    __syncwarp();
-    // the values' order as unsigned numbers, the lane below them (1: -inf or none)
-    uint32_t v = (uint32_t)(argmax_key(group[lane], 0u) >> 32);
-    uint32_t k = __reduce_min_sync(FULL_MASK, v);
-    if (top <= 8 || (best && top < 32))
-        for (int i = 0; i < top; ++i) {
-            k = __reduce_max_sync(FULL_MASK, v);
-            const unsigned at = __ballot_sync(FULL_MASK, v == k);
-            if (lane == __ffs(at) - 1) v = 0;
+    if (threadIdx.x % GROUP == 0) *(volatile float*)(s_group + threadIdx.x / GROUP) = g;
+}
+// A lower bound of the top-th largest logit from the groups' maxima as they are (each a
+// lower bound of what it will be): the top-th largest of them, sorted by a whole warp.
+__device__ __noinline__ float raised_bound(const float* s_group, int top) {
+    const int lane = threadIdx.x & 31;
+    float v = *(const volatile float*)(s_group + lane);
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int o = size / 2; o > 0; o >>= 1) {
+            const float y = __shfl_xor_sync(FULL_MASK, v, o);
+            const bool larger = ((lane & o) == 0) == ((lane & size) == 0);   // of the two goes to the lower lane, in the end
+            v = larger ? fmaxf(v, y) : fminf(v, y);
         }
-    return fmaxf(LP_LOW, __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k));
+    return fmaxf(LP_LOW, __shfl_sync(FULL_MASK, v, top - 1));
 }
 
 // Puts each key of s_keys[0 .. n) that is among the `top` largest into its place: the number of
@@ -354,7 +353,7 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
     Sums q{LP_LOW, 0.f, 0.f, 0};
     bool nan = false;
     float bound = LP_LOW;                        // of the top-th largest logit, from below
-    auto raise = [&](float g, bool best) { bound = raise_bound<T>(g, s_group, top, best); };
+    auto raise = [&]() { bound = raised_bound(s_group, top); };
     // Lists element i of value x if it may be among the largest.
     auto list = [&](float x, int i) {
         if (!(x >= bound && x > LP_LOW)) return;
@@ -385,9 +384,9 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
         float g = LP_LOW;
 #pragma unroll
         for (int k = 0; k < LP_AHEAD; ++k) g = fmaxf(g, L::largest(next[k]));   // (a NaN is left out here, and found below)
-        raise(g, false);
+        leave_maximum<T>(g, s_group);
         __syncthreads();
-        raise(g, false);
+        raise();
         q.m = g;
     }
     const uint64_t k2 = pair(c2, c2);
@@ -453,7 +452,11 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
         const float2 s1 = halves(s), u1 = halves(u);
         q.s += s1.x + s1.y;
         q.u += u1.x + u1.y;
-        if (top > 0 && __any_sync(FULL_MASK, listed)) raise(q.m, false);
+        if (top > 0 && __any_sync(FULL_MASK, listed)) {
+            leave_maximum<T>(q.m, s_group);
+            __syncwarp();
+            raise();
+        }
     }
     if (has_end) {
         const float v = max_nan(x_end, LP_LOW);
@@ -466,14 +469,13 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
         q.u = fmaf(p, d, q.u);
     }
     if (nan) s_nan = 1;
-    const float largest = q.m;                   // of this thread
-    if (top > 0) raise(largest, false);
+    if (top > 0) leave_maximum<T>(q.m, s_group);
     q = join_all<T>(q, c2, s_sums);
 
     // ---- this part's largest above LP_LOW, in order ----
     const int i_lo = max(0, first + lo * VEC), i_hi = (int)min((long long)a.V, first + (long long)hi * VEC);
     if (top > 0) {
-        raise(largest, true);
+        raise();                                 // (of the whole part)
         const int hits = s_hits;
         if (hits <= LP_HITS)
             for (int h = tid; h < hits; h += T) {
