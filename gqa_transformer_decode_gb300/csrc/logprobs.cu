@@ -347,7 +347,6 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
     const int id = a.ids ? a.ids[r] : -1;
     const bool given = id >= 0 && id < a.V;
     const float xi = given ? L::one(row[id]) : 0.f;
-    const bool count_fast = given && xi > LP_LOW;
     const int jid = given ? (id - first) / VEC : -1;                               // its vector
 
     Sums q{LP_LOW, 0.f, 0.f, 0};
@@ -363,7 +362,9 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
     // The same in the batch that the given token's vector lies in or stands between.
     auto count_around = [&](const uint4 (&w)[LP_AHEAD], int j) {
 #pragma unroll
-        for (int k = 0; k < LP_AHEAD; ++k) q.above += j + k * T < jid ? L::template above<true>(w[k], xi) : L::template above<false>(w[k], xi);
+        for (int k = 0; k < LP_AHEAD; ++k)
+            if (j + k * T < whole_hi)            // (-inf stands beyond the part, which may equal xi)
+                q.above += j + k * T < jid ? L::template above<true>(w[k], xi) : L::template above<false>(w[k], xi);
         if ((jid - j) % T == 0 && jid >= whole_lo && jid < whole_hi)   // its own vector: equal ones before it (read again)
             for (int i = first + jid * VEC; i < id; ++i) q.above += L::one(row[i]) == xi;
     };
@@ -412,8 +413,8 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
             if (most > q.m) q.move(most, c2);
         }
         const int j = j0 + tid;
-        if (count_fast && most >= xi) {          // larger ones, before the given token equal ones too
-            if (j + (LP_AHEAD - 1) * T < jid) {
+        if (given && most >= xi) {               // larger ones, before the given token equal ones too
+            if (j + (LP_AHEAD - 1) * T < min(jid, whole_hi)) {
 #pragma unroll
                 for (int k = 0; k < LP_AHEAD; ++k) q.above += L::template above<true>(w[k], xi);
             } else if (j > jid) {
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
         const float v = max_nan(x_end, LP_LOW);
         if (v != v) nan = true;
         else if (v > q.m) q.move(v, c2);
-        if (count_fast) q.above += v > xi || (v == xi && i_end < id);
+        if (given) q.above += x_end > xi || (x_end == xi && i_end < id);
         if (top > 0) list(v, i_end);
         const float d = v - q.m, p = ex2(d * c2);
         q.s += p;
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(T, lp_per_sm(T)) k_logprobs(LogprobsArgs a) {
 
     // ---- what the fast pass leaves out ----
     const bool has_nan = s_nan != 0;
-    if (has_nan || !(q.m > LP_LOW && q.m < -LP_LOW) || (given && !count_fast))
+    if (has_nan || !(q.m > LP_LOW && q.m < -LP_LOW))
         q = sum_slowly<L, T>(row, 0, a.V, given ? id : -1, xi, c2, s_sums);
     else if (given)
         q.above -= id;                           // (sum_slowly's count)

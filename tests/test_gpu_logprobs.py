@@ -237,3 +237,23 @@ def test_masks_of_the_types_lowest_value():
             x[r, keep] = kept
         check(x, ids, 20, 1.0, logprobs(x, ids, top=20))
         check(x, ids, 3, 0.5, logprobs(x, ids, top=3, temperature=0.5))
+
+
+@pytest.mark.parametrize("n", [3, 40, 200])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_given_tokens_that_a_mask_excludes(dtype, n):
+    """-inf and the lowest value as the given token's logit: its rank counts the equal ones before it, in every part of a
+    row, in the row's ends and beside what stands for vectors beyond a part."""
+    V = 33001
+    x, _ = rows(n, V, dtype, 11, pad=3, offset=1)
+    g = torch.Generator().manual_seed(n)
+    for r in range(n):
+        keep = torch.rand(V, generator=g) < (0.5, 0.01, 0.999)[r % 3]
+        x[r, ~keep.cuda()] = float("-inf") if r % 2 else torch.finfo(x.dtype).min
+    ids = torch.randint(V, (n,), generator=g)
+    ids[::5], ids[1::5], ids[2::5] = 0, V - 1, V - 2
+    for r in range(0, n, 2):
+        x[r, ids[r]] = x[r].min()
+    few = list(range(0, n, max(1, n // 24)))
+    got = logprobs(x, ids.int().cuda(), top=6)
+    check(x[few], ids[few].int(), 6, 1.0, type(got)(*(y[few] for y in got)))
