@@ -2,11 +2,12 @@
 // row's own beside it:  y_i = W x_i + bias + s_a B_a (A_a x_i),  a = ids[i].
 //
 // Bound: for few rows the bytes of W and of the adapters that the rows name, for many rows
-// the products.  Two launches: the first takes t_i = s_a A_a x_i (k_adapter<.., true>), the
-// second y (k_adapter<.., false>); the second starts with the first and streams W and x
-// meanwhile, and waits for t only when it has come to the adapters.
+// the products.  Two launches: the first takes t_i = s_a A_a x_i (k_adapter<.., true>, for
+// little work k_adapter_rows), the second y (k_adapter<.., false>); the second starts with
+// the first and streams W and x meanwhile, and waits for t only when it has come to the
+// adapters.
 //
-// Both are the same tcgen05 kernel.  A tile is 128 rows of W (or the R rows of one A_a) by
+// k_adapter is one tcgen05 kernel for both.  A tile is 128 rows of W (or the R rows of one A_a) by
 // up to NT rows of x: the weights are the M = 128 operand, so that a few rows of x waste no
 // tensor work and W streams through at the memory's rate.  The adapters of a tile's rows
 // are further blocks along K: B_a's 128 rows against t, where t stands as zeros for the
@@ -690,15 +691,15 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
     }
 }
 
-// The first launch for few rows: a CTA for eight ranks of a row, its warps for a part of K each.
-// No list of adapters, no tensor memory, no cluster: one row on rank 8 has t 2 us sooner, and what
-// it costs beyond that (A is read for each row that names it, from L2) few rows do not notice.
+// The first launch for little work: a CTA for eight ranks of a row, its warps for a part of K each.
+// No list of adapters, no tensor memory, no cluster: one row on rank 8 has t 2 us sooner.  A is
+// read for each row that names it, from L2, which is what bounds it: 2 n R K bytes.
 constexpr int AR_WARPS = 4, AR_RANKS = 8;
 template <class E>
 __global__ void __launch_bounds__(AR_WARPS * 32) k_adapter_rows(AdapterArgs a, const uint16_t* x, long long ld_x, const uint16_t* la) {
     __shared__ float s_sum[AR_WARPS][AR_RANKS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r = blockIdx.x * AR_RANKS, row = blockIdx.y;
+    const int groups = a.R / AR_RANKS, row = (int)(blockIdx.x / groups), r = (int)(blockIdx.x % groups) * AR_RANKS;
     pdl_wait();
     pdl_trigger();
     const int id = a.ids[row];
@@ -774,7 +775,7 @@ cudaError_t launch_rows(const AdapterArgs& a, const AdapterRows& r, cudaStream_t
         return cudaFuncSetAttribute(k_adapter_rows<E>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     });
     if (e != cudaSuccess) return e;
-    return launch_k(k_adapter_rows<E>, dim3(a.R / AR_RANKS, a.n), dim3(AR_WARPS * 32), 0, s, a, r.x, r.ld_x, r.a);
+    return launch_k(k_adapter_rows<E>, dim3((unsigned)a.n * (a.R / AR_RANKS)), dim3(AR_WARPS * 32), 0, s, a, r.x, r.ld_x, r.a);
 }
 template <class E>
 cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& p, const AdapterRows& r, cudaStream_t s) {
@@ -798,7 +799,12 @@ cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& 
     return launch_low<E, false>(mw, mx, mb, mo, a, p.grid, s);
 }
 
-constexpr int AR_MOST = 1 << 23;                 // multiplications of k_adapter_rows at most
+// Multiplications n R K of k_adapter_rows at most, twice as many from 16 adapters on, since the
+// tcgen05 kernel has a tile for every two (rank 64) that a row tile names, whatever their rows.  On
+// 4096 inputs and outputs (bf16, rows in any order), by rows and with tcgen05: 64 rows of rank 32 on
+// 40 adapters 16 and 36 us; 128 rows of rank 64 on 8 adapters (2^25) 22 and 28; 256 rows of rank 64
+// (2^26) on 2 adapters 35 and 30, on 8 43 and 44, on 32 59 and 69; twice that on 8 adapters 56 and 51.
+constexpr int AR_MOST = 1 << 25, AR_ADAPTERS = 16;
 
 // Cycles of a block's products, 4 of M = 128, N = nt, K = 16: no less than 112 each.
 int block_cycles(int nt) { return max(450, nt * 8 / 3); }
@@ -831,18 +837,15 @@ AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms) {
         }
         if (rt == 1) break;
     }
-    // One row at a time while that is little work: 64 rows of rank 16 on 2048 inputs.
-    if (n <= 64 && (double)n * R * K <= (double)AR_MOST) return p;
+    if ((double)n * R * K <= (double)AR_MOST * (min(n_adapters, n) >= AR_ADAPTERS ? 2 : 1)) return p;
     p.low_nt = min((n + 15) & ~15, 128);
     p.low_row_tiles = (n + p.low_nt - 1) / p.low_nt;
     const int most = (min(n_adapters, p.low_nt) + AD_M / R - 1) / (AD_M / R);   // tiles of a row tile
-    // A CTA for each SM, but few rows' on those that the second launch leaves, since its CTAs then
-    // start at once.  How many adapters a row tile has is known on the device: its clusters share
+    // A CTA for each SM.  How many adapters a row tile has is known on the device: its clusters share
     // them out.
-    const int left = sms - p.grid, room = p.low_row_tiles == 1 && left >= 8 ? left : sms;
     p.low_splits = 1;
-    while (p.low_splits < 8 && nk >= 2 * p.low_splits && p.low_row_tiles * p.low_splits * 2 <= room) p.low_splits *= 2;
-    const int clusters = max(1, min(most, room / (p.low_splits * p.low_row_tiles)));
+    while (p.low_splits < 8 && nk >= 2 * p.low_splits && p.low_row_tiles * p.low_splits * 2 <= sms) p.low_splits *= 2;
+    const int clusters = max(1, min(most, sms / (p.low_splits * p.low_row_tiles)));
     p.low_grid = p.low_row_tiles * clusters * p.low_splits;
     return p;
 }

@@ -261,10 +261,42 @@ def test_status_word_and_inputs_outlive_a_call_on_another_stream():
 
 
 def test_forms_of_the_first_launch():
-    """A x of few rows with and without tensor cores (n rank K either side of 2^23), more adapters than rows, rows of a
-    tile that all name different adapters, one adapter for all of many rows."""
+    """More adapters than rows, rows of a tile that all name different adapters, one adapter for all of many rows."""
     for n, N, K, R, A in ((64, 128, 2048, 64, 3), (64, 128, 2056, 64, 3), (65, 128, 64, 8, 200), (300, 264, 512, 8, 300),
                           (257, 128, 4096, 32, 1), (16, 1024, 8192, 128, 16), (33, 8, 8, 8, 40)):
         c = Case(n, N, K, R, A, ids=np.random.default_rng(n).permutation(max(n, A))[:n] % A)
         c.check(c.run())
         c.check(c.run(out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("n,N,K,R,A", [
+    (5, 72, 65544, 128, 3), (16, 128, 40968, 128, 40), (33, 136, 16456, 128, 5), (64, 64, 16384, 64, 2), (100, 200, 9000, 56, 4),
+    (128, 128, 8200, 72, 3), (129, 136, 8192, 40, 7), (300, 128, 2056, 64, 8), (300, 64, 4104, 128, 300), (1030, 264, 1032, 64, 12),
+    (2100, 128, 520, 128, 60), (4100, 72, 1096, 16, 1),
+])
+def test_the_first_launch_on_tensor_cores(dtype, n, N, K, R, A):
+    """Enough multiplications (2^25, 2^26 from 16 adapters on) that A x goes on tcgen05: each width of its tiles, several
+    row tiles, K split over clusters of every size, runs of rows, rows in any order and without adapters."""
+    assert n * R * K > (1 << 25) * (2 if min(n, A) >= 16 else 1)
+    g = np.random.default_rng(n)
+    for ids in (g.integers(-1, A, n), np.sort(g.integers(0, A, n)), np.full(n, A - 1), np.where(g.random(n) < 0.02, 0, -1)):
+        c = Case(n, N, K, R, A, dtype, ids=ids)
+        y = c.run()
+        c.check(y)
+        assert torch.equal(c.run(), y)
+
+
+def test_errors_of_the_first_launch_on_tensor_cores():
+    c = Case(300, 128, 2056, 64, 8)
+    ids = c.ids.clone()
+    ids[7], ids[200] = 8, 1 << 30
+    y = c.ad.project(c.x, c.w, ids)
+    assert c.ad.sync_status() == 1
+    c.ids = torch.where(ids >= 8, -1, ids)
+    c.check(y)
+    c = Case(300, 128, 2056, 64, 8, "f16")
+    c.ad = adapters(c.a, c.b, torch.full((8,), 1e5, device="cuda"))
+    c.ids[:] = 3
+    y = c.run()
+    assert c.ad.sync_status() == 9 and not torch.isfinite(y).all()
