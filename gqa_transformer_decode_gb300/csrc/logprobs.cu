@@ -29,8 +29,8 @@ namespace ember {
 namespace {
 
 // Threads of a CTA, T: 512 while the rows are few, whose ends (joining, ordering) then take half the
-// time (64 rows of 128256 f32, top 20: 18.6 us, with 256 21.4), else 256, whose rows end one under
-// another's loads (2048 rows of 151936 bf16, top 10: 143 us, with 512 164).  1024 threads of an SM either way.
+// time (64 rows of 128256 f32, top 20: 18.0 us, with 256 20.9), else 256, whose rows end one under
+// another's loads (2048 rows of 151936 bf16, top 10: 143 us, with 512 167).  1024 threads of an SM either way.
 constexpr int lp_per_sm(int T) { return 1024 / T; }
 constexpr int LP_AHEAD = 4;                     // vectors of 16 bytes in flight for each thread
 constexpr int LP_TOP = EMBER_LOGPROBS_MAX_TOP;

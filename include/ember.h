@@ -336,8 +336,10 @@ ember_status ember_logprobs(const void *logits, int32_t dtype, int32_t n, int32_
  *   status: as for the paged operators below; INVALID_ARG for an id >= n_adapters
  *        (the row then goes without adapter), RANGE for f16 where an element of
  *        s_a A_a x lies beyond the type's range (its row is then not finite), TIMEOUT.
- * Products are taken on the type and summed in f32; s_a A_a x is held as the sum of
- * two values of the type (2^-17 relative for bf16, 2^-22 or 2^-25 absolute for f16).
+ * Products are taken on the type and summed in f32 by the tensor cores (off by 1.3e-6
+ * of the outputs' norm at K 1024, where sums rounded to nearest are by 0.6e-6);
+ * s_a A_a x is held as the sum of two values of the type (2^-17 relative for bf16,
+ * 2^-22 or 2^-25 absolute for f16).
  * Element pointers are 16-byte aligned, scale, ids and status 4-byte; row strides
  * multiples of 8 elements; buffers may not overlap.  A b that is not finite makes
  * not finite not only the rows that name its adapter but also rows with others
@@ -359,10 +361,10 @@ ember_status ember_adapter_project(const ember_adapters *ad, const void *x, int6
 
 /* ---- paged key/value cache ------------------------------------------------ */
 
-/* Three operators on one pool of K/V pages that many sequences share, for a
+/* Four operators on one pool of K/V pages that many sequences share, for a
  * serving loop whose sequences grow, end and are replaced: new tokens' rows go
- * in with ember_paged_append, and ember_paged_decode / ember_paged_prefill
- * attend over them.  They are stateless like ember_sample: the pool, the page
+ * in with ember_paged_append, and ember_paged_decode, ember_paged_decode_shared
+ * (for sequences that share a prefix) and ember_paged_prefill attend over them.  They are stateless like ember_sample: the pool, the page
  * table and every other buffer are the caller's, nothing is kept, and they
  * compose on one stream with any other call.  (The cache of ember_kv_alloc --
  * "ember internals", "kv cache" -- is one block of max_len rows per sequence;
@@ -404,7 +406,8 @@ ember_status ember_adapter_project(const ember_adapters *ad, const void *x, int6
  *     or with a scale that is not positive, take it as the sum of two values of the
  *     cache's type (2^-16 relative for bf16, 2^-22 for f16), other prefill as one
  *     (2^-8, 2^-11: about the output's own rounding); f16's is at least 2^-32 of the
- *     largest weight of its row.
+ *     largest weight of its row.  decode_shared: two terms, but one for the keys of
+ *     prefixes that are multiplied for their whole group (large calls).
  *   - B is at most 65535.  No operator has a gradient.
  *   - Buffers and the stream belong to the current device; buffers may not
  *     overlap, except that pages may be shared by the tables of sequences
@@ -472,7 +475,11 @@ ember_status ember_paged_decode(const ember_paged_kv *kv, const void *q, int64_t
  * row's (seqs[b]).  shared [n_groups] is any number, whole pages or not, and may
  * exceed a row's lens[b]; entries of a row's own pages that hold only shared keys
  * are not read.  Every key is seen: there is no window.  What the rows of a group
- * read together is read once for all of them; n_groups is at most B.
+ * read together is read once for all of them; n_groups is at most B.  Calls of few
+ * keys (by the table's width), of fewer than three rows a group on average or with a
+ * scale that is not positive read a row's keys for each row, with the same result up
+ * to rounding.  As in prefill, a K or V value of a prefix that is not finite may make
+ * its whole group not finite.
  * A row outside every group, a prefixes entry outside [0, n_seqs) and a shared entry
  * outside [0, table_width*page_size] raise INVALID_ARG and CAPACITY, and the rows
  * are skipped.  All else as in ember_paged_decode, with
