@@ -300,3 +300,23 @@ def test_errors_of_the_first_launch_on_tensor_cores():
     c.ids[:] = 3
     y = c.run()
     assert c.ad.sync_status() == 9 and not torch.isfinite(y).all()
+
+
+def test_a_graph_sees_new_ids_and_new_adapters():
+    """What a captured call reads is read at every replay: ids, adapters, scales, x and W."""
+    for n, N, K, R, A in ((6, 256, 512, 16, 4), (300, 128, 2056, 64, 8)):
+        c = Case(n, N, K, R, A)
+        c.run()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = c.run()
+        d = Case(n, N, K, R, A, seed=77)
+        for mine, new in ((c.x, d.x), (c.w, d.w), (c.a, d.a), (c.b, d.b), (c.scale, d.scale), (c.ids, d.ids)):
+            mine.copy_(new)
+        g.replay()
+        torch.cuda.synchronize()
+        d.check(y)
+        c.ids.fill_(-1)
+        g.replay()
+        torch.cuda.synchronize()
+        c.check(y)

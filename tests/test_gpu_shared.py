@@ -303,3 +303,28 @@ def test_groups_out_of_order_touch_nothing():
         assert p.cache.sync_status() == 1
     out = p.run(q)
     p.check(q, out, None, rows={0, 61, n - 1})
+
+
+@pytest.mark.parametrize("width", [0, 6000])     # read for each row, and for the group
+def test_the_same_rows_and_prefixes_twice(width):
+    """Several groups on one prefix, with different numbers of its keys, and sequences that stand in several rows."""
+    p = Shared([(300, [310, 420, 300]), (64, [70, 75])], 2, 64, 16, extra_width=width)
+    q = p.queries(8)
+    first, lse = p.run(q, return_lse=True)
+    p.check(q, first, lse)
+    rows = [0, 1, 2, 0, 1, 2, 1, 3, 4, 3]
+    q2 = q[rows].contiguous()
+    lens = p.args[0][rows].contiguous()
+    out, lse2 = p.cache.decode_shared(q2, lens, ints([0, 3, 6, 7, 10]), ints([300, 300, 300, 64]), ints([0, 0, 0, 1]),
+                                      seqs=p.seqs[rows].contiguous(), return_lse=True)
+    tol = 2.0 ** -8 * first.float().abs().max()  # one rounding of the output, and one of the weights, either way
+    assert ((out.float() - first[rows].float()).abs() <= 4 * tol).all() and (lse2 - lse[rows]).abs().max() <= 1e-4
+    assert p.cache.sync_status() == 0
+
+
+def test_nothing_but_padding():
+    p = Shared([(300, [310, 420, 300])], 2, 64, 16, extra_width=6000)
+    q = p.queries(8)
+    out = torch.full_like(q, 3.0)
+    p.cache.decode_shared(q, *p.args, seqs=torch.full_like(p.seqs, -1), out=out)
+    assert (out == 3).all() and p.cache.sync_status() == 0

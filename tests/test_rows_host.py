@@ -71,3 +71,16 @@ def test_the_limit_is_the_headers():
     import re
     with open(os.path.join(os.path.dirname(__file__), "..", "include", "ember.h")) as f:
         assert int(re.search(r"EMBER_LOGPROBS_MAX_TOP (\d+)", f.read()).group(1)) == E.LOGPROBS_MAX_TOP
+
+
+def test_the_torch_side_refuses_tensors_of_the_host():
+    import torch
+    from gqa_transformer_decode_gb300 import runtime
+    x = torch.zeros(2, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        runtime.logprobs(x, torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(TypeError, match="logits"):
+        runtime.logprobs([1.0])
+    a, b = torch.zeros(2, 8, 64, dtype=torch.bfloat16), torch.zeros(2, 64, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="a must be a tensor on a CUDA device"):
+        runtime.Adapters(a, b)
