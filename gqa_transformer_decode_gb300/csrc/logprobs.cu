@@ -255,17 +255,30 @@ struct Search {
     unsigned long long best[32];
     int found[32];
 };
-// Adds to s_top[have ..] the largest elements below the key `before` (first: there is none), in
-// order, until there are `top`: finds the largest, then in one walk all that equal it.
+// Adds to s_top[have ..] the largest elements of values below that of the key `before` (first: there
+// is none), in order, until there are `top`: finds the largest, then in one walk all that equal it.
 template <class L, int T>
 __device__ __noinline__ int take_largest(const typename L::T* row, int i0, int i1, unsigned long long before, bool first,
                                          int have, int top, unsigned long long* s_top, Search& s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     while (have < top) {
         unsigned long long best = 0;
-        for (int i = i0 + tid; i < i1; i += T) {
-            const unsigned long long k = argmax_key(L::one(row[i]), (uint32_t)i);
-            if ((first || k < before) && k > best) best = k;
+        const float limit = key_value(before);
+        if (first || limit != limit) {
+            for (int i = i0 + tid; i < i1; i += T) {
+                const unsigned long long k = argmax_key(L::one(row[i]), (uint32_t)i);
+                if ((first || k < before) && k > best) best = k;
+            }
+        } else {                                     // what a mask has left few of: by value alone, the walk from the start
+            float m = -INFINITY;
+            bool any = false;
+#pragma unroll 8
+            for (int i = i0 + tid; i < i1; i += T) {
+                const float x = L::one(row[i]);
+                any |= x < limit;
+                m = fmaxf(m, x < limit ? x : -INFINITY);
+            }
+            if (any) best = argmax_key(m, (uint32_t)i0);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
