@@ -320,3 +320,9 @@ def test_a_graph_sees_new_ids_and_new_adapters():
         g.replay()
         torch.cuda.synchronize()
         c.check(y)
+
+
+@pytest.mark.parametrize("A", [20, 3])           # A x row by row and on tensor cores
+def test_more_rows_than_65535(A):
+    c = Case(70000, 64, 64, 8, A)
+    c.check(c.run())

@@ -257,3 +257,10 @@ def test_given_tokens_that_a_mask_excludes(dtype, n):
     few = list(range(0, n, max(1, n // 24)))
     got = logprobs(x, ids.int().cuda(), top=6)
     check(x[few], ids[few].int(), 6, 1.0, type(got)(*(y[few] for y in got)))
+
+
+def test_more_rows_than_65535():
+    x, ids = rows(70001, 13, "bf16", 5)
+    got = logprobs(x, ids, top=3)
+    few = list(range(0, 70001, 700))
+    check(x[few], ids[few], 3, 1.0, type(got)(*(y[few] for y in got)))

@@ -328,3 +328,10 @@ def test_nothing_but_padding():
     out = torch.full_like(q, 3.0)
     p.cache.decode_shared(q, *p.args, seqs=torch.full_like(p.seqs, -1), out=out)
     assert (out == 3).all() and p.cache.sync_status() == 0
+
+
+def test_twenty_thousand_rows():
+    p = Shared([(40, [41 + i % 9 for i in range(12000)]), (33, [30 + i % 19 for i in range(8000)])], 1, 16, 16)
+    q = p.queries(4)
+    out, lse = p.run(q, return_lse=True)
+    p.check(q, out, lse, rows=set(range(0, 20000, 251)) | {11999, 12000, 19999})
