@@ -593,14 +593,14 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         asm volatile("bar.sync 1, 128;" ::: "memory");
                         if (tid == 0) put_out(buf, c);
+                    } else if ((c & 48) == 48 || c + 16 >= rows) {   // 64 rows' worth
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        asm volatile("bar.sync 1, 128;" ::: "memory");
+                        if (tid == 0)
+                            for (int d = c & ~63; d <= c; d += 16) put_out(sm + d * row_bytes, d);
                     }
                 }
-                if (last) {
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-                    if (tid == 0)
-                        for (int c = 0; c < rows; c += 16) put_out(sm + c * row_bytes, c);
-                } else if (tid == 0) {
+                if (!last && tid == 0) {
                     bulk_wait_read<0>();         // the next tile begins with the first slice's place again
                 }
                 continue;
