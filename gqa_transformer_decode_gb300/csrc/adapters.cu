@@ -36,8 +36,9 @@ namespace ember {
 
 namespace {
 
-constexpr int AD_BUILDERS = 4;                   // warps that write t's tiles
-constexpr int AD_THREADS = 192 + 32 * AD_BUILDERS;
+// Warps that write t's tiles, and threads of a CTA, by the tile's width.
+constexpr int ad_builders(int nt) { return nt > 128 ? 8 : 4; }
+constexpr int ad_threads(int nt) { return 192 + 32 * ad_builders(nt); }
 constexpr int AD_M = 128;                        // rows of W in a tile
 constexpr int AD_BK = 64;                        // K of a block
 constexpr int AD_SLICE = 32;                     // rows of x that are put out at a time
@@ -79,7 +80,7 @@ __device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
 }
 
 // The adapters of rows [row0, row0 + a.nt) of ids, in the order in which they come first, by the
-// AD_BUILDERS warps together; their number.  Neighbouring rows with one adapter are a run; each
+// ad_builders(NT) warps together; their number.  Neighbouring rows with one adapter are a run; each
 // thread compares its run with all others.  (A search for one adapter after another took 0.15 us
 // for each, a comparison of 256 rows with one another 8 us.)
 struct alignas(16) AdRun {
@@ -89,8 +90,8 @@ struct alignas(16) AdRun {
 };
 template <int NT>
 __device__ __forceinline__ int list_adapters(const AdapterArgs& a, int row0, AdEntry* list, int* s_ids, AdRun* runs, uint32_t* s_word) {
-    constexpr int T = 32 * AD_BUILDERS, PER = (NT + T - 1) / T, WORDS = (NT + 31) / 32;
-    const int tid = threadIdx.x - (AD_THREADS - T), lane = tid & 31;
+    constexpr int T = 32 * ad_builders(NT), PER = (NT + T - 1) / T, WORDS = (NT + 31) / 32;
+    const int tid = threadIdx.x - (ad_threads(NT) - T), lane = tid & 31;
     auto sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(T) : "memory"); };
     // the place of this thread's k-th element among those whose flag is set, by a ballot a warp
     auto count = [&](const bool (&flag)[PER], int (&at)[PER]) {
@@ -225,7 +226,7 @@ __device__ __forceinline__ void store_out(const AdapterArgs& a, int row, int m, 
 
 // (Two CTAs to an SM where they have room: one of each launch.)
 template <class E, int NT, bool LOW>
-__global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
     k_adapter(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
               const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmOut, AdapterArgs a) {
     using L = AdSmem<NT, LOW>;
@@ -264,13 +265,13 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&t_go[s], 1);
-            mbar_init(&t_full[s], AD_BUILDERS);
+            mbar_init(&t_full[s], ad_builders(NT));
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 4);
             mbar_init(&list_full[b], 1);
-            mbar_init(&list_empty[b], 2 + AD_BUILDERS);   // copies, products, builders
+            mbar_init(&list_empty[b], 2 + ad_builders(NT));   // copies, products, builders
         }
         sflag[0] = sflag[1] = sflag[2] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                 int all_ok;
                 asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 2, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                              : "=r"(all_ok)
-                             : "r"((uint32_t)ok), "n"(32 * AD_BUILDERS)
+                             : "r"((uint32_t)ok), "n"(32 * ad_builders(NT))
                              : "memory");
                 ok = all_ok != 0;
                 if (!ok) break;
@@ -461,10 +462,10 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
                 const int rows = min(a.nt, a.n - t.row0);
                 const bool kept = tiles == 1 && all > 0 && rows * RP * 4 <= L::OUT;
                 if (kept) {
-                    const int tid = threadIdx.x - (AD_THREADS - 32 * AD_BUILDERS);
-                    for (int i = tid; i < rows * (RP / 4); i += 32 * AD_BUILDERS)
+                    const int tid = threadIdx.x - (ad_threads(NT) - 32 * ad_builders(NT));
+                    for (int i = tid; i < rows * (RP / 4); i += 32 * ad_builders(NT))
                         reinterpret_cast<uint4*>(s_out)[i] = __ldcg(rows_t + i);
-                    asm volatile("bar.sync 2, %0;" ::"n"(32 * AD_BUILDERS) : "memory");
+                    asm volatile("bar.sync 2, %0;" ::"n"(32 * ad_builders(NT)) : "memory");
                 }
                 Block next(s_list + b * NT + part, slabs, C);
                 for (int f = 0; f < all; f += L::SLABS, ++g) {
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 *reinterpret_cast<uint4*>(dst + (q >> 1) * L::SLAB_T + (((q & 1) ^ (c >> 2 & 1)) << 4)) = v[q];
-                        p += AD_BUILDERS;
+                        p += ad_builders(NT);
                         some = find();
                         if (some) ask();
                     }
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(AD_THREADS, NT <= 128 ? 2 : 1)
             const int rows = min(a.nt, a.n - t.row0);
             const uint32_t at = smem_u32(sm);
             const int all = rows * (AD_M / 8), lo = (int)((long long)all * part / C), hi = (int)((long long)all * (part + 1) / C);
-            for (int i = lo + (int)threadIdx.x; i < hi; i += AD_THREADS) {
+            for (int i = lo + (int)threadIdx.x; i < hi; i += ad_threads(NT)) {
                 const int c = i / (AD_M / 8), f = i % (AD_M / 8) * 8;
                 if (!wanted(t, c, f)) continue;  // (most of the first launch's)
                 float y[8];
@@ -754,8 +755,8 @@ cudaError_t launch_nt(const CUtensorMap& w, const CUtensorMap& x, const CUtensor
     static OncePerDevice once;
     const cudaError_t e = once([&] { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); });
     if (e != cudaSuccess) return e;
-    if (a.splits > 1) return launch_cluster_k(k, dim3(grid), dim3(AD_THREADS), SMEM, a.splits, s, w, x, b, o, a);
-    return launch_k(k, dim3(grid), dim3(AD_THREADS), SMEM, s, w, x, b, o, a);
+    if (a.splits > 1) return launch_cluster_k(k, dim3(grid), dim3(ad_threads(NT)), SMEM, a.splits, s, w, x, b, o, a);
+    return launch_k(k, dim3(grid), dim3(ad_threads(NT)), SMEM, s, w, x, b, o, a);
 }
 template <class E, bool LOW>
 cudaError_t launch_low(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const CUtensorMap& o, const AdapterArgs& a,
