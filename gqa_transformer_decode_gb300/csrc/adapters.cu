@@ -24,7 +24,7 @@
 // calls give equal bits.  Many tiles run persistently, one CTA an SM, the next tile's
 // products under the last one's output.
 //
-// Warp 0: copies; warp 1: TMEM and products; warps 2-5: output; warps 6-9: which adapters a
+// Warp 0: copies; warp 1: TMEM and products; warps 2-5: output; the others: which adapters a
 // tile has, and t's tiles.  Every wait is bounded; a timeout raises EMBER_ERR_TIMEOUT, the
 // CTA drains its copies and frees TMEM.
 #include <cudaTypedefs.h>
@@ -36,7 +36,10 @@ namespace ember {
 
 namespace {
 
-// Warps that write t's tiles, and threads of a CTA, by the tile's width.
+// Warps that write t's tiles, and threads of a CTA, by the tile's width.  Wide tiles of rows in any
+// order are bound by that writing (256 rows of 40 adapters of rank 16 on 4096 30 us, with four warps
+// 37; 777 rows of 9 of rank 32 27 and 37); narrow ones only have more threads to start (128 rows of
+// 8 adapters of rank 16 on 4096 16 us, with eight 18.5).
 constexpr int ad_builders(int nt) { return nt > 128 ? 8 : 4; }
 constexpr int ad_threads(int nt) { return 192 + 32 * ad_builders(nt); }
 constexpr int AD_M = 128;                        // rows of W in a tile
@@ -803,8 +806,9 @@ cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& 
 // Multiplications n R K of k_adapter_rows at most, twice as many from 16 adapters on, since the
 // tcgen05 kernel has a tile for every two (rank 64) that a row tile names, whatever their rows.  On
 // 4096 inputs and outputs (bf16, rows in any order), by rows and with tcgen05: 64 rows of rank 32 on
-// 40 adapters 16 and 36 us; 128 rows of rank 64 on 8 adapters (2^25) 22 and 28; 256 rows of rank 64
-// (2^26) on 2 adapters 35 and 30, on 8 43 and 44, on 32 59 and 69; twice that on 8 adapters 56 and 51.
+// 40 adapters 16 and 25 us; 128 rows of rank 64 on 8 adapters (2^25) 21 and 28; 256 rows of rank 64
+// (2^26) on 2 adapters 32 and 29, on 8 36 and 36, on 32 47 and 58; twice that on 8 adapters 46 and
+// 42, on 64 93 and 126, but 70 and 57 where each adapter's rows stand together.
 constexpr int AR_MOST = 1 << 25, AR_ADAPTERS = 16;
 
 // Cycles of a block's products, 4 of M = 128, N = nt, K = 16: no less than 112 each.
