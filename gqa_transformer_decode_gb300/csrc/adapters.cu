@@ -313,6 +313,21 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
     const int part = rank % C, first_of = rank / C, every = LOW ? CL / C : 1;
     const int tiles = LOW ? max(0, (have - first_of + every - 1) / every) : have;
     const int kb0 = (int)((long long)nk * part / C), kb1 = (int)((long long)nk * (part + 1) / C);
+    // A tile alone has both accumulators, and each gets half of K: the tensor cores' f32 sums lose a
+    // little at every step, so that half the steps lose half (777 rows, K 1024, f32 outputs: off by
+    // 0.66e-6 of their norm in 22.1 us, in one accumulator 1.2e-6 in 21.5).  Whatever the outputs'
+    // type, so that the narrow ones are the f32 ones rounded.
+    const bool two = !LOW && tiles == 1 && kb1 - kb0 >= 2;
+    const int mid = two ? (kb0 + kb1) / 2 : kb1;
+    // sums c .. c + 15 of this thread's row
+    auto sums_of = [&](uint32_t acc, int c, float (&y)[16]) {
+        uint32_t r[16], q[16];
+        tmem_ld16(acc + c, r);
+        if (two) tmem_ld16(acc + NT + c, q);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(r[i]) + (two ? __uint_as_float(q[i]) : 0.f);
+    };
     struct Tile {
         int row0, m0, e0;                        // first row of x, first row of W, first entry (first launch)
     };
@@ -396,7 +411,8 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
                     const uint32_t w = smem_u32(sm + s * L::STAGE), x = w + L::A_BYTES;
 #pragma unroll
                     for (int k = 0; k < AD_BK / 16; ++k)
-                        umma_bf16(acc, sdesc_sw128(w + k * 32), sdesc_sw128(x + k * 32), id_x, kb > kb0 || k > 0);
+                        umma_bf16(kb < mid ? acc : acc + NT, sdesc_sw128(w + k * 32), sdesc_sw128(x + k * 32), id_x,
+                                  (kb != kb0 && kb != mid) || k > 0);
                     umma_commit(&empty[s]);
                 }
                 if (!LOW && ok) {
@@ -550,11 +566,10 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
             if (C > 1) {                         // the whole tile, joined below
                 float* dst = reinterpret_cast<float*>(sm) + quad * 32 + lane;
                 for (int c = 0; c < rows; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(acc + c, r);
-                    tmem_ld_wait();
+                    float y[16];
+                    sums_of(acc, c, y);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) dst[(c + i) * AD_LD] = __uint_as_float(r[i]);
+                    for (int i = 0; i < 16; ++i) dst[(c + i) * AD_LD] = y[i];
                 }
                 break;
             }
@@ -571,9 +586,8 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
                     bulk_commit();
                 };
                 for (int c = 0; c < rows; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(acc + c, r);
-                    tmem_ld_wait();
+                    float y[16];
+                    sums_of(acc, c, y);
                     if (c + 16 >= rows) {
                         tc_fence_before();
                         __syncwarp();
@@ -587,11 +601,11 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
                     if (a.out_f32) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            reinterpret_cast<float*>(buf)[i * AD_M + quad * 32 + lane] = __uint_as_float(r[i]) + add;
+                            reinterpret_cast<float*>(buf)[i * AD_M + quad * 32 + lane] = y[i] + add;
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            reinterpret_cast<uint16_t*>(buf)[i * AD_M + quad * 32 + lane] = (uint16_t)E::pack(__uint_as_float(r[i]) + add, 0.f);
+                            reinterpret_cast<uint16_t*>(buf)[i * AD_M + quad * 32 + lane] = (uint16_t)E::pack(y[i] + add, 0.f);
                     }
                     if (!last) {
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
