@@ -65,13 +65,14 @@ __device__ __forceinline__ PtGroup pt_scan(const PtGroups& a, int g0, unsigned& 
 // them.  That pays while both are short and made of latencies: 64 rows on 8192 keys and up to 512
 // of their own 20.5 us, one kernel after the other 23.  With more than PT_APART tiles an SM they
 // only contend for memory (128 rows on 32768 keys: 98 us beside each other, 90 after each other).
-// In proportion to what each would take one SM: a key tile of a pair 1350 cycles, a pair four
-// tiles more, and a CTA's SM reads 40 bytes a cycle when not all SMs do.
+// In proportion to what each would take one SM: a key tile of a pair 1700 cycles, a pair four
+// tiles more, and a CTA's SM reads 40 bytes a cycle when not all SMs do.  (64 rows on 8192 keys and
+// 512 of their own 29.6 us so, with 1350 or 2300 cycles 30.5.)
 constexpr unsigned PT_APART = 12;
 __device__ __forceinline__ int prefix_sms(unsigned tiles, unsigned pairs, float tail_bytes, int sms) {
     if (tiles == 0) return 0;
     if (!(tail_bytes > 0.f) || tiles > PT_APART * sms) return sms;
-    const float w1 = (tiles + 4.f * pairs) * 1350.f, w2 = tail_bytes * (1.f / 40.f);
+    const float w1 = (tiles + 4.f * pairs) * 1700.f, w2 = tail_bytes * (1.f / 40.f);
     return min(sms - 1, max(1, (int)(sms * (w1 / (w1 + w2)) + 0.5f)));
 }
 

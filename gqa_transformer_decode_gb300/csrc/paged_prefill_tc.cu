@@ -30,9 +30,10 @@
 // P is rounded once to the cache's type, bf16 by 2^-8 of each weight at most, f16 by
 // 2^-11, which in a sum over keys of mixed sign is about the output's own rounding
 // (error against 64 bits 0.0022 and 0.00029, the bare rounding's 0.0016 and 0.00021).
-// A second term, as decode has it, would be another P V product: at head_dim 128, which
-// the tensor pipe bounds, 512 cycles more on the 1263 of a step.  l is summed from the
-// unrounded weights in f32.
+// A second term, as decode has it, is another P V product: at head_dim 128, which
+// the tensor pipe bounds, 512 cycles more on the 1263 of a step.  PT_SHARED takes it, since
+// a decode step's outputs are not to be less exact for the prefix being shared; prefill
+// does not.  l is summed from the unrounded weights in f32.
 //
 // CTAs are persistent: one whose last copies are issued asks the hardware to
 // cancel a CTA that has not started yet (clusterlaunchcontrol) and takes over
@@ -61,7 +62,7 @@
 // "sequence" is then a group of one-token rows, all of which see the group's prefix, and
 // the key tiles of all (pair, kv head)s form a line of which CTA c takes the c-th equal
 // share, as in paged_decode.cu.  What a CTA has of a pair it leaves as (m, l, O) of the
-// pair's rows, which paged_decode.cu joins with the rows' own keys.
+// pair's rows, which paged_shared.cu joins with the rows' own keys.
 //
 // Warps 0-3: tile A; warps 4-7: tile B (a warp reads the TMEM lanes of its index
 // mod 4); warp 8: TMA producer; warp 9: TMEM allocation; warps
@@ -100,7 +101,8 @@ struct PtSmem {
     static_assert(TOTAL <= 232448, "shared memory of a CTA");
     static_assert(2 * PT_ROWS * (DP * 4 + 8) <= OFF_BAR, "the split form's rows");
     // TMEM columns: two S buffers of 64 f32 for each query tile, the weights P (64
-    // values, two to a column) over the first half of theirs; O_A, O_B (DP f32 each)
+    // values, two to a column) over the first half of theirs, their second terms over
+    // the other; O_A, O_B (DP f32 each)
     static constexpr uint32_t col_s(int t, int b) { return t * 128 + b * 64; }
     static constexpr uint32_t col_o(int t) { return 256 + t * DP; }
 };
@@ -328,6 +330,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     using L = PtSmem<DP>;
     constexpr int NS = L::NS;
     constexpr bool SPLIT = FORM == PT_SPLIT, SHARED = FORM == PT_SHARED;
+    constexpr int TERMS = SHARED ? 2 : 1;              // values of the type that a weight is the sum of
     extern __shared__ uint8_t pt_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pt_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
@@ -587,7 +590,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         };
         auto mma_pv = [&](uint32_t c, uint32_t dv, bool acc) {   // O += P (TMEM) . V
 #pragma unroll
-            for (int k = 0; k < PT_KEYS / 16; ++k) mma_ts(col_o, c + k * 8, dv + ((k * 16 * 128) >> 4), idO, acc || k);
+            for (int i = 0; i < TERMS; ++i)
+#pragma unroll
+                for (int k = 0; k < PT_KEYS / 16; ++k)
+                    mma_ts(col_o, c + i * (PT_KEYS / 2) + k * 8, dv + ((k * 16 * 128) >> 4), idO, acc || i || k);
         };
         // one lane issues f() after everything the warp has waited for
         auto issue = [&](auto f) {
@@ -698,6 +704,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             const int n = base + j;
             const uint32_t tS = tmem + L::col_s(t, n & 1) + lane_off;
             uint32_t v[PT_KEYS];                      // the row's products, then its weights
+            uint32_t left[PT_KEYS / 2];               // (two terms) what their rounding left
             // S(n); and P . V(n - 2), complete before it, for its phase to be seen
             const bool odd_lane = n >= 2 && (lane & 1);
             if (!wait_all((odd_lane ? o_full : s_full) + 2 * t + (n & 1), odd_lane ? (n >> 1) - 1 : n >> 1)) {
@@ -745,7 +752,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     w.x = ex2(w.x);
                     w.y = ex2(w.y);
                     rs[(c >> 1) & 3] = add2(rs[(c >> 1) & 3], w);
-                    v[c >> 1] = E::pack(w.x, w.y);
+                    const uint32_t x = TERMS == 2 && E::bf16 ? __byte_perm(__float_as_uint(w.x), __float_as_uint(w.y), 0x7632)
+                                                             : E::pack(w.x, w.y);   // (cut off: the second term has the rest)
+                    v[c >> 1] = x;
+                    if (TERMS == 2) {
+                        const float2 y = add2(w, make_float2(-E::lo(x), -E::hi(x)));
+                        left[c >> 1] = E::pack(y.x, y.y);
+                    }
                 }
                 const float2 r2 = add2(add2(rs[0], rs[1]), add2(rs[2], rs[3]));
                 return r2.x + r2.y;
@@ -788,7 +801,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             }
             // over S(j), all of it read; P . V(j - 2), the last reader here, was issued before S(j)
 #pragma unroll
-            for (int c = 0; c < PT_KEYS / 2; c += 16) tmem_st16(tS + c, v + c);
+            for (int c = 0; c < PT_KEYS / 2; c += 16) {
+                tmem_st16(tS + c, v + c);
+                if (TERMS == 2) tmem_st16(tS + PT_KEYS / 2 + c, left + c);
+            }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();

@@ -407,8 +407,7 @@ ember_status ember_adapter_project(const ember_adapters *ad, const void *x, int6
  *     or with a scale that is not positive, take it as the sum of two values of the
  *     cache's type (2^-16 relative for bf16, 2^-22 for f16), other prefill as one
  *     (2^-8, 2^-11: about the output's own rounding); f16's is at least 2^-32 of the
- *     largest weight of its row.  decode_shared: two terms, but one for the keys of
- *     prefixes that are multiplied for their whole group (large calls).
+ *     largest weight of its row.  decode_shared: two terms, as decode.
  *   - B is at most 65535.  No operator has a gradient.
  *   - Buffers and the stream belong to the current device; buffers may not
  *     overlap, except that pages may be shared by the tables of sequences
