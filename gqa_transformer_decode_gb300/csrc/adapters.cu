@@ -46,6 +46,12 @@ constexpr int AD_M = 128;                        // rows of W in a tile
 constexpr int AD_BK = 64;                        // K of a block
 constexpr int AD_SLICE = 32;                     // rows of x that are put out at a time
 constexpr int AD_LD = AD_M + 4;                  // their distance in shared memory, floats
+// f32 outputs: the tensor cores' sums lose a little at every step, in proportion to the steps, so an
+// accumulator takes at most AD_FOLD blocks of K (64 steps) before the output warps add it to a sum in
+// TMEM, rounded to nearest, under the next blocks' products where there is room for a second
+// accumulator.  Off by 1.1e-6 of the norm, by 0.57e-6 with 8 blocks; 4096 rows at K 8192 by 9.3e-6 in one
+// accumulator.  Outputs of 16 bits do without: their own rounding is 1.6e-3 or 2e-4.
+constexpr int AD_FOLD = 16;
 
 template <int NT, bool LOW>
 struct AdSmem {
@@ -228,13 +234,16 @@ __device__ __forceinline__ void store_out(const AdapterArgs& a, int row, int m, 
 }
 
 // (Two CTAs to an SM where they have room: one of each launch.)
-template <class E, int NT, bool LOW>
+template <class E, int NT, bool LOW, bool FOLD>
 __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
     k_adapter(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
               const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmOut, AdapterArgs a) {
     using L = AdSmem<NT, LOW>;
     constexpr int S = L::STAGES;
-    constexpr uint32_t COLS = 2 * NT < 32 ? 32 : 2 * NT;     // of TMEM: two accumulators
+    // TMEM: two accumulators, which take turns, or one and two and the sum
+    constexpr int ACCS = FOLD && NT > 128 ? 1 : 2;
+    constexpr uint32_t COLS = FOLD && NT <= 128 ? 4 * NT : 2 * NT;
+    static_assert(COLS >= 32 && COLS <= 512 && (ACCS + FOLD) * NT <= COLS, "TMEM");
     extern __shared__ uint8_t ad_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ad_raw) + 1023) & ~uintptr_t(1023));
     float* s_out = reinterpret_cast<float*>(sm + L::OFF_OUT);
@@ -313,20 +322,21 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
     const int part = rank % C, first_of = rank / C, every = LOW ? CL / C : 1;
     const int tiles = LOW ? max(0, (have - first_of + every - 1) / every) : have;
     const int kb0 = (int)((long long)nk * part / C), kb1 = (int)((long long)nk * (part + 1) / C);
-    // A tile alone has both accumulators, and each gets half of K: the tensor cores' f32 sums lose a
-    // little at every step, so that half the steps lose half (777 rows, K 1024, f32 outputs: off by
-    // 0.66e-6 of their norm in 22.1 us, in one accumulator 1.2e-6 in 21.5).  Whatever the outputs'
-    // type, so that the narrow ones are the f32 ones rounded.
-    const bool two = !LOW && tiles == 1 && kb1 - kb0 >= 2;
+    // A tile alone has both accumulators, and each gets half of K: half the steps lose half (777 rows,
+    // K 1024, f32 outputs: off by 0.66e-6 of their norm in 22.1 us, in one accumulator 1.2e-6 in 21.5).
+    // Whatever the outputs' type, so that the narrow ones are the f32 ones rounded up to K 1024.
+    const bool two = !LOW && !FOLD && tiles == 1 && kb1 - kb0 >= 2;
     const int mid = two ? (kb0 + kb1) / 2 : kb1;
-    // sums c .. c + 15 of this thread's row
-    auto sums_of = [&](uint32_t acc, int c, float (&y)[16]) {
+    // A tile's products are one run of blocks in one accumulator, or several in turn.
+    const int runs = FOLD ? max(1, (kb1 - kb0 + AD_FOLD - 1) / AD_FOLD) : 1;
+    // sums c .. c + 15 of this thread's row: an accumulator's and, if there are some, those at `more`
+    auto sums_of = [&](uint32_t acc, bool some, uint32_t more, int c, float (&y)[16]) {
         uint32_t r[16], q[16];
         tmem_ld16(acc + c, r);
-        if (two) tmem_ld16(acc + NT + c, q);
+        if (some) tmem_ld16(more + c, q);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(r[i]) + (two ? __uint_as_float(q[i]) : 0.f);
+        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(r[i]) + (some ? __uint_as_float(q[i]) : 0.f);
     };
     struct Tile {
         int row0, m0, e0;                        // first row of x, first row of W, first entry (first launch)
@@ -400,11 +410,21 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
             bool ok = true;
             for (int li = 0; li < tiles && ok; ++li) {
                 const int b = li & 1;
-                ok = li < 2 || mbar_wait(&acc_empty[b], ((uint32_t)(li >> 1) & 1u) ^ 1u);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t acc = tmem + (uint32_t)(b * NT);
+                int run = li * runs, kr = kb0;   // this run's number of all and its first block
+                auto begin = [&] {
+                    ok = run < ACCS || mbar_wait(&acc_empty[run % ACCS], ((uint32_t)(run / ACCS) & 1u) ^ 1u);
+                    tc_fence_after();
+                    return ok;
+                };
+                if (!begin()) break;
                 for (int kb = kb0; kb < kb1; ++kb, ++g) {
+                    if (FOLD && kb == kr + AD_FOLD) {
+                        umma_commit(&acc_full[run % ACCS]);
+                        ++run;
+                        kr = kb;
+                        if (!begin()) break;
+                    }
+                    const uint32_t acc = tmem + (uint32_t)(run % ACCS * NT);
                     const int s = g % S;
                     if (!(ok = mbar_wait(&full[s], (uint32_t)(g / S) & 1u))) break;
                     tc_fence_after();
@@ -412,10 +432,11 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
 #pragma unroll
                     for (int k = 0; k < AD_BK / 16; ++k)
                         umma_bf16(kb < mid ? acc : acc + NT, sdesc_sw128(w + k * 32), sdesc_sw128(x + k * 32), id_x,
-                                  (kb != kb0 && kb != mid) || k > 0);
+                                  (kb != kr && kb != mid) || k > 0);
                     umma_commit(&empty[s]);
                 }
                 if (!LOW && ok) {
+                    const uint32_t acc = tmem + (uint32_t)(run % ACCS * NT);
                     ok = mbar_wait(&list_full[b], (uint32_t)(li >> 1) & 1u);
                     const int all = ok ? blocks_of(s_count[b]) : 0;
                     Block next(s_list + b * NT + part, slabs, C);
@@ -438,7 +459,7 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
                     }
                     if (ok) mbar_arrive(&list_empty[b]);
                 }
-                if (ok) umma_commit(&acc_full[b]);
+                if (ok) umma_commit(&acc_full[run % ACCS]);
             }
             if (!ok) sflag[0] = 1;
             sflag[2] = g;
@@ -547,27 +568,61 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
     } else {   // ---------------- output, warps 2..5
         const int quad = warp & 3, tid = threadIdx.x - 64;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        const uint32_t sum = tmem + ACCS * NT + lane_off;
         for (int li = 0; li < tiles; ++li) {
-            const int b = li & 1;
             const Tile t = tile_of(li);
-            bool ok = mbar_wait(&acc_full[b], (uint32_t)(li >> 1) & 1u);
-            uint32_t all;                        // the barriers below need all four warps
-            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                         : "=r"(all)
-                         : "r"((uint32_t)ok)
-                         : "memory");
-            if (!all) {
+            const int rows = min(a.nt, a.n - t.row0);
+            int run = li * runs;
+            auto next_run = [&] {                // false for all four warps, which the barriers below need, or none
+                const uint32_t ok = mbar_wait(&acc_full[run % ACCS], (uint32_t)(run / ACCS) & 1u);
+                uint32_t all;
+                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                             : "=r"(all)
+                             : "r"(ok)
+                             : "memory");
+                tc_fence_after();
+                return all != 0;
+            };
+            // every run but the last is added to the sum, and its accumulator is free again
+            constexpr int FOLD_COLS = NT < 32 ? NT : 32;
+            bool ok = next_run();
+            for (int k = 0; FOLD && ok && k + 1 < runs; ++k) {
+                const uint32_t acc = tmem + (uint32_t)(run % ACCS * NT) + lane_off;
+#pragma unroll 1
+                for (int c = 0; c < rows; c += FOLD_COLS) {
+                    uint32_t x[FOLD_COLS], y[FOLD_COLS];
+#pragma unroll
+                    for (int i = 0; i < FOLD_COLS; i += 16) {
+                        tmem_ld16(acc + c + i, x + i);
+                        if (k > 0) tmem_ld16(sum + c + i, y + i);
+                    }
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < FOLD_COLS; ++i)
+                        if (k > 0) x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(y[i]));
+#pragma unroll
+                    for (int i = 0; i < FOLD_COLS; i += 16) tmem_st16(sum + c + i, x + i);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[run % ACCS]);
+                ++run;
+                ok = next_run();
+            }
+            if (!ok) {
                 sflag[0] = 1;
                 break;
             }
-            tc_fence_after();
+            const int b = run % ACCS;
             const uint32_t acc = tmem + (uint32_t)(b * NT) + lane_off;
-            const int rows = min(a.nt, a.n - t.row0);
+            const bool some = two || (FOLD && runs > 1);   // sums beside the accumulator's
+            const uint32_t more = FOLD ? sum : acc + NT;
             if (C > 1) {                         // the whole tile, joined below
                 float* dst = reinterpret_cast<float*>(sm) + quad * 32 + lane;
                 for (int c = 0; c < rows; c += 16) {
                     float y[16];
-                    sums_of(acc, c, y);
+                    sums_of(acc, some, more, c, y);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) dst[(c + i) * AD_LD] = y[i];
                 }
@@ -587,7 +642,7 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
                 };
                 for (int c = 0; c < rows; c += 16) {
                     float y[16];
-                    sums_of(acc, c, y);
+                    sums_of(acc, some, more, c, y);
                     if (c + 16 >= rows) {
                         tc_fence_before();
                         __syncwarp();
@@ -764,25 +819,32 @@ __global__ void __launch_bounds__(AR_WARPS * 32) k_adapter_rows(AdapterArgs a, c
     }
 }
 
-template <class E, int NT, bool LOW>
-cudaError_t launch_nt(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const CUtensorMap& o, const AdapterArgs& a,
+template <class E, int NT, bool LOW, bool FOLD>
+cudaError_t launch_form(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const CUtensorMap& o, const AdapterArgs& a,
                       int grid, cudaStream_t s) {
     constexpr int SMEM = AdSmem<NT, LOW>::TOTAL;
-    auto k = k_adapter<E, NT, LOW>;
+    auto k = k_adapter<E, NT, LOW, FOLD>;
     static OncePerDevice once;
     const cudaError_t e = once([&] { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); });
     if (e != cudaSuccess) return e;
     if (a.splits > 1) return launch_cluster_k(k, dim3(grid), dim3(ad_threads(NT)), SMEM, a.splits, s, w, x, b, o, a);
     return launch_k(k, dim3(grid), dim3(ad_threads(NT)), SMEM, s, w, x, b, o, a);
 }
+template <class E, int NT, bool LOW>
+cudaError_t launch_nt(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const CUtensorMap& o, const AdapterArgs& a,
+                      int grid, bool fold, cudaStream_t s) {
+    if constexpr (!LOW)
+        if (fold) return launch_form<E, NT, LOW, true>(w, x, b, o, a, grid, s);
+    return launch_form<E, NT, LOW, false>(w, x, b, o, a, grid, s);
+}
 template <class E, bool LOW>
 cudaError_t launch_low(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const CUtensorMap& o, const AdapterArgs& a,
-                       int grid, cudaStream_t s) {
-    if (a.nt <= 16) return launch_nt<E, 16, LOW>(w, x, b, o, a, grid, s);
-    if (a.nt <= 32) return launch_nt<E, 32, LOW>(w, x, b, o, a, grid, s);
-    if (a.nt <= 64) return launch_nt<E, 64, LOW>(w, x, b, o, a, grid, s);
-    if (a.nt <= 128) return launch_nt<E, 128, LOW>(w, x, b, o, a, grid, s);
-    if constexpr (!LOW) return launch_nt<E, 256, LOW>(w, x, b, o, a, grid, s);
+                       int grid, bool fold, cudaStream_t s) {
+    if (a.nt <= 16) return launch_nt<E, 16, LOW>(w, x, b, o, a, grid, fold, s);
+    if (a.nt <= 32) return launch_nt<E, 32, LOW>(w, x, b, o, a, grid, fold, s);
+    if (a.nt <= 64) return launch_nt<E, 64, LOW>(w, x, b, o, a, grid, fold, s);
+    if (a.nt <= 128) return launch_nt<E, 128, LOW>(w, x, b, o, a, grid, fold, s);
+    if constexpr (!LOW) return launch_nt<E, 256, LOW>(w, x, b, o, a, grid, fold, s);
     return cudaErrorInvalidValue;
 }
 template <class E>
@@ -807,14 +869,14 @@ cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& 
     a.col_tiles = 1;
     a.splits = p.low_splits;
     a.nt = p.low_nt;
-    const cudaError_t e = p.low_grid ? launch_low<E, true>(ma, mxl, ma, ma, a, p.low_grid, s)
+    const cudaError_t e = p.low_grid ? launch_low<E, true>(ma, mxl, ma, ma, a, p.low_grid, false, s)
                                      : launch_rows<E>(a, r, s);
     if (e != cudaSuccess) return e;
     a.row_tiles = p.row_tiles;
     a.col_tiles = p.col_tiles;
     a.splits = p.splits;
     a.nt = p.nt;
-    return launch_low<E, false>(mw, mx, mb, mo, a, p.grid, s);
+    return launch_low<E, false>(mw, mx, mb, mo, a, p.grid, p.fold, s);
 }
 
 // Multiplications n R K of k_adapter_rows at most, twice as many from 16 adapters on, since the
@@ -830,7 +892,7 @@ int block_cycles(int nt) { return max(450, nt * 8 / 3); }
 
 }  // namespace
 
-AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms) {
+AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, bool out_f32, int sms) {
     AdapterPlan p{};
     const int nk = (K + AD_BK - 1) / AD_BK;
     p.col_tiles = (N + AD_M - 1) / AD_M;
@@ -845,11 +907,14 @@ AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms) {
             const long long tiles = (long long)rt * p.col_tiles;
             if (c > 1 && tiles * c > sms) break;
             const long long rounds = (tiles * c + sms - 1) / sms;
+            // (a tile alone has half of its blocks in each accumulator)
+            const bool fold = out_f32 && (nk + c - 1) / c > AD_FOLD * (rounds == 1 ? 2 : 1);
             const long long cost = rounds * ((nk + c - 1) / c) * block_cycles(nt) + rounds * 8 * nt + (c > 1 ? 2000 : 0);
             if (best < 0 || cost < best) {
                 best = cost;
                 p.nt = nt;
                 p.splits = c;
+                p.fold = fold;
                 p.row_tiles = rt;
                 p.grid = (int)(c > 1 ? tiles * c : min(tiles, (long long)sms));
             }

@@ -488,6 +488,7 @@ struct AdapterArgs {
 // low_grid 0: row by row).
 struct AdapterPlan {
     int nt, row_tiles, col_tiles, splits, grid;
+    bool fold;                   // accumulators are added up every AD_FOLD blocks of K
     int low_nt, low_row_tiles, low_splits, low_grid;
 };
 struct AdapterMaps {
@@ -497,7 +498,7 @@ struct AdapterRows {
     const uint16_t *x, *w, *a, *b;   // [n][ld_x], [N][K], [n_adapters][R][K], [n_adapters][N][R]
     long long ld_x;
 };
-AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, int sms);
+AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, bool out_f32, int sms);
 size_t adapter_ws(int n, int R);
 bool adapter_maps(const AdapterArgs& a, const AdapterPlan& p, const AdapterRows& r, AdapterMaps& m);
 cudaError_t launch_adapter(const AdapterMaps& m, const AdapterArgs& a, const AdapterPlan& p, const AdapterRows& r, bool bf16,

@@ -96,7 +96,7 @@ ember_status ember_adapter_project(const ember_adapters* ad, const void* x, int6
     a.ld_out = ld_out;
     a.out_f32 = out_dtype == EMBER_F32;
     a.status = status;
-    const AdapterPlan plan = adapter_plan(n, N, K, a.R, a.n_adapters, sms);
+    const AdapterPlan plan = adapter_plan(n, N, K, a.R, a.n_adapters, a.out_f32, sms);
     const AdapterRows rows{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), static_cast<const uint16_t*>(ad->a),
                            static_cast<const uint16_t*>(ad->b), ld_x};
     AdapterMaps maps;
