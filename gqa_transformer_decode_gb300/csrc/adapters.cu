@@ -30,6 +30,7 @@
 #include <cudaTypedefs.h>
 
 #include "paged.cuh"
+#include "rounds.h"
 #include "tc_common.cuh"
 
 namespace ember {
@@ -469,19 +470,21 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
             const int builder = warp - 6;
             int g = 0;                           // stages so far
             uint32_t go_phase = 0;
-            bool ok = true, waited = false;
-            for (int li = 0; li < tiles && ok; ++li) {
-                const int b = li & 1;
-                const Tile t = tile_of(li);
-                // (all of them see the phases: a wait names one by its parity alone)
-                ok = li < 2 || mbar_wait(&list_empty[b], ((uint32_t)(li >> 1) & 1u) ^ 1u);
-                int all_ok;
+            bool waited = false;
+            // (all of them see the phases: a wait names one by its parity alone)
+            auto ready = [&](int li) { return li < 2 || mbar_wait(&list_empty[li & 1], ((uint32_t)(li >> 1) & 1u) ^ 1u); };
+            auto all_of_us = [](bool ok) {
+                uint32_t all;
                 asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 2, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                             : "=r"(all_ok)
+                             : "=r"(all)
                              : "r"((uint32_t)ok), "n"(32 * ad_builders(NT))
                              : "memory");
-                ok = all_ok != 0;
-                if (!ok) break;
+                return all != 0;
+            };
+            auto build = [&](int li) {
+                bool ok = true;
+                const int b = li & 1;
+                const Tile t = tile_of(li);
                 const int n = list_adapters<NT>(a, t.row0, s_list + b * NT, s_ids + b * NT, s_runs, s_word);
                 if (builder == 0 && lane == 0) {
                     s_count[b] = n;
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
                     };
                     bool some = find();
                     if (some) ask();
-                    if (!(ok = mbar_wait(&t_go[s], go_phase >> s & 1u))) break;
+                    if (!(ok = __all_sync(FULL_MASK, mbar_wait(&t_go[s], go_phase >> s & 1u)))) break;   // (all lanes or none)
                     go_phase ^= 1u << s;
                     while (some) {
                         uint8_t* dst = sm + s * L::STAGE + L::OFF_T + i * 2 * L::SLAB_T + c * 32;
@@ -561,9 +564,10 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&list_empty[b]);
-            }
+                return ok;
+            };
+            if (!rounds_together(tiles, ready, all_of_us, build)) sflag[0] = 1;
             if (!waited) pdl_wait();             // this grid ends after the first one, whatever happens
-            if (!ok) sflag[0] = 1;
         }
     } else {   // ---------------- output, warps 2..5
         const int quad = warp & 3, tid = threadIdx.x - 64;
