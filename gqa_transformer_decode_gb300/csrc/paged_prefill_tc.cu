@@ -74,6 +74,7 @@
 #include <cudaTypedefs.h>
 
 #include "paged_groups.cuh"
+#include "rounds.h"
 #include "tc_common.cuh"
 
 namespace ember {
@@ -408,10 +409,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     // the CTA index (SHARED: the place in the line) after the it-th pair's: false when there is none left (or, ok = false, no answer)
     auto take_next = [&](int it, unsigned& cta, bool& ok, int nkt) {
         if (SPLIT) return false;
-        if (SHARED) {
-            cta += max(0, nkt);
-            return cta < pairs_all;
-        }
+        if (SHARED) return walk_on(cta, nkt, pairs_all);
         if (!wait_all(&next_full[it & 1], it >> 1)) {
             ok = false;
             return false;

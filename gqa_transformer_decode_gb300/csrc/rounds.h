@@ -1,5 +1,6 @@
-// rounds.h -- rounds of work that several warps begin together, each of which may give up in any
-// of them.  Plain C++, so that the way they end can be tested without a GPU.
+// rounds.h -- loops whose end is not to depend on what they find: rounds of work that several warps
+// begin together, each of which may give up in any of them, and walks along a line.  Plain C++, so
+// that the way they end can be tested without a GPU.
 #pragma once
 
 #ifdef __CUDACC__
@@ -24,6 +25,14 @@ EMBER_ROUNDS bool rounds_together(int n, Ready ready, All all, Work work) {
         ok = work(i);
     }
     return ok;
+}
+
+// From place `at` of a line on by `step`; false at the line's end, and where there is no step, so
+// that a walk ends even if what it reads changes under it.
+EMBER_ROUNDS bool walk_on(unsigned& at, int step, unsigned end) {
+    if (step <= 0 || (unsigned)step >= end - at) return false;
+    at += (unsigned)step;
+    return true;
 }
 
 }  // namespace ember

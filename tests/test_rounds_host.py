@@ -1,6 +1,7 @@
-"""How warps that begin rounds of work together end (csrc/rounds.h, which the builders of ember_adapter_project's tiles go by):
-whoever gives up, in whichever round and place, nobody is left waiting at the vote.  Threads stand for the warps here, a barrier
-with a time limit for the vote; no GPU."""
+"""How loops on the GPU end whatever they find (csrc/rounds.h), without a GPU.  Warps that begin rounds of work together, as the
+builders of ember_adapter_project's tiles do: whoever gives up, in whichever round and place, nobody is left waiting at the vote
+(threads stand for the warps, a barrier with a time limit for the vote).  Walks along a line, as the CTAs of a shared prefix
+make: places that nobody owns, which only arrays that change during the call can make, end them."""
 import os
 import shutil
 import subprocess
@@ -83,10 +84,44 @@ int main() {
 """
 
 
-@pytest.mark.skipif(not shutil.which("g++"), reason="needs g++")
-def test_nobody_is_left_at_the_vote(tmp_path):
+WALKS = r"""
+#include <cstdio>
+
+#include "rounds.h"
+
+int main() {
+    // steps from the place 3 of a line of 10, and where they lead (-1: the end)
+    const struct { int steps[4], places[4]; } walks[] = {
+        {{2, 1, 4, 9}, {5, 6, -1, 0}}, {{7, 0, 0, 0}, {-1, 0, 0, 0}}, {{6, 1, 0, 0}, {9, -1, 0, 0}}, {{100, 0, 0, 0}, {-1, 0, 0, 0}},
+        {{0, 0, 0, 0}, {-1, 0, 0, 0}}, {{-1, 0, 0, 0}, {-1, 0, 0, 0}}, {{2, 0, 0, 0}, {5, -1, 0, 0}}, {{2147483647, 0, 0, 0}, {-1, 0, 0, 0}}};
+    for (const auto& w : walks) {
+        unsigned at = 3;
+        for (int i = 0; i < 4; ++i) {
+            const bool on = ember::walk_on(at, w.steps[i], 10);
+            if (on != (w.places[i] >= 0) || (on && at != (unsigned)w.places[i])) return 1;
+            if (!on) break;
+        }
+    }
+    unsigned at = 4294967290u;                   // no sum beyond 32 bits
+    return ember::walk_on(at, 5, 4294967295u) || !ember::walk_on(at, 4, 4294967295u) || at != 4294967294u;
+}
+"""
+
+
+def run(tmp_path, program):
     src, exe = tmp_path / "rounds.cpp", tmp_path / "rounds"
-    src.write_text(PROGRAM)
+    src.write_text(program)
     subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Werror", "-pthread", "-I" + CSRC, str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
-    assert r.returncode == 0 and "ways to end" in r.stdout, r.stdout + r.stderr
+    assert r.returncode == 0, r.stdout + r.stderr
+    return r.stdout
+
+
+@pytest.mark.skipif(not shutil.which("g++"), reason="needs g++")
+def test_walks_end(tmp_path):
+    run(tmp_path, WALKS)
+
+
+@pytest.mark.skipif(not shutil.which("g++"), reason="needs g++")
+def test_nobody_is_left_at_the_vote(tmp_path):
+    assert "ways to end" in run(tmp_path, PROGRAM)
