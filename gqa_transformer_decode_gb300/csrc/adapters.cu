@@ -199,6 +199,81 @@ struct Block {
     }
 };
 
+// ---- values that are not finite ----
+// A product of a tile's adapter takes in neighbouring rows with others as zeros, and zero times an
+// infinity of B is not zero.  So where an output is not finite the outputs that B may have spoilt are
+// taken again, each from its own row and adapter alone: those that are not finite, of rows of W for
+// which some adapter of the tile's rows has a value in B that is not.  Slow (about 2 us an output and
+// warp at K 8192), but nothing where all is finite: one operation an output that sees it.
+__device__ __forceinline__ bool odd16(uint16_t x, bool bf16) { return bf16 ? (x & 0x7f80) == 0x7f80 : (x & 0x7c00) == 0x7c00; }
+struct AdMend {
+    int ids[256], named[256], n_named;   // the tile's rows' adapters, and each of them once
+    uint32_t rows[AD_M / 32];            // of W, a bit each
+};
+// Outputs [lo, hi) of a tile in eights (row c of x, rows f .. f + 7 of W: c * 16 + f / 8), by the whole CTA.
+template <class E>
+__device__ __noinline__ void take_again(const AdapterArgs& a, int row0, int m0, int lo, int hi, AdMend* s) {
+    const int tid = threadIdx.x, T = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    const int rows = min(a.nt, a.n - row0), RP = (a.R + 15) & ~15;
+    __syncthreads();
+    for (int c = tid; c < rows; c += T) {
+        const int x = a.ids[row0 + c];
+        s->ids[c] = x >= 0 && x < a.n_adapters ? x : -1;
+    }
+    if (tid < AD_M / 32) s->rows[tid] = 0;
+    if (tid == 0) s->n_named = 0;
+    __syncthreads();
+    for (int c = tid; c < rows; c += T) {
+        const int id = s->ids[c];
+        int k = c - 1;
+        while (k >= 0 && s->ids[k] != id) --k;
+        if (id >= 0 && k < 0) s->named[atomicAdd(&s->n_named, 1)] = id;   // (in no order: only marks follow)
+    }
+    __syncthreads();
+    for (int i = tid; i < s->n_named * AD_M; i += T) {
+        const int m = i % AD_M;
+        if (m0 + m >= a.N) continue;
+        const uint4* p = reinterpret_cast<const uint4*>(a.lb + ((long long)s->named[i / AD_M] * a.N + m0 + m) * a.R);
+        bool odd = false;
+        for (int r = 0; r < a.R / 8; ++r) {
+            const uint4 v = __ldg(p + r);
+            for (uint32_t u : {v.x, v.y, v.z, v.w}) odd |= odd16((uint16_t)u, E::bf16) | odd16((uint16_t)(u >> 16), E::bf16);
+        }
+        if (odd) atomicOr(&s->rows[m / 32], 1u << (m % 32));
+    }
+    __syncthreads();
+    for (int i = lo + warp; i < hi; i += T / 32) {
+        const int c = i / (AD_M / 8), f = i % (AD_M / 8) * 8, row = row0 + c, id = s->ids[c];
+        for (int m = f; m < f + 8; ++m) {
+            if (m0 + m >= a.N || !(s->rows[m / 32] >> (m % 32) & 1u)) continue;
+            float* o32 = static_cast<float*>(a.out) + row * a.ld_out + m0 + m;
+            uint16_t* o16 = static_cast<uint16_t*>(a.out) + row * a.ld_out + m0 + m;
+            if (a.out_f32 ? (__float_as_uint(__ldcg(o32)) & 0x7f800000u) != 0x7f800000u : !odd16(__ldcg(o16), E::bf16)) continue;
+            const uint4 *x = reinterpret_cast<const uint4*>(a.x + row * a.ld_x), *w = reinterpret_cast<const uint4*>(a.w + (long long)(m0 + m) * a.K);
+            float y = 0.f, u[8], v[8];
+            for (int k = lane; k < a.K / 8; k += 32) {
+                unpack8w<!E::bf16>(__ldg(x + k), u);
+                unpack8w<!E::bf16>(__ldg(w + k), v);
+                for (int j = 0; j < 8; ++j) y = fmaf(u[j], v[j], y);
+            }
+            if (id >= 0)
+                for (int r = lane; r < a.R; r += 32) {
+                    const uint16_t* t = a.t + (long long)row * 2 * RP + r / 16 * 32 + r % 16;
+                    const uint32_t two = (uint32_t)__ldcg(t) | (uint32_t)__ldcg(t + 16) << 16;
+                    const uint32_t b = a.lb[((long long)id * a.N + m0 + m) * a.R + r];
+                    const float hi = E::lo(two);         // (an infinity's second term is no number)
+                    y = fmaf(E::lo(b), odd16((uint16_t)two, E::bf16) ? hi : hi + E::hi(two), y);
+                }
+            y = warp_sum(y);
+            if (a.bias) y += E::lo((uint32_t)a.bias[m0 + m]);
+            if (lane == 0) {
+                if (a.out_f32) *o32 = y;
+                else *o16 = (uint16_t)E::pack(y, 0.f);
+            }
+        }
+    }
+}
+
 // Eight sums of a row of x.  First launch: ranks r .. r + 7 of its adapter, as two terms (and
 // zeros for the ranks that fill up a product); second: outputs m .. m + 7.  True: beyond f16.
 template <class E>
@@ -236,9 +311,9 @@ __device__ __forceinline__ void store_out(const AdapterArgs& a, int row, int m, 
 
 // (Two CTAs to an SM where they have room: one of each launch.)
 template <class E, int NT, bool LOW, bool FOLD>
-__global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(ad_threads(NT), NT <= 128 && !FOLD ? 2 : 1)
     k_adapter(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmOut, AdapterArgs a) {
+              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ AdapterArgs a) {
     using L = AdSmem<NT, LOW>;
     constexpr int S = L::STAGES;
     // TMEM: two accumulators, which take turns, or one and two and the sum
@@ -263,8 +338,9 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
     uint64_t* list_empty = list_full + 2;
     int* s_count = reinterpret_cast<int*>(list_empty + 2);   // [2] entries of the lists
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_count + 2);
-    int* sflag = reinterpret_cast<int*>(tmem_slot + 1);      // [0] failed, [1] stages issued, [2] consumed
-    static_assert((4 * S + 8) * 8 + 6 * 4 <= L::BARS, "barriers");
+    int* sflag = reinterpret_cast<int*>(tmem_slot + 1);      // [0] failed, [1] stages issued, [2] consumed, [3] an output is not finite
+    static_assert((4 * S + 8) * 8 + 7 * 4 <= L::BARS, "barriers");
+    static_assert(sizeof(AdMend) <= S * L::STAGE, "over the stages");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int CL = a.splits, rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;   // CTAs of a cluster
@@ -286,7 +362,7 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
             mbar_init(&list_full[b], 1);
             mbar_init(&list_empty[b], 2 + ad_builders(NT));   // copies, products, builders
         }
-        sflag[0] = sflag[1] = sflag[2] = 0;
+        sflag[0] = sflag[1] = sflag[2] = sflag[3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -359,6 +435,7 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
         return m < P * a.R && e < s_count[0] && s_list[e].adapter == s_ids[c];
     };
     bool bad = false;                            // f16: t beyond its range
+    float probe[4] = {0.f, 0.f, 0.f, 0.f};       // NaN once an output was not finite (four: a chain of one took 0.5 us)
     auto store = [&](const Tile& t, int c, int m, float (&y)[8]) {
         if (LOW) bad |= store_low<E>(a, t.row0 + c, m % a.R, s_list[t.e0 + m / a.R].scale, y);
         else store_out<E>(a, t.row0 + c, t.m0 + m, y);
@@ -657,6 +734,8 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
                         if (tid == 0) bulk_wait_read<1>();   // the slice before the last one has left
                         asm volatile("bar.sync 1, 128;" ::: "memory");
                     }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) probe[i & 3] = fmaf(y[i], 0.f, probe[i & 3]);
                     if (a.out_f32) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -747,12 +826,15 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) y[j] += add[j];
                 }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) probe[j & 3] = fmaf(y[j], 0.f, probe[j & 3]);
                 store(t, c, f, y);
             }
         }
         cluster_sync_all();                      // no CTA leaves while its shared memory is read
     }
     if (bad) raise_status(a.status, EMBER_ERR_RANGE);
+    if (!LOW && (probe[0] + probe[1]) + (probe[2] + probe[3]) != 0.f) sflag[3] = 1;
     if (!LOW) pdl_trigger();
 
     tc_fence_before();
@@ -765,6 +847,17 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 ? 2 : 1)
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(COLS));
+    }
+    if constexpr (!LOW) {
+        if (sflag[3] && !sflag[0]) {             // (the outputs are written, and nothing is left in flight)
+            pdl_wait();
+            for (int li = 0; li < tiles; ++li) {
+                const Tile t = tile_of(li);
+                const int all = min(a.nt, a.n - t.row0) * (AD_M / 8);
+                take_again<E>(a, t.row0, t.m0, (int)((long long)all * part / C), (int)((long long)all * (part + 1) / C),
+                              reinterpret_cast<AdMend*>(sm));
+            }
+        }
     }
 }
 

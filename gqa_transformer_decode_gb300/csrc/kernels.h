@@ -475,6 +475,8 @@ struct AdapterArgs {
     int n, N, K, R, n_adapters;
     const float* scale;          // [n_adapters] or nullptr (1)
     const uint16_t* bias;        // [N] or nullptr
+    const uint16_t *x, *w, *lb;  // [n][ld_x], [N][K], [n_adapters][N][R]
+    long long ld_x;
     uint16_t* t;                 // [n][R / 16 rounded up][2][16]: s_a A_a x in two terms
     void* out;                   // [n][ld_out], f32 or x's type
     long long ld_out;

@@ -91,6 +91,10 @@ ember_status ember_adapter_project(const ember_adapters* ad, const void* x, int6
     a.n_adapters = ad->n_adapters;
     a.scale = ad->scale;
     a.bias = static_cast<const uint16_t*>(bias);
+    a.x = static_cast<const uint16_t*>(x);
+    a.ld_x = ld_x;
+    a.w = static_cast<const uint16_t*>(w);
+    a.lb = static_cast<const uint16_t*>(ad->b);
     a.t = static_cast<uint16_t*>(workspace);
     a.out = out;
     a.ld_out = ld_out;

@@ -342,10 +342,10 @@ ember_status ember_logprobs(const void *logits, int32_t dtype, int32_t n, int32_
  * nearest are by 0.3e-6 to 1e-6); s_a A_a x is held as the sum of two values of the type (2^-17 relative for bf16, 2^-22 or
  * 2^-25 absolute for f16).
  * Element pointers are 16-byte aligned, scale, ids and status 4-byte; row strides
- * multiples of 8 elements; buffers may not overlap.  A b that is not finite makes
- * not finite not only the rows that name its adapter but also rows with others
- * that stand between two of those, as a product with zero does.  No
- * atomics: equal calls give equal bits.  Asynchronous on `stream`; no gradient.
+ * multiples of 8 elements; buffers may not overlap.  Values of an x, a, b or scale
+ * that are not finite reach the rows that read them and no others; outputs next to
+ * such a b's in a tile are taken again one by one, which is slow.  No
+ * atomics on results: equal calls give equal bits.  Asynchronous on `stream`; no gradient.
  * Host errors: INVALID_ARG, UNSUPPORTED, CAPACITY (workspace), CUDA. */
 typedef struct ember_adapters {
     const void *a, *b;
