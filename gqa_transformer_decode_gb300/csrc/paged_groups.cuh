@@ -36,6 +36,16 @@ __device__ __forceinline__ PtGroup pt_group(const PtGroups& a, int g) {
     r.tiles = (keys + PT_KEYS - 1) / PT_KEYS;
     return r;
 }
+// The keys that some of the rows sees, for a whole warp: the longest length.  (Rows of padding count:
+// to look whether a row is one, in an array that nothing else here needs, took 2 us.)
+__device__ __forceinline__ int pt_seen(const PtGroups& a, int row0, int rows) {
+    int seen = 0;
+    for (int i = row0 + (int)(threadIdx.x & 31); i < row0 + rows; i += 32) {
+        const int len = a.lens[i];
+        if (len <= a.most) seen = max(seen, len);
+    }
+    return __reduce_max_sync(FULL_MASK, seen);
+}
 // Where 32 groups' pairs and key tiles begin, each lane its own group's, after those of `pairs` and `line`
 // before; both are moved on.
 __device__ __forceinline__ PtGroup pt_scan(const PtGroups& a, int g0, unsigned& pairs, unsigned& line, unsigned& pair0,

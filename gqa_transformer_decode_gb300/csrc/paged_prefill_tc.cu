@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         const uint32_t empty_at = smem_u32(kv_empty);
         bool ok = true, asked = false;
         for (;; ++it) {
-            const PtPair p = pair_at(cta, part == 0);
+            PtPair p = pair_at(cta, part == 0);
             if (p.nkt > 0) {
                 // The page of the lane's box of tile j, if some row sees its keys.  What it
                 // loads is looked at two tiles later, so that nothing waits for it.
@@ -460,6 +460,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     return e;
                 };
                 Entry e0 = look_up(0), e1 = look_up(1);
+                if (SHARED) {                          // (asked for beside the pages)
+                    p.end = min(p.end, pt_seen(pt_groups(a, QT), p.row0, p.tokens));
+                    e0.seen &= p.key0(0) + lane * box < p.end;
+                    e1.seen &= p.key0(1) + lane * box < p.end;
+                }
                 const int g = uniform(p.g);
                 ok = pairs == 0 || wait_all(q_empty, pairs - 1);
                 if (!ok) break;
@@ -534,8 +539,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         int base = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            const PtPair p = pair_at(cta, false);
+            PtPair p = pair_at(cta, false);
             const int nkt = max(0, p.nkt);
+            if (SHARED && nkt > 0) p.end = min(p.end, pt_seen(pt_groups(a, QT), p.row0, p.tokens));
             for (int j = 0; ok && j < nkt; ++j) {
                 const int i = 2 * (base + j) + 1, s = i % NS, key0 = p.key0(j);
                 ok = wait_all(&v_raw[s >> 1], i / NS);

@@ -473,13 +473,14 @@ ember_status ember_paged_decode(const ember_paged_kv *kv, const void *q, int64_t
  * [n_groups+1], groups[0] = 0, groups[n_groups] = B) find their keys j < shared[i] in
  * the pages of table row prefixes[i] and the others, up to lens[b], in their own
  * row's (seqs[b]).  shared [n_groups] is any number, whole pages or not, and may
- * exceed a row's lens[b]; entries of a row's own pages that hold only shared keys
+ * exceed a row's lens[b]: beyond the longest of a group's, rows of padding among them,
+ * its prefix may hold anything; entries of a row's own pages that hold only shared keys
  * are not read.  Every key is seen: there is no window.  What the rows of a group
  * read together is read once for all of them; n_groups is at most B.  Calls of few
  * keys (by the table's width), of fewer than three rows a group on average or with a
  * scale that is not positive read a row's keys for each row, with the same result up
- * to rounding.  As in prefill, a K or V value of a prefix that is not finite may make
- * its whole group not finite.
+ * to rounding.  As in prefill, a K or V value of a prefix that is not finite, and that
+ * some row of a group sees, may make the whole group not finite.
  * A row outside every group, a prefixes entry outside [0, n_seqs) and a shared entry
  * outside [0, table_width*page_size] raise INVALID_ARG and CAPACITY, and the rows
  * are skipped.  All else as in ember_paged_decode, with
