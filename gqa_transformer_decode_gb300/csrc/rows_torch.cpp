@@ -85,12 +85,20 @@ struct Adapters {
     Tensor a, b, scale, status;
     ember_stream_t home;             // the stream that status was allocated on
 };
+// Where the tensors lie and whether they are what they were: at every call, since a tensor may get
+// other storage (t.data = ..) or be asked for its gradient at any time.
 Adapters& adapters_of(PyObject* o) {
     auto* p = static_cast<Adapters*>(PyCapsule_GetPointer(o, "ember.adapters"));
     if (!p) throw python_error();
-    no_gradient(p->a, "a");          // at every call: a tensor may be asked for its gradient at any time
+    const int64_t n = p->c.n_adapters, R = p->c.rank;
+    no_gradient(p->a, "a");
     no_gradient(p->b, "b");
-    if (p->scale.defined()) no_gradient(p->scale, "scale");
+    p->c.a = flat(*p, p->a, "a", p->dtype, {n, R, p->K});
+    p->c.b = flat(*p, p->b, "b", p->dtype, {n, p->N, R});
+    if (p->scale.defined()) {
+        no_gradient(p->scale, "scale");
+        p->c.scale = static_cast<const float*>(flat(*p, p->scale, "scale", at::kFloat, {n}));
+    }
     return *p;
 }
 

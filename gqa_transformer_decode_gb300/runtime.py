@@ -291,7 +291,8 @@ class Adapters:
     b      the same type, [n_adapters, N, rank]
     scale  f32 [n_adapters] (default: 1 each)
 
-    All contiguous and the caller's; they may change between calls.  Streams, gradients and errors as in PagedKV:
+    All contiguous and the caller's; they may change between calls, and be moved to other storage of the same type,
+    shape and device (t.data = ..), but not be replaced: the attributes are read-only.  Streams, gradients and errors as in PagedKV:
     calls are asynchronous on `stream` (default: the current one), tensors that require a gradient are refused
     unless gradients are off, device-side errors are read with sync_status().
     """
@@ -300,11 +301,13 @@ class Adapters:
         for t, what in ((a, "a"), (b, "b")):
             if not isinstance(t, torch.Tensor) or not t.is_cuda:
                 raise ValueError(f"{what} must be a tensor on a CUDA device")
-        self.a, self.b, self.scale, self.device = a, b, scale, a.device
+        self._abs, self.device = (a, b, scale), a.device
         self.status = _status_word(self.device)
         self._t = _rows_torch()
         with torch.cuda.device(self.device):
             self._adapters = self._t.adapters(a, b, scale, self.status)
+
+    a, b, scale = (property(lambda self, i=i: self._abs[i]) for i in range(3))
 
     def project(self, x, w, ids, bias=None, out=None, out_dtype=None, workspace=None, stream=None):
         """x [n, K] through the projection w [N, K] (+ bias [N]) with the adapter ids[i] of row i beside it (int32
