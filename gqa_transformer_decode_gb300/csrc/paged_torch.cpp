@@ -23,7 +23,7 @@ struct Cache {
     int32_t* status;
     c10::DeviceIndex device;
     at::ScalarType dtype;
-    Tensor k_pages, v_pages, status_word;
+    Tensor k_pages, v_pages, table, status_word;
     ember_stream_t home = nullptr;   // the stream that status_word was allocated on
     // decode's workspace of the last (B, heads): the query is a function of these
     int64_t ws_rows = -1, ws_heads = -1;
@@ -47,12 +47,30 @@ Rows rows(const Cache& c, const Tensor& t, const char* what, at::ScalarType dtyp
     return {t.data_ptr(), n > 1 ? t.stride(0) : heads * D};
 }
 
+void* pages(const Cache& c, const Tensor& t, const char* what) {
+    on_device(c, t, what);
+    const int64_t shape[4] = {c.kv.n_pages, c.kv.n_kv_heads, c.kv.page_size, c.kv.head_dim};
+    const int64_t strides[4] = {c.kv.page_stride, c.kv.head_stride, c.kv.row_stride, 1};
+    bool same = t.scalar_type() == c.dtype && t.sizes() == at::IntArrayRef(shape, 4);
+    for (int i = 0; same && i < 4; ++i) same = shape[i] == 1 || t.stride(i) == strides[i];
+    if (!same)
+        bad(std::string(what) + " must keep the type, shape and strides that the cache was made with, not become " + describe(t));
+    return t.data_ptr();
+}
+
 Cache& cache_of(PyObject* o) {
     auto* c = static_cast<Cache*>(PyCapsule_GetPointer(o, "ember.paged"));
     if (!c) throw python_error();
-    if (c->k_pages.defined()) {   // at every call: a tensor may be asked for its gradient at any time
+    // Where the tensors lie and whether they are what they were: at every call, since a tensor may
+    // get other storage (t.data = ..) or be asked for its gradient at any time.
+    if (c->k_pages.defined()) {
         no_gradient(c->k_pages, "k_pages");
         no_gradient(c->v_pages, "v_pages");
+    }
+    if (c->table.defined()) {
+        c->kv.k = pages(*c, c->k_pages, "k_pages");
+        c->kv.v = pages(*c, c->v_pages, "v_pages");
+        c->kv.table = static_cast<const int32_t*>(flat(*c, c->table, "table", at::kInt, {c->kv.n_seqs, c->kv.table_width}));
     }
     return *c;
 }
@@ -287,16 +305,17 @@ PyObject* shared_workspace_bytes(PyObject*, PyObject* const* a, Py_ssize_t nargs
     });
 }
 
-// cache(address of an ember_paged_kv, address of the status word, device index[, k_pages, v_pages[, status word]])
+// cache(address of an ember_paged_kv, address of the status word, device index[, k_pages, v_pages[, status word, table]])
 PyObject* cache(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-    return guarded(nargs, nargs == 5 || nargs == 6 ? nargs : 3, [&]() -> PyObject* {
-        Tensor k_pages, v_pages, status_word;
+    return guarded(nargs, nargs == 5 || nargs == 7 ? nargs : 3, [&]() -> PyObject* {
+        Tensor k_pages, v_pages, table, status_word;
         if (nargs >= 5) k_pages = tensor(a[3], "k_pages"), v_pages = tensor(a[4], "v_pages");
-        if (nargs == 6) status_word = tensor(a[5], "status");
+        if (nargs == 7) status_word = tensor(a[5], "status"), table = any_tensor(a[6], "table");
         auto* c = new Cache;
         c->k_pages = k_pages;
         c->v_pages = v_pages;
         c->status_word = status_word;
+        c->table = table;
         c->kv = *static_cast<const ember_paged_kv*>(PyLong_AsVoidPtr(a[0]));
         c->status = static_cast<int32_t*>(PyLong_AsVoidPtr(a[1]));
         c->device = (c10::DeviceIndex)PyLong_AsLong(a[2]);

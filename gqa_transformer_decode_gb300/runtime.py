@@ -155,7 +155,8 @@ class PagedKV:
                       transposed view)
     table             int32 [n_seqs, table_width], the sequences' pages
 
-    The tensors stay the caller's and may change between calls; the object
+    The tensors stay the caller's and may change between calls, and be moved to
+    other storage of the same type, shape, strides and device (t.data = ..); the object
     keeps references and one int32 status word.  Calls are asynchronous on
     `stream` (default: the current stream of the pages' device); device-side
     errors are read with sync_status().  A stream that is passed does not wait
@@ -194,7 +195,7 @@ class PagedKV:
         self.status = _status_word(self.device)
         self._t = _paged_torch()
         self._cache = self._t.cache(C.addressof(c), self.status.data_ptr(), k_pages.get_device(), k_pages, v_pages,
-                                    self.status)
+                                    self.status, table)
 
     def _on(self, stream):
         if stream.device != self.device:

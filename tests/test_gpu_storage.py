@@ -56,3 +56,69 @@ def test_adapters_are_not_replaced_behind_the_objects_back():
         with pytest.raises(AttributeError):
             setattr(c.ad, name, None)
     c.check(c.run())
+
+
+class Paged:
+    """A cache of four sequences, and calls of each operator on it."""
+
+    def __init__(self, seed, row_major=False):
+        from gqa_transformer_decode_gb300 import runtime
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+        self.k, self.v = ((r(16, 16, 2, 64).transpose(1, 2) if row_major else r(16, 2, 16, 64)) for _ in range(2))
+        self.table = torch.arange(16, dtype=torch.int32, device="cuda").view(4, 4).flip(seed % 2).contiguous()
+        self.cache = runtime.PagedKV(self.k, self.v, self.table)
+
+    def calls(self, q):
+        c = self.cache
+        cos = torch.ones(64, 32, device="cuda")
+        c.append(q[:, :2], q[:, 2:4], ints([0, 1, 2, 3]), ints([5, 6, 7, 8]), cos, torch.zeros_like(cos))
+        return [c.decode(q, ints([64, 33, 20, 9])), c.prefill(q, ints([0, 2, 4]), ints([50, 64])),
+                c.decode_shared(q, ints([64, 33, 40, 50]), ints([0, 4]), ints([32]), ints([0]))]
+
+
+@pytest.mark.parametrize("row_major", [False, True])
+def test_a_cache_in_other_storage(row_major):
+    p, o = Paged(0, row_major), Paged(1, row_major)
+    q = torch.randn(4, 8, 64, device="cuda").bfloat16()
+    want = o.calls(q)
+    assert not torch.equal(p.calls(q)[0], want[0])
+    old = Paged(1, row_major)                    # as o was before its append
+    for name in ("k", "v", "table"):
+        src = getattr(old, name)
+        new = torch.empty_like(src)              # of the same strides
+        new.copy_(src)
+        getattr(p, name).data = new
+    gc.collect()
+    junk = filled(p.k, p.v) + [torch.full_like(p.table, -5) for _ in range(4)]
+    got = p.calls(q)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(junk) == 12
+    assert p.cache.sync_status() == 0 and torch.equal(p.k, o.k) and torch.equal(p.v, o.v)
+
+
+@pytest.mark.parametrize("name,new,says", [
+    ("k", lambda t: t.half(), "k_pages must keep"), ("v", lambda t: t[:8].clone(), "v_pages must keep"),
+    ("v", lambda t: t.transpose(1, 2).contiguous().transpose(1, 2), "v_pages must keep"), ("k", lambda t: t.cpu(), "k_pages must be on cuda"),
+    ("table", lambda t: t.long(), "table must be"), ("table", lambda t: t[:2].clone(), "table must be")])
+def test_a_cache_that_became_another(name, new, says):
+    p = Paged(0)
+    q = torch.randn(4, 8, 64, device="cuda").bfloat16()
+    want = p.calls(q)
+    t = getattr(p, name)
+    was = t.data
+    t.data = new(t)
+    for call in (lambda: p.calls(q), lambda: p.cache.decode(q, ints([64, 33, 20, 9])),
+                 lambda: p.cache.prefill(q, ints([0, 2, 4]), ints([50, 64]))):
+        with pytest.raises(ValueError, match=says):
+            call()
+    t.data = was
+    assert all(torch.equal(a, b) for a, b in zip(p.calls(q), want))
+
+
+def test_page_dimensions_of_one_have_any_stride():
+    from gqa_transformer_decode_gb300 import runtime
+    k = torch.randn(4, 1, 16, 64, device="cuda").bfloat16()
+    v = torch.as_strided(k.clone(), k.shape, (16 * 64, 8, 64, 1))
+    cache = runtime.PagedKV(k, v, torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4))
+    q = torch.randn(1, 4, 64, device="cuda").bfloat16()
+    assert cache.decode(q, ints([50])).isfinite().all()
