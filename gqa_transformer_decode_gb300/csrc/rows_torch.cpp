@@ -30,16 +30,6 @@ int64_t matrix(const Tensor& t, const char* what) {
     return t.size(0) > 1 ? t.stride(0) : t.size(1);
 }
 
-// A contiguous tensor on a part of another's memory: five outputs cost one allocation.
-Tensor piece(const Tensor& buffer, int64_t& at, at::IntArrayRef shape, at::ScalarType dtype) {
-    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(),
-                                                        c10::scalarTypeToTypeMeta(dtype));
-    t.unsafeGetTensorImpl()->set_storage_offset(at / 4);
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-    at += (t.numel() * 4 + 15) & ~(int64_t)15;
-    return t;
-}
-
 // logprobs(logits, ids, top, temperature) -> (logprob, rank, entropy, top_ids, top_logprobs)
 PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return guarded(nargs, 4, [&]() -> PyObject* {
@@ -55,11 +45,8 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         const double t = real(a[3]);
         if (top < 0) bad("top must not be negative");
         const c10::cuda::OptionalCUDAGuard on(c10::Device(at::kCUDA, p.device));
-        const Tensor buffer = make(p, {n * (3 + 2 * (int64_t)top) + 20}, at::kFloat);   // + what rounding up to 16 bytes takes
-        int64_t used = 0;
-        Tensor lp, rank, entropy = piece(buffer, used, {n}, at::kFloat), best = piece(buffer, used, {n, top}, at::kInt),
-                         best_lp = piece(buffer, used, {n, top}, at::kFloat);
-        if (ids) lp = piece(buffer, used, {n}, at::kFloat), rank = piece(buffer, used, {n}, at::kInt);
+        Tensor lp, rank, entropy = make(p, {n}, at::kFloat), best = make(p, {n, top}, at::kInt), best_lp = make(p, {n, top}, at::kFloat);
+        if (ids) lp = make(p, {n}, at::kFloat), rank = make(p, {n}, at::kInt);
         auto at_of = [](const Tensor& x) { return x.defined() ? x.data_ptr() : nullptr; };
         check(f_logprobs(l.data_ptr(), type, count(n, "logits"), count(V, "logits"), ld, (float)t, id, top,
                          static_cast<float*>(at_of(lp)), static_cast<int32_t*>(at_of(rank)), static_cast<float*>(at_of(entropy)),
