@@ -624,11 +624,11 @@ bool paged_prefill_maps(const PagedPrefillArgs& a, PagedPrefillMaps& m);
 cudaError_t launch_paged_prefill_tc(const PagedPrefillArgs& a, const PagedPrefillMaps& m, int sms, cudaStream_t s);
 
 // The partials that launch_paged_shared leaves: `head` floats (int2 {tiles of a CTA, tiles of
-// all}, then for each group {its first pair, its first tile}), [slots][256][D] sums, and
-// [slots][256] {m, l}.  A pair holds rows_per_pair rows of a group for one kv head, row
-// (i, h) of them at (i / (half) * 128 + i % half * G + h), half = rows_per_pair / 2;
-// pairs of a group stand by kv head, then by rows, each with ceil(shared / 64) tiles.  What
-// CTA c has of pair p lies in slot p + c.
+// all}, then for each group {its first slot, its first tile}), [slots][G][D] sums, and
+// [slots][G] {m, l}.  A pair holds rows_per_pair rows of a group at most, for one kv head; pairs
+// of a group stand by kv head, then by rows, each with ceil(shared / 64) tiles, and a row has
+// a slot for each kv head in that order.  What CTA c has of a row lies rows_per_pair * c slots
+// further.
 struct PagedSharedWs {
     int head, slots, rows_per_pair;
     size_t floats;

@@ -46,27 +46,28 @@ __device__ __forceinline__ int pt_seen(const PtGroups& a, int row0, int rows) {
     }
     return __reduce_max_sync(FULL_MASK, seen);
 }
-// Where 32 groups' pairs and key tiles begin, each lane its own group's, after those of `pairs` and `line`
-// before; both are moved on.
-__device__ __forceinline__ PtGroup pt_scan(const PtGroups& a, int g0, unsigned& pairs, unsigned& line, unsigned& pair0,
-                                           unsigned& line0) {
+// Where 32 groups' rows (each for every kv head) and key tiles begin, each lane its own group's, after
+// those of `rows` and `line` before; both are moved on, and the number of pairs.
+__device__ __forceinline__ PtGroup pt_scan(const PtGroups& a, int g0, unsigned& pairs, unsigned& rows, unsigned& line,
+                                           unsigned& row0, unsigned& line0) {
     const int lane = threadIdx.x & 31;
     const PtGroup r = pt_group(a, g0 + lane);
-    const unsigned np = (unsigned)r.nx * a.NKV, nl = np * (unsigned)r.tiles;
-    pair0 = np;
+    const unsigned np = (unsigned)r.nx * a.NKV, nr = (unsigned)r.nq * a.NKV, nl = np * (unsigned)r.tiles;
+    pairs += __reduce_add_sync(FULL_MASK, np);
+    row0 = nr;
     line0 = nl;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const unsigned x = __shfl_up_sync(FULL_MASK, pair0, o), y = __shfl_up_sync(FULL_MASK, line0, o);
+        const unsigned x = __shfl_up_sync(FULL_MASK, row0, o), y = __shfl_up_sync(FULL_MASK, line0, o);
         if (lane >= o) {
-            pair0 += x;
+            row0 += x;
             line0 += y;
         }
     }
-    const unsigned all_p = __shfl_sync(FULL_MASK, pair0, 31), all_l = __shfl_sync(FULL_MASK, line0, 31);
-    pair0 += pairs - np;
+    const unsigned all_r = __shfl_sync(FULL_MASK, row0, 31), all_l = __shfl_sync(FULL_MASK, line0, 31);
+    row0 += rows - nr;
     line0 += line - nl;
-    pairs += all_p;
+    rows += all_r;
     line += all_l;
     return r;
 }

@@ -71,6 +71,9 @@
 // its output, stand in registers at once, so a row's thread needs more of them
 // (200) than the other warps (104).  Every mbarrier wait is bounded; a timeout
 // raises EMBER_ERR_TIMEOUT, the CTA drains its copies and frees TMEM.
+#include <algorithm>
+#include <climits>
+
 #include <cudaTypedefs.h>
 
 #include "paged_groups.cuh"
@@ -245,19 +248,19 @@ __device__ __forceinline__ PtGroups pt_groups(const PagedPrefillArgs& a, int QT)
     return PtGroups{a.cu, a.shared, a.seqs, a.lens, a.B, a.n, a.c.n_seqs, a.c.NKV, 2 * QT, (long long)a.c.width << a.c.page_shift};
 }
 // The line's length and a CTA's share of it; one warp of the grid leaves what the join needs
-// to find a pair's partials: the share, then each group's first pair and place in the line.
+// to find a pair's partials: the share, then each group's first slot and place in the line.
 __device__ __forceinline__ void pt_line(const PagedPrefillArgs& a, const PtGroups& gs, bool leave, unsigned& each, unsigned& lo, unsigned& hi) {
     const int lane = threadIdx.x & 31;
-    unsigned pairs = 0, line = 0;
+    unsigned pairs = 0, rows = 0, line = 0;
     int2* head = reinterpret_cast<int2*>(a.ws);
     float own = 0.f;           // the rows' own keys, about
     for (int b = lane; b < a.n; b += 32) own += max(0, a.lens[b]);
     for (int g0 = 0; g0 < a.B; g0 += 32) {
-        unsigned pair0, line0;
-        const PtGroup r = pt_scan(gs, g0, pairs, line, pair0, line0);
+        unsigned row0, line0;
+        const PtGroup r = pt_scan(gs, g0, pairs, rows, line, row0, line0);
         own -= (float)r.nq * r.keys;
         const int g = g0 + lane;
-        if (leave && g < a.B) head[1 + g] = make_int2((int)pair0, (int)line0);
+        if (leave && g < a.B) head[1 + g] = make_int2((int)row0, (int)line0);
     }
     own = fmaxf(0.f, warp_sum(own));
     const int sms = prefix_sms(line, pairs, own * a.c.NKV * a.c.D * 4.f, gridDim.x);
@@ -272,10 +275,10 @@ __device__ __forceinline__ PtPair pt_shared(const PtGroups& a, int QT, unsigned 
     p.nkt = -1;
     p.tokens = 0;
     if (at >= hi) return p;
-    unsigned pairs = 0, line = 0;
+    unsigned pairs = 0, rows = 0, line = 0;
     for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
-        unsigned pair0, line0;
-        const PtGroup mine = pt_scan(a, g0, pairs, line, pair0, line0);
+        unsigned row0, line0;
+        const PtGroup mine = pt_scan(a, g0, pairs, rows, line, row0, line0);
         const unsigned hit =
             __ballot_sync(FULL_MASK, at >= line0 && at - line0 < (unsigned)mine.nx * a.NKV * (unsigned)mine.tiles);
         if (!hit) continue;
@@ -293,8 +296,9 @@ __device__ __forceinline__ PtPair pt_shared(const PtGroups& a, int QT, unsigned 
         p.first = p.sinks = p.ns = p.wb = 0;
         p.j0 = (int)(off % (unsigned)r.tiles);
         p.nkt = (int)min((unsigned)(r.tiles - p.j0), hi - at);
-        // pairs and CTAs both only rise along the line, one of them at each step: no two share a slot
-        p.slot = (int)__shfl_sync(FULL_MASK, pair0, src) + pi + (int)blockIdx.x;
+        // a slot for each of the pair's rows, after those of all pairs before, and a pair's rows further for
+        // each CTA: pairs and CTAs both only rise along the line, one of them at each step, so no two share one
+        p.slot = (int)__shfl_sync(FULL_MASK, row0, src) + p.g * r.nq + x * 2 * QT + (int)blockIdx.x * 2 * QT;
         break;
     }
     return p;
@@ -842,8 +846,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             break;
         }
         if (SHARED) {   // the rows as they are; joined by another kernel
-            const bool store = live && (unsigned)p.slot < (unsigned)a.slots;
-            float* own = store ? a.ws + a.ws_head + ((size_t)p.slot * (2 * PT_ROWS) + t * PT_ROWS + r) * D : nullptr;
+            const size_t at = (size_t)(unsigned)p.slot * G + t * QT * G + r;   // (slots are of a token's G rows)
+            const bool store = live && at < (size_t)a.slots * G;
+            float* own = store ? a.ws + a.ws_head + at * D : nullptr;
             if (ok && nkt > 0) {
                 const int last = base + nkt - 1;
                 ok = wait_all(&o_full[2 * t + (last & 1)], last >> 1);
@@ -870,8 +875,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                         }
                     }
                     if (store)
-                        reinterpret_cast<float2*>(a.ws + a.ws_head + (size_t)a.slots * (2 * PT_ROWS) * D)[(size_t)p.slot * (2 * PT_ROWS) + t * PT_ROWS + r] =
-                            make_float2(m, l);
+                        reinterpret_cast<float2*>(a.ws + a.ws_head + (size_t)a.slots * G * D)[at] = make_float2(m, l);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&o_free[t]);
@@ -1037,9 +1041,9 @@ PagedSharedWs paged_shared_ws(int B, int n_groups, int NH, int NKV, int D, int s
     const int per = 2 * (PT_ROWS / (NH / NKV));
     PagedSharedWs w;
     w.head = (2 * (1 + n_groups) + 3) & ~3;
-    w.slots = (B / per + n_groups) * NKV + sms;        // at most one more pair than full ones for each group
+    w.slots = (int)std::min<long long>((long long)B * NKV + (long long)sms * per, INT_MAX);
     w.rows_per_pair = per;
-    w.floats = w.head + (size_t)w.slots * (2 * PT_ROWS) * (D + 2);
+    w.floats = w.head + (size_t)w.slots * (NH / NKV) * (D + 2);
     return w;
 }
 

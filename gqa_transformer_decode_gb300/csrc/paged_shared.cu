@@ -76,10 +76,10 @@ __global__ void __launch_bounds__(PD_THREADS, pd_ctas_per_sm(HT)) k_shared_tail(
     // as many CTAs as have room on the SMs that the prefixes leave
     const PtGroups gs{a.groups, a.shared, a.prefixes, a.lens, a.n_groups, a.B, a.c.n_seqs, NKV, a.prefix_rows,
                       (long long)a.c.width << a.c.page_shift};
-    unsigned pairs = 0, tiles = 0;
+    unsigned pairs = 0, rows = 0, tiles = 0;
     for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
-        unsigned pair0, line0;
-        (void)pt_scan(gs, g0, pairs, tiles, pair0, line0);
+        unsigned row0, line0;
+        (void)pt_scan(gs, g0, pairs, rows, tiles, row0, line0);
     }
     const int per_sm = pd_ctas_per_sm(HT), sms = (int)gridDim.x / per_sm;
     const int beside = prefix_sms(tiles, pairs, (float)line * (KEYS * DP * 4), sms);
@@ -227,12 +227,11 @@ __global__ void __launch_bounds__(SJ_THREADS) k_shared_join(PagedDecodeArgs a, i
     find_groups(a, row, of);
     const int group = of[0];
     const SeqBlocks s = seq_blocks<16, PD_TAIL>(a, b, a.seqs ? a.seqs[b] : b, a.lens[b], group, false);
-    int pi = 0, at = 0;                          // the pair of row tiles among its group's, the row in it
+    int pi = 0, at = 0;                          // the pair of row tiles among its group's, the row's slot
     if (s.zero && s.from > 0) {
-        const int row0 = a.groups[group], nx = (a.groups[group + 1] - row0 + a.prefix_rows - 1) / a.prefix_rows;
-        const int i = b - row0, r = i % a.prefix_rows, half = a.prefix_rows / 2;
-        pi = g * nx + i / a.prefix_rows;
-        at = r / half * 128 + r % half * G;
+        const int row0 = a.groups[group], nq = a.groups[group + 1] - row0, i = b - row0;
+        pi = g * ((nq + a.prefix_rows - 1) / a.prefix_rows) + i / a.prefix_rows;
+        at = g * nq + i;
     }
     pdl_wait();
     if (!s.zero) return;                         // the row is left as it is
@@ -244,15 +243,17 @@ __global__ void __launch_bounds__(SJ_THREADS) k_shared_join(PagedDecodeArgs a, i
     if (s.from > 0) {
         const unsigned tiles = (unsigned)(s.from + 63) / 64, each = max(1, line.x), p0 = (unsigned)first.y + (unsigned)pi * tiles;
         np = (int)((p0 + tiles - 1) / each - p0 / each) + 1;
-        slot0 = first.x + pi + (int)(p0 / each);
-        if (slot0 < 0 || np < 0 || np > a.prefix_slots || slot0 > a.prefix_slots - np) np = 0;
+        const long long s0 = (long long)first.x + at + (long long)(p0 / each) * a.prefix_rows;
+        if (s0 < 0 || np < 0 || s0 + (long long)(np - 1) * a.prefix_rows >= a.prefix_slots) np = 0;
+        else slot0 = (int)s0;
     }
     int no = rec.y;                              // the row's own
     const int slots = a.B * NKV + warps;
     if (no < 0 || no > slots || rec.x < 0 || rec.x > slots - no) no = 0;
     const float* own = tail_partials(a) + (size_t)rec.x * G * (D + 2);
-    const float* sums = a.prefix + a.prefix_head + ((size_t)slot0 * 256 + at) * D;
-    const float2* ml = reinterpret_cast<const float2*>(a.prefix + a.prefix_head + (size_t)a.prefix_slots * 256 * D) + (size_t)slot0 * 256 + at;
+    const float* sums = a.prefix + a.prefix_head + (size_t)slot0 * G * D;
+    const float2* ml = reinterpret_cast<const float2*>(a.prefix + a.prefix_head + (size_t)a.prefix_slots * G * D) + (size_t)slot0 * G;
+    const size_t apart = (size_t)a.prefix_rows * G;   // from one CTA's partial to the next one's
     const int parts = np + no;
     // Each thread takes four dimensions of a head and every turns-th partial, four at a time, against
     // a maximum of its own; the threads of one place are joined at the end.
@@ -284,8 +285,8 @@ __global__ void __launch_bounds__(SJ_THREADS) k_shared_join(PagedDecodeArgs a, i
                     s2[k] = make_float2(SOFTMAX_FLOOR, 0.f);
                     x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (i < np) {
-                        s2[k] = __ldcg(ml + (size_t)i * 256 + h);
-                        x[k] = __ldcg(reinterpret_cast<const float4*>(sums + ((size_t)i * 256 + h) * D + d));
+                        s2[k] = __ldcg(ml + i * apart + h);
+                        x[k] = __ldcg(reinterpret_cast<const float4*>(sums + (i * apart + h) * D + d));
                     } else if (i < parts) {
                         const float2* p = reinterpret_cast<const float2*>(own + ((size_t)(i - np) * G + h) * (D + 2));
                         const float2 u = __ldcg(p + 1 + d / 2), v = __ldcg(p + 2 + d / 2);
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(SJ_THREADS) k_shared_join(PagedDecodeArgs a, i
 // and 17.8, 69 MB 19.5 and 18.0, 143 MB 26.9 and 18.1; and with fewer than three rows a group on
 // average: 64 rows of 4096 shared and 200 own keys take 150 us so, apart 108 in groups of 2 and 81
 // in groups of 3; but 1024 rows of 256 and 64 keys 258 so, apart 413 in groups of 2, 234 of 3 and
-// 190 of 4, with a gigabyte of partials.
+// 190 of 4.
 constexpr double PD_TOGETHER = 48e6;
 constexpr int PD_APART_ROWS = 3;
 
