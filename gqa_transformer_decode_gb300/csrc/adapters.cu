@@ -51,7 +51,7 @@ constexpr int AD_LD = AD_M + 4;                  // their distance in shared mem
 // accumulator takes at most AD_FOLD blocks of K (64 steps) before the output warps add it to a sum in
 // TMEM, rounded to nearest, under the next blocks' products where there is room for a second
 // accumulator.  Off by 1.1e-6 of the norm, by 0.57e-6 with 8 blocks; 4096 rows at K 8192 by 9.3e-6 in one
-// accumulator.  Outputs of 16 bits do without: their own rounding is 1.6e-3 or 2e-4.
+// accumulator.  The first launch's, whose t's rounding to two terms is of the same size, likewise.  Outputs of 16 bits do without: their own rounding is 1.6e-3 or 2e-4.
 constexpr int AD_FOLD = 16;
 
 template <int NT, bool LOW>
@@ -763,10 +763,9 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 && !FOLD ? 2 : 1)
             }
             const int f = tid % 16 * 8;          // this thread's 8 ranks
             for (int c = 0; c < rows; c += AD_SLICE) {
-                uint32_t r[AD_SLICE];
-                tmem_ld16(acc + c, r);
-                if (NT >= AD_SLICE) tmem_ld16(acc + c + 16, r + 16);
-                tmem_ld_wait();
+                float y[AD_SLICE / 16][16];
+                sums_of(acc, some, more, c, y[0]);
+                if (NT >= AD_SLICE) sums_of(acc, some, more, c + 16, y[1]);
                 if (c + AD_SLICE >= rows) {
                     tc_fence_before();
                     __syncwarp();
@@ -774,7 +773,7 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 && !FOLD ? 2 : 1)
                 }
 #pragma unroll
                 for (int i = 0; i < AD_SLICE; ++i)
-                    if (NT >= AD_SLICE || i < 16) s_out[i * AD_LD + quad * 32 + lane] = __uint_as_float(r[i]);
+                    if (NT >= AD_SLICE || i < 16) s_out[i * AD_LD + quad * 32 + lane] = y[i / 16][i % 16];
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 for (int i = tid / 16; i < min(AD_SLICE, rows - c); i += 8) {
                     if (!wanted(t, c + i, f)) continue;
@@ -930,8 +929,7 @@ cudaError_t launch_form(const CUtensorMap& w, const CUtensorMap& x, const CUtens
 template <class E, int NT, bool LOW>
 cudaError_t launch_nt(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& b, const CUtensorMap& o, const AdapterArgs& a,
                       int grid, bool fold, cudaStream_t s) {
-    if constexpr (!LOW)
-        if (fold) return launch_form<E, NT, LOW, true>(w, x, b, o, a, grid, s);
+    if (fold) return launch_form<E, NT, LOW, true>(w, x, b, o, a, grid, s);
     return launch_form<E, NT, LOW, false>(w, x, b, o, a, grid, s);
 }
 template <class E, bool LOW>
@@ -966,7 +964,7 @@ cudaError_t launch_type(const AdapterMaps& m, AdapterArgs a, const AdapterPlan& 
     a.col_tiles = 1;
     a.splits = p.low_splits;
     a.nt = p.low_nt;
-    const cudaError_t e = p.low_grid ? launch_low<E, true>(ma, mxl, ma, ma, a, p.low_grid, false, s)
+    const cudaError_t e = p.low_grid ? launch_low<E, true>(ma, mxl, ma, ma, a, p.low_grid, p.low_fold, s)
                                      : launch_rows<E>(a, r, s);
     if (e != cudaSuccess) return e;
     a.row_tiles = p.row_tiles;
@@ -1024,6 +1022,7 @@ AdapterPlan adapter_plan(int n, int N, int K, int R, int n_adapters, bool out_f3
     const int most = (min(n_adapters, p.low_nt) + AD_M / R - 1) / (AD_M / R);   // tiles of a row tile
     // A CTA for each SM.  How many adapters a row tile has is known on the device: its clusters share
     // them out.
+    p.low_fold = out_f32 && nk > AD_FOLD;
     p.low_splits = 1;
     while (p.low_splits < 8 && nk >= 2 * p.low_splits && p.low_row_tiles * p.low_splits * 2 <= sms) p.low_splits *= 2;
     const int clusters = max(1, min(most, sms / (p.low_splits * p.low_row_tiles)));

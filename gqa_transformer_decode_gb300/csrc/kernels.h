@@ -490,7 +490,7 @@ struct AdapterArgs {
 // low_grid 0: row by row).
 struct AdapterPlan {
     int nt, row_tiles, col_tiles, splits, grid;
-    bool fold;                   // accumulators are added up every AD_FOLD blocks of K
+    bool fold, low_fold;         // accumulators are added up every AD_FOLD blocks of K
     int low_nt, low_row_tiles, low_splits, low_grid;
 };
 struct AdapterMaps {
