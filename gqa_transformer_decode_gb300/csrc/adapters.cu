@@ -2,8 +2,8 @@
 // row's own beside it:  y_i = W x_i + bias + s_a B_a (A_a x_i),  a = ids[i].
 //
 // Bound: for few rows the bytes of W and of the adapters that the rows name, for many rows
-// the products.  Two launches: the first takes t_i = s_a A_a x_i (k_adapter<.., true>, for
-// little work k_adapter_rows), the second y (k_adapter<.., false>); the second starts with
+// the products.  Two launches: the first takes t_i = s_a A_a x_i (k_adapter with LOW, for
+// little work k_adapter_rows), the second y (k_adapter without); the second starts with
 // the first and streams W and x meanwhile, and waits for t only when it has come to the
 // adapters.
 //
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(ad_threads(NT), NT <= 128 && !FOLD ? 2 : 1)
         t.e0 = LOW ? (first_tile + (first_of + li * every) * step) * P : 0;
         return t;
     };
-    // Stages of a tile's adapters that are this CTA's (entries part, part + C, ..): SLABS blocks each.
+    // Blocks of a tile's adapters that are this CTA's (entries part, part + C, ..); a stage holds SLABS.
     auto blocks_of = [&](int n) { return n > part ? (n - part + C - 1) / C * slabs : 0; };
     // Sums m .. m + 7 of row c of x: whether anybody wants them, and where they go.
     auto wanted = [&](const Tile& t, int c, int m) {

@@ -209,89 +209,89 @@ struct PdState {
     // the block of keys key0 .. whose K and V tiles stand at kt and vt; sc: scale log2 e
     __device__ __forceinline__ void block(uint32_t kt, uint32_t vt, int key0, const SeqBlocks& x, float sc) {
         const int lane = threadIdx.x & 31, g4 = lane >> 2;
-                    const int mi = lane >> 3, r8 = lane & 7;
-                    float s[NSUB][HT][4];            // S^T: keys g4 and g4 + 8 of each 16
+        const int mi = lane >> 3, r8 = lane & 7;
+        float s[NSUB][HT][4];            // S^T: keys g4 and g4 + 8 of each 16
 #pragma unroll
-                    for (int u = 0; u < NSUB; ++u)
+        for (int u = 0; u < NSUB; ++u)
 #pragma unroll
-                        for (int t = 0; t < HT; ++t) s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.f;
+            for (int t = 0; t < HT; ++t) s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.f;
 #pragma unroll
-                    for (int kk = 0; kk < KS; ++kk)
+        for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-                        for (int u = 0; u < NSUB; ++u) {
-                            uint32_t ka[4];
-                            ldsm4(kt + q_off<DP>(16 * u + (mi & 1) * 8 + r8, 2 * kk + (mi >> 1)), ka[0], ka[1], ka[2], ka[3]);
+            for (int u = 0; u < NSUB; ++u) {
+                uint32_t ka[4];
+                ldsm4(kt + q_off<DP>(16 * u + (mi & 1) * 8 + r8, 2 * kk + (mi >> 1)), ka[0], ka[1], ka[2], ka[3]);
 #pragma unroll
-                            for (int t = 0; t < HT; ++t) E::mma(s[u][t], ka, qb[t][kk][0], qb[t][kk][1]);
-                        }
-                    // every key of the block visible: below the end, and all in the window or all among the sinks
-                    const bool whole = key0 + KEYS <= x.end && (key0 >= x.first || key0 + KEYS <= x.sinks);
-                    bool up = false;
+                for (int t = 0; t < HT; ++t) E::mma(s[u][t], ka, qb[t][kk][0], qb[t][kk][1]);
+            }
+        // every key of the block visible: below the end, and all in the window or all among the sinks
+        const bool whole = key0 + KEYS <= x.end && (key0 >= x.first || key0 + KEYS <= x.sinks);
+        bool up = false;
 #pragma unroll
-                    for (int u = 0; u < NSUB; ++u)
+        for (int u = 0; u < NSUB; ++u)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            bool in = true;
-                            if (!whole) {
-                                const int key = key0 + 16 * u + g4 + 8 * (i >> 1);
-                                in = key < x.end && (key >= x.first || key < x.sinks);
-                            }
+            for (int i = 0; i < 4; ++i) {
+                bool in = true;
+                if (!whole) {
+                    const int key = key0 + 16 * u + g4 + 8 * (i >> 1);
+                    in = key < x.end && (key >= x.first || key < x.sinks);
+                }
 #pragma unroll
-                            for (int t = 0; t < HT; ++t) {
-                                s[u][t][i] = in ? s[u][t][i] * sc : -INFINITY;
-                                up |= s[u][t][i] > m[t][i & 1] + (8.f + E::LIFT);
-                            }
-                        }
-                    if (__any_sync(FULL_MASK, up)) {
+                for (int t = 0; t < HT; ++t) {
+                    s[u][t][i] = in ? s[u][t][i] * sc : -INFINITY;
+                    up |= s[u][t][i] > m[t][i & 1] + (8.f + E::LIFT);
+                }
+            }
+        if (__any_sync(FULL_MASK, up)) {
 #pragma unroll
-                        for (int t = 0; t < HT; ++t)
+            for (int t = 0; t < HT; ++t)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float x = -INFINITY;
+                for (int e = 0; e < 2; ++e) {
+                    float x = -INFINITY;
 #pragma unroll
-                                for (int u = 0; u < NSUB; ++u) x = fmaxf(x, fmaxf(s[u][t][e], s[u][t][e + 2]));
+                    for (int u = 0; u < NSUB; ++u) x = fmaxf(x, fmaxf(s[u][t][e], s[u][t][e + 2]));
 #pragma unroll
-                                for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, d));
-                                x = fmaxf(m[t][e], x - E::LIFT);
-                                const float f = ex2(m[t][e] - x);
-                                m[t][e] = x;
-                                l[t][e] *= f;
+                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, d));
+                    x = fmaxf(m[t][e], x - E::LIFT);
+                    const float f = ex2(m[t][e] - x);
+                    m[t][e] = x;
+                    l[t][e] *= f;
 #pragma unroll
-                                for (int i = 0; i < KS; ++i) {
-                                    o[t][i][e] *= f;
-                                    o[t][i][e + 2] *= f;
-                                }
-                            }
+                    for (int i = 0; i < KS; ++i) {
+                        o[t][i][e] *= f;
+                        o[t][i][e + 2] *= f;
                     }
+                }
+        }
 #pragma unroll
-                    for (int u = 0; u < NSUB; ++u) {
-                        uint32_t pb[HT][2], pr[HT][2];   // P^T as B fragments: keys 2 q4, + 1 (and + 8) of head g4
+        for (int u = 0; u < NSUB; ++u) {
+            uint32_t pb[HT][2], pr[HT][2];   // P^T as B fragments: keys 2 q4, + 1 (and + 8) of head g4
 #pragma unroll
-                        for (int t = 0; t < HT; ++t) {
-                            float (&p)[4] = s[u][t];
+            for (int t = 0; t < HT; ++t) {
+                float (&p)[4] = s[u][t];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) p[i] = ex2(p[i] - m[t][i & 1]);
-                            l[t][0] += p[0] + p[2];
-                            l[t][1] += p[1] + p[3];
+                for (int i = 0; i < 4; ++i) p[i] = ex2(p[i] - m[t][i & 1]);
+                l[t][0] += p[0] + p[2];
+                l[t][1] += p[1] + p[3];
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t x = E::pack(p[2 * e], p[2 * e + 1]);
-                                pb[t][e] = transpose8x8(x);
-                                // what the rounding left
-                                pr[t][e] = transpose8x8(E::pack(p[2 * e] - E::lo(x), p[2 * e + 1] - E::hi(x)));
-                            }
-                        }
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t x = E::pack(p[2 * e], p[2 * e + 1]);
+                    pb[t][e] = transpose8x8(x);
+                    // what the rounding left
+                    pr[t][e] = transpose8x8(E::pack(p[2 * e] - E::lo(x), p[2 * e + 1] - E::hi(x)));
+                }
+            }
 #pragma unroll
-                        for (int i = 0; i < KS; ++i) {
-                            uint32_t va[4];
-                            ldsm4t(vt + q_off<DP>(16 * u + (mi >> 1) * 8 + r8, 2 * i + (mi & 1)), va[0], va[1], va[2], va[3]);
+            for (int i = 0; i < KS; ++i) {
+                uint32_t va[4];
+                ldsm4t(vt + q_off<DP>(16 * u + (mi >> 1) * 8 + r8, 2 * i + (mi & 1)), va[0], va[1], va[2], va[3]);
 #pragma unroll
-                            for (int t = 0; t < HT; ++t) {
-                                E::mma(o[t][i], va, pb[t][0], pb[t][1]);
-                                E::mma(o[t][i], va, pr[t][0], pr[t][1]);
-                            }
-                        }
-                    }
+                for (int t = 0; t < HT; ++t) {
+                    E::mma(o[t][i], va, pb[t][0], pb[t][1]);
+                    E::mma(o[t][i], va, pr[t][0], pr[t][1]);
+                }
+            }
+        }
     }
     // l of the heads, over all the lanes' keys
     __device__ __forceinline__ void end() {
