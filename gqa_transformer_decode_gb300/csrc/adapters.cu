@@ -48,11 +48,11 @@ constexpr int AD_BK = 64;                        // K of a block
 constexpr int AD_SLICE = 32;                     // rows of x that are put out at a time
 constexpr int AD_LD = AD_M + 4;                  // their distance in shared memory, floats
 // f32 outputs: the tensor cores' sums lose a little at every step, in proportion to the steps, so an
-// accumulator takes at most AD_FOLD blocks of K (64 steps) before the output warps add it to a sum in
+// accumulator takes at most AD_FOLD blocks of K (48 steps) before the output warps add it to a sum in
 // TMEM, rounded to nearest, under the next blocks' products where there is room for a second
-// accumulator.  Off by 1.1e-6 of the norm, by 0.57e-6 with 8 blocks; 4096 rows at K 8192 by 9.3e-6 in one
-// accumulator.  The first launch's, whose t's rounding to two terms is of the same size, likewise.  Outputs of 16 bits do without: their own rounding is 1.6e-3 or 2e-4.
-constexpr int AD_FOLD = 16;
+// accumulator.  4096 rows at K 8192: off by 0.76e-6 of the norm in 145 us; 16 blocks 1.1e-6 in 138, 8
+// blocks 0.57e-6 in 157, one accumulator 9.3e-6 in 116.  The first launch's, whose t's rounding to two terms is of the same size, likewise.  Outputs of 16 bits do without: their own rounding is 1.6e-3 or 2e-4.
+constexpr int AD_FOLD = 12;
 
 template <int NT, bool LOW>
 struct AdSmem {

@@ -74,8 +74,10 @@ __device__ __forceinline__ PtGroup pt_scan(const PtGroups& a, int g0, unsigned& 
 
 // SMs for the prefixes' products; the others are for the rows' own keys, which then run beside
 // them.  That pays while both are short and made of latencies: 64 rows on 8192 keys and up to 512
-// of their own 20.5 us, one kernel after the other 23.  With more than PT_APART tiles an SM they
-// only contend for memory (128 rows on 32768 keys: 98 us beside each other, 90 after each other).
+// of their own 30.7 us, one kernel after the other 33.3.  With more than PT_APART tiles an SM a
+// share that is off costs more than latencies do: five documents of 75 rows 77 us beside each
+// other, 56 after each other; 256 rows of 32 heads on 8 of 64 on 16384 keys 134 and 95; though 128
+// rows of 32 on 8 of 128 on 32768 104 and 115.
 // In proportion to what each would take one SM: a key tile of a pair 1700 cycles, a pair four
 // tiles more, and a CTA's SM reads 40 bytes a cycle when not all SMs do.  (64 rows on 8192 keys and
 // 512 of their own 29.6 us so, with 1350 or 2300 cycles 30.5.)

@@ -328,12 +328,12 @@ __global__ void __launch_bounds__(SJ_THREADS) k_shared_join(PagedDecodeArgs a, i
 }
 
 // A call reads each row's keys once for each row (paged_decode.cu, PD_SHARED) up to so many bytes of
-// keys and values: one group on 8 kv heads of 128 with 36 MB 15.9 us so and 17.0 apart, 42 MB 16.6
-// and 17.8, 69 MB 19.5 and 18.0, 143 MB 26.9 and 18.1; and with fewer than three rows a group on
-// average: 64 rows of 4096 shared and 200 own keys take 150 us so, apart 108 in groups of 2 and 81
-// in groups of 3; but 1024 rows of 256 and 64 keys 258 so, apart 413 in groups of 2, 234 of 3 and
-// 190 of 4.
-constexpr double PD_TOGETHER = 48e6;
+// keys and values: one group on 8 kv heads of 128 with 36 MB 15.9 us so and 19.3 apart, 52 MB 18.0
+// and 19.3, 69 MB 19.5 and 20.0, 143 MB 26.9 and 20.5; and with fewer than three rows a group on
+// average: 64 rows of 4096 shared and 200 own keys take 149 us so, apart 114 in groups of 2 and 86
+// in groups of 3; but 1024 rows of 256 and 64 keys 246 so, apart 382 in groups of 2, 249 of 3 and
+// 212 of 4.
+constexpr double PD_TOGETHER = 72e6;
 constexpr int PD_APART_ROWS = 3;
 
 struct SharedPlan {

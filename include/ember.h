@@ -337,8 +337,8 @@ ember_status ember_logprobs(const void *logits, int32_t dtype, int32_t n, int32_
  *        (the row then goes without adapter), RANGE for f16 where an element of
  *        s_a A_a x lies beyond the type's range (its row is then not finite), TIMEOUT.
  * Products are taken on the type and summed in f32 by the tensor cores, which cut off;
- * for f32 outputs at most 64 of their steps, whose sums are added rounded to nearest
- * (W x, and A_a x, off by 1.1e-6 of their norms at most, whatever n and K; sums all
+ * for f32 outputs at most 48 of their steps, whose sums are added rounded to nearest
+ * (W x, and A_a x, off by 0.8e-6 of their norms at most, whatever n and K; sums all
  * rounded to nearest are by 0.3e-6 to 1e-6); s_a A_a x is held as the sum of two values of the type (2^-17 relative for bf16, 2^-22 or
  * 2^-25 absolute for f16).
  * Element pointers are 16-byte aligned, scale, ids and status 4-byte; row strides

@@ -3,9 +3,9 @@ for the worst of every step, let pass.
 
 The tensor cores cut their f32 sums off at each step of 16 products, by up to one unit of the last place, on average half of
 one, which is 2^-24 to 2^-23 of the sum so far, on average 0.72 2^-23; and the sum grows with the root of the steps.  So s steps
-lose about 0.36 2^-23 (2/3) s of the final sum's norm, at most 2.8 times as much.  The second launch takes at most 64 steps in
-one accumulator (1.8e-6) and adds the accumulators' rounded to nearest (2^-24 of a part of the norm each): 3e-6 is over one and
-a half times what is expected.  A x as W x; its two terms are off by 2^-18 (bf16) or 2^-22 (f16), and by the mean of that in a norm; B t takes R / 8 steps.
+lose about 0.36 2^-23 (2/3) s of the final sum's norm, at most 2.8 times as much.  The second launch takes at most 48 steps in
+one accumulator (1.4e-6) and adds the accumulators' rounded to nearest (2^-24 of a part of the norm each): 3e-6 is twice what is
+expected.  A x as W x; its two terms are off by 2^-18 (bf16) or 2^-22 (f16), and by the mean of that in a norm; B t takes R / 8 steps.
 A lost second term would be off by 1e-3 / sqrt(3) (bf16) or 1.4e-4 (f16), a lost block or share of K by its share."""
 import pytest
 import torch
