@@ -203,9 +203,17 @@ struct Block {
 // A product of a tile's adapter takes in neighbouring rows with others as zeros, and zero times an
 // infinity of B is not zero.  So where an output is not finite the outputs that B may have spoilt are
 // taken again, each from its own row and adapter alone: those that are not finite, of rows of W for
-// which some adapter of the tile's rows has a value in B that is not.  Slow (about 2 us an output and
-// warp at K 8192), but nothing where all is finite: one operation an output that sees it.
-__device__ __forceinline__ bool odd16(uint16_t x, bool bf16) { return bf16 ? (x & 0x7f80) == 0x7f80 : (x & 0x7c00) == 0x7c00; }
+// which some adapter of the tile's rows has a value in B that is not.  One operation an output sees to
+// it where all is finite.  With a row of x that is not, whose outputs rightly are not either, a look at
+// the tile's B: 64 rows of 40 adapters of rank 16 on 2048 x 16384 22 -> 30 us, 777 rows of 9 of rank 32
+// 22 -> 26.  With one of those 40 b's infinite all over 570 us (an output and warp after another 850).
+__device__ __forceinline__ bool odd16(uint32_t x, bool bf16) { return bf16 ? (x & 0x7f80) == 0x7f80 : (x & 0x7c00) == 0x7c00; }
+template <bool BF16>
+__device__ __forceinline__ bool any_odd(const uint4& v) {
+    bool odd = false;
+    for (uint32_t u : {v.x, v.y, v.z, v.w}) odd |= odd16(u, BF16) | odd16(u >> 16, BF16);
+    return odd;
+}
 struct AdMend {
     int ids[256], named[256], n_named;   // the tile's rows' adapters, and each of them once
     uint32_t rows[AD_M / 32];            // of W, a bit each
@@ -225,51 +233,79 @@ __device__ __noinline__ void take_again(const AdapterArgs& a, int row0, int m0, 
     __syncthreads();
     for (int c = tid; c < rows; c += T) {
         const int id = s->ids[c];
-        int k = c - 1;
-        while (k >= 0 && s->ids[k] != id) --k;
-        if (id >= 0 && k < 0) s->named[atomicAdd(&s->n_named, 1)] = id;   // (in no order: only marks follow)
+        bool seen = id < 0;
+#pragma unroll 8
+        for (int k = 0; k < c; ++k) seen |= s->ids[k] == id;
+        if (!seen) s->named[atomicAdd(&s->n_named, 1)] = id;   // (in no order: only marks follow)
     }
     __syncthreads();
-    for (int i = tid; i < s->n_named * AD_M; i += T) {
-        const int m = i % AD_M;
-        if (m0 + m >= a.N) continue;
-        const uint4* p = reinterpret_cast<const uint4*>(a.lb + ((long long)s->named[i / AD_M] * a.N + m0 + m) * a.R);
-        bool odd = false;
-        for (int r = 0; r < a.R / 8; ++r) {
-            const uint4 v = __ldg(p + r);
-            for (uint32_t u : {v.x, v.y, v.z, v.w}) odd |= odd16((uint16_t)u, E::bf16) | odd16((uint16_t)(u >> 16), E::bf16);
+    const int pieces = min(AD_M, a.N - m0) * (a.R / 8), all = s->n_named * pieces;   // of 16 bytes, side by side for an adapter
+    for (int i0 = tid; i0 < all; i0 += 8 * T) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * T;
+            v[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < all)
+                v[k] = __ldg(reinterpret_cast<const uint4*>(a.lb + ((long long)s->named[i / pieces] * a.N + m0) * a.R) + i % pieces);
         }
-        if (odd) atomicOr(&s->rows[m / 32], 1u << (m % 32));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (any_odd<E::bf16>(v[k])) {
+                const int m = (i0 + k * T) % pieces / (a.R / 8);
+                atomicOr(&s->rows[m / 32], 1u << (m % 32));
+            }
     }
     __syncthreads();
-    for (int i = lo + warp; i < hi; i += T / 32) {
-        const int c = i / (AD_M / 8), f = i % (AD_M / 8) * 8, row = row0 + c, id = s->ids[c];
-        for (int m = f; m < f + 8; ++m) {
-            if (m0 + m >= a.N || !(s->rows[m / 32] >> (m % 32) & 1u)) continue;
-            float* o32 = static_cast<float*>(a.out) + row * a.ld_out + m0 + m;
-            uint16_t* o16 = static_cast<uint16_t*>(a.out) + row * a.ld_out + m0 + m;
-            if (a.out_f32 ? (__float_as_uint(__ldcg(o32)) & 0x7f800000u) != 0x7f800000u : !odd16(__ldcg(o16), E::bf16)) continue;
-            const uint4 *x = reinterpret_cast<const uint4*>(a.x + row * a.ld_x), *w = reinterpret_cast<const uint4*>(a.w + (long long)(m0 + m) * a.K);
-            float y = 0.f, u[8], v[8];
-            for (int k = lane; k < a.K / 8; k += 32) {
-                unpack8w<!E::bf16>(__ldg(x + k), u);
-                unpack8w<!E::bf16>(__ldg(w + k), v);
-                for (int j = 0; j < 8; ++j) y = fmaf(u[j], v[j], y);
+    const auto marks = [&](int g) { return s->rows[g / 4] >> (g % 4 * 8) & 0xffu; };   // of rows 8 g .. 8 g + 7
+    const unsigned groups = __ballot_sync(FULL_MASK, lane < AD_M / 8 && marks(lane) != 0);
+    const int ng = __popc(groups);
+    for (int e = warp; e < rows * ng; e += T / 32) {
+        const int c = e / ng, g = (int)__fns(groups, 0, e % ng + 1), i = c * (AD_M / 8) + g;
+        if (i < lo || i >= hi) continue;
+        const int row = row0 + c, m = m0 + 8 * g, id = s->ids[c];
+        float* o32 = static_cast<float*>(a.out) + row * a.ld_out + m;
+        uint16_t* o16 = static_cast<uint16_t*>(a.out) + row * a.ld_out + m;
+        bool odd = false;
+        if (lane < 8 && (marks(g) >> lane & 1u))
+            odd = a.out_f32 ? (__float_as_uint(__ldcg(o32 + lane)) & 0x7f800000u) == 0x7f800000u : odd16(__ldcg(o16 + lane), E::bf16);
+        if (!__any_sync(FULL_MASK, odd)) continue;
+        // all eight, for one latency
+        float y[8], u[8], v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = 0.f;
+        const uint4 *x = reinterpret_cast<const uint4*>(a.x + row * a.ld_x), *w = reinterpret_cast<const uint4*>(a.w + (long long)m * a.K);
+        for (int k = lane; k < a.K / 8; k += 32) {
+            uint4 q[8];
+            const uint4 xk = __ldg(x + k);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = __ldg(w + (long long)j * (a.K / 8) + k);
+            unpack8w<!E::bf16>(xk, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                unpack8w<!E::bf16>(q[j], v);
+#pragma unroll
+                for (int d = 0; d < 8; ++d) y[j] = fmaf(u[d], v[d], y[j]);
             }
-            if (id >= 0)
-                for (int r = lane; r < a.R; r += 32) {
-                    const uint16_t* t = a.t + (long long)row * 2 * RP + r / 16 * 32 + r % 16;
-                    const uint32_t two = (uint32_t)__ldcg(t) | (uint32_t)__ldcg(t + 16) << 16;
-                    const uint32_t b = a.lb[((long long)id * a.N + m0 + m) * a.R + r];
-                    const float hi = E::lo(two);         // (an infinity's second term is no number)
-                    y = fmaf(E::lo(b), odd16((uint16_t)two, E::bf16) ? hi : hi + E::hi(two), y);
-                }
-            y = warp_sum(y);
-            if (a.bias) y += E::lo((uint32_t)a.bias[m0 + m]);
-            if (lane == 0) {
-                if (a.out_f32) *o32 = y;
-                else *o16 = (uint16_t)E::pack(y, 0.f);
+        }
+        if (id >= 0)
+            for (int r = lane; r < a.R; r += 32) {
+                const uint16_t* t = a.t + (long long)row * 2 * RP + r / 16 * 32 + r % 16;
+                const uint32_t two = (uint32_t)__ldcg(t) | (uint32_t)__ldcg(t + 16) << 16;
+                const float t1 = E::lo(two), tr = odd16(two & 0xffff, E::bf16) ? t1 : t1 + E::hi(two);   // (an infinity's second term is no number)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = fmaf(E::lo((uint32_t)a.lb[((long long)id * a.N + m + j) * a.R + r]), tr, y[j]);
             }
+        float mine = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float sum = warp_sum(y[j]);
+            if (lane == j) mine = sum;
+        }
+        if (odd) {
+            if (a.bias) mine += E::lo((uint32_t)a.bias[m + lane]);
+            if (a.out_f32) o32[lane] = mine;
+            else o16[lane] = (uint16_t)E::pack(mine, 0.f);
         }
     }
 }

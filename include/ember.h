@@ -344,7 +344,8 @@ ember_status ember_logprobs(const void *logits, int32_t dtype, int32_t n, int32_
  * Element pointers are 16-byte aligned, scale, ids and status 4-byte; row strides
  * multiples of 8 elements; buffers may not overlap.  Values of an x, a, b or scale
  * that are not finite reach the rows that read them and no others; outputs next to
- * such a b's in a tile are taken again one by one, which is slow.  No
+ * such a b's are taken again one by one, which is slow (0.6 ms instead of 22 us for
+ * 64 rows of 40 adapters of which one is infinite all over).  No
  * atomics on results: equal calls give equal bits.  Asynchronous on `stream`; no gradient.
  * Host errors: INVALID_ARG, UNSUPPORTED, CAPACITY (workspace), CUDA. */
 typedef struct ember_adapters {
